@@ -49,8 +49,9 @@ EXPORTED = ["lora_pool_create", "lora_pool_reserve", "lora_pool_release", "lora_
             "lora_adapter_acquire", "lora_adapter_release", "lora_adapter_refs", "lora_pool_evict_idle",
             "lora_adapter_ensure", "lora_pool_set_eviction", "lora_adapter_packed_size", "lora_adapter_pack",
             "lora_adapter_load_packed", "lora_adapter_wait", "lora_kv_grow", "lora_kv_free", "lora_kv_length",
-            "lora_kv_table", "lora_kv_batch_table", "lora_attention_decode"]
-KINDS = ("segments", "delta", "gemm", "scatter", "shrink", "attention")
+            "lora_kv_table", "lora_kv_batch_table", "lora_attention_decode", "lora_kv_write",
+            "lora_attention_split_size", "lora_attention_split", "lora_kv_evict", "lora_kv_keep"]
+KINDS = ("segments", "delta", "gemm", "scatter", "shrink", "attention", "kv")
 
 
 class LoraError(RuntimeError):
@@ -125,6 +126,12 @@ def _load():
         "lora_kv_table": (I32, [VP, I64, I32, VP]),
         "lora_kv_batch_table": (I32, [VP, VP, I32, I32, VP, VP, VP]),
         "lora_attention_decode": (I32, [VP, I32, VP, VP, I32, I32, I32, VP, VP, I32, VP]),
+        "lora_kv_write": (I32, [VP, I32, VP, VP, VP, VP, I64, I64, I32, VP, I32, I32, I32, VP]),
+        "lora_attention_split_size": (I64, [VP, I32, I32, I32, I32, I32]),
+        "lora_attention_split": (I32, [VP, I32, VP, VP, I32, I32, I32, VP, I64, VP, I64, I32, I32, VP, VP, VP, I64, VP,
+                                       I64, VP]),
+        "lora_kv_evict": (I32, [VP, I32, VP, VP, I32, I32, VP, I32, I32, VP, VP, VP, VP, I32, VP]),
+        "lora_kv_keep": (I32, [VP, I64, I32, VP, I64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -314,6 +321,49 @@ def lora_attention_decode(pool, n_req: int, table_dev, seq_len_dev, max_len: int
     """Decode attention of one new token per request over its KV pages at `layer`."""
     _check(_load().lora_attention_decode(pool, n_req, _ptr(table_dev), _ptr(seq_len_dev), max_len, layers, layer,
                                          _ptr(q_dev), _ptr(out_dev), n_heads, _stream(stream)))
+
+
+def lora_kv_write(pool, n_rows: int, row_req_dev, row_pos_dev, k_dev, v_dev, n_req: int, table_dev, max_len: int,
+                  layers: int, layer: int, k_stride: int = 0, v_stride: int = 0, stream=None) -> None:
+    """K and V rows into the pages of (request, position) at `layer`; row strides in elements (0: contiguous)."""
+    _check(_load().lora_kv_write(pool, n_rows, _ptr(row_req_dev), _ptr(row_pos_dev), _ptr(k_dev), _ptr(v_dev), k_stride,
+                                 v_stride, n_req, _ptr(table_dev), max_len, layers, layer, _stream(stream)))
+
+
+def lora_attention_split_size(pool, n_req: int, max_len: int, n_heads: int, n_kv_heads: int,
+                              with_weights: bool = False) -> int:
+    n = _load().lora_attention_split_size(pool, n_req, max_len, n_heads, n_kv_heads, 1 if with_weights else 0)
+    if n < 0:
+        raise LoraError(int(n), lora_last_error())
+    return int(n)
+
+
+def lora_attention_split(pool, n_req: int, table_dev, seq_len_dev, max_len: int, layers: int, layer: int, q_dev,
+                         out_dev, n_heads: int, n_kv_heads: int, workspace_dev, workspace_bytes: int, lse_dev=None,
+                         weight_in_dev=None, weight_out_dev=None, weight_stride: int = 0, q_stride: int = 0,
+                         out_stride: int = 0, stream=None) -> None:
+    """Decode attention split over the cache's length, with optional log-sum-exp and accumulated token weights."""
+    _check(_load().lora_attention_split(pool, n_req, _ptr(table_dev), _ptr(seq_len_dev), max_len, layers, layer,
+                                        _ptr(q_dev), q_stride, _ptr(out_dev), out_stride, n_heads, n_kv_heads,
+                                        _ptr(lse_dev), _ptr(weight_in_dev), _ptr(weight_out_dev), weight_stride,
+                                        _ptr(workspace_dev), workspace_bytes, _stream(stream)))
+
+
+def lora_kv_evict(pool, n_req: int, table_dev, seq_len_dev, max_len: int, layers: int, weight_dev, budget: int,
+                  recent: int, keep_dev, new_len_dev, table_out_dev, weight_out_dev, max_len_out: int,
+                  stream=None) -> None:
+    """Tokens that stay under `budget` per layer and request, by accumulated weight; tables and weights compacted."""
+    _check(_load().lora_kv_evict(pool, n_req, _ptr(table_dev), _ptr(seq_len_dev), max_len, layers, _ptr(weight_dev),
+                                 budget, recent, _ptr(keep_dev), _ptr(new_len_dev), _ptr(table_out_dev),
+                                 _ptr(weight_out_dev), max_len_out, _stream(stream)))
+
+
+def lora_kv_keep(pool, request_id: int, keep_host) -> None:
+    """Host bookkeeping of an eviction: keep_host int32 [layers, n_keep], the positions that stayed per layer."""
+    keep = np.ascontiguousarray(keep_host, dtype=np.int32)
+    if keep.ndim != 2:
+        raise ValueError("keep_host must be [layers, n_keep]")
+    _check(_load().lora_kv_keep(pool, request_id, keep.shape[1], _ptr(keep), keep.shape[1]))
 
 
 def lora_adapter_refs(pool, adapter_id: int) -> int:

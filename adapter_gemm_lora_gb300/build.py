@@ -17,7 +17,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "liblora.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["pool.cu", "segments.cu", "lora_gather.cu", "lora_shrink.cu", "gemm_tcgen05.cu", "forward.cu", "noalloc.cu",
-           "attention.cu"]
+           "attention.cu", "attention_split.cu", "kv_cache.cu"]
 
 
 def _nvcc() -> str:

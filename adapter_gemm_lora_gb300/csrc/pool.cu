@@ -364,6 +364,51 @@ int lora_kv_free(lora_pool* p, int64_t request) {
   return LORA_OK;
 }
 
+int lora_kv_keep(lora_pool* p, int64_t request, int32_t n_keep, const int32_t* keep, int64_t stride) {
+  if (!p || n_keep < 0 || (n_keep > 0 && !keep) || stride < 0 || (stride > 0 && stride < n_keep))
+    return lora_fail(LORA_EINVAL, "lora_kv_keep: bad arguments");
+  auto it = p->kv.find(request);
+  if (it == p->kv.end()) return lora_fail(LORA_EINVAL, "lora_kv_keep: request " + std::to_string(request) + " holds no pages");
+  const int32_t L = it->second.layers;
+  std::vector<int32_t>& pages = it->second.pages;
+  const int64_t n = (int64_t)pages.size() / (2 * L);
+  if (stride == 0) stride = n_keep;
+  for (int32_t l = 0; l < L; ++l)
+    for (int32_t i = 0; i < n_keep; ++i) {
+      const int32_t j = keep[l * stride + i];
+      if (j < 0 || j >= n || (i > 0 && j <= keep[l * stride + i - 1]))
+        return lora_fail(LORA_EINVAL, "lora_kv_keep: layer " + std::to_string(l) + ": positions must ascend within " +
+                                          std::to_string(n) + " tokens");
+    }
+  // Position i of layer l takes its old token's pair; the pairs not taken are freed in page order.
+  // A token never moves up (keep[i] >= i), so the list is compacted in place.  Every allocation
+  // comes before the first change.
+  std::vector<uint8_t> stays;
+  try {
+    stays.assign(pages.size(), 0);
+    p->free_list.reserve(p->free_list.size() + pages.size() - (size_t)n_keep * 2 * L);
+  } catch (const std::bad_alloc&) {
+    return lora_fail(LORA_EINVAL, "lora_kv_keep: out of host memory");
+  }
+  for (int32_t l = 0; l < L; ++l)
+    for (int32_t i = 0; i < n_keep; ++i) stays[((int64_t)keep[l * stride + i] * L + l) * 2] = 1;
+  for (size_t i = 0; i < pages.size(); i += 2)
+    if (!stays[i])
+      for (size_t k = i; k < i + 2; ++k) {
+        p->page_state[pages[k]] = 0;
+        p->free_list.push_back(pages[k]);
+      }
+  for (int32_t l = 0; l < L; ++l)
+    for (int32_t i = 0; i < n_keep; ++i) {
+      const int64_t from = ((int64_t)keep[l * stride + i] * L + l) * 2, to = ((int64_t)i * L + l) * 2;
+      pages[to] = pages[from];
+      pages[to + 1] = pages[from + 1];
+    }
+  p->reserved_pages -= (int64_t)pages.size() - (int64_t)n_keep * 2 * L;
+  pages.resize((size_t)n_keep * 2 * L);
+  return LORA_OK;
+}
+
 int64_t lora_kv_length(const lora_pool* p, int64_t request) {
   if (!p) return -1;
   auto it = p->kv.find(request);

@@ -196,6 +196,90 @@ int lora_attention_decode(lora_pool* pool, int32_t n_req, const int32_t* table_d
                           int32_t max_len, int32_t layers, int32_t layer, const void* q, void* out, int32_t n_heads,
                           lora_stream_t stream);
 
+/*
+ * KV rows into their pages: row t of k and v (device bf16, row t at k + t * k_stride elements,
+ * H values) becomes the K page and the V page that table_dev names for request row_req[t],
+ * position row_pos[t], at `layer`:
+ *     page[table[row_req[t]][row_pos[t]][layer][0]] = k[t],   ...[1]] = v[t]
+ * so a decode step writes one row per request and a prefill batch all its prompt rows, with page
+ * ids that never leave the device (the call can be captured into a graph and replayed).
+ *   n_rows          rows, >= 0;   row_req, row_pos: device int32 [n_rows];
+ *                   row_req[t] = -1: row t has no cache entry and is skipped;
+ *   k_stride, v_stride  elements between rows: 0 = H, else a multiple of 8, >= H;
+ *                   k and v 16-byte aligned;
+ *   n_req, table_dev, max_len, layers, layer   as for lora_attention_decode (table 8-byte aligned).
+ * A request index outside [-1, n_req), a position outside [0, max_len) or a page id outside the
+ * pool sets the device error word and that row is skipped.  Two rows must not name one page.
+ */
+int lora_kv_write(lora_pool* pool, int32_t n_rows, const int32_t* row_req, const int32_t* row_pos, const void* k,
+                  const void* v, int64_t k_stride, int64_t v_stride, int32_t n_req, const int32_t* table_dev,
+                  int32_t max_len, int32_t layers, int32_t layer, lora_stream_t stream);
+
+/*
+ * Decode attention split over the cache's length: the tokens of all requests are cut into equal
+ * ranges, one per CTA, and the partial softmaxes of a request whose tokens lie in several ranges
+ * are joined, so one long request, or requests of very different lengths, keep every SM busy.
+ * Per request and query head h, with KV head h / (n_heads / n_kv_heads) of width
+ * D = H / n_kv_heads (64, 128 or 256), over the request's cached tokens j:
+ *     s_j = q_h . K_j / sqrt(D),  lse = log sum_j exp(s_j),  out_h = sum_j exp(s_j - lse) V_j
+ *     weight_out[j] = weight_in[j] + sum_h exp(s_{h,j} - lse_h)
+ *   table_dev, seq_len_dev, max_len, layers, layer   as for lora_attention_decode (max_len >= 1,
+ *              table 8-byte aligned);
+ *   q, out     device bf16, request r's row at r * q_stride / r * out_stride elements (0 =
+ *              n_heads * D, else a multiple of 8, at least that), 16-byte aligned, out not q;
+ *   n_heads    a multiple of n_kv_heads, at most 16 query heads per KV head;
+ *   lse        nullable device fp32 [n_req][n_heads];
+ *   weight_out nullable device fp32, request r's row at r * weight_stride (0 = max_len, else at
+ *              least that): the attention weight that each cached token received, summed over the
+ *              query heads, is added to weight_in (same layout; NULL = zeros; may be weight_out).
+ *              Positions at and past the request's length are not touched;
+ *   workspace  device, 256-byte aligned, at least lora_attention_split_size(...) bytes for the
+ *              same n_req, max_len, heads, and with_weights != 0 if weight_out is given.  Nothing
+ *              in it needs a value before the call; calls that share it must be ordered.
+ * A request with no cached token gets out = 0 and lse = -infinity.  A page id outside the pool
+ * sets the device error word and its token is skipped (it receives no weight); a request length
+ * outside [0, max_len] sets it and is clamped.  If no score of a row is above -infinity the row
+ * counts as empty.  Results do not depend on the order in which CTAs run.  At most 65535
+ * requests per call.
+ */
+int64_t lora_attention_split_size(const lora_pool* pool, int32_t n_req, int32_t max_len, int32_t n_heads,
+                                  int32_t n_kv_heads, int32_t with_weights);
+int lora_attention_split(lora_pool* pool, int32_t n_req, const int32_t* table_dev, const int32_t* seq_len_dev,
+                         int32_t max_len, int32_t layers, int32_t layer, const void* q, int64_t q_stride, void* out,
+                         int64_t out_stride, int32_t n_heads, int32_t n_kv_heads, float* lse, const float* weight_in,
+                         float* weight_out, int64_t weight_stride, void* workspace, int64_t workspace_bytes,
+                         lora_stream_t stream);
+
+/*
+ * Eviction from the KV cache by accumulated attention weight.  Per layer and request of n cached
+ * tokens, the tokens that stay are n_keep = min(n, budget): the newest min(n, recent), and of the
+ * older ones those with the largest weight; equal weights keep the lowest index, NaN counts as
+ * -infinity.  Every layer keeps the same number of tokens, but not the same ones.
+ *   table_dev    as for lora_attention_decode (8-byte aligned; page ids are passed through);
+ *   weight_dev   device fp32 [layers][n_req][max_len], lora_attention_split's weight_out per layer;
+ *   budget >= 1, 0 <= recent <= budget;
+ *   keep_dev     out: device int32 [layers][n_req][budget], the kept positions, ascending, then -1;
+ *   new_len_dev  out: device int32 [n_req], n_keep (may be seq_len_dev's successor, not itself);
+ *   table_out    out: device int32 [n_req][max_len_out][layers][2] (8-byte aligned), the kept
+ *                tokens' pages in that order, then -1;
+ *   weight_out   out: device fp32 [layers][n_req][max_len_out], their weights, then 0;
+ *   max_len_out  >= min(budget, max_len).
+ * A request length outside [0, max_len] sets the device error word and is clamped.  No output may
+ * overlap an input.  Device work only: lora_kv_keep then tells the host bookkeeping, from a copy
+ * of keep_dev and new_len_dev, which tokens stayed, and frees the others' pages.
+ *   lora_kv_keep: token i of `request_id` at layer l becomes its old token
+ *     keep_host[l * keep_stride + i], i < n_keep (keep_stride in elements; 0 = n_keep); every
+ *     layer's positions strictly ascending and within the request's length (LORA_EINVAL otherwise,
+ *     nothing changed).  The pages of the tokens left out go back to the free list in the order
+ *     they were taken.  Host bookkeeping only: as with lora_kv_free, work that still reads those
+ *     pages must be ordered before whatever next writes them.
+ */
+int lora_kv_evict(lora_pool* pool, int32_t n_req, const int32_t* table_dev, const int32_t* seq_len_dev,
+                  int32_t max_len, int32_t layers, const float* weight_dev, int32_t budget, int32_t recent,
+                  int32_t* keep_dev, int32_t* new_len_dev, int32_t* table_out, float* weight_out,
+                  int32_t max_len_out, lora_stream_t stream);
+int lora_kv_keep(lora_pool* pool, int64_t request_id, int32_t n_keep, const int32_t* keep_host, int64_t keep_stride);
+
 /* Give back n reserved pages (appended to the free list in the order given).
  * LORA_EINVAL if any id is not currently reserved or appears twice (nothing released). */
 int lora_pool_release(lora_pool* pool, int64_t n, const int64_t* page_ids_host);
@@ -392,7 +476,8 @@ const char* lora_last_error(void);
 /*
  * Kernel accounting for benchmarks.  Every kernel this library launches for `pool` is counted
  * by kind: 0 segment build, 1 LoRA delta (shrink and expand), 2 base GEMM, 3 page scatter
- * (adapter loads), 4 shrink of the fused tiles of a prefill-shaped batch, 5 decode attention.
+ * (adapter loads), 4 shrink of the fused tiles of a prefill-shaped batch, 5 decode attention,
+ * 6 KV page writes and evictions.
  * With profiling enabled, each launch is also bracketed by CUDA events recorded on the
  * stream it runs on (also inside a stream capture: the events then become graph nodes and
  * are re-recorded by every replay).  lora_profile_read synchronises those events and
@@ -406,7 +491,8 @@ const char* lora_last_error(void);
 #define LORA_KIND_SCATTER  3
 #define LORA_KIND_SHRINK   4
 #define LORA_KIND_ATTENTION 5
-#define LORA_N_KINDS       6
+#define LORA_KIND_KV       6
+#define LORA_N_KINDS       7
 int lora_profile_enable(lora_pool* pool, int32_t enable);
 int lora_profile_read(lora_pool* pool, int32_t n_kinds, int64_t* launches_host, double* ms_host,
                       int32_t reset);

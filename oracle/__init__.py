@@ -3,3 +3,4 @@ from .lora_oracle import (OK, EINVAL, ENOPAGES, EUNKNOWN_ADAPTER, ERANK, EEXIST,
                           EVICT_LOAD_ORDER, EVICT_LRU, EVICT_FARTHEST,
                           PoolModel, bf16_to_f64, bf16_round, gather_adapter, linear_forward, place_adapter,
                           merged_forward, segments, attention_decode)
+from .kv_oracle import attention_split, evict_keep  # noqa: F401

@@ -282,6 +282,24 @@ class PoolModel:
         self.kv_layers.pop(request)
         return OK
 
+    def kv_keep(self, request: int, keep: Sequence[Sequence[int]]) -> int:
+        """Eviction: keep[l] lists the old positions (ascending, one count for every layer) that
+        stay at layer l; the other tokens' pages go back in the order they were taken."""
+        if request not in self.kv:
+            return EINVAL
+        L = self.kv_layers[request]
+        old = np.asarray(self.kv[request], dtype=np.int64).reshape(-1, L, 2)
+        n = old.shape[0]
+        if len(keep) != L or any(len(k) != len(keep[0]) for k in keep):
+            return EINVAL
+        for k in keep:
+            if any(j < 0 or j >= n for j in k) or any(b <= a for a, b in zip(k, k[1:])):
+                return EINVAL
+        self.free.extend(int(old[j, l, i]) for j in range(n) for l in range(L) for i in range(2) if j not in keep[l])
+        self.kv[request] = [int(old[keep[l][i], l, half]) for i in range(len(keep[0])) for l in range(L)
+                            for half in range(2)]
+        return OK
+
     def kv_table(self, request: int, layer: int) -> np.ndarray:
         """int [tokens, 2]: the (K page, V page) of every cached token of the request at a layer."""
         L = self.kv_layers[request]

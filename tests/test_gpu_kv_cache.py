@@ -1,0 +1,637 @@
+"""KV-cache operators on the GPU: page writes, split decode attention with token weights, eviction.
+
+Attention is compared with the fp64 oracle under bounds that follow from the arithmetic (bf16
+inputs, fp32 sums, weights held in two bf16 terms, one bf16 rounding of the output); page writes and
+evictions have to be exact."""
+import numpy as np
+import pytest
+
+import oracle as O
+import workloads
+from helpers import bits_to_torch, torch_to_bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from adapter_gemm_lora_gb300 import build
+    build.build()
+    import adapter_gemm_lora_gb300 as lib
+    lib.library()
+    return lib
+
+
+class Cache:
+    """KV pages of some requests in a shuffled pool whose other pages hold NaN, with their table."""
+
+    def __init__(self, L, H, layers, lengths, seed, scale=1.0, room=3, max_len=None):
+        import torch
+        self.L, self.H, self.layers, self.lengths = L, H, layers, list(lengths)
+        rng = self.rng = np.random.default_rng(seed)
+        need = 2 * layers * sum(lengths)
+        self.num_pages = need + 64
+        order = rng.permutation(self.num_pages)
+        self.pool_t = torch.full((self.num_pages, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+        self.pool = L.lora_pool_create(self.pool_t, self.num_pages, H, 1, 1, order)
+        self.bits = np.full((self.num_pages, H), 0x7FC0, np.uint16)
+        self.n_req, self.max_len = len(lengths), max_len or max(list(lengths) + [0]) + room
+        for r, n in enumerate(lengths):
+            ids = L.lora_kv_grow(self.pool, r, n, layers)
+            if ids:
+                self.bits[ids] = workloads.to_bf16_bits(scale * rng.standard_normal((len(ids), H)).astype(np.float32))
+        self.pool_t.copy_(bits_to_torch(self.bits))
+        self.table = torch.empty((self.n_req, self.max_len, layers, 2), dtype=torch.int32, device="cuda")
+        self.seq = torch.empty(self.n_req, dtype=torch.int32, device="cuda")
+        if self.n_req:
+            L.lora_kv_batch_table(self.pool, list(range(self.n_req)), self.max_len, self.table, self.seq)
+
+    def tables(self, layer):
+        return [self.L.lora_kv_table(self.pool, r, layer).astype(np.int64) for r in range(self.n_req)]
+
+    def workspace(self, n_heads, n_kv, weights):
+        import torch
+        n = self.L.lora_attention_split_size(self.pool, self.n_req, self.max_len, n_heads, n_kv, weights)
+        return torch.full((max(n, 256),), 0xFF, dtype=torch.uint8, device="cuda"), n     # NaN patterns everywhere
+
+    def close(self):
+        self.L.lora_pool_destroy(self.pool)
+
+
+def _tolerances(ref, lengths, D, G):
+    """Error bounds per request from the arithmetic (u = 2^-24, half a step of fp32).
+
+    A score is a sum of D exact products in fp32, scaled once: off by at most
+    delta = (D + 4) u mag + 4 u |s| <= (D + 8) u mag.  exp2 adds 2^-22, sums over n tokens n u, and a
+    weight held in two bf16 terms 2^-16, so p is off by at most p (2 delta + (n + 8) u + 2^-22 + 2^-16).
+    Token weights come out in fp32, which holds nothing between 0 and its smallest numbers: each
+    head's term may be off by the smallest normal number, 2^-126, besides."""
+    u = 2.0 ** -24
+    tol_out, tol_lse, tol_w = [], [], []
+    for i, n in enumerate(lengths):
+        delta = (D + 8) * u * ref["mag"][i]                                     # per query head
+        rel = 2 * delta + (n + 8) * u + 2.0 ** -22 + 2.0 ** -16
+        tol_out.append(2.0 ** -8 * np.abs(ref["out"][i]) + np.repeat(rel, D) * ref["vabs"][i] * 1.01 + 1e-30)
+        lse = np.where(np.isfinite(ref["lse"][i]), ref["lse"][i], 0.0)
+        tol_lse.append(delta + (n + 8) * u + 2.0 ** -22 + 8 * u * np.abs(lse) + 8 * u)
+        tol_w.append((ref["p"][i] * (2 * delta + (n + 8) * u + 2.0 ** -20)[:, None]).sum(0) if n else np.zeros(0))
+    return np.array(tol_out), np.array(tol_lse), tol_w
+
+
+def _check(ref, out, lse, lengths, D, G):
+    tol_out, tol_lse, _ = _tolerances(ref, lengths, D, G)
+    got = O.bf16_to_f64(torch_to_bits(out.contiguous()))
+    assert np.isfinite(got).all()
+    bad = np.abs(got - ref["out"]) > tol_out
+    assert not bad.any(), f"{int(bad.sum())} outputs, first at {np.argwhere(bad)[0]}"
+    if lse is not None:
+        got = lse.cpu().numpy().astype(np.float64)
+        empty = np.isneginf(ref["lse"])
+        assert np.array_equal(np.isneginf(got), empty)
+        err = np.abs(np.where(empty, 0, got) - np.where(empty, 0, ref["lse"]))
+        assert (err <= tol_lse).all(), err.max()
+
+
+def _check_weights(ref, got, w_in, lengths, D, G, n_heads):
+    _, _, tol_w = _tolerances(ref, lengths, D, G)
+    for i, n in enumerate(lengths):
+        want = ref["weight"][i] + (0 if w_in is None else w_in[i, :n])
+        err = np.abs(got[i, :n] - want)
+        assert (err <= tol_w[i] + 2.0 ** -24 * (n_heads + 2) * np.abs(want) + n_heads * 2.0 ** -126).all(), (i, err.max())
+
+
+SHAPES = [   # n_kv, G, D, layers, lengths
+    (2, 1, 128, 2, [1, 5, 0, 33, 7]),
+    (4, 4, 64, 1, [16, 17, 31, 32, 129]),
+    (1, 16, 256, 1, [300, 0, 1]),
+    (1, 1, 64, 1, [513, 2]),
+    (8, 2, 128, 3, [1000, 1, 64]),
+    (5, 3, 128, 1, [77, 4096]),
+    (12, 1, 64, 1, [15, 130]),
+    (9, 9, 128, 1, [127, 1, 128]),
+    (40, 1, 128, 1, [20, 200, 3]),
+    (1, 8, 64, 1, [20001]),
+    (2, 5, 256, 2, [700, 699]),
+    (6, 1, 256, 1, [47, 90]),
+    (64, 1, 256, 1, [33, 18]),          # H = 16384
+    (128, 2, 128, 1, [9, 40]),
+    (3, 7, 128, 1, [0, 0, 0]),
+    (8, 1, 128, 1, [3, 0, 1, 40] * 170),
+    (1, 2, 128, 1, [1] * 3000),
+]
+
+
+@pytest.mark.parametrize("n_kv,G,D,layers,lengths", SHAPES)
+def test_attention_split_matches_the_oracle(L, n_kv, G, D, layers, lengths):
+    import torch
+    n_heads, H = n_kv * G, n_kv * D
+    c = Cache(L, H, layers, lengths, seed=H + G)
+    try:
+        n_req = c.n_req
+        for layer in range(layers):
+            q_bits = workloads.to_bf16_bits(c.rng.standard_normal((n_req, n_heads * D)).astype(np.float32))
+            ref = O.attention_split(c.bits, c.tables(layer), q_bits, n_heads, n_kv)
+            q = bits_to_torch(q_bits)
+            out = torch.full_like(q, float("nan"))
+            lse = torch.full((n_req, n_heads), float("nan"), device="cuda")
+            ws, nb = c.workspace(n_heads, n_kv, False)
+            L.lora_attention_split(c.pool, n_req, c.table, c.seq, c.max_len, layers, layer, q, out, n_heads, n_kv, ws,
+                                   nb, lse_dev=lse)
+            L.lora_status(c.pool)
+            _check(ref, out, lse, lengths, D, G)
+            # with weights: the same output and log-sum-exp, and the weights on top of earlier ones
+            w_in = c.rng.random((n_req, c.max_len)).astype(np.float32)
+            w_out = torch.full((n_req, c.max_len), -7.0, device="cuda")
+            ws, nb = c.workspace(n_heads, n_kv, True)
+            out2, lse2 = torch.full_like(q, float("nan")), torch.full_like(lse, float("nan"))
+            L.lora_attention_split(c.pool, n_req, c.table, c.seq, c.max_len, layers, layer, q, out2, n_heads, n_kv, ws,
+                                   nb, lse_dev=lse2, weight_in_dev=torch.from_numpy(w_in).cuda(), weight_out_dev=w_out)
+            L.lora_status(c.pool)
+            assert torch.equal(out, out2) and torch.equal(lse, lse2)
+            got = w_out.cpu().numpy().astype(np.float64)
+            _check_weights(ref, got, w_in.astype(np.float64), lengths, D, G, n_heads)
+            for i, n in enumerate(lengths):
+                assert (got[i, n:] == -7.0).all()                # past the length: not touched
+    finally:
+        c.close()
+
+
+def test_attention_split_strides_in_place_weights_and_no_lse(L):
+    import torch
+    n_kv, G, D, lengths = 4, 2, 64, [100, 0, 333, 16]
+    n_heads, width = n_kv * G, n_kv * G * D
+    c = Cache(L, n_kv * D, 2, lengths, seed=2)
+    try:
+        wide = torch.full((4, width + 72), float("nan"), dtype=torch.bfloat16, device="cuda")
+        q_bits = workloads.to_bf16_bits(c.rng.standard_normal((4, width)).astype(np.float32))
+        wide[:, 8:8 + width] = bits_to_torch(q_bits)
+        out = torch.full((4, width + 16), -3.0, dtype=torch.bfloat16, device="cuda")
+        w = torch.zeros((4, c.max_len + 5), device="cuda")
+        ws, nb = c.workspace(n_heads, n_kv, True)
+        ref = O.attention_split(c.bits, c.tables(1), q_bits, n_heads, n_kv)
+        for _ in range(2):
+            L.lora_attention_split(c.pool, 4, c.table, c.seq, c.max_len, 2, 1, wide[:, 8:], out, n_heads, n_kv, ws, nb,
+                                   weight_in_dev=w, weight_out_dev=w, weight_stride=c.max_len + 5,
+                                   q_stride=width + 72, out_stride=width + 16)
+        L.lora_status(c.pool)
+        _check(ref, out[:, :width], None, lengths, D, G)
+        assert (out[:, width:] == -3.0).all()
+        got = w.cpu().numpy().astype(np.float64)
+        twice = {**ref, "weight": [2 * x for x in ref["weight"]], "p": [2 * x for x in ref["p"]]}
+        _check_weights(twice, got, None, lengths, D, G, 2 * n_heads)
+        # without earlier weights the sum starts at zero
+        first = torch.full_like(w, 9.0)
+        L.lora_attention_split(c.pool, 4, c.table, c.seq, c.max_len, 2, 1, wide[:, 8:], out, n_heads, n_kv, ws, nb,
+                               weight_out_dev=first, weight_stride=c.max_len + 5, q_stride=width + 72,
+                               out_stride=width + 16)
+        _check_weights(ref, first.cpu().numpy().astype(np.float64), None, lengths, D, G, n_heads)
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("scale,shift", [(30.0, 0.0), (1e-3, 0.0), (1.0, 200.0)])
+def test_attention_split_far_scores(L, scale, shift):
+    """Scores of hundreds (one token takes everything), of nothing, and with a late maximum."""
+    import torch
+    n_kv, D, lengths = 2, 128, [700, 45]
+    c = Cache(L, 256, 1, lengths, seed=11, scale=scale)
+    try:
+        q_bits = workloads.to_bf16_bits(c.rng.standard_normal((2, 256)).astype(np.float32))
+        if shift:                                                # the last token's K along q
+            for r in range(2):
+                k_page = c.tables(0)[r][-1, 0]
+                qf = O.bf16_to_f64(q_bits[r]).reshape(2, 128)
+                k = (qf * shift * np.sqrt(128) / (qf ** 2).sum(1, keepdims=True)).reshape(-1)
+                c.bits[k_page] = workloads.to_bf16_bits(k.astype(np.float32))
+            c.pool_t.copy_(bits_to_torch(c.bits))
+        ref = O.attention_split(c.bits, c.tables(0), q_bits, 2, 2)
+        q, out = bits_to_torch(q_bits), torch.empty((2, 256), dtype=torch.bfloat16, device="cuda")
+        lse, w = torch.empty((2, 2), device="cuda"), torch.zeros((2, c.max_len), device="cuda")
+        ws, nb = c.workspace(2, 2, True)
+        L.lora_attention_split(c.pool, 2, c.table, c.seq, c.max_len, 1, 0, q, out, 2, 2, ws, nb, lse_dev=lse,
+                               weight_out_dev=w)
+        L.lora_status(c.pool)
+        _check(ref, out, lse, lengths, D, 1)
+        _check_weights(ref, w.cpu().numpy().astype(np.float64), None, lengths, D, 1, 2)
+    finally:
+        c.close()
+
+
+def test_attention_split_skips_bad_pages_and_clamps_lengths(L):
+    import torch
+    n_kv, G, D, lengths = 2, 2, 128, [50, 3, 20]
+    c = Cache(L, 256, 1, lengths, seed=4)
+    try:
+        tabs = c.tables(0)
+        drop = {0: [0, 17, 49], 1: [0, 1, 2], 2: []}
+        for r, js in drop.items():
+            for i, j in enumerate(js):
+                c.table[r, j, 0, i % 2] = (1 << 30) if i != 1 else -5
+        q_bits = workloads.to_bf16_bits(c.rng.standard_normal((3, 512)).astype(np.float32))
+        keep = [np.setdiff1d(np.arange(n), drop[r]) for r, n in enumerate(lengths)]
+        ref = O.attention_split(c.bits, [tabs[r][keep[r]] for r in range(3)], q_bits, 4, 2)
+        q, out = bits_to_torch(q_bits), torch.empty((3, 512), dtype=torch.bfloat16, device="cuda")
+        lse, w = torch.empty((3, 4), device="cuda"), torch.full((3, c.max_len), 5.0, device="cuda")
+        ws, nb = c.workspace(4, 2, True)
+        args = (c.pool, 3, c.table, c.seq, c.max_len, 1, 0, q, out, 4, 2, ws, nb)
+        L.lora_attention_split(*args, lse_dev=lse, weight_out_dev=w)
+        with pytest.raises(L.LoraError) as e:
+            L.lora_status(c.pool)
+        assert e.value.code == L.LORA_EDEVICE and "page" in e.value.message
+        _check(ref, out, lse, [len(k) for k in keep], D, G)
+        got = w.cpu().numpy().astype(np.float64)
+        for r, js in drop.items():
+            assert (got[r, js] == 0).all()
+        _check_weights(ref, np.stack([np.pad(got[r, keep[r]], (0, c.max_len - len(keep[r]))) for r in range(3)]), None,
+                       [len(k) for k in keep], D, G, 4)
+        # lengths outside [0, max_len]: reported and clamped
+        c.seq.copy_(torch.tensor([-3, 3, 20], dtype=torch.int32))
+        L.lora_attention_split(*args, lse_dev=lse)
+        with pytest.raises(L.LoraError):
+            L.lora_status(c.pool)
+        assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
+        c.seq.copy_(torch.tensor([c.max_len + 1, 0, 0], dtype=torch.int32))     # the tail of row 0 holds -1 pages
+        L.lora_attention_split(*args, lse_dev=lse)
+        with pytest.raises(L.LoraError):
+            L.lora_status(c.pool)
+        _check({k: v[:1] for k, v in ref.items()}, out[:1], lse[:1], [len(keep[0])], D, G)
+    finally:
+        c.close()
+
+
+def test_attention_split_overflowing_scores_and_infinite_values(L):
+    """A score of -infinity takes no weight; rows whose every score is -infinity count as empty."""
+    import torch
+    c = Cache(L, 128, 1, [40, 21], seed=8)
+    try:
+        big = workloads.to_bf16_bits(np.float32([3e38]))[0]
+        neg = workloads.to_bf16_bits(np.float32([-3e38]))[0]
+        tabs = c.tables(0)
+        q_bits = np.full((2, 128), workloads.to_bf16_bits(np.float32([1.0]))[0], np.uint16)
+        q_bits[:, 0] = big
+        c.bits[tabs[0][7, 0], 0] = neg                             # request 0, token 7: -infinity
+        for j in range(40):
+            if j != 7:
+                c.bits[tabs[0][j, 0], 0] = 0
+        c.bits[tabs[1][:, 0], 0] = neg                             # request 1: every score
+        c.pool_t.copy_(bits_to_torch(c.bits))
+        keep = np.setdiff1d(np.arange(40), [7])
+        ref = O.attention_split(c.bits, [tabs[0][keep], tabs[1][:0]], q_bits, 1, 1)
+        q, out = bits_to_torch(q_bits), torch.empty((2, 128), dtype=torch.bfloat16, device="cuda")
+        lse, w = torch.empty((2, 1), device="cuda"), torch.full((2, c.max_len), 5.0, device="cuda")
+        ws, nb = c.workspace(1, 1, True)
+        L.lora_attention_split(c.pool, 2, c.table, c.seq, c.max_len, 1, 0, q, out, 1, 1, ws, nb, lse_dev=lse,
+                               weight_out_dev=w)
+        L.lora_status(c.pool)
+        _check(ref, out, lse, [39, 0], 128, 1)
+        got = w.cpu().numpy()
+        assert got[0, 7] == 0 and (got[1, :21] == 0).all() and abs(got[0, :40].sum() - 1) < 1e-5
+    finally:
+        c.close()
+
+
+def test_attention_split_nan_stays_in_its_own_heads(L):
+    """A NaN in one KV head of one token spoils that head's query heads of that request, no others."""
+    import torch
+    n_kv, G, D = 2, 2, 64
+    c = Cache(L, 128, 1, [30, 200], seed=9)
+    try:
+        tabs = c.tables(0)
+        q_bits = workloads.to_bf16_bits(c.rng.standard_normal((2, 256)).astype(np.float32))
+        ref = O.attention_split(c.bits, tabs, q_bits, 4, 2)
+        c.bits[tabs[1][150, 0], 64 + 3] = 0x7FC0                   # K of token 150, KV head 1
+        c.pool_t.copy_(bits_to_torch(c.bits))
+        q, out = bits_to_torch(q_bits), torch.empty((2, 256), dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty((2, 4), device="cuda")
+        ws, nb = c.workspace(4, 2, False)
+        L.lora_attention_split(c.pool, 2, c.table, c.seq, c.max_len, 1, 0, q, out, 4, 2, ws, nb, lse_dev=lse)
+        assert torch.isnan(out[1, 128:]).all() and torch.isnan(lse[1, 2:]).all()
+        _check({k: v[:1] for k, v in ref.items()}, out[:1], lse[:1], [30], D, G)
+        half = {k: ref[k][1:, :n] for k, n in (("out", 128), ("vabs", 128), ("lse", 2), ("mag", 2))}
+        half["p"] = [ref["p"][1][:2]]
+        _check(half, out[1:, :128], lse[1:, :2], [200], D, G)
+    finally:
+        c.close()
+
+
+def test_attention_split_same_bits_again_on_a_side_stream_and_in_a_graph(L):
+    import torch
+    n_kv, G, D, lengths = 8, 1, 128, [5000, 3, 0, 260, 1]
+    c = Cache(L, 1024, 1, lengths, seed=6)
+    try:
+        q = bits_to_torch(workloads.to_bf16_bits(c.rng.standard_normal((5, 1024)).astype(np.float32)))
+        ws, nb = c.workspace(8, 8, True)
+
+        def call(out, lse, w, stream=None):
+            L.lora_attention_split(c.pool, 5, c.table, c.seq, c.max_len, 1, 0, q, out, 8, 8, ws, nb, lse_dev=lse,
+                                   weight_out_dev=w, stream=stream)
+
+        def bufs():
+            return torch.empty_like(q), torch.empty((5, 8), device="cuda"), torch.zeros((5, c.max_len), device="cuda")
+        first = bufs()
+        call(*first)
+        for _ in range(3):
+            again = bufs()
+            call(*again)
+            assert all(torch.equal(a, b) for a, b in zip(first, again))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        other = bufs()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            call(*other)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, other))
+        held = bufs()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(*held)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, held))
+        # replayed on other lengths: what an eager call computes
+        c.seq.copy_(torch.tensor([77, 2, 0, 0, 1], dtype=torch.int32))
+        fresh = bufs()
+        call(*fresh)
+        for b in held:
+            b.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(fresh, held))
+        L.lora_status(c.pool)
+    finally:
+        c.close()
+
+
+def test_attention_split_does_not_depend_on_the_other_requests_values(L):
+    """A request's result stays the same when another request's rows and query change."""
+    import torch
+    c = Cache(L, 256, 1, [900, 37, 2500], seed=12)
+    try:
+        q = bits_to_torch(workloads.to_bf16_bits(c.rng.standard_normal((3, 256)).astype(np.float32)))
+        ws, nb = c.workspace(2, 2, False)
+        outs = []
+        for _ in range(2):
+            out = torch.empty_like(q)
+            L.lora_attention_split(c.pool, 3, c.table, c.seq, c.max_len, 1, 0, q, out, 2, 2, ws, nb)
+            outs.append(out)
+            q[1] = -q[1]
+            c.pool_t[torch.from_numpy(c.tables(0)[1].reshape(-1)).cuda()] = 3.0
+        assert torch.equal(outs[0][[0, 2]], outs[1][[0, 2]]) and not torch.equal(outs[0][1], outs[1][1])
+    finally:
+        c.close()
+
+
+# ---- page writes ---------------------------------------------------------------------------------
+@pytest.mark.parametrize("H,layers,lengths,pad", [
+    (64, 1, [1], 0), (256, 2, [5, 0, 9], 8), (5120, 1, [1] * 40, 0), (4096, 3, [130, 1, 17], 64), (16384, 1, [3], 0),
+    (320, 1, [2000], 0),
+])
+def test_kv_write_puts_every_row_in_its_page(L, H, layers, lengths, pad):
+    import torch
+    c = Cache(L, H, layers, lengths, seed=H)
+    try:
+        T = sum(lengths)
+        req = np.repeat(np.arange(len(lengths)), lengths).astype(np.int32)
+        pos = np.concatenate([np.arange(n) for n in lengths]).astype(np.int32)
+        perm = c.rng.permutation(T)
+        req, pos = req[perm], pos[perm]
+        skip = c.rng.random(T) < 0.2
+        req_s = np.where(skip, -1, req).astype(np.int32)
+        rows = [torch.empty((T, H + pad), dtype=torch.bfloat16, device="cuda").normal_() for _ in range(2)]
+        want = c.pool_t.clone()
+        for layer in range(layers):
+            L.lora_kv_write(c.pool, T, torch.from_numpy(req_s).cuda(), torch.from_numpy(pos).cuda(), rows[0], rows[1],
+                            c.n_req, c.table, c.max_len, layers, layer, k_stride=H + pad, v_stride=H + pad)
+            tabs = c.tables(layer)
+            for t in np.flatnonzero(~skip):
+                for half in range(2):
+                    want[int(tabs[req[t]][pos[t], half])] = rows[half][int(t), :H]
+        L.lora_status(c.pool)
+        assert torch.equal(want.view(torch.int16), c.pool_t.view(torch.int16))
+    finally:
+        c.close()
+
+
+def test_kv_write_reports_bad_rows_and_writes_the_others(L):
+    import torch
+    c = Cache(L, 128, 1, [4, 4], seed=1)
+    try:
+        c.table[1, 3, 0, 1] = c.num_pages
+        req = torch.tensor([0, 2, 0, -2, 1, 1], dtype=torch.int32, device="cuda")
+        pos = torch.tensor([0, 0, c.max_len, 0, 3, 1], dtype=torch.int32, device="cuda")
+        k = torch.ones((6, 128), dtype=torch.bfloat16, device="cuda")
+        v = 2 * k
+        want = c.pool_t.clone()
+        tabs = c.tables(0)
+        want[int(tabs[0][0, 0])], want[int(tabs[0][0, 1])] = 1.0, 2.0
+        want[int(tabs[1][1, 0])], want[int(tabs[1][1, 1])] = 1.0, 2.0
+        L.lora_kv_write(c.pool, 6, req, pos, k, v, 2, c.table, c.max_len, 1, 0)
+        with pytest.raises(L.LoraError) as e:
+            L.lora_status(c.pool)
+        assert e.value.code == L.LORA_EDEVICE
+        assert torch.equal(want.view(torch.int16), c.pool_t.view(torch.int16))
+    finally:
+        c.close()
+
+
+def test_offsets_past_32_bits(L):
+    """Pages whose element offset passes 2^31, read and written through a table whose own element
+    index passes 2^31 (two requests far apart)."""
+    import torch
+    H, num_pages = 4096, 600_000
+    layers, max_len = 64, (1 << 24) + 9
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    pool_t = torch.empty((num_pages, H), dtype=torch.bfloat16, device="cuda")
+    table = torch.empty((3, max_len, layers, 2), dtype=torch.int32, device="cuda")
+    pool = L.lora_pool_create(pool_t, num_pages, H, 1, 1)
+    try:
+        n, layer = 37, 63
+        pages = np.arange(num_pages - 2 * n, num_pages).reshape(n, 2)
+        table[2, :n, layer] = torch.from_numpy(pages.astype(np.int32)).cuda()
+        seq = torch.tensor([0, 0, n], dtype=torch.int32, device="cuda")
+        rng = np.random.default_rng(0)
+        kv = workloads.to_bf16_bits(rng.standard_normal((2, n, H)).astype(np.float32))
+        L.lora_kv_write(pool, n, torch.full((n,), 2, dtype=torch.int32, device="cuda"),
+                        torch.arange(n, dtype=torch.int32, device="cuda"), bits_to_torch(kv[0]), bits_to_torch(kv[1]),
+                        3, table, max_len, layers, layer)
+        q_bits = workloads.to_bf16_bits(rng.standard_normal((3, H)).astype(np.float32))
+        out = torch.empty((3, H), dtype=torch.bfloat16, device="cuda")
+        nb = L.lora_attention_split_size(pool, 3, max_len, 32, 32)
+        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        L.lora_attention_split(pool, 3, table, seq, max_len, layers, layer, bits_to_torch(q_bits), out, 32, 32, ws, nb)
+        L.lora_status(pool)
+        bits = kv.transpose(1, 0, 2).reshape(2 * n, H)
+        ref = O.attention_split(bits, [np.zeros((0, 2))] * 2 + [np.arange(2 * n).reshape(n, 2)], q_bits, 32, 32)
+        _check(ref, out, None, [0, 0, n], 128, 1)
+    finally:
+        L.lora_pool_destroy(pool)
+
+
+# ---- eviction ------------------------------------------------------------------------------------
+def _evict(L, pool, table, seq, weight, budget, recent, max_len_out):
+    import torch
+    layers, n_req, max_len = weight.shape
+    keep = torch.full((layers, n_req, budget), -9, dtype=torch.int32, device="cuda")
+    new_len = torch.full((n_req,), -9, dtype=torch.int32, device="cuda")
+    table_out = torch.full((n_req, max_len_out, layers, 2), -9, dtype=torch.int32, device="cuda")
+    weight_out = torch.full((layers, n_req, max_len_out), -9.0, device="cuda")
+    L.lora_kv_evict(pool, n_req, table, seq, max_len, layers, weight, budget, recent, keep, new_len, table_out,
+                    weight_out, max_len_out)
+    return keep.cpu().numpy(), new_len.cpu().numpy(), table_out.cpu().numpy(), weight_out.cpu().numpy()
+
+
+def _evict_expected(table, lengths, weight, budget, recent, max_len_out):
+    layers, n_req, _ = weight.shape
+    keep = np.full((layers, n_req, budget), -1, np.int32)
+    table_out = np.full((n_req, max_len_out, layers, 2), -1, np.int32)
+    weight_out = np.zeros((layers, n_req, max_len_out), np.float32)
+    for l in range(layers):
+        for r, n in enumerate(lengths):
+            k = O.evict_keep(weight[l, r], n, budget, recent)
+            keep[l, r, :len(k)] = k
+            table_out[r, :len(k), l] = table[r, k, l]
+            weight_out[l, r, :len(k)] = weight[l, r, k]
+    return keep, np.minimum(lengths, budget).astype(np.int32), table_out, weight_out
+
+
+def _same(got, want):
+    for name, g, w in zip(("keep", "new_len", "table", "weight"), got, want):
+        eq = (g == w) | ((g != g) & (w != w)) if g.dtype.kind == "f" else g == w
+        assert g.shape == w.shape and eq.all(), (name, np.argwhere(~eq)[:4])
+
+
+KINDS = ["plain", "ties", "zeros", "special", "ascending"]
+
+
+def _weights(kind, rng, shape):
+    w = np.exp(2 * rng.standard_normal(shape)).astype(np.float32)
+    if kind == "ties":
+        w = rng.integers(0, 4, size=shape).astype(np.float32)
+    elif kind == "zeros":
+        w = np.where(rng.random(shape) < 0.9, np.where(rng.random(shape) < 0.5, 0.0, -0.0), w).astype(np.float32)
+    elif kind == "special":
+        pick = rng.integers(0, 7, size=shape)
+        vals = np.float32([np.nan, np.inf, -np.inf, -1.5, 1e-42, -1e-42, 0.0])
+        w = np.where(rng.random(shape) < 0.7, vals[pick], w).astype(np.float32)
+    elif kind == "ascending":
+        w = np.broadcast_to(np.arange(shape[-1], dtype=np.float32), shape).copy()
+    return w
+
+
+@pytest.mark.parametrize("layers,lengths,budget,recent", [
+    (1, [80], 64, 16), (1, [1], 1, 0), (1, [1, 0, 2], 1, 1), (3, [64, 65, 63, 0, 200], 64, 0), (2, [300, 10, 299], 299, 299),
+    (5, [1000, 1, 999], 17, 16), (2, [4097, 2049, 2048, 2047], 1024, 100), (1, [40000, 39999, 7], 2000, 1),
+    (1, [140001, 3], 5000, 512), (2, [70000], 69999, 3), (40, [128] * 20, 100, 10), (1, [5] * 1000, 3, 1),
+])
+@pytest.mark.parametrize("kind", KINDS)
+def test_evict_keeps_what_the_definition_keeps(L, layers, lengths, budget, recent, kind):
+    import torch
+    rng = np.random.default_rng([layers, budget, KINDS.index(kind)])
+    max_len = max(lengths) + int(rng.integers(0, 4))
+    n_req = len(lengths)
+    weight = _weights(kind, rng, (layers, n_req, max_len))
+    table = rng.integers(0, 1 << 31, size=(n_req, max_len, layers, 2)).astype(np.int32)
+    max_len_out = min(budget, max_len) + int(rng.integers(0, 9))
+    pool_t = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    pool = L.lora_pool_create(pool_t, 4, 64, 1, 1)
+    try:
+        got = _evict(L, pool, torch.from_numpy(table).cuda(), torch.tensor(lengths, dtype=torch.int32, device="cuda"),
+                     torch.from_numpy(weight).cuda(), budget, recent, max_len_out)
+        L.lora_status(pool)
+        _same(got, _evict_expected(table, lengths, weight, budget, recent, max_len_out))
+    finally:
+        L.lora_pool_destroy(pool)
+
+
+def test_evict_reports_and_clamps_lengths(L):
+    import torch
+    rng = np.random.default_rng(3)
+    weight = _weights("plain", rng, (2, 3, 50))
+    table = rng.integers(0, 100, size=(3, 50, 2, 2)).astype(np.int32)
+    pool_t = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    pool = L.lora_pool_create(pool_t, 4, 64, 1, 1)
+    try:
+        got = _evict(L, pool, torch.from_numpy(table).cuda(), torch.tensor([51, -1, 30], dtype=torch.int32, device="cuda"),
+                     torch.from_numpy(weight).cuda(), 20, 5, 20)
+        with pytest.raises(L.LoraError) as e:
+            L.lora_status(pool)
+        assert e.value.code == L.LORA_EDEVICE
+        _same(got, _evict_expected(table, [50, 0, 30], weight, 20, 5, 20))
+    finally:
+        L.lora_pool_destroy(pool)
+
+
+def test_evict_then_keep_then_attend(L):
+    """The device's compacted table is the host bookkeeping's after lora_kv_keep, the freed pages are
+    the pool's again, and attention over the kept tokens is attention over those tokens."""
+    import torch
+    n_kv, D, layers, lengths = 2, 64, 3, [70, 20, 41, 0]
+    c = Cache(L, 128, layers, lengths, seed=21)
+    try:
+        weight = c.rng.random((layers, 4, c.max_len)).astype(np.float32)
+        before = [c.tables(l) for l in range(layers)]
+        keep, new_len, table_out, _ = _evict(L, c.pool, c.table, c.seq, torch.from_numpy(weight).cuda(), 32, 8, 35)
+        free0 = L.lora_pool_stats(c.pool)["free"]
+        for r in range(4):
+            L.lora_kv_keep(c.pool, r, keep[:, r, :new_len[r]])
+        assert L.lora_pool_stats(c.pool)["free"] == free0 + 2 * layers * ((70 - 32) + (41 - 32))
+        table = torch.empty((4, 35, layers, 2), dtype=torch.int32, device="cuda")
+        seq = torch.empty(4, dtype=torch.int32, device="cuda")
+        L.lora_kv_batch_table(c.pool, [0, 1, 2, 3], 35, table, seq)
+        assert np.array_equal(table.cpu().numpy(), table_out) and seq.tolist() == new_len.tolist() == [32, 20, 32, 0]
+        q_bits = workloads.to_bf16_bits(c.rng.standard_normal((4, 128)).astype(np.float32))
+        q = bits_to_torch(q_bits)
+        nb = L.lora_attention_split_size(c.pool, 4, 35, 2, 2)
+        ws = torch.empty(max(nb, 256), dtype=torch.uint8, device="cuda")
+        for l in range(layers):
+            out = torch.empty_like(q)
+            L.lora_attention_split(c.pool, 4, torch.from_numpy(table_out).cuda(), seq, 35, layers, l, q, out, 2, 2, ws, nb)
+            kept = [before[l][r][keep[l, r, :new_len[r]]] for r in range(4)]
+            _check(O.attention_split(c.bits, kept, q_bits, 2, 2), out, None, new_len.tolist(), D, 1)
+        L.lora_status(c.pool)
+    finally:
+        c.close()
+
+
+def test_evict_in_a_graph_and_on_a_side_stream(L):
+    import torch
+    rng = np.random.default_rng(4)
+    layers, n_req, max_len = 3, 5, 900
+    lengths = [900, 10, 450, 0, 300]
+    weight = torch.from_numpy(_weights("ties", rng, (layers, n_req, max_len))).cuda()
+    table = torch.from_numpy(rng.integers(0, 99, size=(n_req, max_len, layers, 2)).astype(np.int32)).cuda()
+    seq = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    pool_t = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    pool = L.lora_pool_create(pool_t, 4, 64, 1, 1)
+    try:
+        keep = torch.zeros((layers, n_req, 256), dtype=torch.int32, device="cuda")
+        new_len = torch.zeros(n_req, dtype=torch.int32, device="cuda")
+        t_out = torch.zeros((n_req, 256, layers, 2), dtype=torch.int32, device="cuda")
+        w_out = torch.zeros((layers, n_req, 256), device="cuda")
+        args = (pool, n_req, table, seq, max_len, layers, weight, 256, 32, keep, new_len, t_out, w_out, 256)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            L.lora_kv_evict(*args)
+        side.synchronize()
+        want = _evict_expected(table.cpu().numpy(), lengths, weight.cpu().numpy(), 256, 32, 256)
+        _same([x.cpu().numpy() for x in (keep, new_len, t_out, w_out)], want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            L.lora_kv_evict(*args)
+        weight.neg_()
+        seq[3] = 899
+        g.replay()
+        torch.cuda.synchronize()
+        want = _evict_expected(table.cpu().numpy(), [900, 10, 450, 899, 300], weight.cpu().numpy(), 256, 32, 256)
+        _same([x.cpu().numpy() for x in (keep, new_len, t_out, w_out)], want)
+        L.lora_status(pool)
+    finally:
+        L.lora_pool_destroy(pool)
