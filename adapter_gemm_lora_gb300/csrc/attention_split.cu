@@ -4,6 +4,18 @@
 //     s_j = q_h . K_j / sqrt(D),  lse = log sum_j exp(s_j),  out_h = sum_j exp(s_j - lse) V_j
 //     weight_out[j] = weight_in[j] + sum_h exp(s_{h,j} - lse_h)
 // Softmax in base 2: scores carry log2(e) / sqrt(D).
+//
+// HBM-bound: every cached token's K and V rows (2 x 2 H bytes) are read once, against 4 H G flops.
+//
+// Split.  The tokens of all requests, in units of one ring stage, form one sequence that is cut
+// into P equal ranges; a CTA takes one range for one group of KV heads.  A request inside one range
+// is finished there; one that spans ranges leaves a partial (m, l, sum exp2(s - m) V) per range,
+// and the second kernel joins them: m = max m_i, l = sum l_i 2^(m_i - m), out likewise.  So the
+// work per CTA does not depend on how the lengths are spread, and no result on who finishes first.
+//
+// Weights need the final lse, so the first kernel stores the scores (4 bytes per query head and
+// token, against 4 D G of K and V) and the second turns them into weights, each token's sum over
+// heads taken by one thread in head order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -15,131 +27,715 @@
 
 namespace {
 
-constexpr int kSplitMaxGroup = 16;     // query heads per KV head
+constexpr int kSplitMaxGroup = 16;                  // query heads per KV head
+constexpr int kWarps = 8;                           // consumer warps
+constexpr int kThreads = 32 * (kWarps + 1);         // + the producer warp
+constexpr int kTile = 16;                           // tokens a warp takes at a time
+constexpr int kStageBytes = 64 * 1024;              // K and V of a stage, at most
+constexpr int kMaxStages = 8;
+constexpr int kMaxSmem = 227 * 1024;
+constexpr int kJoinThreads = 256;
+
+// How a call is cut: fixed by the shapes, the same for the size query and the launch.
+struct SplitPlan {
+  int32_t D, group, n_kv;
+  int32_t n_groups, heads;       // groups of KV heads, KV heads per group
+  int32_t tiles;                 // 16-token tiles per stage: so many warps share a head
+  int32_t stages;
+  int32_t parts;                 // ranges the token sequence is cut into
+  bool whole;                    // one range per request: nothing to join
+  int32_t row_bytes, stage_bytes, smem;
+};
 
 struct SplitArgs {
   const uint16_t* pool;
   int64_t num_pages;
   int32_t H, n_req;
-  const int2* table;
+  const int32_t* table;
   const int32_t* seq_len;
   int32_t max_len, layers, layer;
   const uint16_t* q;
   int64_t q_stride;
   uint16_t* out;
   int64_t out_stride;
-  int32_t n_heads, group;
+  int32_t n_heads;
   float* lse;                          // caller's, nullable, natural log
   const float* weight_in;
   float* weight_out;
   int64_t weight_stride;
   float scale_log2;
-  float* ws_lse;                       // [n_req][n_heads], base 2
-  float* ws_scores;                    // [n_req][n_heads][max_len rounded up to 16], base 2; NULL without weights
+  SplitPlan plan;
+  float* ws_lse;                       // [n_req][n_heads], base 2: requests inside one range
+  int2* ws_range;                      // [n_req] first and last range of a request
+  int4* ws_start;                      // [parts] first request and token of a range, its units
+  float2* ws_ml;                       // [2 parts][n_heads] m and l of a partial
+  float* ws_acc;                       // [2 parts][n_heads][D]
+  float* ws_scores;                    // [n_req][n_heads][score_stride], base 2; NULL without weights
   int64_t score_stride;
   int32_t* err;
 };
 
-__device__ __forceinline__ int request_length(const SplitArgs& a, int r, bool report) {
-  int n = a.seq_len[r];
-  if (n < 0 || n > a.max_len) {
-    if (report) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
-    n = n < 0 ? 0 : a.max_len;
-  }
-  return n;
+// A range leaves at most two partials: slot 2 p for a request that began in an earlier range,
+// slot 2 p + 1 for one that begins here and goes on.
+__device__ __forceinline__ int64_t partial_slot(int p, bool starts) { return 2 * (int64_t)p + (starts ? 1 : 0); }
+
+__device__ __forceinline__ int request_length(const SplitArgs& a, int r) {
+  const int n = a.seq_len[r];
+  return n < 0 ? 0 : n > a.max_len ? a.max_len : n;
 }
 
-// One CTA per (query head, request): each of four warps takes every fourth token with its own
-// running maximum, sum and accumulator; the four join in shared memory.
-template <int D>
-__global__ void __launch_bounds__(128) attention_split_kernel(const SplitArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float sm_m[4], sm_l[4], sm_acc[4][D];
-  pdl_wait_then_release();
-  const int h = blockIdx.x, r = blockIdx.y, kvh = h / a.group;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = request_length(a, r, threadIdx.x == 0);
-  float qv[E], acc[E];
-  for (int e = 0; e < E; ++e) {
-    qv[e] = __uint_as_float((uint32_t)a.q[r * a.q_stride + (int64_t)h * D + lane + 32 * e] << 16);
-    acc[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = warp; j < n; j += 4) {
-    const int2 pg = a.table[((int64_t)r * a.max_len + j) * a.layers + a.layer];
-    const bool ok = pg.x >= 0 && pg.x < a.num_pages && pg.y >= 0 && pg.y < a.num_pages;
-    float s = -INFINITY;
-    if (ok) {
-      const uint16_t* k = a.pool + (int64_t)pg.x * a.H + kvh * D;
-      s = 0.f;
-      for (int e = 0; e < E; ++e) s = fmaf(qv[e], __uint_as_float((uint32_t)k[lane + 32 * e] << 16), s);
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      s *= a.scale_log2;
-      const float mn = fmaxf(m, s);
-      if (mn != -INFINITY || s != s) {
-        const float c = exp2f(m - mn), p = exp2f(s - mn);
-        const uint16_t* v = a.pool + (int64_t)pg.y * a.H + kvh * D;
-        l = l * c + p;
-        for (int e = 0; e < E; ++e)
-          acc[e] = fmaf(p, __uint_as_float((uint32_t)v[lane + 32 * e] << 16), acc[e] * c);
-        m = mn;
+__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+enum : int32_t { kFirst = 1, kLast = 2, kStarts = 4, kEnds = 8 };
+
+// One stage's tokens: which request, where, and which of them have data.
+struct StageInfo {
+  int32_t req, tok, n, flags;
+  uint32_t mask[kWarps];         // per tile: bit i = token i has data
+};
+
+// Where a range begins in the sequence of all requests' units.
+struct RangeStart {
+  int32_t req, tok, units;
+};
+
+// The range [p U / P, (p + 1) U / P) of the U units of all requests (one unit: `st` tokens), by
+// the whole CTA: warps sum the units of 32 requests at a time into `sums`, warp 0 finds the
+// request that holds the first unit.
+__device__ RangeStart find_range(const SplitArgs& a, int p, int st, int32_t* sums64, int32_t* found) {
+  long long* sums = reinterpret_cast<long long*>(sums64);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_sums = (a.n_req + 31) / 32;
+  for (int t = warp; t < n_sums; t += kWarps + 1) {
+    const int r = 32 * t + lane;
+    int n = 0;
+    if (r < a.n_req) {
+      n = a.seq_len[r];
+      if (n < 0 || n > a.max_len) {
+        flag_error(a.err, LORA_DEV_BAD_SEGMENT);
+        n = n < 0 ? 0 : a.max_len;
       }
-    } else if (lane == 0) {
-      flag_error(a.err, LORA_DEV_BAD_PAGE);
     }
-    if (a.ws_scores && lane == 0) a.ws_scores[((int64_t)r * a.n_heads + h) * a.score_stride + j] = s;
+    long long u = (n + (long long)st - 1) / st;
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    if (lane == 0) sums[t] = u;
   }
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-  }
-  for (int e = 0; e < E; ++e) sm_acc[warp][lane + 32 * e] = acc[e];
   __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w]);
-  float c[4];
-  for (int w = 0; w < 4; ++w) {
-    c[w] = sm_m[w] == -INFINITY ? 0.f : exp2f(sm_m[w] - M);
-    L += sm_l[w] * c[w];
+  if (warp == 0) {
+    long long total = 0;
+    for (int t = lane; t < n_sums; t += 32) total += sums[t];
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    // No range between two used ones is empty (the join reads a partial of each): P = min(P, U).
+    const long long P = max(min((long long)a.plan.parts, total), 1ll);
+    const int q0 = min((long long)p, P), q1 = min((long long)p + 1, P);
+    // p U / P without overflow: U = d P + m.
+    const long long d = total / P, m = total % P;
+    const long long u0 = q0 * d + q0 * m / P, u1 = q1 * d + q1 * m / P;
+    long long before = 0;                                // units of the requests looked at so far
+    int tile = 0;
+    for (int t0 = 0; t0 < n_sums; t0 += 32) {            // the block of 32 requests that holds u0
+      const long long mine = t0 + lane < n_sums ? sums[t0 + lane] : 0;
+      long long incl = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > u0);
+      if (hit) {
+        const int k = __ffs(hit) - 1;
+        tile = t0 + k;
+        before += __shfl_sync(0xffffffffu, incl - mine, k);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int r = 32 * tile + lane;
+    const long long mine = r < a.n_req ? (request_length(a, r) + (long long)st - 1) / st : 0;
+    long long incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > u0);
+    const int k = hit ? __ffs(hit) - 1 : 0;
+    const long long off = u0 - (before + __shfl_sync(0xffffffffu, incl - mine, k));
+    if (lane == 0) {
+      found[0] = 32 * tile + k;
+      found[1] = (int32_t)(off * st);
+      found[2] = (int32_t)(u1 - u0);
+    }
   }
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float o = 0.f;
-    for (int w = 0; w < 4; ++w) o += sm_acc[w][d] * c[w];
-    a.out[r * a.out_stride + (int64_t)h * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(L != 0.f ? o / L : 0.f));
-  }
-  if (threadIdx.x == 0) {
-    const float lse2 = L != 0.f ? M + log2f(L) : -INFINITY;
-    a.ws_lse[(int64_t)r * a.n_heads + h] = lse2;
-    if (a.lse) a.lse[(int64_t)r * a.n_heads + h] = lse2 * 0.6931471805599453f;
+  __syncthreads();
+  return RangeStart{found[0], found[1], found[2]};
+}
+
+// Walks a range one unit at a time.
+struct UnitWalk {
+  int32_t req, tok, n, left;
+  bool first;
+};
+__device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   // skip to a request with tokens
+  while (w.left > 0 && w.tok >= w.n) {
+    ++w.req;
+    w.tok = 0;
+    w.n = request_length(a, w.req);
   }
 }
 
-__global__ void __launch_bounds__(256) attention_weights_kernel(const SplitArgs a) {
-  pdl_wait_then_release();
-  const int r = blockIdx.y, n = request_length(a, r, false);
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  if (j >= n) return;
-  float w = 0.f;
-  for (int h = 0; h < a.n_heads; ++h) {
-    const float z = a.ws_lse[(int64_t)r * a.n_heads + h];
-    if (z != -INFINITY) w += exp2f(a.ws_scores[((int64_t)r * a.n_heads + h) * a.score_stride + j] - z);
+// One CTA per (group of KV heads, range).  Warp 8 fills a ring of stages: per stage and token the
+// group's slice of the K row and of the V row (heads x D contiguous bf16) by cp.async.bulk, all
+// against the stage's one mbarrier; page ids are read one stage ahead.  A consumer warp owns one
+// KV head and one 16-token tile of the stage.
+//
+// Per tile the products run on m16n8k16 MMAs with the tokens (or the features) as the 16 rows and
+// the query heads of the KV head as the 8 columns: S^T = K q^T, then acc^T += V^T P^T.  A decode
+// step has at most 16 query rows per KV head, far below the 64 or 128 rows of a tcgen05 tile, and
+// every K and V byte is used once, so the tensor work is small; this layout leaves 1/8 instead of
+// 1/16 of the MMA in use at one query head, and the running maximum, sum and rescaling of a column
+// stay in the lanes that hold the column in both products.  P^T is the transpose of S^T's
+// fragment (movmatrix) as two bf16 terms, hi + lo, so the weights carry 16 mantissa bits.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1) attention_split_kernel(const __grid_constant__ SplitArgs a) {
+  constexpr int KS = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kWarps];
+  __shared__ StageInfo info[kMaxStages];
+  __shared__ int32_t found[4];
+  const SplitPlan& pl = a.plan;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g0 = blockIdx.x % pl.n_groups, p = blockIdx.x / pl.n_groups;
+  const int h0 = g0 * pl.heads, n_act = min(pl.heads, pl.n_kv - h0);
+  const int st = kTile * pl.tiles, S = pl.stages;
+  const uint32_t ring = smem_u32(smem), RB = pl.row_bytes;
+  const uint32_t bar_full = smem_u32(bars), bar_empty = bar_full + 8 * kMaxStages;
+  const uint32_t bar_ready = bar_empty + 8 * kMaxStages, bar_done = bar_ready + 8 * kWarps;
+  uint8_t* after_ring = smem + (size_t)S * pl.stage_bytes;
+  float* merge = reinterpret_cast<float*>(after_ring);     // [heads][group][D + 2]
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, n_act * pl.tiles);
+    }
+    for (int h = 0; h < kWarps; ++h) {
+      mbar_init(bar_ready + 8 * h, 1);
+      mbar_init(bar_done + 8 * h, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  a.weight_out[r * a.weight_stride + j] = (a.weight_in ? a.weight_in[r * a.weight_stride + j] : 0.f) + w;
+  pdl_wait_then_release();
+  RangeStart rs;
+  if (pl.whole) {
+    const int n = a.seq_len[p];
+    if (threadIdx.x == 0 && (n < 0 || n > a.max_len)) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
+    rs = RangeStart{p, 0, (int32_t)(((int64_t)request_length(a, p) + st - 1) / st)};
+    __syncthreads();
+  } else {
+    rs = find_range(a, p, st, reinterpret_cast<int32_t*>(after_ring), found);
+    __syncthreads();                                       // the sums lie where heads are merged later
+  }
+  if (g0 == 0 && threadIdx.x == 0) a.ws_start[p] = make_int4(rs.req, rs.tok, rs.units, 0);
+  // Requests without a token get zeros.
+  for (int r = p; r < a.n_req; r += pl.parts) {
+    if (a.seq_len[r] > 0) continue;
+    const int w = n_act * pl.group * D / 8;
+    uint16_t* row = a.out + r * a.out_stride + (int64_t)h0 * pl.group * D;
+    for (int i = threadIdx.x; i < w; i += kThreads) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int i = threadIdx.x; i < n_act * pl.group; i += kThreads)
+        a.lse[(int64_t)r * a.n_heads + h0 * pl.group + i] = -INFINITY;
+  }
+  if (rs.units == 0) return;
+
+  if (warp == kWarps) {
+    // ---- producer ----
+    const uint32_t bytes = (uint32_t)n_act * D * 2;
+    const int half = lane >> 4, ti = lane & 15;            // lanes 0..15: K pages, 16..31: V pages
+    UnitWalk w{rs.req, rs.tok, request_length(a, rs.req), rs.units, true};
+    walk_begin(a, w);
+    int32_t ids[kWarps];
+    const auto fetch = [&](const UnitWalk& u) {
+#pragma unroll
+      for (int c = 0; c < kWarps; ++c) {
+        ids[c] = -1;
+        const int j = u.tok + kTile * c + ti;
+        if (c < pl.tiles && j < u.n)
+          ids[c] = a.table[((((int64_t)u.req * a.max_len + j) * a.layers) + a.layer) * 2 + half];
+      }
+    };
+    fetch(w);
+    bool ok = true;
+    int it = 0;
+    while (w.left > 0) {
+      const int s = it % S;
+      const UnitWalk cur = w;
+      int32_t page[kWarps];
+#pragma unroll
+      for (int c = 0; c < kWarps; ++c) page[c] = ids[c];
+      // the next unit, and its page ids while this one waits for its stage
+      w.tok += st;
+      --w.left;
+      const bool ends = w.tok >= w.n;
+      const bool last = ends || w.left == 0;
+      walk_begin(a, w);
+      w.first = ends;
+      if (w.left > 0) fetch(w);
+      uint32_t mask[kWarps];
+      int n_valid = 0;
+#pragma unroll
+      for (int c = 0; c < kWarps; ++c) {
+        mask[c] = 0;
+        if (c < pl.tiles) {
+          const bool good = page[c] >= 0 && page[c] < a.num_pages;
+          const uint32_t b = __ballot_sync(0xffffffffu, good);
+          mask[c] = b & (b >> 16) & 0xFFFFu;
+          n_valid += __popc(mask[c]);
+          if (!good && cur.tok + kTile * c + ti < cur.n) flag_error(a.err, LORA_DEV_BAD_PAGE);   // token skipped
+        }
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ((it / S) & 1) ^ 1));
+      if (!ok) break;
+      if (lane == 0) {
+        StageInfo& f = info[s];
+        f.req = cur.req;
+        f.tok = cur.tok;
+        f.n = cur.n;
+        const int begun = cur.req == rs.req ? rs.tok : 0;  // the segment's first token
+        f.flags = (cur.first ? kFirst : 0) | (last ? kLast : 0) | (begun == 0 ? kStarts : 0) | (ends ? kEnds : 0);
+#pragma unroll
+        for (int c = 0; c < kWarps; ++c) f.mask[c] = mask[c];
+        mbar_arrive_expect_tx(bar_full + 8 * s, 2 * bytes * n_valid);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < kWarps; ++c)
+        if (c < pl.tiles && ((mask[c] >> ti) & 1u))
+          bulk_g2s(ring + (uint32_t)s * pl.stage_bytes + (uint32_t)((half * pl.tiles + c) * kTile + ti) * RB,
+                   a.pool + (int64_t)page[c] * a.H + h0 * D, bytes, bar_full + 8 * s);
+      ++it;
+    }
+    if (!ok) {
+      if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
+      // the copies already issued land before this CTA's shared memory is released
+      for (int c = it > S ? it - S : 0; c < it; ++c) (void)mbar_wait(bar_full + 8 * (c % S), (c / S) & 1);
+    }
+    return;
+  }
+
+  // ---- consumers ----
+  const int hh = warp % pl.heads, tile = warp / pl.heads;
+  if (tile >= pl.tiles || hh >= n_act) return;
+  const int g = lane >> 2, t = lane & 3;
+  const int G = pl.group, head0 = (h0 + hh) * G;           // the KV head's first query head
+  uint32_t qf[NT][KS][2];
+  float acc[NT][KS][4], m[NT][2], l[NT][2];
+  // lane addresses of the fragments within a stage
+  const uint32_t k_lane = (uint32_t)(tile * kTile + (lane & 15)) * RB + (uint32_t)(hh * D + (lane >> 4) * 8) * 2;
+  const uint32_t v_lane = (uint32_t)((pl.tiles + tile) * kTile + (lane & 7) + (lane >> 4) * 8) * RB +
+                          (uint32_t)(hh * D + ((lane >> 3) & 1) * 8) * 2;
+  int seg = 0;                                             // segments finished: the phase of the merge barriers
+  int left = rs.units;
+  for (int it = 0; left > 0; ++it, --left) {
+    const int s = it % S;
+    if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, (it / S) & 1))) {
+      if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
+      return;
+    }
+    const int req = info[s].req, n = info[s].n, flags = info[s].flags, j0 = info[s].tok + tile * kTile;
+    const uint32_t mask = info[s].mask[tile];
+    if (flags & kFirst) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const bool has = nt * 8 + g < G;
+        const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + req * a.q_stride + (int64_t)(head0 + nt * 8 + g) * D) + t;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          qf[nt][ks][0] = has ? qp[ks * 8] : 0u;
+          qf[nt][ks][1] = has ? qp[ks * 8 + 4] : 0u;
+          acc[nt][ks][0] = acc[nt][ks][1] = acc[nt][ks][2] = acc[nt][ks][3] = 0.f;
+        }
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+      }
+    }
+    if (j0 < n) {
+      const uint32_t base = ring + (uint32_t)s * pl.stage_bytes;
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t kf[4];
+        ldmatrix_x4(kf, base + k_lane + ks * 32);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16x8x16(sc[nt], kf, qf[nt][ks][0], qf[nt][ks][1]);
+      }
+      const bool v0 = (mask >> g) & 1u, v1 = (mask >> (g + 8)) & 1u;
+      uint32_t ph[NT][2], plo[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        sc[nt][0] = v0 ? sc[nt][0] * a.scale_log2 : -INFINITY;
+        sc[nt][1] = v0 ? sc[nt][1] * a.scale_log2 : -INFINITY;
+        sc[nt][2] = v1 ? sc[nt][2] * a.scale_log2 : -INFINITY;
+        sc[nt][3] = v1 ? sc[nt][3] * a.scale_log2 : -INFINITY;
+        if (a.ws_scores) {
+          float* dst = a.ws_scores + ((int64_t)req * a.n_heads + head0 + nt * 8 + 2 * t) * a.score_stride + j0 + g;
+          if (nt * 8 + 2 * t < G) {
+            dst[0] = sc[nt][0];
+            dst[8] = sc[nt][2];
+          }
+          if (nt * 8 + 2 * t + 1 < G) {
+            dst[a.score_stride] = sc[nt][1];
+            dst[a.score_stride + 8] = sc[nt][3];
+          }
+        }
+        float c[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float x = fmaxf(sc[nt][k], sc[nt][2 + k]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float mn = fmaxf(m[nt][k], x);
+          const float ms = mn == -INFINITY ? 0.f : mn;     // no score above -infinity yet: every weight 0
+          c[k] = exp2f(m[nt][k] - ms);
+          sc[nt][k] = exp2f(sc[nt][k] - ms);
+          sc[nt][2 + k] = exp2f(sc[nt][2 + k] - ms);
+          l[nt][k] = fmaf(l[nt][k], c[k], sc[nt][k] + sc[nt][2 + k]);
+          m[nt][k] = mn;
+        }
+        if (__any_sync(0xffffffffu, c[0] != 1.f || c[1] != 1.f)) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            acc[nt][ks][0] *= c[0];
+            acc[nt][ks][1] *= c[1];
+            acc[nt][ks][2] *= c[0];
+            acc[nt][ks][3] *= c[1];
+          }
+        }
+        const uint32_t h_lo = pack_bf16(sc[nt][0], sc[nt][1]), h_hi = pack_bf16(sc[nt][2], sc[nt][3]);
+        ph[nt][0] = transpose_8x8(h_lo);
+        ph[nt][1] = transpose_8x8(h_hi);
+        plo[nt][0] = transpose_8x8(pack_bf16(sc[nt][0] - bf16_lo(h_lo), sc[nt][1] - bf16_hi(h_lo)));
+        plo[nt][1] = transpose_8x8(pack_bf16(sc[nt][2] - bf16_lo(h_hi), sc[nt][3] - bf16_hi(h_hi)));
+      }
+      // V of a token without data is whatever the stage held before: its bits are cleared.
+      const bool partial = mask != 0xFFFFu;
+      const uint32_t b0 = mask >> (2 * t), b1 = mask >> (2 * t + 8);
+      const uint32_t and0 = ((b0 & 1u) ? 0xFFFFu : 0u) | ((b0 & 2u) ? 0xFFFF0000u : 0u);
+      const uint32_t and1 = ((b1 & 1u) ? 0xFFFFu : 0u) | ((b1 & 2u) ? 0xFFFF0000u : 0u);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t vf[4];
+        ldmatrix_x4_trans(vf, base + v_lane + ks * 32);
+        if (partial) {
+          vf[0] &= and0;
+          vf[1] &= and0;
+          vf[2] &= and1;
+          vf[3] &= and1;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16x8x16(acc[nt][ks], vf, ph[nt][0], ph[nt][1]);
+          mma_16x8x16(acc[nt][ks], vf, plo[nt][0], plo[nt][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+    if (!(flags & kLast)) continue;
+
+    // ---- the segment's end: sum l over the token lanes, join the warps that share the head ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 4);
+        l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 8);
+        l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 16);
+      }
+    if (pl.tiles > 1) {
+      float* mb = merge + (size_t)hh * G * (D + 2);        // [group][D + 2]: acc, m, l
+      // One buffer per head, used by its warps in turn: warp `tile` writes it once the warp before
+      // (or, for the first, the last of the previous segment) has been added, and tile 0 adds it.
+      for (int o = 1; o < pl.tiles; ++o) {
+        const uint32_t ready = bar_ready + 8 * (o * pl.heads + hh);
+        if (tile == o) {
+          const int before = o > 1 ? o - 1 : pl.tiles - 1;
+          const uint32_t parity = o > 1 ? seg & 1 : (seg & 1) ^ 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_done + 8 * (before * pl.heads + hh), parity))) {
+            if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
+            return;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int qi = nt * 8 + 2 * t + k;
+              if (qi >= G) continue;
+#pragma unroll
+              for (int ks = 0; ks < KS; ++ks) {
+                mb[qi * (D + 2) + ks * 16 + g] = acc[nt][ks][k];
+                mb[qi * (D + 2) + ks * 16 + g + 8] = acc[nt][ks][2 + k];
+              }
+              if (g == 0) {
+                mb[qi * (D + 2) + D] = m[nt][k];
+                mb[qi * (D + 2) + D + 1] = l[nt][k];
+              }
+            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ready);
+        } else if (tile == 0) {
+          if (!__all_sync(0xffffffffu, mbar_wait(ready, seg & 1))) {
+            if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
+            return;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int qi = nt * 8 + 2 * t + k;
+              if (qi >= G) continue;
+              const float om = mb[qi * (D + 2) + D], ol = mb[qi * (D + 2) + D + 1];
+              const float mn = fmaxf(m[nt][k], om), ms = mn == -INFINITY ? 0.f : mn;
+              const float c0 = exp2f(m[nt][k] - ms), c1 = exp2f(om - ms);
+              m[nt][k] = mn;
+              l[nt][k] = l[nt][k] * c0 + ol * c1;
+#pragma unroll
+              for (int ks = 0; ks < KS; ++ks) {
+                acc[nt][ks][k] = acc[nt][ks][k] * c0 + mb[qi * (D + 2) + ks * 16 + g] * c1;
+                acc[nt][ks][2 + k] = acc[nt][ks][2 + k] * c0 + mb[qi * (D + 2) + ks * 16 + g + 8] * c1;
+              }
+            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_done + 8 * (o * pl.heads + hh));
+        }
+      }
+      ++seg;
+      if (tile != 0) continue;
+    }
+    const bool starts = flags & kStarts, ends = flags & kEnds;
+    if (g0 == 0 && hh == 0 && lane == 0) {
+      if (starts) a.ws_range[req].x = p;
+      if (ends) a.ws_range[req].y = p;
+    }
+    if (starts && ends) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float i0 = l[nt][0] == 0.f ? 0.f : 1.f / l[nt][0], i1 = l[nt][1] == 0.f ? 0.f : 1.f / l[nt][1];
+        uint16_t* row = a.out + req * a.out_stride + (int64_t)(head0 + nt * 8 + g) * D + 2 * t;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t lo = transpose_8x8(pack_bf16(acc[nt][ks][0] * i0, acc[nt][ks][1] * i1));
+          const uint32_t hi = transpose_8x8(pack_bf16(acc[nt][ks][2] * i0, acc[nt][ks][3] * i1));
+          if (nt * 8 + g < G) {
+            *reinterpret_cast<uint32_t*>(row + ks * 16) = lo;
+            *reinterpret_cast<uint32_t*>(row + ks * 16 + 8) = hi;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int qi = nt * 8 + 2 * t + k;
+          if (g == 0 && qi < G) {
+            const float z = l[nt][k] == 0.f ? -INFINITY : m[nt][k] + log2f(l[nt][k]);
+            a.ws_lse[(int64_t)req * a.n_heads + head0 + qi] = z;
+            if (a.lse) a.lse[(int64_t)req * a.n_heads + head0 + qi] = z * 0.6931471805599453f;
+          }
+        }
+      }
+    } else {
+      const int64_t slot = partial_slot(p, starts) * a.n_heads + head0;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int qi = nt * 8 + 2 * t + k;
+          if (qi >= G) continue;
+          float* dst = a.ws_acc + (slot + qi) * D;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            dst[ks * 16 + g] = acc[nt][ks][k];
+            dst[ks * 16 + g + 8] = acc[nt][ks][2 + k];
+          }
+          if (g == 0) a.ws_ml[slot + qi] = make_float2(m[nt][k], l[nt][k]);
+        }
+    }
+  }
+}
+
+// Joins the requests that span ranges and turns scores into weights.  Block (p, s) of `parts` x
+// `subs` takes the requests of range p: of a request that spans ranges its share of the query
+// heads (a warp per head), and of the range's tokens every subs-th run of 256.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
+  extern __shared__ float lse_s[];                         // [n_heads] with weights
+  constexpr int E = D / 32;
+  pdl_wait_then_release();
+  const int p = blockIdx.x / subs, sub = blockIdx.x % subs;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int st = kTile * a.plan.tiles;
+  const int4 w = a.ws_start[p];
+  int r = w.x, tok = w.y;
+  for (int left = w.z; left > 0;) {
+    const int n = request_length(a, r);
+    if (tok >= n) {
+      ++r;
+      tok = 0;
+      continue;
+    }
+    const int units = min(left, (int)(((int64_t)n - tok + st - 1) / st));
+    const int end = min((int64_t)n, tok + (int64_t)units * st);
+    const int2 range = a.ws_range[r];
+    const bool split = range.x != range.y;
+    if (split) {
+      const int nw = (range.y - range.x + 1) * subs * (kJoinThreads / 32);
+      for (int h = ((p - range.x) * subs + sub) * (kJoinThreads / 32) + warp; h < a.n_heads; h += nw) {
+        float M = -INFINITY;
+        for (int i = range.x + lane; i <= range.y; i += 32)
+          M = fmaxf(M, a.ws_ml[partial_slot(i, i == range.x) * a.n_heads + h].x);
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float ms = M == -INFINITY ? 0.f : M;
+        float L = 0.f, acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int i = range.x; i <= range.y; ++i) {
+          const int64_t slot = partial_slot(i, i == range.x) * a.n_heads + h;
+          const float2 ml = a.ws_ml[slot];
+          const float c = exp2f(ml.x - ms);
+          L = fmaf(ml.y, c, L);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(a.ws_acc[slot * D + e * 32 + lane], c, acc[e]);
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        uint16_t* dst = a.out + r * a.out_stride + (int64_t)h * D;
+#pragma unroll
+        for (int e = 0; e < E; ++e) dst[e * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] * inv));
+        if (a.lse && lane == 0)
+          a.lse[(int64_t)r * a.n_heads + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      }
+    }
+    if (a.weight_out) {
+      __syncthreads();                                     // lse_s of the request before is done with
+      for (int h = threadIdx.x; h < a.n_heads; h += kJoinThreads) {
+        float z;
+        if (split) {
+          float M = -INFINITY, L = 0.f;
+          for (int i = range.x; i <= range.y; ++i) M = fmaxf(M, a.ws_ml[partial_slot(i, i == range.x) * a.n_heads + h].x);
+          const float ms = M == -INFINITY ? 0.f : M;
+          for (int i = range.x; i <= range.y; ++i) {
+            const float2 ml = a.ws_ml[partial_slot(i, i == range.x) * a.n_heads + h];
+            L = fmaf(ml.y, exp2f(ml.x - ms), L);
+          }
+          z = L == 0.f ? -INFINITY : M + log2f(L);
+        } else {
+          z = a.ws_lse[(int64_t)r * a.n_heads + h];
+        }
+        lse_s[h] = z == -INFINITY ? INFINITY : z;          // a row without weight: 2^(s - inf) = 0
+      }
+      __syncthreads();
+      for (int64_t j = tok + (int64_t)sub * kJoinThreads + threadIdx.x; j < end; j += (int64_t)subs * kJoinThreads) {
+        const float* sc = a.ws_scores + (int64_t)r * a.n_heads * a.score_stride + j;
+        float x = 0.f;
+#pragma unroll 8
+        for (int h = 0; h < a.n_heads; ++h) x += exp2f(sc[h * a.score_stride] - lse_s[h]);
+        const int64_t at = r * a.weight_stride + j;
+        a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.f) + x;
+      }
+    }
+    left -= units;
+    tok = end;
+  }
 }
 
 struct SplitLayout {
-  size_t lse, scores, total;
+  size_t lse, range, start, ml, acc, scores, total;
   int64_t score_stride;
 };
 
-SplitLayout split_layout(int32_t n_req, int32_t max_len, int32_t n_heads, bool weights) {
+SplitLayout split_layout(const SplitPlan& pl, int32_t n_req, int32_t max_len, int32_t n_heads, bool weights) {
   SplitLayout L{};
-  L.score_stride = ((int64_t)max_len + 15) / 16 * 16;
+  const size_t slots = pl.whole ? 0 : 2 * (size_t)pl.parts;
+  L.score_stride = ((int64_t)max_len + kTile - 1) / kTile * kTile;
   size_t off = 0;
   L.lse = off;     off = align256(off + (size_t)n_req * n_heads * 4);
+  L.range = off;   off = align256(off + (size_t)n_req * sizeof(int2));
+  L.start = off;   off = align256(off + (size_t)pl.parts * sizeof(int4));
+  L.ml = off;      off = align256(off + slots * n_heads * sizeof(float2));
+  L.acc = off;     off = align256(off + slots * n_heads * pl.D * 4);
   L.scores = off;  off = align256(off + (weights ? (size_t)n_req * n_heads * L.score_stride * 4 : 0));
   L.total = off;
   return L;
+}
+
+SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads, int32_t n_kv) {
+  SplitPlan pl{};
+  pl.n_kv = n_kv;
+  pl.D = H / n_kv;
+  pl.group = n_heads / n_kv;
+  // A stage is 16 tokens' K and V slices of up to 8 heads (4 at D = 256), 64 KB at D >= 128; with
+  // fewer heads the warps take more tokens of each.  Head groups are as even as they can be.
+  const int most = pl.D == 256 ? 4 : 8;
+  pl.n_groups = (n_kv + most - 1) / most;
+  pl.heads = (n_kv + pl.n_groups - 1) / pl.n_groups;
+  pl.tiles = std::max(1, std::min(kWarps / pl.heads, kStageBytes / (4 * kTile * pl.heads * pl.D)));
+  pl.row_bytes = pl.heads * pl.D * 2 + 16;                 // + 16: ldmatrix's 8 rows on 8 bank groups
+  pl.stage_bytes = 2 * kTile * pl.tiles * pl.row_bytes;
+  // behind the ring: the sums of find_range (8 bytes per 32 requests), later the merged heads
+  const int merge = pl.tiles > 1 ? pl.heads * pl.group * (pl.D + 2) * 4 : 0;
+  const int tail = std::max(merge, (n_req + 31) / 32 * 8);
+  pl.stages = std::min(kMaxStages, (kMaxSmem - 4096 - tail) / pl.stage_bytes);
+  pl.smem = pl.stages * pl.stage_bytes + tail;
+  const int sms = device_sm_count();
+  pl.whole = max_len <= kTile * pl.tiles;
+  if (pl.whole) {
+    pl.parts = n_req;
+  } else {
+    // One CTA per SM; where the head groups do not divide the SMs, up to 4 rounds of CTAs.
+    double best = 0;
+    for (int k = 1; k <= 4; ++k) {
+      const int parts = k * sms / pl.n_groups;
+      const double used = (double)parts * pl.n_groups / (k * sms);
+      if (used > best + 0.02) {
+        best = used;
+        pl.parts = parts;
+      }
+    }
+    pl.parts = std::max(pl.parts, 1);
+  }
+  return pl;
 }
 
 // Shape checks shared by the size query and the call; 0 or an error code.
@@ -155,6 +751,27 @@ int check_shape(const char* fn, const lora_pool* p, int32_t n_req, int32_t max_l
   return LORA_OK;
 }
 
+template <int D, int NT>
+int launch_split(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
+  static DeviceFlags flags;
+  const int rc = ensure_smem_attr(flags, &attention_split_kernel<D, NT>, kMaxSmem - 4096, "lora_attention_split");
+  if (rc != LORA_OK) return rc;
+  ProfScope prof(p, LORA_KIND_ATTENTION, st);
+  const cudaError_t e = launch_pdl(!p->prof_on, attention_split_kernel<D, NT>, dim3(a.plan.parts * a.plan.n_groups),
+                                   dim3(kThreads), a.plan.smem, st, a);
+  return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_attention_split launch");
+}
+
+template <int D>
+int launch_join(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
+  // With weights about four blocks per SM share the tokens; a join alone takes one block per range.
+  const int subs = a.weight_out ? std::max(1, 4 * device_sm_count() / a.plan.parts) : 1;
+  ProfScope prof(p, LORA_KIND_ATTENTION, st);
+  const cudaError_t e = launch_pdl(!p->prof_on, attention_join_kernel<D>, dim3(a.plan.parts * subs), dim3(kJoinThreads),
+                                   a.weight_out ? (size_t)a.n_heads * 4 : 0, st, a, subs);
+  return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_attention_split launch");
+}
+
 }  // namespace
 
 extern "C" int64_t lora_attention_split_size(const lora_pool* p, int32_t n_req, int32_t max_len, int32_t n_heads,
@@ -162,7 +779,8 @@ extern "C" int64_t lora_attention_split_size(const lora_pool* p, int32_t n_req, 
   const int rc = check_shape("lora_attention_split_size", p, n_req, max_len, n_heads, n_kv_heads);
   if (rc != LORA_OK) return rc;
   if (p->planning) return lora_fail(LORA_EINVAL, "lora_attention_split_size: planning pool has no device state");
-  return (int64_t)split_layout(n_req, max_len, n_heads, with_weights != 0).total;
+  const SplitPlan pl = split_plan(p->H, n_req, max_len, n_heads, n_kv_heads);
+  return (int64_t)split_layout(pl, n_req, max_len, n_heads, with_weights != 0).total;
 }
 
 extern "C" int lora_attention_split(lora_pool* p, int32_t n_req, const int32_t* table_dev, const int32_t* seq_len_dev,
@@ -195,18 +813,18 @@ extern "C" int lora_attention_split(lora_pool* p, int32_t n_req, const int32_t* 
     return lora_fail(LORA_EINVAL, "lora_attention_split: workspace must be 256-byte aligned");
   if (p->planning) return lora_fail(LORA_EINVAL, "lora_attention_split: planning pool has no device state");
   if (n_req == 0) return LORA_OK;
-  const SplitLayout L = split_layout(n_req, max_len, n_heads, weight_out != nullptr);
+  const SplitPlan pl = split_plan(p->H, n_req, max_len, n_heads, n_kv_heads);
+  const SplitLayout L = split_layout(pl, n_req, max_len, n_heads, weight_out != nullptr);
   if (workspace_bytes < (int64_t)L.total)
     return lora_fail(LORA_EINVAL, "lora_attention_split: workspace has " + std::to_string(workspace_bytes) +
                                       " bytes, needs " + std::to_string(L.total));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int D = p->H / n_kv_heads;
   SplitArgs a{};
   a.pool = static_cast<const uint16_t*>(p->pool_dev);
   a.num_pages = p->num_pages;
   a.H = p->H;
   a.n_req = n_req;
-  a.table = reinterpret_cast<const int2*>(table_dev);
+  a.table = table_dev;
   a.seq_len = seq_len_dev;
   a.max_len = max_len;
   a.layers = layers;
@@ -216,29 +834,27 @@ extern "C" int lora_attention_split(lora_pool* p, int32_t n_req, const int32_t* 
   a.out = static_cast<uint16_t*>(out);
   a.out_stride = out_stride;
   a.n_heads = n_heads;
-  a.group = n_heads / n_kv_heads;
   a.lse = lse;
   a.weight_in = weight_in;
   a.weight_out = weight_out;
   a.weight_stride = weight_stride;
-  a.scale_log2 = 1.4426950408889634f / std::sqrt((float)D);
+  a.scale_log2 = 1.4426950408889634f / std::sqrt((float)pl.D);   // log2(e) / sqrt(D)
+  a.plan = pl;
   char* ws = static_cast<char*>(workspace);
   a.ws_lse = reinterpret_cast<float*>(ws + L.lse);
+  a.ws_range = reinterpret_cast<int2*>(ws + L.range);
+  a.ws_start = reinterpret_cast<int4*>(ws + L.start);
+  a.ws_ml = reinterpret_cast<float2*>(ws + L.ml);
+  a.ws_acc = reinterpret_cast<float*>(ws + L.acc);
   a.ws_scores = weight_out ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
   a.score_stride = L.score_stride;
   a.err = p->d_err;
-  const dim3 grid(n_heads, n_req);
-  cudaError_t e;
-  {
-    ProfScope prof(p, LORA_KIND_ATTENTION, st);
-    if (D == 64) e = launch_pdl(!p->prof_on, attention_split_kernel<64>, grid, dim3(128), 0, st, a);
-    else if (D == 128) e = launch_pdl(!p->prof_on, attention_split_kernel<128>, grid, dim3(128), 0, st, a);
-    else e = launch_pdl(!p->prof_on, attention_split_kernel<256>, grid, dim3(128), 0, st, a);
-  }
-  if (e == cudaSuccess && weight_out) {
-    ProfScope prof(p, LORA_KIND_ATTENTION, st);
-    e = launch_pdl(!p->prof_on, attention_weights_kernel, dim3((unsigned)((max_len + 255) / 256), n_req), dim3(256), 0,
-                   st, a);
-  }
-  return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_attention_split launch");
+  const int rc2 = pl.group <= 8 ? (pl.D == 64 ? launch_split<64, 1>(p, a, st)
+                                   : pl.D == 128 ? launch_split<128, 1>(p, a, st)
+                                                 : launch_split<256, 1>(p, a, st))
+                                : (pl.D == 64 ? launch_split<64, 2>(p, a, st)
+                                   : pl.D == 128 ? launch_split<128, 2>(p, a, st)
+                                                 : launch_split<256, 2>(p, a, st));
+  if (rc2 != LORA_OK || (pl.whole && !weight_out)) return rc2;
+  return pl.D == 64 ? launch_join<64>(p, a, st) : pl.D == 128 ? launch_join<128>(p, a, st) : launch_join<256>(p, a, st);
 }
