@@ -28,19 +28,24 @@
 namespace {
 
 constexpr int kSplitMaxGroup = 16;                  // query heads per KV head
-constexpr int kWarps = 8;                           // consumer warps
+constexpr int kWarps = 4;                           // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);         // + the producer warp
+constexpr int kCtasPerSm = 2;
 constexpr int kTile = 16;                           // tokens a warp takes at a time
-constexpr int kStageBytes = 64 * 1024;              // K and V of a stage, at most
+constexpr int kMaxTiles = 8;                        // 16-token tiles per stage, at most
+constexpr int kStageBytes = 32 * 1024;              // K and V of a stage, at most
 constexpr int kMaxStages = 8;
-constexpr int kMaxSmem = 227 * 1024;
+constexpr int kMaxSmem = (228 * 1024 / kCtasPerSm - 1024) & ~1023;   // a CTA's share, 1 KB of it reserved
+constexpr int kStaticSmem = 1024;                   // barriers and stage records
 constexpr int kJoinThreads = 256;
 
 // How a call is cut: fixed by the shapes, the same for the size query and the launch.
 struct SplitPlan {
   int32_t D, group, n_kv;
   int32_t n_groups, heads;       // groups of KV heads, KV heads per group
-  int32_t tiles;                 // 16-token tiles per stage: so many warps share a head
+  int32_t sharers;               // warps that share a head
+  int32_t tile_sharers;          // of them, those that take a stage's tiles in turn; the rest take turns at stages
+  int32_t tiles;                 // 16-token tiles per stage
   int32_t stages;
   int32_t parts;                 // ranges the token sequence is cut into
   bool whole;                    // one range per request: nothing to join
@@ -125,7 +130,8 @@ enum : int32_t { kFirst = 1, kLast = 2, kStarts = 4, kEnds = 8 };
 // One stage's tokens: which request, where, and which of them have data.
 struct StageInfo {
   int32_t req, tok, n, flags;
-  uint32_t mask[kWarps];         // per tile: bit i = token i has data
+  int32_t next;                  // on a request's last stage here: the request that follows, or -1
+  uint16_t mask[kMaxTiles];      // per tile: bit i = token i has data
 };
 
 // Where a range begins in the sequence of all requests' units.
@@ -133,73 +139,66 @@ struct RangeStart {
   int32_t req, tok, units;
 };
 
-// The range [p U / P, (p + 1) U / P) of the U units of all requests (one unit: `st` tokens), by
-// the whole CTA: warps sum the units of 32 requests at a time into `sums`, warp 0 finds the
-// request that holds the first unit.
-__device__ RangeStart find_range(const SplitArgs& a, int p, int st, int32_t* sums64, int32_t* found) {
-  long long* sums = reinterpret_cast<long long*>(sums64);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_sums = (a.n_req + 31) / 32;
-  for (int t = warp; t < n_sums; t += kWarps + 1) {
-    const int r = 32 * t + lane;
-    int n = 0;
-    if (r < a.n_req) {
-      n = a.seq_len[r];
-      if (n < 0 || n > a.max_len) {
-        flag_error(a.err, LORA_DEV_BAD_SEGMENT);
-        n = n < 0 ? 0 : a.max_len;
-      }
-    }
-    long long u = (n + (long long)st - 1) / st;
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    if (lane == 0) sums[t] = u;
+// Prefix sum over the warp's lanes.
+__device__ __forceinline__ int warp_inclusive(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
   }
-  __syncthreads();
-  if (warp == 0) {
-    long long total = 0;
+  return v;
+}
+
+// The range [p U / P, (p + 1) U / P) of the U units of all requests (one unit: `st` tokens).  Up to
+// 32 requests every warp finds it alone; beyond, the warps sum the units of 32 requests at a time
+// into `sums`, and every warp searches those.  Units fit in 32 bits (checked by the host).
+__device__ RangeStart find_range(const SplitArgs& a, int p, int st, int32_t* sums) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_sums = (a.n_req + 31) / 32;
+  const auto units_of = [&](int r) {
+    if (r >= a.n_req) return 0;
+    const int n = a.seq_len[r];
+    if (n < 0 || n > a.max_len) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
+    return (int)(((long long)(n < 0 ? 0 : n > a.max_len ? a.max_len : n) + st - 1) / st);
+  };
+  int total = 0, mine = 0;
+  if (n_sums == 1) {
+    mine = units_of(lane);
+    total = __reduce_add_sync(0xffffffffu, mine);
+  } else {
+    for (int t = warp; t < n_sums; t += kWarps + 1) {
+      const int u = __reduce_add_sync(0xffffffffu, units_of(32 * t + lane));
+      if (lane == 0) sums[t] = u;
+    }
+    __syncthreads();
     for (int t = lane; t < n_sums; t += 32) total += sums[t];
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    // No range between two used ones is empty (the join reads a partial of each): P = min(P, U).
-    const long long P = max(min((long long)a.plan.parts, total), 1ll);
-    const int q0 = min((long long)p, P), q1 = min((long long)p + 1, P);
-    // p U / P without overflow: U = d P + m.
-    const long long d = total / P, m = total % P;
-    const long long u0 = q0 * d + q0 * m / P, u1 = q1 * d + q1 * m / P;
-    long long before = 0;                                // units of the requests looked at so far
-    int tile = 0;
-    for (int t0 = 0; t0 < n_sums; t0 += 32) {            // the block of 32 requests that holds u0
-      const long long mine = t0 + lane < n_sums ? sums[t0 + lane] : 0;
-      long long incl = mine;
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
+    total = __reduce_add_sync(0xffffffffu, total);
+  }
+  // No range between two used ones is empty (the join reads a partial of each): P = min(P, U).
+  const int P = max(min(a.plan.parts, total), 1);
+  const int q0 = min(p, P), q1 = min(p + 1, P);
+  const int d = total / P, m = total % P;                  // p U / P without overflow: U = d P + m
+  const int u0 = q0 * d + q0 * m / P, u1 = q1 * d + q1 * m / P;
+  int before = 0, tile = 0;                                // units of the requests looked at so far
+  if (n_sums > 1) {
+    for (int t0 = 0; t0 < n_sums; t0 += 32) {              // the block of 32 requests that holds u0
+      const int s = t0 + lane < n_sums ? sums[t0 + lane] : 0;
+      const int incl = warp_inclusive(s, lane);
       const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > u0);
       if (hit) {
         const int k = __ffs(hit) - 1;
         tile = t0 + k;
-        before += __shfl_sync(0xffffffffu, incl - mine, k);
+        before += __shfl_sync(0xffffffffu, incl - s, k);
         break;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    const int r = 32 * tile + lane;
-    const long long mine = r < a.n_req ? (request_length(a, r) + (long long)st - 1) / st : 0;
-    long long incl = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > u0);
-    const int k = hit ? __ffs(hit) - 1 : 0;
-    const long long off = u0 - (before + __shfl_sync(0xffffffffu, incl - mine, k));
-    if (lane == 0) {
-      found[0] = 32 * tile + k;
-      found[1] = (int32_t)(off * st);
-      found[2] = (int32_t)(u1 - u0);
-    }
+    mine = units_of(32 * tile + lane);
   }
-  __syncthreads();
-  return RangeStart{found[0], found[1], found[2]};
+  const int incl = warp_inclusive(mine, lane);
+  const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > u0);
+  const int k = hit ? __ffs(hit) - 1 : 0;
+  const int off = u0 - (before + __shfl_sync(0xffffffffu, incl - mine, k));
+  return RangeStart{32 * tile + k, u1 > u0 ? (int)((long long)off * st) : 0, u1 - u0};
 }
 
 // Walks a range one unit at a time.
@@ -215,10 +214,11 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
   }
 }
 
-// One CTA per (group of KV heads, range).  Warp 8 fills a ring of stages: per stage and token the
-// group's slice of the K row and of the V row (heads x D contiguous bf16) by cp.async.bulk, all
-// against the stage's one mbarrier; page ids are read one stage ahead.  A consumer warp owns one
-// KV head and one 16-token tile of the stage.
+// One CTA per (group of KV heads, range).  The last warp fills a ring of stages: per stage and
+// token the group's slice of the K row and of the V row (heads x D contiguous bf16) by
+// cp.async.bulk, all against the stage's one mbarrier; page ids are read one stage ahead.  A
+// consumer warp owns one KV head and the stages' 16-token tiles, shared out between the warps of the
+// head where there are several.
 //
 // Per tile the products run on m16n8k16 MMAs with the tokens (or the features) as the 16 rows and
 // the query heads of the KV head as the 8 columns: S^T = K q^T, then acc^T += V^T P^T.  A decode
@@ -227,27 +227,30 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
 // 1/16 of the MMA in use at one query head, and the running maximum, sum and rescaling of a column
 // stay in the lanes that hold the column in both products.  P^T is the transpose of S^T's
 // fragment (movmatrix) as two bf16 terms, hi + lo, so the weights carry 16 mantissa bits.
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) attention_split_kernel(const __grid_constant__ SplitArgs a) {
+// A tile's K and V fragments are all in registers before its softmax starts, and the stage is given
+// back then: the chain of a tile (products, shuffles, exponentials) holds up no copy.
+template <int D, int NT, int TILES>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_split_kernel(const __grid_constant__ SplitArgs a) {
   constexpr int KS = D / 16;
+  constexpr int VR = NT == 1 || D < 256 ? (KS < 8 ? KS : 8) : 4;   // V fragments held over the softmax
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kWarps];
   __shared__ StageInfo info[kMaxStages];
-  __shared__ int32_t found[4];
   const SplitPlan& pl = a.plan;
+  const int tile_sharers = pl.tile_sharers;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g0 = blockIdx.x % pl.n_groups, p = blockIdx.x / pl.n_groups;
   const int h0 = g0 * pl.heads, n_act = min(pl.heads, pl.n_kv - h0);
-  const int st = kTile * pl.tiles, S = pl.stages;
+  constexpr int st = kTile * TILES;
+  const int S = pl.stages;
   const uint32_t ring = smem_u32(smem), RB = pl.row_bytes;
   const uint32_t bar_full = smem_u32(bars), bar_empty = bar_full + 8 * kMaxStages;
   const uint32_t bar_ready = bar_empty + 8 * kMaxStages, bar_done = bar_ready + 8 * kWarps;
-  uint8_t* after_ring = smem + (size_t)S * pl.stage_bytes;
-  float* merge = reinterpret_cast<float*>(after_ring);     // [heads][group][D + 2]
+  float* merge = reinterpret_cast<float*>(smem + (size_t)S * pl.stage_bytes);   // [heads][group][D + 2]
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, n_act * pl.tiles);
+      mbar_init(bar_empty + 8 * s, n_act * pl.sharers);
     }
     for (int h = 0; h < kWarps; ++h) {
       mbar_init(bar_ready + 8 * h, 1);
@@ -260,72 +263,66 @@ __global__ void __launch_bounds__(kThreads, 1) attention_split_kernel(const __gr
   if (pl.whole) {
     const int n = a.seq_len[p];
     if (threadIdx.x == 0 && (n < 0 || n > a.max_len)) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
-    rs = RangeStart{p, 0, (int32_t)(((int64_t)request_length(a, p) + st - 1) / st)};
-    __syncthreads();
+    rs = RangeStart{p, 0, (int32_t)(((int64_t)(n < 0 ? 0 : min(n, a.max_len)) + st - 1) / st)};
   } else {
-    rs = find_range(a, p, st, reinterpret_cast<int32_t*>(after_ring), found);
-    __syncthreads();                                       // the sums lie where heads are merged later
+    rs = find_range(a, p, st, reinterpret_cast<int32_t*>(merge));
   }
+  __syncthreads();                                         // barriers set up; the sums lie where heads merge
   if (g0 == 0 && threadIdx.x == 0) a.ws_start[p] = make_int4(rs.req, rs.tok, rs.units, 0);
-  // Requests without a token get zeros.
-  for (int r = p; r < a.n_req; r += pl.parts) {
-    if (a.seq_len[r] > 0) continue;
-    const int w = n_act * pl.group * D / 8;
-    uint16_t* row = a.out + r * a.out_stride + (int64_t)h0 * pl.group * D;
-    for (int i = threadIdx.x; i < w; i += kThreads) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (int i = threadIdx.x; i < n_act * pl.group; i += kThreads)
-        a.lse[(int64_t)r * a.n_heads + h0 * pl.group + i] = -INFINITY;
-  }
-  if (rs.units == 0) return;
 
   if (warp == kWarps) {
     // ---- producer ----
     const uint32_t bytes = (uint32_t)n_act * D * 2;
     const int half = lane >> 4, ti = lane & 15;            // lanes 0..15: K pages, 16..31: V pages
-    UnitWalk w{rs.req, rs.tok, request_length(a, rs.req), rs.units, true};
+    const uint32_t dst0 = ring + (uint32_t)(half * TILES * kTile + ti) * RB;
+    const uint16_t* rows = a.pool + h0 * D;
+    const int64_t unit_step = (int64_t)st * a.layers * 2;
+    UnitWalk w{rs.req, rs.tok, rs.units > 0 ? request_length(a, rs.req) : 0, rs.units, true};
     walk_begin(a, w);
-    int32_t ids[kWarps];
+    const auto entry = [&](const UnitWalk& u) {            // this lane's table entry of a unit's first tile
+      return a.table + ((((int64_t)u.req * a.max_len + u.tok + ti) * a.layers) + a.layer) * 2 + half;
+    };
+    const int32_t* tab = entry(w);
+    int32_t ids[TILES];
     const auto fetch = [&](const UnitWalk& u) {
 #pragma unroll
-      for (int c = 0; c < kWarps; ++c) {
-        ids[c] = -1;
-        const int j = u.tok + kTile * c + ti;
-        if (c < pl.tiles && j < u.n)
-          ids[c] = a.table[((((int64_t)u.req * a.max_len + j) * a.layers) + a.layer) * 2 + half];
-      }
+      for (int c = 0; c < TILES; ++c)
+        ids[c] = u.tok + kTile * c + ti < u.n ? tab[(int64_t)c * kTile * a.layers * 2] : -1;
     };
-    fetch(w);
+    if (w.left > 0) fetch(w);
     bool ok = true;
-    int it = 0;
+    int it = 0, s = 0;
+    uint32_t phase = 1;                                    // of the ring's first round: nothing to wait for
     while (w.left > 0) {
-      const int s = it % S;
       const UnitWalk cur = w;
-      int32_t page[kWarps];
+      int32_t page[TILES];
 #pragma unroll
-      for (int c = 0; c < kWarps; ++c) page[c] = ids[c];
+      for (int c = 0; c < TILES; ++c) page[c] = ids[c];
       // the next unit, and its page ids while this one waits for its stage
       w.tok += st;
       --w.left;
+      tab += unit_step;
       const bool ends = w.tok >= w.n;
       const bool last = ends || w.left == 0;
-      walk_begin(a, w);
       w.first = ends;
-      if (w.left > 0) fetch(w);
-      uint32_t mask[kWarps];
+      if (w.left > 0) {
+        if (ends) {
+          walk_begin(a, w);
+          tab = entry(w);
+        }
+        fetch(w);
+      }
+      uint32_t mask[TILES];
       int n_valid = 0;
 #pragma unroll
-      for (int c = 0; c < kWarps; ++c) {
-        mask[c] = 0;
-        if (c < pl.tiles) {
-          const bool good = page[c] >= 0 && page[c] < a.num_pages;
-          const uint32_t b = __ballot_sync(0xffffffffu, good);
-          mask[c] = b & (b >> 16) & 0xFFFFu;
-          n_valid += __popc(mask[c]);
-          if (!good && cur.tok + kTile * c + ti < cur.n) flag_error(a.err, LORA_DEV_BAD_PAGE);   // token skipped
-        }
+      for (int c = 0; c < TILES; ++c) {
+        const bool good = page[c] >= 0 && page[c] < a.num_pages;
+        const uint32_t b = __ballot_sync(0xffffffffu, good);
+        mask[c] = b & (b >> 16) & 0xFFFFu;
+        n_valid += __popc(mask[c]);
+        if (!good && cur.tok + kTile * c + ti < cur.n) flag_error(a.err, LORA_DEV_BAD_PAGE);   // token skipped
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ((it / S) & 1) ^ 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, phase));
       if (!ok) break;
       if (lane == 0) {
         StageInfo& f = info[s];
@@ -334,82 +331,136 @@ __global__ void __launch_bounds__(kThreads, 1) attention_split_kernel(const __gr
         f.n = cur.n;
         const int begun = cur.req == rs.req ? rs.tok : 0;  // the segment's first token
         f.flags = (cur.first ? kFirst : 0) | (last ? kLast : 0) | (begun == 0 ? kStarts : 0) | (ends ? kEnds : 0);
+        f.next = w.left > 0 ? w.req : -1;
 #pragma unroll
-        for (int c = 0; c < kWarps; ++c) f.mask[c] = mask[c];
+        for (int c = 0; c < TILES; ++c) f.mask[c] = (uint16_t)mask[c];
         mbar_arrive_expect_tx(bar_full + 8 * s, 2 * bytes * n_valid);
       }
       __syncwarp();
 #pragma unroll
-      for (int c = 0; c < kWarps; ++c)
-        if (c < pl.tiles && ((mask[c] >> ti) & 1u))
-          bulk_g2s(ring + (uint32_t)s * pl.stage_bytes + (uint32_t)((half * pl.tiles + c) * kTile + ti) * RB,
-                   a.pool + (int64_t)page[c] * a.H + h0 * D, bytes, bar_full + 8 * s);
+      for (int c = 0; c < TILES; ++c)
+        if ((mask[c] >> ti) & 1u)
+          bulk_g2s(dst0 + (uint32_t)s * pl.stage_bytes + (uint32_t)(c * kTile) * RB, rows + (int64_t)page[c] * a.H, bytes,
+                   bar_full + 8 * s);
       ++it;
+      if (++s == S) {
+        s = 0;
+        phase ^= 1;
+      }
     }
     if (!ok) {
       if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
       // the copies already issued land before this CTA's shared memory is released
       for (int c = it > S ? it - S : 0; c < it; ++c) (void)mbar_wait(bar_full + 8 * (c % S), (c / S) & 1);
     }
+    // Requests without a token get zeros.
+    for (int r = p; r < a.n_req; r += pl.parts) {
+      if (a.seq_len[r] > 0) continue;
+      uint16_t* row = a.out + r * a.out_stride + (int64_t)h0 * pl.group * D;
+      for (int i = lane; i < n_act * pl.group * D / 8; i += 32) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int i = lane; i < n_act * pl.group; i += 32) a.lse[(int64_t)r * a.n_heads + h0 * pl.group + i] = -INFINITY;
+    }
     return;
   }
 
   // ---- consumers ----
-  const int hh = warp % pl.heads, tile = warp / pl.heads;
-  if (tile >= pl.tiles || hh >= n_act) return;
+  const int hh = warp % pl.heads, share = warp / pl.heads;
+  if (share >= pl.sharers || hh >= n_act || rs.units == 0) return;
   const int g = lane >> 2, t = lane & 3;
   const int G = pl.group, head0 = (h0 + hh) * G;           // the KV head's first query head
   uint32_t qf[NT][KS][2];
   float acc[NT][KS][4], m[NT][2], l[NT][2];
-  // lane addresses of the fragments within a stage
-  const uint32_t k_lane = (uint32_t)(tile * kTile + (lane & 15)) * RB + (uint32_t)(hh * D + (lane >> 4) * 8) * 2;
-  const uint32_t v_lane = (uint32_t)((pl.tiles + tile) * kTile + (lane & 7) + (lane >> 4) * 8) * RB +
+  const auto load_q = [&](int req) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool has = nt * 8 + g < G;
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + req * a.q_stride + (int64_t)(head0 + nt * 8 + g) * D) + t;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[nt][ks][0] = has ? qp[ks * 8] : 0u;
+        qf[nt][ks][1] = has ? qp[ks * 8 + 4] : 0u;
+      }
+    }
+  };
+  // lane addresses of the fragments within a tile
+  const uint32_t k_lane = (uint32_t)(lane & 15) * RB + (uint32_t)(hh * D + (lane >> 4) * 8) * 2;
+  const uint32_t v_lane = (uint32_t)(TILES * kTile + (lane & 7) + (lane >> 4) * 8) * RB +
                           (uint32_t)(hh * D + ((lane >> 3) & 1) * 8) * 2;
+  const int turns = pl.sharers / tile_sharers, turn = share / tile_sharers;
   int seg = 0;                                             // segments finished: the phase of the merge barriers
-  int left = rs.units;
-  for (int it = 0; left > 0; ++it, --left) {
-    const int s = it % S;
-    if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, (it / S) & 1))) {
+  bool have_q = false;
+  int next_s = 0, next_turn = 0;
+  uint32_t phase = 0;
+  for (int left = rs.units; left > 0; --left) {
+    const int s = next_s;
+    if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, phase))) {
       if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
       return;
     }
-    const int req = info[s].req, n = info[s].n, flags = info[s].flags, j0 = info[s].tok + tile * kTile;
-    const uint32_t mask = info[s].mask[tile];
+    if (++next_s == S) {
+      next_s = 0;
+      phase ^= 1;
+    }
+    const bool mine = next_turn == turn;
+    if (++next_turn == turns) next_turn = 0;
+    const int req = info[s].req, n = info[s].n, flags = info[s].flags, tok = info[s].tok, next = info[s].next;
+    __syncwarp();
     if (flags & kFirst) {
+      if (!have_q) load_q(req);
+      have_q = true;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const bool has = nt * 8 + g < G;
-        const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + req * a.q_stride + (int64_t)(head0 + nt * 8 + g) * D) + t;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          qf[nt][ks][0] = has ? qp[ks * 8] : 0u;
-          qf[nt][ks][1] = has ? qp[ks * 8 + 4] : 0u;
-          acc[nt][ks][0] = acc[nt][ks][1] = acc[nt][ks][2] = acc[nt][ks][3] = 0.f;
-        }
+        for (int ks = 0; ks < KS; ++ks) acc[nt][ks][0] = acc[nt][ks][1] = acc[nt][ks][2] = acc[nt][ks][3] = 0.f;
         m[nt][0] = m[nt][1] = -INFINITY;
         l[nt][0] = l[nt][1] = 0.f;
       }
     }
-    if (j0 < n) {
-      const uint32_t base = ring + (uint32_t)s * pl.stage_bytes;
-      float sc[NT][4];
+    if (!mine && lane == 0) mbar_arrive(bar_empty + 8 * s);
+    for (int tile = mine ? share % tile_sharers : TILES; tile < TILES; tile += tile_sharers) {
+      const int j0 = tok + tile * kTile;
+      const bool final_tile = tile + tile_sharers >= TILES;
+      if (j0 >= n) {
+        if (final_tile) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+        }
+        continue;
+      }
+      const uint32_t mask = info[s].mask[tile];
+      const uint32_t base = ring + (uint32_t)s * pl.stage_bytes + (uint32_t)(tile * kTile) * RB;
+      float sc[NT][4], odd[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uint32_t kf[4];
-        ldmatrix_x4(kf, base + k_lane + ks * 32);
+        for (int i = 0; i < 4; ++i) sc[nt][i] = odd[nt][i] = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16x8x16(sc[nt], kf, qf[nt][ks][0], qf[nt][ks][1]);
+      for (int k0 = 0; k0 < KS; k0 += 4) {
+        uint32_t kf[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ldmatrix_x4(kf[k], base + k_lane + (k0 + k) * 32);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_16x8x16(k & 1 ? odd[nt] : sc[nt], kf[k], qf[nt][k0 + k][0], qf[nt][k0 + k][1]);
+      }
+      uint32_t vf[VR][4];
+#pragma unroll
+      for (int k = 0; k < VR; ++k) ldmatrix_x4_trans(vf[k], base + v_lane + k * 32);
+      if (VR == KS && final_tile) {                        // everything of the stage is in registers
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_empty + 8 * s);
       }
       const bool v0 = (mask >> g) & 1u, v1 = (mask >> (g + 8)) & 1u;
       uint32_t ph[NT][2], plo[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        sc[nt][0] = v0 ? sc[nt][0] * a.scale_log2 : -INFINITY;
-        sc[nt][1] = v0 ? sc[nt][1] * a.scale_log2 : -INFINITY;
-        sc[nt][2] = v1 ? sc[nt][2] * a.scale_log2 : -INFINITY;
-        sc[nt][3] = v1 ? sc[nt][3] * a.scale_log2 : -INFINITY;
+        sc[nt][0] = v0 ? (sc[nt][0] + odd[nt][0]) * a.scale_log2 : -INFINITY;
+        sc[nt][1] = v0 ? (sc[nt][1] + odd[nt][1]) * a.scale_log2 : -INFINITY;
+        sc[nt][2] = v1 ? (sc[nt][2] + odd[nt][2]) * a.scale_log2 : -INFINITY;
+        sc[nt][3] = v1 ? (sc[nt][3] + odd[nt][3]) * a.scale_log2 : -INFINITY;
         if (a.ws_scores) {
           float* dst = a.ws_scores + ((int64_t)req * a.n_heads + head0 + nt * 8 + 2 * t) * a.score_stride + j0 + g;
           if (nt * 8 + 2 * t < G) {
@@ -457,27 +508,37 @@ __global__ void __launch_bounds__(kThreads, 1) attention_split_kernel(const __gr
       const uint32_t and0 = ((b0 & 1u) ? 0xFFFFu : 0u) | ((b0 & 2u) ? 0xFFFF0000u : 0u);
       const uint32_t and1 = ((b1 & 1u) ? 0xFFFFu : 0u) | ((b1 & 2u) ? 0xFFFF0000u : 0u);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uint32_t vf[4];
-        ldmatrix_x4_trans(vf, base + v_lane + ks * 32);
+      for (int k0 = 0; k0 < KS; k0 += VR) {
+        if (k0 > 0) {
+#pragma unroll
+          for (int k = 0; k < VR; ++k) ldmatrix_x4_trans(vf[k], base + v_lane + (k0 + k) * 32);
+        }
         if (partial) {
-          vf[0] &= and0;
-          vf[1] &= and0;
-          vf[2] &= and1;
-          vf[3] &= and1;
+#pragma unroll
+          for (int k = 0; k < VR; ++k) {
+            vf[k][0] &= and0;
+            vf[k][1] &= and0;
+            vf[k][2] &= and1;
+            vf[k][3] &= and1;
+          }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_16x8x16(acc[nt][ks], vf, ph[nt][0], ph[nt][1]);
-          mma_16x8x16(acc[nt][ks], vf, plo[nt][0], plo[nt][1]);
+#pragma unroll
+          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[nt][k0 + k], vf[k], ph[nt][0], ph[nt][1]);
+#pragma unroll
+          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[nt][k0 + k], vf[k], plo[nt][0], plo[nt][1]);
         }
       }
+      if (VR < KS && final_tile) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+      }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_empty + 8 * s);
     if (!(flags & kLast)) continue;
 
     // ---- the segment's end: sum l over the token lanes, join the warps that share the head ----
+    if (next >= 0) load_q(next);                           // on its way while this segment is finished
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -486,14 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_split_kernel(const __gr
         l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 8);
         l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 16);
       }
-    if (pl.tiles > 1) {
+    if (pl.sharers > 1) {
       float* mb = merge + (size_t)hh * G * (D + 2);        // [group][D + 2]: acc, m, l
-      // One buffer per head, used by its warps in turn: warp `tile` writes it once the warp before
-      // (or, for the first, the last of the previous segment) has been added, and tile 0 adds it.
-      for (int o = 1; o < pl.tiles; ++o) {
+      // One buffer per head, used by its warps in turn: warp `share` writes it once the warp before
+      // (or, for the first, the last of the previous segment) has been added, and share 0 adds it.
+      for (int o = 1; o < pl.sharers; ++o) {
         const uint32_t ready = bar_ready + 8 * (o * pl.heads + hh);
-        if (tile == o) {
-          const int before = o > 1 ? o - 1 : pl.tiles - 1;
+        if (share == o) {
+          const int before = o > 1 ? o - 1 : pl.sharers - 1;
           const uint32_t parity = o > 1 ? seg & 1 : (seg & 1) ^ 1;
           if (!__all_sync(0xffffffffu, mbar_wait(bar_done + 8 * (before * pl.heads + hh), parity))) {
             if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
@@ -517,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_split_kernel(const __gr
             }
           __syncwarp();
           if (lane == 0) mbar_arrive(ready);
-        } else if (tile == 0) {
+        } else if (share == 0) {
           if (!__all_sync(0xffffffffu, mbar_wait(ready, seg & 1))) {
             if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
             return;
@@ -544,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_split_kernel(const __gr
         }
       }
       ++seg;
-      if (tile != 0) continue;
+      if (share != 0) continue;
     }
     const bool starts = flags & kStarts, ends = flags & kEnds;
     if (g0 == 0 && hh == 0 && lane == 0) {
@@ -595,12 +656,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_split_kernel(const __gr
   }
 }
 
-// Joins the requests that span ranges and turns scores into weights.  Block (p, s) of `parts` x
+// m and L = sum l_i 2^(m_i - m) of the partials of (request, head) in ranges [p0, p1], by one warp.
+__device__ __forceinline__ float2 join_ml(const SplitArgs& a, int p0, int p1, int h, int lane) {
+  float M = -INFINITY, L = 0.f;
+  for (int i = p0 + lane; i <= p1; i += 32) {
+    const float2 ml = a.ws_ml[partial_slot(i, i == p0) * a.n_heads + h];
+    const float mn = fmaxf(M, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+    L = L * exp2f(M - ms) + ml.y * exp2f(ml.x - ms);
+    M = mn;
+  }
+  float m = M;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  L *= exp2f(M - (m == -INFINITY ? 0.f : m));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  return make_float2(m, L);
+}
+
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinBatch = 4;                              // partials whose loads are in flight together
+
+// Joins the requests that span ranges and turns scores into weights.  Block (p, sub) of `parts` x
 // `subs` takes the requests of range p: of a request that spans ranges its share of the query
-// heads (a warp per head), and of the range's tokens every subs-th run of 256.
+// heads (up to 8 partials a warp per head, beyond that the whole block), and of the range's tokens
+// every subs-th run of 256.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
   extern __shared__ float lse_s[];                         // [n_heads] with weights
+  __shared__ float part[kJoinWarps][D];
   constexpr int E = D / 32;
   pdl_wait_then_release();
   const int p = blockIdx.x / subs, sub = blockIdx.x % subs;
@@ -618,52 +702,66 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
     const int units = min(left, (int)(((int64_t)n - tok + st - 1) / st));
     const int end = min((int64_t)n, tok + (int64_t)units * st);
     const int2 range = a.ws_range[r];
-    const bool split = range.x != range.y;
-    if (split) {
-      const int nw = (range.y - range.x + 1) * subs * (kJoinThreads / 32);
-      for (int h = ((p - range.x) * subs + sub) * (kJoinThreads / 32) + warp; h < a.n_heads; h += nw) {
-        float M = -INFINITY;
-        for (int i = range.x + lane; i <= range.y; i += 32)
-          M = fmaxf(M, a.ws_ml[partial_slot(i, i == range.x) * a.n_heads + h].x);
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float ms = M == -INFINITY ? 0.f : M;
-        float L = 0.f, acc[E];
+    const int np = range.y - range.x + 1;
+    if (np > 1) {
+      const bool wide = np > kJoinWarps;                   // a block per head, its warps share the partials
+      const int block = (p - range.x) * subs + sub, blocks = np * subs;
+      const int step = wide ? blocks : blocks * kJoinWarps;
+      for (int h = wide ? block : block * kJoinWarps + warp; h < a.n_heads; h += step) {
+        const float2 ml = join_ml(a, range.x, range.y, h, lane);
+        const float ms = ml.x == -INFINITY ? 0.f : ml.x;
+        float acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-        for (int i = range.x; i <= range.y; ++i) {
-          const int64_t slot = partial_slot(i, i == range.x) * a.n_heads + h;
-          const float2 ml = a.ws_ml[slot];
-          const float c = exp2f(ml.x - ms);
-          L = fmaf(ml.y, c, L);
+        const int inc = wide ? kJoinWarps : 1;
+        for (int i0 = range.x + (wide ? warp : 0); i0 <= range.y; i0 += kJoinBatch * inc) {
+          float x[kJoinBatch][E], c[kJoinBatch];
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(a.ws_acc[slot * D + e * 32 + lane], c, acc[e]);
+          for (int b = 0; b < kJoinBatch; ++b) {
+            const int i = i0 + b * inc;
+            const bool in = i <= range.y;
+            const int64_t slot = partial_slot(in ? i : range.y, (in ? i : range.y) == range.x) * a.n_heads + h;
+            c[b] = in ? a.ws_ml[slot].x : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[b][e] = in ? a.ws_acc[slot * D + e * 32 + lane] : 0.f;
+          }
+#pragma unroll
+          for (int b = 0; b < kJoinBatch; ++b) {
+            const float f = exp2f(c[b] - ms);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(x[b][e], f, acc[e]);
+          }
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        if (wide) {
+          __syncthreads();
+#pragma unroll
+          for (int e = 0; e < E; ++e) part[warp][e * 32 + lane] = acc[e];
+          __syncthreads();
+          if (warp != 0) continue;
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            for (int v = 1; v < kJoinWarps; ++v) acc[e] += part[v][e * 32 + lane];
+        }
+        const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
         uint16_t* dst = a.out + r * a.out_stride + (int64_t)h * D;
 #pragma unroll
         for (int e = 0; e < E; ++e) dst[e * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] * inv));
         if (a.lse && lane == 0)
-          a.lse[(int64_t)r * a.n_heads + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          a.lse[(int64_t)r * a.n_heads + h] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
       }
     }
     if (a.weight_out) {
       __syncthreads();                                     // lse_s of the request before is done with
-      for (int h = threadIdx.x; h < a.n_heads; h += kJoinThreads) {
-        float z;
-        if (split) {
-          float M = -INFINITY, L = 0.f;
-          for (int i = range.x; i <= range.y; ++i) M = fmaxf(M, a.ws_ml[partial_slot(i, i == range.x) * a.n_heads + h].x);
-          const float ms = M == -INFINITY ? 0.f : M;
-          for (int i = range.x; i <= range.y; ++i) {
-            const float2 ml = a.ws_ml[partial_slot(i, i == range.x) * a.n_heads + h];
-            L = fmaf(ml.y, exp2f(ml.x - ms), L);
-          }
-          z = L == 0.f ? -INFINITY : M + log2f(L);
-        } else {
-          z = a.ws_lse[(int64_t)r * a.n_heads + h];
+      if (np > 1) {
+        for (int h = warp; h < a.n_heads; h += kJoinWarps) {
+          const float2 ml = join_ml(a, range.x, range.y, h, lane);
+          if (lane == 0) lse_s[h] = ml.y == 0.f ? INFINITY : ml.x + log2f(ml.y);
         }
-        lse_s[h] = z == -INFINITY ? INFINITY : z;          // a row without weight: 2^(s - inf) = 0
+      } else {
+        for (int h = threadIdx.x; h < a.n_heads; h += kJoinThreads) {
+          const float z = a.ws_lse[(int64_t)r * a.n_heads + h];
+          lse_s[h] = z == -INFINITY ? INFINITY : z;        // a row without weight: 2^(s - inf) = 0
+        }
       }
       __syncthreads();
       for (int64_t j = tok + (int64_t)sub * kJoinThreads + threadIdx.x; j < end; j += (int64_t)subs * kJoinThreads) {
@@ -705,25 +803,28 @@ SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads,
   pl.n_kv = n_kv;
   pl.D = H / n_kv;
   pl.group = n_heads / n_kv;
-  // A stage is 16 tokens' K and V slices of up to 8 heads (4 at D = 256), 64 KB at D >= 128; with
-  // fewer heads the warps take more tokens of each.  Head groups are as even as they can be.
-  const int most = pl.D == 256 ? 4 : 8;
+  // Head groups as even as they can be: a stage's K and V fit kStageBytes with 16 tokens, a warp has
+  // one head, and with fewer heads than warps some warps share a head and the stage has more tokens.
+  const int most = std::max(1, std::min(kWarps, kStageBytes / (4 * kTile * pl.D)));
   pl.n_groups = (n_kv + most - 1) / most;
   pl.heads = (n_kv + pl.n_groups - 1) / pl.n_groups;
-  pl.tiles = std::max(1, std::min(kWarps / pl.heads, kStageBytes / (4 * kTile * pl.heads * pl.D)));
+  const int room = kStageBytes / (4 * kTile * pl.heads * pl.D);
+  pl.sharers = kWarps / pl.heads;                          // a power of two where it is not 1, as is room then
+  pl.tile_sharers = std::min(pl.sharers, room);
+  pl.tiles = std::min(room / pl.tile_sharers, kMaxTiles / pl.tile_sharers) * pl.tile_sharers;
   pl.row_bytes = pl.heads * pl.D * 2 + 16;                 // + 16: ldmatrix's 8 rows on 8 bank groups
   pl.stage_bytes = 2 * kTile * pl.tiles * pl.row_bytes;
-  // behind the ring: the sums of find_range (8 bytes per 32 requests), later the merged heads
-  const int merge = pl.tiles > 1 ? pl.heads * pl.group * (pl.D + 2) * 4 : 0;
-  const int tail = std::max(merge, (n_req + 31) / 32 * 8);
-  pl.stages = std::min(kMaxStages, (kMaxSmem - 4096 - tail) / pl.stage_bytes);
+  // behind the ring: the sums of find_range (4 bytes per 32 requests), later the merged heads
+  const int merge = pl.sharers > 1 ? pl.heads * pl.group * (pl.D + 2) * 4 : 0;
+  const int tail = std::max(merge, (n_req + 31) / 32 * 4);
+  pl.stages = std::min(kMaxStages, (kMaxSmem - kStaticSmem - tail) / pl.stage_bytes);
   pl.smem = pl.stages * pl.stage_bytes + tail;
-  const int sms = device_sm_count();
+  const int sms = device_sm_count() * kCtasPerSm;
   pl.whole = max_len <= kTile * pl.tiles;
   if (pl.whole) {
     pl.parts = n_req;
   } else {
-    // One CTA per SM; where the head groups do not divide the SMs, up to 4 rounds of CTAs.
+    // As many CTAs as run at once; where the head groups do not divide the SMs, up to 4 rounds of CTAs.
     double best = 0;
     for (int k = 1; k <= 4; ++k) {
       const int parts = k * sms / pl.n_groups;
@@ -751,21 +852,33 @@ int check_shape(const char* fn, const lora_pool* p, int32_t n_req, int32_t max_l
   return LORA_OK;
 }
 
-template <int D, int NT>
+template <int D, int NT, int TILES>
 int launch_split(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   static DeviceFlags flags;
-  const int rc = ensure_smem_attr(flags, &attention_split_kernel<D, NT>, kMaxSmem - 4096, "lora_attention_split");
+  const int rc = ensure_smem_attr(flags, &attention_split_kernel<D, NT, TILES>, kMaxSmem - kStaticSmem, "lora_attention_split");
   if (rc != LORA_OK) return rc;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
-  const cudaError_t e = launch_pdl(!p->prof_on, attention_split_kernel<D, NT>, dim3(a.plan.parts * a.plan.n_groups),
+  const cudaError_t e = launch_pdl(!p->prof_on, attention_split_kernel<D, NT, TILES>, dim3(a.plan.parts * a.plan.n_groups),
                                    dim3(kThreads), a.plan.smem, st, a);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_attention_split launch");
 }
 
+// The kernel of a head width, by the query heads per KV head and the tiles per stage (the three
+// counts that split_plan gives for 3 or 4, 2 and 1 heads per group).
+template <int D, int T0, int T1, int T2>
+int launch_split_d(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
+  const bool one = a.plan.group <= 8;
+  switch (a.plan.tiles) {
+    case T0: return one ? launch_split<D, 1, T0>(p, a, st) : launch_split<D, 2, T0>(p, a, st);
+    case T1: return one ? launch_split<D, 1, T1>(p, a, st) : launch_split<D, 2, T1>(p, a, st);
+    case T2 != T1 ? T2 : -1: return one ? launch_split<D, 1, T2>(p, a, st) : launch_split<D, 2, T2>(p, a, st);
+  }
+  return lora_fail(LORA_EINVAL, "lora_attention_split: no kernel for this geometry");
+}
+
 template <int D>
 int launch_join(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
-  // With weights about four blocks per SM share the tokens; a join alone takes one block per range.
-  const int subs = a.weight_out ? std::max(1, 4 * device_sm_count() / a.plan.parts) : 1;
+  const int subs = std::max(1, 4 * device_sm_count() / a.plan.parts);   // about four blocks per SM
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
   const cudaError_t e = launch_pdl(!p->prof_on, attention_join_kernel<D>, dim3(a.plan.parts * subs), dim3(kJoinThreads),
                                    a.weight_out ? (size_t)a.n_heads * 4 : 0, st, a, subs);
@@ -849,12 +962,9 @@ extern "C" int lora_attention_split(lora_pool* p, int32_t n_req, const int32_t* 
   a.ws_scores = weight_out ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
   a.score_stride = L.score_stride;
   a.err = p->d_err;
-  const int rc2 = pl.group <= 8 ? (pl.D == 64 ? launch_split<64, 1>(p, a, st)
-                                   : pl.D == 128 ? launch_split<128, 1>(p, a, st)
-                                                 : launch_split<256, 1>(p, a, st))
-                                : (pl.D == 64 ? launch_split<64, 2>(p, a, st)
-                                   : pl.D == 128 ? launch_split<128, 2>(p, a, st)
-                                                 : launch_split<256, 2>(p, a, st));
+  const int rc2 = pl.D == 64 ? launch_split_d<64, 2, 4, 8>(p, a, st)
+                  : pl.D == 128 ? launch_split_d<128, 1, 2, 4>(p, a, st)
+                                : launch_split_d<256, 1, 2, 2>(p, a, st);
   if (rc2 != LORA_OK || (pl.whole && !weight_out)) return rc2;
   return pl.D == 64 ? launch_join<64>(p, a, st) : pl.D == 128 ? launch_join<128>(p, a, st) : launch_join<256>(p, a, st);
 }
