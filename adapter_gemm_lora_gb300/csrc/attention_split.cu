@@ -37,7 +37,8 @@ constexpr int kStageBytes = 32 * 1024;              // K and V of a stage, at mo
 constexpr int kMaxStages = 8;
 constexpr int kMaxSmem = (228 * 1024 / kCtasPerSm - 1024) & ~1023;   // a CTA's share, 1 KB of it reserved
 constexpr int kStaticSmem = 1024;                   // barriers and stage records
-constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = 4;
+constexpr int kJoinUnit = 32;                       // tokens whose weights a block takes at a time
 
 // How a call is cut: fixed by the shapes, the same for the size query and the launch.
 struct SplitPlan {
@@ -149,10 +150,11 @@ __device__ __forceinline__ int warp_inclusive(int v, int lane) {
   return v;
 }
 
-// The range [p U / P, (p + 1) U / P) of the U units of all requests (one unit: `st` tokens).  Up to
-// 32 requests every warp finds it alone; beyond, the warps sum the units of 32 requests at a time
-// into `sums`, and every warp searches those.  Units fit in 32 bits (checked by the host).
-__device__ RangeStart find_range(const SplitArgs& a, int p, int st, int32_t* sums) {
+// The range [p U / P, (p + 1) U / P) of the U units of all requests (one unit: `st` tokens), with
+// P = min(parts, U).  Up to 32 requests every warp finds it alone; beyond, the block's warps sum the
+// units of 32 requests at a time into `sums`, and every warp searches those.  Units fit in 32 bits
+// (checked by the host).
+__device__ RangeStart find_range(const SplitArgs& a, int p, int parts, int st, int32_t* sums) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_sums = (a.n_req + 31) / 32;
   const auto units_of = [&](int r) {
     if (r >= a.n_req) return 0;
@@ -165,7 +167,7 @@ __device__ RangeStart find_range(const SplitArgs& a, int p, int st, int32_t* sum
     mine = units_of(lane);
     total = __reduce_add_sync(0xffffffffu, mine);
   } else {
-    for (int t = warp; t < n_sums; t += kWarps + 1) {
+    for (int t = warp; t < n_sums; t += blockDim.x >> 5) {
       const int u = __reduce_add_sync(0xffffffffu, units_of(32 * t + lane));
       if (lane == 0) sums[t] = u;
     }
@@ -174,7 +176,7 @@ __device__ RangeStart find_range(const SplitArgs& a, int p, int st, int32_t* sum
     total = __reduce_add_sync(0xffffffffu, total);
   }
   // No range between two used ones is empty (the join reads a partial of each): P = min(P, U).
-  const int P = max(min(a.plan.parts, total), 1);
+  const int P = max(min(parts, total), 1);
   const int q0 = min(p, P), q1 = min(p + 1, P);
   const int d = total / P, m = total % P;                  // p U / P without overflow: U = d P + m
   const int u0 = q0 * d + q0 * m / P, u1 = q1 * d + q1 * m / P;
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_split_kernel(c
     if (threadIdx.x == 0 && (n < 0 || n > a.max_len)) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
     rs = RangeStart{p, 0, (int32_t)(((int64_t)(n < 0 ? 0 : min(n, a.max_len)) + st - 1) / st)};
   } else {
-    rs = find_range(a, p, st, reinterpret_cast<int32_t*>(merge));
+    rs = find_range(a, p, pl.parts, st, reinterpret_cast<int32_t*>(merge));
   }
   __syncthreads();                                         // barriers set up; the sums lie where heads merge
   if (g0 == 0 && threadIdx.x == 0) a.ws_start[p] = make_int4(rs.req, rs.tok, rs.units, 0);
@@ -656,125 +658,194 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_split_kernel(c
   }
 }
 
-// m and L = sum l_i 2^(m_i - m) of the partials of (request, head) in ranges [p0, p1], by one warp.
-__device__ __forceinline__ float2 join_ml(const SplitArgs& a, int p0, int p1, int h, int lane) {
-  float M = -INFINITY, L = 0.f;
-  for (int i = p0 + lane; i <= p1; i += 32) {
-    const float2 ml = a.ws_ml[partial_slot(i, i == p0) * a.n_heads + h];
-    const float mn = fmaxf(M, ml.x), ms = mn == -INFINITY ? 0.f : mn;
-    L = L * exp2f(M - ms) + ml.y * exp2f(ml.x - ms);
-    M = mn;
-  }
-  float m = M;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  L *= exp2f(M - (m == -INFINITY ? 0.f : m));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  return make_float2(m, L);
-}
-
-constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinBatch = 4;                              // partials whose loads are in flight together
 
-// Joins the requests that span ranges and turns scores into weights.  Block (p, sub) of `parts` x
-// `subs` takes the requests of range p: of a request that spans ranges its share of the query
-// heads (up to 8 partials a warp per head, beyond that the whole block), and of the range's tokens
-// every subs-th run of 256.
+// Adds partials i = p0 + first, + step, ... <= p1 of (request, head) to (m, l, acc); a lane holds
+// every 32nd feature.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
-  extern __shared__ float lse_s[];                         // [n_heads] with weights
-  __shared__ float part[kJoinWarps][D];
+__device__ __forceinline__ void join_partials(const SplitArgs& a, int p0, int p1, int first, int step, int h, int lane,
+                                              float& m, float& l, float (&acc)[D / 32]) {
+  constexpr int E = D / 32;
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int i0 = p0 + first; i0 <= p1; i0 += kJoinBatch * step) {
+    float x[kJoinBatch][E];
+    float2 ml[kJoinBatch];
+#pragma unroll
+    for (int b = 0; b < kJoinBatch; ++b) {
+      const int i = min(i0 + b * step, p1);
+      const int64_t slot = partial_slot(i, i == p0) * a.n_heads + h;
+      ml[b] = a.ws_ml[slot];
+      if (i0 + b * step > p1) ml[b] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[b][e] = i0 + b * step <= p1 ? a.ws_acc[slot * D + e * 32 + lane] : 0.f;
+    }
+    float mn = m;
+#pragma unroll
+    for (int b = 0; b < kJoinBatch; ++b) mn = fmaxf(mn, ml[b].x);
+    const float ms = mn == -INFINITY ? 0.f : mn, c = exp2f(m - ms);
+    m = mn;
+    l *= c;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= c;
+#pragma unroll
+    for (int b = 0; b < kJoinBatch; ++b) {
+      const float f = exp2f(ml[b].x - ms);
+      l = fmaf(ml[b].y, f, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(x[b][e], f, acc[e]);
+    }
+  }
+}
+
+__device__ __forceinline__ void store_lse(const SplitArgs& a, int r, int h, float m, float l) {
+  if (a.lse) a.lse[(int64_t)r * a.n_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Joins the requests that span ranges, and turns scores into weights.
+// Join: a request that spans ranges p0..p1 is the one in whose middle each of p0 + 1..p1 begins, so
+// those ranges' blocks find it at once and share its query heads (up to kJoinWarps partials a warp
+// per head, beyond that a block per head).
+// Weights: the blocks cut the tokens of all requests anew into equal ranges.  Per request a block
+// gathers the heads' lse (of a split request from its partials); then lane i of every warp takes
+// token i of 32, warp w every kJoinWarps-th head, and the warps' sums are added in warp order.
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
+  extern __shared__ float dyn[];                           // with weights: [n_heads] lse, the sums of find_range
+  __shared__ float part[kJoinWarps][D + 2];
   constexpr int E = D / 32;
   pdl_wait_then_release();
-  const int p = blockIdx.x / subs, sub = blockIdx.x % subs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int st = kTile * a.plan.tiles;
-  const int4 w = a.ws_start[p];
-  int r = w.x, tok = w.y;
-  for (int left = w.z; left > 0;) {
+  if (!a.plan.whole) {
+    const int p = blockIdx.x / subs, sub = blockIdx.x % subs;
+    const int4 w = a.ws_start[p];
+    if (w.z > 0 && w.y > 0) {
+      const int r = w.x;
+      const int2 range = a.ws_range[r];
+      const bool wide = range.y - range.x >= kJoinWarps;
+      const int block = (p - range.x - 1) * subs + sub, blocks = (range.y - range.x) * subs;
+      uint16_t* row = a.out + r * a.out_stride;
+      if (wide) {
+        for (int h = block; h < a.n_heads; h += blocks) {
+          float m, l, acc[E];
+          join_partials<D>(a, range.x, range.y, warp, kJoinWarps, h, lane, m, l, acc);
+          __syncthreads();
+#pragma unroll
+          for (int e = 0; e < E; ++e) part[warp][e * 32 + lane] = acc[e];
+          if (lane == 0) {
+            part[warp][D] = m;
+            part[warp][D + 1] = l;
+          }
+          __syncthreads();
+          float M = -INFINITY, L = 0.f, c[kJoinWarps];
+#pragma unroll
+          for (int v = 0; v < kJoinWarps; ++v) M = fmaxf(M, part[v][D]);
+          const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+          for (int v = 0; v < kJoinWarps; ++v) {
+            c[v] = exp2f(part[v][D] - ms);
+            L = fmaf(part[v][D + 1], c[v], L);
+          }
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
+            float x = 0.f;
+#pragma unroll
+            for (int v = 0; v < kJoinWarps; ++v) x = fmaf(part[v][d], c[v], x);
+            row[(int64_t)h * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(x * inv));
+          }
+          if (threadIdx.x == 0) store_lse(a, r, h, M, L);
+        }
+      } else {
+        for (int h = block * kJoinWarps + warp; h < a.n_heads; h += blocks * kJoinWarps) {
+          float m, l, acc[E];
+          join_partials<D>(a, range.x, range.y, 0, 1, h, lane, m, l, acc);
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            row[(int64_t)h * D + e * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] * inv));
+          if (lane == 0) store_lse(a, r, h, m, l);
+        }
+      }
+    }
+  }
+  if (!a.weight_out) return;
+
+  float* lse_s = dyn;
+  const RangeStart rs = find_range(a, blockIdx.x, gridDim.x, kJoinUnit, reinterpret_cast<int32_t*>(dyn + a.n_heads));
+  int r = rs.req, tok = rs.tok;
+  for (int left = rs.units; left > 0;) {
     const int n = request_length(a, r);
     if (tok >= n) {
       ++r;
       tok = 0;
       continue;
     }
-    const int units = min(left, (int)(((int64_t)n - tok + st - 1) / st));
-    const int end = min((int64_t)n, tok + (int64_t)units * st);
+    const int units = min(left, (int)(((int64_t)n - tok + kJoinUnit - 1) / kJoinUnit));
     const int2 range = a.ws_range[r];
-    const int np = range.y - range.x + 1;
-    if (np > 1) {
-      const bool wide = np > kJoinWarps;                   // a block per head, its warps share the partials
-      const int block = (p - range.x) * subs + sub, blocks = np * subs;
-      const int step = wide ? blocks : blocks * kJoinWarps;
-      for (int h = wide ? block : block * kJoinWarps + warp; h < a.n_heads; h += step) {
-        const float2 ml = join_ml(a, range.x, range.y, h, lane);
-        const float ms = ml.x == -INFINITY ? 0.f : ml.x;
-        float acc[E];
+    __syncthreads();                                       // lse_s and part are done with
+    if (range.x == range.y) {
+      for (int h = threadIdx.x; h < a.n_heads; h += 32 * kJoinWarps) {
+        const float z = a.ws_lse[(int64_t)r * a.n_heads + h];
+        lse_s[h] = z == -INFINITY ? INFINITY : z;          // a row without weight: 2^(s - inf) = 0
+      }
+    } else {
+      for (int h0 = 0; h0 < a.n_heads; h0 += 32) {         // 32 heads a lane each, the partials over the warps
+        const int h = min(h0 + lane, a.n_heads - 1);
+        float M = -INFINITY, L = 0.f;
+        for (int i0 = range.x + warp; i0 <= range.y; i0 += 8 * kJoinWarps) {
+          float2 ml[8];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        const int inc = wide ? kJoinWarps : 1;
-        for (int i0 = range.x + (wide ? warp : 0); i0 <= range.y; i0 += kJoinBatch * inc) {
-          float x[kJoinBatch][E], c[kJoinBatch];
-#pragma unroll
-          for (int b = 0; b < kJoinBatch; ++b) {
-            const int i = i0 + b * inc;
-            const bool in = i <= range.y;
-            const int64_t slot = partial_slot(in ? i : range.y, (in ? i : range.y) == range.x) * a.n_heads + h;
-            c[b] = in ? a.ws_ml[slot].x : -INFINITY;
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[b][e] = in ? a.ws_acc[slot * D + e * 32 + lane] : 0.f;
+          for (int b = 0; b < 8; ++b) {
+            const int i = i0 + b * kJoinWarps;
+            ml[b] = i <= range.y ? a.ws_ml[partial_slot(i, i == range.x) * a.n_heads + h] : make_float2(-INFINITY, 0.f);
           }
+          float mn = M;
 #pragma unroll
-          for (int b = 0; b < kJoinBatch; ++b) {
-            const float f = exp2f(c[b] - ms);
+          for (int b = 0; b < 8; ++b) mn = fmaxf(mn, ml[b].x);
+          const float ms = mn == -INFINITY ? 0.f : mn;
+          L *= exp2f(M - ms);
+          M = mn;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(x[b][e], f, acc[e]);
-          }
+          for (int b = 0; b < 8; ++b) L = fmaf(ml[b].y, exp2f(ml[b].x - ms), L);
         }
-        if (wide) {
-          __syncthreads();
+        __syncthreads();
+        part[warp][2 * lane] = M;
+        part[warp][2 * lane + 1] = L;
+        __syncthreads();
+        if (warp == 0 && h0 + lane < a.n_heads) {
+          float m = -INFINITY, l = 0.f;
 #pragma unroll
-          for (int e = 0; e < E; ++e) part[warp][e * 32 + lane] = acc[e];
-          __syncthreads();
-          if (warp != 0) continue;
+          for (int v = 0; v < kJoinWarps; ++v) m = fmaxf(m, part[v][2 * lane]);
+          const float ms = m == -INFINITY ? 0.f : m;
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            for (int v = 1; v < kJoinWarps; ++v) acc[e] += part[v][e * 32 + lane];
+          for (int v = 0; v < kJoinWarps; ++v) l = fmaf(part[v][2 * lane + 1], exp2f(part[v][2 * lane] - ms), l);
+          lse_s[h] = l == 0.f ? INFINITY : m + log2f(l);
         }
-        const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
-        uint16_t* dst = a.out + r * a.out_stride + (int64_t)h * D;
-#pragma unroll
-        for (int e = 0; e < E; ++e) dst[e * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] * inv));
-        if (a.lse && lane == 0)
-          a.lse[(int64_t)r * a.n_heads + h] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
       }
     }
-    if (a.weight_out) {
-      __syncthreads();                                     // lse_s of the request before is done with
-      if (np > 1) {
-        for (int h = warp; h < a.n_heads; h += kJoinWarps) {
-          const float2 ml = join_ml(a, range.x, range.y, h, lane);
-          if (lane == 0) lse_s[h] = ml.y == 0.f ? INFINITY : ml.x + log2f(ml.y);
-        }
-      } else {
-        for (int h = threadIdx.x; h < a.n_heads; h += kJoinThreads) {
-          const float z = a.ws_lse[(int64_t)r * a.n_heads + h];
-          lse_s[h] = z == -INFINITY ? INFINITY : z;        // a row without weight: 2^(s - inf) = 0
-        }
-      }
-      __syncthreads();
-      for (int64_t j = tok + (int64_t)sub * kJoinThreads + threadIdx.x; j < end; j += (int64_t)subs * kJoinThreads) {
+    __syncthreads();
+    for (int u = 0; u < units; ++u) {
+      const int64_t j = tok + (int64_t)u * kJoinUnit + lane;
+      float x = 0.f;
+      if (j < n) {
         const float* sc = a.ws_scores + (int64_t)r * a.n_heads * a.score_stride + j;
-        float x = 0.f;
 #pragma unroll 8
-        for (int h = 0; h < a.n_heads; ++h) x += exp2f(sc[h * a.score_stride] - lse_s[h]);
+        for (int h = warp; h < a.n_heads; h += kJoinWarps) x += exp2f(sc[h * a.score_stride] - lse_s[h]);
+      }
+      part[warp][lane + 32 * (u & 1)] = x;                 // two buffers: one barrier a turn
+      __syncthreads();
+      if (warp == 0 && j < n) {
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < kJoinWarps; ++v) sum += part[v][lane + 32 * (u & 1)];
         const int64_t at = r * a.weight_stride + j;
-        a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.f) + x;
+        a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.f) + sum;
       }
     }
     left -= units;
-    tok = end;
+    tok = (int)min((int64_t)n, tok + (int64_t)units * kJoinUnit);
   }
 }
 
@@ -878,10 +949,11 @@ int launch_split_d(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
 
 template <int D>
 int launch_join(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
-  const int subs = std::max(1, 4 * device_sm_count() / a.plan.parts);   // about four blocks per SM
+  const int subs = std::max(1, 8 * device_sm_count() / a.plan.parts);   // about eight blocks per SM
+  const size_t smem = a.weight_out ? (size_t)(a.n_heads + (a.n_req + 31) / 32) * 4 : 0;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
-  const cudaError_t e = launch_pdl(!p->prof_on, attention_join_kernel<D>, dim3(a.plan.parts * subs), dim3(kJoinThreads),
-                                   a.weight_out ? (size_t)a.n_heads * 4 : 0, st, a, subs);
+  const cudaError_t e = launch_pdl(!p->prof_on, attention_join_kernel<D>, dim3(a.plan.parts * subs), dim3(32 * kJoinWarps),
+                                   smem, st, a, subs);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_attention_split launch");
 }
 
