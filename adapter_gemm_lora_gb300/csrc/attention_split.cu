@@ -29,7 +29,12 @@ namespace {
 
 constexpr int kSplitMaxGroup = 16;                  // query heads per KV head
 constexpr int kWarps = 4;                           // consumer warps
-constexpr int kThreads = 32 * (kWarps + 1);         // + the producer warp
+// A bulk copy costs its warp about 35 cycles to issue, whatever its size, so slices below 1 KB need
+// two producer warps (one for K, one for V) to keep up: 160,000 tokens of 512-byte slices (D = 64,
+// 4 heads a CTA) take 324 us with one and 214 us with two; from 1 KB one is enough (a long request
+// at D = 128: 316 us with one, 321 us with two).
+constexpr int kSmallSlice = 1024;
+constexpr int threads_of(int producers) { return 32 * (kWarps + producers); }
 constexpr int kCtasPerSm = 2;
 constexpr int kTile = 16;                           // tokens a warp takes at a time
 constexpr int kMaxTiles = 8;                        // 16-token tiles per stage, at most
@@ -231,8 +236,8 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
 // fragment (movmatrix) as two bf16 terms, hi + lo, so the weights carry 16 mantissa bits.
 // A tile's K and V fragments are all in registers before its softmax starts, and the stage is given
 // back then: the chain of a tile (products, shuffles, exponentials) holds up no copy.
-template <int D, int NT, int TILES>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_split_kernel(const __grid_constant__ SplitArgs a) {
+template <int D, int NT, int TILES, int NP>
+__global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_kernel(const __grid_constant__ SplitArgs a) {
   constexpr int KS = D / 16;
   constexpr int VR = NT == 1 || D < 256 ? (KS < 8 ? KS : 8) : 4;   // V fragments held over the softmax
   extern __shared__ __align__(128) uint8_t smem[];
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_split_kernel(c
   float* merge = reinterpret_cast<float*>(smem + (size_t)S * pl.stage_bytes);   // [heads][group][D + 2]
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, NP);
       mbar_init(bar_empty + 8 * s, n_act * pl.sharers);
     }
     for (int h = 0; h < kWarps; ++h) {
@@ -272,8 +277,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_split_kernel(c
   __syncthreads();                                         // barriers set up; the sums lie where heads merge
   if (g0 == 0 && threadIdx.x == 0) a.ws_start[p] = make_int4(rs.req, rs.tok, rs.units, 0);
 
-  if (warp == kWarps) {
-    // ---- producer ----
+  if (warp >= kWarps) {
+    // ---- producers: each finds every unit's valid tokens; with two, one copies K and one V ----
+    const int role = warp - kWarps;
     const uint32_t bytes = (uint32_t)n_act * D * 2;
     const int half = lane >> 4, ti = lane & 15;            // lanes 0..15: K pages, 16..31: V pages
     const uint32_t dst0 = ring + (uint32_t)(half * TILES * kTile + ti) * RB;
@@ -327,21 +333,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_split_kernel(c
       ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, phase));
       if (!ok) break;
       if (lane == 0) {
-        StageInfo& f = info[s];
-        f.req = cur.req;
-        f.tok = cur.tok;
-        f.n = cur.n;
-        const int begun = cur.req == rs.req ? rs.tok : 0;  // the segment's first token
-        f.flags = (cur.first ? kFirst : 0) | (last ? kLast : 0) | (begun == 0 ? kStarts : 0) | (ends ? kEnds : 0);
-        f.next = w.left > 0 ? w.req : -1;
+        if (role == 0) {
+          StageInfo& f = info[s];
+          f.req = cur.req;
+          f.tok = cur.tok;
+          f.n = cur.n;
+          const int begun = cur.req == rs.req ? rs.tok : 0;  // the segment's first token
+          f.flags = (cur.first ? kFirst : 0) | (last ? kLast : 0) | (begun == 0 ? kStarts : 0) | (ends ? kEnds : 0);
+          f.next = w.left > 0 ? w.req : -1;
 #pragma unroll
-        for (int c = 0; c < TILES; ++c) f.mask[c] = (uint16_t)mask[c];
-        mbar_arrive_expect_tx(bar_full + 8 * s, 2 * bytes * n_valid);
+          for (int c = 0; c < TILES; ++c) f.mask[c] = (uint16_t)mask[c];
+        }
+        mbar_arrive_expect_tx(bar_full + 8 * s, 2 / NP * bytes * n_valid);
       }
       __syncwarp();
 #pragma unroll
       for (int c = 0; c < TILES; ++c)
-        if ((mask[c] >> ti) & 1u)
+        if (((mask[c] >> ti) & 1u) && (NP == 1 || half == role))
           bulk_g2s(dst0 + (uint32_t)s * pl.stage_bytes + (uint32_t)(c * kTile) * RB, rows + (int64_t)page[c] * a.H, bytes,
                    bar_full + 8 * s);
       ++it;
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_split_kernel(c
       for (int c = it > S ? it - S : 0; c < it; ++c) (void)mbar_wait(bar_full + 8 * (c % S), (c / S) & 1);
     }
     // Requests without a token get zeros.
-    for (int r = p; r < a.n_req; r += pl.parts) {
+    for (int r = role == 0 ? p : a.n_req; r < a.n_req; r += pl.parts) {
       if (a.seq_len[r] > 0) continue;
       uint16_t* row = a.out + r * a.out_stride + (int64_t)h0 * pl.group * D;
       for (int i = lane; i < n_act * pl.group * D / 8; i += 32) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
@@ -923,26 +931,33 @@ int check_shape(const char* fn, const lora_pool* p, int32_t n_req, int32_t max_l
   return LORA_OK;
 }
 
-template <int D, int NT, int TILES>
+template <int D, int NT, int TILES, int NP>
 int launch_split(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   static DeviceFlags flags;
-  const int rc = ensure_smem_attr(flags, &attention_split_kernel<D, NT, TILES>, kMaxSmem - kStaticSmem, "lora_attention_split");
+  const int rc = ensure_smem_attr(flags, &attention_split_kernel<D, NT, TILES, NP>, kMaxSmem - kStaticSmem, "lora_attention_split");
   if (rc != LORA_OK) return rc;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
-  const cudaError_t e = launch_pdl(!p->prof_on, attention_split_kernel<D, NT, TILES>, dim3(a.plan.parts * a.plan.n_groups),
-                                   dim3(kThreads), a.plan.smem, st, a);
+  const cudaError_t e = launch_pdl(!p->prof_on, attention_split_kernel<D, NT, TILES, NP>, dim3(a.plan.parts * a.plan.n_groups),
+                                   dim3(threads_of(NP)), a.plan.smem, st, a);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_attention_split launch");
 }
 
-// The kernel of a head width, by the query heads per KV head and the tiles per stage (the three
-// counts that split_plan gives for 3 or 4, 2 and 1 heads per group).
-template <int D, int T0, int T1, int T2>
-int launch_split_d(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
-  const bool one = a.plan.group <= 8;
-  switch (a.plan.tiles) {
-    case T0: return one ? launch_split<D, 1, T0>(p, a, st) : launch_split<D, 2, T0>(p, a, st);
-    case T1: return one ? launch_split<D, 1, T1>(p, a, st) : launch_split<D, 2, T1>(p, a, st);
-    case T2 != T1 ? T2 : -1: return one ? launch_split<D, 1, T2>(p, a, st) : launch_split<D, 2, T2>(p, a, st);
+// The kernel of a shape: split_plan gives these tile counts, and the slices that take two producers.
+template <int D, int TILES, int NP>
+int launch_split_group(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
+  return a.plan.group <= 8 ? launch_split<D, 1, TILES, NP>(p, a, st) : launch_split<D, 2, TILES, NP>(p, a, st);
+}
+int launch_split_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
+  const bool two = a.plan.heads * a.plan.D * 2 < kSmallSlice;
+  switch (a.plan.D * 16 + a.plan.tiles) {
+    case 64 * 16 + 2: return launch_split_group<64, 2, 2>(p, a, st);
+    case 64 * 16 + 4: return launch_split_group<64, 4, 2>(p, a, st);
+    case 64 * 16 + 8: return launch_split_group<64, 8, 2>(p, a, st);
+    case 128 * 16 + 1: return two ? launch_split_group<128, 1, 2>(p, a, st) : launch_split_group<128, 1, 1>(p, a, st);
+    case 128 * 16 + 2: return launch_split_group<128, 2, 2>(p, a, st);
+    case 128 * 16 + 4: return launch_split_group<128, 4, 2>(p, a, st);
+    case 256 * 16 + 1: return launch_split_group<256, 1, 1>(p, a, st);
+    case 256 * 16 + 2: return launch_split_group<256, 2, 2>(p, a, st);
   }
   return lora_fail(LORA_EINVAL, "lora_attention_split: no kernel for this geometry");
 }
@@ -1034,9 +1049,7 @@ extern "C" int lora_attention_split(lora_pool* p, int32_t n_req, const int32_t* 
   a.ws_scores = weight_out ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
   a.score_stride = L.score_stride;
   a.err = p->d_err;
-  const int rc2 = pl.D == 64 ? launch_split_d<64, 2, 4, 8>(p, a, st)
-                  : pl.D == 128 ? launch_split_d<128, 1, 2, 4>(p, a, st)
-                                : launch_split_d<256, 1, 2, 2>(p, a, st);
+  const int rc2 = launch_split_any(p, a, st);
   if (rc2 != LORA_OK || (pl.whole && !weight_out)) return rc2;
   return pl.D == 64 ? launch_join<64>(p, a, st) : pl.D == 128 ? launch_join<128>(p, a, st) : launch_join<256>(p, a, st);
 }
