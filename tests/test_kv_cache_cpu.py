@@ -88,7 +88,8 @@ def test_kv_write_refuses(L, pool, over, message):
     (dict(keep_dev=None), "null pointer"), (dict(new_len_dev=None), "null pointer"), (dict(table_out_dev=None), "null pointer"),
     (dict(weight_out_dev=None), "null pointer"), (dict(table_dev=A + 4), "8-byte"), (dict(table_out_dev=F + 4), "8-byte"),
     (dict(table_out_dev=A), "inputs"), (dict(weight_out_dev=C), "inputs"), (dict(new_len_dev=B), "inputs"),
-    (dict(n_req=65536, layers=65536), "too many"), (dict(), "planning pool"),
+    (dict(n_req=65536, layers=65536), "too many"), (dict(max_len=(1 << 30) + 1), "2^30"),
+    (dict(max_len_out=(1 << 30) + 1), "2^30"), (dict(), "planning pool"),
 ])
 def test_kv_evict_refuses(L, pool, over, message):
     base = dict(pool=pool, n_req=3, table_dev=A, seq_len_dev=B, max_len=8, layers=2, weight_dev=C, budget=4, recent=2,
