@@ -46,23 +46,75 @@ kv_write_kernel(uint16_t* __restrict__ pool, int64_t num_pages, int32_t H, int32
 }
 
 // ---- eviction ------------------------------------------------------------------------------------
-// Sort key of a weight: ascending with the value, -0 = +0, NaN = -infinity.
+// Sort key of a weight: ascending with the value, -0 = +0, NaN = -infinity.  Keys of weights lie in
+// [0x007FFFFF, 0xFF800000]: outside are a token that stays in any case and one that is not there.
+constexpr uint32_t kKeyStays = 0xFFFFFFFFu, kKeyAbsent = 0u;
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  const uint32_t b = __float_as_uint(w != w ? -INFINITY : w + 0.f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const int32_t b = __float_as_int(fmaxf(w, -INFINITY) + 0.f);       // fmaxf drops a NaN, + 0 a minus sign of 0
+  return (uint32_t)(b ^ ((b >> 31) | INT32_MIN));
 }
 
-// The keys that stay are found by radix selection, digit by digit from the top: a histogram of the
-// digit over the keys that still match the digits chosen so far, and the bin that holds the
-// need-th largest key.  11 + 11 + 10 bits: the first digit (sign, exponent, two bits of the
-// fraction) already spreads weights of like size over many bins, and selection ends with the first
-// digit whose bin is wanted whole, which for weights that differ is the second.
-constexpr int kEvictMaxThreads = 512;
-constexpr int kEvictMaxWarps = kEvictMaxThreads / 32;
-constexpr int kEvictBins = 2048;
-constexpr int kEvictDigits = 3;
+// Per row (one request at one layer) the keys that stay are found by radix selection, 10 bits at a
+// time from the top: a histogram of the digit over the keys that still match the digits chosen so
+// far, and the bin that holds the need-th largest key.  It ends with the first bin that is wanted
+// whole: for weights that differ, after the second digit or the third.
+struct EvictArgs {
+  int32_t n_req;
+  const int2* table;
+  const int32_t* seq_len;
+  int32_t max_len, layers;
+  const float* weight;
+  int32_t budget, recent;
+  int32_t* keep;
+  int32_t* new_len;
+  int2* table_out;
+  float* weight_out;
+  int32_t max_len_out;
+  int32_t* err;
+};
+
+// What stays of one (request, layer) row, before any key is looked at.
+struct EvictRow {
+  int64_t row;                   // layer * n_req + request
+  int r, layer, n, n_keep;
+  int old;                       // tokens that compete; the newer ones stay
+  int need;                      // of them stay
+  uint32_t cut;                  // keys above it stay, and the first `ties` of those equal to it
+  int ties;
+};
+__device__ __forceinline__ EvictRow evict_row(const EvictArgs& a, int id, bool report) {
+  EvictRow e;
+  e.layer = id % a.layers;
+  e.r = id / a.layers;
+  e.row = (int64_t)e.layer * a.n_req + e.r;
+  e.n = a.seq_len[e.r];
+  if (e.n < 0 || e.n > a.max_len) {
+    if (report) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
+    e.n = e.n < 0 ? 0 : a.max_len;
+  }
+  e.n_keep = min(e.n, a.budget);
+  e.old = e.n - min(e.n, a.recent);
+  e.need = e.n_keep - (e.n - e.old);
+  e.cut = e.need >= e.old ? kKeyAbsent : kKeyStays - 1;    // all of them, or none
+  e.ties = 0;
+  return e;
+}
+constexpr int kEvictWarps = 16;                            // of a CTA
+constexpr int kEvictThreads = 32 * kEvictWarps;
+constexpr int kEvictDigitBits = 10;
+constexpr int kEvictDigits = 4;                            // 10 + 10 + 10 + 2 bits
+constexpr int kEvictHist = (1 << kEvictDigitBits) / 32 * 36;   // 32 bins every 36 words: 16-byte reads without conflicts
 constexpr int kEvictMaxCluster = 8;
-__device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : d == 1 ? 10 : 0; }
+__device__ __forceinline__ uint32_t hist_at(uint32_t bin) { return bin + (bin >> 5) * 4; }
+
+__device__ __forceinline__ int warp_scan(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -81,84 +133,99 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, int v) {
   asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-struct EvictArgs {
-  int32_t n_req;
-  const int2* table;
-  const int32_t* seq_len;
-  int32_t max_len, layers;
-  const float* weight;
-  int32_t budget, recent;
-  int32_t* keep;
-  int32_t* new_len;
-  int2* table_out;
-  float* weight_out;
-  int32_t max_len_out;
-  int32_t* err;
-};
+// kRowWarps warps per row: 4, so that a CTA has four rows, or all 16; with kCluster a cluster of
+// `n_cta` CTAs has one row, and the CTAs add their histograms' filled bins into each other's shared
+// memory (integer sums: the order does not matter).  Every warp takes a contiguous part of the row,
+// the keys of 32 K weights held in registers (longer parts are read again in every pass), so the
+// kept tokens are numbered with one exchange of counts.  Their positions go to a list in shared
+// memory first, and the outputs are written from there, 32 neighbours at a time.
+// Four rows a CTA: layers of one request are neighbours, and the page table [token][layer] is
+// compacted for the four together, so that four lanes fill the 32-byte sector of which a row by
+// itself would write 8 bytes at a time.
+// A row is a chain of dependent steps (length, weights, two or three digits, counts, pages), so time
+// goes with the chain's length times the rows per SM: the passes are free of branches within
+// kEvictBatch chunks of 32 weights, whose steps overlap.
+constexpr int kEvictBatch = 4;
+constexpr int kGatherBatch = 8;                            // page reads a thread has in flight
 
-// One cluster of `n_cta` CTAs (one CTA where rows are short or many) per (request, layer), layers
-// next to each other so that the table's 32-byte sectors, which hold four layers, are shared in L2.
-// Every CTA takes a contiguous slice of the row, every warp a contiguous part of that, so the kept
-// tokens are numbered with one exchange of counts: warps count what they keep, and then write from
-// their offset, 32 tokens a step.  Several CTAs add their histograms' filled bins into each other's
-// shared memory (integer sums: the order does not matter).
-// Latency-bound: a row is a chain of dependent steps (length, weights, digits, counts, pages), so
-// what counts is how many rows an SM holds, and for few long rows how many CTAs share one.
-template <bool kCluster>
-__global__ void __launch_bounds__(kEvictMaxThreads) kv_evict_kernel(const EvictArgs a, int32_t n_cta) {
-  extern __shared__ int hist[];                            // [kEvictBins] mine; of a cluster then [digits][bins] all CTAs'
-  __shared__ int warp_sum[kEvictMaxWarps];
-  __shared__ int found[3];                                 // the wanted bin, keys above it, keys in it
-  __shared__ int warp_gt[kEvictMaxWarps], warp_eq[kEvictMaxWarps];
+template <int K, int kRowWarps, bool kCluster>
+__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictArgs a, int32_t n_cta, int32_t keep_cap) {
+  constexpr int kRows = kEvictWarps / kRowWarps;           // rows of a CTA
+  static_assert(!kCluster || kRows == 1, "a cluster shares one row");
+  static_assert(K % kEvictBatch == 0, "whole batches");
+  extern __shared__ __align__(16) int smem_evict[];
+  __shared__ int warp_gt[kEvictWarps], warp_eq[kEvictWarps], keep_n[kRows];
   __shared__ int cta_gt[kEvictMaxCluster], cta_eq[kEvictMaxCluster];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_thr = blockDim.x, n_warp = n_thr >> 5;
-  for (int i = tid; i < kEvictBins * (kCluster ? 1 + kEvictDigits : 1); i += n_thr) hist[i] = 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slot = warp / kRowWarps, part = warp % kRowWarps, rtid = part * 32 + lane;
+  constexpr int n_thr = 32 * kRowWarps;                    // threads of a row in this CTA
+  // per row: the histogram, of a cluster then every digit's sums over the CTAs; then the kept lists:
+  // of a row (four rows a CTA, keep_cap each) or of a warp (32 K each)
+  constexpr int kHists = kCluster ? 1 + kEvictDigits : kRows;
+  int* hist = smem_evict + slot * kEvictHist;
+  int* lists = smem_evict + kHists * kEvictHist;
+  for (int i = tid; i < kEvictHist * kHists; i += kEvictThreads) smem_evict[i] = 0;
+  const auto row_sync = [&] {
+    if (kRows == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "n"(n_thr) : "memory");
+  };
   pdl_wait_then_release();
-  const int rank = kCluster ? (int)cluster_rank() : 0;
-  const int id = kCluster ? blockIdx.x / n_cta : blockIdx.x;
-  const int layer = id % a.layers, r = id / a.layers;
-  int n = a.seq_len[r];
-  if (n < 0 || n > a.max_len) {
-    if (tid == 0) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
-    n = n < 0 ? 0 : a.max_len;
-  }
-  const int n_keep = min(n, a.budget);
-  const int old = n - min(n, a.recent);                    // tokens that compete; the newer ones stay
-  const int64_t row = (int64_t)layer * a.n_req + r;
-  const float* w = a.weight + row * a.max_len;
-  int need = n_keep - (n - old);                           // of the old ones stay
+  const int rows = a.n_req * a.layers, rank = kCluster ? (int)cluster_rank() : 0;
+  const int id = kCluster ? blockIdx.x / n_cta : blockIdx.x * kRows + slot;
+  const bool live = id < rows;                             // the last CTA may have rows to spare
+  EvictRow e{};
+  if (live) e = evict_row(a, id, rtid == 0 && rank == 0);
+  const float* w = a.weight + e.row * a.max_len;
   // this CTA's slice of the row, and this warp's part of it (multiples of 32)
-  const int per_cta = ((n + n_cta - 1) / n_cta + 31) & ~31;
-  const int c0 = (int)min((int64_t)n, (int64_t)rank * per_cta), c1 = min(n, c0 + per_cta);
-  const int per_warp = ((c1 - c0 + n_warp - 1) / n_warp + 31) & ~31;
-  const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
-
-  uint32_t cut = 0;                                        // keys above it stay, and `ties` of those equal to it
-  int ties = 0;
-  const bool select = need > 0 && need < old;
-  if (need >= old) {
-    ties = old;                                            // every old key is >= 0: all stay
-  } else if (!select) {
-    cut = 0xFFFFFFFFu;                                     // none does
-  }
+  const int per_cta = ((e.n + n_cta - 1) / n_cta + 31) & ~31;
+  const int c0 = (int)min((int64_t)e.n, (int64_t)rank * per_cta), c1 = min(e.n, c0 + per_cta);
+  const int per_warp = ((c1 - c0 + kRowWarps - 1) / kRowWarps + 31) & ~31;
+  const int w0 = min(c1, c0 + part * per_warp), w1 = min(c1, w0 + per_warp);
+  const bool held = per_warp <= 32 * K;                    // the part stays in registers
+  uint32_t key[K];
+  const auto load = [&](int j0) {
+    float x[K];
+#pragma unroll
+    for (int b = 0; b < K; ++b) x[b] = j0 + 32 * b + lane < w1 ? __ldg(w + j0 + 32 * b + lane) : 0.f;
+#pragma unroll
+    for (int b = 0; b < K; ++b) {
+      const int j = j0 + 32 * b + lane;
+      key[b] = j >= w1 ? kKeyAbsent : j >= e.old ? kKeyStays : weight_key(x[b]);
+    }
+  };
+  if (held) load(w0);
   __syncthreads();
   if (kCluster) cluster_sync_all();                        // every CTA's histograms are clear
-  if (select) {
-    const int s0 = min(c0, old), s1 = min(c1, old);
+  if (live && e.need > 0 && e.need < e.old) {
     uint32_t prefix = 0, mask = 0;
-    for (int d = 0; d < kEvictDigits; ++d) {
-      const int shift = digit_shift(d);
-      const uint32_t digit = d == 2 ? 1023u : 2047u;
-#pragma unroll 4
-      for (int j = s0 + tid; j < s1; j += n_thr) {
-        const uint32_t key = weight_key(w[j]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1);
+    int need = e.need;
+    for (int d = 0, bits = 32; d < kEvictDigits; ++d) {
+      const int nb = min(kEvictDigitBits, bits);
+      bits -= nb;
+      const uint32_t digit = (1u << nb) - 1;
+      for (int j0 = w0; j0 < w1; j0 += 32 * K) {
+        if (!held) load(j0);
+#pragma unroll
+        for (int b0 = 0; b0 < K; b0 += kEvictBatch) {
+          if (j0 + 32 * b0 >= w1) break;
+          uint32_t at[kEvictBatch];
+          bool in[kEvictBatch];
+#pragma unroll
+          for (int b = 0; b < kEvictBatch; ++b) {
+            const uint32_t k = key[b0 + b];
+            in[b] = (k & mask) == prefix && k - 1 < kKeyStays - 1;                     // not a mark
+            at[b] = hist_at(digit - ((k >> bits) & digit));                            // largest first
+          }
+#pragma unroll
+          for (int b = 0; b < kEvictBatch; ++b)
+            if (in[b]) atomicAdd(&hist[at[b]], 1);
+        }
       }
-      __syncthreads();
+      row_sync();
       const int* all = hist;
       if (kCluster) {
-        int* sum = hist + kEvictBins * (1 + d);
-        for (int i = tid; i < kEvictBins; i += n_thr) {
+        int* sum = hist + kEvictHist * (1 + d);
+        for (int i = tid; i < kEvictHist; i += kEvictThreads) {
           const int v = hist[i];
           if (v == 0) continue;
           hist[i] = 0;
@@ -167,53 +234,51 @@ __global__ void __launch_bounds__(kEvictMaxThreads) kv_evict_kernel(const EvictA
         cluster_sync_all();
         all = sum;
       }
-      // bins from the top: thread t holds the bins [B - (t + 1) per, B - t per)
-      const int per = kEvictBins / n_thr;
+      // every warp finds the bin: first the lane whose 32 bins hold it, then the bin
       int mine = 0;
-      for (int i = 0; i < per; ++i) mine += all[kEvictBins - 1 - tid * per - i];
-      int incl = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+      for (int i = 0; i < 8; ++i) {
+        const int4 v = reinterpret_cast<const int4*>(all)[lane * 9 + i];
+        mine += v.x + v.y + v.z + v.w;
       }
-      if (lane == 31) warp_sum[warp] = incl;
-      __syncthreads();
-      int above = incl - mine;
-      for (int i = 0; i < warp; ++i) above += warp_sum[i];
-      if (above < need && above + mine >= need) {          // one thread: the need-th largest key is in its bins
-        int b = kEvictBins - 1 - tid * per;
-        while (above + all[b] < need) above += all[b--];
-        found[0] = b;
-        found[1] = above;
-        found[2] = all[b];
-      }
-      __syncthreads();
-      need -= found[1];
-      prefix |= (uint32_t)found[0] << shift;
-      mask |= digit << shift;
-      cut = prefix;
-      ties = need;
-      if (found[2] == need) {                              // the whole bin stays
-        cut = prefix - 1;                                  // not 0: a key below it is left out
-        ties = 0;
+      int incl = warp_scan(mine, lane);
+      const int l0 = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
+      const int before = __shfl_sync(0xffffffffu, incl - mine, l0);
+      const int v = all[l0 * 36 + lane];
+      incl = before + warp_scan(v, lane);
+      const int l1 = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
+      const int count = __shfl_sync(0xffffffffu, v, l1);
+      need -= __shfl_sync(0xffffffffu, incl, l1) - count;
+      prefix |= (digit - (uint32_t)(l0 * 32 + l1)) << bits;
+      mask |= digit << bits;
+      e.cut = prefix;
+      e.ties = need;
+      if (count == need) {                                 // the whole bin stays
+        e.cut = prefix - 1;
+        e.ties = 0;
         break;
       }
       if (!kCluster && d + 1 < kEvictDigits) {
-        for (int i = tid; i < kEvictBins; i += n_thr) hist[i] = 0;
-        __syncthreads();
+        row_sync();
+        for (int i = rtid; i < kEvictHist; i += n_thr) hist[i] = 0;
+        row_sync();
       }
     }
   }
 
-  // what each warp keeps: keys above the cut (and the newer tokens), and keys equal to it
+  // what each warp keeps: keys above the cut, and keys equal to it
   int gt = 0, eq = 0;
-#pragma unroll 4
-  for (int j0 = w0; j0 < w1; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t key = j < w1 && j < old ? weight_key(w[j]) : 0u;
-    gt += j < w1 && (j >= old || key > cut);
-    eq += j < w1 && j < old && key == cut;
+  for (int j0 = w0; j0 < w1; j0 += 32 * K) {
+    if (!held) load(j0);
+#pragma unroll
+    for (int b0 = 0; b0 < K; b0 += kEvictBatch) {
+      if (j0 + 32 * b0 >= w1) break;
+#pragma unroll
+      for (int b = b0; b < b0 + kEvictBatch; ++b) {
+        gt += key[b] > e.cut;
+        eq += key[b] == e.cut;
+      }
+    }
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
@@ -221,59 +286,167 @@ __global__ void __launch_bounds__(kEvictMaxThreads) kv_evict_kernel(const EvictA
     warp_gt[warp] = gt;
     warp_eq[warp] = eq;
   }
-  __syncthreads();
-  int gt_before = 0, eq_before = 0;                        // of the row, before this warp's part
+  row_sync();
+  int pos = 0, tied = 0;                                   // kept and tied of the row before this warp's part
   if (kCluster) {
     if (tid < n_cta) {
-      int g = 0, e = 0;
-      for (int i = 0; i < n_warp; ++i) {
+      int g = 0, q = 0;
+      for (int i = 0; i < kRowWarps; ++i) {
         g += warp_gt[i];
-        e += warp_eq[i];
+        q += warp_eq[i];
       }
       cluster_store(cluster_addr(cta_gt + rank, tid), g);
-      cluster_store(cluster_addr(cta_eq + rank, tid), e);
+      cluster_store(cluster_addr(cta_eq + rank, tid), q);
     }
     cluster_sync_all();
     for (int i = 0; i < rank; ++i) {
-      gt_before += cta_gt[i];
-      eq_before += cta_eq[i];
+      pos += cta_gt[i];
+      tied += cta_eq[i];
     }
   }
-  for (int i = 0; i < warp; ++i) {
-    gt_before += warp_gt[i];
-    eq_before += warp_eq[i];
+  for (int i = 0; i < part; ++i) {
+    pos += warp_gt[slot * kRowWarps + i];
+    tied += warp_eq[slot * kRowWarps + i];
   }
-  int pos = gt_before + min(eq_before, ties);
-  int32_t* keep = a.keep + row * a.budget;
-  float* w_out = a.weight_out + row * a.max_len_out;
-  int2* t_out = a.table_out + (int64_t)r * a.max_len_out * a.layers + layer;
-  const int2* t_in = a.table + (int64_t)r * a.max_len * a.layers + layer;
-#pragma unroll 4
-  for (int j0 = w0; j0 < w1; j0 += 32) {
-    const int j = j0 + lane;
-    const float x = j < w1 ? w[j] : 0.f;
-    const uint32_t key = weight_key(x);
-    const bool e = j < w1 && j < old && key == cut;
-    const uint32_t me = __ballot_sync(0xffffffffu, e);
-    const uint32_t below = (1u << lane) - 1;
-    const bool stay = j < w1 && (j >= old || key > cut || (e && eq_before + __popc(me & below) < ties));
-    const uint32_t ms = __ballot_sync(0xffffffffu, stay);
-    if (stay) {
-      const int i = pos + __popc(ms & below);
-      keep[i] = j;
-      w_out[i] = x;
-      t_out[(int64_t)i * a.layers] = t_in[(int64_t)j * a.layers];
+  pos += min(tied, e.ties);
+  int32_t* keep = a.keep + e.row * a.budget;
+  float* w_out = a.weight_out + e.row * a.max_len_out;
+  const int2* t_in = a.table + (int64_t)e.r * a.max_len * a.layers + e.layer;
+  int2* t_out = a.table_out + (int64_t)e.r * a.max_len_out * a.layers + e.layer;
+  const uint32_t below = (1u << lane) - 1;
+  for (int j0 = w0; j0 < w1; j0 += 32 * K) {
+    if (!held) load(j0);
+    int* list = kRows > 1 ? lists + slot * keep_cap + pos : lists + warp * 32 * K;
+    int n_kept = 0;
+#pragma unroll
+    for (int b0 = 0; b0 < K; b0 += kEvictBatch) {
+      if (j0 + 32 * b0 >= w1) break;
+      bool stay[kEvictBatch];
+      int at[kEvictBatch];
+      if (e.ties > 0) {
+#pragma unroll
+        for (int b = 0; b < kEvictBatch; ++b) {
+          const bool q = key[b0 + b] == e.cut;
+          const uint32_t mq = __ballot_sync(0xffffffffu, q);
+          stay[b] = key[b0 + b] > e.cut || (q && tied + __popc(mq & below) < e.ties);
+          tied += __popc(mq);
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < kEvictBatch; ++b) stay[b] = key[b0 + b] > e.cut;
+      }
+#pragma unroll
+      for (int b = 0; b < kEvictBatch; ++b) {
+        const uint32_t ms = __ballot_sync(0xffffffffu, stay[b]);
+        at[b] = n_kept + __popc(ms & below);
+        n_kept += __popc(ms);
+      }
+#pragma unroll
+      for (int b = 0; b < kEvictBatch; ++b)
+        if (stay[b]) list[at[b]] = j0 + 32 * (b0 + b) + lane;
     }
-    pos += __popc(ms);
-    eq_before += __popc(me);
+    __syncwarp();
+    for (int i0 = lane; i0 < n_kept; i0 += 32 * kGatherBatch) {
+      int j[kGatherBatch];
+      float x[kGatherBatch];
+      int2 pages[kGatherBatch];
+#pragma unroll
+      for (int b = 0; b < kGatherBatch; ++b) j[b] = list[min(i0 + 32 * b, n_kept - 1)];
+#pragma unroll
+      for (int b = 0; b < kGatherBatch; ++b) {
+        x[b] = __ldg(w + j[b]);
+        if (kRows == 1) pages[b] = __ldg(t_in + (int64_t)j[b] * a.layers);
+      }
+#pragma unroll
+      for (int b = 0; b < kGatherBatch; ++b) {
+        const int i = pos + i0 + 32 * b;
+        if (i0 + 32 * b >= n_kept) break;
+        keep[i] = j[b];
+        w_out[i] = x[b];
+        if (kRows == 1) t_out[(int64_t)i * a.layers] = pages[b];
+      }
+    }
+    pos += n_kept;
+    __syncwarp();
   }
-  const int step = n_cta * n_thr, first = n_keep + rank * n_thr + tid;
-  for (int i = first; i < a.budget; i += step) keep[i] = -1;
-  for (int i = first; i < a.max_len_out; i += step) {
-    w_out[i] = 0.f;
-    t_out[(int64_t)i * a.layers] = make_int2(-1, -1);
+  if (live) {
+    const int step = n_cta * n_thr, first = e.n_keep + rank * n_thr + rtid;
+    for (int i = first; i < a.budget; i += step) keep[i] = -1;
+    for (int i = first; i < a.max_len_out; i += step) {
+      w_out[i] = 0.f;
+      if (kRows == 1) t_out[(int64_t)i * a.layers] = make_int2(-1, -1);
+    }
+    if (e.layer == 0 && rank == 0 && rtid == 0) a.new_len[e.r] = e.n_keep;
   }
-  if (layer == 0 && rank == 0 && tid == 0) a.new_len[r] = n_keep;
+  if (kRows == 1) return;
+
+  // the page table of the CTA's rows: thread = (position, row), rows fastest
+  if (rtid == 0) keep_n[slot] = e.n_keep;
+  __syncthreads();
+  const int k = tid % kRows, gid = blockIdx.x * kRows + k;
+  if (gid >= rows) return;
+  const int layer = gid % a.layers, r = gid / a.layers, n_keep = keep_n[k];
+  t_in = a.table + (int64_t)r * a.max_len * a.layers + layer;
+  t_out = a.table_out + (int64_t)r * a.max_len_out * a.layers + layer;
+  constexpr int kStep = kEvictThreads / kRows;             // positions a pass of the CTA covers
+  int i0 = tid / kRows;
+  for (; i0 < n_keep; i0 += kStep * kGatherBatch) {
+    int2 pages[kGatherBatch];
+#pragma unroll
+    for (int b = 0; b < kGatherBatch; ++b)
+      pages[b] = __ldg(t_in + (int64_t)lists[k * keep_cap + min(i0 + kStep * b, n_keep - 1)] * a.layers);
+#pragma unroll
+    for (int b = 0; b < kGatherBatch; ++b) {
+      if (i0 + kStep * b >= n_keep) break;
+      t_out[(int64_t)(i0 + kStep * b) * a.layers] = pages[b];
+    }
+  }
+  for (int i = n_keep + tid / kRows; i < a.max_len_out; i += kStep) t_out[(int64_t)i * a.layers] = make_int2(-1, -1);
+}
+
+constexpr int kShortRow = 4096;                            // four rows a CTA up to this length
+constexpr int kEvictMaxSmem = ((1 + kEvictDigits) * kEvictHist + kEvictWarps * 1024) * 4;
+static_assert(kEvictMaxSmem >= (4 * kEvictHist + 4 * kShortRow) * 4, "the kept lists of four rows fit");
+
+template <int K, int kRowWarps, bool kCluster>
+int launch_evict(const lora_pool* p, const EvictArgs& a, int n_cta, cudaStream_t st) {
+  const int64_t rows = (int64_t)a.n_req * a.layers;
+  constexpr int kRows = kEvictWarps / kRowWarps;
+  const int keep_cap = kRows > 1 ? std::min(a.budget, a.max_len) : 0;
+  const int smem = (kEvictHist * (kCluster ? 1 + kEvictDigits : kRows) +
+                    (kRows > 1 ? kRows * keep_cap : kEvictWarps * 32 * K)) * (int)sizeof(int);
+  static DeviceFlags flags;
+  const int rc = ensure_smem_attr(flags, &kv_evict_kernel<K, kRowWarps, kCluster>, kEvictMaxSmem, "lora_kv_evict");
+  if (rc != LORA_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(kCluster ? rows * n_cta : (rows + kRows - 1) / kRows));
+  cfg.blockDim = dim3(kEvictThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = p->prof_on ? 0 : 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = n_cta;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 2 : 1;
+  ProfScope prof(p, LORA_KIND_KV, st);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_kernel<K, kRowWarps, kCluster>, a, (int32_t)n_cta, (int32_t)keep_cap);
+  return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_kv_evict launch");
+}
+
+template <int kRowWarps, bool kCluster>
+int launch_evict_k(const lora_pool* p, const EvictArgs& a, int n_cta, cudaStream_t st) {
+  const int64_t per_cta = (((int64_t)a.max_len + n_cta - 1) / n_cta + 31) / 32 * 32;
+  const int64_t chunks = ((per_cta + kRowWarps - 1) / kRowWarps + 31) / 32;      // of a warp, at most
+  return chunks <= 4    ? launch_evict<4, kRowWarps, kCluster>(p, a, n_cta, st)
+         : chunks <= 8  ? launch_evict<8, kRowWarps, kCluster>(p, a, n_cta, st)
+         : chunks <= 12 ? launch_evict<12, kRowWarps, kCluster>(p, a, n_cta, st)
+         : chunks <= 16 ? launch_evict<16, kRowWarps, kCluster>(p, a, n_cta, st)
+         : chunks <= 20 ? launch_evict<20, kRowWarps, kCluster>(p, a, n_cta, st)
+         : chunks <= 24 ? launch_evict<24, kRowWarps, kCluster>(p, a, n_cta, st)
+                        : launch_evict<32, kRowWarps, kCluster>(p, a, n_cta, st);
 }
 
 }  // namespace
@@ -326,7 +499,7 @@ extern "C" int lora_kv_evict(lora_pool* p, int32_t n_req, const int32_t* table_d
     return lora_fail(LORA_EINVAL, "lora_kv_evict: tables must be 8-byte aligned");
   if (n_req > 0 && (table_dev == table_out || weight_dev == weight_out || seq_len_dev == new_len_dev))
     return lora_fail(LORA_EINVAL, "lora_kv_evict: outputs must not be the inputs");
-  if ((int64_t)n_req * layers > INT32_MAX) return lora_fail(LORA_EINVAL, "lora_kv_evict: too many (request, layer) rows");
+  if ((int64_t)n_req * layers > (1 << 30)) return lora_fail(LORA_EINVAL, "lora_kv_evict: too many (request, layer) rows");
   if (p->planning) return lora_fail(LORA_EINVAL, "lora_kv_evict: planning pool has no device state");
   if (n_req == 0) return LORA_OK;
   EvictArgs a{};
@@ -344,29 +517,14 @@ extern "C" int lora_kv_evict(lora_pool* p, int32_t n_req, const int32_t* table_d
   a.weight_out = weight_out;
   a.max_len_out = max_len_out;
   a.err = p->d_err;
-  // A cluster per row while its slices stay above 2,048 tokens and all CTAs run at once.
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (max_len <= kShortRow) return launch_evict_k<4, false>(p, a, 1, st);
+  // Long rows: a CTA's registers hold 16,384 weights; beyond that, and as long as all CTAs run at
+  // once and slices stay above 2,048 tokens, a cluster per row.
   const int64_t rows = (int64_t)n_req * layers;
   int n_cta = 1;
-  while (n_cta < kEvictMaxCluster && max_len / (2 * n_cta) >= 2048 && rows * n_cta * 2 <= 4 * (int64_t)device_sm_count())
+  while (n_cta < kEvictMaxCluster && max_len / (2 * n_cta) >= 2048 &&
+         (max_len / n_cta > 16384 || rows * n_cta <= 2 * (int64_t)device_sm_count()) && rows * n_cta * 2 <= INT32_MAX)
     n_cta *= 2;
-  if (rows * n_cta > INT32_MAX) return lora_fail(LORA_EINVAL, "lora_kv_evict: too many (request, layer) rows");
-  const int threads = max_len > 4096 ? kEvictMaxThreads : 256;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * n_cta));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = kEvictBins * sizeof(int) * (n_cta > 1 ? 1 + kEvictDigits : 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = p->prof_on ? 0 : 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = n_cta;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = n_cta > 1 ? 2 : 1;
-  ProfScope prof(p, LORA_KIND_KV, st);
-  const cudaError_t e = n_cta > 1 ? cudaLaunchKernelEx(&cfg, kv_evict_kernel<true>, a, n_cta)
-                                  : cudaLaunchKernelEx(&cfg, kv_evict_kernel<false>, a, n_cta);
-  return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_kv_evict launch");
+  return n_cta > 1 ? launch_evict_k<kEvictWarps, true>(p, a, n_cta, st) : launch_evict_k<kEvictWarps, false>(p, a, 1, st);
 }
