@@ -103,9 +103,8 @@ constexpr int kEvictWarps = 16;                            // of a CTA
 constexpr int kEvictThreads = 32 * kEvictWarps;
 constexpr int kEvictDigitBits = 10;
 constexpr int kEvictDigits = 4;                            // 10 + 10 + 10 + 2 bits
-constexpr int kEvictHist = (1 << kEvictDigitBits) / 32 * 36;   // 32 bins every 36 words: 16-byte reads without conflicts
+constexpr int kEvictBins = 1 << kEvictDigitBits;
 constexpr int kEvictMaxCluster = 8;
-__device__ __forceinline__ uint32_t hist_at(uint32_t bin) { return bin + (bin >> 5) * 4; }
 
 __device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
@@ -126,45 +125,52 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ void cluster_add(uint32_t addr, int v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ int2 cluster_load2(uint32_t addr) {
+  int2 v;
+  asm volatile("ld.relaxed.cluster.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ void cluster_store(uint32_t addr, int v) {
   asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // kRowWarps warps per row: 4, so that a CTA has four rows, or all 16; with kCluster a cluster of
-// `n_cta` CTAs has one row, and the CTAs add their histograms' filled bins into each other's shared
-// memory (integer sums: the order does not matter).  Every warp takes a contiguous part of the row,
-// the keys of 32 K weights held in registers (longer parts are read again in every pass), so the
-// kept tokens are numbered with one exchange of counts.  Their positions go to a list in shared
-// memory first, and the outputs are written from there, 32 neighbours at a time.
+// `n_cta` CTAs has one row, and every CTA adds up all CTAs' histograms (integer sums: the order does
+// not matter).  Every warp takes a contiguous part of the row, the keys of 32 K weights held in
+// registers (longer parts are read again in every pass), so the kept tokens are numbered with one
+// exchange of counts.  Their positions go to a list in shared memory first, and the outputs are
+// written from there, 32 neighbours at a time.
 // Four rows a CTA: layers of one request are neighbours, and the page table [token][layer] is
-// compacted for the four together, so that four lanes fill the 32-byte sector of which a row by
-// itself would write 8 bytes at a time.
+// compacted for the four together, so that four lanes write a 32-byte sector of which a row by
+// itself would write 8 bytes at a time (64 requests x 40 layers: 41 us, a CTA per row 73 us; copying
+// the four rows' table entries to shared memory beside the selection, to read whole sectors too:
+// 43 us).
 // A row is a chain of dependent steps (length, weights, two or three digits, counts, pages), so time
 // goes with the chain's length times the rows per SM: the passes are free of branches within
 // kEvictBatch chunks of 32 weights, whose steps overlap.
 constexpr int kEvictBatch = 4;
-constexpr int kGatherBatch = 8;                            // page reads a thread has in flight
 
 template <int K, int kRowWarps, bool kCluster>
 __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictArgs a, int32_t n_cta, int32_t keep_cap) {
   constexpr int kRows = kEvictWarps / kRowWarps;           // rows of a CTA
   static_assert(!kCluster || kRows == 1, "a cluster shares one row");
   static_assert(K % kEvictBatch == 0, "whole batches");
+  static_assert(!kCluster || kEvictBins == 2 * kEvictThreads, "the sum over the CTAs takes two bins a thread");
   extern __shared__ __align__(16) int smem_evict[];
   __shared__ int warp_gt[kEvictWarps], warp_eq[kEvictWarps], keep_n[kRows];
   __shared__ int cta_gt[kEvictMaxCluster], cta_eq[kEvictMaxCluster];
+  __shared__ int found_s[kRows][3];                        // the wanted bin, keys above it, keys in it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slot = warp / kRowWarps, part = warp % kRowWarps, rtid = part * 32 + lane;
   constexpr int n_thr = 32 * kRowWarps;                    // threads of a row in this CTA
-  // per row: the histogram, of a cluster then every digit's sums over the CTAs; then the kept lists:
-  // of a row (four rows a CTA, keep_cap each) or of a warp (32 K each)
-  constexpr int kHists = kCluster ? 1 + kEvictDigits : kRows;
-  int* hist = smem_evict + slot * kEvictHist;
-  int* lists = smem_evict + kHists * kEvictHist;
-  for (int i = tid; i < kEvictHist * kHists; i += kEvictThreads) smem_evict[i] = 0;
+  constexpr int kPer = kEvictBins / n_thr;                 // bins a thread adds up: 8 or 2
+  // Shared memory: a histogram per row, of a cluster one per digit (the other CTAs may still read the
+  // one before); the kept lists, of a row (four rows a CTA, keep_cap each) or of a warp (32 K each).
+  constexpr int kHists = kCluster ? kEvictDigits : kRows;
+  int* hist = smem_evict + slot * kEvictBins;
+  int* lists = smem_evict + kHists * kEvictBins;
+  for (int i = tid; i < kEvictBins * kHists / 4; i += kEvictThreads)
+    reinterpret_cast<int4*>(smem_evict)[i] = make_int4(0, 0, 0, 0);
   const auto row_sync = [&] {
     if (kRows == 1) __syncthreads();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "n"(n_thr) : "memory");
@@ -175,7 +181,6 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   const bool live = id < rows;                             // the last CTA may have rows to spare
   EvictRow e{};
   if (live) e = evict_row(a, id, rtid == 0 && rank == 0);
-  const float* w = a.weight + e.row * a.max_len;
   // this CTA's slice of the row, and this warp's part of it (multiples of 32)
   const int per_cta = ((e.n + n_cta - 1) / n_cta + 31) & ~31;
   const int c0 = (int)min((int64_t)e.n, (int64_t)rank * per_cta), c1 = min(e.n, c0 + per_cta);
@@ -184,18 +189,20 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   const bool held = per_warp <= 32 * K;                    // the part stays in registers
   uint32_t key[K];
   const auto load = [&](int j0) {
-    float x[K];
+    const float* w = a.weight + e.row * a.max_len;
 #pragma unroll
-    for (int b = 0; b < K; ++b) x[b] = j0 + 32 * b + lane < w1 ? __ldg(w + j0 + 32 * b + lane) : 0.f;
+    for (int b = 0; b < K; ++b)
+      key[b] = j0 + 32 * b + lane < w1 ? __float_as_uint(__ldg(w + j0 + 32 * b + lane)) : 0u;
 #pragma unroll
     for (int b = 0; b < K; ++b) {
       const int j = j0 + 32 * b + lane;
-      key[b] = j >= w1 ? kKeyAbsent : j >= e.old ? kKeyStays : weight_key(x[b]);
+      const uint32_t k = weight_key(__uint_as_float(key[b]));
+      key[b] = j >= w1 ? kKeyAbsent : j >= e.old ? kKeyStays : k;
     }
   };
   if (held) load(w0);
   __syncthreads();
-  if (kCluster) cluster_sync_all();                        // every CTA's histograms are clear
+  if (kCluster) cluster_sync_all();                        // every CTA of the cluster runs: its shared memory may be used
   if (live && e.need > 0 && e.need < e.old) {
     uint32_t prefix = 0, mask = 0;
     int need = e.need;
@@ -208,60 +215,64 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
 #pragma unroll
         for (int b0 = 0; b0 < K; b0 += kEvictBatch) {
           if (j0 + 32 * b0 >= w1) break;
-          uint32_t at[kEvictBatch];
-          bool in[kEvictBatch];
 #pragma unroll
-          for (int b = 0; b < kEvictBatch; ++b) {
-            const uint32_t k = key[b0 + b];
-            in[b] = (k & mask) == prefix && k - 1 < kKeyStays - 1;                     // not a mark
-            at[b] = hist_at(digit - ((k >> bits) & digit));                            // largest first
+          for (int b = b0; b < b0 + kEvictBatch; ++b) {
+            const uint32_t k = key[b];
+            const bool in = d == 0 ? k - 1 < kKeyStays - 1 : (k & mask) == prefix;     // the marks match no later prefix
+            if (in) atomicAdd(&hist[digit - ((k >> bits) & digit)], 1);                // largest first
           }
-#pragma unroll
-          for (int b = 0; b < kEvictBatch; ++b)
-            if (in[b]) atomicAdd(&hist[at[b]], 1);
         }
       }
-      row_sync();
-      const int* all = hist;
+      // every thread adds up kPer neighbouring bins, and the row's threads find the one they lie in
+      int v[kPer];
       if (kCluster) {
-        int* sum = hist + kEvictHist * (1 + d);
-        for (int i = tid; i < kEvictHist; i += kEvictThreads) {
-          const int v = hist[i];
-          if (v == 0) continue;
-          hist[i] = 0;
-          for (int c = 0; c < n_cta; ++c) cluster_add(cluster_addr(sum + i, c), v);
-        }
         cluster_sync_all();
-        all = sum;
+        v[0] = v[1] = 0;
+        for (int c = 0; c < n_cta; ++c) {
+          const int2 x = cluster_load2(cluster_addr(hist + 2 * rtid, c));
+          v[0] += x.x;
+          v[1] += x.y;
+        }
+        hist += kEvictBins;
+      } else {
+        row_sync();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[i] = hist[rtid * kPer + i];
       }
-      // every warp finds the bin: first the lane whose 32 bins hold it, then the bin
       int mine = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int4 v = reinterpret_cast<const int4*>(all)[lane * 9 + i];
-        mine += v.x + v.y + v.z + v.w;
+      for (int i = 0; i < kPer; ++i) mine += v[i];
+      const int incl = warp_scan(mine, lane);
+      if (lane == 31) warp_gt[warp] = incl;
+      row_sync();
+      int above = incl - mine;
+#pragma unroll
+      for (int i = 0; i < kRowWarps; ++i) above += i < part ? warp_gt[slot * kRowWarps + i] : 0;
+      if (above < need && above + mine >= need) {          // one thread
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (above < need && above + v[i] >= need) {
+            found_s[slot][0] = rtid * kPer + i;
+            found_s[slot][1] = above;
+            found_s[slot][2] = v[i];
+          }
+          above += v[i];
+        }
       }
-      int incl = warp_scan(mine, lane);
-      const int l0 = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
-      const int before = __shfl_sync(0xffffffffu, incl - mine, l0);
-      const int v = all[l0 * 36 + lane];
-      incl = before + warp_scan(v, lane);
-      const int l1 = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
-      const int count = __shfl_sync(0xffffffffu, v, l1);
-      need -= __shfl_sync(0xffffffffu, incl, l1) - count;
-      prefix |= (digit - (uint32_t)(l0 * 32 + l1)) << bits;
+      if (!kCluster) {                                     // this thread's bins have been read by itself alone
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) hist[rtid * kPer + i] = 0;
+      }
+      row_sync();
+      need -= found_s[slot][1];
+      prefix |= (digit - (uint32_t)found_s[slot][0]) << bits;
       mask |= digit << bits;
       e.cut = prefix;
       e.ties = need;
-      if (count == need) {                                 // the whole bin stays
+      if (found_s[slot][2] == need) {                      // the whole bin stays
         e.cut = prefix - 1;
         e.ties = 0;
         break;
-      }
-      if (!kCluster && d + 1 < kEvictDigits) {
-        row_sync();
-        for (int i = rtid; i < kEvictHist; i += n_thr) hist[i] = 0;
-        row_sync();
       }
     }
   }
@@ -282,6 +293,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
+  row_sync();                                              // warp_gt's sums have been read
   if (lane == 0) {
     warp_gt[warp] = gt;
     warp_eq[warp] = eq;
@@ -304,15 +316,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
       tied += cta_eq[i];
     }
   }
-  for (int i = 0; i < part; ++i) {
-    pos += warp_gt[slot * kRowWarps + i];
-    tied += warp_eq[slot * kRowWarps + i];
+#pragma unroll
+  for (int i = 0; i < kRowWarps; ++i) {
+    pos += i < part ? warp_gt[slot * kRowWarps + i] : 0;
+    tied += i < part ? warp_eq[slot * kRowWarps + i] : 0;
   }
   pos += min(tied, e.ties);
-  int32_t* keep = a.keep + e.row * a.budget;
-  float* w_out = a.weight_out + e.row * a.max_len_out;
-  const int2* t_in = a.table + (int64_t)e.r * a.max_len * a.layers + e.layer;
-  int2* t_out = a.table_out + (int64_t)e.r * a.max_len_out * a.layers + e.layer;
   const uint32_t below = (1u << lane) - 1;
   for (int j0 = w0; j0 < w1; j0 += 32 * K) {
     if (!held) load(j0);
@@ -322,48 +331,51 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
     for (int b0 = 0; b0 < K; b0 += kEvictBatch) {
       if (j0 + 32 * b0 >= w1) break;
       bool stay[kEvictBatch];
-      int at[kEvictBatch];
+#pragma unroll
+      for (int b = 0; b < kEvictBatch; ++b) stay[b] = key[b0 + b] > e.cut;
       if (e.ties > 0) {
 #pragma unroll
         for (int b = 0; b < kEvictBatch; ++b) {
           const bool q = key[b0 + b] == e.cut;
           const uint32_t mq = __ballot_sync(0xffffffffu, q);
-          stay[b] = key[b0 + b] > e.cut || (q && tied + __popc(mq & below) < e.ties);
+          stay[b] = stay[b] || (q && tied + __popc(mq & below) < e.ties);
           tied += __popc(mq);
         }
-      } else {
-#pragma unroll
-        for (int b = 0; b < kEvictBatch; ++b) stay[b] = key[b0 + b] > e.cut;
       }
 #pragma unroll
       for (int b = 0; b < kEvictBatch; ++b) {
         const uint32_t ms = __ballot_sync(0xffffffffu, stay[b]);
-        at[b] = n_kept + __popc(ms & below);
+        if (stay[b]) list[n_kept + __popc(ms & below)] = j0 + 32 * (b0 + b) + lane;
         n_kept += __popc(ms);
       }
-#pragma unroll
-      for (int b = 0; b < kEvictBatch; ++b)
-        if (stay[b]) list[at[b]] = j0 + 32 * (b0 + b) + lane;
     }
     __syncwarp();
-    for (int i0 = lane; i0 < n_kept; i0 += 32 * kGatherBatch) {
-      int j[kGatherBatch];
-      float x[kGatherBatch];
-      int2 pages[kGatherBatch];
+    {
+      const float* w = a.weight + e.row * a.max_len;
+      const int2* t_in = a.table + (int64_t)e.r * a.max_len * a.layers + e.layer;
+      int32_t* keep = a.keep + e.row * a.budget + pos;
+      float* w_out = a.weight_out + e.row * a.max_len_out + pos;
+      int2* t_out = a.table_out + ((int64_t)e.r * a.max_len_out + pos) * a.layers + e.layer;
+      constexpr int kBatch = 4;                            // reads a thread has in flight
+      for (int i0 = lane; i0 < n_kept; i0 += 32 * kBatch) {
+        int j[kBatch];
+        float x[kBatch];
+        int2 pages[kBatch];
 #pragma unroll
-      for (int b = 0; b < kGatherBatch; ++b) j[b] = list[min(i0 + 32 * b, n_kept - 1)];
+        for (int b = 0; b < kBatch; ++b) j[b] = list[min(i0 + 32 * b, n_kept - 1)];
 #pragma unroll
-      for (int b = 0; b < kGatherBatch; ++b) {
-        x[b] = __ldg(w + j[b]);
-        if (kRows == 1) pages[b] = __ldg(t_in + (int64_t)j[b] * a.layers);
-      }
+        for (int b = 0; b < kBatch; ++b) {
+          x[b] = __ldg(w + j[b]);
+          if (kRows == 1) pages[b] = __ldg(t_in + (int64_t)j[b] * a.layers);
+        }
 #pragma unroll
-      for (int b = 0; b < kGatherBatch; ++b) {
-        const int i = pos + i0 + 32 * b;
-        if (i0 + 32 * b >= n_kept) break;
-        keep[i] = j[b];
-        w_out[i] = x[b];
-        if (kRows == 1) t_out[(int64_t)i * a.layers] = pages[b];
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + 32 * b;
+          if (i >= n_kept) break;
+          keep[i] = j[b];
+          w_out[i] = x[b];
+          if (kRows == 1) t_out[(int64_t)i * a.layers] = pages[b];
+        }
       }
     }
     pos += n_kept;
@@ -371,6 +383,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   }
   if (live) {
     const int step = n_cta * n_thr, first = e.n_keep + rank * n_thr + rtid;
+    int32_t* keep = a.keep + e.row * a.budget;
+    float* w_out = a.weight_out + e.row * a.max_len_out;
+    int2* t_out = a.table_out + (int64_t)e.r * a.max_len_out * a.layers + e.layer;
     for (int i = first; i < a.budget; i += step) keep[i] = -1;
     for (int i = first; i < a.max_len_out; i += step) {
       w_out[i] = 0.f;
@@ -381,22 +396,24 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   if (kRows == 1) return;
 
   // the page table of the CTA's rows: thread = (position, row), rows fastest
+  const int trow = tid % kRows, tid_row = blockIdx.x * kRows + trow;
   if (rtid == 0) keep_n[slot] = e.n_keep;
   __syncthreads();
-  const int k = tid % kRows, gid = blockIdx.x * kRows + k;
-  if (gid >= rows) return;
-  const int layer = gid % a.layers, r = gid / a.layers, n_keep = keep_n[k];
-  t_in = a.table + (int64_t)r * a.max_len * a.layers + layer;
-  t_out = a.table_out + (int64_t)r * a.max_len_out * a.layers + layer;
-  constexpr int kStep = kEvictThreads / kRows;             // positions a pass of the CTA covers
-  int i0 = tid / kRows;
-  for (; i0 < n_keep; i0 += kStep * kGatherBatch) {
-    int2 pages[kGatherBatch];
+  if (tid_row >= rows) return;
+  const int layer = tid_row % a.layers, r = tid_row / a.layers, n_keep = keep_n[trow];
+  const int2* t_in = a.table + (int64_t)r * a.max_len * a.layers + layer;
+  int2* t_out = a.table_out + (int64_t)r * a.max_len_out * a.layers + layer;
+  const int* list = lists + trow * keep_cap;
+  constexpr int kStep = kEvictThreads / kRows, kBatch = 8; // positions a pass of the CTA covers, reads in flight
+  for (int i0 = tid / kRows; i0 < n_keep; i0 += kStep * kBatch) {
+    int2 pages[kBatch];
 #pragma unroll
-    for (int b = 0; b < kGatherBatch; ++b)
-      pages[b] = __ldg(t_in + (int64_t)lists[k * keep_cap + min(i0 + kStep * b, n_keep - 1)] * a.layers);
+    for (int b = 0; b < kBatch; ++b) {
+      const int j = list[min(i0 + kStep * b, n_keep - 1)];
+      pages[b] = __ldg(t_in + (int64_t)j * a.layers);
+    }
 #pragma unroll
-    for (int b = 0; b < kGatherBatch; ++b) {
+    for (int b = 0; b < kBatch; ++b) {
       if (i0 + kStep * b >= n_keep) break;
       t_out[(int64_t)(i0 + kStep * b) * a.layers] = pages[b];
     }
@@ -405,18 +422,16 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
 }
 
 constexpr int kShortRow = 4096;                            // four rows a CTA up to this length
-constexpr int kEvictMaxSmem = ((1 + kEvictDigits) * kEvictHist + kEvictWarps * 1024) * 4;
-static_assert(kEvictMaxSmem >= (4 * kEvictHist + 4 * kShortRow) * 4, "the kept lists of four rows fit");
 
 template <int K, int kRowWarps, bool kCluster>
 int launch_evict(const lora_pool* p, const EvictArgs& a, int n_cta, cudaStream_t st) {
   const int64_t rows = (int64_t)a.n_req * a.layers;
-  constexpr int kRows = kEvictWarps / kRowWarps;
+  constexpr int kRows = kEvictWarps / kRowWarps, kHists = kCluster ? kEvictDigits : kRows;
   const int keep_cap = kRows > 1 ? std::min(a.budget, a.max_len) : 0;
-  const int smem = (kEvictHist * (kCluster ? 1 + kEvictDigits : kRows) +
-                    (kRows > 1 ? kRows * keep_cap : kEvictWarps * 32 * K)) * (int)sizeof(int);
+  const int smem = (kHists * kEvictBins + (kRows > 1 ? kRows * keep_cap : kEvictWarps * 32 * K)) * (int)sizeof(int);
+  constexpr int kMost = (kHists * kEvictBins + (kRows > 1 ? kRows * kShortRow : kEvictWarps * 32 * K)) * (int)sizeof(int);
   static DeviceFlags flags;
-  const int rc = ensure_smem_attr(flags, &kv_evict_kernel<K, kRowWarps, kCluster>, kEvictMaxSmem, "lora_kv_evict");
+  const int rc = ensure_smem_attr(flags, &kv_evict_kernel<K, kRowWarps, kCluster>, kMost, "lora_kv_evict");
   if (rc != LORA_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(kCluster ? rows * n_cta : (rows + kRows - 1) / kRows));
@@ -518,13 +533,15 @@ extern "C" int lora_kv_evict(lora_pool* p, int32_t n_req, const int32_t* table_d
   a.max_len_out = max_len_out;
   a.err = p->d_err;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (max_len <= kShortRow) return launch_evict_k<4, false>(p, a, 1, st);
-  // Long rows: a CTA's registers hold 16,384 weights; beyond that, and as long as all CTAs run at
-  // once and slices stay above 2,048 tokens, a cluster per row.
   const int64_t rows = (int64_t)n_req * layers;
+  const int sms = device_sm_count();
+  if (max_len <= kShortRow && rows >= 4 * (int64_t)sms) return launch_evict_k<4, false>(p, a, 1, st);
+  // Few rows or long ones.  A CTA's registers hold 16,384 weights; beyond that, and as long as all
+  // CTAs run at once and slices stay above 2,048 tokens, a cluster per row.
   int n_cta = 1;
   while (n_cta < kEvictMaxCluster && max_len / (2 * n_cta) >= 2048 &&
-         (max_len / n_cta > 16384 || rows * n_cta <= 2 * (int64_t)device_sm_count()) && rows * n_cta * 2 <= INT32_MAX)
+         (max_len / n_cta > 16384 || rows * n_cta <= 2 * (int64_t)sms) && rows * n_cta * 2 <= INT32_MAX)
     n_cta *= 2;
-  return n_cta > 1 ? launch_evict_k<kEvictWarps, true>(p, a, n_cta, st) : launch_evict_k<kEvictWarps, false>(p, a, 1, st);
+  return n_cta > 1 ? launch_evict_k<kEvictWarps, true>(p, a, n_cta, st)
+                   : launch_evict_k<kEvictWarps, false>(p, a, 1, st);
 }
