@@ -158,11 +158,22 @@ def _ptr(obj) -> Optional[int]:
     raise TypeError(f"cannot take a pointer of {type(obj)!r}")
 
 
+_current_stream = None
+
+
 def _stream(stream) -> Optional[int]:
     if stream is not None:
         return int(stream) if not hasattr(stream, "cuda_stream") else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        handle = torch.cuda.current_stream().cuda_stream       # sets CUDA up
+        raw, device = (getattr(torch._C, f, None) for f in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        # The handle without a Stream object around it: 0.2 us instead of 3 us of every call.
+        _current_stream = ((lambda: raw(device())) if raw and device
+                           else (lambda: torch.cuda.current_stream().cuda_stream))
+        return handle
+    return _current_stream()
 
 
 def _check(rc: int) -> None:
