@@ -30,8 +30,8 @@ namespace {
 constexpr int kSplitMaxGroup = 16;                  // query heads per KV head
 constexpr int kWarps = 4;                           // consumer warps
 // A bulk copy costs its warp about 35 cycles to issue, whatever its size, so slices below 1 KB need
-// two producer warps (one for K, one for V) to keep up: 160,000 tokens of 512-byte slices (D = 64,
-// 4 heads a CTA) take 324 us with one and 214 us with two; from 1 KB one is enough (a long request
+// two producer warps (one for K, one for V) to keep up: 160,000 tokens in 512-byte slices (four
+// heads of 64) take 324 us with one and 214 us with two; from 1 KB one is enough (a long request
 // at D = 128: 316 us with one, 321 us with two).
 constexpr int kSmallSlice = 1024;
 constexpr int threads_of(int producers) { return 32 * (kWarps + producers); }
@@ -43,12 +43,13 @@ constexpr int kMaxStages = 8;
 constexpr int kMaxSmem = (228 * 1024 / kCtasPerSm - 1024) & ~1023;   // a CTA's share, 1 KB of it reserved
 constexpr int kStaticSmem = 1024;                   // barriers and stage records
 constexpr int kJoinWarps = 4;
-constexpr int kJoinUnit = 32;                       // tokens whose weights a block takes at a time
+constexpr int kJoinUnit = 64;                       // tokens whose weights a block takes at a time
 
 // How a call is cut: fixed by the shapes, the same for the size query and the launch.
 struct SplitPlan {
   int32_t D, group, n_kv;
   int32_t n_groups, heads;       // groups of KV heads, KV heads per group
+  int32_t head_warps;            // warps that take the group's heads: one head each, or two (D = 64)
   int32_t sharers;               // warps that share a head
   int32_t tile_sharers;          // of them, those that take a stage's tiles in turn; the rest take turns at stages
   int32_t tiles;                 // 16-token tiles per stage
@@ -140,9 +141,9 @@ struct StageInfo {
   uint16_t mask[kMaxTiles];      // per tile: bit i = token i has data
 };
 
-// Where a range begins in the sequence of all requests' units.
+// Where a range begins in the sequence of all requests' units, and the length of its first request.
 struct RangeStart {
-  int32_t req, tok, units;
+  int32_t req, tok, units, n;
 };
 
 // Prefix sum over the warp's lanes.
@@ -156,24 +157,34 @@ __device__ __forceinline__ int warp_inclusive(int v, int lane) {
 }
 
 // The range [p U / P, (p + 1) U / P) of the U units of all requests (one unit: `st` tokens), with
-// P = min(parts, U).  Up to 32 requests every warp finds it alone; beyond, the block's warps sum the
-// units of 32 requests at a time into `sums`, and every warp searches those.  Units fit in 32 bits
-// (checked by the host).
+// P = min(parts, U).  Up to 128 requests every warp finds it alone, four requests a lane; beyond, the
+// block's warps sum the units of 128 requests at a time into `sums`, and every warp searches those.
+// Units fit in 32 bits (checked by the host).
 __device__ RangeStart find_range(const SplitArgs& a, int p, int parts, int st, int32_t* sums) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_sums = (a.n_req + 31) / 32;
-  const auto units_of = [&](int r) {
-    if (r >= a.n_req) return 0;
-    const int n = a.seq_len[r];
-    if (n < 0 || n > a.max_len) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
-    return (int)(((long long)(n < 0 ? 0 : n > a.max_len ? a.max_len : n) + st - 1) / st);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_sums = (a.n_req + 127) / 128;
+  int len[4], units[4], mine = 0, total = 0;               // requests 128 t + 4 lane ..
+  const auto look = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 128 * t + 4 * lane + i;
+      const int n = r < a.n_req ? a.seq_len[r] : 0;
+      if (n < 0 || n > a.max_len) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
+      len[i] = n < 0 ? 0 : n > a.max_len ? a.max_len : n;
+    }
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      units[i] = (int)(((unsigned)len[i] + (unsigned)st - 1) / (unsigned)st);
+      mine += units[i];
+    }
   };
-  int total = 0, mine = 0;
   if (n_sums == 1) {
-    mine = units_of(lane);
+    look(0);
     total = __reduce_add_sync(0xffffffffu, mine);
   } else {
     for (int t = warp; t < n_sums; t += blockDim.x >> 5) {
-      const int u = __reduce_add_sync(0xffffffffu, units_of(32 * t + lane));
+      look(t);
+      const int u = __reduce_add_sync(0xffffffffu, mine);
       if (lane == 0) sums[t] = u;
     }
     __syncthreads();
@@ -185,27 +196,40 @@ __device__ RangeStart find_range(const SplitArgs& a, int p, int parts, int st, i
   const int q0 = min(p, P), q1 = min(p + 1, P);
   const int d = total / P, m = total % P;                  // p U / P without overflow: U = d P + m
   const int u0 = q0 * d + q0 * m / P, u1 = q1 * d + q1 * m / P;
-  int before = 0, tile = 0;                                // units of the requests looked at so far
+  if (u1 == u0) return RangeStart{0, 0, 0, 0};
+  int before = 0, t = 0;                                   // units of the requests looked at so far
   if (n_sums > 1) {
-    for (int t0 = 0; t0 < n_sums; t0 += 32) {              // the block of 32 requests that holds u0
+    for (int t0 = 0; t0 < n_sums; t0 += 32) {              // the block of 128 requests that holds u0
       const int s = t0 + lane < n_sums ? sums[t0 + lane] : 0;
       const int incl = warp_inclusive(s, lane);
       const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > u0);
       if (hit) {
         const int k = __ffs(hit) - 1;
-        tile = t0 + k;
+        t = t0 + k;
         before += __shfl_sync(0xffffffffu, incl - s, k);
         break;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    mine = units_of(32 * tile + lane);
+    look(t);
   }
   const int incl = warp_inclusive(mine, lane);
-  const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > u0);
-  const int k = hit ? __ffs(hit) - 1 : 0;
-  const int off = u0 - (before + __shfl_sync(0xffffffffu, incl - mine, k));
-  return RangeStart{32 * tile + k, u1 > u0 ? (int)((long long)off * st) : 0, u1 - u0};
+  const int k = __ffs(__ballot_sync(0xffffffffu, before + incl > u0)) - 1;      // the lane, then its request
+  before += __shfl_sync(0xffffffffu, incl - mine, k);
+  RangeStart rs{128 * t + 4 * k, 0, u1 - u0, 0};
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int u = __shfl_sync(0xffffffffu, units[i], k), n = __shfl_sync(0xffffffffu, len[i], k);
+    if (!found && before + u > u0) {
+      rs.req += i;
+      rs.tok = (u0 - before) * st;
+      rs.n = n;
+      found = true;
+    }
+    before += u;
+  }
+  return rs;
 }
 
 // Walks a range one unit at a time.
@@ -236,7 +260,7 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
 // fragment (movmatrix) as two bf16 terms, hi + lo, so the weights carry 16 mantissa bits.
 // A tile's K and V fragments are all in registers before its softmax starts, and the stage is given
 // back then: the chain of a tile (products, shuffles, exponentials) holds up no copy.
-template <int D, int NT, int TILES, int NP>
+template <int D, int NT, int TILES, int NP, int HW>
 __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_kernel(const __grid_constant__ SplitArgs a) {
   constexpr int KS = D / 16;
   constexpr int VR = NT == 1 || D < 256 ? (KS < 8 ? KS : 8) : 4;   // V fragments held over the softmax
@@ -257,7 +281,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(bar_full + 8 * s, NP);
-      mbar_init(bar_empty + 8 * s, n_act * pl.sharers);
+      mbar_init(bar_empty + 8 * s, min(pl.head_warps, n_act) * pl.sharers);
     }
     for (int h = 0; h < kWarps; ++h) {
       mbar_init(bar_ready + 8 * h, 1);
@@ -270,7 +294,10 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   if (pl.whole) {
     const int n = a.seq_len[p];
     if (threadIdx.x == 0 && (n < 0 || n > a.max_len)) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
-    rs = RangeStart{p, 0, (int32_t)(((int64_t)(n < 0 ? 0 : min(n, a.max_len)) + st - 1) / st)};
+    rs.req = p;
+    rs.tok = 0;
+    rs.n = n < 0 ? 0 : min(n, a.max_len);
+    rs.units = (int32_t)(((unsigned)rs.n + st - 1) / st);
   } else {
     rs = find_range(a, p, pl.parts, st, reinterpret_cast<int32_t*>(merge));
   }
@@ -285,8 +312,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
     const uint32_t dst0 = ring + (uint32_t)(half * TILES * kTile + ti) * RB;
     const uint16_t* rows = a.pool + h0 * D;
     const int64_t unit_step = (int64_t)st * a.layers * 2;
-    UnitWalk w{rs.req, rs.tok, rs.units > 0 ? request_length(a, rs.req) : 0, rs.units, true};
-    walk_begin(a, w);
+    UnitWalk w{rs.req, rs.tok, rs.n, rs.units, true};
     const auto entry = [&](const UnitWalk& u) {            // this lane's table entry of a unit's first tile
       return a.table + ((((int64_t)u.req * a.max_len + u.tok + ti) * a.layers) + a.layer) * 2 + half;
     };
@@ -375,31 +401,36 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   }
 
   // ---- consumers ----
-  const int hh = warp % pl.heads, share = warp / pl.heads;
+  const int hh = warp % pl.head_warps, share = warp / pl.head_warps;
   if (share >= pl.sharers || hh >= n_act || rs.units == 0) return;
+  const int n_mine = HW == 1 || hh + pl.head_warps >= n_act ? 1 : 2;           // this warp's heads: hh, hh + head_warps
   const int g = lane >> 2, t = lane & 3;
-  const int G = pl.group, head0 = (h0 + hh) * G;           // the KV head's first query head
-  uint32_t qf[NT][KS][2];
-  float acc[NT][KS][4], m[NT][2], l[NT][2];
+  const int G = pl.group;
+  const auto head_of = [&](int u) { return (h0 + hh + u * pl.head_warps) * G; };   // the KV head's first query head
+  uint32_t qf[HW][NT][KS][2];
+  float acc[HW][NT][KS][4], m[HW][NT][2], l[HW][NT][2];
   const auto load_q = [&](int req) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const bool has = nt * 8 + g < G;
-      const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + req * a.q_stride + (int64_t)(head0 + nt * 8 + g) * D) + t;
+    for (int u = 0; u < HW; ++u)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        qf[nt][ks][0] = has ? qp[ks * 8] : 0u;
-        qf[nt][ks][1] = has ? qp[ks * 8 + 4] : 0u;
+      for (int nt = 0; nt < NT; ++nt) {
+        const bool has = nt * 8 + g < G && u < n_mine;
+        const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + req * a.q_stride + (int64_t)(head_of(u) + nt * 8 + g) * D) + t;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          qf[u][nt][ks][0] = has ? qp[ks * 8] : 0u;
+          qf[u][nt][ks][1] = has ? qp[ks * 8 + 4] : 0u;
+        }
       }
-    }
   };
   // lane addresses of the fragments within a tile
   const uint32_t k_lane = (uint32_t)(lane & 15) * RB + (uint32_t)(hh * D + (lane >> 4) * 8) * 2;
   const uint32_t v_lane = (uint32_t)(TILES * kTile + (lane & 7) + (lane >> 4) * 8) * RB +
                           (uint32_t)(hh * D + ((lane >> 3) & 1) * 8) * 2;
+  const uint32_t head_step = (uint32_t)(pl.head_warps * D * 2);
   const int turns = pl.sharers / tile_sharers, turn = share / tile_sharers;
   int seg = 0;                                             // segments finished: the phase of the merge barriers
-  bool have_q = false;
+  load_q(rs.req);                                          // on its way beside the first stages
   int next_s = 0, next_turn = 0;
   uint32_t phase = 0;
   for (int left = rs.units; left > 0; --left) {
@@ -417,15 +448,15 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
     const int req = info[s].req, n = info[s].n, flags = info[s].flags, tok = info[s].tok, next = info[s].next;
     __syncwarp();
     if (flags & kFirst) {
-      if (!have_q) load_q(req);
-      have_q = true;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int u = 0; u < HW; ++u)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) acc[nt][ks][0] = acc[nt][ks][1] = acc[nt][ks][2] = acc[nt][ks][3] = 0.f;
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
-      }
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) acc[u][nt][ks][0] = acc[u][nt][ks][1] = acc[u][nt][ks][2] = acc[u][nt][ks][3] = 0.f;
+          m[u][nt][0] = m[u][nt][1] = -INFINITY;
+          l[u][nt][0] = l[u][nt][1] = 0.f;
+        }
     }
     if (!mine && lane == 0) mbar_arrive(bar_empty + 8 * s);
     for (int tile = mine ? share % tile_sharers : TILES; tile < TILES; tile += tile_sharers) {
@@ -439,110 +470,115 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
         continue;
       }
       const uint32_t mask = info[s].mask[tile];
-      const uint32_t base = ring + (uint32_t)s * pl.stage_bytes + (uint32_t)(tile * kTile) * RB;
-      float sc[NT][4], odd[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < HW; ++u) {
+        if (u >= n_mine) break;
+        const bool release = final_tile && u + 1 == n_mine;
+        const uint32_t base = ring + (uint32_t)s * pl.stage_bytes + (uint32_t)(tile * kTile) * RB + u * head_step;
+        float sc[NT][4], odd[NT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[nt][i] = odd[nt][i] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k0 = 0; k0 < KS; k0 += 4) {
-        uint32_t kf[4][4];
+          for (int i = 0; i < 4; ++i) sc[nt][i] = odd[nt][i] = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ldmatrix_x4(kf[k], base + k_lane + (k0 + k) * 32);
+        for (int k0 = 0; k0 < KS; k0 += 4) {
+          uint32_t kf[4][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k) ldmatrix_x4(kf[k], base + k_lane + (k0 + k) * 32);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_16x8x16(k & 1 ? odd[nt] : sc[nt], kf[k], qf[nt][k0 + k][0], qf[nt][k0 + k][1]);
-      }
-      uint32_t vf[VR][4];
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int k = 0; k < VR; ++k) ldmatrix_x4_trans(vf[k], base + v_lane + k * 32);
-      if (VR == KS && final_tile) {                        // everything of the stage is in registers
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_empty + 8 * s);
-      }
-      const bool v0 = (mask >> g) & 1u, v1 = (mask >> (g + 8)) & 1u;
-      uint32_t ph[NT][2], plo[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        sc[nt][0] = v0 ? (sc[nt][0] + odd[nt][0]) * a.scale_log2 : -INFINITY;
-        sc[nt][1] = v0 ? (sc[nt][1] + odd[nt][1]) * a.scale_log2 : -INFINITY;
-        sc[nt][2] = v1 ? (sc[nt][2] + odd[nt][2]) * a.scale_log2 : -INFINITY;
-        sc[nt][3] = v1 ? (sc[nt][3] + odd[nt][3]) * a.scale_log2 : -INFINITY;
-        if (a.ws_scores) {
-          float* dst = a.ws_scores + ((int64_t)req * a.n_heads + head0 + nt * 8 + 2 * t) * a.score_stride + j0 + g;
-          if (nt * 8 + 2 * t < G) {
-            dst[0] = sc[nt][0];
-            dst[8] = sc[nt][2];
-          }
-          if (nt * 8 + 2 * t + 1 < G) {
-            dst[a.score_stride] = sc[nt][1];
-            dst[a.score_stride + 8] = sc[nt][3];
-          }
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16x8x16(k & 1 ? odd[nt] : sc[nt], kf[k], qf[u][nt][k0 + k][0], qf[u][nt][k0 + k][1]);
         }
-        float c[2];
+        uint32_t vf[VR][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float x = fmaxf(sc[nt][k], sc[nt][2 + k]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          const float mn = fmaxf(m[nt][k], x);
-          const float ms = mn == -INFINITY ? 0.f : mn;     // no score above -infinity yet: every weight 0
-          c[k] = exp2f(m[nt][k] - ms);
-          sc[nt][k] = exp2f(sc[nt][k] - ms);
-          sc[nt][2 + k] = exp2f(sc[nt][2 + k] - ms);
-          l[nt][k] = fmaf(l[nt][k], c[k], sc[nt][k] + sc[nt][2 + k]);
-          m[nt][k] = mn;
+        for (int k = 0; k < VR; ++k) ldmatrix_x4_trans(vf[k], base + v_lane + k * 32);
+        if (VR == KS && release) {                         // everything of the stage is in registers
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_empty + 8 * s);
         }
-        if (__any_sync(0xffffffffu, c[0] != 1.f || c[1] != 1.f)) {
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            acc[nt][ks][0] *= c[0];
-            acc[nt][ks][1] *= c[1];
-            acc[nt][ks][2] *= c[0];
-            acc[nt][ks][3] *= c[1];
-          }
-        }
-        const uint32_t h_lo = pack_bf16(sc[nt][0], sc[nt][1]), h_hi = pack_bf16(sc[nt][2], sc[nt][3]);
-        ph[nt][0] = transpose_8x8(h_lo);
-        ph[nt][1] = transpose_8x8(h_hi);
-        plo[nt][0] = transpose_8x8(pack_bf16(sc[nt][0] - bf16_lo(h_lo), sc[nt][1] - bf16_hi(h_lo)));
-        plo[nt][1] = transpose_8x8(pack_bf16(sc[nt][2] - bf16_lo(h_hi), sc[nt][3] - bf16_hi(h_hi)));
-      }
-      // V of a token without data is whatever the stage held before: its bits are cleared.
-      const bool partial = mask != 0xFFFFu;
-      const uint32_t b0 = mask >> (2 * t), b1 = mask >> (2 * t + 8);
-      const uint32_t and0 = ((b0 & 1u) ? 0xFFFFu : 0u) | ((b0 & 2u) ? 0xFFFF0000u : 0u);
-      const uint32_t and1 = ((b1 & 1u) ? 0xFFFFu : 0u) | ((b1 & 2u) ? 0xFFFF0000u : 0u);
-#pragma unroll
-      for (int k0 = 0; k0 < KS; k0 += VR) {
-        if (k0 > 0) {
-#pragma unroll
-          for (int k = 0; k < VR; ++k) ldmatrix_x4_trans(vf[k], base + v_lane + (k0 + k) * 32);
-        }
-        if (partial) {
-#pragma unroll
-          for (int k = 0; k < VR; ++k) {
-            vf[k][0] &= and0;
-            vf[k][1] &= and0;
-            vf[k][2] &= and1;
-            vf[k][3] &= and1;
-          }
-        }
+        const bool v0 = (mask >> g) & 1u, v1 = (mask >> (g + 8)) & 1u;
+        uint32_t ph[NT][2], plo[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          sc[nt][0] = v0 ? (sc[nt][0] + odd[nt][0]) * a.scale_log2 : -INFINITY;
+          sc[nt][1] = v0 ? (sc[nt][1] + odd[nt][1]) * a.scale_log2 : -INFINITY;
+          sc[nt][2] = v1 ? (sc[nt][2] + odd[nt][2]) * a.scale_log2 : -INFINITY;
+          sc[nt][3] = v1 ? (sc[nt][3] + odd[nt][3]) * a.scale_log2 : -INFINITY;
+          if (a.ws_scores) {
+            float* dst = a.ws_scores + ((int64_t)req * a.n_heads + head_of(u) + nt * 8 + 2 * t) * a.score_stride + j0 + g;
+            if (nt * 8 + 2 * t < G) {
+              dst[0] = sc[nt][0];
+              dst[8] = sc[nt][2];
+            }
+            if (nt * 8 + 2 * t + 1 < G) {
+              dst[a.score_stride] = sc[nt][1];
+              dst[a.score_stride + 8] = sc[nt][3];
+            }
+          }
+          float c[2];
 #pragma unroll
-          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[nt][k0 + k], vf[k], ph[nt][0], ph[nt][1]);
+          for (int k = 0; k < 2; ++k) {
+            float x = fmaxf(sc[nt][k], sc[nt][2 + k]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float mn = fmaxf(m[u][nt][k], x);
+            const float ms = mn == -INFINITY ? 0.f : mn;   // no score above -infinity yet: every weight 0
+            c[k] = exp2f(m[u][nt][k] - ms);
+            sc[nt][k] = exp2f(sc[nt][k] - ms);
+            sc[nt][2 + k] = exp2f(sc[nt][2 + k] - ms);
+            l[u][nt][k] = fmaf(l[u][nt][k], c[k], sc[nt][k] + sc[nt][2 + k]);
+            m[u][nt][k] = mn;
+          }
+          if (__any_sync(0xffffffffu, c[0] != 1.f || c[1] != 1.f)) {
 #pragma unroll
-          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[nt][k0 + k], vf[k], plo[nt][0], plo[nt][1]);
+            for (int ks = 0; ks < KS; ++ks) {
+              acc[u][nt][ks][0] *= c[0];
+              acc[u][nt][ks][1] *= c[1];
+              acc[u][nt][ks][2] *= c[0];
+              acc[u][nt][ks][3] *= c[1];
+            }
+          }
+          const uint32_t h_lo = pack_bf16(sc[nt][0], sc[nt][1]), h_hi = pack_bf16(sc[nt][2], sc[nt][3]);
+          ph[nt][0] = transpose_8x8(h_lo);
+          ph[nt][1] = transpose_8x8(h_hi);
+          plo[nt][0] = transpose_8x8(pack_bf16(sc[nt][0] - bf16_lo(h_lo), sc[nt][1] - bf16_hi(h_lo)));
+          plo[nt][1] = transpose_8x8(pack_bf16(sc[nt][2] - bf16_lo(h_hi), sc[nt][3] - bf16_hi(h_hi)));
         }
-      }
-      if (VR < KS && final_tile) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+        // V of a token without data is whatever the stage held before: its bits are cleared.
+        const bool partial = mask != 0xFFFFu;
+        const uint32_t b0 = mask >> (2 * t), b1 = mask >> (2 * t + 8);
+        const uint32_t and0 = ((b0 & 1u) ? 0xFFFFu : 0u) | ((b0 & 2u) ? 0xFFFF0000u : 0u);
+        const uint32_t and1 = ((b1 & 1u) ? 0xFFFFu : 0u) | ((b1 & 2u) ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int k0 = 0; k0 < KS; k0 += VR) {
+          if (k0 > 0) {
+#pragma unroll
+            for (int k = 0; k < VR; ++k) ldmatrix_x4_trans(vf[k], base + v_lane + (k0 + k) * 32);
+          }
+          if (partial) {
+#pragma unroll
+            for (int k = 0; k < VR; ++k) {
+              vf[k][0] &= and0;
+              vf[k][1] &= and0;
+              vf[k][2] &= and1;
+              vf[k][3] &= and1;
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][nt][k0 + k], vf[k], ph[nt][0], ph[nt][1]);
+#pragma unroll
+            for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][nt][k0 + k], vf[k], plo[nt][0], plo[nt][1]);
+          }
+        }
+        if (VR < KS && release) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+        }
       }
     }
     if (!(flags & kLast)) continue;
@@ -550,23 +586,25 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
     // ---- the segment's end: sum l over the token lanes, join the warps that share the head ----
     if (next >= 0) load_q(next);                           // on its way while this segment is finished
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int u = 0; u < HW; ++u)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 4);
-        l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 8);
-        l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 16);
-      }
-    if (pl.sharers > 1) {
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          l[u][nt][k] += __shfl_xor_sync(0xffffffffu, l[u][nt][k], 4);
+          l[u][nt][k] += __shfl_xor_sync(0xffffffffu, l[u][nt][k], 8);
+          l[u][nt][k] += __shfl_xor_sync(0xffffffffu, l[u][nt][k], 16);
+        }
+    if (HW == 1 && pl.sharers > 1) {
       float* mb = merge + (size_t)hh * G * (D + 2);        // [group][D + 2]: acc, m, l
       // One buffer per head, used by its warps in turn: warp `share` writes it once the warp before
       // (or, for the first, the last of the previous segment) has been added, and share 0 adds it.
       for (int o = 1; o < pl.sharers; ++o) {
-        const uint32_t ready = bar_ready + 8 * (o * pl.heads + hh);
+        const uint32_t ready = bar_ready + 8 * (o * pl.head_warps + hh);
         if (share == o) {
           const int before = o > 1 ? o - 1 : pl.sharers - 1;
           const uint32_t parity = o > 1 ? seg & 1 : (seg & 1) ^ 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(bar_done + 8 * (before * pl.heads + hh), parity))) {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_done + 8 * (before * pl.head_warps + hh), parity))) {
             if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
             return;
           }
@@ -578,12 +616,12 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
               if (qi >= G) continue;
 #pragma unroll
               for (int ks = 0; ks < KS; ++ks) {
-                mb[qi * (D + 2) + ks * 16 + g] = acc[nt][ks][k];
-                mb[qi * (D + 2) + ks * 16 + g + 8] = acc[nt][ks][2 + k];
+                mb[qi * (D + 2) + ks * 16 + g] = acc[0][nt][ks][k];
+                mb[qi * (D + 2) + ks * 16 + g + 8] = acc[0][nt][ks][2 + k];
               }
               if (g == 0) {
-                mb[qi * (D + 2) + D] = m[nt][k];
-                mb[qi * (D + 2) + D + 1] = l[nt][k];
+                mb[qi * (D + 2) + D] = m[0][nt][k];
+                mb[qi * (D + 2) + D + 1] = l[0][nt][k];
               }
             }
           __syncwarp();
@@ -600,18 +638,18 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
               const int qi = nt * 8 + 2 * t + k;
               if (qi >= G) continue;
               const float om = mb[qi * (D + 2) + D], ol = mb[qi * (D + 2) + D + 1];
-              const float mn = fmaxf(m[nt][k], om), ms = mn == -INFINITY ? 0.f : mn;
-              const float c0 = exp2f(m[nt][k] - ms), c1 = exp2f(om - ms);
-              m[nt][k] = mn;
-              l[nt][k] = l[nt][k] * c0 + ol * c1;
+              const float mn = fmaxf(m[0][nt][k], om), ms = mn == -INFINITY ? 0.f : mn;
+              const float c0 = exp2f(m[0][nt][k] - ms), c1 = exp2f(om - ms);
+              m[0][nt][k] = mn;
+              l[0][nt][k] = l[0][nt][k] * c0 + ol * c1;
 #pragma unroll
               for (int ks = 0; ks < KS; ++ks) {
-                acc[nt][ks][k] = acc[nt][ks][k] * c0 + mb[qi * (D + 2) + ks * 16 + g] * c1;
-                acc[nt][ks][2 + k] = acc[nt][ks][2 + k] * c0 + mb[qi * (D + 2) + ks * 16 + g + 8] * c1;
+                acc[0][nt][ks][k] = acc[0][nt][ks][k] * c0 + mb[qi * (D + 2) + ks * 16 + g] * c1;
+                acc[0][nt][ks][2 + k] = acc[0][nt][ks][2 + k] * c0 + mb[qi * (D + 2) + ks * 16 + g + 8] * c1;
               }
             }
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_done + 8 * (o * pl.heads + hh));
+          if (lane == 0) mbar_arrive(bar_done + 8 * (o * pl.head_warps + hh));
         }
       }
       ++seg;
@@ -622,46 +660,51 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
       if (starts) a.ws_range[req].x = p;
       if (ends) a.ws_range[req].y = p;
     }
-    if (starts && ends) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float i0 = l[nt][0] == 0.f ? 0.f : 1.f / l[nt][0], i1 = l[nt][1] == 0.f ? 0.f : 1.f / l[nt][1];
-        uint16_t* row = a.out + req * a.out_stride + (int64_t)(head0 + nt * 8 + g) * D + 2 * t;
+    for (int u = 0; u < HW; ++u) {
+      if (u >= n_mine) break;
+      const int head0 = head_of(u);
+      if (starts && ends) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t lo = transpose_8x8(pack_bf16(acc[nt][ks][0] * i0, acc[nt][ks][1] * i1));
-          const uint32_t hi = transpose_8x8(pack_bf16(acc[nt][ks][2] * i0, acc[nt][ks][3] * i1));
-          if (nt * 8 + g < G) {
-            *reinterpret_cast<uint32_t*>(row + ks * 16) = lo;
-            *reinterpret_cast<uint32_t*>(row + ks * 16 + 8) = hi;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int qi = nt * 8 + 2 * t + k;
-          if (g == 0 && qi < G) {
-            const float z = l[nt][k] == 0.f ? -INFINITY : m[nt][k] + log2f(l[nt][k]);
-            a.ws_lse[(int64_t)req * a.n_heads + head0 + qi] = z;
-            if (a.lse) a.lse[(int64_t)req * a.n_heads + head0 + qi] = z * 0.6931471805599453f;
-          }
-        }
-      }
-    } else {
-      const int64_t slot = partial_slot(p, starts) * a.n_heads + head0;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int qi = nt * 8 + 2 * t + k;
-          if (qi >= G) continue;
-          float* dst = a.ws_acc + (slot + qi) * D;
+        for (int nt = 0; nt < NT; ++nt) {
+          const float i0 = l[u][nt][0] == 0.f ? 0.f : 1.f / l[u][nt][0], i1 = l[u][nt][1] == 0.f ? 0.f : 1.f / l[u][nt][1];
+          uint16_t* row = a.out + req * a.out_stride + (int64_t)(head0 + nt * 8 + g) * D + 2 * t;
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
-            dst[ks * 16 + g] = acc[nt][ks][k];
-            dst[ks * 16 + g + 8] = acc[nt][ks][2 + k];
+            const uint32_t lo = transpose_8x8(pack_bf16(acc[u][nt][ks][0] * i0, acc[u][nt][ks][1] * i1));
+            const uint32_t hi = transpose_8x8(pack_bf16(acc[u][nt][ks][2] * i0, acc[u][nt][ks][3] * i1));
+            if (nt * 8 + g < G) {
+              *reinterpret_cast<uint32_t*>(row + ks * 16) = lo;
+              *reinterpret_cast<uint32_t*>(row + ks * 16 + 8) = hi;
+            }
           }
-          if (g == 0) a.ws_ml[slot + qi] = make_float2(m[nt][k], l[nt][k]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int qi = nt * 8 + 2 * t + k;
+            if (g == 0 && qi < G) {
+              const float z = l[u][nt][k] == 0.f ? -INFINITY : m[u][nt][k] + log2f(l[u][nt][k]);
+              a.ws_lse[(int64_t)req * a.n_heads + head0 + qi] = z;
+              if (a.lse) a.lse[(int64_t)req * a.n_heads + head0 + qi] = z * 0.6931471805599453f;
+            }
+          }
         }
+      } else {
+        const int64_t slot = partial_slot(p, starts) * a.n_heads + head0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int qi = nt * 8 + 2 * t + k;
+            if (qi >= G) continue;
+            float* dst = a.ws_acc + (slot + qi) * D;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              dst[ks * 16 + g] = acc[u][nt][ks][k];
+              dst[ks * 16 + g + 8] = acc[u][nt][ks][2 + k];
+            }
+            if (g == 0) a.ws_ml[slot + qi] = make_float2(m[u][nt][k], l[u][nt][k]);
+          }
+      }
     }
   }
 }
@@ -717,12 +760,13 @@ __device__ __forceinline__ void store_lse(const SplitArgs& a, int r, int h, floa
 // those ranges' blocks find it at once and share its query heads (up to kJoinWarps partials a warp
 // per head, beyond that a block per head).
 // Weights: the blocks cut the tokens of all requests anew into equal ranges.  Per request a block
-// gathers the heads' lse (of a split request from its partials); then lane i of every warp takes
-// token i of 32, warp w every kJoinWarps-th head, and the warps' sums are added in warp order.
+// gathers the heads' lse (of a split request from its partials); then a lane of every warp takes two
+// of 64 tokens, warp w every kJoinWarps-th head, and the warps' sums are added in warp order.
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
   extern __shared__ float dyn[];                           // with weights: [n_heads] lse, the sums of find_range
   __shared__ float part[kJoinWarps][D + 2];
+  __shared__ __align__(8) float sums[2 * kJoinWarps * kJoinUnit];
   constexpr int E = D / 32;
   pdl_wait_then_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -835,21 +879,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
     }
     __syncthreads();
     for (int u = 0; u < units; ++u) {
-      const int64_t j = tok + (int64_t)u * kJoinUnit + lane;
-      float x = 0.f;
+      // two neighbouring tokens a lane; a score row is padded to whole tiles, so the pair is there
+      const int64_t j = tok + (int64_t)u * kJoinUnit + 2 * lane;
+      float x0 = 0.f, x1 = 0.f;
       if (j < n) {
         const float* sc = a.ws_scores + (int64_t)r * a.n_heads * a.score_stride + j;
 #pragma unroll 8
-        for (int h = warp; h < a.n_heads; h += kJoinWarps) x += exp2f(sc[h * a.score_stride] - lse_s[h]);
+        for (int h = warp; h < a.n_heads; h += kJoinWarps) {
+          const float2 v = *reinterpret_cast<const float2*>(sc + h * a.score_stride);
+          x0 += exp2f(v.x - lse_s[h]);
+          x1 += exp2f(v.y - lse_s[h]);
+        }
       }
-      part[warp][lane + 32 * (u & 1)] = x;                 // two buffers: one barrier a turn
+      float* sum = sums + (u & 1) * kJoinWarps * kJoinUnit;                // two buffers: one barrier a turn
+      sum[warp * kJoinUnit + 2 * lane] = x0;
+      sum[warp * kJoinUnit + 2 * lane + 1] = x1;
       __syncthreads();
-      if (warp == 0 && j < n) {
-        float sum = 0.f;
+      const int64_t jt = tok + (int64_t)u * kJoinUnit + threadIdx.x;
+      if (threadIdx.x < kJoinUnit && jt < n) {
+        float x = 0.f;
 #pragma unroll
-        for (int v = 0; v < kJoinWarps; ++v) sum += part[v][lane + 32 * (u & 1)];
-        const int64_t at = r * a.weight_stride + j;
-        a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.f) + sum;
+        for (int v = 0; v < kJoinWarps; ++v) x += sum[v * kJoinUnit + threadIdx.x];
+        const int64_t at = r * a.weight_stride + jt;
+        a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.f) + x;
       }
     }
     left -= units;
@@ -883,19 +935,22 @@ SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads,
   pl.D = H / n_kv;
   pl.group = n_heads / n_kv;
   // Head groups as even as they can be: a stage's K and V fit kStageBytes with 16 tokens, a warp has
-  // one head, and with fewer heads than warps some warps share a head and the stage has more tokens.
-  const int most = std::max(1, std::min(kWarps, kStageBytes / (4 * kTile * pl.D)));
+  // one head, or two of 64 (so that a slice stays 1 KB), and with fewer heads than warps some warps
+  // share a head and the stage has more tokens.
+  const int room_heads = std::max(1, kStageBytes / (4 * kTile * pl.D));
+  const int most = std::min(pl.D == 64 ? 2 * kWarps : kWarps, room_heads);
   pl.n_groups = (n_kv + most - 1) / most;
   pl.heads = (n_kv + pl.n_groups - 1) / pl.n_groups;
+  pl.head_warps = pl.heads > kWarps ? kWarps : pl.heads;   // two heads a warp: hh and hh + kWarps
   const int room = kStageBytes / (4 * kTile * pl.heads * pl.D);
-  pl.sharers = kWarps / pl.heads;                          // a power of two where it is not 1, as is room then
+  pl.sharers = kWarps / pl.head_warps;                     // a power of two where it is not 1, as is room then
   pl.tile_sharers = std::min(pl.sharers, room);
   pl.tiles = std::min(room / pl.tile_sharers, kMaxTiles / pl.tile_sharers) * pl.tile_sharers;
   pl.row_bytes = pl.heads * pl.D * 2 + 16;                 // + 16: ldmatrix's 8 rows on 8 bank groups
   pl.stage_bytes = 2 * kTile * pl.tiles * pl.row_bytes;
-  // behind the ring: the sums of find_range (4 bytes per 32 requests), later the merged heads
+  // behind the ring: the sums of find_range (4 bytes per 128 requests), later the merged heads
   const int merge = pl.sharers > 1 ? pl.heads * pl.group * (pl.D + 2) * 4 : 0;
-  const int tail = std::max(merge, (n_req + 31) / 32 * 4);
+  const int tail = std::max(merge, (n_req + 127) / 128 * 4);
   pl.stages = std::min(kMaxStages, (kMaxSmem - kStaticSmem - tail) / pl.stage_bytes);
   pl.smem = pl.stages * pl.stage_bytes + tail;
   const int sms = device_sm_count() * kCtasPerSm;
@@ -931,33 +986,34 @@ int check_shape(const char* fn, const lora_pool* p, int32_t n_req, int32_t max_l
   return LORA_OK;
 }
 
-template <int D, int NT, int TILES, int NP>
+template <int D, int NT, int TILES, int NP, int HW>
 int launch_split(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   static DeviceFlags flags;
-  const int rc = ensure_smem_attr(flags, &attention_split_kernel<D, NT, TILES, NP>, kMaxSmem - kStaticSmem, "lora_attention_split");
+  const int rc = ensure_smem_attr(flags, &attention_split_kernel<D, NT, TILES, NP, HW>, kMaxSmem - kStaticSmem, "lora_attention_split");
   if (rc != LORA_OK) return rc;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
-  const cudaError_t e = launch_pdl(!p->prof_on, attention_split_kernel<D, NT, TILES, NP>, dim3(a.plan.parts * a.plan.n_groups),
+  const cudaError_t e = launch_pdl(!p->prof_on, attention_split_kernel<D, NT, TILES, NP, HW>, dim3(a.plan.parts * a.plan.n_groups),
                                    dim3(threads_of(NP)), a.plan.smem, st, a);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_attention_split launch");
 }
 
 // The kernel of a shape: split_plan gives these tile counts, and the slices that take two producers.
-template <int D, int TILES, int NP>
+template <int D, int TILES, int NP, int HW>
 int launch_split_group(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
-  return a.plan.group <= 8 ? launch_split<D, 1, TILES, NP>(p, a, st) : launch_split<D, 2, TILES, NP>(p, a, st);
+  return a.plan.group <= 8 ? launch_split<D, 1, TILES, NP, HW>(p, a, st) : launch_split<D, 2, TILES, NP, HW>(p, a, st);
 }
 int launch_split_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   const bool two = a.plan.heads * a.plan.D * 2 < kSmallSlice;
   switch (a.plan.D * 16 + a.plan.tiles) {
-    case 64 * 16 + 2: return launch_split_group<64, 2, 2>(p, a, st);
-    case 64 * 16 + 4: return launch_split_group<64, 4, 2>(p, a, st);
-    case 64 * 16 + 8: return launch_split_group<64, 8, 2>(p, a, st);
-    case 128 * 16 + 1: return two ? launch_split_group<128, 1, 2>(p, a, st) : launch_split_group<128, 1, 1>(p, a, st);
-    case 128 * 16 + 2: return launch_split_group<128, 2, 2>(p, a, st);
-    case 128 * 16 + 4: return launch_split_group<128, 4, 2>(p, a, st);
-    case 256 * 16 + 1: return launch_split_group<256, 1, 1>(p, a, st);
-    case 256 * 16 + 2: return launch_split_group<256, 2, 2>(p, a, st);
+    case 64 * 16 + 1: return two ? launch_split_group<64, 1, 2, 2>(p, a, st) : launch_split_group<64, 1, 1, 2>(p, a, st);
+    case 64 * 16 + 2: return launch_split_group<64, 2, 2, 1>(p, a, st);
+    case 64 * 16 + 4: return launch_split_group<64, 4, 2, 1>(p, a, st);
+    case 64 * 16 + 8: return launch_split_group<64, 8, 2, 1>(p, a, st);
+    case 128 * 16 + 1: return two ? launch_split_group<128, 1, 2, 1>(p, a, st) : launch_split_group<128, 1, 1, 1>(p, a, st);
+    case 128 * 16 + 2: return launch_split_group<128, 2, 2, 1>(p, a, st);
+    case 128 * 16 + 4: return launch_split_group<128, 4, 2, 1>(p, a, st);
+    case 256 * 16 + 1: return launch_split_group<256, 1, 1, 1>(p, a, st);
+    case 256 * 16 + 2: return launch_split_group<256, 2, 2, 1>(p, a, st);
   }
   return lora_fail(LORA_EINVAL, "lora_attention_split: no kernel for this geometry");
 }
@@ -965,7 +1021,7 @@ int launch_split_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
 template <int D>
 int launch_join(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   const int subs = std::max(1, 8 * device_sm_count() / a.plan.parts);   // about eight blocks per SM
-  const size_t smem = a.weight_out ? (size_t)(a.n_heads + (a.n_req + 31) / 32) * 4 : 0;
+  const size_t smem = a.weight_out ? (size_t)(a.n_heads + (a.n_req + 127) / 128) * 4 : 0;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
   const cudaError_t e = launch_pdl(!p->prof_on, attention_join_kernel<D>, dim3(a.plan.parts * subs), dim3(32 * kJoinWarps),
                                    smem, st, a, subs);
