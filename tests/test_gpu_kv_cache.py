@@ -9,6 +9,7 @@ import pytest
 import oracle as O
 import workloads
 from helpers import bits_to_torch, torch_to_bits
+from kv_bounds import attention_tolerances
 
 pytestmark = pytest.mark.gpu
 
@@ -61,28 +62,8 @@ class Cache:
         self.L.lora_pool_destroy(self.pool)
 
 
-def _tolerances(ref, lengths, D, G):
-    """Error bounds per request from the arithmetic (u = 2^-24, half a step of fp32).
-
-    A score is a sum of D exact products in fp32, scaled once: off by at most
-    delta = (D + 4) u mag + 4 u |s| <= (D + 8) u mag.  exp2 adds 2^-22, sums over n tokens n u, and a
-    weight held in two bf16 terms 2^-16, so p is off by at most p (2 delta + (n + 8) u + 2^-22 + 2^-16).
-    Token weights come out in fp32, which holds nothing between 0 and its smallest numbers: each
-    head's term may be off by the smallest normal number, 2^-126, besides."""
-    u = 2.0 ** -24
-    tol_out, tol_lse, tol_w = [], [], []
-    for i, n in enumerate(lengths):
-        delta = (D + 8) * u * ref["mag"][i]                                     # per query head
-        rel = 2 * delta + (n + 8) * u + 2.0 ** -22 + 2.0 ** -16
-        tol_out.append(2.0 ** -8 * np.abs(ref["out"][i]) + np.repeat(rel, D) * ref["vabs"][i] * 1.01 + 1e-30)
-        lse = np.where(np.isfinite(ref["lse"][i]), ref["lse"][i], 0.0)
-        tol_lse.append(delta + (n + 8) * u + 2.0 ** -22 + 8 * u * np.abs(lse) + 8 * u)
-        tol_w.append((ref["p"][i] * (2 * delta + (n + 8) * u + 2.0 ** -20)[:, None]).sum(0) if n else np.zeros(0))
-    return np.array(tol_out), np.array(tol_lse), tol_w
-
-
 def _check(ref, out, lse, lengths, D, G):
-    tol_out, tol_lse, _ = _tolerances(ref, lengths, D, G)
+    tol_out, tol_lse, _ = attention_tolerances(ref, lengths, D)
     got = O.bf16_to_f64(torch_to_bits(out.contiguous()))
     assert np.isfinite(got).all()
     bad = np.abs(got - ref["out"]) > tol_out
@@ -96,7 +77,7 @@ def _check(ref, out, lse, lengths, D, G):
 
 
 def _check_weights(ref, got, w_in, lengths, D, G, n_heads):
-    _, _, tol_w = _tolerances(ref, lengths, D, G)
+    _, _, tol_w = attention_tolerances(ref, lengths, D)
     for i, n in enumerate(lengths):
         want = ref["weight"][i] + (0 if w_in is None else w_in[i, :n])
         err = np.abs(got[i, :n] - want)
