@@ -194,8 +194,7 @@ __device__ RangeStart find_range(const SplitArgs& a, int p, int parts, int st, i
   // No range between two used ones is empty (the join reads a partial of each): P = min(P, U).
   const int P = max(min(parts, total), 1);
   const int q0 = min(p, P), q1 = min(p + 1, P);
-  const int d = total / P, m = total % P;                  // p U / P without overflow: U = d P + m
-  const int u0 = q0 * d + q0 * m / P, u1 = q1 * d + q1 * m / P;
+  const int u0 = (int)((long long)q0 * total / P), u1 = (int)((long long)q1 * total / P);
   if (u1 == u0) return RangeStart{0, 0, 0, 0};
   int before = 0, t = 0;                                   // units of the requests looked at so far
   if (n_sums > 1) {

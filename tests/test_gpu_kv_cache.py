@@ -102,6 +102,10 @@ SHAPES = [   # n_kv, G, D, layers, lengths
     (3, 7, 128, 1, [0, 0, 0]),
     (8, 1, 128, 1, [3, 0, 1, 40] * 170),
     (1, 2, 128, 1, [1] * 3000),
+    (16, 3, 64, 1, [90, 1, 257]),       # two heads of 64 a warp: 8 of 8, 7 + 6, 8 with 9 query heads each
+    (13, 1, 64, 2, [45, 700]),
+    (8, 9, 64, 1, [33, 64, 0, 400]),
+    (3, 2, 128, 1, [129] * 130),        # more than 128 requests: the range search goes through shared memory
 ]
 
 
@@ -346,6 +350,32 @@ def test_attention_split_same_bits_again_on_a_side_stream_and_in_a_graph(L):
         L.lora_status(c.pool)
     finally:
         c.close()
+
+
+def test_attention_split_of_sixty_thousand_requests(L):
+    """One token each (or none): the output is its V, the weight one per query head; whole requests and
+    split ranges."""
+    import torch
+    n, H = 60_000, 64
+    pool_t = torch.randn((2 * n, H), device="cuda").bfloat16()
+    pool = L.lora_pool_create(pool_t, 2 * n, H, 1, 1)
+    try:
+        for max_len in (1, 200):                                   # up to 128 tokens a request is one CTA's
+            table = torch.full((n, max_len, 1, 2), -1, dtype=torch.int32, device="cuda")
+            pages = torch.randperm(2 * n, device="cuda").to(torch.int32).view(n, 2)
+            table[:, 0, 0] = pages
+            seq = (torch.arange(n, device="cuda") % 7 != 3).to(torch.int32)
+            q = torch.randn((n, 2 * H), device="cuda").bfloat16()
+            out, w = torch.full_like(q, float("nan")), torch.full((n, max_len), -1.0, device="cuda")
+            nb = L.lora_attention_split_size(pool, n, max_len, 2, 1, True)
+            ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+            L.lora_attention_split(pool, n, table, seq, max_len, 1, 0, q, out, 2, 1, ws, nb, weight_out_dev=w)
+            L.lora_status(pool)
+            v = pool_t[pages[:, 1].long()] * seq[:, None].to(torch.bfloat16)
+            assert torch.equal(out, torch.cat([v, v], 1))
+            assert torch.equal(w[:, 0], torch.where(seq > 0, 2.0, -1.0))
+    finally:
+        L.lora_pool_destroy(pool)
 
 
 def test_attention_split_does_not_depend_on_the_other_requests_values(L):
