@@ -79,7 +79,7 @@ struct SplitArgs {
   SplitPlan plan;
   float* ws_lse;                       // [n_req][n_heads], base 2: requests inside one range
   int2* ws_range;                      // [n_req] first and last range of a request
-  int4* ws_start;                      // [parts] first request and token of a range, its units
+  int4* ws_start;                      // [parts] a range's first request, its token there, that request's ranges
   float2* ws_ml;                       // [2 parts][n_heads] m and l of a partial
   float* ws_acc;                       // [2 parts][n_heads][D]
   float* ws_scores;                    // [n_req][n_heads][score_stride], base 2; NULL without weights
@@ -141,9 +141,10 @@ struct StageInfo {
   uint16_t mask[kMaxTiles];      // per tile: bit i = token i has data
 };
 
-// Where a range begins in the sequence of all requests' units, and the length of its first request.
+// Where a range begins in the sequence of all requests' units, and of its first request the length
+// and the first and last range.
 struct RangeStart {
-  int32_t req, tok, units, n;
+  int32_t req, tok, units, n, p0, p1;
 };
 
 // Prefix sum over the warp's lanes.
@@ -195,7 +196,7 @@ __device__ RangeStart find_range(const SplitArgs& a, int p, int parts, int st, i
   const int P = max(min(parts, total), 1);
   const int q0 = min(p, P), q1 = min(p + 1, P);
   const int u0 = (int)((long long)q0 * total / P), u1 = (int)((long long)q1 * total / P);
-  if (u1 == u0) return RangeStart{0, 0, 0, 0};
+  if (u1 == u0) return RangeStart{0, 0, 0, 0, 0, 0};
   int before = 0, t = 0;                                   // units of the requests looked at so far
   if (n_sums > 1) {
     for (int t0 = 0; t0 < n_sums; t0 += 32) {              // the block of 128 requests that holds u0
@@ -215,7 +216,7 @@ __device__ RangeStart find_range(const SplitArgs& a, int p, int parts, int st, i
   const int incl = warp_inclusive(mine, lane);
   const int k = __ffs(__ballot_sync(0xffffffffu, before + incl > u0)) - 1;      // the lane, then its request
   before += __shfl_sync(0xffffffffu, incl - mine, k);
-  RangeStart rs{128 * t + 4 * k, 0, u1 - u0, 0};
+  RangeStart rs{128 * t + 4 * k, 0, u1 - u0, 0, 0, 0};
   bool found = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -224,6 +225,9 @@ __device__ RangeStart find_range(const SplitArgs& a, int p, int parts, int st, i
       rs.req += i;
       rs.tok = (u0 - before) * st;
       rs.n = n;
+      // the range that holds unit x is the largest i with i U / P <= x, i.e. i U < (x + 1) P
+      rs.p0 = (int)((((long long)before + 1) * P - 1) / total);
+      rs.p1 = (int)((((long long)before + u) * P - 1) / total);
       found = true;
     }
     before += u;
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait_then_release();
-  RangeStart rs;
+  RangeStart rs{};
   if (pl.whole) {
     const int n = a.seq_len[p];
     if (threadIdx.x == 0 && (n < 0 || n > a.max_len)) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
     rs = find_range(a, p, pl.parts, st, reinterpret_cast<int32_t*>(merge));
   }
   __syncthreads();                                         // barriers set up; the sums lie where heads merge
-  if (g0 == 0 && threadIdx.x == 0) a.ws_start[p] = make_int4(rs.req, rs.tok, rs.units, 0);
+  if (g0 == 0 && threadIdx.x == 0) a.ws_start[p] = make_int4(rs.req, rs.units > 0 ? rs.tok : 0, rs.p0, rs.p1);
 
   if (warp >= kWarps) {
     // ---- producers: each finds every unit's valid tokens; with two, one copies K and one V ----
@@ -772,9 +776,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
   if (!a.plan.whole) {
     const int p = blockIdx.x / subs, sub = blockIdx.x % subs;
     const int4 w = a.ws_start[p];
-    if (w.z > 0 && w.y > 0) {
+    if (w.y > 0) {
       const int r = w.x;
-      const int2 range = a.ws_range[r];
+      const int2 range = make_int2(w.z, w.w);
       const bool wide = range.y - range.x >= kJoinWarps;
       const int block = (p - range.x - 1) * subs + sub, blocks = (range.y - range.x) * subs;
       uint16_t* row = a.out + r * a.out_stride;
