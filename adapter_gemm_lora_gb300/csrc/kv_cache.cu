@@ -54,10 +54,13 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (uint32_t)(b ^ ((b >> 31) | INT32_MIN));
 }
 
-// Per row (one request at one layer) the keys that stay are found by radix selection, 10 bits at a
-// time from the top: a histogram of the digit over the keys that still match the digits chosen so
-// far, and the bin that holds the need-th largest key.  It ends with the first bin that is wanted
-// whole: for weights that differ, after the second digit or the third.
+// Per row (one request at one layer) the keys that stay are found by radix selection, digit by digit
+// from the top: a histogram of the digit over the keys that still match the digits chosen so far, and
+// the bin that holds the need-th largest key.  It ends with the first bin that is wanted whole: for
+// weights that differ, after the second digit or the third.  Digits of 10 bits: of 12 bits a cluster
+// would need two, but reading the other CTAs' 4,096 bins took 32 layers of 131,071 tokens from 38 to
+// 100 us.
+constexpr int kEvictBits = 10, kEvictBins = 1 << kEvictBits;
 struct EvictArgs {
   int32_t n_req;
   const int2* table;
@@ -101,9 +104,6 @@ __device__ __forceinline__ EvictRow evict_row(const EvictArgs& a, int id, bool r
 }
 constexpr int kEvictWarps = 16;                            // of a CTA
 constexpr int kEvictThreads = 32 * kEvictWarps;
-constexpr int kEvictDigitBits = 10;
-constexpr int kEvictDigits = 4;                            // 10 + 10 + 10 + 2 bits
-constexpr int kEvictBins = 1 << kEvictDigitBits;
 constexpr int kEvictMaxCluster = 8;
 
 __device__ __forceinline__ int warp_scan(int v, int lane) {
@@ -130,13 +130,12 @@ __device__ __forceinline__ int2 cluster_load2(uint32_t addr) {
   asm volatile("ld.relaxed.cluster.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void cluster_store(uint32_t addr, int v) {
-  asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // kRowWarps warps per row: 4, so that a CTA has four rows, or all 16; with kCluster a cluster of
 // `n_cta` CTAs has one row, and every CTA adds up all CTAs' histograms (integer sums: the order does
-// not matter).  Every warp takes a contiguous part of the row, the keys of 32 K weights held in
+// not matter), which also tell it how many keys the CTAs before it keep.  Every warp takes a contiguous part of the row, the keys of 32 K weights held in
 // registers (longer parts are read again in every pass), so the kept tokens are numbered with one
 // exchange of counts.  Their positions go to a list in shared memory first, and the outputs are
 // written from there, 32 neighbours at a time.
@@ -155,18 +154,17 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   constexpr int kRows = kEvictWarps / kRowWarps;           // rows of a CTA
   static_assert(!kCluster || kRows == 1, "a cluster shares one row");
   static_assert(K % kEvictBatch == 0, "whole batches");
-  static_assert(!kCluster || kEvictBins == 2 * kEvictThreads, "the sum over the CTAs takes two bins a thread");
   extern __shared__ __align__(16) int smem_evict[];
   __shared__ int warp_gt[kEvictWarps], warp_eq[kEvictWarps], keep_n[kRows];
-  __shared__ int cta_gt[kEvictMaxCluster], cta_eq[kEvictMaxCluster];
   __shared__ int found_s[kRows][3];                        // the wanted bin, keys above it, keys in it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slot = warp / kRowWarps, part = warp % kRowWarps, rtid = part * 32 + lane;
   constexpr int n_thr = 32 * kRowWarps;                    // threads of a row in this CTA
+  constexpr int kHists = kCluster ? 2 : kRows;
   constexpr int kPer = kEvictBins / n_thr;                 // bins a thread adds up: 8 or 2
-  // Shared memory: a histogram per row, of a cluster one per digit (the other CTAs may still read the
+  static_assert(kPer * n_thr == kEvictBins && (!kCluster || kPer == 2), "the CTAs' histograms are read two bins at a time");
+  // Shared memory: a histogram per row, of a cluster two in turn (the other CTAs may still read the
   // one before); the kept lists, of a row (four rows a CTA, keep_cap each) or of a warp (32 K each).
-  constexpr int kHists = kCluster ? kEvictDigits : kRows;
   int* hist = smem_evict + slot * kEvictBins;
   int* lists = smem_evict + kHists * kEvictBins;
   for (int i = tid; i < kEvictBins * kHists / 4; i += kEvictThreads)
@@ -202,12 +200,15 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   };
   if (held) load(w0);
   __syncthreads();
-  if (kCluster) cluster_sync_all();                        // every CTA of the cluster runs: its shared memory may be used
-  if (live && e.need > 0 && e.need < e.old) {
+  // kept and tied keys of the row before this CTA's slice: all tokens, or the newer ones, or what the
+  // digits say
+  int pos = e.need >= e.old ? c0 : max(0, c0 - e.old), tied = 0;
+  const bool select = live && e.need > 0 && e.need < e.old;
+  if (select) {
     uint32_t prefix = 0, mask = 0;
     int need = e.need;
-    for (int d = 0, bits = 32; d < kEvictDigits; ++d) {
-      const int nb = min(kEvictDigitBits, bits);
+    for (int d = 0, bits = 32; bits > 0; ++d) {
+      const int nb = min(kEvictBits, bits);
       bits -= nb;
       const uint32_t digit = (1u << nb) - 1;
       for (int j0 = w0; j0 < w1; j0 += 32 * K) {
@@ -233,7 +234,6 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
           v[0] += x.x;
           v[1] += x.y;
         }
-        hist += kEvictBins;
       } else {
         row_sync();
 #pragma unroll
@@ -264,17 +264,45 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
         for (int i = 0; i < kPer; ++i) hist[rtid * kPer + i] = 0;
       }
       row_sync();
+      const int bin = found_s[slot][0];
       need -= found_s[slot][1];
-      prefix |= (digit - (uint32_t)found_s[slot][0]) << bits;
+      const bool whole = found_s[slot][2] == need;         // the whole bin stays
+      prefix |= (digit - (uint32_t)bin) << bits;
       mask |= digit << bits;
-      e.cut = prefix;
-      e.ties = need;
-      if (found_s[slot][2] == need) {                      // the whole bin stays
-        e.cut = prefix - 1;
-        e.ties = 0;
-        break;
+      e.cut = whole ? prefix - 1 : prefix;
+      e.ties = whole ? 0 : need;
+      if (kCluster) {
+        // of the CTAs before this one: the keys above the bin, and those in it
+        int gt = 0, in = 0;
+        if (2 * rtid <= bin)
+          for (int c = 0; c < rank; ++c) {
+            const int2 x = cluster_load2(cluster_addr(hist + 2 * rtid, c));
+            gt += (2 * rtid < bin ? x.x : 0) + (2 * rtid + 1 < bin ? x.y : 0);
+            in += 2 * rtid == bin ? x.x : 2 * rtid + 1 == bin ? x.y : 0;
+          }
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        in = __reduce_add_sync(0xffffffffu, in);
+        if (lane == 0) {
+          warp_gt[warp] = gt;
+          warp_eq[warp] = in;
+        }
+        row_sync();
+        tied = 0;
+#pragma unroll
+        for (int i = 0; i < kRowWarps; ++i) {
+          pos += warp_gt[i];
+          tied += warp_eq[i];
+        }
+        if (whole) pos += tied;
+        // the other histogram: every CTA had read it when it came to this digit's barrier
+        hist = smem_evict + ((d & 1) ^ 1) * kEvictBins;
+        if (!whole && bits > 0 && d > 0)
+          for (int i = tid; i < kEvictBins / 4; i += kEvictThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+        row_sync();
       }
+      if (whole) break;
     }
+    if (kCluster) cluster_arrive();                        // this CTA reads no other's shared memory any more
   }
 
   // what each warp keeps: keys above the cut, and keys equal to it
@@ -299,23 +327,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
     warp_eq[warp] = eq;
   }
   row_sync();
-  int pos = 0, tied = 0;                                   // kept and tied of the row before this warp's part
-  if (kCluster) {
-    if (tid < n_cta) {
-      int g = 0, q = 0;
-      for (int i = 0; i < kRowWarps; ++i) {
-        g += warp_gt[i];
-        q += warp_eq[i];
-      }
-      cluster_store(cluster_addr(cta_gt + rank, tid), g);
-      cluster_store(cluster_addr(cta_eq + rank, tid), q);
-    }
-    cluster_sync_all();
-    for (int i = 0; i < rank; ++i) {
-      pos += cta_gt[i];
-      tied += cta_eq[i];
-    }
-  }
+  // kept and tied of the row before this warp's part
 #pragma unroll
   for (int i = 0; i < kRowWarps; ++i) {
     pos += i < part ? warp_gt[slot * kRowWarps + i] : 0;
@@ -357,12 +369,13 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
       float* w_out = a.weight_out + e.row * a.max_len_out + pos;
       int2* t_out = a.table_out + ((int64_t)e.r * a.max_len_out + pos) * a.layers + e.layer;
       constexpr int kBatch = 4;                            // reads a thread has in flight
-      for (int i0 = lane; i0 < n_kept; i0 += 32 * kBatch) {
+      const int n_out = min(n_kept, e.n_keep - pos);       // equal; no write passes the row whatever the counts say
+      for (int i0 = lane; i0 < n_out; i0 += 32 * kBatch) {
         int j[kBatch];
         float x[kBatch];
         int2 pages[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) j[b] = list[min(i0 + 32 * b, n_kept - 1)];
+        for (int b = 0; b < kBatch; ++b) j[b] = list[min(i0 + 32 * b, n_out - 1)];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           x[b] = __ldg(w + j[b]);
@@ -371,7 +384,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           const int i = i0 + 32 * b;
-          if (i >= n_kept) break;
+          if (i >= n_out) break;
           keep[i] = j[b];
           w_out[i] = x[b];
           if (kRows == 1) t_out[(int64_t)i * a.layers] = pages[b];
@@ -393,6 +406,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
     }
     if (e.layer == 0 && rank == 0 && rtid == 0) a.new_len[e.r] = e.n_keep;
   }
+  if (kCluster && select) cluster_wait();                  // and no other reads this one's
   if (kRows == 1) return;
 
   // the page table of the CTA's rows: thread = (position, row), rows fastest
@@ -426,10 +440,10 @@ constexpr int kShortRow = 4096;                            // four rows a CTA up
 template <int K, int kRowWarps, bool kCluster>
 int launch_evict(const lora_pool* p, const EvictArgs& a, int n_cta, cudaStream_t st) {
   const int64_t rows = (int64_t)a.n_req * a.layers;
-  constexpr int kRows = kEvictWarps / kRowWarps, kHists = kCluster ? kEvictDigits : kRows;
+  constexpr int kRows = kEvictWarps / kRowWarps, kHistWords = (kCluster ? 2 : kRows) * kEvictBins;
   const int keep_cap = kRows > 1 ? std::min(a.budget, a.max_len) : 0;
-  const int smem = (kHists * kEvictBins + (kRows > 1 ? kRows * keep_cap : kEvictWarps * 32 * K)) * (int)sizeof(int);
-  constexpr int kMost = (kHists * kEvictBins + (kRows > 1 ? kRows * kShortRow : kEvictWarps * 32 * K)) * (int)sizeof(int);
+  const int smem = (kHistWords + (kRows > 1 ? kRows * keep_cap : kEvictWarps * 32 * K)) * (int)sizeof(int);
+  constexpr int kMost = (kHistWords + (kRows > 1 ? kRows * kShortRow : kEvictWarps * 32 * K)) * (int)sizeof(int);
   static DeviceFlags flags;
   const int rc = ensure_smem_attr(flags, &kv_evict_kernel<K, kRowWarps, kCluster>, kMost, "lora_kv_evict");
   if (rc != LORA_OK) return rc;
