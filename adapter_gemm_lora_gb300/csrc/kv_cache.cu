@@ -12,8 +12,10 @@
 namespace {
 
 // ---- page writes -------------------------------------------------------------------------------
-// One warp per (row, K or V): the page id is read through the table and checked, then the row's
-// 2 H bytes are copied 16 bytes a lane.  HBM-bound: every row is read once and written once.
+// One warp per (row, K or V): the page ids are read through the table and checked, then the row's
+// 2 H bytes are copied 16 bytes a lane.  HBM-bound: every row is read once and written once; 11,300
+// prompt rows at H = 4096 take 57.2 us, 6.5 TB/s (0.97 of the copy rate).  One row per request of a
+// decode step is a launch: 256 rows at H = 5120 take 5 us a call, most of it on the host.
 constexpr int kWriteThreads = 256;
 
 __global__ void __launch_bounds__(kWriteThreads)
