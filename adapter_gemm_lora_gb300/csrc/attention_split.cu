@@ -53,8 +53,9 @@ constexpr int kJoinUnit = 64;                       // tokens whose weights a bl
 struct SplitPlan {
   int32_t D, group, n_kv;
   int32_t n_groups, heads;       // groups of KV heads, KV heads per group
-  int32_t head_warps;            // warps that take the group's heads: one head each, or two (D = 64)
-  int32_t sharers;               // warps that share a head
+  int32_t octets;                // warps per head by its query heads, 8 each
+  int32_t head_slots;            // heads taken side by side: one a slot, or two (D = 64)
+  int32_t sharers;               // warps that share a head's tokens
   int32_t tile_sharers;          // of them, those that take a stage's tiles in turn; the rest take turns at stages
   int32_t tiles;                 // 16-token tiles per stage
   int32_t stages;
@@ -255,11 +256,11 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
 // One CTA per (group of KV heads, range).  The last warp fills a ring of stages: per stage and
 // token the group's slice of the K row and of the V row (heads x D contiguous bf16) by
 // cp.async.bulk, all against the stage's one mbarrier; page ids are read one stage ahead.  A
-// consumer warp owns one KV head and the stages' 16-token tiles, shared out between the warps of the
-// head where there are several.
+// consumer warp owns up to 8 query heads of one KV head, or of two of 64, and the stages' 16-token
+// tiles, shared out between the warps of the head where there are several.
 //
 // Per tile the products run on m16n8k16 MMAs with the tokens (or the features) as the 16 rows and
-// the query heads of the KV head as the 8 columns: S^T = K q^T, then acc^T += V^T P^T.  A decode
+// the warp's query heads as the 8 columns: S^T = K q^T, then acc^T += V^T P^T.  A decode
 // step has at most 16 query rows per KV head, far below the 64 or 128 rows of a tcgen05 tile, and
 // every K and V byte is used once, so the tensor work is small; this layout leaves 1/8 instead of
 // 1/16 of the MMA in use at one query head, and the running maximum, sum and rescaling of a column
@@ -272,13 +273,14 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
 // 64 KB stages measured the same.  The producer is what has to be lean, since one warp prepares every
 // copy: with a loop over up to eight tiles, seven of them unused, the batch above took 1,203 us, with
 // the tile count fixed at compile time 840 us; without the consumers' arithmetic 826 us.
-// More than 8 query heads per KV head take two column tiles, whose accumulators spill at D = 256
-// (4 x 40,000 tokens, 16 query heads per KV head: 0.76 of the copy rate at D = 128, 0.45 at 256;
-// 8 or fewer: 0.98 and 0.95).
-template <int D, int NT, int TILES, int NP, int HW>
+// More than 8 query heads per KV head take two warps a head, each with 8 of them and its own read of
+// the head's K and V from shared memory (4 x 40,000 tokens with 16 query heads per KV head: 0.89 of
+// the copy rate at D = 128, 0.94 at 256; one warp with two column tiles, whose accumulators spilled:
+// 0.76 and 0.45).
+template <int D, int TILES, int NP, int HW>
 __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_kernel(const __grid_constant__ SplitArgs a) {
   constexpr int KS = D / 16;
-  constexpr int VR = NT == 1 || D < 256 ? (KS < 8 ? KS : 8) : 4;   // V fragments held over the softmax
+  constexpr int VR = KS < 8 ? KS : 8;                      // V fragments held over the softmax
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kWarps];
   __shared__ StageInfo info[kMaxStages];
@@ -292,11 +294,11 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   const uint32_t ring = smem_u32(smem), RB = pl.row_bytes;
   const uint32_t bar_full = smem_u32(bars), bar_empty = bar_full + 8 * kMaxStages;
   const uint32_t bar_ready = bar_empty + 8 * kMaxStages, bar_done = bar_ready + 8 * kWarps;
-  float* merge = reinterpret_cast<float*>(smem + (size_t)S * pl.stage_bytes);   // [heads][group][D + 2]
+  float* merge = reinterpret_cast<float*>(smem + (size_t)S * pl.stage_bytes);   // [head warps][8][D + 2]
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(bar_full + 8 * s, NP);
-      mbar_init(bar_empty + 8 * s, min(pl.head_warps, n_act) * pl.sharers);
+      mbar_init(bar_empty + 8 * s, min(pl.head_slots, n_act) * pl.octets * pl.sharers);
     }
     for (int h = 0; h < kWarps; ++h) {
       mbar_init(bar_ready + 8 * h, 1);
@@ -416,33 +418,32 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   }
 
   // ---- consumers ----
-  const int hh = warp % pl.head_warps, share = warp / pl.head_warps;
+  const int head_warps = pl.head_slots * pl.octets, hw = warp % head_warps, share = warp / head_warps;
+  const int hh = hw / pl.octets, octet = hw % pl.octets;
   if (share >= pl.sharers || hh >= n_act || rs.units == 0) return;
-  const int n_mine = HW == 1 || hh + pl.head_warps >= n_act ? 1 : 2;           // this warp's heads: hh, hh + head_warps
+  const int n_mine = HW == 1 || hh + pl.head_slots >= n_act ? 1 : 2;           // this warp's heads: hh, hh + head_slots
   const int g = lane >> 2, t = lane & 3;
-  const int G = pl.group;
-  const auto head_of = [&](int u) { return (h0 + hh + u * pl.head_warps) * G; };   // the KV head's first query head
-  uint32_t qf[HW][NT][KS][2];
-  float acc[HW][NT][KS][4], m[HW][NT][2], l[HW][NT][2];
+  const int G = min(8, pl.group - 8 * octet);              // its query heads of each
+  const auto head_of = [&](int u) { return (h0 + hh + u * pl.head_slots) * pl.group + 8 * octet; };
+  uint32_t qf[HW][KS][2];
+  float acc[HW][KS][4], m[HW][2], l[HW][2];
   const auto load_q = [&](int req) {
 #pragma unroll
-    for (int u = 0; u < HW; ++u)
+    for (int u = 0; u < HW; ++u) {
+      const bool has = g < G && u < n_mine;
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + req * a.q_stride + (int64_t)(head_of(u) + g) * D) + t;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const bool has = nt * 8 + g < G && u < n_mine;
-        const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + req * a.q_stride + (int64_t)(head_of(u) + nt * 8 + g) * D) + t;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          qf[u][nt][ks][0] = has ? qp[ks * 8] : 0u;
-          qf[u][nt][ks][1] = has ? qp[ks * 8 + 4] : 0u;
-        }
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[u][ks][0] = has ? qp[ks * 8] : 0u;
+        qf[u][ks][1] = has ? qp[ks * 8 + 4] : 0u;
       }
+    }
   };
   // lane addresses of the fragments within a tile
   const uint32_t k_lane = (uint32_t)(lane & 15) * RB + (uint32_t)(hh * D + (lane >> 4) * 8) * 2;
   const uint32_t v_lane = (uint32_t)(TILES * kTile + (lane & 7) + (lane >> 4) * 8) * RB +
                           (uint32_t)(hh * D + ((lane >> 3) & 1) * 8) * 2;
-  const uint32_t head_step = (uint32_t)(pl.head_warps * D * 2);
+  const uint32_t head_step = (uint32_t)(pl.head_slots * D * 2);
   const int turns = pl.sharers / tile_sharers, turn = share / tile_sharers;
   int seg = 0;                                             // segments finished: the phase of the merge barriers
   load_q(rs.req);                                          // on its way beside the first stages
@@ -464,14 +465,12 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
     __syncwarp();
     if (flags & kFirst) {
 #pragma unroll
-      for (int u = 0; u < HW; ++u)
+      for (int u = 0; u < HW; ++u) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) acc[u][nt][ks][0] = acc[u][nt][ks][1] = acc[u][nt][ks][2] = acc[u][nt][ks][3] = 0.f;
-          m[u][nt][0] = m[u][nt][1] = -INFINITY;
-          l[u][nt][0] = l[u][nt][1] = 0.f;
-        }
+        for (int ks = 0; ks < KS; ++ks) acc[u][ks][0] = acc[u][ks][1] = acc[u][ks][2] = acc[u][ks][3] = 0.f;
+        m[u][0] = m[u][1] = -INFINITY;
+        l[u][0] = l[u][1] = 0.f;
+      }
     }
     if (!mine && lane == 0) mbar_arrive(bar_empty + 8 * s);
     for (int tile = mine ? share % tile_sharers : TILES; tile < TILES; tile += tile_sharers) {
@@ -490,21 +489,16 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
         if (u >= n_mine) break;
         const bool release = final_tile && u + 1 == n_mine;
         const uint32_t base = ring + (uint32_t)s * pl.stage_bytes + (uint32_t)(tile * kTile) * RB + u * head_step;
-        float sc[NT][4], odd[NT][4];
+        float sc[4], odd[4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[nt][i] = odd[nt][i] = 0.f;
+        for (int i = 0; i < 4; ++i) sc[i] = odd[i] = 0.f;
 #pragma unroll
         for (int k0 = 0; k0 < KS; k0 += 4) {
           uint32_t kf[4][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) ldmatrix_x4(kf[k], base + k_lane + (k0 + k) * 32);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_16x8x16(k & 1 ? odd[nt] : sc[nt], kf[k], qf[u][nt][k0 + k][0], qf[u][nt][k0 + k][1]);
+          for (int k = 0; k < 4; ++k) mma_16x8x16(k & 1 ? odd : sc, kf[k], qf[u][k0 + k][0], qf[u][k0 + k][1]);
         }
         uint32_t vf[VR][4];
 #pragma unroll
@@ -514,54 +508,51 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
           if (lane == 0) mbar_arrive(bar_empty + 8 * s);
         }
         const bool v0 = (mask >> g) & 1u, v1 = (mask >> (g + 8)) & 1u;
-        uint32_t ph[NT][2], plo[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          sc[nt][0] = v0 ? (sc[nt][0] + odd[nt][0]) * a.scale_log2 : -INFINITY;
-          sc[nt][1] = v0 ? (sc[nt][1] + odd[nt][1]) * a.scale_log2 : -INFINITY;
-          sc[nt][2] = v1 ? (sc[nt][2] + odd[nt][2]) * a.scale_log2 : -INFINITY;
-          sc[nt][3] = v1 ? (sc[nt][3] + odd[nt][3]) * a.scale_log2 : -INFINITY;
-          if (a.ws_scores) {
-            float* dst = a.ws_scores + ((int64_t)req * a.n_heads + head_of(u) + nt * 8 + 2 * t) * a.score_stride + j0 + g;
-            if (nt * 8 + 2 * t < G) {
-              dst[0] = sc[nt][0];
-              dst[8] = sc[nt][2];
-            }
-            if (nt * 8 + 2 * t + 1 < G) {
-              dst[a.score_stride] = sc[nt][1];
-              dst[a.score_stride + 8] = sc[nt][3];
-            }
+        uint32_t ph[2], plo[2];
+        sc[0] = v0 ? (sc[0] + odd[0]) * a.scale_log2 : -INFINITY;
+        sc[1] = v0 ? (sc[1] + odd[1]) * a.scale_log2 : -INFINITY;
+        sc[2] = v1 ? (sc[2] + odd[2]) * a.scale_log2 : -INFINITY;
+        sc[3] = v1 ? (sc[3] + odd[3]) * a.scale_log2 : -INFINITY;
+        if (a.ws_scores) {
+          float* dst = a.ws_scores + ((int64_t)req * a.n_heads + head_of(u) + 2 * t) * a.score_stride + j0 + g;
+          if (2 * t < G) {
+            dst[0] = sc[0];
+            dst[8] = sc[2];
           }
-          float c[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float x = fmaxf(sc[nt][k], sc[nt][2 + k]);
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float mn = fmaxf(m[u][nt][k], x);
-            const float ms = mn == -INFINITY ? 0.f : mn;   // no score above -infinity yet: every weight 0
-            c[k] = exp2f(m[u][nt][k] - ms);
-            sc[nt][k] = exp2f(sc[nt][k] - ms);
-            sc[nt][2 + k] = exp2f(sc[nt][2 + k] - ms);
-            l[u][nt][k] = fmaf(l[u][nt][k], c[k], sc[nt][k] + sc[nt][2 + k]);
-            m[u][nt][k] = mn;
+          if (2 * t + 1 < G) {
+            dst[a.score_stride] = sc[1];
+            dst[a.score_stride + 8] = sc[3];
           }
-          if (__any_sync(0xffffffffu, c[0] != 1.f || c[1] != 1.f)) {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              acc[u][nt][ks][0] *= c[0];
-              acc[u][nt][ks][1] *= c[1];
-              acc[u][nt][ks][2] *= c[0];
-              acc[u][nt][ks][3] *= c[1];
-            }
-          }
-          const uint32_t h_lo = pack_bf16(sc[nt][0], sc[nt][1]), h_hi = pack_bf16(sc[nt][2], sc[nt][3]);
-          ph[nt][0] = transpose_8x8(h_lo);
-          ph[nt][1] = transpose_8x8(h_hi);
-          plo[nt][0] = transpose_8x8(pack_bf16(sc[nt][0] - bf16_lo(h_lo), sc[nt][1] - bf16_hi(h_lo)));
-          plo[nt][1] = transpose_8x8(pack_bf16(sc[nt][2] - bf16_lo(h_hi), sc[nt][3] - bf16_hi(h_hi)));
         }
+        float c[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float x = fmaxf(sc[k], sc[2 + k]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float mn = fmaxf(m[u][k], x);
+          const float ms = mn == -INFINITY ? 0.f : mn;   // no score above -infinity yet: every weight 0
+          c[k] = exp2f(m[u][k] - ms);
+          sc[k] = exp2f(sc[k] - ms);
+          sc[2 + k] = exp2f(sc[2 + k] - ms);
+          l[u][k] = fmaf(l[u][k], c[k], sc[k] + sc[2 + k]);
+          m[u][k] = mn;
+        }
+        if (__any_sync(0xffffffffu, c[0] != 1.f || c[1] != 1.f)) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            acc[u][ks][0] *= c[0];
+            acc[u][ks][1] *= c[1];
+            acc[u][ks][2] *= c[0];
+            acc[u][ks][3] *= c[1];
+          }
+        }
+        const uint32_t h_lo = pack_bf16(sc[0], sc[1]), h_hi = pack_bf16(sc[2], sc[3]);
+        ph[0] = transpose_8x8(h_lo);
+        ph[1] = transpose_8x8(h_hi);
+        plo[0] = transpose_8x8(pack_bf16(sc[0] - bf16_lo(h_lo), sc[1] - bf16_hi(h_lo)));
+        plo[1] = transpose_8x8(pack_bf16(sc[2] - bf16_lo(h_hi), sc[3] - bf16_hi(h_hi)));
         // V of a token without data is whatever the stage held before: its bits are cleared.
         const bool partial = mask != 0xFFFFu;
         const uint32_t b0 = mask >> (2 * t), b1 = mask >> (2 * t + 8);
@@ -583,12 +574,9 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
             }
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], ph[0], ph[1]);
 #pragma unroll
-            for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][nt][k0 + k], vf[k], ph[nt][0], ph[nt][1]);
-#pragma unroll
-            for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][nt][k0 + k], vf[k], plo[nt][0], plo[nt][1]);
-          }
+          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], plo[0], plo[1]);
         }
         if (VR < KS && release) {
           __syncwarp();
@@ -603,42 +591,38 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
 #pragma unroll
     for (int u = 0; u < HW; ++u)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          l[u][nt][k] += __shfl_xor_sync(0xffffffffu, l[u][nt][k], 4);
-          l[u][nt][k] += __shfl_xor_sync(0xffffffffu, l[u][nt][k], 8);
-          l[u][nt][k] += __shfl_xor_sync(0xffffffffu, l[u][nt][k], 16);
-        }
+      for (int k = 0; k < 2; ++k) {
+        l[u][k] += __shfl_xor_sync(0xffffffffu, l[u][k], 4);
+        l[u][k] += __shfl_xor_sync(0xffffffffu, l[u][k], 8);
+        l[u][k] += __shfl_xor_sync(0xffffffffu, l[u][k], 16);
+      }
     if (HW == 1 && pl.sharers > 1) {
-      float* mb = merge + (size_t)hh * G * (D + 2);        // [group][D + 2]: acc, m, l
+      float* mb = merge + (size_t)hw * 8 * (D + 2);        // [8][D + 2]: acc, m, l
       // One buffer per head, used by its warps in turn: warp `share` writes it once the warp before
       // (or, for the first, the last of the previous segment) has been added, and share 0 adds it.
       for (int o = 1; o < pl.sharers; ++o) {
-        const uint32_t ready = bar_ready + 8 * (o * pl.head_warps + hh);
+        const uint32_t ready = bar_ready + 8 * (o * head_warps + hw);
         if (share == o) {
           const int before = o > 1 ? o - 1 : pl.sharers - 1;
           const uint32_t parity = o > 1 ? seg & 1 : (seg & 1) ^ 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(bar_done + 8 * (before * pl.head_warps + hh), parity))) {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_done + 8 * (before * head_warps + hw), parity))) {
             if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
             return;
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int k = 0; k < 2; ++k) {
+            const int qi = 2 * t + k;
+            if (qi >= G) continue;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int qi = nt * 8 + 2 * t + k;
-              if (qi >= G) continue;
-#pragma unroll
-              for (int ks = 0; ks < KS; ++ks) {
-                mb[qi * (D + 2) + ks * 16 + g] = acc[0][nt][ks][k];
-                mb[qi * (D + 2) + ks * 16 + g + 8] = acc[0][nt][ks][2 + k];
-              }
-              if (g == 0) {
-                mb[qi * (D + 2) + D] = m[0][nt][k];
-                mb[qi * (D + 2) + D + 1] = l[0][nt][k];
-              }
+            for (int ks = 0; ks < KS; ++ks) {
+              mb[qi * (D + 2) + ks * 16 + g] = acc[0][ks][k];
+              mb[qi * (D + 2) + ks * 16 + g + 8] = acc[0][ks][2 + k];
             }
+            if (g == 0) {
+              mb[qi * (D + 2) + D] = m[0][k];
+              mb[qi * (D + 2) + D + 1] = l[0][k];
+            }
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(ready);
         } else if (share == 0) {
@@ -647,31 +631,29 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
             return;
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int k = 0; k < 2; ++k) {
+            const int qi = 2 * t + k;
+            if (qi >= G) continue;
+            const float om = mb[qi * (D + 2) + D], ol = mb[qi * (D + 2) + D + 1];
+            const float mn = fmaxf(m[0][k], om), ms = mn == -INFINITY ? 0.f : mn;
+            const float c0 = exp2f(m[0][k] - ms), c1 = exp2f(om - ms);
+            m[0][k] = mn;
+            l[0][k] = l[0][k] * c0 + ol * c1;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int qi = nt * 8 + 2 * t + k;
-              if (qi >= G) continue;
-              const float om = mb[qi * (D + 2) + D], ol = mb[qi * (D + 2) + D + 1];
-              const float mn = fmaxf(m[0][nt][k], om), ms = mn == -INFINITY ? 0.f : mn;
-              const float c0 = exp2f(m[0][nt][k] - ms), c1 = exp2f(om - ms);
-              m[0][nt][k] = mn;
-              l[0][nt][k] = l[0][nt][k] * c0 + ol * c1;
-#pragma unroll
-              for (int ks = 0; ks < KS; ++ks) {
-                acc[0][nt][ks][k] = acc[0][nt][ks][k] * c0 + mb[qi * (D + 2) + ks * 16 + g] * c1;
-                acc[0][nt][ks][2 + k] = acc[0][nt][ks][2 + k] * c0 + mb[qi * (D + 2) + ks * 16 + g + 8] * c1;
-              }
+            for (int ks = 0; ks < KS; ++ks) {
+              acc[0][ks][k] = acc[0][ks][k] * c0 + mb[qi * (D + 2) + ks * 16 + g] * c1;
+              acc[0][ks][2 + k] = acc[0][ks][2 + k] * c0 + mb[qi * (D + 2) + ks * 16 + g + 8] * c1;
             }
+          }
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_done + 8 * (o * pl.head_warps + hh));
+          if (lane == 0) mbar_arrive(bar_done + 8 * (o * head_warps + hw));
         }
       }
       ++seg;
       if (share != 0) continue;
     }
     const bool starts = flags & kStarts, ends = flags & kEnds;
-    if (g0 == 0 && hh == 0 && lane == 0) {
+    if (g0 == 0 && hw == 0 && lane == 0) {
       if (starts) a.ws_range[req].x = p;
       if (ends) a.ws_range[req].y = p;
     }
@@ -680,45 +662,40 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
       if (u >= n_mine) break;
       const int head0 = head_of(u);
       if (starts && ends) {
+        const float i0 = l[u][0] == 0.f ? 0.f : 1.f / l[u][0], i1 = l[u][1] == 0.f ? 0.f : 1.f / l[u][1];
+        uint16_t* row = a.out + req * a.out_stride + (int64_t)(head0 + g) * D + 2 * t;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float i0 = l[u][nt][0] == 0.f ? 0.f : 1.f / l[u][nt][0], i1 = l[u][nt][1] == 0.f ? 0.f : 1.f / l[u][nt][1];
-          uint16_t* row = a.out + req * a.out_stride + (int64_t)(head0 + nt * 8 + g) * D + 2 * t;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const uint32_t lo = transpose_8x8(pack_bf16(acc[u][nt][ks][0] * i0, acc[u][nt][ks][1] * i1));
-            const uint32_t hi = transpose_8x8(pack_bf16(acc[u][nt][ks][2] * i0, acc[u][nt][ks][3] * i1));
-            if (nt * 8 + g < G) {
-              *reinterpret_cast<uint32_t*>(row + ks * 16) = lo;
-              *reinterpret_cast<uint32_t*>(row + ks * 16 + 8) = hi;
-            }
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t lo = transpose_8x8(pack_bf16(acc[u][ks][0] * i0, acc[u][ks][1] * i1));
+          const uint32_t hi = transpose_8x8(pack_bf16(acc[u][ks][2] * i0, acc[u][ks][3] * i1));
+          if (g < G) {
+            *reinterpret_cast<uint32_t*>(row + ks * 16) = lo;
+            *reinterpret_cast<uint32_t*>(row + ks * 16 + 8) = hi;
           }
+        }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int qi = nt * 8 + 2 * t + k;
-            if (g == 0 && qi < G) {
-              const float z = l[u][nt][k] == 0.f ? -INFINITY : m[u][nt][k] + log2f(l[u][nt][k]);
-              a.ws_lse[(int64_t)req * a.n_heads + head0 + qi] = z;
-              if (a.lse) a.lse[(int64_t)req * a.n_heads + head0 + qi] = z * 0.6931471805599453f;
-            }
+        for (int k = 0; k < 2; ++k) {
+          const int qi = 2 * t + k;
+          if (g == 0 && qi < G) {
+            const float z = l[u][k] == 0.f ? -INFINITY : m[u][k] + log2f(l[u][k]);
+            a.ws_lse[(int64_t)req * a.n_heads + head0 + qi] = z;
+            if (a.lse) a.lse[(int64_t)req * a.n_heads + head0 + qi] = z * 0.6931471805599453f;
           }
         }
       } else {
         const int64_t slot = partial_slot(p, starts) * a.n_heads + head0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int k = 0; k < 2; ++k) {
+          const int qi = 2 * t + k;
+          if (qi >= G) continue;
+          float* dst = a.ws_acc + (slot + qi) * D;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int qi = nt * 8 + 2 * t + k;
-            if (qi >= G) continue;
-            float* dst = a.ws_acc + (slot + qi) * D;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              dst[ks * 16 + g] = acc[u][nt][ks][k];
-              dst[ks * 16 + g + 8] = acc[u][nt][ks][2 + k];
-            }
-            if (g == 0) a.ws_ml[slot + qi] = make_float2(m[u][nt][k], l[u][nt][k]);
+          for (int ks = 0; ks < KS; ++ks) {
+            dst[ks * 16 + g] = acc[u][ks][k];
+            dst[ks * 16 + g + 8] = acc[u][ks][2 + k];
           }
+          if (g == 0) a.ws_ml[slot + qi] = make_float2(m[u][k], l[u][k]);
+        }
       }
     }
   }
@@ -950,22 +927,23 @@ SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads,
   pl.n_kv = n_kv;
   pl.D = H / n_kv;
   pl.group = n_heads / n_kv;
-  // Head groups as even as they can be: a stage's K and V fit kStageBytes with 16 tokens, a warp has
-  // one head, or two of 64 (so that a slice stays 1 KB), and with fewer heads than warps some warps
-  // share a head and the stage has more tokens.
-  const int room_heads = std::max(1, kStageBytes / (4 * kTile * pl.D));
-  const int most = std::min(pl.D == 64 ? 2 * kWarps : kWarps, room_heads);
+  // A warp has 8 query heads of one KV head, or of two of 64 (so that a slice stays 1 KB); head groups
+  // as even as they can be, a stage's K and V within kStageBytes at 16 tokens; with fewer heads than
+  // warps some warps share a head's tokens and the stage has more of them.
+  pl.octets = (pl.group + 7) / 8;
+  const int slots = kWarps / pl.octets, room_heads = std::max(1, kStageBytes / (4 * kTile * pl.D));
+  const int most = std::min(pl.D == 64 ? 2 * slots : slots, room_heads);
   pl.n_groups = (n_kv + most - 1) / most;
   pl.heads = (n_kv + pl.n_groups - 1) / pl.n_groups;
-  pl.head_warps = pl.heads > kWarps ? kWarps : pl.heads;   // two heads a warp: hh and hh + kWarps
+  pl.head_slots = std::min(pl.heads, slots);
   const int room = kStageBytes / (4 * kTile * pl.heads * pl.D);
-  pl.sharers = kWarps / pl.head_warps;                     // a power of two where it is not 1, as is room then
+  pl.sharers = slots / pl.head_slots;                      // a power of two where it is not 1, as is room then
   pl.tile_sharers = std::min(pl.sharers, room);
   pl.tiles = std::min(room / pl.tile_sharers, kMaxTiles / pl.tile_sharers) * pl.tile_sharers;
   pl.row_bytes = pl.heads * pl.D * 2 + 16;                 // + 16: ldmatrix's 8 rows on 8 bank groups
   pl.stage_bytes = 2 * kTile * pl.tiles * pl.row_bytes;
   // behind the ring: the sums of find_range (4 bytes per 128 requests), later the merged heads
-  const int merge = pl.sharers > 1 ? pl.heads * pl.group * (pl.D + 2) * 4 : 0;
+  const int merge = pl.sharers > 1 ? pl.head_slots * pl.octets * 8 * (pl.D + 2) * 4 : 0;
   const int tail = std::max(merge, (n_req + 127) / 128 * 4);
   pl.stages = std::min(kMaxStages, (kMaxSmem - kStaticSmem - tail) / pl.stage_bytes);
   pl.smem = pl.stages * pl.stage_bytes + tail;
@@ -1002,34 +980,31 @@ int check_shape(const char* fn, const lora_pool* p, int32_t n_req, int32_t max_l
   return LORA_OK;
 }
 
-template <int D, int NT, int TILES, int NP, int HW>
+template <int D, int TILES, int NP, int HW>
 int launch_split(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   static DeviceFlags flags;
-  const int rc = ensure_smem_attr(flags, &attention_split_kernel<D, NT, TILES, NP, HW>, kMaxSmem - kStaticSmem, "lora_attention_split");
+  const int rc = ensure_smem_attr(flags, &attention_split_kernel<D, TILES, NP, HW>, kMaxSmem - kStaticSmem, "lora_attention_split");
   if (rc != LORA_OK) return rc;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
-  const cudaError_t e = launch_pdl(!p->prof_on, attention_split_kernel<D, NT, TILES, NP, HW>, dim3(a.plan.parts * a.plan.n_groups),
+  const cudaError_t e = launch_pdl(!p->prof_on, attention_split_kernel<D, TILES, NP, HW>, dim3(a.plan.parts * a.plan.n_groups),
                                    dim3(threads_of(NP)), a.plan.smem, st, a);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_attention_split launch");
 }
 
 // The kernel of a shape: split_plan gives these tile counts, and the slices that take two producers.
-template <int D, int TILES, int NP, int HW>
-int launch_split_group(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
-  return a.plan.group <= 8 ? launch_split<D, 1, TILES, NP, HW>(p, a, st) : launch_split<D, 2, TILES, NP, HW>(p, a, st);
-}
 int launch_split_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
-  const bool two = a.plan.heads * a.plan.D * 2 < kSmallSlice;
-  switch (a.plan.D * 16 + a.plan.tiles) {
-    case 64 * 16 + 1: return two ? launch_split_group<64, 1, 2, 2>(p, a, st) : launch_split_group<64, 1, 1, 2>(p, a, st);
-    case 64 * 16 + 2: return launch_split_group<64, 2, 2, 1>(p, a, st);
-    case 64 * 16 + 4: return launch_split_group<64, 4, 2, 1>(p, a, st);
-    case 64 * 16 + 8: return launch_split_group<64, 8, 2, 1>(p, a, st);
-    case 128 * 16 + 1: return two ? launch_split_group<128, 1, 2, 1>(p, a, st) : launch_split_group<128, 1, 1, 1>(p, a, st);
-    case 128 * 16 + 2: return launch_split_group<128, 2, 2, 1>(p, a, st);
-    case 128 * 16 + 4: return launch_split_group<128, 4, 2, 1>(p, a, st);
-    case 256 * 16 + 1: return launch_split_group<256, 1, 1, 1>(p, a, st);
-    case 256 * 16 + 2: return launch_split_group<256, 2, 2, 1>(p, a, st);
+  const SplitPlan& pl = a.plan;
+  const bool two = pl.heads * pl.D * 2 < kSmallSlice, pairs = pl.heads > pl.head_slots;
+  switch (pl.D * 16 + pl.tiles) {
+    case 64 * 16 + 1: return two ? launch_split<64, 1, 2, 2>(p, a, st) : launch_split<64, 1, 1, 2>(p, a, st);
+    case 64 * 16 + 2: return pairs ? launch_split<64, 2, 2, 2>(p, a, st) : launch_split<64, 2, 2, 1>(p, a, st);
+    case 64 * 16 + 4: return launch_split<64, 4, 2, 1>(p, a, st);
+    case 64 * 16 + 8: return launch_split<64, 8, 2, 1>(p, a, st);
+    case 128 * 16 + 1: return two ? launch_split<128, 1, 2, 1>(p, a, st) : launch_split<128, 1, 1, 1>(p, a, st);
+    case 128 * 16 + 2: return launch_split<128, 2, 2, 1>(p, a, st);
+    case 128 * 16 + 4: return launch_split<128, 4, 2, 1>(p, a, st);
+    case 256 * 16 + 1: return launch_split<256, 1, 1, 1>(p, a, st);
+    case 256 * 16 + 2: return launch_split<256, 2, 2, 1>(p, a, st);
   }
   return lora_fail(LORA_EINVAL, "lora_attention_split: no kernel for this geometry");
 }

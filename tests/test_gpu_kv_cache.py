@@ -105,6 +105,9 @@ SHAPES = [   # n_kv, G, D, layers, lengths
     (16, 3, 64, 1, [90, 1, 257]),       # two heads of 64 a warp: 8 of 8, 7 + 6, 8 with 9 query heads each
     (13, 1, 64, 2, [45, 700]),
     (8, 9, 64, 1, [33, 64, 0, 400]),
+    (4, 12, 64, 1, [50, 333]),          # 8 + 4 query heads on two warps, each with two heads of 64
+    (3, 11, 256, 1, [40, 1, 100]),
+    (2, 16, 128, 1, [1000, 17]),
     (3, 2, 128, 1, [129] * 130),        # more than 128 requests: the range search goes through shared memory
 ]
 
