@@ -969,14 +969,15 @@ SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads,
 
 // Shape checks shared by the size query and the call; 0 or an error code.
 int check_shape(const char* fn, const lora_pool* p, int32_t n_req, int32_t max_len, int32_t n_heads, int32_t n_kv) {
-  const std::string f(fn);
-  if (!p || n_req < 0 || max_len < 1 || n_heads < 1 || n_kv < 1) return lora_fail(LORA_EINVAL, f + ": bad arguments");
-  if (n_req > 65535) return lora_fail(LORA_EINVAL, f + ": at most 65535 requests per call");
+  const auto fail = [fn](const char* what) { return lora_fail(LORA_EINVAL, std::string(fn) + what); };
+  if (!p || n_req < 0 || max_len < 1 || n_heads < 1 || n_kv < 1) return fail(": bad arguments");
+  if (n_req > 65535) return fail(": at most 65535 requests per call");
+  if (n_req * (((int64_t)max_len + kTile - 1) / kTile) > INT32_MAX) return fail(": n_req x max_len is at most 16 x 2^31");
   if (n_heads % n_kv != 0 || n_heads / n_kv > kSplitMaxGroup)
-    return lora_fail(LORA_EINVAL, f + ": n_heads must be 1 to 16 times n_kv_heads");
-  if (p->H % n_kv != 0) return lora_fail(LORA_EINVAL, f + ": H is not a multiple of n_kv_heads");
+    return fail(": n_heads must be 1 to 16 times n_kv_heads");
+  if (p->H % n_kv != 0) return fail(": H is not a multiple of n_kv_heads");
   const int D = p->H / n_kv;
-  if (D != 64 && D != 128 && D != 256) return lora_fail(LORA_EINVAL, f + ": head width must be 64, 128 or 256");
+  if (D != 64 && D != 128 && D != 256) return fail(": head width must be 64, 128 or 256");
   return LORA_OK;
 }
 

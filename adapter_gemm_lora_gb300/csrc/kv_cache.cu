@@ -17,13 +17,14 @@ namespace {
 // prompt rows at H = 4096 take 57.2 us, 6.5 TB/s (0.97 of the copy rate).  One row per request of a
 // decode step is a launch: 256 rows at H = 5120 take 5 us a call, most of it on the host.
 constexpr int kWriteThreads = 256;
+constexpr int kWriteBatch = 4;                             // 16-byte reads a lane has in flight
 
+// The inputs are not marked read-only: this kernel may start while the one that writes them still
+// runs (it waits before it reads), which read-only loads do not allow.
 __global__ void __launch_bounds__(kWriteThreads)
-kv_write_kernel(uint16_t* __restrict__ pool, int64_t num_pages, int32_t H, int32_t n_rows,
-                const int32_t* __restrict__ row_req, const int32_t* __restrict__ row_pos,
-                const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t k_stride, int64_t v_stride,
-                int32_t n_req, const int2* __restrict__ table, int32_t max_len, int32_t layers, int32_t layer,
-                int32_t* err) {
+kv_write_kernel(uint16_t* pool, int64_t num_pages, int32_t H, int32_t n_rows, const int32_t* row_req,
+                const int32_t* row_pos, const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride,
+                int32_t n_req, const int2* table, int32_t max_len, int32_t layers, int32_t layer, int32_t* err) {
   pdl_wait_then_release();
   const int64_t item = (int64_t)blockIdx.x * (kWriteThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -44,7 +45,16 @@ kv_write_kernel(uint16_t* __restrict__ pool, int64_t num_pages, int32_t H, int32
   const int32_t page = half ? pg.y : pg.x;
   const uint4* src = reinterpret_cast<const uint4*>(half ? v + t * v_stride : k + t * k_stride);
   uint4* dst = reinterpret_cast<uint4*>(pool + (int64_t)page * H);
-  for (int i = lane; i < H / 8; i += 32) dst[i] = src[i];
+  const int n = H / 8;
+  for (int i0 = lane; i0 < n; i0 += 32 * kWriteBatch) {
+    uint4 x[kWriteBatch];
+#pragma unroll
+    for (int b = 0; b < kWriteBatch; ++b)
+      if (i0 + 32 * b < n) x[b] = src[i0 + 32 * b];
+#pragma unroll
+    for (int b = 0; b < kWriteBatch; ++b)
+      if (i0 + 32 * b < n) dst[i0 + 32 * b] = x[b];
+  }
 }
 
 // ---- eviction ------------------------------------------------------------------------------------
@@ -192,7 +202,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
     const float* w = a.weight + e.row * a.max_len;
 #pragma unroll
     for (int b = 0; b < K; ++b)
-      key[b] = j0 + 32 * b + lane < w1 ? __float_as_uint(__ldg(w + j0 + 32 * b + lane)) : 0u;
+      key[b] = j0 + 32 * b + lane < w1 ? __float_as_uint(w[j0 + 32 * b + lane]) : 0u;
 #pragma unroll
     for (int b = 0; b < K; ++b) {
       const int j = j0 + 32 * b + lane;
@@ -380,8 +390,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
         for (int b = 0; b < kBatch; ++b) j[b] = list[min(i0 + 32 * b, n_out - 1)];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          x[b] = __ldg(w + j[b]);
-          if (kRows == 1) pages[b] = __ldg(t_in + (int64_t)j[b] * a.layers);
+          x[b] = w[j[b]];
+          if (kRows == 1) pages[b] = t_in[(int64_t)j[b] * a.layers];
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
@@ -426,7 +436,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int j = list[min(i0 + kStep * b, n_keep - 1)];
-      pages[b] = __ldg(t_in + (int64_t)j * a.layers);
+      pages[b] = t_in[(int64_t)j * a.layers];
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {

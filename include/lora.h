@@ -240,7 +240,7 @@ int lora_kv_write(lora_pool* pool, int32_t n_rows, const int32_t* row_req, const
  * sets the device error word and its token is skipped (it receives no weight); a request length
  * outside [0, max_len] sets it and is clamped.  If no score of a row is above -infinity the row
  * counts as empty.  Results do not depend on the order in which CTAs run.  At most 65535
- * requests per call.
+ * requests per call, and n_req x max_len at most 16 x 2^31.
  */
 int64_t lora_attention_split_size(const lora_pool* pool, int32_t n_req, int32_t max_len, int32_t n_heads,
                                   int32_t n_kv_heads, int32_t with_weights);

@@ -42,7 +42,8 @@ def _attend(L, pool):
 
 @pytest.mark.parametrize("over,message", [
     (dict(n_req=-1), "bad arguments"), (dict(max_len=0), "bad arguments"), (dict(n_heads=0), "bad arguments"),
-    (dict(n_kv_heads=0), "bad arguments"), (dict(n_req=65536), "65535"), (dict(n_heads=6), "1 to 16 times"),
+    (dict(n_kv_heads=0), "bad arguments"), (dict(n_req=65536), "65535"), (dict(n_req=65535, max_len=1 << 20), "16 x 2^31"),
+    (dict(n_heads=6), "1 to 16 times"),
     (dict(n_heads=68), "1 to 16 times"), (dict(n_heads=3, n_kv_heads=3), "multiple of n_kv_heads"),
     (dict(n_heads=8, n_kv_heads=8), "head width"), (dict(layers=0), "layer outside"), (dict(layer=2), "layer outside"),
     (dict(layer=-1), "layer outside"), (dict(weight_in_dev=F), "weight_in without"), (dict(table_dev=None), "null pointer"),
