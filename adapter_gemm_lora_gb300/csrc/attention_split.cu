@@ -33,10 +33,11 @@ namespace {
 
 constexpr int kSplitMaxGroup = 16;                  // query heads per KV head
 constexpr int kWarps = 4;                           // consumer warps
-// A bulk copy costs its warp about 35 cycles to issue, whatever its size, so slices below 1 KB need
-// two producer warps (one for K, one for V) to keep up: 160,000 tokens in 512-byte slices (four
-// heads of 64) take 324 us with one and 214 us with two; from 1 KB one is enough (a long request
-// at D = 128: 316 us with one, 321 us with two).
+// A bulk copy costs its warp about 66 cycles to issue, whatever its size (with several producers on an
+// SM still 33 each), so slices below 1 KB need two producer warps (one for K, one for V) to keep up:
+// 160,000 tokens in 512-byte slices (four heads of 64) take 324 us with one and 214 us with two.  From
+// 1 KB one is enough for a long request (316 us with one, 321 with two), but a request that one CTA
+// takes whole waits for the issue: 61 tokens 7.8 us with one, 6.3 with two.
 constexpr int kSmallSlice = 1024;
 constexpr int threads_of(int producers) { return 32 * (kWarps + producers); }
 constexpr int kCtasPerSm = 2;
@@ -948,11 +949,17 @@ SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads,
   pl.stages = std::min(kMaxStages, (kMaxSmem - kStaticSmem - tail) / pl.stage_bytes);
   pl.smem = pl.stages * pl.stage_bytes + tail;
   const int sms = device_sm_count() * kCtasPerSm;
-  pl.whole = max_len <= kTile * pl.tiles;
+  // One CTA per request and head group, and no join, where a request is at most four tiles and all
+  // CTAs run in two rounds.  H = 4096, one GB300, us a call, whole requests / ranges: 1 request of 13
+  // tokens 3.7 / 6.8, of 61 6.3 / 7.0, of 125 9.8 / 7.2; 64 requests (512 CTAs) of 61 13.6 / 16.4; 256
+  // requests (2,048 CTAs) of 13 24.6 / 18.1, of 61 59 / 47.
+  pl.whole = max_len <= 4 * kTile && (int64_t)n_req * pl.n_groups <= 2 * sms;
   if (pl.whole) {
     pl.parts = n_req;
   } else {
-    // As many CTAs as run at once; where the head groups do not divide the SMs, up to 4 rounds of CTAs.
+    // As many CTAs as run at once; where the head groups do not divide them, up to 4 rounds (32 groups,
+    // H = 16384: 60,000 tokens 587 us in one round of 288 CTAs, 567 in two of 304; 16 requests of 500
+    // tokens 84.6 and 87.2).
     double best = 0;
     for (int k = 1; k <= 4; ++k) {
       const int parts = k * sms / pl.n_groups;
@@ -995,7 +1002,7 @@ int launch_split(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
 // The kernel of a shape: split_plan gives these tile counts, and the slices that take two producers.
 int launch_split_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   const SplitPlan& pl = a.plan;
-  const bool two = pl.heads * pl.D * 2 < kSmallSlice, pairs = pl.heads > pl.head_slots;
+  const bool two = pl.whole || pl.heads * pl.D * 2 < kSmallSlice, pairs = pl.heads > pl.head_slots;
   switch (pl.D * 16 + pl.tiles) {
     case 64 * 16 + 1: return two ? launch_split<64, 1, 2, 2>(p, a, st) : launch_split<64, 1, 1, 2>(p, a, st);
     case 64 * 16 + 2: return pairs ? launch_split<64, 2, 2, 2>(p, a, st) : launch_split<64, 2, 2, 1>(p, a, st);
@@ -1004,7 +1011,7 @@ int launch_split_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
     case 128 * 16 + 1: return two ? launch_split<128, 1, 2, 1>(p, a, st) : launch_split<128, 1, 1, 1>(p, a, st);
     case 128 * 16 + 2: return launch_split<128, 2, 2, 1>(p, a, st);
     case 128 * 16 + 4: return launch_split<128, 4, 2, 1>(p, a, st);
-    case 256 * 16 + 1: return launch_split<256, 1, 1, 1>(p, a, st);
+    case 256 * 16 + 1: return two ? launch_split<256, 1, 2, 1>(p, a, st) : launch_split<256, 1, 1, 1>(p, a, st);
     case 256 * 16 + 2: return launch_split<256, 2, 2, 1>(p, a, st);
   }
   return lora_fail(LORA_EINVAL, "lora_attention_split: no kernel for this geometry");

@@ -108,6 +108,10 @@ SHAPES = [   # n_kv, G, D, layers, lengths
     (4, 12, 64, 1, [50, 333]),          # 8 + 4 query heads on two warps, each with two heads of 64
     (3, 11, 256, 1, [40, 1, 100]),
     (2, 16, 128, 1, [1000, 17]),
+    (8, 1, 128, 1, [61, 0, 16, 1]),     # one CTA per request and head group: D = 128, 64, 256, several warps a head
+    (8, 2, 64, 1, [60, 33]),
+    (4, 3, 256, 1, [17, 61, 48]),
+    (1, 1, 128, 1, [61, 2]),
     (3, 2, 128, 1, [129] * 130),        # more than 128 requests: the range search goes through shared memory
 ]
 
@@ -356,14 +360,13 @@ def test_attention_split_same_bits_again_on_a_side_stream_and_in_a_graph(L):
 
 
 def test_attention_split_of_sixty_thousand_requests(L):
-    """One token each (or none): the output is its V, the weight one per query head; whole requests and
-    split ranges."""
+    """One token each (or none): the output is its V, the weight one per query head."""
     import torch
     n, H = 60_000, 64
     pool_t = torch.randn((2 * n, H), device="cuda").bfloat16()
     pool = L.lora_pool_create(pool_t, 2 * n, H, 1, 1)
     try:
-        for max_len in (1, 200):                                   # up to 128 tokens a request is one CTA's
+        for max_len in (1, 200):
             table = torch.full((n, max_len, 1, 2), -1, dtype=torch.int32, device="cuda")
             pages = torch.randperm(2 * n, device="cuda").to(torch.int32).view(n, 2)
             table[:, 0, 0] = pages
