@@ -1062,8 +1062,9 @@ extern "C" int lora_attention_split(lora_pool* p, int32_t n_req, const int32_t* 
   if (n_req > 0 && q == out) return lora_fail(LORA_EINVAL, "lora_attention_split: out must not alias q");
   if ((reinterpret_cast<uintptr_t>(table_dev) & 7) != 0)
     return lora_fail(LORA_EINVAL, "lora_attention_split: the table must be 8-byte aligned");
-  if (((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(weight_in) | reinterpret_cast<uintptr_t>(weight_out)) & 3) != 0)
-    return lora_fail(LORA_EINVAL, "lora_attention_split: lse and weights must be 4-byte aligned");
+  if (((reinterpret_cast<uintptr_t>(seq_len_dev) | reinterpret_cast<uintptr_t>(lse) |
+        reinterpret_cast<uintptr_t>(weight_in) | reinterpret_cast<uintptr_t>(weight_out)) & 3) != 0)
+    return lora_fail(LORA_EINVAL, "lora_attention_split: lengths, lse and weights must be 4-byte aligned");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
     return lora_fail(LORA_EINVAL, "lora_attention_split: workspace must be 256-byte aligned");
   if (p->planning) return lora_fail(LORA_EINVAL, "lora_attention_split: planning pool has no device state");

@@ -259,7 +259,7 @@ int lora_attention_split(lora_pool* pool, int32_t n_req, const int32_t* table_de
  *   weight_dev   device fp32 [layers][n_req][max_len], lora_attention_split's weight_out per layer;
  *   budget >= 1, 0 <= recent <= budget;
  *   keep_dev     out: device int32 [layers][n_req][budget], the kept positions, ascending, then -1;
- *   new_len_dev  out: device int32 [n_req], n_keep (may be seq_len_dev's successor, not itself);
+ *   new_len_dev  out: device int32 [n_req], n_keep;
  *   table_out    out: device int32 [n_req][max_len_out][layers][2] (8-byte aligned), the kept
  *                tokens' pages in that order, then -1;
  *   weight_out   out: device fp32 [layers][n_req][max_len_out], their weights, then 0;

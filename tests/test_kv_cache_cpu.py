@@ -52,7 +52,8 @@ def _attend(L, pool):
     (dict(out_stride=8), "strides"), (dict(q_stride=-8), "strides"), (dict(weight_out_dev=F, weight_stride=7), "weight_stride"),
     (dict(q_dev=C + 8), "16-byte"), (dict(out_dev=D + 2), "16-byte"), (dict(out_dev=C), "alias"),
     (dict(table_dev=A + 4), "8-byte"), (dict(workspace_dev=E + 128), "256-byte"), (dict(lse_dev=F + 2), "4-byte"),
-    (dict(weight_out_dev=F + 1), "4-byte"), (dict(), "planning pool"), (dict(n_req=0), "planning pool"),
+    (dict(weight_out_dev=F + 1), "4-byte"), (dict(seq_len_dev=B + 2), "4-byte"),
+    (dict(), "planning pool"), (dict(n_req=0), "planning pool"),
 ])
 def test_attention_split_refuses(L, pool, over, message):
     _refused(L, _attend(L, pool), message, **over)
@@ -74,7 +75,8 @@ def test_attention_split_size_refuses(L, pool):
     (dict(row_req_dev=None), "null pointer"), (dict(row_pos_dev=None), "null pointer"), (dict(k_dev=None), "null pointer"),
     (dict(v_dev=None), "null pointer"), (dict(table_dev=None), "null pointer"), (dict(k_stride=248), "strides"),
     (dict(v_stride=260), "strides"), (dict(k_dev=C + 8), "16-byte"), (dict(v_dev=D + 4), "16-byte"),
-    (dict(table_dev=E + 4), "8-byte"), (dict(), "planning pool"),
+    (dict(table_dev=E + 4), "8-byte"), (dict(row_req_dev=A + 2), "4-byte"), (dict(row_pos_dev=B + 1), "4-byte"),
+    (dict(), "planning pool"),
 ])
 def test_kv_write_refuses(L, pool, over, message):
     base = dict(pool=pool, n_rows=4, row_req_dev=A, row_pos_dev=B, k_dev=C, v_dev=D, n_req=2, table_dev=E, max_len=8,
@@ -88,7 +90,8 @@ def test_kv_write_refuses(L, pool, over, message):
     (dict(table_dev=None), "null pointer"), (dict(seq_len_dev=None), "null pointer"), (dict(weight_dev=None), "null pointer"),
     (dict(keep_dev=None), "null pointer"), (dict(new_len_dev=None), "null pointer"), (dict(table_out_dev=None), "null pointer"),
     (dict(weight_out_dev=None), "null pointer"), (dict(table_dev=A + 4), "8-byte"), (dict(table_out_dev=F + 4), "8-byte"),
-    (dict(table_out_dev=A), "inputs"), (dict(weight_out_dev=C), "inputs"), (dict(new_len_dev=B), "inputs"),
+    (dict(seq_len_dev=B + 2), "4-byte"), (dict(weight_dev=C + 1), "4-byte"), (dict(keep_dev=D + 2), "4-byte"),
+    (dict(new_len_dev=E + 2), "4-byte"), (dict(weight_out_dev=G + 2), "4-byte"), (dict(table_out_dev=A), "inputs"), (dict(weight_out_dev=C), "inputs"), (dict(new_len_dev=B), "inputs"),
     (dict(n_req=65536, layers=65536), "too many"), (dict(max_len=(1 << 30) + 1), "2^30"),
     (dict(max_len_out=(1 << 30) + 1), "2^30"), (dict(), "planning pool"),
 ])
