@@ -403,6 +403,35 @@ def test_attention_split_does_not_depend_on_the_other_requests_values(L):
         c.close()
 
 
+def test_attention_split_on_two_streams_at_once(L):
+    """Calls with workspaces of their own may overlap: each gives what it gives alone."""
+    import torch
+    c = Cache(L, 512, 1, [3000, 0, 700, 65], seed=31)
+    try:
+        qs = [bits_to_torch(workloads.to_bf16_bits(c.rng.standard_normal((4, 1024)).astype(np.float32))) for _ in range(2)]
+        spaces = [c.workspace(8, 4, True) for _ in range(2)]
+
+        def call(i, out, w, stream=None):
+            L.lora_attention_split(c.pool, 4, c.table, c.seq, c.max_len, 1, 0, qs[i], out, 8, 4, *spaces[i],
+                                   weight_out_dev=w, stream=stream)
+        alone = [(torch.empty_like(q), torch.zeros((4, c.max_len), device="cuda")) for q in qs]
+        for i in range(2):
+            call(i, *alone[i])
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        both = [(torch.empty_like(q), torch.zeros((4, c.max_len), device="cuda")) for q in qs]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for i in range(2):
+                call(i, *both[i], stream=streams[i])
+        torch.cuda.synchronize()
+        L.lora_status(c.pool)
+        for a, b in zip(alone, both):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    finally:
+        c.close()
+
+
 # ---- page writes ---------------------------------------------------------------------------------
 @pytest.mark.parametrize("H,layers,lengths,pad", [
     (64, 1, [1], 0), (256, 2, [5, 0, 9], 8), (5120, 1, [1] * 40, 0), (4096, 3, [130, 1, 17], 64), (16384, 1, [3], 0),
@@ -617,11 +646,12 @@ def test_evict_then_keep_then_attend(L):
         c.close()
 
 
-def test_evict_in_a_graph_and_on_a_side_stream(L):
+@pytest.mark.parametrize("long", [900, 20000])                    # a CTA per row, a cluster per row
+def test_evict_in_a_graph_and_on_a_side_stream(L, long):
     import torch
     rng = np.random.default_rng(4)
-    layers, n_req, max_len = 3, 5, 900
-    lengths = [900, 10, 450, 0, 300]
+    layers, n_req, max_len = 3, 5, long
+    lengths = [long, 10, long // 2, 0, 300]
     weight = torch.from_numpy(_weights("ties", rng, (layers, n_req, max_len))).cuda()
     table = torch.from_numpy(rng.integers(0, 99, size=(n_req, max_len, layers, 2)).astype(np.int32)).cuda()
     seq = torch.tensor(lengths, dtype=torch.int32, device="cuda")
@@ -644,10 +674,10 @@ def test_evict_in_a_graph_and_on_a_side_stream(L):
         with torch.cuda.graph(g):
             L.lora_kv_evict(*args)
         weight.neg_()
-        seq[3] = 899
+        seq[3] = long - 1
         g.replay()
         torch.cuda.synchronize()
-        want = _evict_expected(table.cpu().numpy(), [900, 10, 450, 899, 300], weight.cpu().numpy(), 256, 32, 256)
+        want = _evict_expected(table.cpu().numpy(), [long, 10, long // 2, long - 1, 300], weight.cpu().numpy(), 256, 32, 256)
         _same([x.cpu().numpy() for x in (keep, new_len, t_out, w_out)], want)
         L.lora_status(pool)
     finally:
