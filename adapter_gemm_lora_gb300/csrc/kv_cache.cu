@@ -57,6 +57,70 @@ kv_write_kernel(uint16_t* pool, int64_t num_pages, int32_t H, int32_t n_rows, co
   }
 }
 
+// Many short rows: a warp per row leaves most of its lanes idle and pays three dependent reads (row,
+// table, row's data) for a few bytes.  Here L = 8, 16 or 32 lanes copy a row and a warp takes 128 / L
+// tokens: one lane per token reads its page ids while the first loads of k and v are under way, and
+// each lane has kWritePacked 16-byte loads in flight.  160 MB in and out, us with a warp per row and
+// here: H = 64 290 / 59.6, 128 153 / 55.4, 256 87.7 / 51.1, 512 58.6 / 50.1 (0.83 to 0.96 of the copy
+// rate); 768 52.5 / 50.1, but 10,368 rows of it 7.5 / 9.7, and 1,024 49.2 / 51.9.  Rows that fit the
+// SMs' warps once are quicker with a warp each: 64 rows of H = 64 2.2 / 2.9, 960 of 512 2.6 / 3.8; at
+// 6,208 rows of 320 both take 4.2.
+constexpr int kWritePacked = 8;
+constexpr int kWritePackedMaxH = 512;
+template <int L>
+__global__ void __launch_bounds__(kWriteThreads)
+kv_write_packed_kernel(uint16_t* pool, int64_t num_pages, int32_t H, int32_t n_rows, const int32_t* row_req,
+                       const int32_t* row_pos, const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                       int64_t v_stride, int32_t n_req, const int2* table, int32_t max_len, int32_t layers,
+                       int32_t layer, int32_t* err) {
+  constexpr int kRows = 32 / L;                            // rows (a token's K or V) at a time
+  constexpr int kTokens = kRows * kWritePacked / 2;
+  static_assert(kTokens <= 32, "a lane reads one token's entry");
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31;
+  const int64_t t0 = ((int64_t)blockIdx.x * (kWriteThreads / 32) + (threadIdx.x >> 5)) * kTokens;
+  if (t0 >= n_rows) return;
+  int32_t r = -1, j = 0;
+  if (lane < kTokens && t0 + lane < n_rows) {
+    r = row_req[t0 + lane];
+    j = row_pos[t0 + lane];
+  }
+  bool live = r != -1;
+  if (live && (r < 0 || r >= n_req || j < 0 || j >= max_len)) {
+    flag_error(err, LORA_DEV_BAD_SEGMENT);
+    live = false;
+  }
+  int2 pg = make_int2(-1, -1);
+  if (live) pg = table[((int64_t)r * max_len + j) * layers + layer];
+  const unsigned lives = __ballot_sync(0xffffffffu, live);
+  const int n = H / 8, col = lane % L, half = (lane / L) & 1;
+  // Row b of this lane: token (b * kRows + lane / L) / 2; with one row at a time K and V take turns.
+  bool first = true;
+  for (int i = col; i - col < n; i += L) {
+    uint4 x[kWritePacked];
+#pragma unroll
+    for (int b = 0; b < kWritePacked; ++b) {
+      const int row = b * kRows + lane / L;
+      const bool is_v = kRows == 1 ? (b & 1) : half;
+      const int64_t t = t0 + (row >> 1);
+      const uint16_t* src = is_v ? v + t * v_stride : k + t * k_stride;
+      if (i < n && ((lives >> (row >> 1)) & 1)) x[b] = reinterpret_cast<const uint4*>(src)[i];
+    }
+    if (first && live && (pg.x < 0 || pg.x >= num_pages || pg.y < 0 || pg.y >= num_pages)) {
+      flag_error(err, LORA_DEV_BAD_PAGE);
+      pg = make_int2(-1, -1);
+    }
+    first = false;
+#pragma unroll
+    for (int b = 0; b < kWritePacked; ++b) {
+      const int row = b * kRows + lane / L;
+      const int32_t px = __shfl_sync(0xffffffffu, pg.x, row >> 1), py = __shfl_sync(0xffffffffu, pg.y, row >> 1);
+      const int32_t page = (kRows == 1 ? (b & 1) : half) ? py : px;
+      if (i < n && page >= 0) reinterpret_cast<uint4*>(pool + (int64_t)page * H)[i] = x[b];
+    }
+  }
+}
+
 // ---- eviction ------------------------------------------------------------------------------------
 // Sort key of a weight: ascending with the value, -0 = +0, NaN = -infinity.  Keys of weights lie in
 // [0x007FFFFF, 0xFF800000]: outside are a token that stays in any case and one that is not there.
@@ -513,14 +577,20 @@ extern "C" int lora_kv_write(lora_pool* p, int32_t n_rows, const int32_t* row_re
   if (p->planning) return lora_fail(LORA_EINVAL, "lora_kv_write: planning pool has no device state");
   if (n_rows == 0) return LORA_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t items = 2 * (int64_t)n_rows;
-  const unsigned grid = (unsigned)((items + kWriteThreads / 32 - 1) / (kWriteThreads / 32));
   ProfScope prof(p, LORA_KIND_KV, st);
-  const cudaError_t e =
-      launch_pdl(!p->prof_on, kv_write_kernel, dim3(grid), dim3(kWriteThreads), 0, st,
-                 static_cast<uint16_t*>(p->pool_dev), p->num_pages, p->H, n_rows, row_req, row_pos,
-                 static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_stride, v_stride, n_req,
-                 reinterpret_cast<const int2*>(table_dev), max_len, layers, layer, p->d_err);
+  const auto launch = [&](auto* kernel, int64_t warps) {
+    const int per = kWriteThreads / 32;
+    return launch_pdl(!p->prof_on, kernel, dim3((unsigned)((warps + per - 1) / per)), dim3(kWriteThreads), 0, st,
+                      static_cast<uint16_t*>(p->pool_dev), p->num_pages, p->H, n_rows, row_req, row_pos,
+                      static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_stride, v_stride, n_req,
+                      reinterpret_cast<const int2*>(table_dev), max_len, layers, layer, p->d_err);
+  };
+  const int64_t rows = n_rows;
+  const bool packed = p->H <= kWritePackedMaxH && 2 * rows > 64 * (int64_t)device_sm_count();
+  const cudaError_t e = !packed       ? launch(kv_write_kernel, 2 * rows)
+                        : p->H <= 64  ? launch(kv_write_packed_kernel<8>, (rows + 15) / 16)
+                        : p->H <= 128 ? launch(kv_write_packed_kernel<16>, (rows + 7) / 8)
+                                      : launch(kv_write_packed_kernel<32>, (rows + 3) / 4);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_kv_write launch");
 }
 

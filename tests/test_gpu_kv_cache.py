@@ -463,6 +463,50 @@ def test_kv_write_puts_every_row_in_its_page(L, H, layers, lengths, pad):
         c.close()
 
 
+@pytest.mark.parametrize("H,pad", [(64, 0), (128, 8), (192, 0), (256, 64), (320, 8), (512, 0), (576, 0)])
+@pytest.mark.parametrize("bad", [False, True])
+def test_kv_write_of_many_short_rows(L, H, pad, bad):
+    """Enough rows that warps take several; the count ends inside a warp's share."""
+    import torch
+    lengths = [3000, 0, 1, 2998]
+    layers, layer = 2, 1
+    c = Cache(L, H, layers, lengths, seed=H)
+    try:
+        T = sum(lengths)
+        rng = np.random.default_rng(H)
+        req = np.repeat(np.arange(len(lengths)), lengths).astype(np.int32)
+        pos = np.concatenate([np.arange(n) for n in lengths]).astype(np.int32)
+        perm = rng.permutation(T)
+        req, pos = req[perm], pos[perm]
+        rows = [torch.empty((T, H + pad), dtype=torch.bfloat16, device="cuda").normal_() for _ in range(2)]
+        tabs = c.tables(layer)
+        pages = torch.from_numpy(np.stack([tabs[r][p] for r, p in zip(req, pos)])).cuda()
+        keep = rng.random(T) < 0.8
+        keep[-1] = True
+        req = np.where(keep, req, -1).astype(np.int32)
+        if bad:                                            # the row after each of these is written
+            req[5], pos[6], pos[17], req[T - 3] = len(lengths), -1, c.max_len, -2
+            bad_page = int(np.flatnonzero(keep[100:])[0]) + 100
+            c.table[int(req[bad_page]), int(pos[bad_page]), layer, 1] = c.num_pages
+            req[6] = req[17] = 0
+            keep[[5, 6, 17, T - 3, bad_page]] = False
+        want = c.pool_t.clone()
+        sel = torch.from_numpy(np.flatnonzero(keep)).cuda()
+        for half in range(2):
+            want[pages[sel, half]] = rows[half][sel, :H]
+        L.lora_kv_write(c.pool, T, torch.from_numpy(req).cuda(), torch.from_numpy(pos).cuda(), rows[0], rows[1], c.n_req,
+                        c.table, c.max_len, layers, layer, k_stride=H + pad, v_stride=H + pad)
+        if bad:
+            with pytest.raises(L.LoraError) as e:
+                L.lora_status(c.pool)
+            assert e.value.code == L.LORA_EDEVICE
+        else:
+            L.lora_status(c.pool)
+        assert torch.equal(want.view(torch.int16), c.pool_t.view(torch.int16))
+    finally:
+        c.close()
+
+
 def test_kv_write_reports_bad_rows_and_writes_the_others(L):
     import torch
     c = Cache(L, 128, 1, [4, 4], seed=1)
