@@ -39,6 +39,12 @@ constexpr int kWarps = 4;                           // consumer warps
 // 1 KB one is enough for a long request (316 us with one, 321 with two), but a request that one CTA
 // takes whole waits for the issue: 61 tokens 7.8 us with one, 6.3 with two.
 constexpr int kSmallSlice = 1024;
+// Rows of up to 384 bytes have no producer: the consumer warps load K and V rows from their pages
+// straight into MMA fragments, since a copy's cost does not fall with its size.  64 x 10,000 tokens,
+// 1 query head per KV head, us by copies / direct: one head of 64 88 / 34.9 (one of 128 92 / 58), two
+// of 64 93 / 58.5, three 107 / 94; but four 107 / 131, and at D = 128 two 106 / 106, four 196 / 204
+// (eight heads of 64 197 / 311).  Short calls: 8 x 2,000 tokens of one head of 64 11.7 / 8.0.
+constexpr int kDirectSlice = 384;
 constexpr int threads_of(int producers) { return 32 * (kWarps + producers); }
 constexpr int kCtasPerSm = 2;
 constexpr int kTile = 16;                           // tokens a warp takes at a time
@@ -67,6 +73,7 @@ struct SplitPlan {
   int32_t stages;
   int32_t parts;                 // ranges the token sequence is cut into
   bool whole;                    // one range per request: nothing to join
+  bool direct;                   // the consumers read the rows themselves, a tile of a unit each
   int32_t row_bytes, stage_bytes, smem;
 };
 
@@ -295,7 +302,8 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g0 = blockIdx.x % pl.n_groups, p = blockIdx.x / pl.n_groups;
   const int h0 = g0 * pl.heads, n_act = min(pl.heads, pl.n_kv - h0);
-  constexpr int st = kTile * TILES;
+  constexpr bool kDirect = NP == 0;
+  const int st = kDirect ? kTile * pl.tiles : kTile * TILES;
   const int S = pl.stages;
   const uint32_t ring = smem_u32(smem), RB = pl.row_bytes;
   const uint32_t bar_full = smem_u32(bars), bar_empty = bar_full + 8 * kMaxStages;
@@ -303,7 +311,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   float* merge = reinterpret_cast<float*>(smem + (size_t)S * pl.stage_bytes);   // [head warps][8][D + 2]
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(bar_full + 8 * s, NP);
+      mbar_init(bar_full + 8 * s, NP > 0 ? NP : 1);
       mbar_init(bar_empty + 8 * s, min(pl.head_slots, n_act) * pl.octets * pl.sharers);
     }
     for (int h = 0; h < kWarps; ++h) {
@@ -327,7 +335,18 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   __syncthreads();                                         // barriers set up; the sums lie where heads merge
   if (g0 == 0 && threadIdx.x == 0) a.ws_start[p] = make_int4(rs.req, rs.units > 0 ? rs.tok : 0, rs.p0, rs.p1);
 
-  if (warp >= kWarps) {
+  const auto zero_empty = [&] {                            // requests without a token get zeros
+    for (int r = p; r < a.n_req; r += pl.parts) {
+      if (a.seq_len[r] > 0) continue;
+      uint16_t* row = a.out + r * a.out_stride + (int64_t)h0 * pl.group * D;
+      for (int i = lane; i < n_act * pl.group * D / 8; i += 32) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int i = lane; i < n_act * pl.group; i += 32) a.lse[(int64_t)r * a.n_heads + h0 * pl.group + i] = -INFINITY;
+    }
+  };
+  if (kDirect) {
+    if (warp == kWarps - 1) zero_empty();
+  } else if (warp >= kWarps) {
     // ---- producers: each finds every unit's valid tokens; with two, one copies K and one V ----
     const int role = warp - kWarps;
     const uint32_t bytes = (uint32_t)n_act * D * 2;
@@ -393,7 +412,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
 #pragma unroll
           for (int c = 0; c < TILES; ++c) f.mask[c] = (uint16_t)mask[c];
         }
-        mbar_arrive_expect_tx(bar_full + 8 * s, 2 / NP * bytes * n_valid);
+        mbar_arrive_expect_tx(bar_full + 8 * s, 2 / (NP > 0 ? NP : 1) * bytes * n_valid);
       }
       __syncwarp();
 #pragma unroll
@@ -412,14 +431,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
       // the copies already issued land before this CTA's shared memory is released
       for (int c = it > S ? it - S : 0; c < it; ++c) (void)mbar_wait(bar_full + 8 * (c % S), (c / S) & 1);
     }
-    // Requests without a token get zeros.
-    for (int r = role == 0 ? p : a.n_req; r < a.n_req; r += pl.parts) {
-      if (a.seq_len[r] > 0) continue;
-      uint16_t* row = a.out + r * a.out_stride + (int64_t)h0 * pl.group * D;
-      for (int i = lane; i < n_act * pl.group * D / 8; i += 32) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
-      if (a.lse)
-        for (int i = lane; i < n_act * pl.group; i += 32) a.lse[(int64_t)r * a.n_heads + h0 * pl.group + i] = -INFINITY;
-    }
+    if (role == 0) zero_empty();
     return;
   }
 
@@ -427,22 +439,41 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   const int head_warps = pl.head_slots * pl.octets, hw = warp % head_warps, share = warp / head_warps;
   const int hh = hw / pl.octets, octet = hw % pl.octets;
   if (share >= pl.sharers || hh >= n_act || rs.units == 0) return;
-  const int n_mine = HW == 1 || hh + pl.head_slots >= n_act ? 1 : 2;           // this warp's heads: hh, hh + head_slots
+  // HW = 2: two KV heads, hh and hh + head_slots, or (direct) one with up to 16 query heads.
+  const int n_mine = kDirect ? HW : HW == 1 || hh + pl.head_slots >= n_act ? 1 : 2;
   const int g = lane >> 2, t = lane & 3;
-  const int G = min(8, pl.group - 8 * octet);              // its query heads of each
-  const auto head_of = [&](int u) { return (h0 + hh + u * pl.head_slots) * pl.group + 8 * octet; };
+  const auto n_query = [&](int u) { return min(8, pl.group - 8 * (kDirect ? octet + u : octet)); };
+  const auto head_of = [&](int u) {
+    return kDirect ? (h0 + hh) * pl.group + 8 * (octet + u) : (h0 + hh + u * pl.head_slots) * pl.group + 8 * octet;
+  };
   uint32_t qf[HW][KS][2];
   float acc[HW][KS][4], m[HW][2], l[HW][2];
+  // The features that a lane holds: of a fragment's row g (+ 8 where hi), and of columns 2t and 2t + 1.
+  const auto row_of = [&](int ks, int hi) {
+    return kDirect ? 32 * (ks / 2) + 8 * (g / 2) + (g & 1) + 4 * (ks & 1) + 2 * hi : 16 * ks + g + 8 * hi;
+  };
+  const auto pair_of = [&](int ks, int hi) {
+    return kDirect ? 32 * (ks / 2) + 8 * t + 4 * (ks & 1) + 2 * hi : 16 * ks + 2 * t + 8 * hi;
+  };
   const auto load_q = [&](int req) {
 #pragma unroll
     for (int u = 0; u < HW; ++u) {
-      const bool has = g < G && u < n_mine;
-      const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + req * a.q_stride + (int64_t)(head_of(u) + g) * D) + t;
+      const bool has = u < n_mine && g < n_query(u);
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + req * a.q_stride + (int64_t)(head_of(u) + g) * D);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        qf[u][ks][0] = has ? qp[ks * 8] : 0u;
-        qf[u][ks][1] = has ? qp[ks * 8 + 4] : 0u;
+        qf[u][ks][0] = has ? qp[pair_of(ks, 0) / 2] : 0u;
+        qf[u][ks][1] = has ? qp[pair_of(ks, 1) / 2] : 0u;
       }
+    }
+  };
+  const auto begin_segment = [&] {
+#pragma unroll
+    for (int u = 0; u < HW; ++u) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) acc[u][ks][0] = acc[u][ks][1] = acc[u][ks][2] = acc[u][ks][3] = 0.f;
+      m[u][0] = m[u][1] = -INFINITY;
+      l[u][0] = l[u][1] = 0.f;
     }
   };
   // lane addresses of the fragments within a tile
@@ -451,12 +482,181 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
                           (uint32_t)(hh * D + ((lane >> 3) & 1) * 8) * 2;
   const uint32_t head_step = (uint32_t)(pl.head_slots * D * 2);
   const int turns = pl.sharers / tile_sharers, turn = share / tile_sharers;
+  // Scores of NT tiles into weights 2^(s - m), transposed for the V product, hi and lo terms.
+  constexpr int NT = kDirect ? TILES : 1;
+  const auto tile_weights = [&](int u, int req, int j0, int n, uint32_t mask, float (&sc)[NT][4],
+                                const float (&odd)[NT][4], uint32_t (&ph)[NT][2], uint32_t (&plo)[NT][2]) {
+    const int G = n_query(u);
+    float x[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sc[i][e] = (mask >> (16 * i + g + (e & 2) * 4)) & 1u ? (sc[i][e] + odd[i][e]) * a.scale_log2 : -INFINITY;
+      if (a.ws_scores && (i == 0 || j0 + i * kTile < n)) {
+        float* dst = a.ws_scores + ((int64_t)req * a.n_heads + head_of(u) + 2 * t) * a.score_stride + j0 + i * kTile + g;
+        if (2 * t < G) {
+          dst[0] = sc[i][0];
+          dst[8] = sc[i][2];
+        }
+        if (2 * t + 1 < G) {
+          dst[a.score_stride] = sc[i][1];
+          dst[a.score_stride + 8] = sc[i][3];
+        }
+      }
+      x[0] = fmaxf(x[0], fmaxf(sc[i][0], sc[i][2]));
+      x[1] = fmaxf(x[1], fmaxf(sc[i][1], sc[i][3]));
+    }
+    if (__any_sync(0xffffffffu, x[0] > m[u][0] + kMaxSlack || x[1] > m[u][1] + kMaxSlack)) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) x[k] = fmaxf(x[k], __shfl_xor_sync(0xffffffffu, x[k], o));
+      float c[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float mn = fmaxf(m[u][k], x[k]);
+        c[k] = mn == -INFINITY ? 0.f : exp2f(m[u][k] - mn);   // no score above -infinity yet: nothing to keep
+        l[u][k] *= c[k];
+        m[u][k] = mn;
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        acc[u][ks][0] *= c[0];
+        acc[u][ks][1] *= c[1];
+        acc[u][ks][2] *= c[0];
+        acc[u][ks][3] *= c[1];
+      }
+    }
+    const float ms[2] = {m[u][0] == -INFINITY ? 0.f : m[u][0], m[u][1] == -INFINITY ? 0.f : m[u][1]};   // every weight 0 there
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        sc[i][k] = exp2f(sc[i][k] - ms[k]);
+        sc[i][2 + k] = exp2f(sc[i][2 + k] - ms[k]);
+        l[u][k] += sc[i][k] + sc[i][2 + k];
+      }
+      const uint32_t h_lo = pack_bf16(sc[i][0], sc[i][1]), h_hi = pack_bf16(sc[i][2], sc[i][3]);
+      ph[i][0] = transpose_8x8(h_lo);
+      ph[i][1] = transpose_8x8(h_hi);
+      plo[i][0] = transpose_8x8(pack_bf16(sc[i][0] - bf16_lo(h_lo), sc[i][1] - bf16_hi(h_lo)));
+      plo[i][1] = transpose_8x8(pack_bf16(sc[i][2] - bf16_lo(h_hi), sc[i][3] - bf16_hi(h_hi)));
+    }
+  };
   int seg = 0;                                             // segments finished: the phase of the merge barriers
   load_q(rs.req);                                          // on its way beside the first stages
   int next_s = 0, next_turn = 0;
   uint32_t phase = 0;
+  // Direct: a warp takes NT neighbouring tiles of a unit; the page ids of its tokens (one a lane) are
+  // read two units ahead and their rows one unit ahead.
+  constexpr int KI = kDirect ? D / 32 : 1;
+  uint4 kn[2 * NT][KI], vn[2 * NT][KI];                    // [token g + 8 ..][features 32 i + 8 t ..]
+  UnitWalk wi{rs.req, rs.tok, rs.n, rs.units, true}, wc = wi;   // of the page ids, of the products
+  uint32_t mask_next = 0;
+  int2 id = make_int2(-1, -1);
+  bool no_token = true;
+  const auto read_ids = [&] {
+    id = make_int2(-1, -1);
+    no_token = true;
+    if (wi.left == 0) return;
+    const int j = wi.tok + share * NT * kTile + lane;
+    if (lane < NT * kTile && j < wi.n) {
+      no_token = false;
+      id = reinterpret_cast<const int2*>(a.table)[((int64_t)wi.req * a.max_len + j) * a.layers + a.layer];
+    }
+    wi.tok += st;
+    --wi.left;
+    walk_begin(a, wi);
+  };
+  const auto read_rows = [&] {
+    const bool good = id.x >= 0 && id.x < a.num_pages && id.y >= 0 && id.y < a.num_pages;
+    if (!good && !no_token) flag_error(a.err, LORA_DEV_BAD_PAGE);   // token skipped
+    mask_next = __ballot_sync(0xffffffffu, good);
+    const uint16_t* rows = a.pool + (h0 + hh) * D + 8 * t;
+#pragma unroll
+    for (int h = 0; h < 2 * NT; ++h) {
+      const int pk = __shfl_sync(0xffffffffu, id.x, g + 8 * h), pv = __shfl_sync(0xffffffffu, id.y, g + 8 * h);
+      const bool has = (mask_next >> (g + 8 * h)) & 1u;
+      const uint4* kp = reinterpret_cast<const uint4*>(rows + (int64_t)pk * a.H);
+      const uint4* vp = reinterpret_cast<const uint4*>(rows + (int64_t)pv * a.H);
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        kn[h][i] = has ? kp[4 * i] : make_uint4(0, 0, 0, 0);
+        vn[h][i] = has ? vp[4 * i] : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  if (kDirect) {
+    read_ids();
+    read_rows();
+    read_ids();
+  }
   for (int left = rs.units; left > 0; --left) {
     const int s = next_s;
+    int req, n, flags, tok, next;
+    if constexpr (kDirect) {
+      const uint32_t mask = mask_next;
+      uint4 kc[2 * NT][KI], vc[2 * NT][KI];
+#pragma unroll
+      for (int h = 0; h < 2 * NT; ++h)
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+          kc[h][i] = kn[h][i];
+          vc[h][i] = vn[h][i];
+        }
+      read_rows();
+      read_ids();
+      req = wc.req;
+      n = wc.n;
+      tok = wc.tok;
+      const bool first = wc.first, ends = wc.tok + st >= wc.n;
+      wc.tok += st;
+      --wc.left;
+      wc.first = ends;
+      walk_begin(a, wc);
+      const int begun = req == rs.req ? rs.tok : 0;        // the segment's first token
+      flags = (first ? kFirst : 0) | (ends || wc.left == 0 ? kLast : 0) | (begun == 0 ? kStarts : 0) | (ends ? kEnds : 0);
+      next = wc.left > 0 ? wc.req : -1;
+      if (first) begin_segment();
+      const int j0 = tok + share * NT * kTile;
+      if (j0 < n) {
+        uint32_t ph[HW][NT][2], plo[HW][NT][2];
+#pragma unroll
+        for (int u = 0; u < HW; ++u) {
+          float sc[NT][4], odd[NT][4];
+#pragma unroll
+          for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[b][i] = odd[b][i] = 0.f;
+#pragma unroll
+          for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int i = 0; i < KI; ++i) {
+              const uint4 &x = kc[2 * b][i], &y = kc[2 * b + 1][i];
+              const uint32_t k0[4] = {x.x, y.x, x.y, y.y}, k1[4] = {x.z, y.z, x.w, y.w};
+              mma_16x8x16(sc[b], k0, qf[u][2 * i][0], qf[u][2 * i][1]);
+              mma_16x8x16(odd[b], k1, qf[u][2 * i + 1][0], qf[u][2 * i + 1][1]);
+            }
+          tile_weights(u, req, j0, n, mask, sc, odd, ph[u], plo[u]);
+        }
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+          for (int i = 0; i < KI; ++i) {
+            const uint4 &x = vc[2 * b][i], &y = vc[2 * b + 1][i];
+            const uint32_t v0[4] = {transpose_8x8(x.x), transpose_8x8(x.y), transpose_8x8(y.x), transpose_8x8(y.y)};
+            const uint32_t v1[4] = {transpose_8x8(x.z), transpose_8x8(x.w), transpose_8x8(y.z), transpose_8x8(y.w)};
+#pragma unroll
+            for (int u = 0; u < HW; ++u) {
+              mma_16x8x16(acc[u][2 * i], v0, ph[u][b][0], ph[u][b][1]);
+              mma_16x8x16(acc[u][2 * i + 1], v1, ph[u][b][0], ph[u][b][1]);
+              mma_16x8x16(acc[u][2 * i], v0, plo[u][b][0], plo[u][b][1]);
+              mma_16x8x16(acc[u][2 * i + 1], v1, plo[u][b][0], plo[u][b][1]);
+            }
+          }
+      }
+    } else {
     if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, phase))) {
       if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
       return;
@@ -467,17 +667,13 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
     }
     const bool mine = next_turn == turn;
     if (++next_turn == turns) next_turn = 0;
-    const int req = info[s].req, n = info[s].n, flags = info[s].flags, tok = info[s].tok, next = info[s].next;
+    req = info[s].req;
+    n = info[s].n;
+    flags = info[s].flags;
+    tok = info[s].tok;
+    next = info[s].next;
     __syncwarp();
-    if (flags & kFirst) {
-#pragma unroll
-      for (int u = 0; u < HW; ++u) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) acc[u][ks][0] = acc[u][ks][1] = acc[u][ks][2] = acc[u][ks][3] = 0.f;
-        m[u][0] = m[u][1] = -INFINITY;
-        l[u][0] = l[u][1] = 0.f;
-      }
-    }
+    if (flags & kFirst) begin_segment();
     if (!mine && lane == 0) mbar_arrive(bar_empty + 8 * s);
     for (int tile = mine ? share % tile_sharers : TILES; tile < TILES; tile += tile_sharers) {
       const int j0 = tok + tile * kTile;
@@ -495,16 +691,16 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
         if (u >= n_mine) break;
         const bool release = final_tile && u + 1 == n_mine;
         const uint32_t base = ring + (uint32_t)s * pl.stage_bytes + (uint32_t)(tile * kTile) * RB + u * head_step;
-        float sc[4], odd[4];
+        float sc[NT][4], odd[NT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[i] = odd[i] = 0.f;
+        for (int i = 0; i < 4; ++i) sc[0][i] = odd[0][i] = 0.f;
 #pragma unroll
         for (int k0 = 0; k0 < KS; k0 += 4) {
           uint32_t kf[4][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) ldmatrix_x4(kf[k], base + k_lane + (k0 + k) * 32);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_16x8x16(k & 1 ? odd : sc, kf[k], qf[u][k0 + k][0], qf[u][k0 + k][1]);
+          for (int k = 0; k < 4; ++k) mma_16x8x16(k & 1 ? odd[0] : sc[0], kf[k], qf[u][k0 + k][0], qf[u][k0 + k][1]);
         }
         uint32_t vf[VR][4];
 #pragma unroll
@@ -513,58 +709,8 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_empty + 8 * s);
         }
-        const bool v0 = (mask >> g) & 1u, v1 = (mask >> (g + 8)) & 1u;
-        uint32_t ph[2], plo[2];
-        sc[0] = v0 ? (sc[0] + odd[0]) * a.scale_log2 : -INFINITY;
-        sc[1] = v0 ? (sc[1] + odd[1]) * a.scale_log2 : -INFINITY;
-        sc[2] = v1 ? (sc[2] + odd[2]) * a.scale_log2 : -INFINITY;
-        sc[3] = v1 ? (sc[3] + odd[3]) * a.scale_log2 : -INFINITY;
-        if (a.ws_scores) {
-          float* dst = a.ws_scores + ((int64_t)req * a.n_heads + head_of(u) + 2 * t) * a.score_stride + j0 + g;
-          if (2 * t < G) {
-            dst[0] = sc[0];
-            dst[8] = sc[2];
-          }
-          if (2 * t + 1 < G) {
-            dst[a.score_stride] = sc[1];
-            dst[a.score_stride + 8] = sc[3];
-          }
-        }
-        const float x0 = fmaxf(sc[0], sc[2]), x1 = fmaxf(sc[1], sc[3]);
-        if (__any_sync(0xffffffffu, x0 > m[u][0] + kMaxSlack || x1 > m[u][1] + kMaxSlack)) {
-          float x[2] = {x0, x1};
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) x[k] = fmaxf(x[k], __shfl_xor_sync(0xffffffffu, x[k], o));
-          float c[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float mn = fmaxf(m[u][k], x[k]);
-            c[k] = mn == -INFINITY ? 0.f : exp2f(m[u][k] - mn);   // no score above -infinity yet: nothing to keep
-            l[u][k] *= c[k];
-            m[u][k] = mn;
-          }
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            acc[u][ks][0] *= c[0];
-            acc[u][ks][1] *= c[1];
-            acc[u][ks][2] *= c[0];
-            acc[u][ks][3] *= c[1];
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float ms = m[u][k] == -INFINITY ? 0.f : m[u][k];   // no score above -infinity yet: every weight 0
-          sc[k] = exp2f(sc[k] - ms);
-          sc[2 + k] = exp2f(sc[2 + k] - ms);
-          l[u][k] += sc[k] + sc[2 + k];
-        }
-        const uint32_t h_lo = pack_bf16(sc[0], sc[1]), h_hi = pack_bf16(sc[2], sc[3]);
-        ph[0] = transpose_8x8(h_lo);
-        ph[1] = transpose_8x8(h_hi);
-        plo[0] = transpose_8x8(pack_bf16(sc[0] - bf16_lo(h_lo), sc[1] - bf16_hi(h_lo)));
-        plo[1] = transpose_8x8(pack_bf16(sc[2] - bf16_lo(h_hi), sc[3] - bf16_hi(h_hi)));
+        uint32_t ph[NT][2], plo[NT][2];
+        tile_weights(u, req, j0, n, mask, sc, odd, ph, plo);
         // V of a token without data is whatever the stage held before: its bits are cleared.
         const bool partial = mask != 0xFFFFu;
         const uint32_t b0 = mask >> (2 * t), b1 = mask >> (2 * t + 8);
@@ -586,15 +732,16 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
             }
           }
 #pragma unroll
-          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], ph[0], ph[1]);
+          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], ph[0][0], ph[0][1]);
 #pragma unroll
-          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], plo[0], plo[1]);
+          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], plo[0][0], plo[0][1]);
         }
         if (VR < KS && release) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_empty + 8 * s);
         }
       }
+    }
     }
     if (!(flags & kLast)) continue;
 
@@ -608,8 +755,8 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
         l[u][k] += __shfl_xor_sync(0xffffffffu, l[u][k], 8);
         l[u][k] += __shfl_xor_sync(0xffffffffu, l[u][k], 16);
       }
-    if (HW == 1 && pl.sharers > 1) {
-      float* mb = merge + (size_t)hw * 8 * (D + 2);        // [8][D + 2]: acc, m, l
+    if ((kDirect || HW == 1) && pl.sharers > 1) {
+      float* merged = merge + (size_t)hw * HW * 8 * (D + 2);   // [HW][8][D + 2]: acc, m, l
       // One buffer per head, used by its warps in turn: warp `share` writes it once the warp before
       // (or, for the first, the last of the previous segment) has been added, and share 0 adds it.
       for (int o = 1; o < pl.sharers; ++o) {
@@ -622,17 +769,18 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
             return;
           }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int qi = 2 * t + k;
-            if (qi >= G) continue;
+          for (int uk = 0; uk < 2 * HW; ++uk) {
+            const int u = uk / 2, k = uk & 1, qi = 2 * t + k;
+            float* mb = merged + (size_t)u * 8 * (D + 2);
+            if (qi >= n_query(u)) continue;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-              mb[qi * (D + 2) + ks * 16 + g] = acc[0][ks][k];
-              mb[qi * (D + 2) + ks * 16 + g + 8] = acc[0][ks][2 + k];
+              mb[qi * (D + 2) + ks * 16 + g] = acc[u][ks][k];
+              mb[qi * (D + 2) + ks * 16 + g + 8] = acc[u][ks][2 + k];
             }
             if (g == 0) {
-              mb[qi * (D + 2) + D] = m[0][k];
-              mb[qi * (D + 2) + D + 1] = l[0][k];
+              mb[qi * (D + 2) + D] = m[u][k];
+              mb[qi * (D + 2) + D + 1] = l[u][k];
             }
           }
           __syncwarp();
@@ -643,18 +791,19 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
             return;
           }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int qi = 2 * t + k;
-            if (qi >= G) continue;
+          for (int uk = 0; uk < 2 * HW; ++uk) {
+            const int u = uk / 2, k = uk & 1, qi = 2 * t + k;
+            float* mb = merged + (size_t)u * 8 * (D + 2);
+            if (qi >= n_query(u)) continue;
             const float om = mb[qi * (D + 2) + D], ol = mb[qi * (D + 2) + D + 1];
-            const float mn = fmaxf(m[0][k], om), ms = mn == -INFINITY ? 0.f : mn;
-            const float c0 = exp2f(m[0][k] - ms), c1 = exp2f(om - ms);
-            m[0][k] = mn;
-            l[0][k] = l[0][k] * c0 + ol * c1;
+            const float mn = fmaxf(m[u][k], om), ms = mn == -INFINITY ? 0.f : mn;
+            const float c0 = exp2f(m[u][k] - ms), c1 = exp2f(om - ms);
+            m[u][k] = mn;
+            l[u][k] = l[u][k] * c0 + ol * c1;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-              acc[0][ks][k] = acc[0][ks][k] * c0 + mb[qi * (D + 2) + ks * 16 + g] * c1;
-              acc[0][ks][2 + k] = acc[0][ks][2 + k] * c0 + mb[qi * (D + 2) + ks * 16 + g + 8] * c1;
+              acc[u][ks][k] = acc[u][ks][k] * c0 + mb[qi * (D + 2) + ks * 16 + g] * c1;
+              acc[u][ks][2 + k] = acc[u][ks][2 + k] * c0 + mb[qi * (D + 2) + ks * 16 + g + 8] * c1;
             }
           }
           __syncwarp();
@@ -672,17 +821,17 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
 #pragma unroll
     for (int u = 0; u < HW; ++u) {
       if (u >= n_mine) break;
-      const int head0 = head_of(u);
+      const int head0 = head_of(u), G = n_query(u);
       if (starts && ends) {
         const float i0 = l[u][0] == 0.f ? 0.f : 1.f / l[u][0], i1 = l[u][1] == 0.f ? 0.f : 1.f / l[u][1];
-        uint16_t* row = a.out + req * a.out_stride + (int64_t)(head0 + g) * D + 2 * t;
+        uint16_t* row = a.out + req * a.out_stride + (int64_t)(head0 + g) * D;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const uint32_t lo = transpose_8x8(pack_bf16(acc[u][ks][0] * i0, acc[u][ks][1] * i1));
           const uint32_t hi = transpose_8x8(pack_bf16(acc[u][ks][2] * i0, acc[u][ks][3] * i1));
           if (g < G) {
-            *reinterpret_cast<uint32_t*>(row + ks * 16) = lo;
-            *reinterpret_cast<uint32_t*>(row + ks * 16 + 8) = hi;
+            *reinterpret_cast<uint32_t*>(row + pair_of(ks, 0)) = lo;
+            *reinterpret_cast<uint32_t*>(row + pair_of(ks, 1)) = hi;
           }
         }
 #pragma unroll
@@ -703,8 +852,8 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
           float* dst = a.ws_acc + (slot + qi) * D;
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
-            dst[ks * 16 + g] = acc[u][ks][k];
-            dst[ks * 16 + g + 8] = acc[u][ks][2 + k];
+            dst[row_of(ks, 0)] = acc[u][ks][k];
+            dst[row_of(ks, 1)] = acc[u][ks][2 + k];
           }
           if (g == 0) a.ws_ml[slot + qi] = make_float2(m[u][k], l[u][k]);
         }
@@ -939,12 +1088,14 @@ SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads,
   pl.n_kv = n_kv;
   pl.D = H / n_kv;
   pl.group = n_heads / n_kv;
-  // A warp has 8 query heads of one KV head, or of two of 64 (so that a slice stays 1 KB); head groups
-  // as even as they can be, a stage's K and V within kStageBytes at 16 tokens; with fewer heads than
-  // warps some warps share a head's tokens and the stage has more of them.
-  pl.octets = (pl.group + 7) / 8;
+  // Direct: a warp has one KV head, with all its query heads at D = 64 and 8 of them at D = 128.
+  // Else a warp has 8 query heads of one KV head, or of two of 64 (so that a slice stays 1 KB); head
+  // groups as even as they can be, a stage's K and V within kStageBytes at 16 tokens; with fewer heads
+  // than warps some warps share a head's tokens and the stage has more of them.
+  pl.direct = pl.D <= 128 && H * 2 <= kDirectSlice;
+  pl.octets = pl.direct && pl.D == 64 ? 1 : (pl.group + 7) / 8;
   const int slots = kWarps / pl.octets, room_heads = std::max(1, kStageBytes / (4 * kTile * pl.D));
-  const int most = std::min(pl.D == 64 ? 2 * slots : slots, room_heads);
+  const int most = std::min(pl.D == 64 && !pl.direct ? 2 * slots : slots, room_heads);
   pl.n_groups = (n_kv + most - 1) / most;
   pl.heads = (n_kv + pl.n_groups - 1) / pl.n_groups;
   pl.head_slots = std::min(pl.heads, slots);
@@ -952,12 +1103,13 @@ SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads,
   pl.sharers = slots / pl.head_slots;                      // a power of two where it is not 1, as is room then
   pl.tile_sharers = std::min(pl.sharers, room);
   pl.tiles = std::min(room / pl.tile_sharers, kMaxTiles / pl.tile_sharers) * pl.tile_sharers;
+  if (pl.direct) pl.tiles = pl.sharers * (128 / pl.D);     // a unit: so many tiles per warp
   pl.row_bytes = pl.heads * pl.D * 2 + 16;                 // + 16: ldmatrix's 8 rows on 8 bank groups
-  pl.stage_bytes = 2 * kTile * pl.tiles * pl.row_bytes;
+  pl.stage_bytes = pl.direct ? 0 : 2 * kTile * pl.tiles * pl.row_bytes;
   // behind the ring: the sums of find_range (4 bytes per 128 requests), later the merged heads
-  const int merge = pl.sharers > 1 ? pl.head_slots * pl.octets * 8 * (pl.D + 2) * 4 : 0;
+  const int merge = pl.sharers > 1 ? pl.head_slots * ((pl.group + 7) / 8) * 8 * (pl.D + 2) * 4 : 0;
   const int tail = std::max(merge, (n_req + 127) / 128 * 4);
-  pl.stages = std::min(kMaxStages, (kMaxSmem - kStaticSmem - tail) / pl.stage_bytes);
+  pl.stages = pl.direct ? 0 : std::min(kMaxStages, (kMaxSmem - kStaticSmem - tail) / pl.stage_bytes);
   pl.smem = pl.stages * pl.stage_bytes + tail;
   const int sms = device_sm_count() * kCtasPerSm;
   // One CTA per request and head group, and no join, where a request is at most four tiles and all
@@ -1014,6 +1166,8 @@ int launch_split(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
 int launch_split_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   const SplitPlan& pl = a.plan;
   const bool two = pl.whole || pl.heads * pl.D * 2 < kSmallSlice, pairs = pl.heads > pl.head_slots;
+  if (pl.direct && pl.D == 128) return launch_split<128, 1, 0, 1>(p, a, st);
+  if (pl.direct) return pl.group > 8 ? launch_split<64, 2, 0, 2>(p, a, st) : launch_split<64, 2, 0, 1>(p, a, st);
   switch (pl.D * 16 + pl.tiles) {
     case 64 * 16 + 1: return two ? launch_split<64, 1, 2, 2>(p, a, st) : launch_split<64, 1, 1, 2>(p, a, st);
     case 64 * 16 + 2: return pairs ? launch_split<64, 2, 2, 2>(p, a, st) : launch_split<64, 2, 2, 1>(p, a, st);

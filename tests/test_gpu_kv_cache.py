@@ -112,6 +112,18 @@ SHAPES = [   # n_kv, G, D, layers, lengths
     (8, 2, 64, 1, [60, 33]),
     (4, 3, 256, 1, [17, 61, 48]),
     (1, 1, 128, 1, [61, 2]),
+    (1, 16, 64, 1, [5000, 33, 31]),     # rows of up to 384 bytes: tiles of one head on four warps, two or one
+    (1, 9, 64, 2, [129, 0, 127, 16, 17, 128]),
+    (2, 3, 64, 1, [1, 0, 700, 64, 63, 65]),
+    (2, 12, 64, 1, [300] * 30),
+    (3, 1, 64, 1, [31, 33, 6000]),
+    (3, 16, 64, 1, [32, 0, 900]),
+    (1, 7, 128, 2, [64, 65, 2000, 0, 63]),
+    (1, 16, 128, 1, [1, 47, 3000]),
+    (1, 10, 64, 1, [61, 1, 32, 33, 0, 17]),   # whole requests of such rows
+    (3, 2, 64, 1, [5, 61, 0]),
+    (1, 12, 128, 1, [60, 17, 0, 48]),
+    (1, 3, 64, 1, [3, 0, 90] * 100),
     (3, 2, 128, 1, [129] * 130),        # more than 128 requests: the range search goes through shared memory
 ]
 
@@ -212,23 +224,24 @@ def test_attention_split_far_scores(L, scale, shift):
         c.close()
 
 
-def test_attention_split_skips_bad_pages_and_clamps_lengths(L):
+@pytest.mark.parametrize("n_kv,G,D", [(2, 2, 128), (1, 9, 64), (3, 2, 64), (1, 3, 128)])
+def test_attention_split_skips_bad_pages_and_clamps_lengths(L, n_kv, G, D):
     import torch
-    n_kv, G, D, lengths = 2, 2, 128, [50, 3, 20]
-    c = Cache(L, 256, 1, lengths, seed=4)
+    lengths, n_heads, width = [50, 3, 20], n_kv * G, n_kv * G * D
+    c = Cache(L, n_kv * D, 1, lengths, seed=4)
     try:
         tabs = c.tables(0)
         drop = {0: [0, 17, 49], 1: [0, 1, 2], 2: []}
         for r, js in drop.items():
             for i, j in enumerate(js):
                 c.table[r, j, 0, i % 2] = (1 << 30) if i != 1 else -5
-        q_bits = workloads.to_bf16_bits(c.rng.standard_normal((3, 512)).astype(np.float32))
+        q_bits = workloads.to_bf16_bits(c.rng.standard_normal((3, width)).astype(np.float32))
         keep = [np.setdiff1d(np.arange(n), drop[r]) for r, n in enumerate(lengths)]
-        ref = O.attention_split(c.bits, [tabs[r][keep[r]] for r in range(3)], q_bits, 4, 2)
-        q, out = bits_to_torch(q_bits), torch.empty((3, 512), dtype=torch.bfloat16, device="cuda")
-        lse, w = torch.empty((3, 4), device="cuda"), torch.full((3, c.max_len), 5.0, device="cuda")
-        ws, nb = c.workspace(4, 2, True)
-        args = (c.pool, 3, c.table, c.seq, c.max_len, 1, 0, q, out, 4, 2, ws, nb)
+        ref = O.attention_split(c.bits, [tabs[r][keep[r]] for r in range(3)], q_bits, n_heads, n_kv)
+        q, out = bits_to_torch(q_bits), torch.empty((3, width), dtype=torch.bfloat16, device="cuda")
+        lse, w = torch.empty((3, n_heads), device="cuda"), torch.full((3, c.max_len), 5.0, device="cuda")
+        ws, nb = c.workspace(n_heads, n_kv, True)
+        args = (c.pool, 3, c.table, c.seq, c.max_len, 1, 0, q, out, n_heads, n_kv, ws, nb)
         L.lora_attention_split(*args, lse_dev=lse, weight_out_dev=w)
         with pytest.raises(L.LoraError) as e:
             L.lora_status(c.pool)
@@ -238,7 +251,7 @@ def test_attention_split_skips_bad_pages_and_clamps_lengths(L):
         for r, js in drop.items():
             assert (got[r, js] == 0).all()
         _check_weights(ref, np.stack([np.pad(got[r, keep[r]], (0, c.max_len - len(keep[r]))) for r in range(3)]), None,
-                       [len(k) for k in keep], D, G, 4)
+                       [len(k) for k in keep], D, G, n_heads)
         # lengths outside [0, max_len]: reported and clamped
         c.seq.copy_(torch.tensor([-3, 3, 20], dtype=torch.int32))
         L.lora_attention_split(*args, lse_dev=lse)
