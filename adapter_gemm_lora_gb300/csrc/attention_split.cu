@@ -58,7 +58,8 @@ constexpr int kStageBytes = 32 * 1024;              // K and V of a stage, at mo
 constexpr int kMaxStages = 8;
 constexpr int kMaxSmem = (228 * 1024 / kCtasPerSm - 1024) & ~1023;   // a CTA's share, 1 KB of it reserved
 constexpr int kStaticSmem = 1024;                   // barriers and stage records
-constexpr int kJoinWarps = 4;
+constexpr int kFewWarps = 4, kManyWarps = 8;        // of a block of the join
+constexpr int kJoinMany = 32;                       // partials per request from which a join is spread wider
 constexpr int kJoinUnit = 64;                       // tokens whose weights a block takes at a time
 
 // How a call is cut: fixed by the shapes, the same for the size query and the launch.
@@ -279,6 +280,11 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
 // 1/16 of the MMA in use at one query head, and the running maximum, sum and rescaling of a column
 // stay in the lanes that hold the column in both products.  P^T is the transpose of S^T's
 // fragment (movmatrix) as two bf16 terms, hi + lo, so the weights carry 16 mantissa bits.
+// Direct (NP = 0): no ring and no producer.  A lane loads 16 bytes (8 features) of its token's row at a
+// time, and the products take the features in that order: K's registers are the first product's
+// fragments as they come (q is read in the same order), V's are transposed (movmatrix) into the
+// second's.  Page ids are two tiles ahead of the products and rows one, so a warp has 8 KB on its way;
+// with half of that (one tile of 64 features) one KV head of 64 took 41 us instead of 34.9.
 // A tile's K and V fragments are all in registers before its softmax starts (at D = 256 the second
 // half of V follows it), and the stage is given back then: the chain of a tile (products, shuffles,
 // exponentials) holds up no copy.
@@ -904,6 +910,38 @@ __device__ __forceinline__ void join_partials(const SplitArgs& a, int p0, int p1
   }
 }
 
+// The same of 32 features, d0 + lane, for many partials: 16 of them at a time, a lane with the m and l
+// of one and all the lane's loads in flight together.
+template <int D>
+__device__ __forceinline__ void join_many(const SplitArgs& a, int p0, int p1, int first, int step, int h, int d0, int lane,
+                                          float& m, float& l, float& acc) {
+  m = -INFINITY;
+  l = acc = 0.f;
+  for (int i0 = p0 + first; i0 <= p1; i0 += 16 * step) {
+    const int mine = i0 + (lane & 15) * step;
+    const float2 ml = mine <= p1 ? a.ws_ml[partial_slot(mine, mine == p0) * a.n_heads + h] : make_float2(-INFINITY, 0.f);
+    float x[16];
+#pragma unroll
+    for (int b = 0; b < 16; ++b) {
+      const int i = i0 + b * step;
+      x[b] = i <= p1 ? a.ws_acc[(partial_slot(i, i == p0) * a.n_heads + h) * D + d0 + lane] : 0.f;
+    }
+    float mn = ml.x;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mn = fmaxf(mn, m);
+    const float ms = mn == -INFINITY ? 0.f : mn, c = exp2f(m - ms), f = exp2f(ml.x - ms);
+    m = mn;
+    float add = ml.y * f;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+    l = fmaf(l, c, add);
+    acc *= c;
+#pragma unroll
+    for (int b = 0; b < 16; ++b) acc = fmaf(x[b], __shfl_sync(0xffffffffu, f, b), acc);
+  }
+}
+
 __device__ __forceinline__ void store_lse(const SplitArgs& a, int r, int h, float m, float l) {
   if (a.lse) a.lse[(int64_t)r * a.n_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
@@ -911,16 +949,18 @@ __device__ __forceinline__ void store_lse(const SplitArgs& a, int r, int h, floa
 // Joins the requests that span ranges, and turns scores into weights: latency-bound, 4.5 us for a
 // join alone, 10 us with the weights of 68,000 tokens x 32 heads (17 MB of scores read).
 // Join: a request that spans ranges p0..p1 is the one in whose middle each of p0 + 1..p1 begins, so
-// those ranges' blocks find it at once and share its query heads (up to kJoinWarps partials a warp
-// per head, beyond that a block per head).
+// those ranges' blocks find it at once and share its query heads: up to JW partials a warp per head,
+// beyond that a block per head, from kJoinMany on (JW = kManyWarps) a block per 32 features of one.
 // Weights: the blocks cut the tokens of all requests anew into equal ranges.  Per request a block
 // gathers the heads' lse (of a split request from its partials); then a lane of every warp takes two
-// of 64 tokens, warp w every kJoinWarps-th head, and the warps' sums are added in warp order.
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
+// of 64 tokens, warp w every JW-th head, and the warps' sums are added in warp order.
+// Registers are held to what lets 40 (or 32) warps share an SM, also with the split kernel's last blocks:
+// at 60 instead of 48 one request of 8 KV heads of 128 with 4 query heads each took 15.2 us, not 11.9.
+template <int D, int JW>
+__global__ void __launch_bounds__(32 * JW, (JW == kFewWarps && D < 256 ? 40 : 32) / JW) attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
   extern __shared__ float dyn[];                           // with weights: [n_heads] lse, the sums of find_range
-  __shared__ float part[kJoinWarps][D + 2];
-  __shared__ __align__(8) float sums[2 * kJoinWarps * kJoinUnit];
+  __shared__ float part[JW][D + 2];
+  __shared__ __align__(8) float sums[2 * JW * kJoinUnit];
   constexpr int E = D / 32;
   pdl_wait_then_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -930,13 +970,40 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
     if (w.y > 0) {
       const int r = w.x;
       const int2 range = make_int2(w.z, w.w);
-      const bool wide = range.y - range.x >= kJoinWarps;
+      const bool wide = range.y - range.x >= JW;
       const int block = (p - range.x - 1) * subs + sub, blocks = (range.y - range.x) * subs;
       uint16_t* row = a.out + r * a.out_stride;
-      if (wide) {
+      if (JW > kFewWarps && range.y - range.x >= kJoinMany) {
+        for (int item = block; item < a.n_heads * E; item += blocks) {
+          const int h = item / E, d0 = item % E * 32;
+          float m, l, acc;
+          join_many<D>(a, range.x, range.y, warp, JW, h, d0, lane, m, l, acc);
+          __syncthreads();
+          part[warp][lane] = acc;
+          if (lane == 0) {
+            part[warp][D] = m;
+            part[warp][D + 1] = l;
+          }
+          __syncthreads();
+          if (warp == 0) {
+            float M = -INFINITY, L = 0.f, x = 0.f;
+#pragma unroll
+            for (int v = 0; v < JW; ++v) M = fmaxf(M, part[v][D]);
+            const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int v = 0; v < JW; ++v) {
+              const float c = exp2f(part[v][D] - ms);
+              L = fmaf(part[v][D + 1], c, L);
+              x = fmaf(part[v][lane], c, x);
+            }
+            row[(int64_t)h * D + d0 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(L == 0.f ? 0.f : x * (1.f / L)));
+            if (d0 == 0 && lane == 0) store_lse(a, r, h, M, L);
+          }
+        }
+      } else if (wide) {
         for (int h = block; h < a.n_heads; h += blocks) {
           float m, l, acc[E];
-          join_partials<D>(a, range.x, range.y, warp, kJoinWarps, h, lane, m, l, acc);
+          join_partials<D>(a, range.x, range.y, warp, JW, h, lane, m, l, acc);
           __syncthreads();
 #pragma unroll
           for (int e = 0; e < E; ++e) part[warp][e * 32 + lane] = acc[e];
@@ -945,26 +1012,26 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
             part[warp][D + 1] = l;
           }
           __syncthreads();
-          float M = -INFINITY, L = 0.f, c[kJoinWarps];
+          float M = -INFINITY, L = 0.f, c[JW];
 #pragma unroll
-          for (int v = 0; v < kJoinWarps; ++v) M = fmaxf(M, part[v][D]);
+          for (int v = 0; v < JW; ++v) M = fmaxf(M, part[v][D]);
           const float ms = M == -INFINITY ? 0.f : M;
 #pragma unroll
-          for (int v = 0; v < kJoinWarps; ++v) {
+          for (int v = 0; v < JW; ++v) {
             c[v] = exp2f(part[v][D] - ms);
             L = fmaf(part[v][D + 1], c[v], L);
           }
           const float inv = L == 0.f ? 0.f : 1.f / L;
-          for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
+          for (int d = threadIdx.x; d < D; d += 32 * JW) {
             float x = 0.f;
 #pragma unroll
-            for (int v = 0; v < kJoinWarps; ++v) x = fmaf(part[v][d], c[v], x);
+            for (int v = 0; v < JW; ++v) x = fmaf(part[v][d], c[v], x);
             row[(int64_t)h * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(x * inv));
           }
           if (threadIdx.x == 0) store_lse(a, r, h, M, L);
         }
       } else {
-        for (int h = block * kJoinWarps + warp; h < a.n_heads; h += blocks * kJoinWarps) {
+        for (int h = block * JW + warp; h < a.n_heads; h += blocks * JW) {
           float m, l, acc[E];
           join_partials<D>(a, range.x, range.y, 0, 1, h, lane, m, l, acc);
           const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -992,19 +1059,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
     const int2 range = a.ws_range[r];
     __syncthreads();                                       // lse_s and part are done with
     if (range.x == range.y) {
-      for (int h = threadIdx.x; h < a.n_heads; h += 32 * kJoinWarps) {
+      for (int h = threadIdx.x; h < a.n_heads; h += 32 * JW) {
         const float z = a.ws_lse[(int64_t)r * a.n_heads + h];
         lse_s[h] = z == -INFINITY ? INFINITY : z;          // a row without weight: 2^(s - inf) = 0
       }
     } else {
-      for (int h0 = 0; h0 < a.n_heads; h0 += 32) {         // 32 heads a lane each, the partials over the warps
-        const int h = min(h0 + lane, a.n_heads - 1);
+      // up to 32 heads, a lane each, the partials over the warps and over what lanes are left
+      const int side = JW == kFewWarps || a.n_heads > 16 ? 32 : a.n_heads > 8 ? 16 : a.n_heads > 4 ? 8 : 4, rows = JW * (32 / side);
+      for (int h0 = 0; h0 < a.n_heads; h0 += 32) {
+        const int h = min(h0 + lane % side, a.n_heads - 1);
         float M = -INFINITY, L = 0.f;
-        for (int i0 = range.x + warp; i0 <= range.y; i0 += 8 * kJoinWarps) {
+        for (int i0 = range.x + warp * (32 / side) + lane / side; i0 <= range.y; i0 += 8 * rows) {
           float2 ml[8];
 #pragma unroll
           for (int b = 0; b < 8; ++b) {
-            const int i = i0 + b * kJoinWarps;
+            const int i = i0 + b * rows;
             ml[b] = i <= range.y ? a.ws_ml[partial_slot(i, i == range.x) * a.n_heads + h] : make_float2(-INFINITY, 0.f);
           }
           float mn = M;
@@ -1016,6 +1085,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
 #pragma unroll
           for (int b = 0; b < 8; ++b) L = fmaf(ml[b].y, exp2f(ml[b].x - ms), L);
         }
+        for (int o = side; o < 32; o <<= 1) {
+          const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+          const float mn = fmaxf(M, m2), ms = mn == -INFINITY ? 0.f : mn;
+          L = L * exp2f(M - ms) + l2 * exp2f(m2 - ms);
+          M = mn;
+        }
         __syncthreads();
         part[warp][2 * lane] = M;
         part[warp][2 * lane + 1] = L;
@@ -1023,10 +1098,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
         if (warp == 0 && h0 + lane < a.n_heads) {
           float m = -INFINITY, l = 0.f;
 #pragma unroll
-          for (int v = 0; v < kJoinWarps; ++v) m = fmaxf(m, part[v][2 * lane]);
+          for (int v = 0; v < JW; ++v) m = fmaxf(m, part[v][2 * lane]);
           const float ms = m == -INFINITY ? 0.f : m;
 #pragma unroll
-          for (int v = 0; v < kJoinWarps; ++v) l = fmaf(part[v][2 * lane + 1], exp2f(part[v][2 * lane] - ms), l);
+          for (int v = 0; v < JW; ++v) l = fmaf(part[v][2 * lane + 1], exp2f(part[v][2 * lane] - ms), l);
           lse_s[h] = l == 0.f ? INFINITY : m + log2f(l);
         }
       }
@@ -1039,13 +1114,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
       if (j < n) {
         const float* sc = a.ws_scores + (int64_t)r * a.n_heads * a.score_stride + j;
 #pragma unroll 8
-        for (int h = warp; h < a.n_heads; h += kJoinWarps) {
+        for (int h = warp; h < a.n_heads; h += JW) {
           const float2 v = *reinterpret_cast<const float2*>(sc + h * a.score_stride);
           x0 += exp2f(v.x - lse_s[h]);
           x1 += exp2f(v.y - lse_s[h]);
         }
       }
-      float* sum = sums + (u & 1) * kJoinWarps * kJoinUnit;                // two buffers: one barrier a turn
+      float* sum = sums + (u & 1) * JW * kJoinUnit;                // two buffers: one barrier a turn
       sum[warp * kJoinUnit + 2 * lane] = x0;
       sum[warp * kJoinUnit + 2 * lane + 1] = x1;
       __syncthreads();
@@ -1053,7 +1128,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
       if (threadIdx.x < kJoinUnit && jt < n) {
         float x = 0.f;
 #pragma unroll
-        for (int v = 0; v < kJoinWarps; ++v) x += sum[v * kJoinUnit + threadIdx.x];
+        for (int v = 0; v < JW; ++v) x += sum[v * kJoinUnit + threadIdx.x];
         const int64_t at = r * a.weight_stride + jt;
         a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.f) + x;
       }
@@ -1182,14 +1257,26 @@ int launch_split_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   return lora_fail(LORA_EINVAL, "lora_attention_split: no kernel for this geometry");
 }
 
-template <int D>
+template <int D, int JW>
 int launch_join(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
-  const int subs = std::max(1, 8 * device_sm_count() / a.plan.parts);   // about eight blocks per SM
+  const int subs = std::max(1, 32 / JW * device_sm_count() / a.plan.parts);   // 32 warps per SM
   const size_t smem = a.weight_out ? (size_t)(a.n_heads + (a.n_req + 127) / 128) * 4 : 0;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
-  const cudaError_t e = launch_pdl(!p->prof_on, attention_join_kernel<D>, dim3(a.plan.parts * subs), dim3(32 * kJoinWarps),
+  const cudaError_t e = launch_pdl(!p->prof_on, attention_join_kernel<D, JW>, dim3(a.plan.parts * subs), dim3(32 * JW),
                                    smem, st, a, subs);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_attention_split launch");
+}
+
+template <int D>
+int launch_join_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
+  // Few heads with many partials each leave most blocks of four warps without a head, so a block of
+  // eight warps takes 32 features of a head.  One GB300, 8 MB of K and V, us a call by few / many warps:
+  // one request (304 partials a head) of 1 head of 64 17.7 / 11.2, of 2 KV heads of 256 with 16 query
+  // heads each 23.8 / 15.7; 4 requests (76) of 1 head, 32 MB, 16.4 / 14.9.  With more heads the blocks
+  // are busy: one request (152) of 128 heads of 128 11.4 / 13.6, with weights 20.3 / 24.9.
+  const int64_t per = std::max(kJoinMany, 8 * a.n_heads);
+  const bool many = !a.plan.whole && a.plan.parts >= per * a.n_req;
+  return many ? launch_join<D, kManyWarps>(p, a, st) : launch_join<D, kFewWarps>(p, a, st);
 }
 
 }  // namespace
@@ -1272,5 +1359,5 @@ extern "C" int lora_attention_split(lora_pool* p, int32_t n_req, const int32_t* 
   a.err = p->d_err;
   const int rc2 = launch_split_any(p, a, st);
   if (rc2 != LORA_OK || (pl.whole && !weight_out)) return rc2;
-  return pl.D == 64 ? launch_join<64>(p, a, st) : pl.D == 128 ? launch_join<128>(p, a, st) : launch_join<256>(p, a, st);
+  return pl.D == 64 ? launch_join_any<64>(p, a, st) : pl.D == 128 ? launch_join_any<128>(p, a, st) : launch_join_any<256>(p, a, st);
 }

@@ -124,6 +124,10 @@ SHAPES = [   # n_kv, G, D, layers, lengths
     (3, 2, 64, 1, [5, 61, 0]),
     (1, 12, 128, 1, [60, 17, 0, 48]),
     (1, 3, 64, 1, [3, 0, 90] * 100),
+    (2, 16, 256, 1, [9000]),            # few heads with many partials each
+    (1, 2, 128, 1, [7000, 40]),
+    (5, 1, 64, 1, [0, 5000, 0]),
+    (1, 3, 256, 1, [2600]),
     (3, 2, 128, 1, [129] * 130),        # more than 128 requests: the range search goes through shared memory
 ]
 
