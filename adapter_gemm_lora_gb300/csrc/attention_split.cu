@@ -45,6 +45,7 @@ constexpr int kSmallSlice = 1024;
 // of 64 93 / 58.5, three 107 / 94; but four 107 / 131, and at D = 128 two 106 / 106, four 196 / 204
 // (eight heads of 64 197 / 311).  Short calls: 8 x 2,000 tokens of one head of 64 11.7 / 8.0.
 constexpr int kDirectSlice = 384;
+constexpr int64_t kTogetherBytes = 384 << 20;       // the cache's size, by max_len
 constexpr int threads_of(int producers) { return 32 * (kWarps + producers); }
 constexpr int kCtasPerSm = 2;
 constexpr int kTile = 16;                           // tokens a warp takes at a time
@@ -74,7 +75,8 @@ struct SplitPlan {
   int32_t stages;
   int32_t parts;                 // ranges the token sequence is cut into
   bool whole;                    // one range per request: nothing to join
-  bool direct;                   // the consumers read the rows themselves, a tile of a unit each
+  bool direct;                   // the consumers read the rows themselves
+  bool pair, meet;               // direct: a warp has both KV heads of 64; the heads' warps wait for one another
   int32_t row_bytes, stage_bytes, smem;
 };
 
@@ -309,6 +311,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   const int g0 = blockIdx.x % pl.n_groups, p = blockIdx.x / pl.n_groups;
   const int h0 = g0 * pl.heads, n_act = min(pl.heads, pl.n_kv - h0);
   constexpr bool kDirect = NP == 0;
+  constexpr bool kPair = kDirect && HW * TILES * D < 256 && HW == 2;   // direct, two KV heads of 64 a warp
   const int st = kDirect ? kTile * pl.tiles : kTile * TILES;
   const int S = pl.stages;
   const uint32_t ring = smem_u32(smem), RB = pl.row_bytes;
@@ -445,12 +448,12 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   const int head_warps = pl.head_slots * pl.octets, hw = warp % head_warps, share = warp / head_warps;
   const int hh = hw / pl.octets, octet = hw % pl.octets;
   if (share >= pl.sharers || hh >= n_act || rs.units == 0) return;
-  // HW = 2: two KV heads, hh and hh + head_slots, or (direct) one with up to 16 query heads.
+  // HW = 2: two KV heads, hh and hh + head_slots, or (direct, not kPair) one with up to 16 query heads.
   const int n_mine = kDirect ? HW : HW == 1 || hh + pl.head_slots >= n_act ? 1 : 2;
   const int g = lane >> 2, t = lane & 3;
-  const auto n_query = [&](int u) { return min(8, pl.group - 8 * (kDirect ? octet + u : octet)); };
+  const auto n_query = [&](int u) { return min(8, pl.group - 8 * (kDirect && !kPair ? octet + u : octet)); };
   const auto head_of = [&](int u) {
-    return kDirect ? (h0 + hh) * pl.group + 8 * (octet + u) : (h0 + hh + u * pl.head_slots) * pl.group + 8 * octet;
+    return kDirect && !kPair ? (h0 + hh) * pl.group + 8 * (octet + u) : (h0 + hh + u * pl.head_slots) * pl.group + 8 * octet;
   };
   uint32_t qf[HW][KS][2];
   float acc[HW][KS][4], m[HW][2], l[HW][2];
@@ -552,11 +555,12 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
   };
   int seg = 0;                                             // segments finished: the phase of the merge barriers
   load_q(rs.req);                                          // on its way beside the first stages
+  bool broken = false;                                     // a wait ran out
   int next_s = 0, next_turn = 0;
   uint32_t phase = 0;
   // Direct: a warp takes NT neighbouring tiles of a unit; the page ids of its tokens (one a lane) are
   // read two units ahead and their rows one unit ahead.
-  constexpr int KI = kDirect ? D / 32 : 1;
+  constexpr int KH = D / 32, KI = kPair ? 2 * KH : kDirect ? KH : 1;
   uint4 kn[2 * NT][KI], vn[2 * NT][KI];                    // [token g + 8 ..][features 32 i + 8 t ..]
   UnitWalk wi{rs.req, rs.tok, rs.n, rs.units, true}, wc = wi;   // of the page ids, of the products
   uint32_t mask_next = 0;
@@ -611,6 +615,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
           kc[h][i] = kn[h][i];
           vc[h][i] = vn[h][i];
         }
+      if (pl.meet) asm volatile("bar.sync %0, %1;" ::"r"(1 + share), "r"(32 * head_warps) : "memory");
       read_rows();
       read_ids();
       req = wc.req;
@@ -638,8 +643,9 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
 #pragma unroll
           for (int b = 0; b < NT; ++b)
 #pragma unroll
-            for (int i = 0; i < KI; ++i) {
-              const uint4 &x = kc[2 * b][i], &y = kc[2 * b + 1][i];
+            for (int i = 0; i < KH; ++i) {
+              const int c = kPair ? KH * u + i : i;
+              const uint4 &x = kc[2 * b][c], &y = kc[2 * b + 1][c];
               const uint32_t k0[4] = {x.x, y.x, x.y, y.y}, k1[4] = {x.z, y.z, x.w, y.w};
               mma_16x8x16(sc[b], k0, qf[u][2 * i][0], qf[u][2 * i][1]);
               mma_16x8x16(odd[b], k1, qf[u][2 * i + 1][0], qf[u][2 * i + 1][1]);
@@ -655,10 +661,12 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
             const uint32_t v1[4] = {transpose_8x8(x.z), transpose_8x8(x.w), transpose_8x8(y.z), transpose_8x8(y.w)};
 #pragma unroll
             for (int u = 0; u < HW; ++u) {
-              mma_16x8x16(acc[u][2 * i], v0, ph[u][b][0], ph[u][b][1]);
-              mma_16x8x16(acc[u][2 * i + 1], v1, ph[u][b][0], ph[u][b][1]);
-              mma_16x8x16(acc[u][2 * i], v0, plo[u][b][0], plo[u][b][1]);
-              mma_16x8x16(acc[u][2 * i + 1], v1, plo[u][b][0], plo[u][b][1]);
+              if (kPair && u != i / KH) continue;
+              const int ks = 2 * (i % KH);
+              mma_16x8x16(acc[u][ks], v0, ph[u][b][0], ph[u][b][1]);
+              mma_16x8x16(acc[u][ks + 1], v1, ph[u][b][0], ph[u][b][1]);
+              mma_16x8x16(acc[u][ks], v0, plo[u][b][0], plo[u][b][1]);
+              mma_16x8x16(acc[u][ks + 1], v1, plo[u][b][0], plo[u][b][1]);
             }
           }
       }
@@ -762,17 +770,20 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
         l[u][k] += __shfl_xor_sync(0xffffffffu, l[u][k], 16);
       }
     if ((kDirect || HW == 1) && pl.sharers > 1) {
-      float* merged = merge + (size_t)hw * HW * 8 * (D + 2);   // [HW][8][D + 2]: acc, m, l
-      // One buffer per head, used by its warps in turn: warp `share` writes it once the warp before
-      // (or, for the first, the last of the previous segment) has been added, and share 0 adds it.
-      for (int o = 1; o < pl.sharers; ++o) {
+      constexpr int kMerged = HW * 8 * (D + 2);            // [HW][8][D + 2]: acc, m, l
+      // Share 0 adds the other warps' parts in order.  One buffer per head, used by its warps in turn:
+      // warp `share` writes it once the warp before (or, for the first, the last of the previous segment)
+      // has been added.  Direct, where shared memory is free, every warp has its own.
+      for (int o = 1; o < pl.sharers && !broken; ++o) {
         const uint32_t ready = bar_ready + 8 * (o * head_warps + hw);
+        float* merged = merge + (size_t)(kDirect ? (o - 1) * head_warps + hw : hw) * kMerged;
         if (share == o) {
-          const int before = o > 1 ? o - 1 : pl.sharers - 1;
-          const uint32_t parity = o > 1 ? seg & 1 : (seg & 1) ^ 1;
+          const int before = kDirect ? o : o > 1 ? o - 1 : pl.sharers - 1;
+          const uint32_t parity = kDirect || o == 1 ? (seg & 1) ^ 1 : seg & 1;
           if (!__all_sync(0xffffffffu, mbar_wait(bar_done + 8 * (before * head_warps + hw), parity))) {
             if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
-            return;
+            broken = true;
+            break;
           }
 #pragma unroll
           for (int uk = 0; uk < 2 * HW; ++uk) {
@@ -794,7 +805,8 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
         } else if (share == 0) {
           if (!__all_sync(0xffffffffu, mbar_wait(ready, seg & 1))) {
             if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
-            return;
+            broken = true;
+            break;
           }
 #pragma unroll
           for (int uk = 0; uk < 2 * HW; ++uk) {
@@ -817,7 +829,8 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
         }
       }
       ++seg;
-      if (share != 0) continue;
+      if (broken && !kDirect) return;                      // direct: the other warps wait at a barrier
+      if (share != 0 || broken) continue;
     }
     const bool starts = flags & kStarts, ends = flags & kEnds;
     if (g0 == 0 && hw == 0 && lane == 0) {
@@ -1168,21 +1181,28 @@ SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads,
   // groups as even as they can be, a stage's K and V within kStageBytes at 16 tokens; with fewer heads
   // than warps some warps share a head's tokens and the stage has more of them.
   pl.direct = pl.D <= 128 && H * 2 <= kDirectSlice;
+  // In a large cache the heads of a token have to be read together, or each read opens a DRAM row anew:
+  // two heads of 64 by one warp, else by warps that wait for one another.  64 requests, us without /
+  // with, one query head per KV head: two heads of 64, 1 GB 242 / 165 (the warps waiting: 216), 512 MB
+  // 95.5 / 88.3, 256 MB 49.8 / 49.6, 2 MB 4.8 / 6.2; three heads, 1 GB 226 / 203, 128 MB 31.6 / 33.2.
+  const bool together = pl.direct && (int64_t)n_req * max_len * 4 * H >= kTogetherBytes;
+  pl.pair = together && pl.D == 64 && n_kv == 2 && pl.group <= 8;
   pl.octets = pl.direct && pl.D == 64 ? 1 : (pl.group + 7) / 8;
   const int slots = kWarps / pl.octets, room_heads = std::max(1, kStageBytes / (4 * kTile * pl.D));
   const int most = std::min(pl.D == 64 && !pl.direct ? 2 * slots : slots, room_heads);
   pl.n_groups = (n_kv + most - 1) / most;
   pl.heads = (n_kv + pl.n_groups - 1) / pl.n_groups;
-  pl.head_slots = std::min(pl.heads, slots);
+  pl.head_slots = pl.pair ? 1 : std::min(pl.heads, slots);
+  pl.meet = together && pl.head_slots > 1;
   const int room = kStageBytes / (4 * kTile * pl.heads * pl.D);
   pl.sharers = slots / pl.head_slots;                      // a power of two where it is not 1, as is room then
   pl.tile_sharers = std::min(pl.sharers, room);
   pl.tiles = std::min(room / pl.tile_sharers, kMaxTiles / pl.tile_sharers) * pl.tile_sharers;
-  if (pl.direct) pl.tiles = pl.sharers * (128 / pl.D);     // a unit: so many tiles per warp
+  if (pl.direct) pl.tiles = pl.sharers * (pl.pair ? 1 : 128 / pl.D);     // a unit: so many tiles per warp
   pl.row_bytes = pl.heads * pl.D * 2 + 16;                 // + 16: ldmatrix's 8 rows on 8 bank groups
   pl.stage_bytes = pl.direct ? 0 : 2 * kTile * pl.tiles * pl.row_bytes;
   // behind the ring: the sums of find_range (4 bytes per 128 requests), later the merged heads
-  const int merge = pl.sharers > 1 ? pl.head_slots * ((pl.group + 7) / 8) * 8 * (pl.D + 2) * 4 : 0;
+  const int merge = pl.sharers > 1 ? (pl.direct ? (pl.sharers - 1) * pl.heads : pl.heads) * ((pl.group + 7) / 8) * 8 * (pl.D + 2) * 4 : 0;
   const int tail = std::max(merge, (n_req + 127) / 128 * 4);
   pl.stages = pl.direct ? 0 : std::min(kMaxStages, (kMaxSmem - kStaticSmem - tail) / pl.stage_bytes);
   pl.smem = pl.stages * pl.stage_bytes + tail;
@@ -1242,6 +1262,7 @@ int launch_split_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   const SplitPlan& pl = a.plan;
   const bool two = pl.whole || pl.heads * pl.D * 2 < kSmallSlice, pairs = pl.heads > pl.head_slots;
   if (pl.direct && pl.D == 128) return launch_split<128, 1, 0, 1>(p, a, st);
+  if (pl.pair) return launch_split<64, 1, 0, 2>(p, a, st);
   if (pl.direct) return pl.group > 8 ? launch_split<64, 2, 0, 2>(p, a, st) : launch_split<64, 2, 0, 1>(p, a, st);
   switch (pl.D * 16 + pl.tiles) {
     case 64 * 16 + 1: return two ? launch_split<64, 1, 2, 2>(p, a, st) : launch_split<64, 1, 1, 2>(p, a, st);

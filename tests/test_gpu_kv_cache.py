@@ -167,6 +167,41 @@ def test_attention_split_matches_the_oracle(L, n_kv, G, D, layers, lengths):
         c.close()
 
 
+@pytest.mark.parametrize("n_kv,G,lengths", [
+    (2, 1, [300, 0, 1, 33]), (2, 8, [16, 2000, 64, 65]), (2, 9, [100, 31]), (3, 1, [900, 17, 0]), (3, 16, [5, 128]),
+])
+def test_attention_split_of_a_large_cache_with_short_requests(L, n_kv, G, lengths):
+    """max_len says that the cache is large, so that heads of 64 are read together."""
+    import torch
+    D = 64
+    n_heads, H, n_req = n_kv * G, 64 * n_kv, len(lengths)
+    max_len = (400 << 20) // (4 * H * n_req) + 1
+    c = Cache(L, H, 1, lengths, seed=H + G, max_len=max_len)
+    try:
+        tabs = c.tables(0)
+        c.table[0, 3, 0, 1] = c.num_pages                      # a bad page: its token is skipped
+        keep = np.setdiff1d(np.arange(lengths[0]), [3])
+        q_bits = workloads.to_bf16_bits(c.rng.standard_normal((n_req, n_heads * D)).astype(np.float32))
+        ref = O.attention_split(c.bits, [tabs[0][keep]] + tabs[1:], q_bits, n_heads, n_kv)
+        q = bits_to_torch(q_bits)
+        out = torch.full_like(q, float("nan"))
+        lse = torch.full((n_req, n_heads), float("nan"), device="cuda")
+        w = torch.zeros((n_req, max_len), device="cuda")
+        ws, nb = c.workspace(n_heads, n_kv, True)
+        L.lora_attention_split(c.pool, n_req, c.table, c.seq, max_len, 1, 0, q, out, n_heads, n_kv, ws, nb, lse_dev=lse,
+                               weight_out_dev=w)
+        with pytest.raises(L.LoraError) as e:
+            L.lora_status(c.pool)
+        assert e.value.code == L.LORA_EDEVICE
+        n_tok = [len(keep)] + lengths[1:]
+        _check(ref, out, lse, n_tok, D, G)
+        got = w[:, :max(lengths)].cpu().numpy().astype(np.float64)
+        got[0, :len(keep)] = got[0, keep]
+        _check_weights(ref, got, None, n_tok, D, G, n_heads)
+    finally:
+        c.close()
+
+
 def test_attention_split_strides_in_place_weights_and_no_lse(L):
     import torch
     n_kv, G, D, lengths = 4, 2, 64, [100, 0, 333, 16]
