@@ -7,11 +7,11 @@
 //
 // HBM-bound: every cached token's K and V rows (2 x 2 H bytes) are read once, against 4 H G flops.
 // One GB300: 256 requests of 128 to 2,048 tokens at H = 5120 825 us (7.1 TB/s, 1.06 of the copy rate:
-// reads alone pass what a copy reaches), one request of 131,072 tokens at H = 4096 309 us (6.9 TB/s),
-// 64 requests with weights 182 us (0.92), 33 requests of up to 515 tokens 18.9 us (0.45: 3 us to the
+// reads alone pass what a copy reaches), one request of 131,072 tokens at H = 4096 308 us (6.9 TB/s),
+// 64 requests with weights 181 us (0.93), 33 requests of up to 515 tokens 18.3 us (0.46: 3 us to the
 // first data, 3 us of join).
 //
-// Split.  The tokens of all requests, in units of one ring stage, form one sequence that is cut
+// Split.  The tokens of all requests, in units of one ring stage (or one turn of the warps), form one sequence that is cut
 // into P equal ranges; a CTA takes one range for one group of KV heads.  A request inside one range
 // is finished there; one that spans ranges leaves a partial (m, l, sum exp2(s - m) V) per range,
 // and the second kernel joins them: m = max m_i, l = sum l_i 2^(m_i - m), out likewise.  So the
@@ -61,6 +61,7 @@ constexpr int kMaxSmem = (228 * 1024 / kCtasPerSm - 1024) & ~1023;   // a CTA's 
 constexpr int kStaticSmem = 1024;                   // barriers and stage records
 constexpr int kFewWarps = 4, kManyWarps = 8;        // of a block of the join
 constexpr int kJoinMany = 32;                       // partials per request from which a join is spread wider
+constexpr int kWarpHeads = 8;                       // up to so many heads a warp adds its tokens' weights alone
 constexpr int kJoinUnit = 64;                       // tokens whose weights a block takes at a time
 
 // How a call is cut: fixed by the shapes, the same for the size query and the launch.
@@ -269,7 +270,7 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
   }
 }
 
-// One CTA per (group of KV heads, range).  The last warp fills a ring of stages: per stage and
+// One CTA per (group of KV heads, range).  NP producer warps fill a ring of stages: per stage and
 // token the group's slice of the K row and of the V row (heads x D contiguous bf16) by
 // cp.async.bulk, all against the stage's one mbarrier; page ids are read one stage ahead.  A
 // consumer warp owns up to 8 query heads of one KV head, or of two of 64, and the stages' 16-token
@@ -295,9 +296,9 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
 // copy: with a loop over up to eight tiles, seven of them unused, the batch above took 1,203 us, with
 // the tile count fixed at compile time 840 us; without the consumers' arithmetic 826 us.
 // More than 8 query heads per KV head take two warps a head, each with 8 of them and its own read of
-// the head's K and V from shared memory (4 x 40,000 tokens with 16 query heads per KV head: 0.89 of
-// the copy rate at D = 128, 0.94 at 256; one warp with two column tiles, whose accumulators spilled:
-// 0.76 and 0.45).
+// the head's K and V from shared memory: 4 x 40,000 tokens of H = 1024 with 16 query heads per KV head
+// 116 us at D = 128 and at 256, join included (0.84 of the copy rate; 8 query heads 108 us).  One warp
+// with two column tiles, whose accumulators spilled, reached 0.76 and 0.45.
 template <int D, int TILES, int NP, int HW>
 __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_kernel(const __grid_constant__ SplitArgs a) {
   constexpr int KS = D / 16;
@@ -966,7 +967,9 @@ __device__ __forceinline__ void store_lse(const SplitArgs& a, int r, int h, floa
 // beyond that a block per head, from kJoinMany on (JW = kManyWarps) a block per 32 features of one.
 // Weights: the blocks cut the tokens of all requests anew into equal ranges.  Per request a block
 // gathers the heads' lse (of a split request from its partials); then a lane of every warp takes two
-// of 64 tokens, warp w every JW-th head, and the warps' sums are added in warp order.
+// of 64 tokens, warp w every JW-th head, and the warps' sums are added in warp order.  With few heads
+// every warp has tokens of its own instead and nothing to wait for: 64 requests of 8,000 to 15,625
+// tokens of one head of 64 57 -> 48 us with the attention, but 32 heads of 128 46.6 -> 50.8.
 // Registers are held to what lets 40 (or 32) warps share an SM, also with the split kernel's last blocks:
 // at 60 instead of 48 one request of 8 KV heads of 128 with 4 query heads each took 15.2 us, not 11.9.
 template <int D, int JW>
@@ -1120,12 +1123,31 @@ __global__ void __launch_bounds__(32 * JW, (JW == kFewWarps && D < 256 ? 40 : 32
       }
     }
     __syncthreads();
+    // two neighbouring tokens a lane; a score row is padded to whole tiles, so the pair is there
+    const float* row = a.ws_scores + (int64_t)r * a.n_heads * a.score_stride;
+    if (a.n_heads <= kWarpHeads) {                         // a warp takes all heads of its tokens
+      for (int u = warp; u < units; u += JW) {
+        const int64_t j = tok + (int64_t)u * kJoinUnit + 2 * lane;
+        if (j >= n) continue;
+        const int64_t at = r * a.weight_stride + j;
+        const bool two = j + 1 < n;
+        float x0 = 0.f, x1 = 0.f;
+        const float w0 = a.weight_in ? a.weight_in[at] : 0.f, w1 = a.weight_in && two ? a.weight_in[at + 1] : 0.f;
+#pragma unroll 8
+        for (int h = 0; h < a.n_heads; ++h) {
+          const float2 v = *reinterpret_cast<const float2*>(row + j + h * a.score_stride);
+          x0 += exp2f(v.x - lse_s[h]);
+          x1 += exp2f(v.y - lse_s[h]);
+        }
+        a.weight_out[at] = w0 + x0;
+        if (two) a.weight_out[at + 1] = w1 + x1;
+      }
+    } else {
     for (int u = 0; u < units; ++u) {
-      // two neighbouring tokens a lane; a score row is padded to whole tiles, so the pair is there
       const int64_t j = tok + (int64_t)u * kJoinUnit + 2 * lane;
       float x0 = 0.f, x1 = 0.f;
       if (j < n) {
-        const float* sc = a.ws_scores + (int64_t)r * a.n_heads * a.score_stride + j;
+        const float* sc = row + j;
 #pragma unroll 8
         for (int h = warp; h < a.n_heads; h += JW) {
           const float2 v = *reinterpret_cast<const float2*>(sc + h * a.score_stride);
@@ -1145,6 +1167,7 @@ __global__ void __launch_bounds__(32 * JW, (JW == kFewWarps && D < 256 ? 40 : 32
         const int64_t at = r * a.weight_stride + jt;
         a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.f) + x;
       }
+    }
     }
     left -= units;
     tok = (int)min((int64_t)n, tok + (int64_t)units * kJoinUnit);

@@ -128,6 +128,9 @@ SHAPES = [   # n_kv, G, D, layers, lengths
     (1, 2, 128, 1, [7000, 40]),
     (5, 1, 64, 1, [0, 5000, 0]),
     (1, 3, 256, 1, [2600]),
+    (1, 8, 256, 2, [700, 63, 0, 65]),   # eight and nine heads: tokens' weights by a warp, by all
+    (3, 3, 128, 1, [1, 127, 700]),
+    (2, 4, 128, 1, [2 * 64 + 1] * 40),
     (3, 2, 128, 1, [129] * 130),        # more than 128 requests: the range search goes through shared memory
 ]
 
