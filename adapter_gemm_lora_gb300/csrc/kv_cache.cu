@@ -209,57 +209,39 @@ __device__ __forceinline__ int2 cluster_load2(uint32_t addr) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// kRowWarps warps per row: 4, so that a CTA has four rows, or all 16; with kCluster a cluster of
-// `n_cta` CTAs has one row, and every CTA adds up all CTAs' histograms (integer sums: the order does
-// not matter), which also tell it how many keys the CTAs before it keep.  Every warp takes a
-// contiguous part of the row, the keys of 32 K weights held in registers (longer parts are read
-// again in every pass), so the kept tokens are numbered with one exchange of counts.  Their positions
-// go to a list in shared memory first, and the outputs are written from there, 32 neighbours at a time.
-// Four rows a CTA: layers of one request are neighbours, and the page table [token][layer] is
-// compacted for the four together, so that four lanes write a 32-byte sector of which a row by
-// itself would write 8 bytes at a time (64 requests x 40 layers: 39 us, a CTA per row 73 us; copying
-// the four rows' table entries to shared memory beside the selection, to read whole sectors too:
-// 41 us).
+// One row per CTA, or with kCluster per cluster of `n_cta` CTAs, of which every one adds up all CTAs'
+// histograms (integer sums: the order does not matter), which also tell it how many keys the CTAs
+// before it keep.  Every warp takes a contiguous part of the row, the keys of 32 K weights held in
+// registers (longer parts are read again in every pass), so the kept tokens are numbered with one
+// exchange of counts.  Their positions go to a list in shared memory first, and the outputs are
+// written from there, 32 neighbours at a time.
 // A row is a chain of dependent steps (length, weights, two or three digits, counts, pages), so time
 // goes with the chain's length times the rows per SM: the passes are free of branches within
 // kEvictBatch chunks of 32 weights, whose steps overlap.
 constexpr int kEvictBatch = 4;
 
-template <int K, int kRowWarps, bool kCluster>
-__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictArgs a, int32_t n_cta, int32_t keep_cap) {
-  constexpr int kRows = kEvictWarps / kRowWarps;           // rows of a CTA
-  static_assert(!kCluster || kRows == 1, "a cluster shares one row");
+template <int K, bool kCluster>
+__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictArgs a, int32_t n_cta) {
   static_assert(K % kEvictBatch == 0, "whole batches");
+  constexpr int kHists = kCluster ? 2 : 1, kPer = kEvictBins / kEvictThreads;   // bins a thread adds up
+  static_assert(kPer == 2, "the CTAs' histograms are read two bins at a time");
+  // Shared memory: a histogram, of a cluster two in turn (the other CTAs may still read the one
+  // before); the kept list of each warp.
   extern __shared__ __align__(16) int smem_evict[];
-  __shared__ int warp_gt[kEvictWarps], warp_eq[kEvictWarps], keep_n[kRows];
-  __shared__ int found_s[kRows][3];                        // the wanted bin, keys above it, keys in it
+  __shared__ int warp_gt[kEvictWarps], warp_eq[kEvictWarps];
+  __shared__ int found_s[3];                               // the wanted bin, keys above it, keys in it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int slot = warp / kRowWarps, part = warp % kRowWarps, rtid = part * 32 + lane;
-  constexpr int n_thr = 32 * kRowWarps;                    // threads of a row in this CTA
-  constexpr int kHists = kCluster ? 2 : kRows;
-  constexpr int kPer = kEvictBins / n_thr;                 // bins a thread adds up: 8 or 2
-  static_assert(kPer * n_thr == kEvictBins && (!kCluster || kPer == 2), "the CTAs' histograms are read two bins at a time");
-  // Shared memory: a histogram per row, of a cluster two in turn (the other CTAs may still read the
-  // one before); the kept lists, of a row (four rows a CTA, keep_cap each) or of a warp (32 K each).
-  int* hist = smem_evict + slot * kEvictBins;
-  int* lists = smem_evict + kHists * kEvictBins;
+  int* hist = smem_evict;
   for (int i = tid; i < kEvictBins * kHists / 4; i += kEvictThreads)
     reinterpret_cast<int4*>(smem_evict)[i] = make_int4(0, 0, 0, 0);
-  const auto row_sync = [&] {
-    if (kRows == 1) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "n"(n_thr) : "memory");
-  };
   pdl_wait_then_release();
-  const int rows = a.n_req * a.layers, rank = kCluster ? (int)cluster_rank() : 0;
-  const int id = kCluster ? blockIdx.x / n_cta : blockIdx.x * kRows + slot;
-  const bool live = id < rows;                             // the last CTA may have rows to spare
-  EvictRow e{};
-  if (live) e = evict_row(a, id, rtid == 0 && rank == 0);
+  const int rank = kCluster ? (int)cluster_rank() : 0;
+  EvictRow e = evict_row(a, kCluster ? blockIdx.x / n_cta : blockIdx.x, tid == 0 && rank == 0);
   // this CTA's slice of the row, and this warp's part of it (multiples of 32)
   const int per_cta = ((e.n + n_cta - 1) / n_cta + 31) & ~31;
   const int c0 = (int)min((int64_t)e.n, (int64_t)rank * per_cta), c1 = min(e.n, c0 + per_cta);
-  const int per_warp = ((c1 - c0 + kRowWarps - 1) / kRowWarps + 31) & ~31;
-  const int w0 = min(c1, c0 + part * per_warp), w1 = min(c1, w0 + per_warp);
+  const int per_warp = ((c1 - c0 + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+  const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
   const bool held = per_warp <= 32 * K;                    // the part stays in registers
   uint32_t key[K];
   const auto load = [&](int j0) {
@@ -279,7 +261,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   // kept and tied keys of the row before this CTA's slice: all tokens, or the newer ones, or what the
   // digits say
   int pos = e.need >= e.old ? c0 : max(0, c0 - e.old), tied = 0;
-  const bool select = live && e.need > 0 && e.need < e.old;
+  const bool select = e.need > 0 && e.need < e.old;
   if (select) {
     uint32_t prefix = 0, mask = 0;
     int need = e.need;
@@ -306,43 +288,43 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
         cluster_sync_all();
         v[0] = v[1] = 0;
         for (int c = 0; c < n_cta; ++c) {
-          const int2 x = cluster_load2(cluster_addr(hist + 2 * rtid, c));
+          const int2 x = cluster_load2(cluster_addr(hist + 2 * tid, c));
           v[0] += x.x;
           v[1] += x.y;
         }
       } else {
-        row_sync();
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = hist[rtid * kPer + i];
+        for (int i = 0; i < kPer; ++i) v[i] = hist[tid * kPer + i];
       }
       int mine = 0;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) mine += v[i];
       const int incl = warp_scan(mine, lane);
       if (lane == 31) warp_gt[warp] = incl;
-      row_sync();
+      __syncthreads();
       int above = incl - mine;
 #pragma unroll
-      for (int i = 0; i < kRowWarps; ++i) above += i < part ? warp_gt[slot * kRowWarps + i] : 0;
+      for (int i = 0; i < kEvictWarps; ++i) above += i < warp ? warp_gt[i] : 0;
       if (above < need && above + mine >= need) {          // one thread
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           if (above < need && above + v[i] >= need) {
-            found_s[slot][0] = rtid * kPer + i;
-            found_s[slot][1] = above;
-            found_s[slot][2] = v[i];
+            found_s[0] = tid * kPer + i;
+            found_s[1] = above;
+            found_s[2] = v[i];
           }
           above += v[i];
         }
       }
       if (!kCluster) {                                     // this thread's bins have been read by itself alone
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) hist[rtid * kPer + i] = 0;
+        for (int i = 0; i < kPer; ++i) hist[tid * kPer + i] = 0;
       }
-      row_sync();
-      const int bin = found_s[slot][0];
-      need -= found_s[slot][1];
-      const bool whole = found_s[slot][2] == need;         // the whole bin stays
+      __syncthreads();
+      const int bin = found_s[0];
+      need -= found_s[1];
+      const bool whole = found_s[2] == need;               // the whole bin stays
       prefix |= (digit - (uint32_t)bin) << bits;
       mask |= digit << bits;
       e.cut = whole ? prefix - 1 : prefix;
@@ -350,11 +332,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
       if (kCluster) {
         // of the CTAs before this one: the keys above the bin, and those in it
         int gt = 0, in = 0;
-        if (2 * rtid <= bin)
+        if (2 * tid <= bin)
           for (int c = 0; c < rank; ++c) {
-            const int2 x = cluster_load2(cluster_addr(hist + 2 * rtid, c));
-            gt += (2 * rtid < bin ? x.x : 0) + (2 * rtid + 1 < bin ? x.y : 0);
-            in += 2 * rtid == bin ? x.x : 2 * rtid + 1 == bin ? x.y : 0;
+            const int2 x = cluster_load2(cluster_addr(hist + 2 * tid, c));
+            gt += (2 * tid < bin ? x.x : 0) + (2 * tid + 1 < bin ? x.y : 0);
+            in += 2 * tid == bin ? x.x : 2 * tid + 1 == bin ? x.y : 0;
           }
         gt = __reduce_add_sync(0xffffffffu, gt);
         in = __reduce_add_sync(0xffffffffu, in);
@@ -362,10 +344,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
           warp_gt[warp] = gt;
           warp_eq[warp] = in;
         }
-        row_sync();
+        __syncthreads();
         tied = 0;
 #pragma unroll
-        for (int i = 0; i < kRowWarps; ++i) {
+        for (int i = 0; i < kEvictWarps; ++i) {
           pos += warp_gt[i];
           tied += warp_eq[i];
         }
@@ -374,7 +356,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
         hist = smem_evict + ((d & 1) ^ 1) * kEvictBins;
         if (!whole && bits > 0 && d > 0)
           for (int i = tid; i < kEvictBins / 4; i += kEvictThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
-        row_sync();
+        __syncthreads();
       }
       if (whole) break;
     }
@@ -397,23 +379,23 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
-  row_sync();                                              // warp_gt's sums have been read
+  __syncthreads();                                         // warp_gt's sums have been read
   if (lane == 0) {
     warp_gt[warp] = gt;
     warp_eq[warp] = eq;
   }
-  row_sync();
+  __syncthreads();
   // kept and tied of the row before this warp's part
 #pragma unroll
-  for (int i = 0; i < kRowWarps; ++i) {
-    pos += i < part ? warp_gt[slot * kRowWarps + i] : 0;
-    tied += i < part ? warp_eq[slot * kRowWarps + i] : 0;
+  for (int i = 0; i < kEvictWarps; ++i) {
+    pos += i < warp ? warp_gt[i] : 0;
+    tied += i < warp ? warp_eq[i] : 0;
   }
   pos += min(tied, e.ties);
   const uint32_t below = (1u << lane) - 1;
   for (int j0 = w0; j0 < w1; j0 += 32 * K) {
     if (!held) load(j0);
-    int* list = kRows > 1 ? lists + slot * keep_cap + pos : lists + warp * 32 * K;
+    int* list = smem_evict + kHists * kEvictBins + warp * 32 * K;
     int n_kept = 0;
 #pragma unroll
     for (int b0 = 0; b0 < K; b0 += kEvictBatch) {
@@ -455,7 +437,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           x[b] = w[j[b]];
-          if (kRows == 1) pages[b] = t_in[(int64_t)j[b] * a.layers];
+          pages[b] = t_in[(int64_t)j[b] * a.layers];
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
@@ -463,43 +445,217 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
           if (i >= n_out) break;
           keep[i] = j[b];
           w_out[i] = x[b];
-          if (kRows == 1) t_out[(int64_t)i * a.layers] = pages[b];
+          t_out[(int64_t)i * a.layers] = pages[b];
         }
       }
     }
     pos += n_kept;
     __syncwarp();
   }
+  const int step = n_cta * kEvictThreads, first = e.n_keep + rank * kEvictThreads + tid;
+  int32_t* keep = a.keep + e.row * a.budget;
+  float* w_out = a.weight_out + e.row * a.max_len_out;
+  int2* t_out = a.table_out + (int64_t)e.r * a.max_len_out * a.layers + e.layer;
+  for (int i = first; i < a.budget; i += step) keep[i] = -1;
+  for (int i = first; i < a.max_len_out; i += step) {
+    w_out[i] = 0.f;
+    t_out[(int64_t)i * a.layers] = make_int2(-1, -1);
+  }
+  if (e.layer == 0 && rank == 0 && tid == 0) a.new_len[e.r] = e.n_keep;
+  if (kCluster && select) cluster_wait();                  // and no other reads this one's
+}
+
+// Many short rows: four a CTA, four warps each.  Layers of one request are neighbours, and the page
+// table [token][layer] is compacted for the four together, so that four lanes write a 32-byte sector of
+// which a row by itself would write 8 bytes at a time.  The keys stay in shared memory: the first
+// digit is counted while they come in, a warp's kept positions take the place of the keys it has read,
+// and one exchange of counts numbers them.  64 requests x 40 layers of 500 to 2,048 tokens to 1,024:
+// 31 us (a CTA per row 73); with the keys in registers, whose passes are unrolled to the longest row,
+// 39; three CTAs per SM with 40 registers 34, two or three rows a CTA 33 and 32.
+constexpr int kShortRow = 4096;                            // four rows a CTA up to this length
+constexpr int kShortRows = 4, kShortThreads = 128 * kShortRows;
+constexpr int kEvictLoads = 8;                             // weights a lane has on their way
+
+__global__ void __launch_bounds__(kShortThreads, 2) kv_evict_rows_kernel(const EvictArgs a, int32_t cap) {
+  constexpr int kRows = kShortRows, kRowWarps = 4, n_thr = 32 * kRowWarps, kPer = kEvictBins / n_thr;
+  extern __shared__ __align__(16) int smem_evict[];
+  __shared__ int warp_sum[kRows * kRowWarps], found_s[kRows][3];
+  __shared__ int out_s[kRows][kRowWarps], part_s[kRows], keep_s[kRows];   // outputs before a warp's, its part's length
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slot = warp / kRowWarps, part = warp % kRowWarps, rtid = part * 32 + lane;
+  int* hist = smem_evict + slot * kEvictBins;
+  int* keys = smem_evict + kRows * kEvictBins + slot * cap;
+  for (int i = tid; i < kEvictBins * kRows / 4; i += kShortThreads)
+    reinterpret_cast<int4*>(smem_evict)[i] = make_int4(0, 0, 0, 0);
+  const auto row_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "n"(n_thr) : "memory"); };
+  pdl_wait_then_release();
+  const int rows = a.n_req * a.layers, id = blockIdx.x * kRows + slot;
+  const bool live = id < rows;                             // the last CTA may have rows to spare
+  EvictRow e{};
+  if (live) e = evict_row(a, id, rtid == 0);
+  const int per_warp = ((e.n + kRowWarps - 1) / kRowWarps + 31) & ~31;
+  const int w0 = min(e.n, part * per_warp), w1 = min(e.n, w0 + per_warp);
+  const bool select = live && e.need > 0 && e.need < e.old;
+  const float* w = a.weight + e.row * a.max_len;
+  __syncthreads();
+  for (int j0 = w0 + lane; j0 - lane < w1; j0 += 32 * kEvictLoads) {
+    float x[kEvictLoads];
+#pragma unroll
+    for (int b = 0; b < kEvictLoads; ++b) x[b] = j0 + 32 * b < w1 ? w[j0 + 32 * b] : 0.f;
+#pragma unroll
+    for (int b = 0; b < kEvictLoads; ++b) {
+      const int j = j0 + 32 * b;
+      if (j >= w1) continue;
+      const uint32_t k = j >= e.old ? kKeyStays : weight_key(x[b]);
+      keys[j] = (int)k;
+      if (select && k != kKeyStays) atomicAdd(&hist[kEvictBins - 1 - (k >> (32 - kEvictBits))], 1);   // largest first
+    }
+  }
+  const auto key = [&](int j) { return j < w1 ? (uint32_t)keys[j] : kKeyAbsent; };
+  if (select) {
+    uint32_t prefix = 0, mask = 0;
+    int need = e.need;
+    for (int d = 0, bits = 32; bits > 0; ++d) {
+      const int nb = min(kEvictBits, bits);
+      bits -= nb;
+      const uint32_t digit = (1u << nb) - 1;
+      if (d > 0) {
+        for (int j0 = w0 + lane; j0 - lane < w1; j0 += 32 * kEvictBatch) {
+          uint32_t k[kEvictBatch];
+#pragma unroll
+          for (int b = 0; b < kEvictBatch; ++b) k[b] = key(j0 + 32 * b);
+#pragma unroll
+          for (int b = 0; b < kEvictBatch; ++b)
+            if ((k[b] & mask) == prefix) atomicAdd(&hist[digit - ((k[b] >> bits) & digit)], 1);   // the marks match no prefix
+        }
+      }
+      row_sync();
+      // every thread adds up kPer neighbouring bins, and the row's threads find the one they lie in
+      int v[kPer], mine = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; i += 4) {
+        int4* bins = reinterpret_cast<int4*>(hist + rtid * kPer + i);
+        const int4 x = *bins;
+        *bins = make_int4(0, 0, 0, 0);
+        v[i] = x.x;
+        v[i + 1] = x.y;
+        v[i + 2] = x.z;
+        v[i + 3] = x.w;
+        mine += x.x + x.y + x.z + x.w;
+      }
+      const int incl = warp_scan(mine, lane);
+      if (lane == 31) warp_sum[warp] = incl;
+      row_sync();
+      int above = incl - mine;
+#pragma unroll
+      for (int i = 0; i < kRowWarps; ++i) above += i < part ? warp_sum[slot * kRowWarps + i] : 0;
+      if (above < need && above + mine >= need) {          // one thread
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (above < need && above + v[i] >= need) {
+            found_s[slot][0] = rtid * kPer + i;
+            found_s[slot][1] = above;
+            found_s[slot][2] = v[i];
+          }
+          above += v[i];
+        }
+      }
+      row_sync();
+      need -= found_s[slot][1];
+      const bool whole = found_s[slot][2] == need;         // the whole bin stays
+      prefix |= (digit - (uint32_t)found_s[slot][0]) << bits;
+      mask |= digit << bits;
+      e.cut = whole ? prefix - 1 : prefix;
+      e.ties = whole ? 0 : need;
+      if (whole) break;
+    }
+  }
+  int tied = 0;                                            // keys equal to the cut before this warp's part
+  if (e.ties > 0) {
+    int eq = 0;
+    for (int j = w0 + lane; j < w1; j += 32) eq += (uint32_t)keys[j] == e.cut;
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    row_sync();                                            // warp_sum has been read
+    if (lane == 0) warp_sum[warp] = eq;
+    row_sync();
+#pragma unroll
+    for (int i = 0; i < kRowWarps; ++i) tied += i < part ? warp_sum[slot * kRowWarps + i] : 0;
+  }
+  // the kept positions, in place of the keys this warp has read
+  const uint32_t below = (1u << lane) - 1;
+  int* list = keys + w0;
+  int n_kept = 0;
+  for (int j0 = w0 + lane; j0 - lane < w1; j0 += 32 * kEvictBatch) {
+    uint32_t k[kEvictBatch];
+#pragma unroll
+    for (int b = 0; b < kEvictBatch; ++b) k[b] = key(j0 + 32 * b);
+    __syncwarp();
+#pragma unroll
+    for (int b = 0; b < kEvictBatch; ++b) {
+      bool stay = k[b] > e.cut;
+      if (e.ties > 0) {
+        const bool q = k[b] == e.cut;
+        const uint32_t mq = __ballot_sync(0xffffffffu, q);
+        stay = stay || (q && tied + __popc(mq & below) < e.ties);
+        tied += __popc(mq);
+      }
+      const uint32_t ms = __ballot_sync(0xffffffffu, stay);
+      if (stay) list[n_kept + __popc(ms & below)] = j0 + 32 * b;
+      n_kept += __popc(ms);
+    }
+    __syncwarp();
+  }
+  row_sync();                                              // warp_sum has been read
+  if (lane == 0) warp_sum[warp] = n_kept;
+  row_sync();
+  int pos = 0;
+#pragma unroll
+  for (int i = 0; i < kRowWarps; ++i) pos += i < part ? warp_sum[slot * kRowWarps + i] : 0;
+  if (lane == 0) out_s[slot][part] = pos;
+  if (rtid == 0) {
+    part_s[slot] = per_warp;
+    keep_s[slot] = e.n_keep;
+  }
+  __syncthreads();
   if (live) {
-    const int step = n_cta * n_thr, first = e.n_keep + rank * n_thr + rtid;
     int32_t* keep = a.keep + e.row * a.budget;
     float* w_out = a.weight_out + e.row * a.max_len_out;
-    int2* t_out = a.table_out + (int64_t)e.r * a.max_len_out * a.layers + e.layer;
-    for (int i = first; i < a.budget; i += step) keep[i] = -1;
-    for (int i = first; i < a.max_len_out; i += step) {
-      w_out[i] = 0.f;
-      if (kRows == 1) t_out[(int64_t)i * a.layers] = make_int2(-1, -1);
+    const int n_out = min(n_kept, e.n_keep - pos);         // equal; no write passes the row whatever the counts say
+    for (int i0 = lane; i0 < n_out; i0 += 32 * kEvictBatch) {
+      int j[kEvictBatch];
+      float x[kEvictBatch];
+#pragma unroll
+      for (int b = 0; b < kEvictBatch; ++b) j[b] = list[min(i0 + 32 * b, n_out - 1)];
+#pragma unroll
+      for (int b = 0; b < kEvictBatch; ++b) x[b] = w[j[b]];
+#pragma unroll
+      for (int b = 0; b < kEvictBatch; ++b) {
+        if (i0 + 32 * b >= n_out) break;
+        keep[pos + i0 + 32 * b] = j[b];
+        w_out[pos + i0 + 32 * b] = x[b];
+      }
     }
-    if (e.layer == 0 && rank == 0 && rtid == 0) a.new_len[e.r] = e.n_keep;
+    for (int i = e.n_keep + rtid; i < a.budget; i += n_thr) keep[i] = -1;
+    for (int i = e.n_keep + rtid; i < a.max_len_out; i += n_thr) w_out[i] = 0.f;
+    if (e.layer == 0 && rtid == 0) a.new_len[e.r] = e.n_keep;
   }
-  if (kCluster && select) cluster_wait();                  // and no other reads this one's
-  if (kRows == 1) return;
 
   // the page table of the CTA's rows: thread = (position, row), rows fastest
   const int trow = tid % kRows, tid_row = blockIdx.x * kRows + trow;
-  if (rtid == 0) keep_n[slot] = e.n_keep;
-  __syncthreads();
   if (tid_row >= rows) return;
-  const int layer = tid_row % a.layers, r = tid_row / a.layers, n_keep = keep_n[trow];
+  const int layer = tid_row % a.layers, r = tid_row / a.layers, n_keep = keep_s[trow], per = part_s[trow];
+  const int o1 = out_s[trow][1], o2 = out_s[trow][2], o3 = out_s[trow][3];
   const int2* t_in = a.table + (int64_t)r * a.max_len * a.layers + layer;
   int2* t_out = a.table_out + (int64_t)r * a.max_len_out * a.layers + layer;
-  const int* list = lists + trow * keep_cap;
-  constexpr int kStep = kEvictThreads / kRows, kBatch = 8; // positions a pass of the CTA covers, reads in flight
+  const int* kept = smem_evict + kRows * kEvictBins + trow * cap;
+  constexpr int kStep = kShortThreads / kRows, kBatch = 8; // positions a pass of the CTA covers, reads in flight
   for (int i0 = tid / kRows; i0 < n_keep; i0 += kStep * kBatch) {
     int2 pages[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int j = list[min(i0 + kStep * b, n_keep - 1)];
+      const int i = min(i0 + kStep * b, n_keep - 1);
+      const int p = (i >= o1) + (i >= o2) + (i >= o3);     // the warp that kept it
+      const int j = kept[p * per + i - (p == 0 ? 0 : p == 1 ? o1 : p == 2 ? o2 : o3)];
       pages[b] = t_in[(int64_t)j * a.layers];
     }
 #pragma unroll
@@ -511,20 +667,27 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   for (int i = n_keep + tid / kRows; i < a.max_len_out; i += kStep) t_out[(int64_t)i * a.layers] = make_int2(-1, -1);
 }
 
-constexpr int kShortRow = 4096;                            // four rows a CTA up to this length
+int launch_evict_rows(const lora_pool* p, const EvictArgs& a, cudaStream_t st) {
+  const int64_t rows = (int64_t)a.n_req * a.layers;
+  const int cap = (a.max_len + 31) & ~31;
+  static DeviceFlags flags;
+  const int rc = ensure_smem_attr(flags, &kv_evict_rows_kernel, kShortRows * (kEvictBins + kShortRow) * (int)sizeof(int), "lora_kv_evict");
+  if (rc != LORA_OK) return rc;
+  ProfScope prof(p, LORA_KIND_KV, st);
+  const cudaError_t e = launch_pdl(!p->prof_on, kv_evict_rows_kernel, dim3((unsigned)((rows + kShortRows - 1) / kShortRows)), dim3(kShortThreads),
+                                   kShortRows * (size_t)(kEvictBins + cap) * sizeof(int), st, a, (int32_t)cap);
+  return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_kv_evict launch");
+}
 
-template <int K, int kRowWarps, bool kCluster>
+template <int K, bool kCluster>
 int launch_evict(const lora_pool* p, const EvictArgs& a, int n_cta, cudaStream_t st) {
   const int64_t rows = (int64_t)a.n_req * a.layers;
-  constexpr int kRows = kEvictWarps / kRowWarps, kHistWords = (kCluster ? 2 : kRows) * kEvictBins;
-  const int keep_cap = kRows > 1 ? std::min(a.budget, a.max_len) : 0;
-  const int smem = (kHistWords + (kRows > 1 ? kRows * keep_cap : kEvictWarps * 32 * K)) * (int)sizeof(int);
-  constexpr int kMost = (kHistWords + (kRows > 1 ? kRows * kShortRow : kEvictWarps * 32 * K)) * (int)sizeof(int);
+  constexpr int smem = ((kCluster ? 2 : 1) * kEvictBins + kEvictWarps * 32 * K) * (int)sizeof(int);
   static DeviceFlags flags;
-  const int rc = ensure_smem_attr(flags, &kv_evict_kernel<K, kRowWarps, kCluster>, kMost, "lora_kv_evict");
+  const int rc = ensure_smem_attr(flags, &kv_evict_kernel<K, kCluster>, smem, "lora_kv_evict");
   if (rc != LORA_OK) return rc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(kCluster ? rows * n_cta : (rows + kRows - 1) / kRows));
+  cfg.gridDim = dim3((unsigned)(kCluster ? rows * n_cta : rows));
   cfg.blockDim = dim3(kEvictThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -537,21 +700,21 @@ int launch_evict(const lora_pool* p, const EvictArgs& a, int n_cta, cudaStream_t
   cfg.attrs = attr;
   cfg.numAttrs = kCluster ? 2 : 1;
   ProfScope prof(p, LORA_KIND_KV, st);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_kernel<K, kRowWarps, kCluster>, a, (int32_t)n_cta, (int32_t)keep_cap);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_kernel<K, kCluster>, a, (int32_t)n_cta);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_kv_evict launch");
 }
 
-template <int kRowWarps, bool kCluster>
+template <bool kCluster>
 int launch_evict_k(const lora_pool* p, const EvictArgs& a, int n_cta, cudaStream_t st) {
   const int64_t per_cta = (((int64_t)a.max_len + n_cta - 1) / n_cta + 31) / 32 * 32;
-  const int64_t chunks = ((per_cta + kRowWarps - 1) / kRowWarps + 31) / 32;      // of a warp, at most
-  return chunks <= 4    ? launch_evict<4, kRowWarps, kCluster>(p, a, n_cta, st)
-         : chunks <= 8  ? launch_evict<8, kRowWarps, kCluster>(p, a, n_cta, st)
-         : chunks <= 12 ? launch_evict<12, kRowWarps, kCluster>(p, a, n_cta, st)
-         : chunks <= 16 ? launch_evict<16, kRowWarps, kCluster>(p, a, n_cta, st)
-         : chunks <= 20 ? launch_evict<20, kRowWarps, kCluster>(p, a, n_cta, st)
-         : chunks <= 24 ? launch_evict<24, kRowWarps, kCluster>(p, a, n_cta, st)
-                        : launch_evict<32, kRowWarps, kCluster>(p, a, n_cta, st);
+  const int64_t chunks = ((per_cta + kEvictWarps - 1) / kEvictWarps + 31) / 32;      // of a warp, at most
+  return chunks <= 4    ? launch_evict<4, kCluster>(p, a, n_cta, st)
+         : chunks <= 8  ? launch_evict<8, kCluster>(p, a, n_cta, st)
+         : chunks <= 12 ? launch_evict<12, kCluster>(p, a, n_cta, st)
+         : chunks <= 16 ? launch_evict<16, kCluster>(p, a, n_cta, st)
+         : chunks <= 20 ? launch_evict<20, kCluster>(p, a, n_cta, st)
+         : chunks <= 24 ? launch_evict<24, kCluster>(p, a, n_cta, st)
+                        : launch_evict<32, kCluster>(p, a, n_cta, st);
 }
 
 }  // namespace
@@ -637,9 +800,9 @@ extern "C" int lora_kv_evict(lora_pool* p, int32_t n_req, const int32_t* table_d
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t rows = (int64_t)n_req * layers;
   const int sms = device_sm_count();
-  // Four rows a CTA where there are enough to fill the SMs (2,560 rows of up to 2,048 tokens 39 us, a
+  // Four rows a CTA where there are enough to fill the SMs (2,560 rows of up to 2,048 tokens 31 us, a
   // CTA each 73; 40 rows 16.4, a CTA each 12.7).
-  if (max_len <= kShortRow && rows >= 4 * (int64_t)sms) return launch_evict_k<4, false>(p, a, 1, st);
+  if (max_len <= kShortRow && rows >= 4 * (int64_t)sms) return launch_evict_rows(p, a, st);
   // Few rows or long ones.  A CTA's registers hold 16,384 weights; beyond that, and as long as all
   // CTAs run at once and slices stay above 2,048 tokens, a cluster per row (one row of 100,000 tokens
   // 20 us with 8 CTAs, 31 with 4; 32 rows of 131,071 37 us with 8, 45 with 4, 60 with 16).
@@ -647,6 +810,6 @@ extern "C" int lora_kv_evict(lora_pool* p, int32_t n_req, const int32_t* table_d
   while (n_cta < kEvictMaxCluster && max_len / (2 * n_cta) >= 2048 &&
          (max_len / n_cta > 16384 || rows * n_cta <= 2 * (int64_t)sms) && rows * n_cta * 2 <= INT32_MAX)
     n_cta *= 2;
-  return n_cta > 1 ? launch_evict_k<kEvictWarps, true>(p, a, n_cta, st)
-                   : launch_evict_k<kEvictWarps, false>(p, a, 1, st);
+  return n_cta > 1 ? launch_evict_k<true>(p, a, n_cta, st)
+                   : launch_evict_k<false>(p, a, 1, st);
 }
