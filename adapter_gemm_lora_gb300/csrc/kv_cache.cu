@@ -236,7 +236,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
     reinterpret_cast<int4*>(smem_evict)[i] = make_int4(0, 0, 0, 0);
   pdl_wait_then_release();
   const int rank = kCluster ? (int)cluster_rank() : 0;
-  EvictRow e = evict_row(a, kCluster ? blockIdx.x / n_cta : blockIdx.x, tid == 0 && rank == 0);
+  const int id = kCluster ? blockIdx.x / n_cta : blockIdx.x;
+  const bool live = id < a.n_req * a.layers;               // always: the test saves registers (16 x 32 rows of 16,384 117 -> 112 us)
+  EvictRow e{};
+  if (live) e = evict_row(a, id, tid == 0 && rank == 0);
   // this CTA's slice of the row, and this warp's part of it (multiples of 32)
   const int per_cta = ((e.n + n_cta - 1) / n_cta + 31) & ~31;
   const int c0 = (int)min((int64_t)e.n, (int64_t)rank * per_cta), c1 = min(e.n, c0 + per_cta);
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
   // kept and tied keys of the row before this CTA's slice: all tokens, or the newer ones, or what the
   // digits say
   int pos = e.need >= e.old ? c0 : max(0, c0 - e.old), tied = 0;
-  const bool select = e.need > 0 && e.need < e.old;
+  const bool select = live && e.need > 0 && e.need < e.old;
   if (select) {
     uint32_t prefix = 0, mask = 0;
     int need = e.need;
