@@ -149,10 +149,14 @@ def library():
 def _ptr(obj) -> Optional[int]:
     if obj is None:
         return None
+    if obj.__class__ is int:
+        return obj
+    try:
+        return obj.data_ptr()                                  # most arguments are tensors: 0.1 us each
+    except AttributeError:
+        pass
     if isinstance(obj, int):
         return obj
-    if hasattr(obj, "data_ptr"):
-        return obj.data_ptr()
     if isinstance(obj, np.ndarray):
         return obj.ctypes.data
     raise TypeError(f"cannot take a pointer of {type(obj)!r}")
