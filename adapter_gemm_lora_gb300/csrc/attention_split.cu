@@ -54,7 +54,7 @@ constexpr int kTile = 16;                           // tokens a warp takes at a 
 // starts with a vote in place of the shuffles of a maximum: 64 x 10,000 tokens with 16 query heads per
 // KV head, 8 KV heads of 64 283 -> 237 us, 4 of them 151 -> 128; where copies bound it, the same.
 constexpr float kMaxSlack = 8.f;
-constexpr int kMaxTiles = 8;                        // 16-token tiles per stage, at most
+constexpr int kMaxTiles = 2;                        // 16-token tiles per stage, at most
 constexpr int kStageBytes = 32 * 1024;              // K and V of a stage, at most
 constexpr int kMaxStages = 8;
 constexpr int kMaxSmem = (228 * 1024 / kCtasPerSm - 1024) & ~1023;   // a CTA's share, 1 KB of it reserved
@@ -672,91 +672,91 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
           }
       }
     } else {
-    if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, phase))) {
-      if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
-      return;
-    }
-    if (++next_s == S) {
-      next_s = 0;
-      phase ^= 1;
-    }
-    const bool mine = next_turn == turn;
-    if (++next_turn == turns) next_turn = 0;
-    req = info[s].req;
-    n = info[s].n;
-    flags = info[s].flags;
-    tok = info[s].tok;
-    next = info[s].next;
-    __syncwarp();
-    if (flags & kFirst) begin_segment();
-    if (!mine && lane == 0) mbar_arrive(bar_empty + 8 * s);
-    for (int tile = mine ? share % tile_sharers : TILES; tile < TILES; tile += tile_sharers) {
-      const int j0 = tok + tile * kTile;
-      const bool final_tile = tile + tile_sharers >= TILES;
-      if (j0 >= n) {
-        if (final_tile) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_empty + 8 * s);
-        }
-        continue;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, phase))) {
+        if (lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
+        return;
       }
-      const uint32_t mask = info[s].mask[tile];
-#pragma unroll
-      for (int u = 0; u < HW; ++u) {
-        if (u >= n_mine) break;
-        const bool release = final_tile && u + 1 == n_mine;
-        const uint32_t base = ring + (uint32_t)s * pl.stage_bytes + (uint32_t)(tile * kTile) * RB + u * head_step;
-        float sc[NT][4], odd[NT][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[0][i] = odd[0][i] = 0.f;
-#pragma unroll
-        for (int k0 = 0; k0 < KS; k0 += 4) {
-          uint32_t kf[4][4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ldmatrix_x4(kf[k], base + k_lane + (k0 + k) * 32);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma_16x8x16(k & 1 ? odd[0] : sc[0], kf[k], qf[u][k0 + k][0], qf[u][k0 + k][1]);
-        }
-        uint32_t vf[VR][4];
-#pragma unroll
-        for (int k = 0; k < VR; ++k) ldmatrix_x4_trans(vf[k], base + v_lane + k * 32);
-        if (VR == KS && release) {                         // everything of the stage is in registers
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_empty + 8 * s);
-        }
-        uint32_t ph[NT][2], plo[NT][2];
-        tile_weights(u, req, j0, n, mask, sc, odd, ph, plo);
-        // V of a token without data is whatever the stage held before: its bits are cleared.
-        const bool partial = mask != 0xFFFFu;
-        const uint32_t b0 = mask >> (2 * t), b1 = mask >> (2 * t + 8);
-        const uint32_t and0 = ((b0 & 1u) ? 0xFFFFu : 0u) | ((b0 & 2u) ? 0xFFFF0000u : 0u);
-        const uint32_t and1 = ((b1 & 1u) ? 0xFFFFu : 0u) | ((b1 & 2u) ? 0xFFFF0000u : 0u);
-#pragma unroll
-        for (int k0 = 0; k0 < KS; k0 += VR) {
-          if (k0 > 0) {
-#pragma unroll
-            for (int k = 0; k < VR; ++k) ldmatrix_x4_trans(vf[k], base + v_lane + (k0 + k) * 32);
+      if (++next_s == S) {
+        next_s = 0;
+        phase ^= 1;
+      }
+      const bool mine = next_turn == turn;
+      if (++next_turn == turns) next_turn = 0;
+      req = info[s].req;
+      n = info[s].n;
+      flags = info[s].flags;
+      tok = info[s].tok;
+      next = info[s].next;
+      __syncwarp();
+      if (flags & kFirst) begin_segment();
+      if (!mine && lane == 0) mbar_arrive(bar_empty + 8 * s);
+      for (int tile = mine ? share % tile_sharers : TILES; tile < TILES; tile += tile_sharers) {
+        const int j0 = tok + tile * kTile;
+        const bool final_tile = tile + tile_sharers >= TILES;
+        if (j0 >= n) {
+          if (final_tile) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_empty + 8 * s);
           }
-          if (partial) {
+          continue;
+        }
+        const uint32_t mask = info[s].mask[tile];
 #pragma unroll
-            for (int k = 0; k < VR; ++k) {
-              vf[k][0] &= and0;
-              vf[k][1] &= and0;
-              vf[k][2] &= and1;
-              vf[k][3] &= and1;
+        for (int u = 0; u < HW; ++u) {
+          if (u >= n_mine) break;
+          const bool release = final_tile && u + 1 == n_mine;
+          const uint32_t base = ring + (uint32_t)s * pl.stage_bytes + (uint32_t)(tile * kTile) * RB + u * head_step;
+          float sc[NT][4], odd[NT][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[0][i] = odd[0][i] = 0.f;
+#pragma unroll
+          for (int k0 = 0; k0 < KS; k0 += 4) {
+            uint32_t kf[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ldmatrix_x4(kf[k], base + k_lane + (k0 + k) * 32);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_16x8x16(k & 1 ? odd[0] : sc[0], kf[k], qf[u][k0 + k][0], qf[u][k0 + k][1]);
+          }
+          uint32_t vf[VR][4];
+#pragma unroll
+          for (int k = 0; k < VR; ++k) ldmatrix_x4_trans(vf[k], base + v_lane + k * 32);
+          if (VR == KS && release) {                         // everything of the stage is in registers
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+          }
+          uint32_t ph[NT][2], plo[NT][2];
+          tile_weights(u, req, j0, n, mask, sc, odd, ph, plo);
+          // V of a token without data is whatever the stage held before: its bits are cleared.
+          const bool partial = mask != 0xFFFFu;
+          const uint32_t b0 = mask >> (2 * t), b1 = mask >> (2 * t + 8);
+          const uint32_t and0 = ((b0 & 1u) ? 0xFFFFu : 0u) | ((b0 & 2u) ? 0xFFFF0000u : 0u);
+          const uint32_t and1 = ((b1 & 1u) ? 0xFFFFu : 0u) | ((b1 & 2u) ? 0xFFFF0000u : 0u);
+#pragma unroll
+          for (int k0 = 0; k0 < KS; k0 += VR) {
+            if (k0 > 0) {
+#pragma unroll
+              for (int k = 0; k < VR; ++k) ldmatrix_x4_trans(vf[k], base + v_lane + (k0 + k) * 32);
             }
+            if (partial) {
+#pragma unroll
+              for (int k = 0; k < VR; ++k) {
+                vf[k][0] &= and0;
+                vf[k][1] &= and0;
+                vf[k][2] &= and1;
+                vf[k][3] &= and1;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], ph[0][0], ph[0][1]);
+#pragma unroll
+            for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], plo[0][0], plo[0][1]);
           }
-#pragma unroll
-          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], ph[0][0], ph[0][1]);
-#pragma unroll
-          for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], plo[0][0], plo[0][1]);
-        }
-        if (VR < KS && release) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+          if (VR < KS && release) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+          }
         }
       }
-    }
     }
     if (!(flags & kLast)) continue;
 
@@ -973,7 +973,8 @@ __device__ __forceinline__ void store_lse(const SplitArgs& a, int r, int h, floa
 // Registers are held to what lets 40 (or 32) warps share an SM, also with the split kernel's last blocks:
 // at 60 instead of 48 one request of 8 KV heads of 128 with 4 query heads each took 15.2 us, not 11.9.
 template <int D, int JW>
-__global__ void __launch_bounds__(32 * JW, (JW == kFewWarps && D < 256 ? 40 : 32) / JW) attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
+__global__ void __launch_bounds__(32 * JW, (JW == kFewWarps && D < 256 ? 40 : 32) / JW)
+attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
   extern __shared__ float dyn[];                           // with weights: [n_heads] lse, the sums of find_range
   __shared__ float part[JW][D + 2];
   __shared__ __align__(8) float sums[2 * JW * kJoinUnit];
@@ -1081,7 +1082,8 @@ __global__ void __launch_bounds__(32 * JW, (JW == kFewWarps && D < 256 ? 40 : 32
       }
     } else {
       // up to 32 heads, a lane each, the partials over the warps and over what lanes are left
-      const int side = JW == kFewWarps || a.n_heads > 16 ? 32 : a.n_heads > 8 ? 16 : a.n_heads > 4 ? 8 : 4, rows = JW * (32 / side);
+      const int side = JW == kFewWarps || a.n_heads > 16 ? 32 : a.n_heads > 8 ? 16 : a.n_heads > 4 ? 8 : 4;
+      const int rows = JW * (32 / side);
       for (int h0 = 0; h0 < a.n_heads; h0 += 32) {
         const int h = min(h0 + lane % side, a.n_heads - 1);
         float M = -INFINITY, L = 0.f;
@@ -1225,7 +1227,8 @@ SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads,
   pl.row_bytes = pl.heads * pl.D * 2 + 16;                 // + 16: ldmatrix's 8 rows on 8 bank groups
   pl.stage_bytes = pl.direct ? 0 : 2 * kTile * pl.tiles * pl.row_bytes;
   // behind the ring: the sums of find_range (4 bytes per 128 requests), later the merged heads
-  const int merge = pl.sharers > 1 ? (pl.direct ? (pl.sharers - 1) * pl.heads : pl.heads) * ((pl.group + 7) / 8) * 8 * (pl.D + 2) * 4 : 0;
+  const int buffers = pl.sharers == 1 ? 0 : (pl.direct ? pl.sharers - 1 : 1) * pl.heads * ((pl.group + 7) / 8);
+  const int merge = buffers * 8 * (pl.D + 2) * 4;
   const int tail = std::max(merge, (n_req + 127) / 128 * 4);
   pl.stages = pl.direct ? 0 : std::min(kMaxStages, (kMaxSmem - kStaticSmem - tail) / pl.stage_bytes);
   pl.smem = pl.stages * pl.stage_bytes + tail;
@@ -1290,11 +1293,8 @@ int launch_split_any(const lora_pool* p, const SplitArgs& a, cudaStream_t st) {
   switch (pl.D * 16 + pl.tiles) {
     case 64 * 16 + 1: return two ? launch_split<64, 1, 2, 2>(p, a, st) : launch_split<64, 1, 1, 2>(p, a, st);
     case 64 * 16 + 2: return pairs ? launch_split<64, 2, 2, 2>(p, a, st) : launch_split<64, 2, 2, 1>(p, a, st);
-    case 64 * 16 + 4: return launch_split<64, 4, 2, 1>(p, a, st);
-    case 64 * 16 + 8: return launch_split<64, 8, 2, 1>(p, a, st);
     case 128 * 16 + 1: return two ? launch_split<128, 1, 2, 1>(p, a, st) : launch_split<128, 1, 1, 1>(p, a, st);
     case 128 * 16 + 2: return launch_split<128, 2, 2, 1>(p, a, st);
-    case 128 * 16 + 4: return launch_split<128, 4, 2, 1>(p, a, st);
     case 256 * 16 + 1: return two ? launch_split<256, 1, 2, 1>(p, a, st) : launch_split<256, 1, 1, 1>(p, a, st);
     case 256 * 16 + 2: return launch_split<256, 2, 2, 1>(p, a, st);
   }
@@ -1403,5 +1403,7 @@ extern "C" int lora_attention_split(lora_pool* p, int32_t n_req, const int32_t* 
   a.err = p->d_err;
   const int rc2 = launch_split_any(p, a, st);
   if (rc2 != LORA_OK || (pl.whole && !weight_out)) return rc2;
-  return pl.D == 64 ? launch_join_any<64>(p, a, st) : pl.D == 128 ? launch_join_any<128>(p, a, st) : launch_join_any<256>(p, a, st);
+  return pl.D == 64    ? launch_join_any<64>(p, a, st)
+         : pl.D == 128 ? launch_join_any<128>(p, a, st)
+                       : launch_join_any<256>(p, a, st);
 }
