@@ -674,6 +674,7 @@ def _weights(kind, rng, shape):
     (1, [80], 64, 16), (1, [1], 1, 0), (1, [1, 0, 2], 1, 1), (3, [64, 65, 63, 0, 200], 64, 0), (2, [300, 10, 299], 299, 299),
     (5, [1000, 1, 999], 17, 16), (2, [4097, 2049, 2048, 2047], 1024, 100), (1, [40000, 39999, 7], 2000, 1),
     (1, [140001, 3], 5000, 512), (2, [70000], 69999, 3), (40, [128] * 20, 100, 10), (1, [5] * 1000, 3, 1),
+    (4, [4090, 0, 33, 4089] * 40, 4000, 3), (32, [2000, 1999, 3] * 7, 1, 1),
     (4, [4096, 0, 1, 31, 33, 127, 4095, 513] * 20, 500, 3), (7, [300, 1, 64, 0, 257] * 23, 64, 0), (1, [700] * 609, 700, 8),
 ])
 @pytest.mark.parametrize("kind", KINDS)
