@@ -50,10 +50,11 @@ constexpr int threads_of(int producers) { return 32 * (kWarps + producers); }
 constexpr int kCtasPerSm = 2;
 constexpr int kTile = 16;                           // tokens a warp takes at a time
 // The running maximum m follows the scores only where one passes it by more than kMaxSlack: any m gives
-// the same softmax, and weights of up to 2^8 lose nothing in fp32 or as two bf16 terms.  A tile then
+// the same softmax, and weights of up to 2^8 lose nothing in fp32 or as bf16 terms.  A tile then
 // starts with a vote in place of the shuffles of a maximum: 64 x 10,000 tokens with 16 query heads per
 // KV head, 8 KV heads of 64 283 -> 237 us, 4 of them 151 -> 128; where copies bound it, the same.
 constexpr float kMaxSlack = 8.f;
+constexpr int kTerms = 3;                           // bf16 terms of a weight in the V product
 constexpr int kMaxTiles = 2;                        // 16-token tiles per stage, at most
 constexpr int kStageBytes = 32 * 1024;              // K and V of a stage, at most
 constexpr int kMaxStages = 8;
@@ -151,8 +152,33 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ uint32_t pack_bf16_down(float lo, float hi) {        // toward zero
+  uint32_t y;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// Two weights as bf16 terms, without loss: each term but the last is the largest bf16 strictly below what
+// is left, so 24 bits are used up in three, and no term of a weight above 2^-100 is zero or negative.  The
+// terms' products with an infinite V are then that infinity, where a zero or negative term would add NaN.
+// Two rounded terms hold 16 bits, which shows where V's terms cancel.  The third makes four MMAs of three:
+// nothing where HBM bounds (256 x 128 to 2,048 tokens, H = 5120 831 / 834 us), 16
+// query heads on 8 KV heads of 64 237 / 250, one KV head of 64 x 40,000 tokens 147 / 160.
+__device__ __forceinline__ void weight_terms(float p0, float p1, uint32_t (&term)[kTerms]) {
+  constexpr float kBelow = 1.f - 1.f / (1 << 24);          // x kBelow: the next smaller fp32
+#pragma unroll
+  for (int k = 0; k + 1 < kTerms; ++k) {
+    term[k] = pack_bf16_down(p0 * kBelow, p1 * kBelow);
+    p0 -= bf16_lo(term[k]);
+    p1 -= bf16_hi(term[k]);
+  }
+  term[kTerms - 1] = pack_bf16(p0, p1);
+}
+
+// What turns the sum of weights x V into their mean; 0 for a row without weight.
+__device__ __forceinline__ float normalizer(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 enum : int32_t { kFirst = 1, kLast = 2, kStarts = 4, kEnds = 8 };
 
@@ -282,7 +308,7 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
 // every K and V byte is used once, so the tensor work is small; this layout leaves 1/8 instead of
 // 1/16 of the MMA in use at one query head, and the running maximum, sum and rescaling of a column
 // stay in the lanes that hold the column in both products.  P^T is the transpose of S^T's
-// fragment (movmatrix) as two bf16 terms, hi + lo, so the weights carry 16 mantissa bits.
+// fragment (movmatrix) as three bf16 terms, so the weights reach the product with all their fp32 bits.
 // Direct (NP = 0): no ring and no producer.  A lane loads 16 bytes (8 features) of its token's row at a
 // time, and the products take the features in that order: K's registers are the first product's
 // fragments as they come (q is read in the same order), V's are transposed (movmatrix) into the
@@ -492,10 +518,10 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
                           (uint32_t)(hh * D + ((lane >> 3) & 1) * 8) * 2;
   const uint32_t head_step = (uint32_t)(pl.head_slots * D * 2);
   const int turns = pl.sharers / tile_sharers, turn = share / tile_sharers;
-  // Scores of NT tiles into weights 2^(s - m), transposed for the V product, hi and lo terms.
+  // Scores of NT tiles into weights 2^(s - m), transposed for the V product, in terms.
   constexpr int NT = kDirect ? TILES : 1;
   const auto tile_weights = [&](int u, int req, int j0, int n, uint32_t mask, float (&sc)[NT][4],
-                                const float (&odd)[NT][4], uint32_t (&ph)[NT][2], uint32_t (&plo)[NT][2]) {
+                                const float (&odd)[NT][4], uint32_t (&pt)[NT][kTerms][2]) {
     const int G = n_query(u);
     float x[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -547,11 +573,13 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
         sc[i][2 + k] = exp2f(sc[i][2 + k] - ms[k]);
         l[u][k] += sc[i][k] + sc[i][2 + k];
       }
-      const uint32_t h_lo = pack_bf16(sc[i][0], sc[i][1]), h_hi = pack_bf16(sc[i][2], sc[i][3]);
-      ph[i][0] = transpose_8x8(h_lo);
-      ph[i][1] = transpose_8x8(h_hi);
-      plo[i][0] = transpose_8x8(pack_bf16(sc[i][0] - bf16_lo(h_lo), sc[i][1] - bf16_hi(h_lo)));
-      plo[i][1] = transpose_8x8(pack_bf16(sc[i][2] - bf16_lo(h_hi), sc[i][3] - bf16_hi(h_hi)));
+#pragma unroll
+      for (int hi = 0; hi < 2; ++hi) {
+        uint32_t term[kTerms];
+        weight_terms(sc[i][2 * hi], sc[i][2 * hi + 1], term);
+#pragma unroll
+        for (int k = 0; k < kTerms; ++k) pt[i][k][hi] = transpose_8x8(term[k]);
+      }
     }
   };
   int seg = 0;                                             // segments finished: the phase of the merge barriers
@@ -633,7 +661,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
       if (first) begin_segment();
       const int j0 = tok + share * NT * kTile;
       if (j0 < n) {
-        uint32_t ph[HW][NT][2], plo[HW][NT][2];
+        uint32_t pt[HW][NT][kTerms][2];
 #pragma unroll
         for (int u = 0; u < HW; ++u) {
           float sc[NT][4], odd[NT][4];
@@ -651,7 +679,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
               mma_16x8x16(sc[b], k0, qf[u][2 * i][0], qf[u][2 * i][1]);
               mma_16x8x16(odd[b], k1, qf[u][2 * i + 1][0], qf[u][2 * i + 1][1]);
             }
-          tile_weights(u, req, j0, n, mask, sc, odd, ph[u], plo[u]);
+          tile_weights(u, req, j0, n, mask, sc, odd, pt[u]);
         }
 #pragma unroll
         for (int b = 0; b < NT; ++b)
@@ -664,10 +692,11 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
             for (int u = 0; u < HW; ++u) {
               if (kPair && u != i / KH) continue;
               const int ks = 2 * (i % KH);
-              mma_16x8x16(acc[u][ks], v0, ph[u][b][0], ph[u][b][1]);
-              mma_16x8x16(acc[u][ks + 1], v1, ph[u][b][0], ph[u][b][1]);
-              mma_16x8x16(acc[u][ks], v0, plo[u][b][0], plo[u][b][1]);
-              mma_16x8x16(acc[u][ks + 1], v1, plo[u][b][0], plo[u][b][1]);
+#pragma unroll
+              for (int k = 0; k < kTerms; ++k) {
+                mma_16x8x16(acc[u][ks], v0, pt[u][b][k][0], pt[u][b][k][1]);
+                mma_16x8x16(acc[u][ks + 1], v1, pt[u][b][k][0], pt[u][b][k][1]);
+              }
             }
           }
       }
@@ -724,8 +753,8 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_empty + 8 * s);
           }
-          uint32_t ph[NT][2], plo[NT][2];
-          tile_weights(u, req, j0, n, mask, sc, odd, ph, plo);
+          uint32_t pt[NT][kTerms][2];
+          tile_weights(u, req, j0, n, mask, sc, odd, pt);
           // V of a token without data is whatever the stage held before: its bits are cleared.
           const bool partial = mask != 0xFFFFu;
           const uint32_t b0 = mask >> (2 * t), b1 = mask >> (2 * t + 8);
@@ -747,9 +776,9 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
               }
             }
 #pragma unroll
-            for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], ph[0][0], ph[0][1]);
+            for (int i = 0; i < kTerms; ++i)
 #pragma unroll
-            for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], plo[0][0], plo[0][1]);
+              for (int k = 0; k < VR; ++k) mma_16x8x16(acc[u][k0 + k], vf[k], pt[0][i][0], pt[0][i][1]);
           }
           if (VR < KS && release) {
             __syncwarp();
@@ -843,7 +872,7 @@ __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_ke
       if (u >= n_mine) break;
       const int head0 = head_of(u), G = n_query(u);
       if (starts && ends) {
-        const float i0 = l[u][0] == 0.f ? 0.f : 1.f / l[u][0], i1 = l[u][1] == 0.f ? 0.f : 1.f / l[u][1];
+        const float i0 = normalizer(l[u][0]), i1 = normalizer(l[u][1]);
         uint16_t* row = a.out + req * a.out_stride + (int64_t)(head0 + g) * D;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -1013,7 +1042,7 @@ attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
               L = fmaf(part[v][D + 1], c, L);
               x = fmaf(part[v][lane], c, x);
             }
-            row[(int64_t)h * D + d0 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(L == 0.f ? 0.f : x * (1.f / L)));
+            row[(int64_t)h * D + d0 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(x * normalizer(L)));
             if (d0 == 0 && lane == 0) store_lse(a, r, h, M, L);
           }
         }
@@ -1038,7 +1067,7 @@ attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
             c[v] = exp2f(part[v][D] - ms);
             L = fmaf(part[v][D + 1], c[v], L);
           }
-          const float inv = L == 0.f ? 0.f : 1.f / L;
+          const float inv = normalizer(L);
           for (int d = threadIdx.x; d < D; d += 32 * JW) {
             float x = 0.f;
 #pragma unroll
@@ -1051,7 +1080,7 @@ attention_join_kernel(const __grid_constant__ SplitArgs a, int32_t subs) {
         for (int h = block * JW + warp; h < a.n_heads; h += blocks * JW) {
           float m, l, acc[E];
           join_partials<D>(a, range.x, range.y, 0, 1, h, lane, m, l, acc);
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const float inv = normalizer(l);
 #pragma unroll
           for (int e = 0; e < E; ++e)
             row[(int64_t)h * D + e * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] * inv));

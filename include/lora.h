@@ -239,7 +239,9 @@ int lora_kv_write(lora_pool* pool, int32_t n_rows, const int32_t* row_req, const
  * A request with no cached token gets out = 0 and lse = -infinity.  A page id outside the pool
  * sets the device error word and its token is skipped (it receives no weight); a request length
  * outside [0, max_len] sets it and is clamped.  If no score of a row is above -infinity the row
- * counts as empty.  Results do not depend on the order in which CTAs run.  At most 65535
+ * counts as empty.  Weights reach the V product with all their fp32 bits, and an infinite V gives
+ * that infinity (NaN where both signs meet, or where its token's weight is zero or below 2^-100 of
+ * the row's largest).  Results do not depend on the order in which CTAs run.  At most 65535
  * requests per call, and n_req x max_len at most 16 x 2^31.
  */
 int64_t lora_attention_split_size(const lora_pool* pool, int32_t n_req, int32_t max_len, int32_t n_heads,

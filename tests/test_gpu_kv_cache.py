@@ -487,6 +487,104 @@ def test_attention_split_on_two_streams_at_once(L):
         c.close()
 
 
+def _attend(L, c, q, n_heads, n_kv, layer=0):
+    """One call with log-sum-exp and token weights: (out, lse, weights)."""
+    import torch
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((c.n_req, n_heads), 7.0, device="cuda")
+    w = torch.zeros((c.n_req, c.max_len), device="cuda")
+    ws, nb = c.workspace(n_heads, n_kv, True)
+    L.lora_attention_split(c.pool, c.n_req, c.table, c.seq, c.max_len, c.layers, layer, q, out, n_heads, n_kv, ws, nb,
+                           lse_dev=lse, weight_out_dev=w)
+    L.lora_status(c.pool)
+    return out, lse, w.cpu().numpy().astype(np.float64)
+
+
+# Shapes of every form: rows read directly (one warp a head, several, two heads a warp in a cache that max_len
+# calls large), copied stages of each head width, requests taken whole and split.
+FORMS = [
+    (1, 1, 64, [1, 2, 33, 700], None), (1, 12, 64, [5, 300], None), (3, 2, 64, [1, 40, 129], None),
+    (2, 3, 64, [17, 260], 1 << 20), (3, 1, 64, [90, 2], 1 << 20), (1, 3, 128, [1, 64, 999], None),
+    (1, 9, 128, [3, 61], None), (8, 1, 128, [1, 5, 60], None), (8, 2, 128, [900, 1, 64], None),
+    (4, 12, 64, [50, 333], None), (13, 1, 64, [45, 700], None), (6, 2, 256, [47, 1, 90], None),
+    (1, 16, 256, [300, 2], None), (1, 1, 64, [20001], None), (4, 1, 128, [9000], None),
+]
+
+
+@pytest.mark.parametrize("n_kv,G,D,lengths,max_len", FORMS)
+def test_attention_split_infinite_values(L, n_kv, G, D, lengths, max_len):
+    """A weight times an infinite V is that infinity, whatever the weight's bits; V of both signs gives NaN; the
+    other features, and the weights, stay what they are."""
+    n_heads, H = n_kv * G, n_kv * D
+    c = Cache(L, H, 1, lengths, seed=H + G, max_len=max_len)
+    try:
+        n_req, tabs, inf = c.n_req, c.tables(0), 0x7F80
+        q_bits = workloads.to_bf16_bits(c.rng.standard_normal((n_req, n_heads * D)).astype(np.float32))
+        want = np.zeros((n_req, n_heads, D))                       # infinities; the rest from the oracle
+        for r, n in enumerate(lengths):
+            a, b, third = c.rng.integers(0, n), c.rng.integers(0, n), n - 1
+            v = c.bits[tabs[r][:, 1]].reshape(n, n_kv, D)
+            v[:, :, :4] = workloads.to_bf16_bits(np.float32([0.0]))[0]
+            v[a, :, 0], v[b, :, 1] = inf, inf | 0x8000
+            v[third, :, 2], v[:, :, 3] = inf, inf
+            if n > 1:
+                v[0, :, 2] = inf | 0x8000
+            c.bits[tabs[r][:, 1]] = v.reshape(n, H)
+            want[r, :, 0], want[r, :, 1], want[r, :, 3] = np.inf, -np.inf, np.inf
+            want[r, :, 2] = np.nan if n > 1 else np.inf
+        c.pool_t.copy_(bits_to_torch(c.bits))
+        finite = c.bits.copy()
+        finite[(finite & 0x7FFF) == inf] = 0
+        ref = O.attention_split(finite, tabs, q_bits, n_heads, n_kv)
+        out, lse, w = _attend(L, c, bits_to_torch(q_bits), n_heads, n_kv)
+        got = out.float().cpu().numpy().reshape(n_req, n_heads, D)
+        assert np.array_equal(got[:, :, :4], want[:, :, :4], equal_nan=True)
+        out.view(n_req, n_heads, D)[:, :, :4] = 0
+        _check(ref, out, lse, lengths, D, G)
+        _check_weights(ref, w[:, :max(lengths)], None, lengths, D, G, n_heads)
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("n_kv,G,D,n", [(4, 1, 128, 6), (1, 2, 64, 5), (3, 1, 64, 8), (1, 1, 128, 7), (2, 1, 256, 6),
+                                        (8, 3, 64, 4), (1, 12, 64, 6)])
+def test_attention_split_weights_reach_the_product_in_full(L, n_kv, G, D, n):
+    """V whose last three rows cancel the others, so that what is left of an output is what the weights lost.
+
+    One coordinate of q is not zero, so a score is one exact product q K, times log2(e) / sqrt(D) (itself off by 2 u):
+    with |s| <= 0.36 in base 2, s and m are off by 1.1 u each and their difference by another 0.4 u, a weight by
+    ln(2) 2.6 u and by exp2's two ulps, 4 u: 6 u in all.  The normaliser adds n sums, 6 u of its own and two
+    roundings, the V product one rounding (or cut, 2 u) per term and one of the scaling, 8 u, the last product u:
+    (n + 24) u of sum p |V|.  Weights of 16 bits would be off by 2^-17, 128 u, each."""
+    n_heads, H, n_req = n_kv * G, n_kv * D, 24
+    c = Cache(L, H, 1, [n] * n_req, seed=n + H)
+    try:
+        tabs, rng = c.tables(0), c.rng
+        one = workloads.to_bf16_bits(np.float32([1.0]))[0]
+        q_bits = np.zeros((n_req, n_heads, D), np.uint16)
+        q_bits[:, :, 5] = one
+        for r in range(n_req):
+            k = rng.standard_normal((n, n_kv, D)).astype(np.float32)
+            k[:, :, 5] = rng.uniform(-0.25, 0.25, (n, n_kv)) * np.sqrt(D)
+            k_bits = workloads.to_bf16_bits(k.reshape(n, H))
+            p = np.exp(O.bf16_to_f64(k_bits).reshape(n, n_kv, D)[:, :, 5] / np.sqrt(D))
+            v = np.zeros((n, n_kv, D))
+            for j in range(n):                                     # each of the last three cancels what is there
+                x = rng.standard_normal((n_kv, D)) if j < n - 3 else -(p[:j, :, None] * v[:j]).sum(0) / p[j][:, None]
+                v[j] = O.bf16_to_f64(workloads.to_bf16_bits(x.astype(np.float32)))
+            c.bits[tabs[r][:, 0]], c.bits[tabs[r][:, 1]] = k_bits, workloads.to_bf16_bits(v.reshape(n, H).astype(np.float32))
+        c.pool_t.copy_(bits_to_torch(c.bits))
+        q_bits = q_bits.reshape(n_req, -1)
+        ref = O.attention_split(c.bits, tabs, q_bits, n_heads, n_kv)
+        out, _, _ = _attend(L, c, bits_to_torch(q_bits), n_heads, n_kv)
+        got = O.bf16_to_f64(torch_to_bits(out))
+        tol = 2.0 ** -8 * np.abs(ref["out"]) + (n + 24) * 2.0 ** -24 * ref["vabs"] * 1.01
+        bad = np.abs(got - ref["out"]) > tol
+        assert not bad.any(), (int(bad.sum()), (np.abs(got - ref["out"]) / tol).max())
+    finally:
+        c.close()
+
+
 # ---- page writes ---------------------------------------------------------------------------------
 @pytest.mark.parametrize("H,layers,lengths,pad", [
     (64, 1, [1], 0), (256, 2, [5, 0, 9], 8), (5120, 1, [1] * 40, 0), (4096, 3, [130, 1, 17], 64), (16384, 1, [3], 0),
