@@ -585,6 +585,34 @@ def test_attention_split_weights_reach_the_product_in_full(L, n_kv, G, D, n):
         c.close()
 
 
+@pytest.mark.parametrize("n_kv,G,D,lengths", [
+    (4, 1, 128, [60] * 8), (16, 2, 64, [60] * 3), (4, 1, 256, [60] * 2), (3, 1, 64, [2000] * 30), (8, 2, 128, [500] * 40),
+])
+def test_attention_split_large_values_under_late_scores(L, n_kv, G, D, lengths):
+    """Scores 5.4 higher in a request's second half, 221 times the weight.  Weights relative to the largest are at
+    most 1 and their sum times |V| stays below 2^127, so no sum may overflow."""
+    n_heads, H = n_kv * G, n_kv * D
+    c = Cache(L, H, 1, lengths, seed=H + G)
+    try:
+        n_req, tabs = c.n_req, c.tables(0)
+        q_bits = workloads.to_bf16_bits(c.rng.standard_normal((n_req, n_heads * D)).astype(np.float32))
+        q = O.bf16_to_f64(q_bits).reshape(n_req, n_kv, G, D)[:, :, 0]
+        high = (5.4 * np.sqrt(D) * q / (q ** 2).sum(-1, keepdims=True)).reshape(n_req, H)
+        top = 126 - int(np.ceil(np.log2(2 * max(lengths))))
+        for r, n in enumerate(lengths):
+            k = np.where(np.arange(n)[:, None] < n // 2, 0.0, high[r])
+            v = np.minimum(np.abs(c.rng.standard_normal((n, H))), 4.0) * 2.0 ** top
+            c.bits[tabs[r][:, 0]] = workloads.to_bf16_bits(k.astype(np.float32))
+            c.bits[tabs[r][:, 1]] = workloads.to_bf16_bits(v.astype(np.float32))
+        c.pool_t.copy_(bits_to_torch(c.bits))
+        ref = O.attention_split(c.bits, tabs, q_bits, n_heads, n_kv)
+        out, lse, w = _attend(L, c, bits_to_torch(q_bits), n_heads, n_kv)
+        _check(ref, out, lse, lengths, D, G)
+        _check_weights(ref, w, None, lengths, D, G, n_heads)
+    finally:
+        c.close()
+
+
 # ---- page writes ---------------------------------------------------------------------------------
 @pytest.mark.parametrize("H,layers,lengths,pad", [
     (64, 1, [1], 0), (256, 2, [5, 0, 9], 8), (5120, 1, [1] * 40, 0), (4096, 3, [130, 1, 17], 64), (16384, 1, [3], 0),
