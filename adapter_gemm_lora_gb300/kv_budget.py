@@ -66,9 +66,12 @@ class BudgetedCache:
         self.lengths = lengths
 
     def grow(self) -> None:
-        """Pages for one new token per request."""
+        """Pages for one new token per request; LORA_ENOPAGES, and none taken, if the pool has too few for all of them."""
         import torch
         self.make_room()
+        need, free = 2 * self.layers * len(self.ids), self.lib.lora_pool_stats(self.pool)["free"]
+        if need > free:                                        # before any request holds a token the table does not name
+            raise self.lib.LoraError(self.lib.LORA_ENOPAGES, f"BudgetedCache.grow: {need} pages asked, {free} free")
         rows = np.array([self.lib.lora_kv_grow(self.pool, r, 1, self.layers) for r in self.ids], dtype=np.int32)
         n = len(self.ids)
         pos = torch.tensor(self.lengths, dtype=torch.int64)
