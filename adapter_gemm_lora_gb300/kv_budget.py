@@ -24,7 +24,8 @@ class BudgetedCache:
     """The KV cache of a decode batch, one token per request and step.
 
     A request holds at most ``budget + slack`` tokens; ``make_room`` cuts the batch back to ``budget``
-    when one of them is full.  All device state is allocated here; ``attend`` only enqueues work.
+    when one of them is full.  The requests must hold no KV pages yet.  All device state is allocated
+    here; ``attend`` only enqueues work.
     """
 
     def __init__(self, lib, pool, request_ids, layers: int, n_heads: int, n_kv_heads: int, budget: int, recent: int,
@@ -33,6 +34,11 @@ class BudgetedCache:
         if slack < 1:
             raise ValueError("slack must be at least 1")
         self.lib, self.pool, self.ids = lib, pool, list(request_ids)
+        if len(set(self.ids)) < len(self.ids):
+            raise ValueError("a request is named twice")
+        for r in self.ids:                                     # the tables start empty
+            if lib.lora_kv_length(pool, r) >= 0:
+                raise ValueError(f"request {r} holds KV pages already: free it first")
         self.layers, self.n_heads, self.n_kv_heads = layers, n_heads, n_kv_heads
         self.budget, self.recent, self.cap = budget, recent, budget + slack
         n = len(self.ids)

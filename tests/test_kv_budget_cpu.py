@@ -89,3 +89,21 @@ def test_a_refused_growth_leaves_host_and_device_alike(L, on_cpu, spare):
         _host_is_device(L, pool, cache)
     finally:
         L.lora_pool_destroy(pool)
+
+
+def test_requests_that_hold_tokens_or_come_twice_are_refused(L, on_cpu):
+    """The cache starts every request empty, so one with pages of its own, or in two rows, would not match its table."""
+    from adapter_gemm_lora_gb300.kv_budget import BudgetedCache
+    pool = L.lora_pool_create(None, 64, 64, 1, 1)
+    try:
+        for layers in (2, 3):                                     # a zero growth fixes the layer count: 2
+            L.lora_kv_grow(pool, 5, 0 if layers == 2 else 1, 2)
+            with pytest.raises(ValueError, match="holds"):
+                BudgetedCache(HostLib(L), pool, [4, 5], layers, 1, 1, 4, 2, 2)
+        with pytest.raises(ValueError, match="twice"):
+            BudgetedCache(HostLib(L), pool, [1, 2, 1], 2, 1, 1, 4, 2, 2)
+        assert L.lora_pool_stats(pool)["reserved"] == 4
+        L.lora_kv_free(pool, 5)
+        BudgetedCache(HostLib(L), pool, [4, 5], 3, 1, 1, 4, 2, 2).grow()
+    finally:
+        L.lora_pool_destroy(pool)
