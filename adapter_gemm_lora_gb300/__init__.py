@@ -131,7 +131,7 @@ def _load():
         "lora_attention_split": (I32, [VP, I32, VP, VP, I32, I32, I32, VP, I64, VP, I64, I32, I32, VP, VP, VP, I64, VP,
                                        I64, VP]),
         "lora_kv_evict": (I32, [VP, I32, VP, VP, I32, I32, VP, I32, I32, VP, VP, VP, VP, I32, VP]),
-        "lora_kv_keep": (I32, [VP, I64, I32, VP, I64]),
+        "lora_kv_keep": (I32, [VP, I64, I32, I32, VP, I64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -374,11 +374,12 @@ def lora_kv_evict(pool, n_req: int, table_dev, seq_len_dev, max_len: int, layers
 
 
 def lora_kv_keep(pool, request_id: int, keep_host) -> None:
-    """Host bookkeeping of an eviction: keep_host int32 [layers, n_keep], the positions that stayed per layer."""
+    """Host bookkeeping of an eviction: keep_host int32 [layers, n_keep], the positions that stayed at each of the
+    request's layers."""
     keep = np.ascontiguousarray(keep_host, dtype=np.int32)
     if keep.ndim != 2:
         raise ValueError("keep_host must be [layers, n_keep]")
-    _check(_load().lora_kv_keep(pool, request_id, keep.shape[1], _ptr(keep), keep.shape[1]))
+    _check(_load().lora_kv_keep(pool, request_id, keep.shape[0], keep.shape[1], _ptr(keep), keep.shape[1]))
 
 
 def lora_adapter_refs(pool, adapter_id: int) -> int:

@@ -364,12 +364,15 @@ int lora_kv_free(lora_pool* p, int64_t request) {
   return LORA_OK;
 }
 
-int lora_kv_keep(lora_pool* p, int64_t request, int32_t n_keep, const int32_t* keep, int64_t stride) {
+int lora_kv_keep(lora_pool* p, int64_t request, int32_t layers, int32_t n_keep, const int32_t* keep, int64_t stride) {
   if (!p || n_keep < 0 || (n_keep > 0 && !keep) || stride < 0 || (stride > 0 && stride < n_keep))
     return lora_fail(LORA_EINVAL, "lora_kv_keep: bad arguments");
   auto it = p->kv.find(request);
   if (it == p->kv.end()) return lora_fail(LORA_EINVAL, "lora_kv_keep: request " + std::to_string(request) + " holds no pages");
   const int32_t L = it->second.layers;
+  if (layers != L)
+    return lora_fail(LORA_EINVAL, "lora_kv_keep: request " + std::to_string(request) + " has " + std::to_string(L) +
+                                      " layers, not " + std::to_string(layers));
   std::vector<int32_t>& pages = it->second.pages;
   const int64_t n = (int64_t)pages.size() / (2 * L);
   if (stride == 0) stride = n_keep;

@@ -270,17 +270,19 @@ int lora_attention_split(lora_pool* pool, int32_t n_req, const int32_t* table_de
  * overlap an input.  Device work only: lora_kv_keep then tells the host bookkeeping, from a copy
  * of keep_dev and new_len_dev, which tokens stayed, and frees the others' pages.
  *   lora_kv_keep: token i of `request_id` at layer l becomes its old token
- *     keep_host[l * keep_stride + i], i < n_keep (keep_stride in elements; 0 = n_keep); every
- *     layer's positions strictly ascending and within the request's length (LORA_EINVAL otherwise,
- *     nothing changed).  The pages of the tokens left out go back to the free list in the order
- *     they were taken.  Host bookkeeping only: as with lora_kv_free, work that still reads those
- *     pages must be ordered before whatever next writes them.
+ *     keep_host[l * keep_stride + i], i < n_keep (keep_stride in elements; 0 = n_keep); `layers`
+ *     the request's layer count, every layer's positions strictly ascending and within the
+ *     request's length (LORA_EINVAL otherwise, nothing changed).  The pages of the tokens left out
+ *     go back to the free list in the order they were taken.  Host bookkeeping only: as with
+ *     lora_kv_free, work that still reads those pages must be ordered before whatever next writes
+ *     them.
  */
 int lora_kv_evict(lora_pool* pool, int32_t n_req, const int32_t* table_dev, const int32_t* seq_len_dev,
                   int32_t max_len, int32_t layers, const float* weight_dev, int32_t budget, int32_t recent,
                   int32_t* keep_dev, int32_t* new_len_dev, int32_t* table_out, float* weight_out,
                   int32_t max_len_out, lora_stream_t stream);
-int lora_kv_keep(lora_pool* pool, int64_t request_id, int32_t n_keep, const int32_t* keep_host, int64_t keep_stride);
+int lora_kv_keep(lora_pool* pool, int64_t request_id, int32_t layers, int32_t n_keep, const int32_t* keep_host,
+                 int64_t keep_stride);
 
 /* Give back n reserved pages (appended to the free list in the order given).
  * LORA_EINVAL if any id is not currently reserved or appears twice (nothing released). */

@@ -130,6 +130,18 @@ def test_kv_keep_refuses_and_changes_nothing(L, pool, keep, message):
         L.lora_kv_keep(pool, 1, [0, 1])
 
 
+@pytest.mark.parametrize("keep", [[[0]], [[0, 1]], [[0], [0], [0]], np.zeros((0, 1)), np.zeros((0, 0)), np.zeros((3, 0)),
+                                  np.zeros((1, 0))])
+def test_kv_keep_refuses_rows_that_are_not_the_layers(L, pool, keep):
+    """One row per layer of the request, neither fewer (the rest would be read past the array) nor more."""
+    L.lora_kv_grow(pool, 1, 3, 2)
+    before = [L.lora_kv_table(pool, 1, l).tolist() for l in range(2)], L.lora_pool_stats(pool)
+    _refused(L, lambda: L.lora_kv_keep(pool, 1, keep), "2 layers")
+    assert ([L.lora_kv_table(pool, 1, l).tolist() for l in range(2)], L.lora_pool_stats(pool)) == before
+    L.lora_kv_keep(pool, 1, np.zeros((2, 0)))
+    assert L.lora_kv_length(pool, 1) == 0
+
+
 def test_kv_keep_matches_the_oracle_over_random_sequences(L):
     rng = np.random.default_rng(17)
     order = rng.permutation(600)
