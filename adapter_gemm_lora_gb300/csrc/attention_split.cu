@@ -1291,6 +1291,7 @@ int check_shape(const char* fn, const lora_pool* p, int32_t n_req, int32_t max_l
   const auto fail = [fn](const char* what) { return lora_fail(LORA_EINVAL, std::string(fn) + what); };
   if (!p || n_req < 0 || max_len < 1 || n_heads < 1 || n_kv < 1) return fail(": bad arguments");
   if (n_req > 65535) return fail(": at most 65535 requests per call");
+  if (max_len > (1 << 30)) return fail(": max_len is at most 2^30");   // positions are 32-bit, units pass the end
   if (n_req * (((int64_t)max_len + kTile - 1) / kTile) > INT32_MAX) return fail(": n_req x max_len is at most 16 x 2^31");
   if (n_heads % n_kv != 0 || n_heads / n_kv > kSplitMaxGroup)
     return fail(": n_heads must be 1 to 16 times n_kv_heads");

@@ -242,7 +242,7 @@ int lora_kv_write(lora_pool* pool, int32_t n_rows, const int32_t* row_req, const
  * counts as empty.  Weights reach the V product with all their fp32 bits, and an infinite V gives
  * that infinity (NaN where both signs meet, or where its token's weight is zero or below 2^-100 of
  * the row's largest).  Results do not depend on the order in which CTAs run.  At most 65535
- * requests per call, and n_req x max_len at most 16 x 2^31.
+ * requests per call, max_len at most 2^30 and n_req x max_len at most 16 x 2^31.
  */
 int64_t lora_attention_split_size(const lora_pool* pool, int32_t n_req, int32_t max_len, int32_t n_heads,
                                   int32_t n_kv_heads, int32_t with_weights);

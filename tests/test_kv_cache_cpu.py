@@ -59,6 +59,16 @@ def test_attention_split_refuses(L, pool, over, message):
     _refused(L, _attend(L, pool), message, **over)
 
 
+@pytest.mark.parametrize("max_len", [(1 << 30) + 1, (1 << 31) - 128, (1 << 31) - 1])
+def test_attention_split_refuses_positions_near_32_bits(L, pool, max_len):
+    """Positions are 32-bit in the kernels, which look a few tiles past a request's end."""
+    _refused(L, _attend(L, pool), "2^30", max_len=max_len)
+    with pytest.raises(L.LoraError) as e:
+        L.lora_attention_split_size(pool, 3, max_len, 8, 4)
+    assert e.value.code == L.LORA_EINVAL and "2^30" in e.value.message
+    _refused(L, _attend(L, pool), "planning pool", max_len=1 << 30)
+
+
 def test_attention_split_size_refuses(L, pool):
     for args, message in [((0, 1, 8, 4), "planning"), ((-1, 1, 8, 4), "bad arguments"), ((1, 0, 8, 4), "bad arguments"),
                           ((1, 1, 9, 4), "1 to 16 times"), ((1, 1, 8, 8), "head width")]:
