@@ -767,8 +767,8 @@ extern "C" int lora_kv_evict(lora_pool* p, int32_t n_req, const int32_t* table_d
   if (!p || n_req < 0 || max_len < 1 || layers < 1) return lora_fail(LORA_EINVAL, "lora_kv_evict: bad arguments");
   if (budget < 1 || recent < 0 || recent > budget)
     return lora_fail(LORA_EINVAL, "lora_kv_evict: budget must be at least 1 and recent within [0, budget]");
-  if (max_len > (1 << 30) || max_len_out > (1 << 30))
-    return lora_fail(LORA_EINVAL, "lora_kv_evict: max_len and max_len_out are at most 2^30");
+  if (max_len > (1 << 30) || max_len_out > (1 << 30) || budget > (1 << 30))
+    return lora_fail(LORA_EINVAL, "lora_kv_evict: max_len, max_len_out and budget are at most 2^30");
   if (max_len_out < std::min(budget, max_len))
     return lora_fail(LORA_EINVAL, "lora_kv_evict: max_len_out is below min(budget, max_len)");
   if (n_req > 0 && (!table_dev || !seq_len_dev || !weight_dev || !keep_dev || !new_len_dev || !table_out ||

@@ -265,7 +265,8 @@ int lora_attention_split(lora_pool* pool, int32_t n_req, const int32_t* table_de
  *   table_out    out: device int32 [n_req][max_len_out][layers][2] (8-byte aligned), the kept
  *                tokens' pages in that order, then -1;
  *   weight_out   out: device fp32 [layers][n_req][max_len_out], their weights, then 0;
- *   max_len_out  >= min(budget, max_len); max_len and max_len_out at most 2^30.
+ *   max_len_out  >= min(budget, max_len); max_len, max_len_out and budget at most
+ *                2^30.
  * A request length outside [0, max_len] sets the device error word and is clamped.  No output may
  * overlap an input.  Device work only: lora_kv_keep then tells the host bookkeeping, from a copy
  * of keep_dev and new_len_dev, which tokens stayed, and frees the others' pages.

@@ -823,6 +823,27 @@ def test_evict_keeps_what_the_definition_keeps(L, layers, lengths, budget, recen
         L.lora_pool_destroy(pool)
 
 
+@pytest.mark.parametrize("layers,lengths,budget,recent", [
+    (2, [100, 0, 37], 6000, 50), (1, [40000, 3], 50001, 49999), (40, [60] * 20, 5000, 0), (3, [17], 18, 18),
+])
+def test_evict_with_a_budget_above_the_longest_row(L, layers, lengths, budget, recent):
+    """Everything stays; the kept list is filled up to the budget, table and weights to max_len_out."""
+    import torch
+    rng = np.random.default_rng(budget)
+    max_len, n_req = max(lengths) + 1, len(lengths)
+    weight = _weights("special", rng, (layers, n_req, max_len))
+    table = rng.integers(0, 1 << 31, size=(n_req, max_len, layers, 2)).astype(np.int32)
+    pool_t = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    pool = L.lora_pool_create(pool_t, 4, 64, 1, 1)
+    try:
+        got = _evict(L, pool, torch.from_numpy(table).cuda(), torch.tensor(lengths, dtype=torch.int32, device="cuda"),
+                     torch.from_numpy(weight).cuda(), budget, recent, max_len + 3)
+        L.lora_status(pool)
+        _same(got, _evict_expected(table, lengths, weight, budget, recent, max_len + 3))
+    finally:
+        L.lora_pool_destroy(pool)
+
+
 def test_evict_reports_and_clamps_lengths(L):
     import torch
     rng = np.random.default_rng(3)

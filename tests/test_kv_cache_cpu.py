@@ -111,6 +111,15 @@ def test_kv_evict_refuses(L, pool, over, message):
     _refused(L, lambda **o: L.lora_kv_evict(**{**base, **o}), message, **over)
 
 
+@pytest.mark.parametrize("budget", [(1 << 30) + 1, (1 << 31) - 4096, (1 << 31) - 1])
+def test_kv_evict_refuses_budgets_near_32_bits(L, pool, budget):
+    """The kernels step past the end of a row's kept list in 32 bits."""
+    base = dict(pool=pool, n_req=1, table_dev=A, seq_len_dev=B, max_len=8, layers=1, weight_dev=C, recent=2, keep_dev=D,
+                new_len_dev=E, table_out_dev=F, weight_out_dev=G, max_len_out=8, stream=0)
+    _refused(L, lambda **o: L.lora_kv_evict(**{**base, **o}), "2^30", budget=budget)
+    _refused(L, lambda **o: L.lora_kv_evict(**{**base, **o}), "planning pool", budget=1 << 30)
+
+
 # ---- bookkeeping of an eviction ----------------------------------------------------------------
 def test_kv_keep_by_hand(L):
     """Three tokens of two layers on 14 pages: layer 0 keeps tokens 0 and 2, layer 1 tokens 1 and 2."""
