@@ -613,6 +613,55 @@ def test_attention_split_large_values_under_late_scores(L, n_kv, G, D, lengths):
         c.close()
 
 
+@pytest.mark.parametrize("n_kv,D", [(4, 128), (8, 64), (3, 64)])
+def test_attention_split_sums_round_once_a_tile(L, n_kv, D):
+    """Sums that climb over most of a long request and fall back to nothing, so that what the roundings on the way
+    left is what is left of an output.  The shapes let one warp take a head's 16-token tiles in their order.
+
+    The first token has the largest score, so the sum S_t after tile t is relative to it throughout, and each
+    addition of a tile rounds to within u |S_t| (u = 2^-24).  Besides, a weight is off by 7 u (scores as in the
+    test of the weights in full, |s| <= 0.72 in base 2), a tile's three terms by a rounding or cut of 2 u each,
+    and the join of a request that is cut in two by a few: 20 u of sum p |V| in all."""
+    import torch
+    H, n, u = n_kv * D, 6400, 2.0 ** -24
+    n_req = 2 * torch.cuda.get_device_properties(0).multi_processor_count     # as many as there are ranges
+    c = Cache(L, H, 1, [n], seed=H)
+    try:
+        rng, tab = c.rng, c.tables(0)[0]
+        k = rng.standard_normal((n, n_kv, D)).astype(np.float32)
+        k[:, :, 5] = rng.uniform(-0.25, 0.25, (n, n_kv)) * np.sqrt(D)
+        k[0, :, 5] = 0.5 * np.sqrt(D)
+        k_bits = workloads.to_bf16_bits(k.reshape(n, H))
+        s = O.bf16_to_f64(k_bits).reshape(n, n_kv, D)[:, :, 5] / np.sqrt(D)
+        p = np.exp(s - s[0])[:, :, None]
+        v = rng.uniform(1, 2, (n, n_kv, D))
+        v[n * 3 // 4:] *= -3
+        v *= np.where(rng.random((n_kv, D)) < 0.5, 1, -1)
+        v = O.bf16_to_f64(workloads.to_bf16_bits(v.astype(np.float32)))
+        for j in range(n - 3, n):
+            v[j] = O.bf16_to_f64(workloads.to_bf16_bits((-(p[:j] * v[:j]).sum(0) / p[j]).astype(np.float32)))
+        c.bits[tab[:, 0]], c.bits[tab[:, 1]] = k_bits, workloads.to_bf16_bits(v.reshape(n, H).astype(np.float32))
+        c.pool_t.copy_(bits_to_torch(c.bits))
+        q_bits = np.zeros((1, n_kv, D), np.uint16)
+        q_bits[:, :, 5] = workloads.to_bf16_bits(np.float32([1.0]))[0]
+        ref = O.attention_split(c.bits, [tab], q_bits.reshape(1, H), n_kv, n_kv)
+        climbs = np.abs(np.cumsum(p * v, axis=0)[15::16]).sum(0) / p.sum(0)
+        tol = 2.0 ** -8 * np.abs(ref["out"]) + u * climbs.reshape(1, H) + 20 * u * ref["vabs"]
+        # every request is the same tokens
+        table = c.table.expand(n_req, -1, -1, -1).contiguous()
+        seq = c.seq.expand(n_req).contiguous()
+        q = bits_to_torch(np.repeat(q_bits.reshape(1, H), n_req, axis=0))
+        out = torch.empty_like(q)
+        nb = L.lora_attention_split_size(c.pool, n_req, c.max_len, n_kv, n_kv)
+        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        L.lora_attention_split(c.pool, n_req, table, seq, c.max_len, 1, 0, q, out, n_kv, n_kv, ws, nb)
+        L.lora_status(c.pool)
+        err = np.abs(O.bf16_to_f64(torch_to_bits(out)) - ref["out"])
+        assert (err <= tol).all(), (int((err > tol).sum()), (err / tol).max())
+    finally:
+        c.close()
+
+
 # ---- page writes ---------------------------------------------------------------------------------
 @pytest.mark.parametrize("H,layers,lengths,pad", [
     (64, 1, [1], 0), (256, 2, [5, 0, 9], 8), (5120, 1, [1] * 40, 0), (4096, 3, [130, 1, 17], 64), (16384, 1, [3], 0),
