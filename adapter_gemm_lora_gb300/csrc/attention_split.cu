@@ -6,10 +6,10 @@
 // Softmax in base 2: scores carry log2(e) / sqrt(D).
 //
 // HBM-bound: every cached token's K and V rows (2 x 2 H bytes) are read once, against 4 H G flops.
-// One GB300: 256 requests of 128 to 2,048 tokens at H = 5120 825 us (7.1 TB/s, 1.06 of the copy rate:
-// reads alone pass what a copy reaches), one request of 131,072 tokens at H = 4096 308 us (6.9 TB/s),
-// 64 requests with weights 181 us (0.93), 33 requests of up to 515 tokens 18.3 us (0.46: 3 us to the
-// first data, 3 us of join).
+// One GB300, a call: 256 requests of 128 to 2,048 tokens at H = 5120 826 us (7.1 TB/s, 1.06 of the copy
+// rate: reads alone pass what a copy reaches), one request of 131,072 tokens at H = 4096 307 us (7.0
+// TB/s), 64 requests with weights 179 us (0.94), 33 requests of up to 515 tokens 18.8 us (0.45: 3 us to
+// the first data, 3 us of join).
 //
 // Split.  The tokens of all requests, in units of one ring stage (or one turn of the warps), form one sequence that is cut
 // into P equal ranges; a CTA takes one range for one group of KV heads.  A request inside one range
@@ -41,9 +41,9 @@ constexpr int kWarps = 4;                           // consumer warps
 constexpr int kSmallSlice = 1024;
 // Rows of up to 384 bytes have no producer: the consumer warps load K and V rows from their pages
 // straight into MMA fragments, since a copy's cost does not fall with its size.  64 x 10,000 tokens,
-// 1 query head per KV head, us by copies / direct: one head of 64 88 / 34.9 (one of 128 92 / 58), two
-// of 64 93 / 58.5, three 107 / 94; but four 107 / 131, and at D = 128 two 106 / 106, four 196 / 204
-// (eight heads of 64 197 / 311).  Short calls: 8 x 2,000 tokens of one head of 64 11.7 / 8.0.
+// 1 query head per KV head, us by copies / direct: one head of 64 88 / 34.9 (one of 128 92 / 58.5),
+// two of 64 93 / 58.9, three 107 / 94; but four 107 / 131, and at D = 128 two 106 / 106, four 196 / 204
+// (eight heads of 64 197 / 311).  Short calls: 8 x 2,000 tokens of one head of 64 11.7 / 8.3.
 constexpr int kDirectSlice = 384;
 constexpr int64_t kTogetherBytes = 384 << 20;       // the cache's size, by max_len
 constexpr int threads_of(int producers) { return 32 * (kWarps + producers); }
@@ -141,7 +141,7 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4
 // A tile's V products are summed from zero, the smallest term first, and then added in fp32: MMAs cut
 // their sums instead of rounding them, and the cuts of an accumulator that runs through a long request add
 // up.  Outputs that are not the exact ones' rounding, one request of 131,072 tokens 0.7 % -> 0.02 % (0.3 %
-// with fp32 products and sums), 256 of 128 to 2,048 0.2 % -> 0.02 %.  At most 3 % slower (16 query heads on
+// with fp32 products and sums), 256 of 128 to 2,048 0.2 % -> 0.02 %.  At most 4 % slower (16 query heads on
 // 8 KV heads of 64, 64 x 10,000 tokens 254 -> 264 us), one KV head of 64, 64 x 40,000 tokens 141 -> 123.
 constexpr int kBlocks = 4;                          // of 16 features, summed beside one another
 __device__ __forceinline__ void add_tile(float (&acc)[4], const float (&sum)[4]) {
@@ -327,9 +327,10 @@ __device__ __forceinline__ void walk_begin(const SplitArgs& a, UnitWalk& w) {   
 // copy: with a loop over up to eight tiles, seven of them unused, the batch above took 1,203 us, with
 // the tile count fixed at compile time 840 us; without the consumers' arithmetic 826 us.
 // More than 8 query heads per KV head take two warps a head, each with 8 of them and its own read of
-// the head's K and V from shared memory: 4 x 40,000 tokens of H = 1024 with 16 query heads per KV head
-// 116 us at D = 128 and at 256, join included (0.84 of the copy rate; 8 query heads 108 us).  One warp
-// with two column tiles, whose accumulators spilled, reached 0.76 and 0.45.
+// the head's K and V from shared memory: 4 x 40,000 tokens with 16 query heads per KV head take, join
+// included, 116 us at D = 128 and 115 at 256 at H = 1024 (0.84 of the copy rate; 8 query heads 106 us), and
+// 221 and 208 us at H = 2048, where one warp with two column tiles, whose accumulators spilled, took 260
+// and 437.
 template <int D, int TILES, int NP, int HW>
 __global__ void __launch_bounds__(threads_of(NP), kCtasPerSm) attention_split_kernel(const __grid_constant__ SplitArgs a) {
   constexpr int KS = D / 16;
@@ -1253,10 +1254,10 @@ SplitPlan split_plan(int32_t H, int32_t n_req, int32_t max_len, int32_t n_heads,
   // groups as even as they can be, a stage's K and V within kStageBytes at 16 tokens; with fewer heads
   // than warps some warps share a head's tokens and the stage has more of them.
   pl.direct = pl.D <= 128 && H * 2 <= kDirectSlice;
-  // In a large cache the heads of a token have to be read together, or each read opens a DRAM row anew:
-  // two heads of 64 by one warp, else by warps that wait for one another.  64 requests, us without /
-  // with, one query head per KV head: two heads of 64, 1 GB 242 / 165 (the warps waiting: 216), 512 MB
-  // 95.5 / 88.3, 256 MB 49.8 / 49.6, 2 MB 4.8 / 6.2; three heads, 1 GB 226 / 203, 128 MB 31.6 / 33.2.
+  // In a large cache it pays to read the heads of a token together: two heads of 64 by one warp, else by
+  // warps that wait for one another.  64 requests, us without / with, one query head per KV head: two
+  // heads of 64, 1 GB 251 / 171 (the warps waiting: 216), 512 MB 101 / 90.8, 256 MB 49.7 / 50.1, 2 MB
+  // 4.0 / 5.6; three heads, 1 GB 246 / 201, 128 MB 31.5 / 32.8.
   const bool together = pl.direct && (int64_t)n_req * max_len * 4 * H >= kTogetherBytes;
   pl.pair = together && pl.D == 64 && n_kv == 2 && pl.group <= 8;
   pl.octets = pl.direct && pl.D == 64 ? 1 : (pl.group + 7) / 8;
