@@ -37,6 +37,7 @@ LORA_MAX_RANK = 64
 LORA_MAX_ADAPTERS = 16384
 LORA_MAX_TOKENS = 65536
 LORA_MAX_GROUP = 4
+LORA_MAX_TREE = 64
 LORA_NOALLOC_MAX_TOKENS = 128
 LORA_NOALLOC_MAX_H = 8192
 LORA_NOALLOC_SCRATCH_BYTES = 17 * 1024 * 1024
@@ -50,7 +51,9 @@ EXPORTED = ["lora_pool_create", "lora_pool_reserve", "lora_pool_release", "lora_
             "lora_adapter_ensure", "lora_pool_set_eviction", "lora_adapter_packed_size", "lora_adapter_pack",
             "lora_adapter_load_packed", "lora_adapter_wait", "lora_kv_grow", "lora_kv_free", "lora_kv_length",
             "lora_kv_table", "lora_kv_batch_table", "lora_attention_decode", "lora_kv_write",
-            "lora_attention_split_size", "lora_attention_split", "lora_kv_evict", "lora_kv_keep"]
+            "lora_attention_split_size", "lora_attention_split", "lora_kv_evict", "lora_kv_keep",
+            "lora_kv_append", "lora_attention_prompt_size", "lora_attention_prompt", "lora_attention_tree_size",
+            "lora_attention_tree"]
 KINDS = ("segments", "delta", "gemm", "scatter", "shrink", "attention", "kv")
 
 
@@ -132,6 +135,12 @@ def _load():
                                        I64, VP]),
         "lora_kv_evict": (I32, [VP, I32, VP, VP, I32, I32, VP, I32, I32, VP, VP, VP, VP, I32, VP]),
         "lora_kv_keep": (I32, [VP, I64, I32, I32, VP, I64]),
+        "lora_kv_append": (I32, [VP, I32, VP, VP, VP, I32, VP, I32, I32, VP, VP, VP, VP, VP]),
+        "lora_attention_prompt_size": (I64, [VP, I32, I32, I32, I32]),
+        "lora_attention_prompt": (I32, [VP, I32, VP, I32, VP, I64, VP, I64, VP, I64, VP, I64, I32, I32, VP, VP, I64, VP]),
+        "lora_attention_tree_size": (I64, [VP, I32, I32, I32, I32]),
+        "lora_attention_tree": (I32, [VP, I32, VP, VP, I32, I32, I32, VP, I32, VP, VP, I64, VP, I64, I32, I32, VP, VP, I64,
+                                      VP]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -380,6 +389,47 @@ def lora_kv_keep(pool, request_id: int, keep_host) -> None:
     if keep.ndim != 2:
         raise ValueError("keep_host must be [layers, n_keep]")
     _check(_load().lora_kv_keep(pool, request_id, keep.shape[0], keep.shape[1], _ptr(keep), keep.shape[1]))
+
+
+def lora_kv_append(pool, n_req: int, count_dev, old_len_dev, pages_dev, row_cap: int, table_dev, max_len: int, layers: int,
+                   new_len_dev, row_start_dev, row_req_dev, row_pos_dev, stream=None) -> None:
+    """Page table, lengths and slot maps of count_dev[r] new tokens per request; old_len_dev None: a new table."""
+    _check(_load().lora_kv_append(pool, n_req, _ptr(count_dev), _ptr(old_len_dev), _ptr(pages_dev), row_cap,
+                                  _ptr(table_dev), max_len, layers, _ptr(new_len_dev), _ptr(row_start_dev),
+                                  _ptr(row_req_dev), _ptr(row_pos_dev), _stream(stream)))
+
+
+def lora_attention_prompt_size(pool, n_seq: int, n_rows: int, n_heads: int, n_kv_heads: int) -> int:
+    n = _load().lora_attention_prompt_size(pool, n_seq, n_rows, n_heads, n_kv_heads)
+    if n < 0:
+        raise LoraError(int(n), lora_last_error())
+    return int(n)
+
+
+def lora_attention_prompt(pool, n_seq: int, seq_start_dev, n_rows: int, q_dev, k_dev, v_dev, out_dev, n_heads: int,
+                          n_kv_heads: int, workspace_dev, workspace_bytes: int, lse_dev=None, q_stride: int = 0,
+                          k_stride: int = 0, v_stride: int = 0, out_stride: int = 0, stream=None) -> None:
+    """Causal attention over packed prompts; row strides in elements (0: contiguous)."""
+    _check(_load().lora_attention_prompt(pool, n_seq, _ptr(seq_start_dev), n_rows, _ptr(q_dev), q_stride, _ptr(k_dev),
+                                         k_stride, _ptr(v_dev), v_stride, _ptr(out_dev), out_stride, n_heads, n_kv_heads,
+                                         _ptr(lse_dev), _ptr(workspace_dev), workspace_bytes, _stream(stream)))
+
+
+def lora_attention_tree_size(pool, n_req: int, max_len: int, n_heads: int, n_kv_heads: int) -> int:
+    n = _load().lora_attention_tree_size(pool, n_req, max_len, n_heads, n_kv_heads)
+    if n < 0:
+        raise LoraError(int(n), lora_last_error())
+    return int(n)
+
+
+def lora_attention_tree(pool, n_req: int, table_dev, seq_len_dev, max_len: int, layers: int, layer: int, node_start_dev,
+                        n_rows: int, mask_dev, q_dev, out_dev, n_heads: int, n_kv_heads: int, workspace_dev,
+                        workspace_bytes: int, lse_dev=None, q_stride: int = 0, out_stride: int = 0, stream=None) -> None:
+    """Attention of each request's drafted tokens, the last ones of its cache, under their 64-bit masks."""
+    _check(_load().lora_attention_tree(pool, n_req, _ptr(table_dev), _ptr(seq_len_dev), max_len, layers, layer,
+                                       _ptr(node_start_dev), n_rows, _ptr(mask_dev), _ptr(q_dev), q_stride, _ptr(out_dev),
+                                       out_stride, n_heads, n_kv_heads, _ptr(lse_dev), _ptr(workspace_dev),
+                                       workspace_bytes, _stream(stream)))
 
 
 def lora_adapter_refs(pool, adapter_id: int) -> int:

@@ -121,6 +121,127 @@ kv_write_packed_kernel(uint16_t* pool, int64_t num_pages, int32_t H, int32_t n_r
   }
 }
 
+// ---- page table and slot maps from token counts ----------------------------------------------------
+// A block of rows per CTA, and with a new table a block of its positions per further CTA.  Every CTA sums
+// the counts itself (a thread adds up n_req / 256 requests, one scan over the threads), so the call is one
+// launch; a row's request is then found by bisection over the threads and a walk over that thread's
+// requests.  Pages are moved 8 bytes (one layer's K and V) a thread, neighbours together.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendEntries = 2048;                       // table entries a CTA writes, about
+constexpr int kAppendMaxRows = 512;                        // rows a CTA takes, at most
+
+struct AppendArgs {
+  int32_t n_req;
+  const int32_t* count;
+  const int32_t* old_len;
+  const int2* pages;
+  int32_t row_cap;
+  int2* table;
+  int32_t max_len, layers;
+  int32_t* new_len;
+  int32_t* row_start;
+  int32_t* row_req;
+  int32_t* row_pos;
+  int32_t rows_per_cta, row_ctas;
+  int32_t* err;
+};
+
+__device__ __forceinline__ int32_t append_old(const AppendArgs& a, int r) {
+  return a.old_len ? min(max(a.old_len[r], 0), a.max_len) : 0;
+}
+
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
+  __shared__ int64_t before[kAppendThreads];               // rows of the requests of the threads before
+  __shared__ int64_t warp_sum[kAppendThreads / 32];
+  __shared__ int32_t req_s[kAppendMaxRows], pos_s[kAppendMaxRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait_then_release();
+  const int per = (a.n_req + kAppendThreads - 1) / kAppendThreads;
+  const int r0 = (int)min((int64_t)a.n_req, (int64_t)tid * per), r1 = min(a.n_req, r0 + per);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) mine += max(a.count[r], 0);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t start = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kAppendThreads / 32; ++w) start += w < warp ? warp_sum[w] : 0;
+  before[tid] = start;
+  __syncthreads();
+
+  if (blockIdx.x == 0) {                                   // lengths and row starts
+    for (int r = r0; r < r1; ++r) {
+      const int32_t c = a.count[r], old = append_old(a, r);
+      const int64_t room = min((int64_t)max(c, 0), max((int64_t)a.row_cap - start, (int64_t)0));   // rows that the arrays hold
+      if (c < 0 || (a.old_len && a.old_len[r] != old) || old + (int64_t)max(c, 0) > a.max_len || room < c)
+        flag_error(a.err, LORA_DEV_BAD_SEGMENT);
+      a.new_len[r] = (int32_t)min((int64_t)a.max_len, old + room);
+      a.row_start[r] = (int32_t)min((int64_t)a.row_cap, start);
+      start += max(c, 0);
+    }
+    if (tid == kAppendThreads - 1) a.row_start[a.n_req] = (int32_t)min((int64_t)a.row_cap, start);
+  }
+
+  if ((int)blockIdx.x < a.row_ctas) {
+    const int64_t t0 = (int64_t)blockIdx.x * a.rows_per_cta;
+    const int n = (int)min((int64_t)a.rows_per_cta, a.row_cap - t0);
+    for (int i = tid; i < n; i += kAppendThreads) {
+      const int64_t t = t0 + i;
+      int lo = 0;                                          // the last thread whose requests start at or before t
+#pragma unroll
+      for (int step = kAppendThreads / 2; step > 0; step >>= 1)
+        if (before[lo + step] <= t) lo += step;
+      int64_t s = before[lo];
+      int r = min((int64_t)a.n_req, (int64_t)lo * per);
+      const int end = min(a.n_req, r + per);
+      int32_t req = -1, pos = 0;
+      for (; r < end; ++r) {
+        const int32_t c = max(a.count[r], 0);
+        if (t < s + c) {
+          const int64_t p = append_old(a, r) + (t - s);
+          if (p < a.max_len) {
+            req = r;
+            pos = (int32_t)p;
+          }
+          break;
+        }
+        s += c;
+      }
+      req_s[i] = req;
+      pos_s[i] = pos;
+      a.row_req[t] = req;
+      a.row_pos[t] = pos;
+    }
+    __syncthreads();
+    const int entries = n * a.layers;
+    for (int e = tid; e < entries; e += kAppendThreads) {
+      const int i = e / a.layers;
+      if (req_s[i] >= 0)
+        a.table[((int64_t)req_s[i] * a.max_len + pos_s[i]) * a.layers + e - i * a.layers] = a.pages[t0 * a.layers + e];
+    }
+    return;
+  }
+  // a new table: -1 behind every request's tokens
+  const int64_t j0 = (int64_t)(blockIdx.x - a.row_ctas) * a.rows_per_cta, all = (int64_t)a.n_req * a.max_len;
+  const int n = (int)min((int64_t)a.rows_per_cta, all - j0);
+  for (int i = tid; i < n; i += kAppendThreads) {
+    const int r = (int)((j0 + i) / a.max_len), c = r / per;
+    int64_t s = before[c];
+    for (int x = c * per; x < r; ++x) s += max(a.count[x], 0);
+    const int64_t held = min((int64_t)max(a.count[r], 0), max((int64_t)a.row_cap - s, (int64_t)0));
+    req_s[i] = (j0 + i) - (int64_t)r * a.max_len >= held;
+  }
+  __syncthreads();
+  const int64_t entries = (int64_t)n * a.layers;
+  for (int64_t e = tid; e < entries; e += kAppendThreads)
+    if (req_s[(int)(e / a.layers)]) a.table[j0 * a.layers + e] = make_int2(-1, -1);
+}
+
 // ---- eviction ------------------------------------------------------------------------------------
 // Sort key of a weight: ascending with the value, -0 = +0, NaN = -infinity.  Keys of weights lie in
 // [0x007FFFFF, 0xFF800000]: outside are a token that stays in any case and one that is not there.
@@ -815,4 +936,51 @@ extern "C" int lora_kv_evict(lora_pool* p, int32_t n_req, const int32_t* table_d
     n_cta *= 2;
   return n_cta > 1 ? launch_evict_k<true>(p, a, n_cta, st)
                    : launch_evict_k<false>(p, a, 1, st);
+}
+
+extern "C" int lora_kv_append(lora_pool* p, int32_t n_req, const int32_t* count, const int32_t* old_len,
+                              const int32_t* pages, int32_t row_cap, int32_t* table_dev, int32_t max_len, int32_t layers,
+                              int32_t* new_len, int32_t* row_start, int32_t* row_req, int32_t* row_pos,
+                              lora_stream_t stream) {
+  if (!p || n_req < 0 || row_cap < 0 || max_len < 1 || layers < 1) return lora_fail(LORA_EINVAL, "lora_kv_append: bad arguments");
+  if (n_req > 65535) return lora_fail(LORA_EINVAL, "lora_kv_append: at most 65535 requests per call");
+  if (max_len > (1 << 30)) return lora_fail(LORA_EINVAL, "lora_kv_append: max_len is at most 2^30");
+  if (layers > (1 << 20)) return lora_fail(LORA_EINVAL, "lora_kv_append: at most 2^20 layers");
+  if (!row_start || (n_req > 0 && (!count || !table_dev || !new_len)) || (row_cap > 0 && (!pages || !row_req || !row_pos)))
+    return lora_fail(LORA_EINVAL, "lora_kv_append: null pointer");
+  if (((reinterpret_cast<uintptr_t>(table_dev) | reinterpret_cast<uintptr_t>(pages)) & 7) != 0)
+    return lora_fail(LORA_EINVAL, "lora_kv_append: table and pages must be 8-byte aligned");
+  if (((reinterpret_cast<uintptr_t>(count) | reinterpret_cast<uintptr_t>(old_len) | reinterpret_cast<uintptr_t>(new_len) |
+        reinterpret_cast<uintptr_t>(row_start) | reinterpret_cast<uintptr_t>(row_req) |
+        reinterpret_cast<uintptr_t>(row_pos)) & 3) != 0)
+    return lora_fail(LORA_EINVAL, "lora_kv_append: counts, lengths and rows must be 4-byte aligned");
+  if (n_req > 0 && (new_len == old_len || new_len == count || row_start == count || row_start == old_len ||
+                    row_start == new_len))
+    return lora_fail(LORA_EINVAL, "lora_kv_append: outputs must not be the inputs");
+  if (row_cap > 0 && (pages == table_dev || row_req == row_pos))
+    return lora_fail(LORA_EINVAL, "lora_kv_append: outputs must not be the inputs");
+  AppendArgs a{};
+  a.n_req = n_req;
+  a.count = count;
+  a.old_len = old_len;
+  a.pages = reinterpret_cast<const int2*>(pages);
+  a.row_cap = row_cap;
+  a.table = reinterpret_cast<int2*>(table_dev);
+  a.max_len = max_len;
+  a.layers = layers;
+  a.new_len = new_len;
+  a.row_start = row_start;
+  a.row_req = row_req;
+  a.row_pos = row_pos;
+  a.rows_per_cta = std::min(std::max(kAppendEntries / layers, 1), kAppendMaxRows);
+  const int64_t rest = old_len ? 0 : ((int64_t)n_req * max_len + a.rows_per_cta - 1) / a.rows_per_cta;
+  a.row_ctas = (int32_t)std::max(((int64_t)row_cap + a.rows_per_cta - 1) / a.rows_per_cta, (int64_t)1);
+  if (a.row_ctas + rest > INT32_MAX) return lora_fail(LORA_EINVAL, "lora_kv_append: the table is too large for one call");
+  if (p->planning) return lora_fail(LORA_EINVAL, "lora_kv_append: planning pool has no device state");
+  a.err = p->d_err;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope prof(p, LORA_KIND_KV, st);
+  const cudaError_t e = launch_pdl(!p->prof_on, kv_append_kernel, dim3((unsigned)(a.row_ctas + rest)), dim3(kAppendThreads), 0,
+                                   st, a);
+  return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_kv_append launch");
 }

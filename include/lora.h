@@ -285,6 +285,100 @@ int lora_kv_evict(lora_pool* pool, int32_t n_req, const int32_t* table_dev, cons
 int lora_kv_keep(lora_pool* pool, int64_t request_id, int32_t layers, int32_t n_keep, const int32_t* keep_host,
                  int64_t keep_stride);
 
+/*
+ * Page table, lengths and slot maps of a batch's new tokens, built on the device from the requests' token
+ * counts: request r gets count[r] tokens behind the old_len[r] that it has cached, and the batch's rows are
+ * the new tokens of all requests one behind another, request by request:
+ *     row_start[r] = sum of count[i], i < r   (row_start[n_req]: all rows);
+ *     row t of request r, i = t - row_start[r]:  row_req[t] = r,  row_pos[t] = old_len[r] + i,
+ *     table[r][old_len[r] + i][layer][K, V] = pages[t][layer][K, V];
+ *     new_len[r] = old_len[r] + count[r]
+ * which is what lora_kv_write, lora_attention_split, lora_attention_prompt (row_start as seq_start) and
+ * lora_attention_tree (row_start as node_start) take.  Device work only: it can be captured and replayed.
+ *   count      device int32 [n_req], >= 0;
+ *   old_len    device int32 [n_req], or NULL: nothing is cached and the table is built anew, -1 in every
+ *              entry that gets no page (otherwise other entries are left as they were);
+ *   pages      device int32 [row_cap][layers][2], as lora_kv_grow's page_ids for the requests in turn
+ *              (8-byte aligned; ids are passed through);
+ *   row_cap    rows that pages, row_req and row_pos hold, >= 0.  Rows at and past row_start[n_req] get
+ *              row_req = -1 (lora_kv_write skips them) and row_pos = 0;
+ *   table_dev  out: device int32 [n_req][max_len][layers][2] (8-byte aligned);
+ *   new_len    out: device int32 [n_req], not old_len;   row_start out: device int32 [n_req + 1];
+ *   row_req, row_pos  out: device int32 [row_cap].
+ * A negative count (taken as 0), an old length outside [0, max_len] (clamped), a token at or past max_len
+ * (its row gets row_req = -1 and its page goes nowhere) and rows past row_cap (dropped) set the device error
+ * word; new_len counts what the table holds.  At most 65535 requests; max_len at most 2^30.
+ */
+int lora_kv_append(lora_pool* pool, int32_t n_req, const int32_t* count, const int32_t* old_len, const int32_t* pages,
+                   int32_t row_cap, int32_t* table_dev, int32_t max_len, int32_t layers, int32_t* new_len,
+                   int32_t* row_start, int32_t* row_req, int32_t* row_pos, lora_stream_t stream);
+
+/*
+ * Attention over whole prompts, causal, before any token is decoded: the rows of q, k and v are the prompts'
+ * tokens, packed one behind another.  Per sequence s, its rows i >= j in [seq_start[s], seq_start[s + 1]), and
+ * query head h with KV head h / (n_heads / n_kv_heads) of width D = H / n_kv_heads (64, 128 or 256):
+ *     s_ij = q_{i,h} . k_j / sqrt(D),  lse_{i,h} = log sum_{j <= i} exp(s_ij),
+ *     out_{i,h} = sum_{j <= i} exp(s_ij - lse_{i,h}) v_j
+ *   seq_start  device int32 [n_seq + 1], ascending within [0, n_rows]; a sequence may be empty.  Rows
+ *              before seq_start[0] and from seq_start[n_seq] on belong to no sequence: nothing of them is
+ *              written;
+ *   n_rows     rows of q, k, v and out, 0 .. LORA_MAX_TOKENS;
+ *   q, out     device bf16, row t at t * q_stride / t * out_stride elements (0 = n_heads * D, else a
+ *              multiple of 8, at least that, at most 2^32); k, v device bf16, row t at t * k_stride /
+ *              t * v_stride (0 = H, else likewise, at least H): the q, k, v of one projection group, or
+ *              columns of a wider matrix.  All 16-byte aligned; out must be none of the inputs;
+ *   n_heads    a multiple of n_kv_heads, at most 16 query heads per KV head;
+ *   lse        nullable device fp32 [n_rows][n_heads];
+ *   workspace  device, 256-byte aligned, at least lora_attention_prompt_size(...) bytes for the same n_seq,
+ *              n_rows and heads.  Nothing in it needs a value before the call; calls that share it must be
+ *              ordered (two captured graphs that share it must not run at once).
+ * A row depends on its own sequence's rows up to itself alone, whatever stands in other rows.  Scores and sums
+ * are fp32; a weight enters the V product as bf16.  An infinite V gives that infinity where it is seen (NaN
+ * where both signs meet, or where its weight is below 2^-100 of the row's largest).  If no score of a row is
+ * above -infinity, out is 0 and lse -infinity.  Starts that descend or leave [0, n_rows] set the device error
+ * word and each is taken as the largest up to it, clamped.  At most 65535 sequences.
+ */
+int64_t lora_attention_prompt_size(const lora_pool* pool, int32_t n_seq, int32_t n_rows, int32_t n_heads,
+                                   int32_t n_kv_heads);
+int lora_attention_prompt(lora_pool* pool, int32_t n_seq, const int32_t* seq_start, int32_t n_rows, const void* q,
+                          int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* out,
+                          int64_t out_stride, int32_t n_heads, int32_t n_kv_heads, float* lse, void* workspace,
+                          int64_t workspace_bytes, lora_stream_t stream);
+
+/*
+ * Attention of drafted tokens over the KV cache: every request has a tree of up to LORA_MAX_TREE drafted
+ * tokens, whose K and V rows are the last of its cached tokens (lora_kv_write put them there).  Request r of
+ * n = seq_len[r] cached tokens has the nodes i of rows node_start[r] + i, m = node_start[r + 1] -
+ * node_start[r] of them, at positions n - m + i.  Node i sees every position below n - m, and n - m + j where
+ * bit j of its mask is set:
+ *     out_{i,h} = sum_j exp(s_ij - lse_{i,h}) V_j over the tokens that it sees, heads and s as for
+ *     lora_attention_split (one KV head per n_heads / n_kv_heads query heads, D = 64, 128 or 256)
+ * so a tree's mask holds the node itself and its ancestors, a chain's (the next tokens of one guess) bits
+ * 0 .. i, and one node of mask 1 is plain decode attention.
+ *   table_dev, seq_len_dev, max_len, layers, layer   as for lora_attention_split;
+ *   node_start device int32 [n_req + 1], ascending within [0, n_rows]; a request may have no node;
+ *   n_rows     rows of q, out and mask, >= 0;   mask: device uint64 [n_rows] (8-byte aligned);
+ *   q, out     device bf16, row t at t * q_stride / t * out_stride elements, as for lora_attention_prompt;
+ *   lse        nullable device fp32 [n_rows][n_heads];
+ *   workspace  device, 256-byte aligned, at least lora_attention_tree_size(...) bytes for the same n_req,
+ *              max_len and heads; as for lora_attention_prompt.
+ * A node that sees no token gets out = 0 and lse = -infinity; rows that belong to no request are left as they
+ * were.  A page id outside the pool sets the device error word and its token is skipped.  A length outside
+ * [0, max_len] is clamped, of more than LORA_MAX_TREE nodes the rest's rows are left as they were, nodes past
+ * the length have no position (n - m is taken as 0), and starts are treated as lora_attention_prompt's; each
+ * sets the error word.  Values and precision as for lora_attention_prompt; what a node does not see, and
+ * pages of no token, may hold anything.  Results do not depend on the order in which CTAs run.  At most 65535
+ * requests; max_len at most 2^30.
+ */
+#define LORA_MAX_TREE 64
+int64_t lora_attention_tree_size(const lora_pool* pool, int32_t n_req, int32_t max_len, int32_t n_heads,
+                                 int32_t n_kv_heads);
+int lora_attention_tree(lora_pool* pool, int32_t n_req, const int32_t* table_dev, const int32_t* seq_len_dev,
+                        int32_t max_len, int32_t layers, int32_t layer, const int32_t* node_start, int32_t n_rows,
+                        const uint64_t* mask, const void* q, int64_t q_stride, void* out, int64_t out_stride,
+                        int32_t n_heads, int32_t n_kv_heads, float* lse, void* workspace, int64_t workspace_bytes,
+                        lora_stream_t stream);
+
 /* Give back n reserved pages (appended to the free list in the order given).
  * LORA_EINVAL if any id is not currently reserved or appears twice (nothing released). */
 int lora_pool_release(lora_pool* pool, int64_t n, const int64_t* page_ids_host);
@@ -481,8 +575,8 @@ const char* lora_last_error(void);
 /*
  * Kernel accounting for benchmarks.  Every kernel this library launches for `pool` is counted
  * by kind: 0 segment build, 1 LoRA delta (shrink and expand), 2 base GEMM, 3 page scatter
- * (adapter loads), 4 shrink of the fused tiles of a prefill-shaped batch, 5 decode attention,
- * 6 KV page writes and evictions.
+ * (adapter loads), 4 shrink of the fused tiles of a prefill-shaped batch, 5 attention (decode,
+ * prompt, tree), 6 KV page writes, slot maps and evictions.
  * With profiling enabled, each launch is also bracketed by CUDA events recorded on the
  * stream it runs on (also inside a stream capture: the events then become graph nodes and
  * are re-recorded by every replay).  lora_profile_read synchronises those events and
