@@ -10,29 +10,35 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "tc_ptx.h"
 
 namespace {
 
 constexpr int kRowsMaxGroup = 16;                   // query heads per KV head
-// Weights are 2^(s - m - kShift), m the largest score: the sums of up to 2^24 weights times V stay within the
-// range of V.
-constexpr float kShift = 24.f;
+constexpr int kBlock = 128;                         // tokens of K and V at a time
+constexpr int kTileRows = 128;                      // query rows of a tile
+// Weights are 2^(s - m - kShift), where m is at most kSlack below the largest score so far: any m gives the
+// same softmax, and the sums of up to 2^(kShift - kSlack) weights times V stay within the range of V.  With
+// the slack a tile's sums are rescaled in few of its blocks.
+constexpr float kShift = 24.f, kSlack = 6.f;
 
 struct RowsArgs {
-  const uint16_t* q;
-  int64_t q_stride;
-  const uint16_t* k;                                // prompt: rows; tree: unused
-  int64_t k_stride;
-  const uint16_t* v;
-  int64_t v_stride;
   uint16_t* out;
   int64_t out_stride;
   float* lse;
-  int32_t n_req, n_rows, n_heads, n_kv;
+  int32_t n_req, n_rows, n_heads, n_kv, group;
+  int32_t npt;                                      // tokens (or nodes) of a tile: kTileRows / group
   const int32_t* start;                             // caller's row starts
   int32_t* bounds;                                  // workspace: the same, ascending within [0, n_rows]
+  float scale_log2;
+  int32_t* err;
+  // prompt
+  const uint16_t* v;
+  int64_t v_stride;
+  int32_t* n_items;                                 // workspace: work items per KV head, and they: (sequence, tile pair)
+  int2* items;
   // tree
   const uint16_t* pool;
   int64_t num_pages;
@@ -41,31 +47,57 @@ struct RowsArgs {
   const int32_t* seq_len;
   int32_t max_len, layers, layer;
   const uint64_t* mask;
-  float scale_log2;
-  int32_t* err;
+  int64_t* prefix;                                  // workspace: [n_req + 1] units of the requests before, per KV head
+  int4* ws_start;                                   // [parts] (head, request, pair, last part) of a segment cut behind this part
+  float2* ws_ml;                                    // [2 parts][slot_rows] m and l of a partial
+  float* ws_acc;                                    // [2 parts][slot_rows][D]
+  int32_t parts, slot_rows;
 };
 
+// Exclusive sum over the block's threads, and the total.
+template <typename T>
+__device__ __forceinline__ T block_exclusive(T v, T* part, T& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = blockDim.x >> 5;
+  T incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  T before = 0;
+  total = 0;
+  for (int w = 0; w < n; ++w) {
+    before += w < warp ? part[w] : 0;
+    total += part[w];
+  }
+  return before + incl - v;
+}
+
 // Row starts as the running maximum of the caller's, clamped into [0, n_rows]: sequences never overlap.
-__global__ void __launch_bounds__(1024) rows_bounds_kernel(const RowsArgs a) {
-  __shared__ int32_t part[32];
-  pdl_wait_then_release();
+constexpr int kPlanThreads = 1024;
+__device__ void plan_bounds(const RowsArgs& a) {
+  __shared__ int32_t part[kPlanThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int32_t before = 0;
-  for (int i0 = 0; i0 <= a.n_req; i0 += 1024) {
+  for (int i0 = 0; i0 <= a.n_req; i0 += kPlanThreads) {
     const int i = i0 + threadIdx.x;
-    const int32_t x = i <= a.n_req ? a.start[i] : 0;
+    const int32_t x = i <= a.n_req ? a.start[i] : INT32_MIN;
     int32_t m = x;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t y = __shfl_up_sync(0xffffffffu, m, o);
       if (lane >= o) m = max(m, y);
     }
     if (lane == 31) part[warp] = m;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) m = max(m, part[w]);
     m = max(m, before);
-    int32_t all = before;
-    for (int w = 0; w < 32; ++w) all = max(all, part[w]);
-    before = all;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) m = max(m, part[w]);
+      before = max(before, part[w]);
+    }
     const int32_t b = min(max(m, 0), a.n_rows);
     if (i <= a.n_req) {
       if (b != x) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
@@ -75,72 +107,872 @@ __global__ void __launch_bounds__(1024) rows_bounds_kernel(const RowsArgs a) {
   }
 }
 
-// One warp per (row, query head), a running maximum and sum over the tokens one by one.
-template <int D, bool kTree>
-__global__ void __launch_bounds__(128) rows_simple_kernel(const RowsArgs a) {
-  constexpr int E = D / 32;
+// The prompts' work items, the longest first: item (s, L) is the L-th tile pair of sequence s, and it reads
+// about L + 1 times as much as the first.  Counting sort by L; the order within one L does not matter.
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const RowsArgs a, int32_t per_item, int32_t levels) {
+  extern __shared__ int32_t cursor[];                      // [levels]
+  __shared__ int32_t part[kPlanThreads / 32];
+  const int tid = threadIdx.x;
+  for (int i = tid; i < levels; i += kPlanThreads) cursor[i] = 0;
   pdl_wait_then_release();
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int64_t row = item / a.n_heads;
-  const int h = (int)(item % a.n_heads), kvh = h / (a.n_heads / a.n_kv);
-  if (row >= a.n_rows) return;
-  int lo = 0, hi = a.n_req;                         // the request whose rows hold this one: bounds[lo] <= row < bounds[lo + 1]
-  if (row < a.bounds[0] || row >= a.bounds[a.n_req]) return;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.bounds[mid] <= row) lo = mid; else hi = mid;
+  plan_bounds(a);
+  for (int s = tid; s < a.n_req; s += kPlanThreads) {
+    const int n = (a.bounds[s + 1] - a.bounds[s] + per_item - 1) / per_item;
+    if (n > 0) atomicAdd(&cursor[n - 1], 1);
   }
-  const int first = a.bounds[lo], node = (int)row - first;
-  int n = node + 1, base = 0;
-  uint64_t mask = ~0ull;
-  if (kTree) {
-    const int raw = a.seq_len[lo], len = min(max(raw, 0), a.max_len), m = a.bounds[lo + 1] - first;
-    if (raw != len || m > LORA_MAX_TREE || m > len) {
-      if (lane == 0) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
-    }
-    if (node >= LORA_MAX_TREE) return;
-    n = len;
-    base = max(len - min(m, LORA_MAX_TREE), 0);
-    mask = a.mask[row];
+  __syncthreads();
+  // from the top level down: sequences with this level, then items above it
+  const int per = (levels + kPlanThreads - 1) / kPlanThreads, hi = levels - tid * per, lo = max(hi - per, 0);
+  int32_t mine = 0, total;
+  for (int L = hi - 1; L >= lo; --L) mine += cursor[L];
+  int32_t run = block_exclusive<int32_t>(mine, part, total);
+  int32_t items = 0;
+  for (int L = hi - 1; L >= lo; --L) {
+    run += cursor[L];
+    cursor[L] = run;
+    items += run;
   }
-  float q[E], acc[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) {
-    q[e] = __uint_as_float((uint32_t)a.q[row * a.q_stride + (int64_t)h * D + e * 32 + lane] << 16);
-    acc[e] = 0.f;
+  int32_t at = block_exclusive<int32_t>(items, part, total);
+  for (int L = hi - 1; L >= lo; --L) {
+    const int32_t n = cursor[L];
+    cursor[L] = at;
+    at += n;
   }
-  for (int j = 0; j < n; ++j) {
-    const uint16_t *k, *v;
-    if (kTree) {
-      const int2 pg = a.table[((int64_t)lo * a.max_len + j) * a.layers + a.layer];
-      if (pg.x < 0 || pg.x >= a.num_pages || pg.y < 0 || pg.y >= a.num_pages) {
-        if (lane == 0) flag_error(a.err, LORA_DEV_BAD_PAGE);
-        continue;
-      }
-      if (j >= base && !((mask >> (j - base)) & 1)) continue;
-      k = a.pool + (int64_t)pg.x * a.H + kvh * D;
-      v = a.pool + (int64_t)pg.y * a.H + kvh * D;
-    } else {
-      k = a.k + (first + j) * a.k_stride + kvh * D;
-      v = a.v + (first + j) * a.v_stride + kvh * D;
-    }
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], __uint_as_float((uint32_t)k[e * 32 + lane] << 16), s);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s), ms = mn == -INFINITY ? 0.f : mn, c = m == mn ? 1.f : exp2f(m - ms), p = exp2f(s - ms - kShift);
-    m = mn;
-    l = l * c + p;
-    for (int e = 0; e < E; ++e) {
-      const float x = __uint_as_float((uint32_t)v[e * 32 + lane] << 16);
-      acc[e] = (c == 1.f ? acc[e] : acc[e] * c) + (p == 0.f ? 0.f : p * x);
-    }
+  if (tid == 0) *a.n_items = total;
+  __syncthreads();
+  const int warp = tid >> 5, lane = tid & 31;
+  for (int s = warp; s < a.n_req; s += kPlanThreads / 32) {
+    const int n = (a.bounds[s + 1] - a.bounds[s] + per_item - 1) / per_item;
+    for (int L = lane; L < n; L += 32) a.items[atomicAdd(&cursor[L], 1)] = make_int2(s, L);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int e = 0; e < E; ++e) a.out[row * a.out_stride + (int64_t)h * D + e * 32 + lane] = f32_to_bf16_rn(acc[e] * inv);
-  if (a.lse && lane == 0) a.lse[row * a.n_heads + h] = l == 0.f ? -INFINITY : (m + kShift + log2f(l)) * 0.6931471805599453f;
 }
 
+// Of a tree request: its nodes that count, its cached tokens, and its units (blocks of tokens times tile pairs).
+struct TreeReq {
+  int row0, nodes, len, base, blocks, pairs;
+};
+template <int NT>
+__device__ __forceinline__ TreeReq tree_request(const RowsArgs& a, int r) {
+  TreeReq q;
+  q.row0 = a.bounds[r];
+  q.nodes = min(a.bounds[r + 1] - q.row0, LORA_MAX_TREE);
+  q.len = min(max(a.seq_len[r], 0), a.max_len);
+  q.base = max(q.len - q.nodes, 0);
+  q.blocks = max((q.len + kBlock - 1) / kBlock, 1);
+  q.pairs = (q.nodes + NT * a.npt - 1) / (NT * a.npt);
+  return q;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const RowsArgs a) {
+  __shared__ int64_t part[kPlanThreads / 32];
+  pdl_wait_then_release();
+  plan_bounds(a);
+  int64_t before = 0;
+  for (int r0 = 0; r0 < a.n_req; r0 += kPlanThreads) {
+    const int r = r0 + threadIdx.x;
+    int64_t units = 0, total;
+    if (r < a.n_req) {
+      const TreeReq q = tree_request<NT>(a, r);
+      const int m = a.bounds[r + 1] - q.row0;
+      if (a.seq_len[r] != q.len || m > LORA_MAX_TREE || m > q.len) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
+      units = (int64_t)q.blocks * q.pairs;
+    }
+    const int64_t at = before + block_exclusive<int64_t>(units, part, total);
+    if (r < a.n_req) a.prefix[r] = at;
+    before += total;
+  }
+  if (threadIdx.x == 0) a.prefix[a.n_req] = before;
+}
+
+// ---- the kernel ----------------------------------------------------------------------------------
+template <int D_, bool kTree_>
+struct Geo {
+  static constexpr int D = D_;
+  static constexpr bool kTree = kTree_;
+  static constexpr int NT = D == 256 ? 1 : 2;              // row tiles of an item
+  static constexpr int NB = 3 - NT;                        // score buffers of a tile
+  static constexpr int DS = D < 128 ? D : 128;             // features of a ring slot
+  static constexpr int PD = D / DS;                        // slots of a block of K or of V
+  static constexpr int PANELS = DS / 64;                   // 128-byte wide panels of a slot
+  static constexpr uint32_t kPanel = kBlock * 128;
+  static constexpr uint32_t kSlot = PANELS * kPanel;
+  static constexpr uint32_t kQTile = kTileRows * D * 2;
+  static constexpr int NS = D == 64 ? 10 : 5;              // slots
+  static constexpr int kSoftWarps = 4 * NT;
+  static constexpr int kMmaWarp = kSoftWarps;
+  static constexpr int kLoadWarp = kSoftWarps + 1;         // prompt: one TMA warp; tree: four copying warps
+  static constexpr int kLoadWarps = kTree ? 4 : 1;
+  static constexpr int kScanWarp = kLoadWarp + 1;          // prompt: two warps
+  static constexpr int kScanWarps = 2;
+  static constexpr int kThreads = 32 * (kSoftWarps + 1 + (kTree ? kLoadWarps : 1 + kScanWarps));
+  static constexpr int kLag = NS - 2;                      // tree: slots whose copies a warp has on their way
+  static constexpr uint32_t kData = NT * kQTile + NS * kSlot;
+  // barriers: full and empty per slot, landed and clean per guarded V slot in turn; Q full and empty; scores and
+  // weights per buffer; sums full and drained per tile; products
+  static constexpr int kBars = 4 * NS + 2 + 4 + 4 + 1;
+  static constexpr int kWordsRing = 8;                     // blocks whose token masks are kept
+  static constexpr uint32_t kSmem = 1024 + kData + kBars * 8 + kWordsRing * 16 + 64;
+  static constexpr uint32_t kTmemO = 256;                  // scores in columns [0, 256), sums behind them
+};
+
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two fp32 values in one register pair: x * s + b, and sums.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// A bf16 pair's halves with an exponent of all ones (infinity, NaN): 0x8000 and 0x80000000.
+__device__ __forceinline__ uint32_t non_finite2(uint32_t u) { return ((u & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t u, uint32_t bad) {
+  return u & ~((bad & 0x8000u ? 0xFFFFu : 0u) | (bad & 0x80000000u ? 0xFFFF0000u : 0u));
+}
+// 16 bytes of V in shared memory without their infinities and NaN; whether there were any.
+__device__ __forceinline__ bool clean16(uint32_t addr) {
+  uint4 x = lds128(addr);
+  const uint4 b = make_uint4(non_finite2(x.x), non_finite2(x.y), non_finite2(x.z), non_finite2(x.w));
+  if ((b.x | b.y | b.z | b.w) == 0) return false;
+  x.x = finite_or_zero(x.x, b.x);
+  x.y = finite_or_zero(x.y, b.y);
+  x.z = finite_or_zero(x.z, b.z);
+  x.w = finite_or_zero(x.w, b.w);
+  sts128(addr, x);
+  return true;
+}
+
+// What a CTA works on at a time: the rows of a tile pair of one sequence and KV head, over some blocks of its tokens.
+struct Item {
+  int head;                      // KV head
+  int req;
+  int row0, pos0, count;         // first row of the item, that row's token (prompt) or node (tree), rows' tokens or nodes left from it on
+  int b0, b1;                    // blocks of tokens
+  int guard;                     // first block in which some row does not see every token
+  // tree
+  int len, base;                 // cached tokens, the first node's position
+  int blocks;                    // of all parts
+  int slot;                      // partial, or -1: the item has all blocks
+};
+
+// The items of a CTA, one after another; every warp walks them by itself.
+template <typename G>
+struct Walk {
+  int64_t u, u1, per_head;       // tree: units left are [u, u1)
+  int64_t w, step, all;          // prompt: turn, CTAs, items times heads
+  __device__ __forceinline__ Walk(const RowsArgs& a) {
+    if (G::kTree) {
+      per_head = a.prefix[a.n_req];
+      const int64_t units = per_head * a.n_kv, parts = min((int64_t)a.parts, units), p = blockIdx.x;
+      u = p < parts ? p * units / parts : 0;
+      u1 = p < parts ? (p + 1) * units / parts : 0;
+    } else {
+      w = 0;
+      step = gridDim.x;
+      all = (int64_t)*a.n_items * a.n_kv;
+    }
+  }
+  // All lanes of a warp take part.
+  __device__ __forceinline__ bool next(const RowsArgs& a, Item& it) {
+    if (G::kTree) {
+      if (u >= u1) return false;
+      it.head = (int)(u / per_head);
+      const int64_t x = u - it.head * per_head;
+      int lo = 0, hi = a.n_req;                            // prefix[lo] <= x < prefix[hi]: 32 places a turn
+      const int lane = threadIdx.x & 31;
+      while (hi - lo > 1) {
+        const int stride = (hi - lo + 31) / 32, at = lo + lane * stride;
+        const unsigned in = __ballot_sync(0xffffffffu, at < hi && a.prefix[min(at, hi)] <= x);
+        lo += (31 - __clz(in)) * stride;
+        hi = min(hi, lo + stride);
+      }
+      const TreeReq q = tree_request<G::NT>(a, lo);
+      const int y = (int)(x - a.prefix[lo]), pair = y / q.blocks;
+      it.req = lo;
+      it.b0 = y - pair * q.blocks;
+      it.b1 = (int)min((int64_t)q.blocks, it.b0 + (u1 - u));
+      it.pos0 = pair * G::NT * a.npt;
+      it.row0 = q.row0 + it.pos0;
+      it.count = q.nodes - it.pos0;
+      it.len = q.len;
+      it.base = q.base;
+      it.guard = q.base / kBlock;
+      it.blocks = q.blocks;
+      it.slot = it.b0 == 0 && it.b1 == q.blocks ? -1 : 2 * (int)blockIdx.x + (it.b0 == 0 ? 1 : 0);
+      u += it.b1 - it.b0;
+      return true;
+    }
+    // There and back over the CTAs, so that none has the longer item of every turn.
+    const int64_t x = w * step + ((w & 1) ? step - 1 - blockIdx.x : blockIdx.x);
+    if (x >= all) return false;
+    ++w;
+    it.head = (int)(x % a.n_kv);
+    const int2 e = a.items[x / a.n_kv];
+    const int first = a.bounds[e.x], n = a.bounds[e.x + 1] - first;
+    it.req = e.x;
+    it.pos0 = e.y * G::NT * a.npt;
+    it.row0 = first + it.pos0;
+    it.count = n - it.pos0;
+    it.b0 = 0;
+    it.b1 = (it.pos0 + min(it.count, G::NT * a.npt) + kBlock - 1) / kBlock;
+    it.guard = it.pos0 / kBlock;
+    it.slot = -1;
+    it.blocks = it.b1;
+    it.len = n;
+    it.base = 0;
+    return true;
+  }
+  // Blocks of tile t, counted from b0: none if it has no row.
+  static __device__ __forceinline__ int blocks(const RowsArgs& a, const Item& it, int t) {
+    const int left = it.count - t * a.npt;
+    if (left <= 0) return 0;
+    return G::kTree ? it.b1 - it.b0 : (it.pos0 + t * a.npt + min(left, a.npt) + kBlock - 1) / kBlock;
+  }
+};
+
+// Place of a block's K and V in the order of the ring's loads, in slots, for n blocks.  Two tiles: K0 V0 K1 V1 ...;
+// one tile with two score buffers: K0 K1 V0 K2 V1 ...
+template <typename G>
+__device__ __forceinline__ int seq_k(int i) {
+  return (G::NB == 1 ? 2 * i : i == 0 ? 0 : 2 * i - 1) * G::PD;
+}
+template <typename G>
+__device__ __forceinline__ int seq_v(int i, int n) {
+  return (G::NB == 1 || i == n - 1 ? 2 * i + 1 : 2 * i + 2) * G::PD;
+}
+
+template <typename G>
+__global__ void __launch_bounds__(G::kThreads, 1)
+rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ RowsArgs a) {
+  constexpr int D = G::D, NT = G::NT, NB = G::NB, PD = G::PD, NS = G::NS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t tmem_s;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t s_q = base, s_ring = base + NT * G::kQTile, s_bar = base + G::kData;
+  const uint32_t bar_full = s_bar, bar_empty = bar_full + 8 * NS, bar_clean = bar_empty + 8 * NS;
+  const uint32_t bar_landed = bar_clean + 8 * NS;
+  const uint32_t bar_qfull = bar_landed + 8 * NS, bar_qempty = bar_qfull + 8, bar_scores = bar_qempty + 8;
+  const uint32_t bar_weights = bar_scores + 16, bar_sums = bar_weights + 16, bar_drained = bar_sums + 16;
+  const uint32_t bar_product = bar_drained + 16;
+  uint8_t* tail = smem_raw + (base - smem_u32(smem_raw)) + G::kData + G::kBars * 8 + (G::kBars & 1) * 8;
+  volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(tail);        // [kWordsRing][4]: a block's tokens that have data
+  volatile int* first_bad = reinterpret_cast<volatile int*>(words + G::kWordsRing * 4);   // this CTA's first item with V cleared
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bar_full + 8 * s, G::kTree ? G::kLoadWarps : 1);
+      mbar_init(bar_empty + 8 * s, 1);
+      mbar_init(bar_clean + 8 * s, G::kScanWarps);
+      mbar_init(bar_landed + 8 * s, 1);
+    }
+    mbar_init(bar_qfull, 1);
+    mbar_init(bar_qempty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_scores + 8 * i, 1);
+      mbar_init(bar_weights + 8 * i, 4);
+      mbar_init(bar_sums + 8 * i, 1);
+      mbar_init(bar_drained + 8 * i, 4);
+    }
+    mbar_init(bar_product, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *first_bad = INT32_MAX;
+  }
+  pdl_wait_then_release();                                 // TMEM is taken after it: an earlier kernel may still need its own
+  if (warp == G::kMmaWarp) {
+    tmem_alloc(smem_u32(&tmem_s), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  Walk<G> walk(a);
+  Item it;
+  bool ok = true;
+
+  if (warp < G::kSoftWarps) {
+    // ---- softmax: a thread per row ----
+    const int t = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const int tok = row / a.group, g = row - tok * a.group;
+    const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+    uint32_t use[2] = {0, 0}, items_t = 0, products = 0, blocks_done = 0;
+    for (int n_item = 0; ok && walk.next(a, it); ++n_item) {
+      const int nb = Walk<G>::blocks(a, it, t), nb_all = it.b1 - it.b0;
+      if (nb == 0) {
+        blocks_done += nb_all;
+        continue;
+      }
+      const int left = min(it.count - t * a.npt, a.npt);   // tokens (nodes) of the tile
+      const bool live = tok < left;
+      const int pos = it.pos0 + t * a.npt + min(tok, left - 1);
+      uint64_t mask = 0;
+      if (G::kTree) mask = a.mask[it.row0 + t * a.npt + min(tok, left - 1)];
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < nb; ++i) {
+        const int x = NB == 1 ? t : (i & 1);
+        const uint32_t scores = tmem + (uint32_t)(x * 128) + lane_off;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_scores + 8 * x, use[x] & 1))) {
+          ok = false;
+          break;
+        }
+        ++use[x];
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(scores + 32 * c, s[c]);
+        tmem_ld_wait();
+        const int j0 = (it.b0 + i) * kBlock;
+        if (G::kTree) {
+          uint32_t vis[4];
+          bool all = true;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int j = j0 + 32 * c, d = j - it.base;
+            uint32_t v = words[((blocks_done + i) % G::kWordsRing) * 4 + c];
+            if (d + 32 > 0) v &= d >= 64 ? 0u : d >= 0 ? (uint32_t)(mask >> d) : ((uint32_t)mask << -d) | ((1u << -d) - 1u);
+            vis[c] = v;
+            all = all && v == 0xffffffffu;
+          }
+          if (__any_sync(0xffffffffu, !all)) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (!((vis[c / 32] >> (c % 32)) & 1)) s[c / 32][c % 32] = 0xff800000u;
+          }
+        } else if (it.b0 + i >= (it.pos0 + t * a.npt) / kBlock) {
+          const int last = pos - j0;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > last) s[c / 32][c % 32] = 0xff800000u;
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c / 32][c % 32]));
+        const float bm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+        const bool grow = bm > m + kSlack;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? bm : m, c = grow ? ex2(m - mn) : 1.f;
+          l *= c;
+          m = mn;
+          if (i > 0) {
+            if (NB == 2 && !__all_sync(0xffffffffu, mbar_wait(bar_product, (products + i - 1) & 1))) {
+              ok = false;
+              break;
+            }
+            const uint32_t sums = tmem + G::kTmemO + (uint32_t)(t * D) + lane_off;
+            const uint64_t c2 = pack2(c, c);
+            tc_fence_after();
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(sums + d, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const uint64_t y = mul2((uint64_t)o[e] | ((uint64_t)o[e + 1] << 32), c2);
+                o[e] = (uint32_t)y;
+                o[e + 1] = (uint32_t)(y >> 32);
+              }
+              tmem_st_32x32b_x32(sums + d, o);
+            }
+          }
+        }
+        const float shift = -((m == -INFINITY ? 0.f : m) + kShift);
+        const uint64_t shift2 = pack2(shift, shift);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int e = 64 * half + 2 * c;
+            const uint64_t y = fma2((uint64_t)s[e / 32][e % 32] | ((uint64_t)s[e / 32][e % 32 + 1] << 32), scale2, shift2);
+            const float p0 = ex2(lo2(y)), p1 = ex2(hi2(y));
+            sum[c & 1] = add2(sum[c & 1], pack2(p0, p1));
+            p[c] = pack_bf16(p0, p1);
+          }
+          tmem_st_32x32b_x32(scores + 32 * half, p);
+        }
+        sum[0] = add2(sum[0], sum[1]);
+        l += lo2(sum[0]) + hi2(sum[0]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_weights + 8 * x);
+      }
+      if (!ok) break;
+      products += nb;
+      blocks_done += nb_all;
+      // ---- the tile's outputs ----
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_sums + 8 * t, items_t & 1))) {
+        ok = false;
+        break;
+      }
+      ++items_t;
+      tc_fence_after();
+      const bool dirty = n_item >= *first_bad;
+      const bool part = it.slot >= 0;
+      const int64_t orow = it.row0 + t * a.npt + tok;
+      const int head = it.head * a.group + g;
+      const int64_t prow = (int64_t)it.slot * a.slot_rows + t * kTileRows + row;
+      const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const uint32_t sums = tmem + G::kTmemO + (uint32_t)(t * D) + lane_off;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(sums + d, o);
+        tmem_ld_wait();
+        float y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv;
+        if (dirty && live && l != 0.f) {
+          // infinities and NaN of V in the blocks that not every row sees whole were left out of the products
+          const int j1 = G::kTree ? min(it.b1 * kBlock, it.len) : pos + 1;
+          for (int j = max(it.b0, it.guard) * kBlock; j < j1; ++j) {
+            const uint16_t* v;
+            if (G::kTree) {
+              if (j >= it.base && !((mask >> (j - it.base)) & 1)) continue;
+              const int2 pg = a.table[((int64_t)it.req * a.max_len + j) * a.layers + a.layer];
+              if (pg.x < 0 || pg.x >= a.num_pages || pg.y < 0 || pg.y >= a.num_pages) continue;
+              v = a.pool + (int64_t)pg.y * a.H + it.head * D + d;
+            } else {
+              v = a.v + (it.row0 - it.pos0 + j) * a.v_stride + it.head * D + d;
+            }
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t b = v[e];
+              if ((b & 0x7F80u) == 0x7F80u) {
+#pragma unroll
+                for (int f = 0; f < 32; ++f)
+                  if (f == e) y[f] += __uint_as_float(b << 16);
+              }
+            }
+          }
+        }
+        if (live && part) {
+          float4* dst = reinterpret_cast<float4*>(a.ws_acc + prow * D + d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + orow * a.out_stride + (int64_t)head * D + d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]),
+                                pack_bf16(y[8 * e + 4], y[8 * e + 5]), pack_bf16(y[8 * e + 6], y[8 * e + 7]));
+        }
+      }
+      if (live && part) a.ws_ml[prow] = make_float2(m, l);
+      if (live && !part && a.lse)
+        a.lse[orow * a.n_heads + head] = l == 0.f ? -INFINITY : (m + kShift + log2f(l)) * 0.6931471805599453f;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_drained + 8 * t);
+    }
+  } else if (warp == G::kMmaWarp) {
+    // ---- products: lane 0 issues ----
+    constexpr uint32_t kIdescS = make_idesc_bf16(kTileRows, kBlock);
+    constexpr uint32_t kIdescO = make_idesc_bf16(kTileRows, G::DS) | (1u << 16);        // B (V) is MN-major
+    uint32_t use[2] = {0, 0}, items_t[2] = {0, 0}, guarded = 0;         // guarded: V slots that were scanned so far
+    int sq = 0;                                            // ring slots of the items before
+    if (G::kTree && lane == 0) a.ws_start[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    const auto wait_lane0 = [&](uint32_t bar, uint32_t parity) { return lane != 0 || mbar_wait(bar, parity); };
+    for (int n_item = 0; ok && walk.next(a, it); ++n_item) {
+      int nb[2] = {Walk<G>::blocks(a, it, 0), NT == 2 ? Walk<G>::blocks(a, it, 1) : 0};
+      const int n = it.b1 - it.b0;
+      if (G::kTree && lane == 0) {                         // Q of the item
+        if (it.slot >= 0 && it.b0 == 0) {                  // cut behind this part: the join goes on to the part of its last unit
+          const int64_t units = walk.per_head * a.n_kv, parts = min((int64_t)a.parts, units), x = walk.u - it.b1 + it.blocks;
+          a.ws_start[blockIdx.x] = make_int4(it.head, it.req, it.pos0 / (NT * a.npt), (int)((x * parts - 1) / units));
+        }
+        ok = mbar_wait(bar_qempty, (n_item & 1) ^ 1);
+        if (ok) {
+          const uint32_t bytes = (uint32_t)(a.npt * a.group * 128 * (D / 64));
+          mbar_arrive_expect_tx(bar_qfull, nb[1] > 0 ? 2 * bytes : bytes);
+          for (int t = 0; t < NT; ++t)
+            for (int p = 0; p < D / 64 && nb[t] > 0; ++p)
+              tma_load_3d(s_q + t * G::kQTile + p * G::kPanel, &tm_q, 64 * p, it.head * a.group, it.row0 + t * a.npt, bar_qfull);
+        }
+      }
+      ok = ok && wait_lane0(bar_qfull, n_item & 1);
+      const auto slot = [&](int seq) { return (uint32_t)((sq + seq) % NS); };
+      const auto phase = [&](int seq) { return (uint32_t)((sq + seq) / NS) & 1u; };
+      const auto issue_scores = [&](int t, int x, int i) {               // scores buffer x = Q_t K_i^T
+        for (int p = 0; p < PD; ++p) {
+          const int q = seq_k<G>(i) + p;
+          if (!mbar_wait(bar_full + 8 * slot(q), phase(q))) return false;
+          tc_fence_after();
+          const uint64_t qd = sw128_kmajor_desc(s_q + t * G::kQTile + p * G::PANELS * G::kPanel);
+          const uint64_t kd = sw128_kmajor_desc(s_ring + slot(q) * G::kSlot);
+#pragma unroll
+          for (int k = 0; k < G::DS / 16; ++k) {
+            const uint64_t off = ((k / 4) * G::kPanel + (k % 4) * 32) >> 4;
+            mma_bf16_ss(tmem + x * 128, qd + off, kd + off, kIdescS, p > 0 || k > 0);
+          }
+        }
+        mma_commit(bar_scores + 8 * x);
+        return true;
+      };
+      const auto issue_product = [&](int t, int x, int i) {              // sums of tile t += weights buffer x V_i
+        for (int p = 0; p < PD; ++p) {
+          const int q = seq_v<G>(i, n) + p;
+          const uint32_t s = slot(q);
+          if (!G::kTree && it.b0 + i >= it.guard) {
+            const uint32_t n_th = guarded + p;             // landed and cleared of infinities
+            if (!mbar_wait(bar_clean + 8 * (n_th % NS), (n_th / NS) & 1)) return false;
+          } else if (!mbar_wait(bar_full + 8 * s, phase(q))) {
+            return false;
+          }
+          tc_fence_after();
+          const uint64_t vd = sw128_mnmajor_desc(s_ring + s * G::kSlot, G::kPanel, 1024);
+#pragma unroll
+          for (int k = 0; k < kBlock / 16; ++k)
+            mma_bf16_ts(tmem + G::kTmemO + t * D + p * G::DS, tmem + x * 128 + k * 8, vd + ((k * 2048) >> 4), kIdescO, i > 0 || k > 0);
+        }
+        return true;
+      };
+      const auto release = [&](int seq) {
+        for (int p = 0; p < PD; ++p) mma_commit(bar_empty + 8 * slot(seq + p));
+      };
+      if (ok && lane == 0) {
+        tc_fence_after();
+        if (NB == 1) {
+          for (int t = 0; t < NT && ok; ++t)
+            if (nb[t] > 0) ok = issue_scores(t, t, 0);
+          if (ok) release(seq_k<G>(0));
+          if (ok && n == 1) mma_commit(bar_qempty);
+          for (int i = 0; i < n && ok; ++i) {
+            for (int t = 0; t < NT && ok; ++t) {
+              if (i >= nb[t]) continue;
+              ok = mbar_wait(bar_weights + 8 * t, use[t]++ & 1);
+              if (ok && i == 0) ok = mbar_wait(bar_drained + 8 * t, (items_t[t]++ & 1) ^ 1);
+              tc_fence_after();
+              ok = ok && issue_product(t, t, i);
+              if (ok && i + 1 == nb[t]) mma_commit(bar_sums + 8 * t);
+              if (ok && i + 1 < nb[t]) ok = issue_scores(t, t, i + 1);
+            }
+            if (!ok) break;
+            if (!G::kTree && it.b0 + i >= it.guard) guarded += PD;
+            release(seq_v<G>(i, n));
+            if (i + 1 < n) release(seq_k<G>(i + 1));
+            if (i + 2 == n) mma_commit(bar_qempty);
+          }
+        } else {
+          for (int i = 0; i < 2 && i < n && ok; ++i) {
+            ok = issue_scores(0, i, i);
+            if (ok) release(seq_k<G>(i));
+          }
+          if (ok && n <= 2) mma_commit(bar_qempty);
+          for (int i = 0; i < n && ok; ++i) {
+            const int x = i & 1;
+            ok = mbar_wait(bar_weights + 8 * x, use[x]++ & 1);
+            if (ok && i == 0) ok = mbar_wait(bar_drained, (items_t[0]++ & 1) ^ 1);
+            tc_fence_after();
+            ok = ok && issue_product(0, x, i);
+            if (!ok) break;
+            if (!G::kTree && it.b0 + i >= it.guard) guarded += PD;
+            release(seq_v<G>(i, n));
+            mma_commit(bar_product);
+            if (i + 1 == n) mma_commit(bar_sums);
+            if (i + 2 < n) {
+              ok = issue_scores(0, x, i + 2);
+              if (ok) release(seq_k<G>(i + 2));
+              if (ok && i + 3 == n) mma_commit(bar_qempty);
+            }
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      sq += 2 * PD * n;
+    }
+  } else if (!G::kTree && warp == G::kLoadWarp) {
+    // ---- prompt: TMA loads ----
+    int sq = 0;
+    uint32_t guarded = 0;
+    for (int n_item = 0; ok && walk.next(a, it); ++n_item) {
+      const int n = it.b1 - it.b0, first = it.row0 - it.pos0;
+      if (lane == 0) {
+        ok = mbar_wait(bar_qempty, (n_item & 1) ^ 1);
+        if (ok) {
+          const bool two = NT == 2 && Walk<G>::blocks(a, it, 1) > 0;
+          const uint32_t bytes = (uint32_t)(a.npt * a.group * 128 * (D / 64));
+          mbar_arrive_expect_tx(bar_qfull, two ? 2 * bytes : bytes);
+          for (int t = 0; t < (two ? 2 : 1); ++t)
+            for (int p = 0; p < D / 64; ++p)
+              tma_load_3d(s_q + t * G::kQTile + p * G::kPanel, &tm_q, 64 * p, it.head * a.group, it.row0 + t * a.npt, bar_qfull);
+        }
+        int seq = 0;
+        const auto load = [&](const CUtensorMap* map, int i) {
+          for (int p = 0; p < PD && ok; ++p, ++seq) {
+            const uint32_t s = (uint32_t)((sq + seq) % NS);
+            ok = mbar_wait(bar_empty + 8 * s, ((uint32_t)((sq + seq) / NS) & 1u) ^ 1u);
+            if (!ok) return;
+            uint32_t bar = bar_full + 8 * s;
+            if (map == &tm_v && it.b0 + i >= it.guard) {   // goes through the scan: the slot's own phase ends at once
+              mbar_arrive(bar);
+              bar = bar_landed + 8 * (guarded++ % NS);
+            }
+            mbar_arrive_expect_tx(bar, G::kSlot);
+            for (int c = 0; c < G::PANELS; ++c)
+              tma_load_2d_plain(s_ring + s * G::kSlot + c * G::kPanel, map, it.head * D + p * G::DS + 64 * c,
+                                first + (it.b0 + i) * kBlock, bar);
+          }
+        };
+        if (ok) load(&tm_k, 0);
+        for (int i = 0; i < n && ok; ++i) {
+          if (NB == 2) {
+            if (i + 1 < n) load(&tm_k, i + 1);
+            if (ok) load(&tm_v, i);
+          } else {
+            load(&tm_v, i);
+            if (ok && i + 1 < n) load(&tm_k, i + 1);
+          }
+        }
+        if (!ok) {                                         // wait for the copies in flight: the CTA may leave
+          for (int c = 0; c < NS; ++c) {
+            const int q = sq + seq - 1 - c;
+            if (q >= 0) (void)mbar_wait(bar_full + 8 * (q % NS), (uint32_t)(q / NS) & 1u);
+          }
+          for (uint32_t c = guarded > NS ? guarded - NS : 0; c < guarded; ++c)
+            (void)mbar_wait(bar_landed + 8 * (c % NS), (c / NS) & 1);
+          (void)mbar_wait(bar_qfull, n_item & 1);
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      sq += 2 * PD * n;
+    }
+  } else if (!G::kTree) {
+    // ---- prompt: V blocks of which a row does not see every token are cleared of infinities and NaN, whose
+    // products with the weights 0 would be NaN; the tile's outputs get those that a row does see ----
+    const int w = warp - G::kScanWarp;
+    int sq = 0;
+    uint32_t guarded = 0;
+    for (int n_item = 0; ok && walk.next(a, it); ++n_item) {
+      const int n = it.b1 - it.b0;
+      bool any = false;
+      for (int i = max(it.guard - it.b0, 0); i < n && ok; ++i)
+        for (int p = 0; p < PD && ok; ++p) {
+          const int q = sq + seq_v<G>(i, n) + p;
+          const uint32_t s = (uint32_t)(q % NS);
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_landed + 8 * (guarded % NS), (guarded / NS) & 1));
+          if (!ok) break;
+          const uint32_t at = s_ring + s * G::kSlot + w * (G::kSlot / 2) + lane * 16;
+          bool bad = false;
+#pragma unroll 8
+          for (uint32_t o = 0; o < G::kSlot / 2; o += 512) bad |= clean16(at + o);
+          any |= bad;
+          if (__any_sync(0xffffffffu, any)) {
+            if (lane == 0) atomicMin(const_cast<int*>(first_bad), n_item);
+            fence_proxy_async_shared();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_clean + 8 * (guarded % NS));
+          ++guarded;
+        }
+      sq += 2 * PD * n;
+    }
+  } else {
+    // ---- tree: rows of K and V from their pages, 16 bytes a lane, each warp 32 of a block's tokens ----
+    const int w = warp - G::kLoadWarp;
+    constexpr int kChunks = G::DS / 8, kRowsAt = 32 / kChunks;          // 16-byte chunks of a slot's row; rows at a time
+    const int chunk = lane % kChunks, sub = lane / kChunks;
+    int k = 0;                                             // slots issued
+    uint32_t guard_hist = 0;                               // of the slots on their way, a bit each: V to be cleared
+    const auto row_addr = [&](uint32_t s, int r) {
+      return s_ring + s * G::kSlot + (uint32_t)(chunk >> 3) * G::kPanel + (uint32_t)(r >> 3) * 1024u + sw128_offset(r, chunk & 7);
+    };
+    // Slot j's copies of this warp have landed; it belongs to the given item or a later one.
+    const auto signal = [&](int j, bool guard, int item) {
+      const uint32_t s = (uint32_t)(j % NS);
+      if (guard) {
+        bool bad = false;
+#pragma unroll 4
+        for (int i = 0; i < 32 / kRowsAt; ++i) bad |= clean16(row_addr(s, 32 * w + i * kRowsAt + sub));
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicMin(const_cast<int*>(first_bad), item);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_full + 8 * s);
+    };
+    int blocks_done = 0, n_item = 0;
+    for (; ok && walk.next(a, it); ++n_item) {
+      const int n = it.b1 - it.b0;
+      const auto entry = [&](int i) {                      // this lane's token of block i
+        const int j = (it.b0 + i) * kBlock + 32 * w + lane;
+        return i < n && j < it.len ? a.table[((int64_t)it.req * a.max_len + j) * a.layers + a.layer] : make_int2(-2, -2);
+      };
+      const auto checked = [&](int2 e, int i) {            // -1: no data
+        if (e.x >= 0 && e.x < a.num_pages && e.y >= 0 && e.y < a.num_pages) return e;
+        const int j = (it.b0 + i) * kBlock + 32 * w + lane;
+        if (i < n && j < it.len) flag_error(a.err, LORA_DEV_BAD_PAGE);
+        return make_int2(-1, -1);
+      };
+      const auto load = [&](int page, bool is_v, int i, int2 e) {
+        for (int p = 0; p < PD && ok; ++p, ++k) {
+          const uint32_t s = (uint32_t)(k % NS);
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ((uint32_t)(k / NS) & 1u) ^ 1u));
+          if (!ok) return;
+          if (!is_v && p == 0) {
+            const unsigned has = __ballot_sync(0xffffffffu, e.x >= 0);
+            if (lane == 0) words[((blocks_done + i) % G::kWordsRing) * 4 + w] = has;
+          }
+          const int64_t col = (int64_t)it.head * D + p * G::DS + chunk * 8;
+#pragma unroll
+          for (int r = 0; r < 32 / kRowsAt; ++r) {
+            const int own = r * kRowsAt + sub, pg = __shfl_sync(0xffffffffu, page, own);
+            cp_async_16(row_addr(s, 32 * w + own), a.pool + (pg >= 0 ? (int64_t)pg * a.H + col : 0), pg >= 0);
+          }
+          cp_async_commit();
+          if (k >= G::kLag) {
+            cp_async_wait<G::kLag>();
+            signal(k - G::kLag, (guard_hist >> (G::kLag - 1)) & 1, n_item - G::kLag);
+          }
+          guard_hist = guard_hist << 1 | (is_v && it.b0 + i >= it.guard ? 1u : 0u);
+        }
+      };
+      int2 e0 = checked(entry(0), 0), e1 = entry(1);
+      load(e0.x, false, 0, e0);
+      for (int i = 0; i < n && ok; ++i) {
+        const int2 e2 = entry(i + 2);
+        e1 = checked(e1, i + 1);
+        if (NB == 2) {
+          if (i + 1 < n) load(e1.x, false, i + 1, e1);
+          if (ok) load(e0.y, true, i, e0);
+        } else {
+          load(e0.y, true, i, e0);
+          if (ok && i + 1 < n) load(e1.x, false, i + 1, e1);
+        }
+        e0 = e1;
+        e1 = e2;
+      }
+      blocks_done += n;
+    }
+    // the last slots
+    const auto drain = [&](auto self, auto left) {
+      constexpr int r = decltype(left)::value;
+      cp_async_wait<r>();
+      if (ok && k - 1 - r >= 0) signal(k - 1 - r, (guard_hist >> r) & 1, n_item - 1 - r);
+      if constexpr (r > 0) self(self, std::integral_constant<int, r - 1>{});
+    };
+    drain(drain, std::integral_constant<int, G::kLag - 1>{});
+  }
+  if (!ok && lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == G::kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// ---- joining a segment's partials ------------------------------------------------------------------
+// Segments that lie in several parts: block (p, y) takes the one that begins in part p and goes on behind it, a
+// warp per row.  m = max m_i, l = sum l_i 2^(m_i - m), out = sum o_i 2^(m_i - m) / l, in the parts' order.
+constexpr int kJoinWarps = 8;
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ RowsArgs a) {
+  constexpr int E = D / 32;
+  pdl_wait_then_release();
+  const int p = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 rec = a.ws_start[p];
+  if (rec.x < 0) return;
+  const TreeReq q = tree_request<NT>(a, rec.y);
+  const int pos0 = rec.z * NT * a.npt, rows = min(q.nodes - pos0, NT * a.npt) * a.group;
+  for (int x = blockIdx.y * kJoinWarps + warp; x < rows; x += gridDim.y * kJoinWarps) {
+    const int node = x / a.group, g = x - node * a.group, t = node / a.npt;
+    const int64_t at = t * kTileRows + (node - t * a.npt) * a.group + g;
+    const auto slot = [&](int i) { return (2 * (int64_t)i + (i == p ? 1 : 0)) * a.slot_rows + at; };
+    float m = -INFINITY;
+    for (int i = p + lane; i <= rec.w; i += 32) m = fmaxf(m, a.ws_ml[slot(i)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ms = m == -INFINITY ? 0.f : m;
+    float l = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int i0 = p; i0 <= rec.w; i0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (i0 + lane <= rec.w) ml = a.ws_ml[slot(i0 + lane)];
+      const float c_own = ex2(ml.x - ms);
+      const int n = min(32, rec.w - i0 + 1);
+      for (int b = 0; b < n; ++b) {
+        const float c = __shfl_sync(0xffffffffu, c_own, b);
+        l = fmaf(__shfl_sync(0xffffffffu, ml.y, b), c, l);
+        if (c == 0.f) continue;
+        const float* src = a.ws_acc + slot(i0 + b) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(src + e);
+          acc[e] = fmaf(v.x, c, acc[e]);
+          acc[e + 1] = fmaf(v.y, c, acc[e + 1]);
+        }
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t row = q.row0 + pos0 + node;
+    const int head = rec.x * a.group + g;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * a.out_stride + (int64_t)head * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = l == 0.f ? 0u : pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[row * a.n_heads + head] = l == 0.f ? -INFINITY : (m + kShift + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+// ---- host side -------------------------------------------------------------------------------------
 int check_heads(const std::string& fn, const lora_pool* p, int32_t n_req, int32_t n_heads, int32_t n_kv) {
   if (!p || n_req < 0 || n_heads < 1 || n_kv < 1) return lora_fail(LORA_EINVAL, fn + ": bad arguments");
   if (n_req > 65535) return lora_fail(LORA_EINVAL, fn + ": at most 65535 sequences per call");
@@ -172,23 +1004,112 @@ int check_workspace(const std::string& fn, const void* ws, int64_t bytes, int64_
   return LORA_OK;
 }
 
-int64_t prompt_bytes(int32_t n_seq) { return (int64_t)align256(((size_t)n_seq + 1) * 4); }
-int64_t tree_bytes(int32_t n_req) { return (int64_t)align256(((size_t)n_req + 1) * 4); }
 
-template <bool kTree>
-int launch_rows(const lora_pool* p, const RowsArgs& a, const char* what, cudaStream_t st) {
-  const int D = p->H / a.n_kv;
+int encode_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+               const cuuint32_t* box) {
+  auto fn = get_encode_fn();
+  if (!fn) return lora_fail(LORA_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return lora_fail(LORA_ECUDA, "cuTensorMapEncodeTiled failed with code " + std::to_string((int)r));
+  return LORA_OK;
+}
+// Query rows [row][head][feature]: a box is 64 features of one KV head's query heads of a tile's tokens.
+int encode_q(CUtensorMap* map, const void* q, int D, int n_heads, int64_t n_rows, int64_t stride, int group, int npt) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)n_heads, (cuuint64_t)n_rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)npt};
+  return encode_map(map, q, 3, dims, strides, box);
+}
+int encode_kv(CUtensorMap* map, const void* k, int H, int64_t n_rows, int64_t stride) {
+  const cuuint64_t dims[2] = {(cuuint64_t)H, (cuuint64_t)n_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {64, kBlock};
+  return encode_map(map, k, 2, dims, strides, box);
+}
+
+int tiles_of(int D) { return D == 256 ? 1 : 2; }
+
+// Workspaces; every array starts on a 256-byte boundary.
+struct PromptLayout {
+  size_t bounds, n_items, items, total;
+  int32_t per_item, levels;
+};
+PromptLayout prompt_layout(int D, int32_t n_seq, int32_t n_rows, int32_t group) {
+  PromptLayout L{};
+  L.per_item = tiles_of(D) * (kTileRows / group);
+  L.levels = (n_rows + L.per_item - 1) / L.per_item;
+  size_t off = 0;
+  L.bounds = off;   off = align256(off + ((size_t)n_seq + 1) * 4);
+  L.n_items = off;  off = align256(off + 4);
+  L.items = off;    off = align256(off + ((size_t)n_rows / L.per_item + n_seq) * sizeof(int2));
+  L.total = off;
+  return L;
+}
+struct TreeLayout {
+  size_t bounds, prefix, start, ml, acc, total;
+  int32_t parts, slot_rows;
+};
+TreeLayout tree_layout(int D, int32_t n_req, int32_t group) {
+  TreeLayout L{};
+  L.parts = device_sm_count();
+  L.slot_rows = kTileRows / group >= LORA_MAX_TREE ? LORA_MAX_TREE * group : tiles_of(D) * kTileRows;
+  const size_t slots = 2 * (size_t)L.parts * L.slot_rows;
+  size_t off = 0;
+  L.bounds = off;  off = align256(off + ((size_t)n_req + 1) * 4);
+  L.prefix = off;  off = align256(off + ((size_t)n_req + 1) * 8);
+  L.start = off;   off = align256(off + (size_t)L.parts * sizeof(int4));
+  L.ml = off;      off = align256(off + slots * sizeof(float2));
+  L.acc = off;     off = align256(off + slots * D * 4);
+  L.total = off;
+  return L;
+}
+
+template <typename G>
+int launch_rows(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                int ctas, const char* what, cudaStream_t st) {
+  static DeviceFlags flags;
+  const int rc = ensure_smem_attr(flags, &rows_kernel<G>, (int)G::kSmem, what);
+  if (rc != LORA_OK) return rc;
+  ProfScope prof(p, LORA_KIND_ATTENTION, st);
+  const cudaError_t e = launch_pdl(!p->prof_on, rows_kernel<G>, dim3(ctas), dim3(G::kThreads), G::kSmem, st, q, k, v, a);
+  return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, what);
+}
+
+int launch_prompt(const lora_pool* p, const RowsArgs& a, const PromptLayout& L, const CUtensorMap& q, const CUtensorMap& k,
+                  const CUtensorMap& v, cudaStream_t st) {
+  const char* what = "lora_attention_prompt launch";
   cudaError_t e;
   {
     ProfScope prof(p, LORA_KIND_ATTENTION, st);
-    e = launch_pdl(!p->prof_on, rows_bounds_kernel, dim3(1), dim3(1024), 0, st, a);
+    e = launch_pdl(!p->prof_on, prompt_plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)L.levels * 4, st, a, L.per_item, L.levels);
   }
   if (e != cudaSuccess) return lora_cuda_fail(e, what);
+  const int64_t most = ((int64_t)a.n_rows / L.per_item + a.n_req) * a.n_kv;
+  const int ctas = (int)std::min<int64_t>(device_sm_count(), most);
+  switch (p->H / a.n_kv) {
+    case 64: return launch_rows<Geo<64, false>>(p, a, q, k, v, ctas, what, st);
+    case 128: return launch_rows<Geo<128, false>>(p, a, q, k, v, ctas, what, st);
+    default: return launch_rows<Geo<256, false>>(p, a, q, k, v, ctas, what, st);
+  }
+}
+
+template <int D>
+int launch_tree(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, cudaStream_t st) {
+  using G = Geo<D, true>;
+  const char* what = "lora_attention_tree launch";
+  cudaError_t e;
+  {
+    ProfScope prof(p, LORA_KIND_ATTENTION, st);
+    e = launch_pdl(!p->prof_on, tree_plan_kernel<G::NT>, dim3(1), dim3(kPlanThreads), 0, st, a);
+  }
+  if (e != cudaSuccess) return lora_cuda_fail(e, what);
+  const int rc = launch_rows<G>(p, a, q, q, q, a.parts, what, st);
+  if (rc != LORA_OK) return rc;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
-  const dim3 grid((unsigned)(((int64_t)a.n_rows * a.n_heads + 3) / 4));
-  e = D == 64    ? launch_pdl(!p->prof_on, rows_simple_kernel<64, kTree>, grid, dim3(128), 0, st, a)
-      : D == 128 ? launch_pdl(!p->prof_on, rows_simple_kernel<128, kTree>, grid, dim3(128), 0, st, a)
-                 : launch_pdl(!p->prof_on, rows_simple_kernel<256, kTree>, grid, dim3(128), 0, st, a);
+  e = launch_pdl(!p->prof_on, tree_join_kernel<D, G::NT>, dim3(a.parts, 8), dim3(32 * kJoinWarps), 0, st, a);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, what);
 }
 
@@ -201,7 +1122,7 @@ extern "C" int64_t lora_attention_prompt_size(const lora_pool* p, int32_t n_seq,
   if (rc != LORA_OK) return rc;
   if (n_rows < 0 || n_rows > LORA_MAX_TOKENS)
     return lora_fail(LORA_EINVAL, fn + ": n_rows must lie in [0, " + std::to_string(LORA_MAX_TOKENS) + "]");
-  return prompt_bytes(n_seq);
+  return (int64_t)prompt_layout(p->H / n_kv_heads, n_seq, n_rows, n_heads / n_kv_heads).total;
 }
 
 extern "C" int lora_attention_prompt(lora_pool* p, int32_t n_seq, const int32_t* seq_start, int32_t n_rows, const void* q,
@@ -221,17 +1142,19 @@ extern "C" int lora_attention_prompt(lora_pool* p, int32_t n_seq, const int32_t*
   if (some && (out == q || out == k || out == v)) return lora_fail(LORA_EINVAL, fn + ": out must not alias q, k or v");
   if (((reinterpret_cast<uintptr_t>(seq_start) | reinterpret_cast<uintptr_t>(lse)) & 3) != 0)
     return lora_fail(LORA_EINVAL, fn + ": starts and lse must be 4-byte aligned");
-  rc = check_workspace(fn, workspace, some ? workspace_bytes : prompt_bytes(n_seq), prompt_bytes(n_seq));
+  const int D = p->H / n_kv_heads, group = n_heads / n_kv_heads;
+  const PromptLayout L = prompt_layout(D, n_seq, n_rows, group);
+  rc = check_workspace(fn, workspace, workspace_bytes, some ? (int64_t)L.total : 0);
   if (rc != LORA_OK) return rc;
   if (p->planning) return lora_fail(LORA_EINVAL, fn + ": planning pool has no device state");
   if (!some) return LORA_OK;
+  CUtensorMap tm_q, tm_k, tm_v;
+  rc = encode_q(&tm_q, q, D, n_heads, n_rows, q_stride, group, kTileRows / group);
+  if (rc == LORA_OK) rc = encode_kv(&tm_k, k, p->H, n_rows, k_stride);
+  if (rc == LORA_OK) rc = encode_kv(&tm_v, v, p->H, n_rows, v_stride);
+  if (rc != LORA_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
   RowsArgs a{};
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_stride = q_stride;
-  a.k = static_cast<const uint16_t*>(k);
-  a.k_stride = k_stride;
-  a.v = static_cast<const uint16_t*>(v);
-  a.v_stride = v_stride;
   a.out = static_cast<uint16_t*>(out);
   a.out_stride = out_stride;
   a.lse = lse;
@@ -239,11 +1162,17 @@ extern "C" int lora_attention_prompt(lora_pool* p, int32_t n_seq, const int32_t*
   a.n_rows = n_rows;
   a.n_heads = n_heads;
   a.n_kv = n_kv_heads;
+  a.group = group;
+  a.npt = kTileRows / group;
   a.start = seq_start;
-  a.bounds = static_cast<int32_t*>(workspace);
-  a.scale_log2 = 1.4426950408889634f / std::sqrt((float)(p->H / n_kv_heads));
+  a.bounds = reinterpret_cast<int32_t*>(ws + L.bounds);
+  a.scale_log2 = 1.4426950408889634f / std::sqrt((float)D);
   a.err = p->d_err;
-  return launch_rows<false>(p, a, "lora_attention_prompt launch", reinterpret_cast<cudaStream_t>(stream));
+  a.v = static_cast<const uint16_t*>(v);
+  a.v_stride = v_stride;
+  a.n_items = reinterpret_cast<int32_t*>(ws + L.n_items);
+  a.items = reinterpret_cast<int2*>(ws + L.items);
+  return launch_prompt(p, a, L, tm_q, tm_k, tm_v, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int64_t lora_attention_tree_size(const lora_pool* p, int32_t n_req, int32_t max_len, int32_t n_heads,
@@ -252,7 +1181,8 @@ extern "C" int64_t lora_attention_tree_size(const lora_pool* p, int32_t n_req, i
   const int rc = check_heads(fn, p, n_req, n_heads, n_kv_heads);
   if (rc != LORA_OK) return rc;
   if (max_len < 1 || max_len > (1 << 30)) return lora_fail(LORA_EINVAL, fn + ": max_len must lie in [1, 2^30]");
-  return tree_bytes(n_req);
+  if (p->planning) return lora_fail(LORA_EINVAL, fn + ": planning pool has no device state");
+  return (int64_t)tree_layout(p->H / n_kv_heads, n_req, n_heads / n_kv_heads).total;
 }
 
 extern "C" int lora_attention_tree(lora_pool* p, int32_t n_req, const int32_t* table_dev, const int32_t* seq_len_dev,
@@ -277,13 +1207,17 @@ extern "C" int lora_attention_tree(lora_pool* p, int32_t n_req, const int32_t* t
     return lora_fail(LORA_EINVAL, fn + ": table and mask must be 8-byte aligned");
   if (((reinterpret_cast<uintptr_t>(seq_len_dev) | reinterpret_cast<uintptr_t>(node_start) | reinterpret_cast<uintptr_t>(lse)) & 3) != 0)
     return lora_fail(LORA_EINVAL, fn + ": lengths, starts and lse must be 4-byte aligned");
-  rc = check_workspace(fn, workspace, some ? workspace_bytes : tree_bytes(n_req), tree_bytes(n_req));
-  if (rc != LORA_OK) return rc;
   if (p->planning) return lora_fail(LORA_EINVAL, fn + ": planning pool has no device state");
+  const int D = p->H / n_kv_heads, group = n_heads / n_kv_heads;
+  const TreeLayout L = tree_layout(D, n_req, group);
+  rc = check_workspace(fn, workspace, workspace_bytes, some ? (int64_t)L.total : 0);
+  if (rc != LORA_OK) return rc;
   if (!some) return LORA_OK;
+  CUtensorMap tm_q;
+  rc = encode_q(&tm_q, q, D, n_heads, n_rows, q_stride, group, kTileRows / group);
+  if (rc != LORA_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
   RowsArgs a{};
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_stride = q_stride;
   a.out = static_cast<uint16_t*>(out);
   a.out_stride = out_stride;
   a.lse = lse;
@@ -291,8 +1225,12 @@ extern "C" int lora_attention_tree(lora_pool* p, int32_t n_req, const int32_t* t
   a.n_rows = n_rows;
   a.n_heads = n_heads;
   a.n_kv = n_kv_heads;
+  a.group = group;
+  a.npt = kTileRows / group;
   a.start = node_start;
-  a.bounds = static_cast<int32_t*>(workspace);
+  a.bounds = reinterpret_cast<int32_t*>(ws + L.bounds);
+  a.scale_log2 = 1.4426950408889634f / std::sqrt((float)D);
+  a.err = p->d_err;
   a.pool = static_cast<const uint16_t*>(p->pool_dev);
   a.num_pages = p->num_pages;
   a.H = p->H;
@@ -302,7 +1240,16 @@ extern "C" int lora_attention_tree(lora_pool* p, int32_t n_req, const int32_t* t
   a.layers = layers;
   a.layer = layer;
   a.mask = mask;
-  a.scale_log2 = 1.4426950408889634f / std::sqrt((float)(p->H / n_kv_heads));
-  a.err = p->d_err;
-  return launch_rows<true>(p, a, "lora_attention_tree launch", reinterpret_cast<cudaStream_t>(stream));
+  a.prefix = reinterpret_cast<int64_t*>(ws + L.prefix);
+  a.ws_start = reinterpret_cast<int4*>(ws + L.start);
+  a.ws_ml = reinterpret_cast<float2*>(ws + L.ml);
+  a.ws_acc = reinterpret_cast<float*>(ws + L.acc);
+  a.parts = L.parts;
+  a.slot_rows = L.slot_rows;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  switch (D) {
+    case 64: return launch_tree<64>(p, a, tm_q, st);
+    case 128: return launch_tree<128>(p, a, tm_q, st);
+    default: return launch_tree<256>(p, a, tm_q, st);
+  }
 }
