@@ -201,11 +201,14 @@ struct Geo {
   static constexpr int NS = D == 64 ? 10 : 5;              // slots
   static constexpr int kSoftWarps = 4 * NT;
   static constexpr int kMmaWarp = kSoftWarps;
-  static constexpr int kLoadWarp = kSoftWarps + 1;         // prompt: one TMA warp; tree: four copying warps
+  static constexpr int kLoadWarp = kSoftWarps + (kTree ? 4 : 1);   // prompt: one TMA warp; tree: four copying warps
   static constexpr int kLoadWarps = kTree ? 4 : 1;
   static constexpr int kScanWarp = kLoadWarp + 1;          // prompt: two warps
   static constexpr int kScanWarps = 2;
-  static constexpr int kThreads = 32 * (kSoftWarps + 1 + (kTree ? kLoadWarps : 1 + kScanWarps));
+  static constexpr int kThreads = 32 * (kSoftWarps + (kTree ? 8 : 4));       // whole warpgroups: they trade registers
+  // Registers a thread: a softmax thread holds a row of scores.  Launch 128 or 168 (D = 256: 168 or 255).
+  static constexpr int kSoftRegs = NT == 1 ? 232 : kTree ? 192 : 208;
+  static constexpr int kOtherRegs = NT == 1 ? (kTree ? 136 : 232) : kTree ? 64 : 88;
   static constexpr int kLag = NS - 2;                      // tree: slots whose copies a warp has on their way
   static constexpr uint32_t kData = NT * kQTile + NS * kSlot;
   // barriers: full and empty per slot, landed and clean per guarded V slot in turn; Q full and empty; scores and
@@ -448,6 +451,11 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   Item it;
   bool ok = true;
 
+  if (warp < G::kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftRegs));
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+  }
   if (warp < G::kSoftWarps) {
     // ---- softmax: a thread per row ----
     const int t = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
@@ -798,7 +806,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       ok = __all_sync(0xffffffffu, ok);
       sq += 2 * PD * n;
     }
-  } else if (!G::kTree) {
+  } else if (!G::kTree && warp >= G::kScanWarp) {
     // ---- prompt: V blocks of which a row does not see every token are cleared of infinities and NaN, whose
     // products with the weights 0 would be NaN; the tile's outputs get those that a row does see ----
     const int w = warp - G::kScanWarp;
@@ -828,7 +836,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
       sq += 2 * PD * n;
     }
-  } else {
+  } else if (G::kTree && warp >= G::kLoadWarp) {
     // ---- tree: rows of K and V from their pages, 16 bytes a lane, each warp 32 of a block's tokens ----
     const int w = warp - G::kLoadWarp;
     constexpr int kChunks = G::DS / 8, kRowsAt = 32 / kChunks;          // 16-byte chunks of a slot's row; rows at a time
