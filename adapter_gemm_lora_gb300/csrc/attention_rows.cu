@@ -212,8 +212,8 @@ struct Geo {
   static constexpr int kLag = NS - 2;                      // tree: slots whose copies a warp has on their way
   static constexpr uint32_t kData = NT * kQTile + NS * kSlot;
   // barriers: full and empty per slot, landed and clean per guarded V slot in turn; Q full and empty; scores and
-  // weights per buffer; sums full and drained per tile; products
-  static constexpr int kBars = 4 * NS + 2 + 4 + 4 + 1;
+  // weights (two halves) per buffer; sums full and drained per tile; products
+  static constexpr int kBars = 4 * NS + 2 + 2 + 4 + 4 + 1;
   static constexpr int kWordsRing = 8;                     // blocks whose token masks are kept
   static constexpr uint32_t kSmem = 1024 + kData + kBars * 8 + kWordsRing * 16 + 64;
   static constexpr uint32_t kTmemO = 256;                  // scores in columns [0, 256), sums behind them
@@ -246,9 +246,21 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
+// One thread of the warp, the same every time.  The compiler knows that a branch on it leaves one thread and keeps
+// descriptors in uniform registers: eight MMAs issue in 80 cycles, behind a branch on the lane's number in 490.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {      // NaN counts as missing
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -390,6 +402,23 @@ struct Walk {
   }
 };
 
+// Where a role stands in the ring.
+template <int NS>
+struct Ring {
+  uint32_t at, phase;
+  __device__ __forceinline__ void next() {
+    if (++at == NS) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void skip() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) next();
+  }
+};
+
 // Place of a block's K and V in the order of the ring's loads, in slots, for n blocks.  Two tiles: K0 V0 K1 V1 ...;
 // one tile with two score buffers: K0 K1 V0 K2 V1 ...
 template <typename G>
@@ -413,7 +442,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   const uint32_t bar_full = s_bar, bar_empty = bar_full + 8 * NS, bar_clean = bar_empty + 8 * NS;
   const uint32_t bar_landed = bar_clean + 8 * NS;
   const uint32_t bar_qfull = bar_landed + 8 * NS, bar_qempty = bar_qfull + 8, bar_scores = bar_qempty + 8;
-  const uint32_t bar_weights = bar_scores + 16, bar_sums = bar_weights + 16, bar_drained = bar_sums + 16;
+  const uint32_t bar_weights = bar_scores + 16, bar_sums = bar_weights + 32, bar_drained = bar_sums + 16;
   const uint32_t bar_product = bar_drained + 16;
   uint8_t* tail = smem_raw + (base - smem_u32(smem_raw)) + G::kData + G::kBars * 8 + (G::kBars & 1) * 8;
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(tail);        // [kWordsRing][4]: a block's tokens that have data
@@ -430,7 +459,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     mbar_init(bar_qempty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_scores + 8 * i, 1);
-      mbar_init(bar_weights + 8 * i, 4);
+      mbar_init(bar_weights + 16 * i, 4);
+      mbar_init(bar_weights + 16 * i + 8, 4);
       mbar_init(bar_sums + 8 * i, 1);
       mbar_init(bar_drained + 8 * i, 4);
     }
@@ -513,7 +543,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c / 32][c % 32]));
+        for (int c = 0; c < 128; c += 2) top[(c / 2) & 3] = max3(top[(c / 2) & 3], s[c / 32][c % 32], s[c / 32][c % 32 + 1]);
         const float bm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
         const bool grow = bm > m + kSlack;
         if (__any_sync(0xffffffffu, grow)) {
@@ -558,13 +588,13 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             p[c] = pack_bf16(p0, p1);
           }
           tmem_st_32x32b_x32(scores + 32 * half, p);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_weights + 16 * x + 8 * half);
         }
         sum[0] = add2(sum[0], sum[1]);
         l += lo2(sum[0]) + hi2(sum[0]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_weights + 8 * x);
       }
       if (!ok) break;
       products += nb;
@@ -635,11 +665,16 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       if (lane == 0) mbar_arrive(bar_drained + 8 * t);
     }
   } else if (warp == G::kMmaWarp) {
-    // ---- products: lane 0 issues ----
+    // ---- products: one thread issues ----
     constexpr uint32_t kIdescS = make_idesc_bf16(kTileRows, kBlock);
     constexpr uint32_t kIdescO = make_idesc_bf16(kTileRows, G::DS) | (1u << 16);        // B (V) is MN-major
     uint32_t use[2] = {0, 0}, items_t[2] = {0, 0}, guarded = 0;         // guarded: V slots that were scanned so far
-    int sq = 0;                                            // ring slots of the items before
+    Ring<NS> ring{0, 0};
+    // Operands' descriptors: the low words move, the high ones (strides, version, swizzle) do not.
+    const uint32_t lo_q = (uint32_t)sw128_kmajor_desc(s_q), lo_ring = (s_ring & 0x3FFFFu) >> 4;
+    constexpr uint32_t kLdK = 1u << 16, kLdV = (G::kPanel >> 4) << 16;   // leading-dimension offsets
+    const uint32_t kHiK = (uint32_t)(sw128_kmajor_desc(0) >> 32), kHiV = (uint32_t)(sw128_mnmajor_desc(0, G::kPanel, 1024) >> 32);
+    const auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
     if (G::kTree && lane == 0) a.ws_start[blockIdx.x] = make_int4(-1, 0, 0, 0);
     const auto wait_lane0 = [&](uint32_t bar, uint32_t parity) { return lane != 0 || mbar_wait(bar, parity); };
     for (int n_item = 0; ok && walk.next(a, it); ++n_item) {
@@ -659,96 +694,104 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               tma_load_3d(s_q + t * G::kQTile + p * G::kPanel, &tm_q, 64 * p, it.head * a.group, it.row0 + t * a.npt, bar_qfull);
         }
       }
-      ok = ok && wait_lane0(bar_qfull, n_item & 1);
-      const auto slot = [&](int seq) { return (uint32_t)((sq + seq) % NS); };
-      const auto phase = [&](int seq) { return (uint32_t)((sq + seq) / NS) & 1u; };
-      const auto issue_scores = [&](int t, int x, int i) {               // scores buffer x = Q_t K_i^T
-        for (int p = 0; p < PD; ++p) {
-          const int q = seq_k<G>(i) + p;
-          if (!mbar_wait(bar_full + 8 * slot(q), phase(q))) return false;
+      ok = __all_sync(0xffffffffu, ok && wait_lane0(bar_qfull, n_item & 1));
+      // Scores buffer x = Q_t K^T, K in the ring from r on.
+      const auto issue_scores = [&](int t, int x, Ring<NS> r) {
+#pragma unroll
+        for (int p = 0; p < PD; ++p, r.next()) {
+          if (!mbar_wait(bar_full + 8 * r.at, r.phase)) return false;
           tc_fence_after();
-          const uint64_t qd = sw128_kmajor_desc(s_q + t * G::kQTile + p * G::PANELS * G::kPanel);
-          const uint64_t kd = sw128_kmajor_desc(s_ring + slot(q) * G::kSlot);
+          const uint32_t qd = lo_q + (((uint32_t)t * G::kQTile + (uint32_t)p * G::PANELS * G::kPanel) >> 4);
+          const uint32_t kd = (lo_ring | kLdK) + r.at * (G::kSlot >> 4);
 #pragma unroll
           for (int k = 0; k < G::DS / 16; ++k) {
-            const uint64_t off = ((k / 4) * G::kPanel + (k % 4) * 32) >> 4;
-            mma_bf16_ss(tmem + x * 128, qd + off, kd + off, kIdescS, p > 0 || k > 0);
+            const uint32_t off = ((k / 4) * G::kPanel + (k % 4) * 32) >> 4;
+            mma_bf16_ss(tmem + x * 128, desc(qd + off, kHiK), desc(kd + off, kHiK), kIdescS, p > 0 || k > 0);
           }
         }
         mma_commit(bar_scores + 8 * x);
         return true;
       };
-      const auto issue_product = [&](int t, int x, int i) {              // sums of tile t += weights buffer x V_i
-        for (int p = 0; p < PD; ++p) {
-          const int q = seq_v<G>(i, n) + p;
-          const uint32_t s = slot(q);
-          if (!G::kTree && it.b0 + i >= it.guard) {
-            const uint32_t n_th = guarded + p;             // landed and cleared of infinities
-            if (!mbar_wait(bar_clean + 8 * (n_th % NS), (n_th / NS) & 1)) return false;
-          } else if (!mbar_wait(bar_full + 8 * s, phase(q))) {
-            return false;
-          }
-          tc_fence_after();
-          const uint64_t vd = sw128_mnmajor_desc(s_ring + s * G::kSlot, G::kPanel, 1024);
+      // Sums of tile t += weights buffer x times V, V in the ring from r on.
+      const auto issue_product = [&](int t, int x, Ring<NS> r, bool guard, bool add) {
 #pragma unroll
-          for (int k = 0; k < kBlock / 16; ++k)
-            mma_bf16_ts(tmem + G::kTmemO + t * D + p * G::DS, tmem + x * 128 + k * 8, vd + ((k * 2048) >> 4), kIdescO, i > 0 || k > 0);
+        for (int p = 0; p < PD; ++p, r.next()) {
+          const uint32_t n_th = guarded + p;               // of the V slots that are scanned: landed and cleared of infinities
+          if (!(!G::kTree && guard ? mbar_wait(bar_clean + 8 * (n_th % NS), (n_th / NS) & 1) : mbar_wait(bar_full + 8 * r.at, r.phase)))
+            return false;
+          const uint32_t vd = (lo_ring | kLdV) + r.at * (G::kSlot >> 4);
+#pragma unroll
+          for (int k = 0; k < kBlock / 16; ++k) {
+            if (p == 0 && k % 4 == 0) {                    // half of the weights
+              if (!mbar_wait(bar_weights + 16 * x + 2 * k, use[x] & 1)) return false;
+              tc_fence_after();
+            }
+            mma_bf16_ts(tmem + G::kTmemO + t * D + p * G::DS, tmem + x * 128 + k * 8, desc(vd + ((k * 2048) >> 4), kHiV), kIdescO, add || k > 0);
+          }
         }
+        ++use[x];
         return true;
       };
-      const auto release = [&](int seq) {
-        for (int p = 0; p < PD; ++p) mma_commit(bar_empty + 8 * slot(seq + p));
+      const auto release = [&](Ring<NS> r) {
+#pragma unroll
+        for (int p = 0; p < PD; ++p, r.next()) mma_commit(bar_empty + 8 * r.at);
       };
-      if (ok && lane == 0) {
+      if (ok && elect_one()) {
         tc_fence_after();
-        if (NB == 1) {
+        if (NB == 1) {                                     // K0 V0 K1 V1 ...
           for (int t = 0; t < NT && ok; ++t)
-            if (nb[t] > 0) ok = issue_scores(t, t, 0);
-          if (ok) release(seq_k<G>(0));
+            if (nb[t] > 0) ok = issue_scores(t, t, ring);
+          if (ok) release(ring);
           if (ok && n == 1) mma_commit(bar_qempty);
+          ring.next();
           for (int i = 0; i < n && ok; ++i) {
-            for (int t = 0; t < NT && ok; ++t) {
-              if (i >= nb[t]) continue;
-              ok = mbar_wait(bar_weights + 8 * t, use[t]++ & 1);
-              if (ok && i == 0) ok = mbar_wait(bar_drained + 8 * t, (items_t[t]++ & 1) ^ 1);
-              tc_fence_after();
-              ok = ok && issue_product(t, t, i);
+            const bool guard = it.b0 + i >= it.guard;
+            Ring<NS> next = ring;
+            next.next();
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              if (!ok || i >= nb[t]) continue;
+              if (i == 0) ok = mbar_wait(bar_drained + 8 * t, (items_t[t]++ & 1) ^ 1);
+              ok = ok && issue_product(t, t, ring, guard, i > 0);
               if (ok && i + 1 == nb[t]) mma_commit(bar_sums + 8 * t);
-              if (ok && i + 1 < nb[t]) ok = issue_scores(t, t, i + 1);
+              if (ok && i + 1 < nb[t]) ok = issue_scores(t, t, next);
             }
             if (!ok) break;
-            if (!G::kTree && it.b0 + i >= it.guard) guarded += PD;
-            release(seq_v<G>(i, n));
-            if (i + 1 < n) release(seq_k<G>(i + 1));
+            if (guard) guarded += PD;
+            release(ring);
+            if (i + 1 < n) release(next);
             if (i + 2 == n) mma_commit(bar_qempty);
+            ring = next;
+            if (i + 1 < n) ring.next();
           }
-        } else {
+        } else {                                           // K0 K1 V0 K2 V1 ...
           for (int i = 0; i < 2 && i < n && ok; ++i) {
-            ok = issue_scores(0, i, i);
-            if (ok) release(seq_k<G>(i));
+            ok = issue_scores(0, i, ring);
+            if (ok) release(ring);
+            ring.template skip<PD>();
           }
           if (ok && n <= 2) mma_commit(bar_qempty);
           for (int i = 0; i < n && ok; ++i) {
             const int x = i & 1;
-            ok = mbar_wait(bar_weights + 8 * x, use[x]++ & 1);
-            if (ok && i == 0) ok = mbar_wait(bar_drained, (items_t[0]++ & 1) ^ 1);
-            tc_fence_after();
-            ok = ok && issue_product(0, x, i);
+            const bool guard = it.b0 + i >= it.guard;
+            if (i == 0) ok = mbar_wait(bar_drained, (items_t[0]++ & 1) ^ 1);
+            ok = ok && issue_product(0, x, ring, guard, i > 0);
             if (!ok) break;
-            if (!G::kTree && it.b0 + i >= it.guard) guarded += PD;
-            release(seq_v<G>(i, n));
+            if (guard) guarded += PD;
+            release(ring);
+            ring.template skip<PD>();
             mma_commit(bar_product);
             if (i + 1 == n) mma_commit(bar_sums);
             if (i + 2 < n) {
-              ok = issue_scores(0, x, i + 2);
-              if (ok) release(seq_k<G>(i + 2));
+              ok = issue_scores(0, x, ring);
+              if (ok) release(ring);
+              ring.template skip<PD>();
               if (ok && i + 3 == n) mma_commit(bar_qempty);
             }
           }
         }
       }
       ok = __all_sync(0xffffffffu, ok);
-      sq += 2 * PD * n;
     }
   } else if (!G::kTree && warp == G::kLoadWarp) {
     // ---- prompt: TMA loads ----
