@@ -203,13 +203,12 @@ struct Geo {
   static constexpr int kMmaWarp = kSoftWarps;
   static constexpr int kLoadWarp = kSoftWarps + (kTree ? 4 : 1);   // prompt: one TMA warp; tree: four copying warps
   static constexpr int kLoadWarps = kTree ? 4 : 1;
-  static constexpr int kScanWarp = kLoadWarp + 1;          // prompt: two warps
+  static constexpr int kScanWarp = kSoftWarps + 2;         // two warps
   static constexpr int kScanWarps = 2;
   static constexpr int kThreads = 32 * (kSoftWarps + (kTree ? 8 : 4));       // whole warpgroups: they trade registers
   // Registers a thread: a softmax thread holds a row of scores.  Launch 128 or 168 (D = 256: 168 or 255).
   static constexpr int kSoftRegs = NT == 1 ? 232 : kTree ? 192 : 208;
   static constexpr int kOtherRegs = NT == 1 ? (kTree ? 136 : 232) : kTree ? 64 : 88;
-  static constexpr int kLag = NS - 2;                      // tree: slots whose copies a warp has on their way
   static constexpr uint32_t kData = NT * kQTile + NS * kSlot;
   // barriers: full and empty per slot, landed and clean per guarded V slot in turn; Q full and empty; scores and
   // weights (two halves) per buffer; sums full and drained per tile; products
@@ -239,6 +238,11 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// One arrival on `bar` when this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
@@ -450,10 +454,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(bar_full + 8 * s, G::kTree ? G::kLoadWarps : 1);
+      mbar_init(bar_full + 8 * s, G::kTree ? 33 * G::kLoadWarps : 1);
       mbar_init(bar_empty + 8 * s, 1);
       mbar_init(bar_clean + 8 * s, G::kScanWarps);
-      mbar_init(bar_landed + 8 * s, 1);
+      mbar_init(bar_landed + 8 * s, G::kTree ? 32 * G::kLoadWarps : 1);
     }
     mbar_init(bar_qfull, 1);
     mbar_init(bar_qempty, 1);
@@ -700,6 +704,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
         for (int p = 0; p < PD; ++p, r.next()) {
           if (!mbar_wait(bar_full + 8 * r.at, r.phase)) return false;
+          if (G::kTree) fence_proxy_async_shared();        // K and V come by cp.async
           tc_fence_after();
           const uint32_t qd = lo_q + (((uint32_t)t * G::kQTile + (uint32_t)p * G::PANELS * G::kPanel) >> 4);
           const uint32_t kd = (lo_ring | kLdK) + r.at * (G::kSlot >> 4);
@@ -717,8 +722,9 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
         for (int p = 0; p < PD; ++p, r.next()) {
           const uint32_t n_th = guarded + p;               // of the V slots that are scanned: landed and cleared of infinities
-          if (!(!G::kTree && guard ? mbar_wait(bar_clean + 8 * (n_th % NS), (n_th / NS) & 1) : mbar_wait(bar_full + 8 * r.at, r.phase)))
+          if (!(guard ? mbar_wait(bar_clean + 8 * (n_th % NS), (n_th / NS) & 1) : mbar_wait(bar_full + 8 * r.at, r.phase)))
             return false;
+          if (G::kTree) fence_proxy_async_shared();
           const uint32_t vd = (lo_ring | kLdV) + r.at * (G::kSlot >> 4);
 #pragma unroll
           for (int k = 0; k < kBlock / 16; ++k) {
@@ -849,8 +855,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       ok = __all_sync(0xffffffffu, ok);
       sq += 2 * PD * n;
     }
-  } else if (!G::kTree && warp >= G::kScanWarp) {
-    // ---- prompt: V blocks of which a row does not see every token are cleared of infinities and NaN, whose
+  } else if (warp >= G::kScanWarp && warp < G::kScanWarp + G::kScanWarps) {
+    // ---- V blocks of which a row does not see every token are cleared of infinities and NaN, whose
     // products with the weights 0 would be NaN; the tile's outputs get those that a row does see ----
     const int w = warp - G::kScanWarp;
     int sq = 0;
@@ -884,26 +890,13 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int w = warp - G::kLoadWarp;
     constexpr int kChunks = G::DS / 8, kRowsAt = 32 / kChunks;          // 16-byte chunks of a slot's row; rows at a time
     const int chunk = lane % kChunks, sub = lane / kChunks;
-    int k = 0;                                             // slots issued
-    uint32_t guard_hist = 0;                               // of the slots on their way, a bit each: V to be cleared
+    Ring<NS> ring{0, 1};                                   // phase: of the slot's release
+    uint32_t guarded = 0;
     const auto row_addr = [&](uint32_t s, int r) {
       return s_ring + s * G::kSlot + (uint32_t)(chunk >> 3) * G::kPanel + (uint32_t)(r >> 3) * 1024u + sw128_offset(r, chunk & 7);
     };
-    // Slot j's copies of this warp have landed; it belongs to the given item or a later one.
-    const auto signal = [&](int j, bool guard, int item) {
-      const uint32_t s = (uint32_t)(j % NS);
-      if (guard) {
-        bool bad = false;
-#pragma unroll 4
-        for (int i = 0; i < 32 / kRowsAt; ++i) bad |= clean16(row_addr(s, 32 * w + i * kRowsAt + sub));
-        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicMin(const_cast<int*>(first_bad), item);
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_full + 8 * s);
-    };
-    int blocks_done = 0, n_item = 0;
-    for (; ok && walk.next(a, it); ++n_item) {
+    int blocks_done = 0;
+    while (ok && walk.next(a, it)) {
       const int n = it.b1 - it.b0;
       const auto entry = [&](int i) {                      // this lane's token of block i
         const int j = (it.b0 + i) * kBlock + 32 * w + lane;
@@ -916,26 +909,29 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         return make_int2(-1, -1);
       };
       const auto load = [&](int page, bool is_v, int i, int2 e) {
-        for (int p = 0; p < PD && ok; ++p, ++k) {
-          const uint32_t s = (uint32_t)(k % NS);
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ((uint32_t)(k / NS) & 1u) ^ 1u));
+        for (int p = 0; p < PD; ++p, ring.next()) {
+          const uint32_t s = ring.at;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ring.phase));
           if (!ok) return;
           if (!is_v && p == 0) {
             const unsigned has = __ballot_sync(0xffffffffu, e.x >= 0);
             if (lane == 0) words[((blocks_done + i) % G::kWordsRing) * 4 + w] = has;
           }
+          if (lane == 0) mbar_arrive(bar_full + 8 * s);    // with the words: the copies' own arrivals order no other write
           const int64_t col = (int64_t)it.head * D + p * G::DS + chunk * 8;
 #pragma unroll
           for (int r = 0; r < 32 / kRowsAt; ++r) {
             const int own = r * kRowsAt + sub, pg = __shfl_sync(0xffffffffu, page, own);
             cp_async_16(row_addr(s, 32 * w + own), a.pool + (pg >= 0 ? (int64_t)pg * a.H + col : 0), pg >= 0);
           }
-          cp_async_commit();
-          if (k >= G::kLag) {
-            cp_async_wait<G::kLag>();
-            signal(k - G::kLag, (guard_hist >> (G::kLag - 1)) & 1, n_item - G::kLag);
+          // Every lane arrives when its copies have landed.  (A warp that waited for them and put a proxy fence
+          // behind had one slot at a time on its way: the fence waits for the thread's later copies too.)
+          uint32_t bar = bar_full + 8 * s;
+          if (is_v && it.b0 + i >= it.guard) {             // goes through the scan: the slot's own phase ends at once
+            mbar_arrive(bar);
+            bar = bar_landed + 8 * (guarded++ % NS);
           }
-          guard_hist = guard_hist << 1 | (is_v && it.b0 + i >= it.guard ? 1u : 0u);
+          cp_async_arrive(bar);
         }
       };
       int2 e0 = checked(entry(0), 0), e1 = entry(1);
@@ -955,14 +951,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       }
       blocks_done += n;
     }
-    // the last slots
-    const auto drain = [&](auto self, auto left) {
-      constexpr int r = decltype(left)::value;
-      cp_async_wait<r>();
-      if (ok && k - 1 - r >= 0) signal(k - 1 - r, (guard_hist >> r) & 1, n_item - 1 - r);
-      if constexpr (r > 0) self(self, std::integral_constant<int, r - 1>{});
-    };
-    drain(drain, std::integral_constant<int, G::kLag - 1>{});
+    cp_async_wait_all();                                   // in any case: the CTA may leave
   }
   if (!ok && lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
   tc_fence_before();
