@@ -238,11 +238,14 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-// One arrival on `bar` when this thread's cp.async copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+// Four rows of a tensor map whose box is one row high, one behind another in shared memory; rows outside the tensor
+// are zero.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int4 rows, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
@@ -441,6 +444,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   constexpr int D = G::D, NT = G::NT, NB = G::NB, PD = G::PD, NS = G::NS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_s;
+  __shared__ __align__(16) int32_t ids_s[G::kTree ? G::kLoadWarps * 64 : 4];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t s_q = base, s_ring = base + NT * G::kQTile, s_bar = base + G::kData;
   const uint32_t bar_full = s_bar, bar_empty = bar_full + 8 * NS, bar_clean = bar_empty + 8 * NS;
@@ -454,10 +458,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(bar_full + 8 * s, G::kTree ? 33 * G::kLoadWarps : 1);
+      mbar_init(bar_full + 8 * s, G::kLoadWarps);
       mbar_init(bar_empty + 8 * s, 1);
       mbar_init(bar_clean + 8 * s, G::kScanWarps);
-      mbar_init(bar_landed + 8 * s, G::kTree ? 32 * G::kLoadWarps : 1);
+      mbar_init(bar_landed + 8 * s, G::kLoadWarps);
     }
     mbar_init(bar_qfull, 1);
     mbar_init(bar_qempty, 1);
@@ -704,7 +708,6 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
         for (int p = 0; p < PD; ++p, r.next()) {
           if (!mbar_wait(bar_full + 8 * r.at, r.phase)) return false;
-          if (G::kTree) fence_proxy_async_shared();        // K and V come by cp.async
           tc_fence_after();
           const uint32_t qd = lo_q + (((uint32_t)t * G::kQTile + (uint32_t)p * G::PANELS * G::kPanel) >> 4);
           const uint32_t kd = (lo_ring | kLdK) + r.at * (G::kSlot >> 4);
@@ -724,7 +727,6 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           const uint32_t n_th = guarded + p;               // of the V slots that are scanned: landed and cleared of infinities
           if (!(guard ? mbar_wait(bar_clean + 8 * (n_th % NS), (n_th / NS) & 1) : mbar_wait(bar_full + 8 * r.at, r.phase)))
             return false;
-          if (G::kTree) fence_proxy_async_shared();
           const uint32_t vd = (lo_ring | kLdV) + r.at * (G::kSlot >> 4);
 #pragma unroll
           for (int k = 0; k < kBlock / 16; ++k) {
@@ -886,72 +888,77 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       sq += 2 * PD * n;
     }
   } else if (G::kTree && warp >= G::kLoadWarp) {
-    // ---- tree: rows of K and V from their pages, 16 bytes a lane, each warp 32 of a block's tokens ----
+    // ---- tree: rows of K and V from their pages, gathered four at a time by TMA, each warp 32 of a block's tokens ----
     const int w = warp - G::kLoadWarp;
-    constexpr int kChunks = G::DS / 8, kRowsAt = 32 / kChunks;          // 16-byte chunks of a slot's row; rows at a time
-    const int chunk = lane % kChunks, sub = lane / kChunks;
+    int32_t* ids = ids_s + w * 64;                         // of a block: 32 K pages, 32 V pages; -1 (zeros): no data
     Ring<NS> ring{0, 1};                                   // phase: of the slot's release
     uint32_t guarded = 0;
-    const auto row_addr = [&](uint32_t s, int r) {
-      return s_ring + s * G::kSlot + (uint32_t)(chunk >> 3) * G::kPanel + (uint32_t)(r >> 3) * 1024u + sw128_offset(r, chunk & 7);
-    };
-    int blocks_done = 0;
+    int blocks_done = 0, issued = 0;
     while (ok && walk.next(a, it)) {
       const int n = it.b1 - it.b0;
       const auto entry = [&](int i) {                      // this lane's token of block i
         const int j = (it.b0 + i) * kBlock + 32 * w + lane;
-        return i < n && j < it.len ? a.table[((int64_t)it.req * a.max_len + j) * a.layers + a.layer] : make_int2(-2, -2);
+        return i < n && j < it.len ? a.table[((int64_t)it.req * a.max_len + j) * a.layers + a.layer] : make_int2(-1, -1);
       };
-      const auto checked = [&](int2 e, int i) {            // -1: no data
+      const auto checked = [&](int2 e, int i) {
         if (e.x >= 0 && e.x < a.num_pages && e.y >= 0 && e.y < a.num_pages) return e;
-        const int j = (it.b0 + i) * kBlock + 32 * w + lane;
-        if (i < n && j < it.len) flag_error(a.err, LORA_DEV_BAD_PAGE);
+        if (i < n && (it.b0 + i) * kBlock + 32 * w + lane < it.len) flag_error(a.err, LORA_DEV_BAD_PAGE);
         return make_int2(-1, -1);
       };
-      const auto load = [&](int page, bool is_v, int i, int2 e) {
+      const auto load = [&](int2 e, bool is_v, int i) {
+        __syncwarp();
+        ids[lane] = is_v ? e.y : e.x;
+        const unsigned has = __ballot_sync(0xffffffffu, e.x >= 0);
+        __syncwarp();
+#pragma unroll
         for (int p = 0; p < PD; ++p, ring.next()) {
           const uint32_t s = ring.at;
           ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ring.phase));
           if (!ok) return;
-          if (!is_v && p == 0) {
-            const unsigned has = __ballot_sync(0xffffffffu, e.x >= 0);
-            if (lane == 0) words[((blocks_done + i) % G::kWordsRing) * 4 + w] = has;
-          }
-          if (lane == 0) mbar_arrive(bar_full + 8 * s);    // with the words: the copies' own arrivals order no other write
-          const int64_t col = (int64_t)it.head * D + p * G::DS + chunk * 8;
+          const bool guard = is_v && it.b0 + i >= it.guard;
+          if (elect_one()) {
+            if (!is_v && p == 0) words[((blocks_done + i) % G::kWordsRing) * 4 + w] = has;
+            uint32_t bar = bar_full + 8 * s;
+            if (guard) {                                   // goes through the scan: the slot's own phase ends at once
+              mbar_arrive(bar);
+              bar = bar_landed + 8 * (guarded % NS);
+            }
+            mbar_arrive_expect_tx(bar, 32 * G::DS * 2);
+            const uint32_t dst = s_ring + s * G::kSlot + w * 32 * 128;
+            const int x = it.head * D + p * G::DS;
 #pragma unroll
-          for (int r = 0; r < 32 / kRowsAt; ++r) {
-            const int own = r * kRowsAt + sub, pg = __shfl_sync(0xffffffffu, page, own);
-            cp_async_16(row_addr(s, 32 * w + own), a.pool + (pg >= 0 ? (int64_t)pg * a.H + col : 0), pg >= 0);
+            for (int g = 0; g < 8; ++g) {
+              const int4 rows = *reinterpret_cast<const int4*>(ids + 4 * g);
+#pragma unroll
+              for (int c = 0; c < G::PANELS; ++c) tma_gather4(dst + c * G::kPanel + g * 512, &tm_k, x + 64 * c, rows, bar);
+            }
           }
-          // Every lane arrives when its copies have landed.  (A warp that waited for them and put a proxy fence
-          // behind had one slot at a time on its way: the fence waits for the thread's later copies too.)
-          uint32_t bar = bar_full + 8 * s;
-          if (is_v && it.b0 + i >= it.guard) {             // goes through the scan: the slot's own phase ends at once
-            mbar_arrive(bar);
-            bar = bar_landed + 8 * (guarded++ % NS);
-          }
-          cp_async_arrive(bar);
+          guarded += guard;
+          ++issued;
         }
       };
       int2 e0 = checked(entry(0), 0), e1 = entry(1);
-      load(e0.x, false, 0, e0);
+      load(e0, false, 0);
       for (int i = 0; i < n && ok; ++i) {
         const int2 e2 = entry(i + 2);
         e1 = checked(e1, i + 1);
         if (NB == 2) {
-          if (i + 1 < n) load(e1.x, false, i + 1, e1);
-          if (ok) load(e0.y, true, i, e0);
+          if (i + 1 < n) load(e1, false, i + 1);
+          if (ok) load(e0, true, i);
         } else {
-          load(e0.y, true, i, e0);
-          if (ok && i + 1 < n) load(e1.x, false, i + 1, e1);
+          load(e0, true, i);
+          if (ok && i + 1 < n) load(e1, false, i + 1);
         }
         e0 = e1;
         e1 = e2;
       }
       blocks_done += n;
     }
-    cp_async_wait_all();                                   // in any case: the CTA may leave
+    if (!ok && lane == 0) {                                // wait for the copies in flight: the CTA may leave
+      for (int q = issued > NS ? issued - NS : 0; q < issued; ++q) (void)mbar_wait(bar_full + 8 * (q % NS), (uint32_t)(q / NS) & 1u);
+      for (uint32_t c = guarded > NS ? guarded - NS : 0; c < guarded; ++c)
+        (void)mbar_wait(bar_landed + 8 * (c % NS), (c / NS) & 1);
+    }
   }
   if (!ok && lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
   tc_fence_before();
@@ -1070,6 +1077,14 @@ int encode_kv(CUtensorMap* map, const void* k, int H, int64_t n_rows, int64_t st
   return encode_map(map, k, 2, dims, strides, box);
 }
 
+// Pages of the pool, one row of 64 features a box: what TMA gathers.
+int encode_pages(CUtensorMap* map, const void* pool, int H, int64_t num_pages) {
+  const cuuint64_t dims[2] = {(cuuint64_t)H, (cuuint64_t)num_pages};
+  const cuuint64_t strides[1] = {(cuuint64_t)H * 2};
+  const cuuint32_t box[2] = {64, 1};
+  return encode_map(map, pool, 2, dims, strides, box);
+}
+
 int tiles_of(int D) { return D == 256 ? 1 : 2; }
 
 // Workspaces; every array starts on a 256-byte boundary.
@@ -1137,7 +1152,7 @@ int launch_prompt(const lora_pool* p, const RowsArgs& a, const PromptLayout& L, 
 }
 
 template <int D>
-int launch_tree(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, cudaStream_t st) {
+int launch_tree(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, const CUtensorMap& pages, cudaStream_t st) {
   using G = Geo<D, true>;
   const char* what = "lora_attention_tree launch";
   cudaError_t e;
@@ -1146,7 +1161,7 @@ int launch_tree(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, cud
     e = launch_pdl(!p->prof_on, tree_plan_kernel<G::NT>, dim3(1), dim3(kPlanThreads), 0, st, a);
   }
   if (e != cudaSuccess) return lora_cuda_fail(e, what);
-  const int rc = launch_rows<G>(p, a, q, q, q, a.parts, what, st);
+  const int rc = launch_rows<G>(p, a, q, pages, pages, a.parts, what, st);
   if (rc != LORA_OK) return rc;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
   e = launch_pdl(!p->prof_on, tree_join_kernel<D, G::NT>, dim3(a.parts, 8), dim3(32 * kJoinWarps), 0, st, a);
@@ -1253,8 +1268,9 @@ extern "C" int lora_attention_tree(lora_pool* p, int32_t n_req, const int32_t* t
   rc = check_workspace(fn, workspace, workspace_bytes, some ? (int64_t)L.total : 0);
   if (rc != LORA_OK) return rc;
   if (!some) return LORA_OK;
-  CUtensorMap tm_q;
-  rc = encode_q(&tm_q, q, D, n_heads, n_rows, q_stride, group, kTileRows / group);
+  CUtensorMap tm_q, tm_pages;
+  rc = encode_pages(&tm_pages, p->pool_dev, p->H, p->num_pages);
+  if (rc == LORA_OK) rc = encode_q(&tm_q, q, D, n_heads, n_rows, q_stride, group, kTileRows / group);
   if (rc != LORA_OK) return rc;
   char* ws = static_cast<char*>(workspace);
   RowsArgs a{};
@@ -1288,8 +1304,8 @@ extern "C" int lora_attention_tree(lora_pool* p, int32_t n_req, const int32_t* t
   a.slot_rows = L.slot_rows;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   switch (D) {
-    case 64: return launch_tree<64>(p, a, tm_q, st);
-    case 128: return launch_tree<128>(p, a, tm_q, st);
-    default: return launch_tree<256>(p, a, tm_q, st);
+    case 64: return launch_tree<64>(p, a, tm_q, tm_pages, st);
+    case 128: return launch_tree<128>(p, a, tm_q, tm_pages, st);
+    default: return launch_tree<256>(p, a, tm_q, tm_pages, st);
   }
 }
