@@ -30,6 +30,7 @@ struct RowsArgs {
   float* lse;
   int32_t n_req, n_rows, n_heads, n_kv, group;
   int32_t npt;                                      // tokens (or nodes) of a tile: kTileRows / group
+  uint32_t group_inv;                               // 2^16 / group, rounded up: (r * group_inv) >> 16 = r / group for a tile's rows
   const int32_t* start;                             // caller's row starts
   int32_t* bounds;                                  // workspace: the same, ascending within [0, n_rows]
   float scale_log2;
@@ -201,7 +202,8 @@ struct Geo {
   static constexpr int NS = D == 64 ? 10 : 5;              // slots
   static constexpr int kSoftWarps = 4 * NT;
   static constexpr int kMmaWarp = kSoftWarps;
-  static constexpr int kLoadWarp = kSoftWarps + (kTree ? 4 : 1);   // prompt: one TMA warp; tree: four copying warps
+  static constexpr int kPlanWarp = kSoftWarps + 1;         // finds the items; prompt: loads Q, K and V; tree: Q
+  static constexpr int kLoadWarp = kSoftWarps + 4;         // tree: four warps that gather K and V
   static constexpr int kLoadWarps = kTree ? 4 : 1;
   static constexpr int kScanWarp = kSoftWarps + 2;         // two warps
   static constexpr int kScanWarps = 2;
@@ -212,7 +214,9 @@ struct Geo {
   static constexpr uint32_t kData = NT * kQTile + NS * kSlot;
   // barriers: full and empty per slot, landed and clean per guarded V slot in turn; Q full and empty; scores and
   // weights (two halves) per buffer; sums full and drained per tile; products
-  static constexpr int kBars = 4 * NS + 2 + 2 + 4 + 4 + 1;
+  static constexpr int kItems = 4;                         // items handed out at a time
+  static constexpr int kTakers = kSoftWarps + 1 + kScanWarps + (kTree ? kLoadWarps : 0);   // warps that take every item
+  static constexpr int kBars = 4 * NS + 2 + 2 + 4 + 4 + 1 + 2 * kItems;
   static constexpr int kWordsRing = 8;                     // blocks whose token masks are kept
   static constexpr uint32_t kSmem = 1024 + kData + kBars * 8 + kWordsRing * 16 + 64;
   static constexpr uint32_t kTmemO = 256;                  // scores in columns [0, 256), sums behind them
@@ -295,6 +299,22 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// v[e] of lane j becomes v[j] of lane e, for every four lanes.
+__device__ __forceinline__ void transpose_4x4(uint4 (&v)[4], int lane) {
+#pragma unroll
+  for (int s = 1; s <= 2; s <<= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e & s) continue;
+      const uint4 give = up ? v[e] : v[e | s];
+      const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, s), __shfl_xor_sync(0xffffffffu, give.y, s),
+                                   __shfl_xor_sync(0xffffffffu, give.z, s), __shfl_xor_sync(0xffffffffu, give.w, s));
+      if (up) v[e] = got;
+      else v[e | s] = got;
+    }
+  }
+}
 // A bf16 pair's halves with an exponent of all ones (infinity, NaN): 0x8000 and 0x80000000.
 __device__ __forceinline__ uint32_t non_finite2(uint32_t u) { return ((u & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -334,11 +354,11 @@ struct Item {
   int slot;                      // partial, or -1: the item has all blocks
 };
 
-// The items of a CTA, one after another; every warp walks them by itself.
+// The items of a CTA, one after another.
 template <typename G>
 struct Walk {
   int64_t u, u1, per_head;       // tree: units left are [u, u1)
-  int64_t w, step, all;          // prompt: turn, CTAs, items times heads
+  int w, step, all;              // prompt: turn, CTAs, items times heads
   __device__ __forceinline__ Walk(const RowsArgs& a) {
     if (G::kTree) {
       per_head = a.prefix[a.n_req];
@@ -348,7 +368,7 @@ struct Walk {
     } else {
       w = 0;
       step = gridDim.x;
-      all = (int64_t)*a.n_items * a.n_kv;
+      all = *a.n_items * a.n_kv;
     }
   }
   // All lanes of a warp take part.
@@ -382,10 +402,10 @@ struct Walk {
       return true;
     }
     // There and back over the CTAs, so that none has the longer item of every turn.
-    const int64_t x = w * step + ((w & 1) ? step - 1 - blockIdx.x : blockIdx.x);
+    const int x = w * step + ((w & 1) ? step - 1 - (int)blockIdx.x : (int)blockIdx.x);
     if (x >= all) return false;
     ++w;
-    it.head = (int)(x % a.n_kv);
+    it.head = x % a.n_kv;
     const int2 e = a.items[x / a.n_kv];
     const int first = a.bounds[e.x], n = a.bounds[e.x + 1] - first;
     it.req = e.x;
@@ -444,6 +464,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   constexpr int D = G::D, NT = G::NT, NB = G::NB, PD = G::PD, NS = G::NS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_s;
+  __shared__ Item items_s[G::kItems];
   __shared__ __align__(16) int32_t ids_s[G::kTree ? G::kLoadWarps * 64 : 4];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t s_q = base, s_ring = base + NT * G::kQTile, s_bar = base + G::kData;
@@ -451,7 +472,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   const uint32_t bar_landed = bar_clean + 8 * NS;
   const uint32_t bar_qfull = bar_landed + 8 * NS, bar_qempty = bar_qfull + 8, bar_scores = bar_qempty + 8;
   const uint32_t bar_weights = bar_scores + 16, bar_sums = bar_weights + 32, bar_drained = bar_sums + 16;
-  const uint32_t bar_product = bar_drained + 16;
+  const uint32_t bar_product = bar_drained + 16, bar_item = bar_product + 8, bar_taken = bar_item + 8 * G::kItems;
   uint8_t* tail = smem_raw + (base - smem_u32(smem_raw)) + G::kData + G::kBars * 8 + (G::kBars & 1) * 8;
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(tail);        // [kWordsRing][4]: a block's tokens that have data
   volatile int* first_bad = reinterpret_cast<volatile int*>(words + G::kWordsRing * 4);   // this CTA's first item with V cleared
@@ -473,6 +494,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       mbar_init(bar_drained + 8 * i, 4);
     }
     mbar_init(bar_product, 1);
+    for (int i = 0; i < G::kItems; ++i) {
+      mbar_init(bar_item + 8 * i, 1);
+      mbar_init(bar_taken + 8 * i, G::kTakers);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *first_bad = INT32_MAX;
   }
@@ -485,9 +510,20 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
-  Walk<G> walk(a);
   Item it;
   bool ok = true;
+  // The n-th item, as the planning warp found it; false behind the last one.
+  const auto take = [&](int n) {
+    const int at = n % G::kItems;
+    if (!__all_sync(0xffffffffu, mbar_wait(bar_item + 8 * at, (uint32_t)(n / G::kItems) & 1u))) {
+      ok = false;
+      return false;
+    }
+    it = items_s[at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_taken + 8 * at);
+    return it.req >= 0;
+  };
 
   if (warp < G::kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftRegs));
@@ -498,10 +534,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // ---- softmax: a thread per row ----
     const int t = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const int tok = row / a.group, g = row - tok * a.group;
+    const int tok = (int)(row * a.group_inv >> 16), g = row - tok * a.group;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     uint32_t use[2] = {0, 0}, items_t = 0, products = 0, blocks_done = 0;
-    for (int n_item = 0; ok && walk.next(a, it); ++n_item) {
+    for (int n_item = 0; ok && take(n_item); ++n_item) {
       const int nb = Walk<G>::blocks(a, it, t), nb_all = it.b1 - it.b0;
       if (nb == 0) {
         blocks_done += nb_all;
@@ -614,25 +650,61 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       }
       ++items_t;
       tc_fence_after();
-      const bool dirty = n_item >= *first_bad;
       const bool part = it.slot >= 0;
       const int64_t orow = it.row0 + t * a.npt + tok;
       const int head = it.head * a.group + g;
       const int64_t prow = (int64_t)it.slot * a.slot_rows + t * kTileRows + row;
       const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
       const uint32_t sums = tmem + G::kTmemO + (uint32_t)(t * D) + lane_off;
+      // Of a finished tile four lanes exchange their 16-byte pieces, so that each store covers 64 bytes of eight
+      // rows: with a row a lane a store touches 32 rows, half a sector each.  dst: this lane's place in its four rows.
+      uint16_t* dst[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = (row & ~3) + e, tok_r = (int)(r * a.group_inv >> 16);
+        dst[e] = tok_r < left ? a.out + (it.row0 + t * a.npt + tok_r) * a.out_stride +
+                                    (int64_t)(it.head * a.group + r - tok_r * a.group) * D + 8 * (lane & 3)
+                              : nullptr;
+      }
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t o[32];
         __syncwarp();
         tmem_ld_32x32b_x32(sums + d, o);
         tmem_ld_wait();
-        float y[32];
+        if (part) {
+          if (!live) continue;
+          uint4* to = reinterpret_cast<uint4*>(a.ws_acc + prow * D + d);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv;
-        if (dirty && live && l != 0.f) {
-          // infinities and NaN of V in the blocks that not every row sees whole were left out of the products
-          const int j1 = G::kTree ? min(it.b1 * kBlock, it.len) : pos + 1;
+          for (int e = 0; e < 8; ++e) to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else {
+          uint4 v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t u[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+              u[f] = pack_bf16(__uint_as_float(o[8 * e + 2 * f]) * inv, __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
+            v[e] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          transpose_4x4(v, lane);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (dst[e]) *reinterpret_cast<uint4*>(dst[e] + d) = v[e];
+        }
+      }
+      if (live && part) a.ws_ml[prow] = make_float2(m, l);
+      if (live && !part && a.lse)
+        a.lse[orow * a.n_heads + head] = l == 0.f ? -INFINITY : (m + kShift + log2f(l)) * 0.6931471805599453f;
+      if (n_item >= *first_bad) {
+        // Infinities and NaN of V in the blocks that not every row sees whole were left out of the products: the rows
+        // that see them get them here.
+        __syncwarp();
+        const int j1 = G::kTree ? min(it.b1 * kBlock, it.len) : pos + 1;
+#pragma unroll 1
+        for (int d = 0; d < D && live && l != 0.f; ++d) {
+          float c = 0.f;
+#pragma unroll 1
           for (int j = max(it.b0, it.guard) * kBlock; j < j1; ++j) {
             const uint16_t* v;
             if (G::kTree) {
@@ -643,31 +715,18 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             } else {
               v = a.v + (it.row0 - it.pos0 + j) * a.v_stride + it.head * D + d;
             }
-            for (int e = 0; e < 32; ++e) {
-              const uint32_t b = v[e];
-              if ((b & 0x7F80u) == 0x7F80u) {
-#pragma unroll
-                for (int f = 0; f < 32; ++f)
-                  if (f == e) y[f] += __uint_as_float(b << 16);
-              }
-            }
+            const uint32_t x = *v;
+            if ((x & 0x7F80u) == 0x7F80u) c += __uint_as_float(x << 16);
+          }
+          if (c == 0.f) continue;
+          if (part) {
+            a.ws_acc[prow * D + d] += c;
+          } else {
+            uint16_t* y = a.out + orow * a.out_stride + (int64_t)head * D + d;
+            *y = f32_to_bf16_rn(__uint_as_float((uint32_t)*y << 16) + c);
           }
         }
-        if (live && part) {
-          float4* dst = reinterpret_cast<float4*>(a.ws_acc + prow * D + d);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-        } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + orow * a.out_stride + (int64_t)head * D + d);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]),
-                                pack_bf16(y[8 * e + 4], y[8 * e + 5]), pack_bf16(y[8 * e + 6], y[8 * e + 7]));
-        }
       }
-      if (live && part) a.ws_ml[prow] = make_float2(m, l);
-      if (live && !part && a.lse)
-        a.lse[orow * a.n_heads + head] = l == 0.f ? -INFINITY : (m + kShift + log2f(l)) * 0.6931471805599453f;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_drained + 8 * t);
@@ -683,25 +742,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     constexpr uint32_t kLdK = 1u << 16, kLdV = (G::kPanel >> 4) << 16;   // leading-dimension offsets
     const uint32_t kHiK = (uint32_t)(sw128_kmajor_desc(0) >> 32), kHiV = (uint32_t)(sw128_mnmajor_desc(0, G::kPanel, 1024) >> 32);
     const auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
-    if (G::kTree && lane == 0) a.ws_start[blockIdx.x] = make_int4(-1, 0, 0, 0);
     const auto wait_lane0 = [&](uint32_t bar, uint32_t parity) { return lane != 0 || mbar_wait(bar, parity); };
-    for (int n_item = 0; ok && walk.next(a, it); ++n_item) {
+    for (int n_item = 0; ok && take(n_item); ++n_item) {
       int nb[2] = {Walk<G>::blocks(a, it, 0), NT == 2 ? Walk<G>::blocks(a, it, 1) : 0};
       const int n = it.b1 - it.b0;
-      if (G::kTree && lane == 0) {                         // Q of the item
-        if (it.slot >= 0 && it.b0 == 0) {                  // cut behind this part: the join goes on to the part of its last unit
-          const int64_t units = walk.per_head * a.n_kv, parts = min((int64_t)a.parts, units), x = walk.u - it.b1 + it.blocks;
-          a.ws_start[blockIdx.x] = make_int4(it.head, it.req, it.pos0 / (NT * a.npt), (int)((x * parts - 1) / units));
-        }
-        ok = mbar_wait(bar_qempty, (n_item & 1) ^ 1);
-        if (ok) {
-          const uint32_t bytes = (uint32_t)(a.npt * a.group * 128 * (D / 64));
-          mbar_arrive_expect_tx(bar_qfull, nb[1] > 0 ? 2 * bytes : bytes);
-          for (int t = 0; t < NT; ++t)
-            for (int p = 0; p < D / 64 && nb[t] > 0; ++p)
-              tma_load_3d(s_q + t * G::kQTile + p * G::kPanel, &tm_q, 64 * p, it.head * a.group, it.row0 + t * a.npt, bar_qfull);
-        }
-      }
       ok = __all_sync(0xffffffffu, ok && wait_lane0(bar_qfull, n_item & 1));
       // Scores buffer x = Q_t K^T, K in the ring from r on.
       const auto issue_scores = [&](int t, int x, Ring<NS> r) {
@@ -801,61 +845,79 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       }
       ok = __all_sync(0xffffffffu, ok);
     }
-  } else if (!G::kTree && warp == G::kLoadWarp) {
-    // ---- prompt: TMA loads ----
-    int sq = 0;
+  } else if (warp == G::kPlanWarp) {
+    // ---- the items, and TMA loads: Q, and of prompts K and V ----
+    Walk<G> walk(a);
+    Ring<NS> ring{0, 1};                                   // phase: of the slot's release
     uint32_t guarded = 0;
-    for (int n_item = 0; ok && walk.next(a, it); ++n_item) {
-      const int n = it.b1 - it.b0, first = it.row0 - it.pos0;
-      if (lane == 0) {
-        ok = mbar_wait(bar_qempty, (n_item & 1) ^ 1);
+    int issued = 0;
+    if (G::kTree && lane == 0) a.ws_start[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    for (int n_item = 0; ok; ++n_item) {
+      const bool more = walk.next(a, it);
+      if (!more) it.req = -1;
+      if (G::kTree && more && lane == 0 && it.slot >= 0 && it.b0 == 0) {
+        // cut behind this part: the join goes on to the part of its last unit
+        const int64_t units = walk.per_head * a.n_kv, parts = min((int64_t)a.parts, units), x = walk.u - it.b1 + it.blocks;
+        a.ws_start[blockIdx.x] = make_int4(it.head, it.req, it.pos0 / (NT * a.npt), (int)((x * parts - 1) / units));
+      }
+      if (elect_one()) {
+        const int at = n_item % G::kItems;
+        ok = mbar_wait(bar_taken + 8 * at, ((uint32_t)(n_item / G::kItems) & 1u) ^ 1u);
         if (ok) {
+          items_s[at] = it;
+          mbar_arrive(bar_item + 8 * at);
+        }
+        const auto load_q = [&] {
+          ok = ok && mbar_wait(bar_qempty, (n_item & 1) ^ 1);
+          if (!ok) return;
           const bool two = NT == 2 && Walk<G>::blocks(a, it, 1) > 0;
           const uint32_t bytes = (uint32_t)(a.npt * a.group * 128 * (D / 64));
           mbar_arrive_expect_tx(bar_qfull, two ? 2 * bytes : bytes);
           for (int t = 0; t < (two ? 2 : 1); ++t)
             for (int p = 0; p < D / 64; ++p)
               tma_load_3d(s_q + t * G::kQTile + p * G::kPanel, &tm_q, 64 * p, it.head * a.group, it.row0 + t * a.npt, bar_qfull);
-        }
-        int seq = 0;
+        };
         const auto load = [&](const CUtensorMap* map, int i) {
-          for (int p = 0; p < PD && ok; ++p, ++seq) {
-            const uint32_t s = (uint32_t)((sq + seq) % NS);
-            ok = mbar_wait(bar_empty + 8 * s, ((uint32_t)((sq + seq) / NS) & 1u) ^ 1u);
+#pragma unroll
+          for (int p = 0; p < PD; ++p, ring.next(), ++issued) {
+            ok = ok && mbar_wait(bar_empty + 8 * ring.at, ring.phase);
             if (!ok) return;
-            uint32_t bar = bar_full + 8 * s;
+            uint32_t bar = bar_full + 8 * ring.at;
             if (map == &tm_v && it.b0 + i >= it.guard) {   // goes through the scan: the slot's own phase ends at once
               mbar_arrive(bar);
               bar = bar_landed + 8 * (guarded++ % NS);
             }
             mbar_arrive_expect_tx(bar, G::kSlot);
             for (int c = 0; c < G::PANELS; ++c)
-              tma_load_2d_plain(s_ring + s * G::kSlot + c * G::kPanel, map, it.head * D + p * G::DS + 64 * c,
-                                first + (it.b0 + i) * kBlock, bar);
+              tma_load_2d_plain(s_ring + ring.at * G::kSlot + c * G::kPanel, map, it.head * D + p * G::DS + 64 * c,
+                                it.row0 - it.pos0 + (it.b0 + i) * kBlock, bar);
           }
         };
-        if (ok) load(&tm_k, 0);
-        for (int i = 0; i < n && ok; ++i) {
-          if (NB == 2) {
-            if (i + 1 < n) load(&tm_k, i + 1);
-            if (ok) load(&tm_v, i);
-          } else {
-            load(&tm_v, i);
-            if (ok && i + 1 < n) load(&tm_k, i + 1);
+        const int n = it.b1 - it.b0;
+        if (more && G::kTree) load_q();
+        if (more && !G::kTree) {
+          load(&tm_k, 0);                                  // may land while the item before still has its Q
+          load_q();
+          for (int i = 0; i < n && ok; ++i) {
+            if (NB == 2) {
+              if (i + 1 < n) load(&tm_k, i + 1);
+              load(&tm_v, i);
+            } else {
+              load(&tm_v, i);
+              if (i + 1 < n) load(&tm_k, i + 1);
+            }
           }
         }
         if (!ok) {                                         // wait for the copies in flight: the CTA may leave
-          for (int c = 0; c < NS; ++c) {
-            const int q = sq + seq - 1 - c;
-            if (q >= 0) (void)mbar_wait(bar_full + 8 * (q % NS), (uint32_t)(q / NS) & 1u);
-          }
+          for (int q = issued > NS ? issued - NS : 0; q < issued; ++q) (void)mbar_wait(bar_full + 8 * (q % NS), (uint32_t)(q / NS) & 1u);
           for (uint32_t c = guarded > NS ? guarded - NS : 0; c < guarded; ++c)
             (void)mbar_wait(bar_landed + 8 * (c % NS), (c / NS) & 1);
+          if (n_item > 0) (void)mbar_wait(bar_qfull, (n_item - 1) & 1);
           (void)mbar_wait(bar_qfull, n_item & 1);
         }
       }
       ok = __all_sync(0xffffffffu, ok);
-      sq += 2 * PD * n;
+      if (!more) break;
     }
   } else if (warp >= G::kScanWarp && warp < G::kScanWarp + G::kScanWarps) {
     // ---- V blocks of which a row does not see every token are cleared of infinities and NaN, whose
@@ -863,7 +925,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int w = warp - G::kScanWarp;
     int sq = 0;
     uint32_t guarded = 0;
-    for (int n_item = 0; ok && walk.next(a, it); ++n_item) {
+    for (int n_item = 0; ok && take(n_item); ++n_item) {
       const int n = it.b1 - it.b0;
       bool any = false;
       for (int i = max(it.guard - it.b0, 0); i < n && ok; ++i)
@@ -894,7 +956,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     Ring<NS> ring{0, 1};                                   // phase: of the slot's release
     uint32_t guarded = 0;
     int blocks_done = 0, issued = 0;
-    while (ok && walk.next(a, it)) {
+    for (int n_item = 0; ok && take(n_item); ++n_item) {
       const int n = it.b1 - it.b0;
       const auto entry = [&](int i) {                      // this lane's token of block i
         const int j = (it.b0 + i) * kBlock + 32 * w + lane;
@@ -1219,6 +1281,7 @@ extern "C" int lora_attention_prompt(lora_pool* p, int32_t n_seq, const int32_t*
   a.n_kv = n_kv_heads;
   a.group = group;
   a.npt = kTileRows / group;
+  a.group_inv = (65536 + group - 1) / group;
   a.start = seq_start;
   a.bounds = reinterpret_cast<int32_t*>(ws + L.bounds);
   a.scale_log2 = 1.4426950408889634f / std::sqrt((float)D);
@@ -1283,6 +1346,7 @@ extern "C" int lora_attention_tree(lora_pool* p, int32_t n_req, const int32_t* t
   a.n_kv = n_kv_heads;
   a.group = group;
   a.npt = kTileRows / group;
+  a.group_inv = (65536 + group - 1) / group;
   a.start = node_start;
   a.bounds = reinterpret_cast<int32_t*>(ws + L.bounds);
   a.scale_log2 = 1.4426950408889634f / std::sqrt((float)D);
