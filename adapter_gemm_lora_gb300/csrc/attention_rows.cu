@@ -148,23 +148,26 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const RowsArg
   }
 }
 
-// Of a tree request: its nodes that count, its cached tokens, and its units (blocks of tokens times tile pairs).
+// Of a tree request: its nodes that count, its cached tokens, and its units (blocks of tokens times tile groups).
 struct TreeReq {
-  int row0, nodes, len, base, blocks, pairs;
+  int row0, nodes, len, base, blocks, groups;
 };
-template <int NT>
-__device__ __forceinline__ TreeReq tree_request(const RowsArgs& a, int r) {
+template <int RT>
+__device__ __forceinline__ TreeReq tree_request(const RowsArgs& a, int row0, int row1, int length) {
   TreeReq q;
-  q.row0 = a.bounds[r];
-  q.nodes = min(a.bounds[r + 1] - q.row0, LORA_MAX_TREE);
-  q.len = min(max(a.seq_len[r], 0), a.max_len);
+  q.row0 = row0;
+  q.nodes = min(row1 - row0, LORA_MAX_TREE);
+  q.len = min(max(length, 0), a.max_len);
   q.base = max(q.len - q.nodes, 0);
   q.blocks = max((q.len + kBlock - 1) / kBlock, 1);
-  q.pairs = (q.nodes + NT * a.npt - 1) / (NT * a.npt);
+  q.groups = RT == 1 && a.npt >= LORA_MAX_TREE ? (q.nodes > 0 ? 1 : 0) : (q.nodes + RT * a.npt - 1) / (RT * a.npt);
   return q;
 }
+__device__ __forceinline__ bool tree_request_bad(const RowsArgs& a, int rows, int length) {
+  return length < 0 || length > a.max_len || rows > LORA_MAX_TREE || rows > length;
+}
 
-template <int NT>
+template <int RT>
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const RowsArgs a) {
   __shared__ int64_t part[kPlanThreads / 32];
   pdl_wait_then_release();
@@ -174,10 +177,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const RowsArgs 
     const int r = r0 + threadIdx.x;
     int64_t units = 0, total;
     if (r < a.n_req) {
-      const TreeReq q = tree_request<NT>(a, r);
-      const int m = a.bounds[r + 1] - q.row0;
-      if (a.seq_len[r] != q.len || m > LORA_MAX_TREE || m > q.len) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
-      units = (int64_t)q.blocks * q.pairs;
+      const int row0 = a.bounds[r], row1 = a.bounds[r + 1], length = a.seq_len[r];
+      if (tree_request_bad(a, row1 - row0, length)) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
+      const TreeReq q = tree_request<RT>(a, row0, row1, length);
+      units = (int64_t)q.blocks * q.groups;
     }
     const int64_t at = before + block_exclusive<int64_t>(units, part, total);
     if (r < a.n_req) a.prefix[r] = at;
@@ -187,11 +190,17 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const RowsArgs 
 }
 
 // ---- the kernel ----------------------------------------------------------------------------------
-template <int D_, bool kTree_>
+// An item is two tiles of query rows that work side by side (one tile at D = 256): rows of one KV head, which share
+// its K and V blocks, or with kPair (at most 64 nodes in a tile) the same rows of two neighbouring KV heads.
+template <int D_, bool kTree_, bool kPair_ = false>
 struct Geo {
   static constexpr int D = D_;
   static constexpr bool kTree = kTree_;
-  static constexpr int NT = D == 256 ? 1 : 2;              // row tiles of an item
+  static constexpr bool kPair = kPair_;
+  static constexpr int NT = D == 256 ? 1 : 2;              // tiles of an item
+  static constexpr int RT = kPair ? 1 : NT;                // of the rows of one head
+  static constexpr int HT = kPair ? NT : 1;                // heads
+  static_assert(!kPair || NT == 2, "a pair has two tiles");
   static constexpr int NB = 3 - NT;                        // score buffers of a tile
   static constexpr int DS = D < 128 ? D : 128;             // features of a ring slot
   static constexpr int PD = D / DS;                        // slots of a block of K or of V
@@ -202,11 +211,11 @@ struct Geo {
   static constexpr int NS = D == 64 ? 10 : 5;              // slots
   static constexpr int kSoftWarps = 4 * NT;
   static constexpr int kMmaWarp = kSoftWarps;
-  static constexpr int kPlanWarp = kSoftWarps + 1;         // finds the items; prompt: loads Q, K and V; tree: Q
-  static constexpr int kLoadWarp = kSoftWarps + 4;         // tree: four warps that gather K and V
+  static constexpr int kPlanWarp = kSoftWarps + 1;         // finds the items; tree: loads Q
+  static constexpr int kLoadWarp = kSoftWarps + (kTree ? 4 : 2);        // prompt: one warp that loads Q, K and V; tree: four that gather K and V
   static constexpr int kLoadWarps = kTree ? 4 : 1;
-  static constexpr int kScanWarp = kSoftWarps + 2;         // two warps
-  static constexpr int kScanWarps = 2;
+  static constexpr int kScanWarp = kSoftWarps + (kTree ? 2 : 3);
+  static constexpr int kScanWarps = kTree ? 2 : 1;
   static constexpr int kThreads = 32 * (kSoftWarps + (kTree ? 8 : 4));       // whole warpgroups: they trade registers
   // Registers a thread: a softmax thread holds a row of scores.  Launch 128 or 168 (D = 256: 168 or 255).
   static constexpr int kSoftRegs = NT == 1 ? 232 : kTree ? 192 : 208;
@@ -215,10 +224,10 @@ struct Geo {
   // barriers: full and empty per slot, landed and clean per guarded V slot in turn; Q full and empty; scores and
   // weights (two halves) per buffer; sums full and drained per tile; products
   static constexpr int kItems = 4;                         // items handed out at a time
-  static constexpr int kTakers = kSoftWarps + 1 + kScanWarps + (kTree ? kLoadWarps : 0);   // warps that take every item
+  static constexpr int kTakers = kSoftWarps + 1 + kScanWarps + kLoadWarps;      // warps that take every item
   static constexpr int kBars = 4 * NS + 2 + 2 + 4 + 4 + 1 + 2 * kItems;
   static constexpr int kWordsRing = 8;                     // blocks whose token masks are kept
-  static constexpr uint32_t kSmem = 1024 + kData + kBars * 8 + kWordsRing * 16 + 64;
+  static constexpr uint32_t kSmem = 1024 + kData + kBars * 8 + kWordsRing * 16 + 16 + NS * 4 + 8;
   static constexpr uint32_t kTmemO = 256;                  // scores in columns [0, 256), sums behind them
 };
 
@@ -256,6 +265,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
+}
+// mbar_wait in fewer instructions: the kernel has some thirty waits, and its warps share the instruction cache.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long c0 = clock64();
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (clock64() - c0 < kWaitLimitCycles);
+  return false;
 }
 // One thread of the warp, the same every time.  The compiler knows that a branch on it leaves one thread and keeps
 // descriptors in uniform registers: eight MMAs issue in 80 cycles, behind a branch on the lane's number in 490.
@@ -328,17 +346,18 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t u, uint32_t bad) {
   return u & ~((bad & 0x8000u ? 0xFFFFu : 0u) | (bad & 0x80000000u ? 0xFFFF0000u : 0u));
 }
-// 16 bytes of V in shared memory without their infinities and NaN; whether there were any.
-__device__ __forceinline__ bool clean16(uint32_t addr) {
+// 16 bytes of V in shared memory: whether they hold an infinity or NaN, and those bytes without them.
+__device__ __forceinline__ bool non_finite16(uint32_t addr) {
+  const uint4 x = lds128(addr);
+  return (non_finite2(x.x) | non_finite2(x.y) | non_finite2(x.z) | non_finite2(x.w)) != 0;
+}
+__device__ __forceinline__ void clean16(uint32_t addr) {
   uint4 x = lds128(addr);
-  const uint4 b = make_uint4(non_finite2(x.x), non_finite2(x.y), non_finite2(x.z), non_finite2(x.w));
-  if ((b.x | b.y | b.z | b.w) == 0) return false;
-  x.x = finite_or_zero(x.x, b.x);
-  x.y = finite_or_zero(x.y, b.y);
-  x.z = finite_or_zero(x.z, b.z);
-  x.w = finite_or_zero(x.w, b.w);
+  x.x = finite_or_zero(x.x, non_finite2(x.x));
+  x.y = finite_or_zero(x.y, non_finite2(x.y));
+  x.z = finite_or_zero(x.z, non_finite2(x.z));
+  x.w = finite_or_zero(x.w, non_finite2(x.w));
   sts128(addr, x);
-  return true;
 }
 
 // What a CTA works on at a time: the rows of a tile pair of one sequence and KV head, over some blocks of its tokens.
@@ -350,54 +369,171 @@ struct Item {
   int guard;                     // first block in which some row does not see every token
   // tree
   int len, base;                 // cached tokens, the first node's position
-  int blocks;                    // of all parts
   int slot;                      // partial, or -1: the item has all blocks
 };
 
-// The items of a CTA, one after another.
+// The items of a CTA, one after another, found by one warp.  Up to kFew sequences it reads the caller's starts and
+// lengths itself, four a lane; beyond, a kernel before this one has listed the items (prompt) or added up the units (tree).
+constexpr int kFew = 127;
 template <typename G>
 struct Walk {
-  int64_t u, u1, per_head;       // tree: units left are [u, u1)
   int w, step, all;              // prompt: turn, CTAs, items times heads
+  int level;                     // prompt, few: the level that the walk is at
+  int64_t u, u1, per_head;       // tree: units left are [u, u1)
+  int row0[4], row1[4], len[4];  // few: rows (and cached tokens) of sequences 4 lane ..
+  int tiles[4];                  // prompt, few: items of these sequences
+  int64_t before;                // tree, few: units before this lane's requests, and theirs
+  int mine[4];
+  int top_above;                 // prompt, few, at most 32 levels: items above level `lane`
+  bool few;
+
   __device__ __forceinline__ Walk(const RowsArgs& a) {
+    const int lane = threadIdx.x & 31, heads = (a.n_kv + G::HT - 1) / G::HT;
+    few = a.n_req <= kFew;
+    if (few) {
+      int32_t x[4], m = INT32_MIN;
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {                        // the running maximum, as plan_bounds
+        const int i = min(4 * lane + j, a.n_req);
+        x[j] = a.start[i];
+        if (G::kTree) len[j] = i < a.n_req ? a.seq_len[i] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        row0[j] = x[j];
+        m = x[j] = max(m, x[j]);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, m, o);
+        if (lane >= o) m = max(m, y);
+      }
+      const int32_t up = __shfl_up_sync(0xffffffffu, m, 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int32_t b = min(max(lane > 0 ? max(x[j], up) : x[j], 0), a.n_rows);
+        bad |= b != row0[j];
+        row0[j] = b;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) row1[j] = j < 3 ? row0[j + 1] : __shfl_down_sync(0xffffffffu, row0[0], 1);
+      if (lane == 31) row1[3] = row0[3];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) bad |= G::kTree && 4 * lane + j < a.n_req && tree_request_bad(a, row1[j] - row0[j], len[j]);
+      if (bad && blockIdx.x == 0) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
+    }
     if (G::kTree) {
-      per_head = a.prefix[a.n_req];
-      const int64_t units = per_head * a.n_kv, parts = min((int64_t)a.parts, units), p = blockIdx.x;
-      u = p < parts ? p * units / parts : 0;
-      u1 = p < parts ? (p + 1) * units / parts : 0;
+      if (few) {
+        int64_t sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const TreeReq q = tree_request<G::RT>(a, row0[j], row1[j], len[j]);
+          sum += mine[j] = q.blocks * q.groups;
+        }
+        int64_t incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        before = incl - sum;
+        per_head = __shfl_sync(0xffffffffu, incl, 31);
+      } else {
+        per_head = a.prefix[a.n_req];
+      }
+      const int64_t total = per_head * heads, parts = min((int64_t)a.parts, total), p = blockIdx.x;
+      u = p < parts ? p * total / parts : 0;
+      u1 = p < parts ? (p + 1) * total / parts : 0;
     } else {
       w = 0;
       step = gridDim.x;
-      all = *a.n_items * a.n_kv;
+      if (few) {
+        int sum = 0, top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          tiles[j] = (row1[j] - row0[j] + G::RT * a.npt - 1) / (G::RT * a.npt);
+          sum += tiles[j];
+          top = max(top, tiles[j]);
+        }
+        all = __reduce_add_sync(0xffffffffu, sum) * heads;
+        level = __reduce_max_sync(0xffffffffu, top) - 1;
+        top_above = -1;
+        if (level < 32) {
+          top_above = 0;
+#pragma unroll 1
+          for (int k = 0; 4 * k < a.n_req; ++k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top_above += max(__shfl_sync(0xffffffffu, tiles[j], k) - 1 - lane, 0);
+          }
+        }
+      } else {
+        all = *a.n_items * heads;
+      }
     }
+  }
+  // The part that holds unit x of all heads.
+  __device__ __forceinline__ int part_of(const RowsArgs& a, int64_t x) const {
+    const int64_t total = per_head * ((a.n_kv + G::HT - 1) / G::HT);
+    return (int)(((x + 1) * min((int64_t)a.parts, total) - 1) / total);
   }
   // All lanes of a warp take part.
   __device__ __forceinline__ bool next(const RowsArgs& a, Item& it) {
+    const int lane = threadIdx.x & 31;
     if (G::kTree) {
       if (u >= u1) return false;
-      it.head = (int)(u / per_head);
-      const int64_t x = u - it.head * per_head;
-      int lo = 0, hi = a.n_req;                            // prefix[lo] <= x < prefix[hi]: 32 places a turn
-      const int lane = threadIdx.x & 31;
-      while (hi - lo > 1) {
-        const int stride = (hi - lo + 31) / 32, at = lo + lane * stride;
-        const unsigned in = __ballot_sync(0xffffffffu, at < hi && a.prefix[min(at, hi)] <= x);
-        lo += (31 - __clz(in)) * stride;
-        hi = min(hi, lo + stride);
+      const int head = (int)(u / per_head);
+      const int64_t x = u - head * per_head;
+      int64_t y = 0;                                       // unit of the request
+      TreeReq q{};
+      if (few) {
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, before <= x));      // the lane; requests without units come after
+        y = x - __shfl_sync(0xffffffffu, before, k);
+        int r0 = 0, r1 = 0, length = 0;
+        bool found = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = __shfl_sync(0xffffffffu, mine[j], k), x0 = __shfl_sync(0xffffffffu, row0[j], k);
+          const int x1 = __shfl_sync(0xffffffffu, row1[j], k), xl = __shfl_sync(0xffffffffu, len[j], k);
+          if (found) continue;
+          found = y < n;
+          if (found) {
+            r0 = x0;
+            r1 = x1;
+            length = xl;
+            it.req = 4 * k + j;
+          } else {
+            y -= n;
+          }
+        }
+        q = tree_request<G::RT>(a, r0, r1, length);
+      } else {
+        int lo = 0, hi = a.n_req;                          // prefix[lo] <= x < prefix[hi]: 32 places a turn
+#pragma unroll 1
+        while (hi - lo > 1) {
+          const int stride = (hi - lo + 31) / 32, at = lo + lane * stride;
+          const unsigned in = __ballot_sync(0xffffffffu, at < hi && a.prefix[min(at, hi)] <= x);
+          lo += (31 - __clz(in)) * stride;
+          hi = min(hi, lo + stride);
+        }
+        q = tree_request<G::RT>(a, a.bounds[lo], a.bounds[lo + 1], a.seq_len[lo]);
+        y = x - a.prefix[lo];
+        it.req = lo;
       }
-      const TreeReq q = tree_request<G::NT>(a, lo);
-      const int y = (int)(x - a.prefix[lo]), pair = y / q.blocks;
-      it.req = lo;
-      it.b0 = y - pair * q.blocks;
+      const int group = (int)y / q.blocks;                 // a request has fewer than 2^31 units
+      it.head = head * G::HT;
+      it.b0 = (int)y - group * q.blocks;
       it.b1 = (int)min((int64_t)q.blocks, it.b0 + (u1 - u));
-      it.pos0 = pair * G::NT * a.npt;
+      it.pos0 = group * G::RT * a.npt;
       it.row0 = q.row0 + it.pos0;
       it.count = q.nodes - it.pos0;
       it.len = q.len;
       it.base = q.base;
       it.guard = q.base / kBlock;
-      it.blocks = q.blocks;
       it.slot = it.b0 == 0 && it.b1 == q.blocks ? -1 : 2 * (int)blockIdx.x + (it.b0 == 0 ? 1 : 0);
+      // cut behind this part: the join goes on to the part of its last unit
+      if (lane == 0 && it.slot >= 0 && it.b0 == 0)
+        a.ws_start[blockIdx.x] = make_int4(it.head, it.row0, min(it.count, G::RT * a.npt), part_of(a, u + q.blocks - 1));
       u += it.b1 - it.b0;
       return true;
     }
@@ -405,27 +541,76 @@ struct Walk {
     const int x = w * step + ((w & 1) ? step - 1 - (int)blockIdx.x : (int)blockIdx.x);
     if (x >= all) return false;
     ++w;
-    it.head = x % a.n_kv;
-    const int2 e = a.items[x / a.n_kv];
-    const int first = a.bounds[e.x], n = a.bounds[e.x + 1] - first;
-    it.req = e.x;
-    it.pos0 = e.y * G::NT * a.npt;
+    const int heads = (a.n_kv + G::HT - 1) / G::HT, place = x / heads;
+    int first = 0, end = 0, tile = 0;
+    it.head = (x - place * heads) * G::HT;
+    if (few) {
+      // The longest first: the lowest level with `place` or fewer items above it; the k-th sequence that has it.
+      const auto above = [&](int L) {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n += max(tiles[j] - 1 - L, 0);
+        return __reduce_add_sync(0xffffffffu, n);
+      };
+      int k;
+      if (top_above >= 0) {
+        level = __ffs(__ballot_sync(0xffffffffu, top_above <= place)) - 1;
+        k = place - __shfl_sync(0xffffffffu, top_above, level);
+      } else {
+        int lo = 0;
+#pragma unroll 1
+        while (lo < level) {
+          const int mid = (lo + level) / 2;
+          if (above(mid) <= place) level = mid;
+          else lo = mid + 1;
+        }
+        k = place - above(level);
+      }
+      bool found = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        unsigned has = __ballot_sync(0xffffffffu, tiles[j] > level);
+        const int c = __popc(has);
+        if (!found && k < c) {
+          found = true;
+#pragma unroll 1
+          for (int i = 0; i < k; ++i) has &= has - 1;
+          first = __shfl_sync(0xffffffffu, row0[j], __ffs(has) - 1);
+          end = __shfl_sync(0xffffffffu, row1[j], __ffs(has) - 1);
+        }
+        k -= c;
+      }
+      tile = level;
+      it.req = 0;
+    } else {
+      const int2 e = a.items[place];
+      first = a.bounds[e.x];
+      end = a.bounds[e.x + 1];
+      it.req = e.x;
+      tile = e.y;
+    }
+    it.pos0 = tile * G::RT * a.npt;
     it.row0 = first + it.pos0;
-    it.count = n - it.pos0;
+    it.count = end - first - it.pos0;
     it.b0 = 0;
-    it.b1 = (it.pos0 + min(it.count, G::NT * a.npt) + kBlock - 1) / kBlock;
+    it.b1 = (it.pos0 + min(it.count, G::RT * a.npt) + kBlock - 1) / kBlock;
     it.guard = it.pos0 / kBlock;
     it.slot = -1;
-    it.blocks = it.b1;
-    it.len = n;
+    it.len = end - first;
     it.base = 0;
     return true;
   }
-  // Blocks of tile t, counted from b0: none if it has no row.
+  // Of tile t of an item: its KV head, its first row from the item's, its rows' tokens (nodes), its blocks from b0 on.
+  static __device__ __forceinline__ int head(const Item& it, int t) { return it.head + (G::kPair ? t : 0); }
+  static __device__ __forceinline__ int offset(const RowsArgs& a, int t) { return G::kPair ? 0 : t * a.npt; }
+  static __device__ __forceinline__ int count(const RowsArgs& a, const Item& it, int t) {
+    if (G::kPair && it.head + t >= a.n_kv) return 0;
+    return min(it.count - offset(a, t), a.npt);
+  }
   static __device__ __forceinline__ int blocks(const RowsArgs& a, const Item& it, int t) {
-    const int left = it.count - t * a.npt;
-    if (left <= 0) return 0;
-    return G::kTree ? it.b1 - it.b0 : (it.pos0 + t * a.npt + min(left, a.npt) + kBlock - 1) / kBlock;
+    const int n = count(a, it, t);
+    if (n <= 0) return 0;
+    return G::kTree ? it.b1 - it.b0 : (it.pos0 + offset(a, t) + n + kBlock - 1) / kBlock;
   }
 };
 
@@ -446,17 +631,17 @@ struct Ring {
   }
 };
 
-// Place of a block's K and V in the order of the ring's loads, in slots, for n blocks.  Two tiles: K0 V0 K1 V1 ...;
-// one tile with two score buffers: K0 K1 V0 K2 V1 ...
+// The order of the ring's loads and their use, a block of K or V at a time (PD slots):
+//   two tiles of one head  K0 V0 K1 V1 ...
+//   one tile, two buffers  K0 K1 V0 K2 V1 ...
+//   two heads a, b         K0a K0b V0a K1a V0b K1b ...
+// Step s of the 2 n of an item's n blocks: whether V, and which block.
 template <typename G>
-__device__ __forceinline__ int seq_k(int i) {
-  return (G::NB == 1 ? 2 * i : i == 0 ? 0 : 2 * i - 1) * G::PD;
+__device__ __forceinline__ bool step_of(int s, int n, int& i) {
+  const bool is_v = G::NB == 1 ? s & 1 : s > 0 && (!(s & 1) || s == 2 * n - 1);
+  i = G::NB == 1 ? s / 2 : is_v ? (s == 2 * n - 1 ? n - 1 : s / 2 - 1) : (s + 1) / 2;
+  return is_v;
 }
-template <typename G>
-__device__ __forceinline__ int seq_v(int i, int n) {
-  return (G::NB == 1 || i == n - 1 ? 2 * i + 1 : 2 * i + 2) * G::PD;
-}
-
 template <typename G>
 __global__ void __launch_bounds__(G::kThreads, 1)
 rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -476,8 +661,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   uint8_t* tail = smem_raw + (base - smem_u32(smem_raw)) + G::kData + G::kBars * 8 + (G::kBars & 1) * 8;
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(tail);        // [kWordsRing][4]: a block's tokens that have data
   volatile int* first_bad = reinterpret_cast<volatile int*>(words + G::kWordsRing * 4);   // this CTA's first item with V cleared
+  volatile uint32_t* guard_slot = words + G::kWordsRing * 4 + 4;                // [NS]: where guarded V slots lie, in turn
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int s = 0; s < NS; ++s) {
       mbar_init(bar_full + 8 * s, G::kLoadWarps);
       mbar_init(bar_empty + 8 * s, 1);
@@ -515,7 +702,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   // The n-th item, as the planning warp found it; false behind the last one.
   const auto take = [&](int n) {
     const int at = n % G::kItems;
-    if (!__all_sync(0xffffffffu, mbar_wait(bar_item + 8 * at, (uint32_t)(n / G::kItems) & 1u))) {
+    if (!__all_sync(0xffffffffu, wait_for(bar_item + 8 * at, (uint32_t)(n / G::kItems) & 1u))) {
       ok = false;
       return false;
     }
@@ -523,6 +710,19 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_taken + 8 * at);
     return it.req >= 0;
+  };
+  // Q of the item `it`, the n-th, by one thread.
+  const auto load_q = [&](int n) {
+    if (!wait_for(bar_qempty, (n & 1) ^ 1)) return false;
+    const bool two = NT == 2 && Walk<G>::blocks(a, it, 1) > 0;
+    const uint32_t bytes = (uint32_t)(a.npt * a.group * 128 * (D / 64));
+    mbar_arrive_expect_tx(bar_qfull, two ? 2 * bytes : bytes);
+#pragma unroll 1
+    for (int t = 0; t < (two ? 2 : 1); ++t)
+      for (int p = 0; p < D / 64; ++p)
+        tma_load_3d(s_q + t * G::kQTile + p * G::kPanel, &tm_q, 64 * p, Walk<G>::head(it, t) * a.group,
+                    it.row0 + Walk<G>::offset(a, t), bar_qfull);
+    return true;
   };
 
   if (warp < G::kSoftWarps) {
@@ -543,16 +743,17 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         blocks_done += nb_all;
         continue;
       }
-      const int left = min(it.count - t * a.npt, a.npt);   // tokens (nodes) of the tile
+      const int left = Walk<G>::count(a, it, t), row0 = it.row0 + Walk<G>::offset(a, t);
+      const int pos0 = it.pos0 + Walk<G>::offset(a, t);    // left: tokens (nodes) of the tile
       const bool live = tok < left;
-      const int pos = it.pos0 + t * a.npt + min(tok, left - 1);
+      const int pos = pos0 + min(tok, left - 1);
       uint64_t mask = 0;
-      if (G::kTree) mask = a.mask[it.row0 + t * a.npt + min(tok, left - 1)];
+      if (G::kTree) mask = a.mask[row0 + min(tok, left - 1)];
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < nb; ++i) {
         const int x = NB == 1 ? t : (i & 1);
         const uint32_t scores = tmem + (uint32_t)(x * 128) + lane_off;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_scores + 8 * x, use[x] & 1))) {
+        if (!__all_sync(0xffffffffu, wait_for(bar_scores + 8 * x, use[x] & 1))) {
           ok = false;
           break;
         }
@@ -579,7 +780,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             for (int c = 0; c < 128; ++c)
               if (!((vis[c / 32] >> (c % 32)) & 1)) s[c / 32][c % 32] = 0xff800000u;
           }
-        } else if (it.b0 + i >= (it.pos0 + t * a.npt) / kBlock) {
+        } else if (it.b0 + i >= pos0 / kBlock) {
           const int last = pos - j0;
 #pragma unroll
           for (int c = 0; c < 128; ++c)
@@ -595,7 +796,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           l *= c;
           m = mn;
           if (i > 0) {
-            if (NB == 2 && !__all_sync(0xffffffffu, mbar_wait(bar_product, (products + i - 1) & 1))) {
+            if (NB == 2 && !__all_sync(0xffffffffu, wait_for(bar_product, (products + i - 1) & 1))) {
               ok = false;
               break;
             }
@@ -644,16 +845,16 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       products += nb;
       blocks_done += nb_all;
       // ---- the tile's outputs ----
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_sums + 8 * t, items_t & 1))) {
+      if (!__all_sync(0xffffffffu, wait_for(bar_sums + 8 * t, items_t & 1))) {
         ok = false;
         break;
       }
       ++items_t;
       tc_fence_after();
       const bool part = it.slot >= 0;
-      const int64_t orow = it.row0 + t * a.npt + tok;
-      const int head = it.head * a.group + g;
-      const int64_t prow = (int64_t)it.slot * a.slot_rows + t * kTileRows + row;
+      const int64_t orow = row0 + tok;
+      const int kv = Walk<G>::head(it, t), head = kv * a.group + g;
+      const int64_t prow = (int64_t)it.slot * a.slot_rows + t * (a.slot_rows / NT) + row;
       const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
       const uint32_t sums = tmem + G::kTmemO + (uint32_t)(t * D) + lane_off;
       // Of a finished tile four lanes exchange their 16-byte pieces, so that each store covers 64 bytes of eight
@@ -662,8 +863,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = (row & ~3) + e, tok_r = (int)(r * a.group_inv >> 16);
-        dst[e] = tok_r < left ? a.out + (it.row0 + t * a.npt + tok_r) * a.out_stride +
-                                    (int64_t)(it.head * a.group + r - tok_r * a.group) * D + 8 * (lane & 3)
+        dst[e] = tok_r < left ? a.out + (int64_t)(row0 + tok_r) * a.out_stride + (int64_t)(kv * a.group + r - tok_r * a.group) * D + 8 * (lane & 3)
                               : nullptr;
       }
 #pragma unroll 1
@@ -711,9 +911,9 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               if (j >= it.base && !((mask >> (j - it.base)) & 1)) continue;
               const int2 pg = a.table[((int64_t)it.req * a.max_len + j) * a.layers + a.layer];
               if (pg.x < 0 || pg.x >= a.num_pages || pg.y < 0 || pg.y >= a.num_pages) continue;
-              v = a.pool + (int64_t)pg.y * a.H + it.head * D + d;
+              v = a.pool + (int64_t)pg.y * a.H + kv * D + d;
             } else {
-              v = a.v + (it.row0 - it.pos0 + j) * a.v_stride + it.head * D + d;
+              v = a.v + (row0 - pos0 + j) * a.v_stride + kv * D + d;
             }
             const uint32_t x = *v;
             if ((x & 0x7F80u) == 0x7F80u) c += __uint_as_float(x << 16);
@@ -735,23 +935,23 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // ---- products: one thread issues ----
     constexpr uint32_t kIdescS = make_idesc_bf16(kTileRows, kBlock);
     constexpr uint32_t kIdescO = make_idesc_bf16(kTileRows, G::DS) | (1u << 16);        // B (V) is MN-major
-    uint32_t use[2] = {0, 0}, items_t[2] = {0, 0}, guarded = 0;         // guarded: V slots that were scanned so far
+    uint32_t used = 0, items_t = 0, guarded = 0;           // bit x: phases of buffer x, tile x; V slots that were scanned so far
     Ring<NS> ring{0, 0};
     // Operands' descriptors: the low words move, the high ones (strides, version, swizzle) do not.
     const uint32_t lo_q = (uint32_t)sw128_kmajor_desc(s_q), lo_ring = (s_ring & 0x3FFFFu) >> 4;
     constexpr uint32_t kLdK = 1u << 16, kLdV = (G::kPanel >> 4) << 16;   // leading-dimension offsets
     const uint32_t kHiK = (uint32_t)(sw128_kmajor_desc(0) >> 32), kHiV = (uint32_t)(sw128_mnmajor_desc(0, G::kPanel, 1024) >> 32);
     const auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
-    const auto wait_lane0 = [&](uint32_t bar, uint32_t parity) { return lane != 0 || mbar_wait(bar, parity); };
+    const auto wait_lane0 = [&](uint32_t bar, uint32_t parity) { return lane != 0 || wait_for(bar, parity); };
     for (int n_item = 0; ok && take(n_item); ++n_item) {
-      int nb[2] = {Walk<G>::blocks(a, it, 0), NT == 2 ? Walk<G>::blocks(a, it, 1) : 0};
+      const int nb0 = Walk<G>::blocks(a, it, 0), nb1 = NT == 2 ? Walk<G>::blocks(a, it, 1) : 0;
       const int n = it.b1 - it.b0;
       ok = __all_sync(0xffffffffu, ok && wait_lane0(bar_qfull, n_item & 1));
       // Scores buffer x = Q_t K^T, K in the ring from r on.
       const auto issue_scores = [&](int t, int x, Ring<NS> r) {
 #pragma unroll
         for (int p = 0; p < PD; ++p, r.next()) {
-          if (!mbar_wait(bar_full + 8 * r.at, r.phase)) return false;
+          if (!wait_for(bar_full + 8 * r.at, r.phase)) return false;
           tc_fence_after();
           const uint32_t qd = lo_q + (((uint32_t)t * G::kQTile + (uint32_t)p * G::PANELS * G::kPanel) >> 4);
           const uint32_t kd = (lo_ring | kLdK) + r.at * (G::kSlot >> 4);
@@ -769,19 +969,19 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
         for (int p = 0; p < PD; ++p, r.next()) {
           const uint32_t n_th = guarded + p;               // of the V slots that are scanned: landed and cleared of infinities
-          if (!(guard ? mbar_wait(bar_clean + 8 * (n_th % NS), (n_th / NS) & 1) : mbar_wait(bar_full + 8 * r.at, r.phase)))
+          if (!(guard ? wait_for(bar_clean + 8 * (n_th % NS), (n_th / NS) & 1) : wait_for(bar_full + 8 * r.at, r.phase)))
             return false;
           const uint32_t vd = (lo_ring | kLdV) + r.at * (G::kSlot >> 4);
 #pragma unroll
           for (int k = 0; k < kBlock / 16; ++k) {
             if (p == 0 && k % 4 == 0) {                    // half of the weights
-              if (!mbar_wait(bar_weights + 16 * x + 2 * k, use[x] & 1)) return false;
+              if (!wait_for(bar_weights + 16 * x + 2 * k, (used >> x) & 1)) return false;
               tc_fence_after();
             }
             mma_bf16_ts(tmem + G::kTmemO + t * D + p * G::DS, tmem + x * 128 + k * 8, desc(vd + ((k * 2048) >> 4), kHiV), kIdescO, add || k > 0);
           }
         }
-        ++use[x];
+        used ^= 1u << x;
         return true;
       };
       const auto release = [&](Ring<NS> r) {
@@ -790,100 +990,96 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       };
       if (ok && elect_one()) {
         tc_fence_after();
-        if (NB == 1) {                                     // K0 V0 K1 V1 ...
-          for (int t = 0; t < NT && ok; ++t)
-            if (nb[t] > 0) ok = issue_scores(t, t, ring);
-          if (ok) release(ring);
-          if (ok && n == 1) mma_commit(bar_qempty);
-          ring.next();
-          for (int i = 0; i < n && ok; ++i) {
-            const bool guard = it.b0 + i >= it.guard;
-            Ring<NS> next = ring;
-            next.next();
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              if (!ok || i >= nb[t]) continue;
-              if (i == 0) ok = mbar_wait(bar_drained + 8 * t, (items_t[t]++ & 1) ^ 1);
-              ok = ok && issue_product(t, t, ring, guard, i > 0);
-              if (ok && i + 1 == nb[t]) mma_commit(bar_sums + 8 * t);
-              if (ok && i + 1 < nb[t]) ok = issue_scores(t, t, next);
+        constexpr bool kOwn = G::kPair || NB == 2;         // no two tiles share a block
+        // Scores are NB blocks ahead of the products.
+#pragma unroll 1
+        for (int i = -NB; i < n && ok; ++i) {
+          const bool guard = it.b0 + i >= it.guard;
+          Ring<NS> next = ring;                            // where the scores' K lies
+          if (i >= 0) next.template skip<PD>();
+#pragma unroll 1
+          for (int t = 0; t < NT && ok; ++t) {
+            const int x = NB == 1 ? t : (i & 1);
+            const int nb = t == 0 ? nb0 : nb1;
+            if (i >= nb) continue;
+            if (i >= 0) {
+              if (i == 0) {
+                ok = wait_for(bar_drained + 8 * t, ((items_t >> t) & 1) ^ 1);
+                items_t ^= 1u << t;
+              }
+              ok = ok && issue_product(t, x, ring, guard, i > 0);
+              if (!ok) continue;
+              if (kOwn) {
+                release(ring);
+                ring.template skip<PD>();
+                if (guard) guarded += PD;
+              }
+              if (NB == 2) mma_commit(bar_product);
+              if (i + 1 == nb) mma_commit(bar_sums + 8 * t);
             }
-            if (!ok) break;
-            if (guard) guarded += PD;
-            release(ring);
-            if (i + 1 < n) release(next);
-            if (i + 2 == n) mma_commit(bar_qempty);
-            ring = next;
-            if (i + 1 < n) ring.next();
+            if (i + NB < nb) {
+              ok = issue_scores(t, x, kOwn ? ring : next);
+              if (ok && kOwn) {
+                release(ring);
+                ring.template skip<PD>();
+              }
+            }
           }
-        } else {                                           // K0 K1 V0 K2 V1 ...
-          for (int i = 0; i < 2 && i < n && ok; ++i) {
-            ok = issue_scores(0, i, ring);
-            if (ok) release(ring);
-            ring.template skip<PD>();
-          }
-          if (ok && n <= 2) mma_commit(bar_qempty);
-          for (int i = 0; i < n && ok; ++i) {
-            const int x = i & 1;
-            const bool guard = it.b0 + i >= it.guard;
-            if (i == 0) ok = mbar_wait(bar_drained, (items_t[0]++ & 1) ^ 1);
-            ok = ok && issue_product(0, x, ring, guard, i > 0);
-            if (!ok) break;
-            if (guard) guarded += PD;
-            release(ring);
-            ring.template skip<PD>();
-            mma_commit(bar_product);
-            if (i + 1 == n) mma_commit(bar_sums);
-            if (i + 2 < n) {
-              ok = issue_scores(0, x, ring);
-              if (ok) release(ring);
+          if (!ok) break;
+          if (!kOwn) {
+            if (i >= 0) {
+              release(ring);
+              ring = next;
+              if (guard) guarded += PD;
+            }
+            if (i + NB < n) {
+              release(ring);
               ring.template skip<PD>();
-              if (ok && i + 3 == n) mma_commit(bar_qempty);
             }
           }
+          if (i + NB + 1 == n) mma_commit(bar_qempty);
         }
       }
       ok = __all_sync(0xffffffffu, ok);
     }
   } else if (warp == G::kPlanWarp) {
-    // ---- the items, and TMA loads: Q, and of prompts K and V ----
+    // ---- the items; of trees Q ----
     Walk<G> walk(a);
-    Ring<NS> ring{0, 1};                                   // phase: of the slot's release
-    uint32_t guarded = 0;
-    int issued = 0;
     if (G::kTree && lane == 0) a.ws_start[blockIdx.x] = make_int4(-1, 0, 0, 0);
     for (int n_item = 0; ok; ++n_item) {
       const bool more = walk.next(a, it);
       if (!more) it.req = -1;
-      if (G::kTree && more && lane == 0 && it.slot >= 0 && it.b0 == 0) {
-        // cut behind this part: the join goes on to the part of its last unit
-        const int64_t units = walk.per_head * a.n_kv, parts = min((int64_t)a.parts, units), x = walk.u - it.b1 + it.blocks;
-        a.ws_start[blockIdx.x] = make_int4(it.head, it.req, it.pos0 / (NT * a.npt), (int)((x * parts - 1) / units));
-      }
       if (elect_one()) {
         const int at = n_item % G::kItems;
-        ok = mbar_wait(bar_taken + 8 * at, ((uint32_t)(n_item / G::kItems) & 1u) ^ 1u);
+        ok = wait_for(bar_taken + 8 * at, ((uint32_t)(n_item / G::kItems) & 1u) ^ 1u);
         if (ok) {
           items_s[at] = it;
           mbar_arrive(bar_item + 8 * at);
         }
-        const auto load_q = [&] {
-          ok = ok && mbar_wait(bar_qempty, (n_item & 1) ^ 1);
-          if (!ok) return;
-          const bool two = NT == 2 && Walk<G>::blocks(a, it, 1) > 0;
-          const uint32_t bytes = (uint32_t)(a.npt * a.group * 128 * (D / 64));
-          mbar_arrive_expect_tx(bar_qfull, two ? 2 * bytes : bytes);
-          for (int t = 0; t < (two ? 2 : 1); ++t)
-            for (int p = 0; p < D / 64; ++p)
-              tma_load_3d(s_q + t * G::kQTile + p * G::kPanel, &tm_q, 64 * p, it.head * a.group, it.row0 + t * a.npt, bar_qfull);
-        };
-        const auto load = [&](const CUtensorMap* map, int i) {
+        if (G::kTree && more) {
+          ok = ok && load_q(n_item);
+          if (!ok && n_item > 0) (void)wait_for(bar_qfull, (n_item - 1) & 1);    // a copy may be in flight: the CTA may leave
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!more) break;
+    }
+  } else if (!G::kTree && warp == G::kLoadWarp) {
+    // ---- prompt: TMA loads ----
+    Ring<NS> ring{0, 1};                                   // phase: of the slot's release
+    uint32_t guarded = 0;
+    int issued = 0;
+    for (int n_item = 0; ok && take(n_item); ++n_item) {
+      if (elect_one()) {
+        const auto load = [&](bool is_v, int i) {
+          const CUtensorMap* map = is_v ? &tm_v : &tm_k;
 #pragma unroll
           for (int p = 0; p < PD; ++p, ring.next(), ++issued) {
-            ok = ok && mbar_wait(bar_empty + 8 * ring.at, ring.phase);
+            ok = ok && wait_for(bar_empty + 8 * ring.at, ring.phase);
             if (!ok) return;
             uint32_t bar = bar_full + 8 * ring.at;
-            if (map == &tm_v && it.b0 + i >= it.guard) {   // goes through the scan: the slot's own phase ends at once
+            if (is_v && it.b0 + i >= it.guard) {   // goes through the scan: the slot's own phase ends at once
+              guard_slot[guarded % NS] = ring.at;
               mbar_arrive(bar);
               bar = bar_landed + 8 * (guarded++ % NS);
             }
@@ -894,60 +1090,51 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           }
         };
         const int n = it.b1 - it.b0;
-        if (more && G::kTree) load_q();
-        if (more && !G::kTree) {
-          load(&tm_k, 0);                                  // may land while the item before still has its Q
-          load_q();
-          for (int i = 0; i < n && ok; ++i) {
-            if (NB == 2) {
-              if (i + 1 < n) load(&tm_k, i + 1);
-              load(&tm_v, i);
-            } else {
-              load(&tm_v, i);
-              if (i + 1 < n) load(&tm_k, i + 1);
-            }
-          }
+#pragma unroll 1
+        for (int s = 0; s < 2 * n && ok; ++s) {            // K0 may land while the item before still has its Q
+          int i;
+          const bool is_v = step_of<G>(s, n, i);
+          load(is_v, i);
+          if (s == 0) ok = ok && load_q(n_item);
         }
         if (!ok) {                                         // wait for the copies in flight: the CTA may leave
-          for (int q = issued > NS ? issued - NS : 0; q < issued; ++q) (void)mbar_wait(bar_full + 8 * (q % NS), (uint32_t)(q / NS) & 1u);
+#pragma unroll 1
+          for (int q = issued > NS ? issued - NS : 0; q < issued; ++q) (void)wait_for(bar_full + 8 * (q % NS), (uint32_t)(q / NS) & 1u);
+#pragma unroll 1
           for (uint32_t c = guarded > NS ? guarded - NS : 0; c < guarded; ++c)
-            (void)mbar_wait(bar_landed + 8 * (c % NS), (c / NS) & 1);
-          if (n_item > 0) (void)mbar_wait(bar_qfull, (n_item - 1) & 1);
-          (void)mbar_wait(bar_qfull, n_item & 1);
+            (void)wait_for(bar_landed + 8 * (c % NS), (c / NS) & 1);
+          if (n_item > 0) (void)wait_for(bar_qfull, (n_item - 1) & 1);
+          (void)wait_for(bar_qfull, n_item & 1);
         }
       }
       ok = __all_sync(0xffffffffu, ok);
-      if (!more) break;
     }
   } else if (warp >= G::kScanWarp && warp < G::kScanWarp + G::kScanWarps) {
     // ---- V blocks of which a row does not see every token are cleared of infinities and NaN, whose
     // products with the weights 0 would be NaN; the tile's outputs get those that a row does see ----
     const int w = warp - G::kScanWarp;
-    int sq = 0;
     uint32_t guarded = 0;
     for (int n_item = 0; ok && take(n_item); ++n_item) {
-      const int n = it.b1 - it.b0;
-      bool any = false;
-      for (int i = max(it.guard - it.b0, 0); i < n && ok; ++i)
-        for (int p = 0; p < PD && ok; ++p) {
-          const int q = sq + seq_v<G>(i, n) + p;
-          const uint32_t s = (uint32_t)(q % NS);
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_landed + 8 * (guarded % NS), (guarded / NS) & 1));
+      const int n = it.b1 - it.b0, tiles = G::kPair && Walk<G>::blocks(a, it, 1) > 0 ? 2 : 1;
+#pragma unroll 1
+      for (int left = (n - max(it.guard - it.b0, 0)) * PD * tiles; left > 0 && ok; --left) {
+          ok = __all_sync(0xffffffffu, wait_for(bar_landed + 8 * (guarded % NS), (guarded / NS) & 1));
           if (!ok) break;
-          const uint32_t at = s_ring + s * G::kSlot + w * (G::kSlot / 2) + lane * 16;
+          const uint32_t s = guard_slot[guarded % NS];
+          const uint32_t at = s_ring + s * G::kSlot + w * (G::kSlot / G::kScanWarps) + lane * 16;
           bool bad = false;
-#pragma unroll 8
-          for (uint32_t o = 0; o < G::kSlot / 2; o += 512) bad |= clean16(at + o);
-          any |= bad;
-          if (__any_sync(0xffffffffu, any)) {
+#pragma unroll 4
+          for (uint32_t o = 0; o < G::kSlot / G::kScanWarps; o += 512) bad |= non_finite16(at + o);
+          if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+            for (uint32_t o = 0; o < G::kSlot / G::kScanWarps; o += 512) clean16(at + o);
             if (lane == 0) atomicMin(const_cast<int*>(first_bad), n_item);
             fence_proxy_async_shared();
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_clean + 8 * (guarded % NS));
           ++guarded;
-        }
-      sq += 2 * PD * n;
+      }
     }
   } else if (G::kTree && warp >= G::kLoadWarp) {
     // ---- tree: rows of K and V from their pages, gathered four at a time by TMA, each warp 32 of a block's tokens ----
@@ -967,7 +1154,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         if (i < n && (it.b0 + i) * kBlock + 32 * w + lane < it.len) flag_error(a.err, LORA_DEV_BAD_PAGE);
         return make_int2(-1, -1);
       };
-      const auto load = [&](int2 e, bool is_v, int i) {
+      const auto load = [&](int2 e, bool is_v, int i, int t) {
         __syncwarp();
         ids[lane] = is_v ? e.y : e.x;
         const unsigned has = __ballot_sync(0xffffffffu, e.x >= 0);
@@ -975,19 +1162,20 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
         for (int p = 0; p < PD; ++p, ring.next()) {
           const uint32_t s = ring.at;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * s, ring.phase));
+          ok = __all_sync(0xffffffffu, wait_for(bar_empty + 8 * s, ring.phase));
           if (!ok) return;
           const bool guard = is_v && it.b0 + i >= it.guard;
           if (elect_one()) {
-            if (!is_v && p == 0) words[((blocks_done + i) % G::kWordsRing) * 4 + w] = has;
+            if (!is_v && p == 0 && t == 0) words[((blocks_done + i) % G::kWordsRing) * 4 + w] = has;
             uint32_t bar = bar_full + 8 * s;
             if (guard) {                                   // goes through the scan: the slot's own phase ends at once
+              guard_slot[guarded % NS] = s;
               mbar_arrive(bar);
               bar = bar_landed + 8 * (guarded % NS);
             }
             mbar_arrive_expect_tx(bar, 32 * G::DS * 2);
             const uint32_t dst = s_ring + s * G::kSlot + w * 32 * 128;
-            const int x = it.head * D + p * G::DS;
+            const int x = Walk<G>::head(it, t) * D + p * G::DS;
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
               const int4 rows = *reinterpret_cast<const int4*>(ids + 4 * g);
@@ -1000,26 +1188,43 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
       };
       int2 e0 = checked(entry(0), 0), e1 = entry(1);
-      load(e0, false, 0);
-      for (int i = 0; i < n && ok; ++i) {
-        const int2 e2 = entry(i + 2);
-        e1 = checked(e1, i + 1);
-        if (NB == 2) {
-          if (i + 1 < n) load(e1, false, i + 1);
-          if (ok) load(e0, true, i);
-        } else {
-          load(e0, true, i);
-          if (ok && i + 1 < n) load(e1, false, i + 1);
+      const int tiles = G::kPair && Walk<G>::blocks(a, it, 1) > 0 ? 2 : 1;
+#pragma unroll 1
+      for (int s = 0; s < 2 * n && ok; ++s) {
+        int i;
+        const bool is_v = step_of<G>(s, n, i);
+        int2 e2 = e1;
+        if (is_v) {                                        // entries are read two blocks ahead
+          e2 = entry(i + 2);
+          if (NB == 1) e1 = checked(e1, i + 1);
+        } else if (NB == 2 && i > 0) {
+          e1 = checked(e1, i);
         }
-        e0 = e1;
-        e1 = e2;
+        if (!G::kPair) {
+          load(is_v || i == 0 || NB == 1 ? e0 : e1, is_v, i, 0);
+          if (is_v) {
+            e0 = e1;
+            e1 = e2;
+          }
+        } else if (s == 0) {
+#pragma unroll 1
+          for (int t = 0; t < tiles && ok; ++t) load(e0, false, 0, t);
+        } else if (is_v) {                                 // V_i of a head, then its K of the next block
+#pragma unroll 1
+          for (int u = 0; u < 2 * tiles && ok; ++u)
+            if (!(u & 1) || i + 1 < n) load(u & 1 ? e1 : e0, !(u & 1), i + (u & 1), u >> 1);
+          e0 = e1;
+          e1 = e2;
+        }
       }
       blocks_done += n;
     }
     if (!ok && lane == 0) {                                // wait for the copies in flight: the CTA may leave
-      for (int q = issued > NS ? issued - NS : 0; q < issued; ++q) (void)mbar_wait(bar_full + 8 * (q % NS), (uint32_t)(q / NS) & 1u);
+#pragma unroll 1
+      for (int q = issued > NS ? issued - NS : 0; q < issued; ++q) (void)wait_for(bar_full + 8 * (q % NS), (uint32_t)(q / NS) & 1u);
+#pragma unroll 1
       for (uint32_t c = guarded > NS ? guarded - NS : 0; c < guarded; ++c)
-        (void)mbar_wait(bar_landed + 8 * (c % NS), (c / NS) & 1);
+        (void)wait_for(bar_landed + 8 * (c % NS), (c / NS) & 1);
     }
   }
   if (!ok && lane == 0) flag_error(a.err, LORA_DEV_WAIT_TIMEOUT);
@@ -1032,20 +1237,22 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 // Segments that lie in several parts: block (p, y) takes the one that begins in part p and goes on behind it, a
 // warp per row.  m = max m_i, l = sum l_i 2^(m_i - m), out = sum o_i 2^(m_i - m) / l, in the parts' order.
 constexpr int kJoinWarps = 8;
-template <int D, int NT>
+template <typename G>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ RowsArgs a) {
-  constexpr int E = D / 32;
+  constexpr int D = G::D, E = D / 32;
   pdl_wait_then_release();
   const int p = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 rec = a.ws_start[p];
+  const int4 rec = a.ws_start[p];                          // head, first row, nodes, last part
   if (rec.x < 0) return;
-  const TreeReq q = tree_request<NT>(a, rec.y);
-  const int pos0 = rec.z * NT * a.npt, rows = min(q.nodes - pos0, NT * a.npt) * a.group;
-  for (int x = blockIdx.y * kJoinWarps + warp; x < rows; x += gridDim.y * kJoinWarps) {
-    const int node = x / a.group, g = x - node * a.group, t = node / a.npt;
-    const int64_t at = t * kTileRows + (node - t * a.npt) * a.group + g;
+  const int rows = rec.z * a.group, heads = min(G::HT, a.n_kv - rec.x);
+#pragma unroll 1
+  for (int x = blockIdx.y * kJoinWarps + warp; x < rows * heads; x += gridDim.y * kJoinWarps) {
+    const int h = x / rows, r = x - h * rows, node = r / a.group, g = r - node * a.group;
+    const int t = G::kPair ? h : node / a.npt;
+    const int64_t at = t * (a.slot_rows / G::NT) + (G::kPair ? node : node - t * a.npt) * a.group + g;
     const auto slot = [&](int i) { return (2 * (int64_t)i + (i == p ? 1 : 0)) * a.slot_rows + at; };
     float m = -INFINITY;
+#pragma unroll 1
     for (int i = p + lane; i <= rec.w; i += 32) m = fmaxf(m, a.ws_ml[slot(i)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -1053,6 +1260,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
     float l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
     for (int i0 = p; i0 <= rec.w; i0 += 32) {
       float2 ml = make_float2(-INFINITY, 0.f);
       if (i0 + lane <= rec.w) ml = a.ws_ml[slot(i0 + lane)];
@@ -1072,8 +1280,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
       }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t row = q.row0 + pos0 + node;
-    const int head = rec.x * a.group + g;
+    const int64_t row = rec.y + node;
+    const int head = (rec.x + h) * a.group + g;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * a.out_stride + (int64_t)head * D + lane * E);
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = l == 0.f ? 0u : pack_bf16(acc[e] * inv, acc[e + 1] * inv);
@@ -1172,7 +1380,8 @@ struct TreeLayout {
 TreeLayout tree_layout(int D, int32_t n_req, int32_t group) {
   TreeLayout L{};
   L.parts = device_sm_count();
-  L.slot_rows = kTileRows / group >= LORA_MAX_TREE ? LORA_MAX_TREE * group : tiles_of(D) * kTileRows;
+  const bool one = kTileRows / group >= LORA_MAX_TREE;     // a request's nodes fit a tile: two heads side by side
+  L.slot_rows = one ? tiles_of(D) * LORA_MAX_TREE * group : tiles_of(D) * kTileRows;
   const size_t slots = 2 * (size_t)L.parts * L.slot_rows;
   size_t off = 0;
   L.bounds = off;  off = align256(off + ((size_t)n_req + 1) * 4);
@@ -1198,12 +1407,12 @@ int launch_rows(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, con
 int launch_prompt(const lora_pool* p, const RowsArgs& a, const PromptLayout& L, const CUtensorMap& q, const CUtensorMap& k,
                   const CUtensorMap& v, cudaStream_t st) {
   const char* what = "lora_attention_prompt launch";
-  cudaError_t e;
-  {
+  if (a.n_req > kFew) {
     ProfScope prof(p, LORA_KIND_ATTENTION, st);
-    e = launch_pdl(!p->prof_on, prompt_plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)L.levels * 4, st, a, L.per_item, L.levels);
+    const cudaError_t e = launch_pdl(!p->prof_on, prompt_plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)L.levels * 4, st, a,
+                                     L.per_item, L.levels);
+    if (e != cudaSuccess) return lora_cuda_fail(e, what);
   }
-  if (e != cudaSuccess) return lora_cuda_fail(e, what);
   const int64_t most = ((int64_t)a.n_rows / L.per_item + a.n_req) * a.n_kv;
   const int ctas = (int)std::min<int64_t>(device_sm_count(), most);
   switch (p->H / a.n_kv) {
@@ -1213,20 +1422,18 @@ int launch_prompt(const lora_pool* p, const RowsArgs& a, const PromptLayout& L, 
   }
 }
 
-template <int D>
+template <typename G>
 int launch_tree(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, const CUtensorMap& pages, cudaStream_t st) {
-  using G = Geo<D, true>;
   const char* what = "lora_attention_tree launch";
-  cudaError_t e;
-  {
+  if (a.n_req > kFew) {
     ProfScope prof(p, LORA_KIND_ATTENTION, st);
-    e = launch_pdl(!p->prof_on, tree_plan_kernel<G::NT>, dim3(1), dim3(kPlanThreads), 0, st, a);
+    const cudaError_t e = launch_pdl(!p->prof_on, tree_plan_kernel<G::RT>, dim3(1), dim3(kPlanThreads), 0, st, a);
+    if (e != cudaSuccess) return lora_cuda_fail(e, what);
   }
-  if (e != cudaSuccess) return lora_cuda_fail(e, what);
   const int rc = launch_rows<G>(p, a, q, pages, pages, a.parts, what, st);
   if (rc != LORA_OK) return rc;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
-  e = launch_pdl(!p->prof_on, tree_join_kernel<D, G::NT>, dim3(a.parts, 8), dim3(32 * kJoinWarps), 0, st, a);
+  const cudaError_t e = launch_pdl(!p->prof_on, tree_join_kernel<G>, dim3(a.parts, 8), dim3(32 * kJoinWarps), 0, st, a);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, what);
 }
 
@@ -1367,9 +1574,10 @@ extern "C" int lora_attention_tree(lora_pool* p, int32_t n_req, const int32_t* t
   a.parts = L.parts;
   a.slot_rows = L.slot_rows;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool one = a.npt >= LORA_MAX_TREE;                 // as tree_layout
   switch (D) {
-    case 64: return launch_tree<64>(p, a, tm_q, tm_pages, st);
-    case 128: return launch_tree<128>(p, a, tm_q, tm_pages, st);
-    default: return launch_tree<256>(p, a, tm_q, tm_pages, st);
+    case 64: return one ? launch_tree<Geo<64, true, true>>(p, a, tm_q, tm_pages, st) : launch_tree<Geo<64, true>>(p, a, tm_q, tm_pages, st);
+    case 128: return one ? launch_tree<Geo<128, true, true>>(p, a, tm_q, tm_pages, st) : launch_tree<Geo<128, true>>(p, a, tm_q, tm_pages, st);
+    default: return launch_tree<Geo<256, true>>(p, a, tm_q, tm_pages, st);
   }
 }
