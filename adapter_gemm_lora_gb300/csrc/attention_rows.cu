@@ -29,6 +29,7 @@ struct RowsArgs {
   int64_t out_stride;
   float* lse;
   int32_t n_req, n_rows, n_heads, n_kv, group;
+  int32_t few;                                      // the CTAs plan for themselves
   int32_t npt;                                      // tokens (or nodes) of a tile: kTileRows / group
   uint32_t group_inv;                               // 2^16 / group, rounded up: (r * group_inv) >> 16 = r / group for a tile's rows
   const int32_t* start;                             // caller's row starts
@@ -227,7 +228,6 @@ struct Geo {
   static constexpr int kTakers = kSoftWarps + 1 + kScanWarps + kLoadWarps;      // warps that take every item
   static constexpr int kBars = 4 * NS + 2 + 2 + 4 + 4 + 1 + 2 * kItems;
   static constexpr int kWordsRing = 8;                     // blocks whose token masks are kept
-  static constexpr uint32_t kSmem = 1024 + kData + kBars * 8 + kWordsRing * 16 + 16 + NS * 4 + 8;
   static constexpr uint32_t kTmemO = 256;                  // scores in columns [0, 256), sums behind them
 };
 
@@ -372,104 +372,96 @@ struct Item {
   int slot;                      // partial, or -1: the item has all blocks
 };
 
-// The items of a CTA, one after another, found by one warp.  Up to kFew sequences it reads the caller's starts and
-// lengths itself, four a lane; beyond, a kernel before this one has listed the items (prompt) or added up the units (tree).
-constexpr int kFew = 127;
+// Shared memory behind the tiles of Q and the ring.
+constexpr int kFew = 127;                                  // sequences that a CTA plans for itself, at most
+template <typename G>
+struct Tail {
+  uint64_t bars[G::kBars];
+  uint32_t words[G::kWordsRing][4];      // a block's tokens that have data, a bit each
+  int32_t first_bad;                     // this CTA's first item with V cleared of infinities
+  uint32_t tmem;
+  uint32_t guard_slot[G::NS];            // where guarded V slots lie, in turn
+  Item items[G::kItems];
+  int32_t bounds[kFew + 1];              // few sequences: their row starts, and
+  int32_t units[kFew + 1];               // items (prompt) or units of the requests before (tree)
+  alignas(16) int32_t ids[4][32];        // tree: a loading warp's pages
+};
+template <typename G>
+constexpr uint32_t smem_bytes() { return G::kData + sizeof(Tail<G>); }
+
+// The items of a CTA, one after another, found by one warp.  Up to kFew sequences it looks at the caller's starts and
+// lengths itself; beyond, a kernel before this one has listed the items (prompt) or added up the units (tree).
 template <typename G>
 struct Walk {
+  int32_t* bounds_s;             // few: Tail's
+  int32_t* units_s;
   int w, step, all;              // prompt: turn, CTAs, items times heads
   int level;                     // prompt, few: the level that the walk is at
   int64_t u, u1, per_head;       // tree: units left are [u, u1)
-  int row0[4], row1[4], len[4];  // few: rows (and cached tokens) of sequences 4 lane ..
-  int tiles[4];                  // prompt, few: items of these sequences
-  int64_t before;                // tree, few: units before this lane's requests, and theirs
-  int mine[4];
-  int top_above;                 // prompt, few, at most 32 levels: items above level `lane`
-  bool few;
 
-  __device__ __forceinline__ Walk(const RowsArgs& a) {
+  __device__ __forceinline__ Walk(const RowsArgs& a, int32_t* bounds, int32_t* units) : bounds_s(bounds), units_s(units) {
     const int lane = threadIdx.x & 31, heads = (a.n_kv + G::HT - 1) / G::HT;
-    few = a.n_req <= kFew;
-    if (few) {
-      int32_t x[4], m = INT32_MIN;
+    int total = 0, top = 0;
+    if (a.few) {
       bool bad = false;
+      int32_t carry = INT32_MIN;
+#pragma unroll 1
+      for (int r0 = 0; r0 <= a.n_req; r0 += 32) {          // the running maximum, as plan_bounds
+        const int r = r0 + lane;
+        const int32_t x = a.start[min(r, a.n_req)];
+        int32_t m = max(x, carry);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {                        // the running maximum, as plan_bounds
-        const int i = min(4 * lane + j, a.n_req);
-        x[j] = a.start[i];
-        if (G::kTree) len[j] = i < a.n_req ? a.seq_len[i] : 0;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int32_t y = __shfl_up_sync(0xffffffffu, m, o);
+          if (lane >= o) m = max(m, y);
+        }
+        carry = __shfl_sync(0xffffffffu, m, 31);
+        const int32_t b = min(max(m, 0), a.n_rows);
+        if (r <= a.n_req) {
+          bad |= b != x;
+          bounds_s[r] = b;
+        }
       }
+      __syncwarp();
+#pragma unroll 1
+      for (int r0 = 0; r0 < a.n_req; r0 += 32) {
+        const int r = min(r0 + lane, a.n_req - 1);
+        const bool live = r0 + lane < a.n_req;
+        const int row0 = bounds_s[r], row1 = bounds_s[r + 1];
+        int n = 0;
+        if (G::kTree) {
+          const int length = a.seq_len[r];
+          bad |= tree_request_bad(a, row1 - row0, length);
+          const TreeReq q = tree_request<G::RT>(a, row0, row1, length);
+          if (live) n = q.blocks * q.groups;
+          int incl = n;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        row0[j] = x[j];
-        m = x[j] = max(m, x[j]);
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+          }
+          if (live) units_s[r] = total + incl - n;
+          total += __shfl_sync(0xffffffffu, incl, 31);
+        } else {
+          if (live) n = (row1 - row0 + G::RT * a.npt - 1) / (G::RT * a.npt);
+          if (live) units_s[r] = n;
+          total += __reduce_add_sync(0xffffffffu, n);
+          top = max(top, (int)__reduce_max_sync(0xffffffffu, n));
+        }
       }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t y = __shfl_up_sync(0xffffffffu, m, o);
-        if (lane >= o) m = max(m, y);
-      }
-      const int32_t up = __shfl_up_sync(0xffffffffu, m, 1);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int32_t b = min(max(lane > 0 ? max(x[j], up) : x[j], 0), a.n_rows);
-        bad |= b != row0[j];
-        row0[j] = b;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) row1[j] = j < 3 ? row0[j + 1] : __shfl_down_sync(0xffffffffu, row0[0], 1);
-      if (lane == 31) row1[3] = row0[3];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) bad |= G::kTree && 4 * lane + j < a.n_req && tree_request_bad(a, row1[j] - row0[j], len[j]);
+      __syncwarp();
       if (bad && blockIdx.x == 0) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
     }
     if (G::kTree) {
-      if (few) {
-        int64_t sum = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const TreeReq q = tree_request<G::RT>(a, row0[j], row1[j], len[j]);
-          sum += mine[j] = q.blocks * q.groups;
-        }
-        int64_t incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        before = incl - sum;
-        per_head = __shfl_sync(0xffffffffu, incl, 31);
-      } else {
-        per_head = a.prefix[a.n_req];
-      }
-      const int64_t total = per_head * heads, parts = min((int64_t)a.parts, total), p = blockIdx.x;
-      u = p < parts ? p * total / parts : 0;
-      u1 = p < parts ? (p + 1) * total / parts : 0;
+      per_head = a.few ? total : a.prefix[a.n_req];
+      const int64_t units = per_head * heads, parts = min((int64_t)a.parts, units), p = blockIdx.x;
+      u = p < parts ? p * units / parts : 0;
+      u1 = p < parts ? (p + 1) * units / parts : 0;
     } else {
       w = 0;
       step = gridDim.x;
-      if (few) {
-        int sum = 0, top = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          tiles[j] = (row1[j] - row0[j] + G::RT * a.npt - 1) / (G::RT * a.npt);
-          sum += tiles[j];
-          top = max(top, tiles[j]);
-        }
-        all = __reduce_add_sync(0xffffffffu, sum) * heads;
-        level = __reduce_max_sync(0xffffffffu, top) - 1;
-        top_above = -1;
-        if (level < 32) {
-          top_above = 0;
-#pragma unroll 1
-          for (int k = 0; 4 * k < a.n_req; ++k) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top_above += max(__shfl_sync(0xffffffffu, tiles[j], k) - 1 - lane, 0);
-          }
-        }
-      } else {
-        all = *a.n_items * heads;
-      }
+      level = top - 1;
+      all = (a.few ? total : *a.n_items) * heads;
     }
   }
   // The part that holds unit x of all heads.
@@ -484,31 +476,13 @@ struct Walk {
       if (u >= u1) return false;
       const int head = (int)(u / per_head);
       const int64_t x = u - head * per_head;
-      int64_t y = 0;                                       // unit of the request
-      TreeReq q{};
-      if (few) {
-        const int k = 31 - __clz(__ballot_sync(0xffffffffu, before <= x));      // the lane; requests without units come after
-        y = x - __shfl_sync(0xffffffffu, before, k);
-        int r0 = 0, r1 = 0, length = 0;
-        bool found = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = __shfl_sync(0xffffffffu, mine[j], k), x0 = __shfl_sync(0xffffffffu, row0[j], k);
-          const int x1 = __shfl_sync(0xffffffffu, row1[j], k), xl = __shfl_sync(0xffffffffu, len[j], k);
-          if (found) continue;
-          found = y < n;
-          if (found) {
-            r0 = x0;
-            r1 = x1;
-            length = xl;
-            it.req = 4 * k + j;
-          } else {
-            y -= n;
-          }
-        }
-        q = tree_request<G::RT>(a, r0, r1, length);
+      int lo = 0;                                          // the request: prefix[lo] <= x < prefix[lo + 1]
+      if (a.few) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < a.n_req; r0 += 32) lo += __popc(__ballot_sync(0xffffffffu, r0 + lane < a.n_req && units_s[min(r0 + lane, kFew)] <= x));
+        --lo;
       } else {
-        int lo = 0, hi = a.n_req;                          // prefix[lo] <= x < prefix[hi]: 32 places a turn
+        int hi = a.n_req;                                  // 32 places a turn
 #pragma unroll 1
         while (hi - lo > 1) {
           const int stride = (hi - lo + 31) / 32, at = lo + lane * stride;
@@ -516,10 +490,11 @@ struct Walk {
           lo += (31 - __clz(in)) * stride;
           hi = min(hi, lo + stride);
         }
-        q = tree_request<G::RT>(a, a.bounds[lo], a.bounds[lo + 1], a.seq_len[lo]);
-        y = x - a.prefix[lo];
-        it.req = lo;
       }
+      const int32_t* bounds = a.few ? bounds_s : a.bounds;
+      const TreeReq q = tree_request<G::RT>(a, bounds[lo], bounds[lo + 1], a.seq_len[lo]);
+      const int64_t y = x - (a.few ? units_s[lo] : a.prefix[lo]);
+      it.req = lo;
       const int group = (int)y / q.blocks;                 // a request has fewer than 2^31 units
       it.head = head * G::HT;
       it.b0 = (int)y - group * q.blocks;
@@ -544,44 +519,38 @@ struct Walk {
     const int heads = (a.n_kv + G::HT - 1) / G::HT, place = x / heads;
     int first = 0, end = 0, tile = 0;
     it.head = (x - place * heads) * G::HT;
-    if (few) {
+    if (a.few) {
       // The longest first: the lowest level with `place` or fewer items above it; the k-th sequence that has it.
       const auto above = [&](int L) {
         int n = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) n += max(tiles[j] - 1 - L, 0);
+#pragma unroll 1
+        for (int r = lane; r < a.n_req; r += 32) n += max(units_s[r] - 1 - L, 0);
         return __reduce_add_sync(0xffffffffu, n);
       };
-      int k;
-      if (top_above >= 0) {
-        level = __ffs(__ballot_sync(0xffffffffu, top_above <= place)) - 1;
-        k = place - __shfl_sync(0xffffffffu, top_above, level);
-      } else {
-        int lo = 0;
+      int lo = 0;
 #pragma unroll 1
-        while (lo < level) {
-          const int mid = (lo + level) / 2;
-          if (above(mid) <= place) level = mid;
-          else lo = mid + 1;
-        }
-        k = place - above(level);
+      while (lo < level) {
+        const int mid = (lo + level) / 2;
+        if (above(mid) <= place) level = mid;
+        else lo = mid + 1;
       }
-      bool found = false;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        unsigned has = __ballot_sync(0xffffffffu, tiles[j] > level);
-        const int c = __popc(has);
-        if (!found && k < c) {
-          found = true;
+      int k = place - above(level), s = 0;
 #pragma unroll 1
-          for (int i = 0; i < k; ++i) has &= has - 1;
-          first = __shfl_sync(0xffffffffu, row0[j], __ffs(has) - 1);
-          end = __shfl_sync(0xffffffffu, row1[j], __ffs(has) - 1);
+      for (int r0 = 0; r0 < a.n_req; r0 += 32) {
+        unsigned has = __ballot_sync(0xffffffffu, r0 + lane < a.n_req && units_s[min(r0 + lane, kFew)] > level);
+        const int c = __popc(has);
+        if (k < c) {
+#pragma unroll 1
+          for (; k > 0; --k) has &= has - 1;
+          s = r0 + __ffs(has) - 1;
+          break;
         }
         k -= c;
       }
+      first = bounds_s[s];
+      end = bounds_s[s + 1];
       tile = level;
-      it.req = 0;
+      it.req = s;
     } else {
       const int2 e = a.items[place];
       first = a.bounds[e.x];
@@ -647,21 +616,22 @@ __global__ void __launch_bounds__(G::kThreads, 1)
 rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ RowsArgs a) {
   constexpr int D = G::D, NT = G::NT, NB = G::NB, PD = G::PD, NS = G::NS;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint32_t tmem_s;
-  __shared__ Item items_s[G::kItems];
-  __shared__ __align__(16) int32_t ids_s[G::kTree ? G::kLoadWarps * 64 : 4];
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t s_q = base, s_ring = base + NT * G::kQTile, s_bar = base + G::kData;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = smem_u32(smem_raw);
+  if ((base & 1023u) != 0) {                               // the tiles' layout counts on it
+    if (threadIdx.x == 0) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
+    return;
+  }
+  Tail<G>& tail = *reinterpret_cast<Tail<G>*>(smem_raw + G::kData);
+  const uint32_t s_q = base, s_ring = base + NT * G::kQTile, s_bar = smem_u32(tail.bars);
   const uint32_t bar_full = s_bar, bar_empty = bar_full + 8 * NS, bar_clean = bar_empty + 8 * NS;
   const uint32_t bar_landed = bar_clean + 8 * NS;
   const uint32_t bar_qfull = bar_landed + 8 * NS, bar_qempty = bar_qfull + 8, bar_scores = bar_qempty + 8;
   const uint32_t bar_weights = bar_scores + 16, bar_sums = bar_weights + 32, bar_drained = bar_sums + 16;
   const uint32_t bar_product = bar_drained + 16, bar_item = bar_product + 8, bar_taken = bar_item + 8 * G::kItems;
-  uint8_t* tail = smem_raw + (base - smem_u32(smem_raw)) + G::kData + G::kBars * 8 + (G::kBars & 1) * 8;
-  volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(tail);        // [kWordsRing][4]: a block's tokens that have data
-  volatile int* first_bad = reinterpret_cast<volatile int*>(words + G::kWordsRing * 4);   // this CTA's first item with V cleared
-  volatile uint32_t* guard_slot = words + G::kWordsRing * 4 + 4;                // [NS]: where guarded V slots lie, in turn
+  volatile uint32_t* words = &tail.words[0][0];
+  volatile int* first_bad = &tail.first_bad;
+  volatile uint32_t* guard_slot = tail.guard_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
 #pragma unroll 1
@@ -690,13 +660,13 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   }
   pdl_wait_then_release();                                 // TMEM is taken after it: an earlier kernel may still need its own
   if (warp == G::kMmaWarp) {
-    tmem_alloc(smem_u32(&tmem_s), 512);
+    tmem_alloc(smem_u32(&tail.tmem), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_s;
+  const uint32_t tmem = tail.tmem;
   Item it;
   bool ok = true;
   // The n-th item, as the planning warp found it; false behind the last one.
@@ -706,7 +676,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       ok = false;
       return false;
     }
-    it = items_s[at];
+    it = tail.items[at];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_taken + 8 * at);
     return it.req >= 0;
@@ -1044,7 +1014,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
   } else if (warp == G::kPlanWarp) {
     // ---- the items; of trees Q ----
-    Walk<G> walk(a);
+    Walk<G> walk(a, tail.bounds, tail.units);
     if (G::kTree && lane == 0) a.ws_start[blockIdx.x] = make_int4(-1, 0, 0, 0);
     for (int n_item = 0; ok; ++n_item) {
       const bool more = walk.next(a, it);
@@ -1053,7 +1023,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const int at = n_item % G::kItems;
         ok = wait_for(bar_taken + 8 * at, ((uint32_t)(n_item / G::kItems) & 1u) ^ 1u);
         if (ok) {
-          items_s[at] = it;
+          tail.items[at] = it;
           mbar_arrive(bar_item + 8 * at);
         }
         if (G::kTree && more) {
@@ -1139,7 +1109,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   } else if (G::kTree && warp >= G::kLoadWarp) {
     // ---- tree: rows of K and V from their pages, gathered four at a time by TMA, each warp 32 of a block's tokens ----
     const int w = warp - G::kLoadWarp;
-    int32_t* ids = ids_s + w * 64;                         // of a block: 32 K pages, 32 V pages; -1 (zeros): no data
+    int32_t* ids = tail.ids[w];                            // K or V pages of a block; -1 (zeros): no data
     Ring<NS> ring{0, 1};                                   // phase: of the slot's release
     uint32_t guarded = 0;
     int blocks_done = 0, issued = 0;
@@ -1397,17 +1367,17 @@ template <typename G>
 int launch_rows(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                 int ctas, const char* what, cudaStream_t st) {
   static DeviceFlags flags;
-  const int rc = ensure_smem_attr(flags, &rows_kernel<G>, (int)G::kSmem, what);
+  const int rc = ensure_smem_attr(flags, &rows_kernel<G>, (int)smem_bytes<G>(), what);
   if (rc != LORA_OK) return rc;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
-  const cudaError_t e = launch_pdl(!p->prof_on, rows_kernel<G>, dim3(ctas), dim3(G::kThreads), G::kSmem, st, q, k, v, a);
+  const cudaError_t e = launch_pdl(!p->prof_on, rows_kernel<G>, dim3(ctas), dim3(G::kThreads), smem_bytes<G>(), st, q, k, v, a);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, what);
 }
 
 int launch_prompt(const lora_pool* p, const RowsArgs& a, const PromptLayout& L, const CUtensorMap& q, const CUtensorMap& k,
                   const CUtensorMap& v, cudaStream_t st) {
   const char* what = "lora_attention_prompt launch";
-  if (a.n_req > kFew) {
+  if (!a.few) {
     ProfScope prof(p, LORA_KIND_ATTENTION, st);
     const cudaError_t e = launch_pdl(!p->prof_on, prompt_plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)L.levels * 4, st, a,
                                      L.per_item, L.levels);
@@ -1425,7 +1395,7 @@ int launch_prompt(const lora_pool* p, const RowsArgs& a, const PromptLayout& L, 
 template <typename G>
 int launch_tree(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, const CUtensorMap& pages, cudaStream_t st) {
   const char* what = "lora_attention_tree launch";
-  if (a.n_req > kFew) {
+  if (!a.few) {
     ProfScope prof(p, LORA_KIND_ATTENTION, st);
     const cudaError_t e = launch_pdl(!p->prof_on, tree_plan_kernel<G::RT>, dim3(1), dim3(kPlanThreads), 0, st, a);
     if (e != cudaSuccess) return lora_cuda_fail(e, what);
@@ -1493,6 +1463,7 @@ extern "C" int lora_attention_prompt(lora_pool* p, int32_t n_seq, const int32_t*
   a.bounds = reinterpret_cast<int32_t*>(ws + L.bounds);
   a.scale_log2 = 1.4426950408889634f / std::sqrt((float)D);
   a.err = p->d_err;
+  a.few = n_seq <= kFew;
   a.v = static_cast<const uint16_t*>(v);
   a.v_stride = v_stride;
   a.n_items = reinterpret_cast<int32_t*>(ws + L.n_items);
@@ -1567,6 +1538,8 @@ extern "C" int lora_attention_tree(lora_pool* p, int32_t n_req, const int32_t* t
   a.layers = layers;
   a.layer = layer;
   a.mask = mask;
+  // units of all requests in 32 bits: at most 8 groups of tiles each
+  a.few = n_req <= kFew && (int64_t)n_req * ((max_len + kBlock - 1) / kBlock + 1) * 8 <= INT32_MAX;
   a.prefix = reinterpret_cast<int64_t*>(ws + L.prefix);
   a.ws_start = reinterpret_cast<int4*>(ws + L.start);
   a.ws_ml = reinterpret_cast<float2*>(ws + L.ml);
