@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstring>
 #include <string>
 
 #include "tc_ptx.h"
@@ -125,24 +126,28 @@ kv_write_packed_kernel(uint16_t* pool, int64_t num_pages, int32_t H, int32_t n_r
 // A block of rows per CTA, and with a new table a block of its positions per further CTA.  Every CTA sums
 // the counts itself (a thread adds up n_req / 256 requests, one scan over the threads), so the call is one
 // launch; a row's request is then found by bisection over the threads and a walk over that thread's
-// requests.  Pages are moved 8 bytes (one layer's K and V) a thread, neighbours together.
+// requests.  Pages are moved a layer's K and V (8 bytes) a thread, or two layers' (16) where the layers are even and
+// the arrays aligned.  64 prompts of 500 to 2,048 tokens, 40 layers, into a new table: 71 MB in 16.4 us, 4.3 TB/s (0.64 of
+// the copy rate; entries are moved in 1.7 rounds of CTAs that each begin with the counts).
 constexpr int kAppendThreads = 256;
-constexpr int kAppendEntries = 2048;                       // table entries a CTA writes, about
-constexpr int kAppendMaxRows = 512;                        // rows a CTA takes, at most
+constexpr int kAppendBatch = 8;                            // entries a thread has in flight
+constexpr int kAppendEntries = 2 * kAppendBatch * kAppendThreads;   // entries that a CTA writes, about
+constexpr int kAppendMaxRows = 1024;                       // rows a CTA takes, at most
 
 struct AppendArgs {
   int32_t n_req;
   const int32_t* count;
   const int32_t* old_len;
-  const int2* pages;
+  const void* pages;
   int32_t row_cap;
-  int2* table;
-  int32_t max_len, layers;
+  void* table;
+  int32_t max_len, layers;       // layers: entries of a token
   int32_t* new_len;
   int32_t* row_start;
   int32_t* row_req;
   int32_t* row_pos;
   int32_t rows_per_cta, row_ctas;
+  uint64_t layers_inv;           // 2^40 / layers, rounded up: (e * layers_inv) >> 40 = e / layers for a CTA's entries (one row: 0)
   int32_t* err;
 };
 
@@ -150,6 +155,7 @@ __device__ __forceinline__ int32_t append_old(const AppendArgs& a, int r) {
   return a.old_len ? min(max(a.old_len[r], 0), a.max_len) : 0;
 }
 
+template <typename T>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
   __shared__ int64_t before[kAppendThreads];               // rows of the requests of the threads before
   __shared__ int64_t warp_sum[kAppendThreads / 32];
@@ -219,10 +225,20 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
     }
     __syncthreads();
     const int entries = n * a.layers;
-    for (int e = tid; e < entries; e += kAppendThreads) {
-      const int i = e / a.layers;
-      if (req_s[i] >= 0)
-        a.table[((int64_t)req_s[i] * a.max_len + pos_s[i]) * a.layers + e - i * a.layers] = a.pages[t0 * a.layers + e];
+    const T* from = static_cast<const T*>(a.pages) + t0 * a.layers;
+    T* table = static_cast<T*>(a.table);
+    for (int e0 = tid; e0 < entries; e0 += kAppendBatch * kAppendThreads) {
+      T v[kAppendBatch];
+#pragma unroll
+      for (int b = 0; b < kAppendBatch; ++b)
+        if (e0 + b * kAppendThreads < entries) v[b] = from[e0 + b * kAppendThreads];
+#pragma unroll
+      for (int b = 0; b < kAppendBatch; ++b) {
+        const int e = e0 + b * kAppendThreads;
+        if (e >= entries) break;
+        const int i = (int)(e * a.layers_inv >> 40);
+        if (req_s[i] >= 0) table[((int64_t)req_s[i] * a.max_len + pos_s[i]) * a.layers + e - i * a.layers] = v[b];
+      }
     }
     return;
   }
@@ -237,9 +253,12 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
     req_s[i] = (j0 + i) - (int64_t)r * a.max_len >= held;
   }
   __syncthreads();
-  const int64_t entries = (int64_t)n * a.layers;
-  for (int64_t e = tid; e < entries; e += kAppendThreads)
-    if (req_s[(int)(e / a.layers)]) a.table[j0 * a.layers + e] = make_int2(-1, -1);
+  const int entries = n * a.layers;
+  T* to = static_cast<T*>(a.table) + j0 * a.layers, none;
+  memset(&none, 0xff, sizeof(T));
+#pragma unroll 4
+  for (int e = tid; e < entries; e += kAppendThreads)
+    if (req_s[(int)(e * a.layers_inv >> 40)]) to[e] = none;
 }
 
 // ---- eviction ------------------------------------------------------------------------------------
@@ -963,9 +982,12 @@ extern "C" int lora_kv_append(lora_pool* p, int32_t n_req, const int32_t* count,
   a.n_req = n_req;
   a.count = count;
   a.old_len = old_len;
-  a.pages = reinterpret_cast<const int2*>(pages);
+  // Two layers at a time (64 prompts of 500 to 2,048 tokens, 40 layers: 16.4 us, one at a time 19.2).
+  const bool wide = layers % 2 == 0 && ((reinterpret_cast<uintptr_t>(table_dev) | reinterpret_cast<uintptr_t>(pages)) & 15) == 0;
+  if (wide) layers /= 2;
+  a.pages = pages;
   a.row_cap = row_cap;
-  a.table = reinterpret_cast<int2*>(table_dev);
+  a.table = table_dev;
   a.max_len = max_len;
   a.layers = layers;
   a.new_len = new_len;
@@ -973,6 +995,7 @@ extern "C" int lora_kv_append(lora_pool* p, int32_t n_req, const int32_t* count,
   a.row_req = row_req;
   a.row_pos = row_pos;
   a.rows_per_cta = std::min(std::max(kAppendEntries / layers, 1), kAppendMaxRows);
+  a.layers_inv = a.rows_per_cta > 1 ? (((uint64_t)1 << 40) + layers - 1) / layers : 0;
   const int64_t rest = old_len ? 0 : ((int64_t)n_req * max_len + a.rows_per_cta - 1) / a.rows_per_cta;
   a.row_ctas = (int32_t)std::max(((int64_t)row_cap + a.rows_per_cta - 1) / a.rows_per_cta, (int64_t)1);
   if (a.row_ctas + rest > INT32_MAX) return lora_fail(LORA_EINVAL, "lora_kv_append: the table is too large for one call");
@@ -980,7 +1003,7 @@ extern "C" int lora_kv_append(lora_pool* p, int32_t n_req, const int32_t* count,
   a.err = p->d_err;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope prof(p, LORA_KIND_KV, st);
-  const cudaError_t e = launch_pdl(!p->prof_on, kv_append_kernel, dim3((unsigned)(a.row_ctas + rest)), dim3(kAppendThreads), 0,
-                                   st, a);
+  const cudaError_t e = launch_pdl(!p->prof_on, wide ? kv_append_kernel<int4> : kv_append_kernel<int2>,
+                                   dim3((unsigned)(a.row_ctas + rest)), dim3(kAppendThreads), 0, st, a);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, "lora_kv_append launch");
 }

@@ -785,6 +785,26 @@ def test_append_reports_what_does_not_fit(L, small_pool, count, old, max_len, ro
         assert np.array_equal(g, w)
 
 
+def test_append_of_even_layers_in_unaligned_arrays(L, small_pool):
+    """An even number of layers in arrays that start 8 bytes behind a 16-byte boundary."""
+    import torch
+    rng = np.random.default_rng(7)
+    count, old, layers, max_len = [3, 0, 40, 7], [1, 2, 0, 5], 4, 50
+    rows = sum(count) + 2
+    pages = rng.integers(0, 99, (rows, layers, 2)).astype(np.int32)
+    table = rng.integers(0, 99, (4, max_len, layers, 2)).astype(np.int32)
+    want = O.kv_append(count, old, pages, table, rows)
+    shifted = lambda x: torch.cat([torch.zeros(2, dtype=torch.int32), torch.from_numpy(x).view(-1)]).cuda()[2:]  # noqa: E731
+    t, p = shifted(table), shifted(pages)
+    assert t.data_ptr() % 16 == 8
+    outs = [torch.full((m,), -99, dtype=torch.int32, device="cuda") for m in (4, 5, rows, rows)]
+    as_dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    L.lora_kv_append(small_pool, 4, as_dev(count), as_dev(old), p, rows, t, max_len, layers, *outs)
+    L.lora_status(small_pool)
+    for g, w in zip((t.view(table.shape), *outs), want):
+        assert np.array_equal(g.cpu().numpy(), w)
+
+
 def test_append_many_requests(L, small_pool):
     """65,535 requests, most of them with nothing new."""
     rng = np.random.default_rng(3)
