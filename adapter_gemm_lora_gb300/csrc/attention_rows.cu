@@ -729,33 +729,42 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         ++use[x];
         tc_fence_after();
+        // Blocks of which a row does not see every token: what it does not see becomes -infinity, in place, so that the
+        // code of the other blocks serves them too.
+        const int j0 = (it.b0 + i) * kBlock;
+        bool some = !G::kTree && it.b0 + i >= pos0 / kBlock;
+        if (G::kTree) {
+          bool all = j0 + kBlock <= it.base;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) all = all && words[((blocks_done + i) % G::kWordsRing) * 4 + c] == 0xffffffffu;
+          some = !all;
+        }
+        if (some) {                                        // the same for all lanes
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v, u[32];
+            if (G::kTree) {
+              const int d = j0 + 32 * c - it.base;
+              v = words[((blocks_done + i) % G::kWordsRing) * 4 + c];
+              if (d + 32 > 0) v &= d >= 64 ? 0u : d >= 0 ? (uint32_t)(mask >> d) : ((uint32_t)mask << -d) | ((1u << -d) - 1u);
+            } else {
+              const int n = pos - j0 - 32 * c;             // the last token of these that the row sees
+              v = n < 0 ? 0u : n >= 31 ? 0xffffffffu : (2u << n) - 1u;
+            }
+            if (!__any_sync(0xffffffffu, v != 0xffffffffu)) continue;
+            tmem_ld_32x32b_x32(scores + 32 * c, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((v >> e) & 1)) u[e] = 0xff800000u;
+            tmem_st_32x32b_x32(scores + 32 * c, u);
+          }
+          tmem_st_wait();
+        }
         uint32_t s[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(scores + 32 * c, s[c]);
         tmem_ld_wait();
-        const int j0 = (it.b0 + i) * kBlock;
-        if (G::kTree) {
-          uint32_t vis[4];
-          bool all = true;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int j = j0 + 32 * c, d = j - it.base;
-            uint32_t v = words[((blocks_done + i) % G::kWordsRing) * 4 + c];
-            if (d + 32 > 0) v &= d >= 64 ? 0u : d >= 0 ? (uint32_t)(mask >> d) : ((uint32_t)mask << -d) | ((1u << -d) - 1u);
-            vis[c] = v;
-            all = all && v == 0xffffffffu;
-          }
-          if (__any_sync(0xffffffffu, !all)) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (!((vis[c / 32] >> (c % 32)) & 1)) s[c / 32][c % 32] = 0xff800000u;
-          }
-        } else if (it.b0 + i >= pos0 / kBlock) {
-          const int last = pos - j0;
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > last) s[c / 32][c % 32] = 0xff800000u;
-        }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 128; c += 2) top[(c / 2) & 3] = max3(top[(c / 2) & 3], s[c / 32][c % 32], s[c / 32][c % 32 + 1]);
