@@ -370,6 +370,7 @@ struct Item {
   // tree
   int len, base;                 // cached tokens, the first node's position
   int slot;                      // partial, or -1: the item has all blocks
+  int nb0, nb1;                  // blocks of the tiles, 0: no rows
 };
 
 // Shared memory behind the tiles of Q and the ring.
@@ -667,7 +668,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tail.tmem;
-  Item it;
+  Item it = {};
   bool ok = true;
   // The n-th item, as the planning warp found it; false behind the last one.
   const auto take = [&](int n) {
@@ -684,7 +685,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   // Q of the item `it`, the n-th, by one thread.
   const auto load_q = [&](int n) {
     if (!wait_for(bar_qempty, (n & 1) ^ 1)) return false;
-    const bool two = NT == 2 && Walk<G>::blocks(a, it, 1) > 0;
+    const bool two = it.nb1 > 0;
     const uint32_t bytes = (uint32_t)(a.npt * a.group * 128 * (D / 64));
     mbar_arrive_expect_tx(bar_qfull, two ? 2 * bytes : bytes);
 #pragma unroll 1
@@ -708,7 +709,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     uint32_t use[2] = {0, 0}, items_t = 0, products = 0, blocks_done = 0;
     for (int n_item = 0; ok && take(n_item); ++n_item) {
-      const int nb = Walk<G>::blocks(a, it, t), nb_all = it.b1 - it.b0;
+      const int nb = t == 0 ? it.nb0 : it.nb1, nb_all = it.b1 - it.b0;
       if (nb == 0) {
         blocks_done += nb_all;
         continue;
@@ -921,11 +922,21 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     constexpr uint32_t kLdK = 1u << 16, kLdV = (G::kPanel >> 4) << 16;   // leading-dimension offsets
     const uint32_t kHiK = (uint32_t)(sw128_kmajor_desc(0) >> 32), kHiV = (uint32_t)(sw128_mnmajor_desc(0, G::kPanel, 1024) >> 32);
     const auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
-    const auto wait_lane0 = [&](uint32_t bar, uint32_t parity) { return lane != 0 || wait_for(bar, parity); };
-    for (int n_item = 0; ok && take(n_item); ++n_item) {
-      const int nb0 = Walk<G>::blocks(a, it, 0), nb1 = NT == 2 ? Walk<G>::blocks(a, it, 1) : 0;
-      const int n = it.b1 - it.b0;
-      ok = __all_sync(0xffffffffu, ok && wait_lane0(bar_qfull, n_item & 1));
+    if (elect_one()) {
+      // What is needed of an item is read while the one before it still runs.
+      struct Mine {
+        int n, guard, nb0, nb1;                            // blocks, the first guarded one; n < 0: behind the last item
+      };
+      const auto read = [&](int k, Mine& x) {
+        const int at = k % G::kItems;
+        if (!wait_for(bar_item + 8 * at, (uint32_t)(k / G::kItems) & 1u)) return false;
+        const Item& y = tail.items[at];
+        x = Mine{y.req < 0 ? -1 : y.b1 - y.b0, y.guard - y.b0, y.nb0, y.nb1};
+        mbar_arrive(bar_taken + 8 * at);
+        return true;
+      };
+      Mine cur, nxt;
+      ok = read(0, cur);
       // Scores buffer x = Q_t K^T, K in the ring from r on.
       const auto issue_scores = [&](int t, int x, Ring<NS> r) {
 #pragma unroll
@@ -967,19 +978,22 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
         for (int p = 0; p < PD; ++p, r.next()) mma_commit(bar_empty + 8 * r.at);
       };
-      if (ok && elect_one()) {
+      constexpr bool kOwn = G::kPair || NB == 2;           // no two tiles share a block
+      for (int n_item = 0; ok && cur.n >= 0; ++n_item, cur = nxt) {
+        const int n = cur.n;
+        ok = wait_for(bar_qfull, n_item & 1);
         tc_fence_after();
-        constexpr bool kOwn = G::kPair || NB == 2;         // no two tiles share a block
         // Scores are NB blocks ahead of the products.
 #pragma unroll 1
         for (int i = -NB; i < n && ok; ++i) {
-          const bool guard = it.b0 + i >= it.guard;
+          const bool guard = i >= cur.guard;
+          if (i + 1 == n) ok = read(n_item + 1, nxt);
           Ring<NS> next = ring;                            // where the scores' K lies
           if (i >= 0) next.template skip<PD>();
 #pragma unroll 1
           for (int t = 0; t < NT && ok; ++t) {
             const int x = NB == 1 ? t : (i & 1);
-            const int nb = t == 0 ? nb0 : nb1;
+            const int nb = t == 0 ? cur.nb0 : cur.nb1;
             if (i >= nb) continue;
             if (i >= 0) {
               if (i == 0) {
@@ -1019,8 +1033,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           if (i + NB + 1 == n) mma_commit(bar_qempty);
         }
       }
-      ok = __all_sync(0xffffffffu, ok);
     }
+    ok = __all_sync(0xffffffffu, ok);
   } else if (warp == G::kPlanWarp) {
     // ---- the items; of trees Q ----
     Walk<G> walk(a, tail.bounds, tail.units);
@@ -1028,6 +1042,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     for (int n_item = 0; ok; ++n_item) {
       const bool more = walk.next(a, it);
       if (!more) it.req = -1;
+      it.nb0 = Walk<G>::blocks(a, it, 0);
+      it.nb1 = NT == 2 ? Walk<G>::blocks(a, it, 1) : 0;
       if (elect_one()) {
         const int at = n_item % G::kItems;
         ok = wait_for(bar_taken + 8 * at, ((uint32_t)(n_item / G::kItems) & 1u) ^ 1u);
@@ -1094,7 +1110,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int w = warp - G::kScanWarp;
     uint32_t guarded = 0;
     for (int n_item = 0; ok && take(n_item); ++n_item) {
-      const int n = it.b1 - it.b0, tiles = G::kPair && Walk<G>::blocks(a, it, 1) > 0 ? 2 : 1;
+      const int n = it.b1 - it.b0, tiles = G::kPair && it.nb1 > 0 ? 2 : 1;
 #pragma unroll 1
       for (int left = (n - max(it.guard - it.b0, 0)) * PD * tiles; left > 0 && ok; --left) {
           ok = __all_sync(0xffffffffu, wait_for(bar_landed + 8 * (guarded % NS), (guarded / NS) & 1));
@@ -1167,7 +1183,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
       };
       int2 e0 = checked(entry(0), 0), e1 = entry(1);
-      const int tiles = G::kPair && Walk<G>::blocks(a, it, 1) > 0 ? 2 : 1;
+      const int tiles = G::kPair && it.nb1 > 0 ? 2 : 1;
 #pragma unroll 1
       for (int s = 0; s < 2 * n && ok; ++s) {
         int i;
