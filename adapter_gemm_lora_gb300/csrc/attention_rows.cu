@@ -671,16 +671,17 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   Item it = {};
   bool ok = true;
   // The n-th item, as the planning warp found it; false behind the last one.
-  const auto take = [&](int n) {
+  const auto read_item = [&](int n, Item& x) {
     const int at = n % G::kItems;
-    if (!__all_sync(0xffffffffu, wait_for(bar_item + 8 * at, (uint32_t)(n / G::kItems) & 1u))) {
-      ok = false;
-      return false;
-    }
-    it = tail.items[at];
+    if (!__all_sync(0xffffffffu, wait_for(bar_item + 8 * at, (uint32_t)(n / G::kItems) & 1u))) return false;
+    x = tail.items[at];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_taken + 8 * at);
-    return it.req >= 0;
+    return true;
+  };
+  const auto take = [&](int n) {
+    ok = read_item(n, it);
+    return ok && it.req >= 0;
   };
   // Q of the item `it`, the n-th, by one thread.
   const auto load_q = [&](int n) {
@@ -708,10 +709,13 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int tok = (int)(row * a.group_inv >> 16), g = row - tok * a.group;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     uint32_t use[2] = {0, 0}, items_t = 0, products = 0, blocks_done = 0;
-    for (int n_item = 0; ok && take(n_item); ++n_item) {
+    Item nxt;
+    take(0);
+    for (int n_item = 0; ok && it.req >= 0; ++n_item, it = nxt) {
       const int nb = t == 0 ? it.nb0 : it.nb1, nb_all = it.b1 - it.b0;
       if (nb == 0) {
         blocks_done += nb_all;
+        ok = read_item(n_item + 1, nxt);
         continue;
       }
       const int left = Walk<G>::count(a, it, t), row0 = it.row0 + Walk<G>::offset(a, t);
@@ -825,12 +829,6 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       products += nb;
       blocks_done += nb_all;
       // ---- the tile's outputs ----
-      if (!__all_sync(0xffffffffu, wait_for(bar_sums + 8 * t, items_t & 1))) {
-        ok = false;
-        break;
-      }
-      ++items_t;
-      tc_fence_after();
       const bool part = it.slot >= 0;
       const int64_t orow = row0 + tok;
       const int kv = Walk<G>::head(it, t), head = kv * a.group + g;
@@ -846,6 +844,12 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         dst[e] = tok_r < left ? a.out + (int64_t)(row0 + tok_r) * a.out_stride + (int64_t)(kv * a.group + r - tok_r * a.group) * D + 8 * (lane & 3)
                               : nullptr;
       }
+      if (!read_item(n_item + 1, nxt) || !__all_sync(0xffffffffu, wait_for(bar_sums + 8 * t, items_t & 1))) {
+        ok = false;
+        break;
+      }
+      ++items_t;
+      tc_fence_after();
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t o[32];
