@@ -325,11 +325,14 @@ __device__ __forceinline__ void transpose_4x4(uint4 (&v)[4], int lane) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (e & s) continue;
-      const uint4 give = up ? v[e] : v[e | s];
-      const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, s), __shfl_xor_sync(0xffffffffu, give.y, s),
-                                   __shfl_xor_sync(0xffffffffu, give.z, s), __shfl_xor_sync(0xffffffffu, give.w, s));
-      if (up) v[e] = got;
-      else v[e | s] = got;
+      const uint4 x = v[e], y = v[e | s];
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, up ? x.x : y.x, s);
+      got.y = __shfl_xor_sync(0xffffffffu, up ? x.y : y.y, s);
+      got.z = __shfl_xor_sync(0xffffffffu, up ? x.z : y.z, s);
+      got.w = __shfl_xor_sync(0xffffffffu, up ? x.w : y.w, s);
+      v[e] = make_uint4(up ? got.x : x.x, up ? got.y : x.y, up ? got.z : x.z, up ? got.w : x.w);
+      v[e | s] = make_uint4(up ? y.x : got.x, up ? y.y : got.y, up ? y.z : got.z, up ? y.w : got.w);
     }
   }
 }
@@ -829,7 +832,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       products += nb;
       blocks_done += nb_all;
       // ---- the tile's outputs ----
-      const bool part = it.slot >= 0;
+      const bool part = G::kTree && it.slot >= 0;
       const int64_t orow = row0 + tok;
       const int kv = Walk<G>::head(it, t), head = kv * a.group + g;
       const int64_t prow = (int64_t)it.slot * a.slot_rows + t * (a.slot_rows / NT) + row;
