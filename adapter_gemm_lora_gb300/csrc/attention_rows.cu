@@ -387,6 +387,8 @@ struct Tail {
   uint64_t bars[G::kBars];
   uint32_t words[G::kWordsRing][4];      // a block's tokens that have data, a bit each
   int32_t first_bad;                     // this CTA's first item with V cleared of infinities
+  uint32_t bad[8][G::kScanWarps][2][4];  // which tokens' of its guarded blocks, an item's in turn: 64 nodes, 128 tokens,
+                                         // or 256 from a multiple of 256 on lie in two blocks
   uint32_t tmem;
   uint32_t guard_slot[G::NS];            // where guarded V slots lie, in turn
   Item items[G::kItems];
@@ -891,23 +893,43 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         // Infinities and NaN of V in the blocks that not every row sees whole were left out of the products: the rows
         // that see them get them here.
         __syncwarp();
-        const int j1 = G::kTree ? min(it.b1 * kBlock, it.len) : pos + 1;
+        const int first = max(it.b0, it.guard);
+        const volatile uint32_t* bad_words = &tail.bad[n_item % 8][0][0][0];
+        const auto seen = [&](int c) {                     // of 32 tokens those with any that the row sees
+          uint32_t v = bad_words[c];
+          if (G::kScanWarps == 2) v |= bad_words[8 + c];
+          const int j0 = first * kBlock + 32 * c;
+          if (G::kTree) {
+            const int d = j0 - it.base;
+            if (d + 32 > 0) v &= d >= 64 ? 0u : d >= 0 ? (uint32_t)(mask >> d) : ((uint32_t)mask << -d) | ((1u << -d) - 1u);
+          } else {
+            const int n = pos - j0;
+            v &= n < 0 ? 0u : n >= 31 ? 0xffffffffu : (2u << n) - 1u;
+          }
+          return v;
+        };
+        uint32_t any = 0;
 #pragma unroll 1
-        for (int d = 0; d < D && live && l != 0.f; ++d) {
+        for (int c = 0; c < 8; ++c) any |= seen(c);
+#pragma unroll 1
+        for (int d = 0; d < D && live && any && l != 0.f; ++d) {
           float c = 0.f;
 #pragma unroll 1
-          for (int j = max(it.b0, it.guard) * kBlock; j < j1; ++j) {
-            const uint16_t* v;
-            if (G::kTree) {
-              if (j >= it.base && !((mask >> (j - it.base)) & 1)) continue;
-              const int2 pg = a.table[((int64_t)it.req * a.max_len + j) * a.layers + a.layer];
-              if (pg.x < 0 || pg.x >= a.num_pages || pg.y < 0 || pg.y >= a.num_pages) continue;
-              v = a.pool + (int64_t)pg.y * a.H + kv * D + d;
-            } else {
-              v = a.v + (row0 - pos0 + j) * a.v_stride + kv * D + d;
+          for (int at = 0; at < 8; ++at) {
+#pragma unroll 1
+            for (uint32_t v = seen(at); v; v &= v - 1) {
+              const int j = first * kBlock + 32 * at + __ffs(v) - 1;
+              const uint16_t* from;
+              if (G::kTree) {
+                const int2 pg = a.table[((int64_t)it.req * a.max_len + j) * a.layers + a.layer];
+                if (pg.x < 0 || pg.x >= a.num_pages || pg.y < 0 || pg.y >= a.num_pages) continue;
+                from = a.pool + (int64_t)pg.y * a.H + kv * D + d;
+              } else {
+                from = a.v + (row0 - pos0 + j) * a.v_stride + kv * D + d;
+              }
+              const uint32_t x = *from;
+              if ((x & 0x7F80u) == 0x7F80u) c += __uint_as_float(x << 16);
             }
-            const uint32_t x = *v;
-            if ((x & 0x7F80u) == 0x7F80u) c += __uint_as_float(x << 16);
           }
           if (c == 0.f) continue;
           if (part) {
@@ -1122,19 +1144,34 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     uint32_t guarded = 0;
     for (int n_item = 0; ok && take(n_item); ++n_item) {
       const int n = it.b1 - it.b0, tiles = G::kPair && it.nb1 > 0 ? 2 : 1;
+      const int slots = (n - max(it.guard - it.b0, 0)) * PD * tiles;
+      uint32_t* bad_words = &tail.bad[n_item % 8][w][0][0];
+      __syncwarp();
+      if (lane < 8) bad_words[lane] = 0;                   // eight items ago: its outputs are written
+      __syncwarp();
 #pragma unroll 1
-      for (int left = (n - max(it.guard - it.b0, 0)) * PD * tiles; left > 0 && ok; --left) {
+      for (int k = 0; k < slots && ok; ++k) {
           ok = __all_sync(0xffffffffu, wait_for(bar_landed + 8 * (guarded % NS), (guarded / NS) & 1));
           if (!ok) break;
           const uint32_t s = guard_slot[guarded % NS];
-          const uint32_t at = s_ring + s * G::kSlot + w * (G::kSlot / G::kScanWarps) + lane * 16;
+          const uint32_t off = w * (G::kSlot / G::kScanWarps), at = s_ring + s * G::kSlot + off + lane * 16;
           bool bad = false;
 #pragma unroll 4
           for (uint32_t o = 0; o < G::kSlot / G::kScanWarps; o += 512) bad |= non_finite16(at + o);
           if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll 1
-            for (uint32_t o = 0; o < G::kSlot / G::kScanWarps; o += 512) clean16(at + o);
+            for (uint32_t o = 0; o < G::kSlot / G::kScanWarps; o += 512) {     // four tokens, 128 bytes of each
+              const unsigned in = __ballot_sync(0xffffffffu, non_finite16(at + o));
+              if (in == 0) continue;
+              clean16(at + o);
+              if (lane == 0) {
+                const uint32_t token = (off + o) % G::kPanel / 128;
+                bad_words[4 * (k / (PD * tiles)) + token / 32] |=
+                    ((in & 0xffu ? 1u : 0u) | (in & 0xff00u ? 2u : 0u) | (in & 0xff0000u ? 4u : 0u) | (in & 0xff000000u ? 8u : 0u)) << (token % 32);
+              }
+            }
             if (lane == 0) atomicMin(const_cast<int*>(first_bad), n_item);
+            __threadfence_block();
             fence_proxy_async_shared();
           }
           __syncwarp();

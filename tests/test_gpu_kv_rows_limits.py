@@ -182,3 +182,65 @@ def test_slot_maps_in_a_row(L):  # noqa: F811
         assert np.array_equal(t.cpu().numpy(), table)
     finally:
         L.lora_pool_destroy(pool)
+
+
+VALUES = np.array([0x7F80, 0xFF80, 0x7FC0], np.uint16)
+
+
+@pytest.mark.parametrize("n_kv,G,D", [(9, 1, 64), (6, 2, 128), (5, 3, 128), (7, 1, 256), (2, 16, 64)])
+def test_infinities_all_over_many_prompts(L, n_kv, G, D):  # noqa: F811
+    """Many items per CTA, infinities and NaN in any of them and in the rows behind the last sequence."""
+    import torch
+    rng = np.random.default_rng(42)
+    lengths = [int(x) for x in rng.integers(1, 300, 70)]
+    c = Prompt(L, n_kv, G, D, lengths, seed=43, behind=60)
+    try:
+        want, z = c.run()
+        expect = want.float().view(c.rows, n_kv, G, D).clone()
+        for _ in range(900):
+            s, d, kv = int(rng.integers(0, 70)), int(rng.integers(0, D)), int(rng.integers(0, n_kv))
+            row, value = c.starts[s] + int(rng.integers(0, lengths[s])), rng.choice(VALUES, 1)
+            if c.v[row, kv * D + d] & 0x7F80 != 0x7F80:
+                c.v[row, kv * D + d] = value[0]
+                expect[row:c.starts[s + 1], kv, :, d] += bits_to_torch(value).float()
+        c.v[c.starts[-1]:] = 0x7FC0
+        got, z2 = c.run()
+        L.lora_status(c.pool)
+        assert torch.equal(z, z2)
+        expect = expect.view(c.rows, -1)
+        assert torch.equal(got.isnan(), expect.isnan())
+        assert torch.equal(got.float().nan_to_num(0), expect.nan_to_num(0))
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("n_kv,G,D", [(9, 1, 64), (5, 2, 128), (4, 3, 128), (3, 1, 256), (2, 16, 64)])
+def test_infinities_all_over_many_trees(L, n_kv, G, D):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(44)
+    lengths = [int(x) for x in rng.integers(64, 700, 40)]
+    nodes = [int(x) for x in rng.integers(1, 65, 40)]
+    c = Tree(L, n_kv, G, D, lengths, nodes, seed=45, kinds=KINDS)
+    try:
+        want, z = c.run()
+        alive = ~torch.isneginf(z).view(c.rows, n_kv, G, 1)                                # rows that see a token
+        expect = want.float().view(c.rows, n_kv, G, D).clone()
+        tabs = c.tables()
+        for _ in range(600):
+            r, d, kv = int(rng.integers(0, 40)), int(rng.integers(0, D)), int(rng.integers(0, n_kv))
+            base = lengths[r] - nodes[r]
+            j, value = max(0, lengths[r] - 1 - int(rng.integers(0, 130))), rng.choice(VALUES, 1)
+            if c.bits[tabs[r][j, 1], kv * D + d] & 0x7F80 == 0x7F80:
+                continue
+            c.bits[tabs[r][j, 1], kv * D + d] = value[0]
+            for i in range(nodes[r]):
+                if j < base or (c.masks[c.starts[r] + i] >> (j - base)) & 1:
+                    expect[c.starts[r] + i, kv, :, d] += bits_to_torch(value).float()
+        got, z2 = c.run()
+        L.lora_status(c.pool)
+        assert torch.equal(z, z2)
+        expect = torch.where(alive, expect, torch.zeros_like(expect)).view(c.rows, -1)
+        assert torch.equal(got.isnan(), expect.isnan())
+        assert torch.equal(got.float().nan_to_num(0), expect.nan_to_num(0))
+    finally:
+        c.close()
