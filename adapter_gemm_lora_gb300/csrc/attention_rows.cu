@@ -41,6 +41,8 @@ struct RowsArgs {
   int64_t v_stride;
   int32_t* n_items;                                 // workspace: work items per KV head, and they: (sequence, tile pair)
   int2* items;
+  int32_t heads_at;                                 // KV heads whose items run at the same time
+  int32_t tickets;                                  // 0: a fixed share of the items a CTA; else CTAs of the grid, taken by those that run
   // tree
   const uint16_t* pool;
   int64_t num_pages;
@@ -226,7 +228,7 @@ struct Geo {
   // weights (two halves) per buffer; sums full and drained per tile; products
   static constexpr int kItems = 4;                         // items handed out at a time
   static constexpr int kTakers = kSoftWarps + 1 + kScanWarps + kLoadWarps;      // warps that take every item
-  static constexpr int kBars = 4 * NS + 2 + 2 + 4 + 4 + 1 + 2 * kItems;
+  static constexpr int kBars = 4 * NS + 2 + 2 + 4 + 4 + 1 + 2 * kItems + 1;
   static constexpr int kWordsRing = 8;                     // blocks whose token masks are kept
   static constexpr uint32_t kTmemO = 256;                  // scores in columns [0, 256), sums behind them
 };
@@ -278,6 +280,21 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
   for (uint32_t i = 0; i < kWaitPolls; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
+}
+// Takes a CTA of the grid that has not been launched out of it, in place of the hardware: 16 bytes into shared memory
+// say whether there was one, and which.  Not to be asked again after a no.
+__device__ __forceinline__ void try_cancel(uint32_t dst, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst), "r"(bar) : "memory");
+}
+__device__ __forceinline__ int cancelled(uint32_t src) {   // the CTA's index, or -1
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "mov.s32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}" : "=r"(x) : "r"(src) : "memory");
+  return x;
 }
 // One thread of the warp, the same every time.  The compiler knows that a branch on it leaves one thread and keeps
 // descriptors in uniform registers: eight MMAs issue in 80 cycles, behind a branch on the lane's number in 490.
@@ -394,7 +411,7 @@ struct Tail {
   Item items[G::kItems];
   int32_t bounds[kFew + 1];              // few sequences: their row starts, and
   int32_t units[kFew + 1];               // items (prompt) or units of the requests before (tree)
-  alignas(16) int32_t ids[4][32];        // tree: a loading warp's pages
+  alignas(16) int32_t ids[4][32];        // tree: a loading warp's pages; prompt: the answer of try_cancel
 };
 template <typename G>
 constexpr uint32_t smem_bytes() { return G::kData + sizeof(Tail<G>); }
@@ -405,13 +422,15 @@ template <typename G>
 struct Walk {
   int32_t* bounds_s;             // few: Tail's
   int32_t* units_s;
-  int w, step, all;              // prompt: turn, CTAs, items times heads
-  int level;                     // prompt, few: the level that the walk is at
+  int w, step, all;              // prompt: turn (or the ticket's next item), CTAs, items of a head
+  uint32_t ticket, bar_ticket, asked;      // tickets: their place and barrier in shared memory, how many so far
+  bool failed;
+  int top;                       // prompt, few: the highest level
   int64_t u, u1, per_head;       // tree: units left are [u, u1)
 
   __device__ __forceinline__ Walk(const RowsArgs& a, int32_t* bounds, int32_t* units) : bounds_s(bounds), units_s(units) {
     const int lane = threadIdx.x & 31, heads = (a.n_kv + G::HT - 1) / G::HT;
-    int total = 0, top = 0;
+    int total = 0, most = 0;
     if (a.few) {
       bool bad = false;
       int32_t carry = INT32_MIN;
@@ -456,7 +475,7 @@ struct Walk {
           if (live) n = (row1 - row0 + G::RT * a.npt - 1) / (G::RT * a.npt);
           if (live) units_s[r] = n;
           total += __reduce_add_sync(0xffffffffu, n);
-          top = max(top, (int)__reduce_max_sync(0xffffffffu, n));
+          most = max(most, (int)__reduce_max_sync(0xffffffffu, n));
         }
       }
       __syncwarp();
@@ -468,10 +487,12 @@ struct Walk {
       u = p < parts ? p * units / parts : 0;
       u1 = p < parts ? (p + 1) * units / parts : 0;
     } else {
-      w = 0;
+      w = a.tickets ? (int)blockIdx.x : 0;
+      asked = 0;
+      failed = false;
       step = gridDim.x;
-      level = top - 1;
-      all = (a.few ? total : *a.n_items) * heads;
+      top = most - 1;
+      all = a.few ? total : *a.n_items;
     }
   }
   // The part that holds unit x of all heads.
@@ -522,13 +543,32 @@ struct Walk {
       u += it.b1 - it.b0;
       return true;
     }
-    // There and back over the CTAs, so that none has the longer item of every turn.
-    const int x = w * step + ((w & 1) ? step - 1 - (int)blockIdx.x : (int)blockIdx.x);
-    if (x >= all) return false;
-    ++w;
-    const int heads = (a.n_kv + G::HT - 1) / G::HT, place = x / heads;
+    // Some heads at a time (their K and V stay in L2), of these the longest items of all sequences first.
+    int x = w;
+    if (a.tickets == 0) {                                  // there and back over the CTAs: none has the longer item of every turn
+      x = w * step + ((w & 1) ? step - 1 - (int)blockIdx.x : (int)blockIdx.x);
+      if (x >= all * a.n_kv) return false;
+      ++w;
+    } else {
+      while (x >= all * a.n_kv) {                          // none (left) of this ticket
+        if (lane == 0) {
+          fence_proxy_async_shared();
+          mbar_arrive_expect_tx(bar_ticket, 16);
+          try_cancel(ticket, bar_ticket);
+        }
+        __syncwarp();
+        const bool got = __all_sync(0xffffffffu, wait_for(bar_ticket, asked++ & 1));
+        x = got ? cancelled(ticket) : -1;
+        __syncwarp();
+        failed = !got;
+        if (x < 0) return false;
+      }
+      w = x + a.tickets;                                   // the item behind the last ticket's
+    }
+    const int turn = x / (all * a.heads_at), in = x - turn * all * a.heads_at, now = min(a.heads_at, a.n_kv - turn * a.heads_at);
+    const int place = in / now;
     int first = 0, end = 0, tile = 0;
-    it.head = (x - place * heads) * G::HT;
+    it.head = turn * a.heads_at + in - place * now;
     if (a.few) {
       // The longest first: the lowest level with `place` or fewer items above it; the k-th sequence that has it.
       const auto above = [&](int L) {
@@ -537,7 +577,7 @@ struct Walk {
         for (int r = lane; r < a.n_req; r += 32) n += max(units_s[r] - 1 - L, 0);
         return __reduce_add_sync(0xffffffffu, n);
       };
-      int lo = 0;
+      int lo = 0, level = top;
 #pragma unroll 1
       while (lo < level) {
         const int mid = (lo + level) / 2;
@@ -639,6 +679,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   const uint32_t bar_qfull = bar_landed + 8 * NS, bar_qempty = bar_qfull + 8, bar_scores = bar_qempty + 8;
   const uint32_t bar_weights = bar_scores + 16, bar_sums = bar_weights + 32, bar_drained = bar_sums + 16;
   const uint32_t bar_product = bar_drained + 16, bar_item = bar_product + 8, bar_taken = bar_item + 8 * G::kItems;
+  const uint32_t bar_ticket = bar_taken + 8 * G::kItems;
   volatile uint32_t* words = &tail.words[0][0];
   volatile int* first_bad = &tail.first_bad;
   volatile uint32_t* guard_slot = tail.guard_slot;
@@ -661,6 +702,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       mbar_init(bar_drained + 8 * i, 4);
     }
     mbar_init(bar_product, 1);
+    mbar_init(bar_ticket, 1);
     for (int i = 0; i < G::kItems; ++i) {
       mbar_init(bar_item + 8 * i, 1);
       mbar_init(bar_taken + 8 * i, G::kTakers);
@@ -1071,9 +1113,17 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   } else if (warp == G::kPlanWarp) {
     // ---- the items; of trees Q ----
     Walk<G> walk(a, tail.bounds, tail.units);
+    walk.ticket = smem_u32(tail.ids);
+    walk.bar_ticket = bar_ticket;
     if (G::kTree && lane == 0) a.ws_start[blockIdx.x] = make_int4(-1, 0, 0, 0);
     for (int n_item = 0; ok; ++n_item) {
+      if (!G::kTree && a.tickets && n_item >= 2) {         // no earlier: it might run sooner elsewhere
+        const int at = (n_item - 2) % G::kItems;
+        ok = __all_sync(0xffffffffu, wait_for(bar_taken + 8 * at, (uint32_t)((n_item - 2) / G::kItems) & 1u));
+        if (!ok) break;
+      }
       const bool more = walk.next(a, it);
+      if (!G::kTree && walk.failed) ok = false;
       if (!more) it.req = -1;
       it.nb0 = Walk<G>::blocks(a, it, 0);
       it.nb1 = NT == 2 ? Walk<G>::blocks(a, it, 1) : 0;
@@ -1398,6 +1448,8 @@ int encode_pages(CUtensorMap* map, const void* pool, int H, int64_t num_pages) {
   return encode_map(map, pool, 2, dims, strides, box);
 }
 
+constexpr int64_t kKvInL2 = 96 << 20;
+constexpr int64_t kShortRows = 1280 * 256;          // mean length times rows of an item
 int tiles_of(int D) { return D == 256 ? 1 : 2; }
 
 // Workspaces; every array starts on a 256-byte boundary.
@@ -1457,7 +1509,7 @@ int launch_prompt(const lora_pool* p, const RowsArgs& a, const PromptLayout& L, 
     if (e != cudaSuccess) return lora_cuda_fail(e, what);
   }
   const int64_t most = ((int64_t)a.n_rows / L.per_item + a.n_req) * a.n_kv;
-  const int ctas = (int)std::min<int64_t>(device_sm_count(), most);
+  const int ctas = a.tickets ? a.tickets : (int)std::min<int64_t>(device_sm_count(), most);
   switch (p->H / a.n_kv) {
     case 64: return launch_rows<Geo<64, false>>(p, a, q, k, v, ctas, what, st);
     case 128: return launch_rows<Geo<128, false>>(p, a, q, k, v, ctas, what, st);
@@ -1541,6 +1593,19 @@ extern "C" int lora_attention_prompt(lora_pool* p, int32_t n_seq, const int32_t*
   a.v_stride = v_stride;
   a.n_items = reinterpret_cast<int32_t*>(ws + L.n_items);
   a.items = reinterpret_cast<int2*>(ws + L.items);
+  // A ticket per full item, the CTAs of the grid: those that run take the others' in turn, so that each has its share
+  // by time.  Against a fixed share 0 to 10 % less (24,000 tokens of 32 heads of 128 in 4 prompts 324 -> 314 us).  Not
+  // where the sequences are shorter than an item, of which a ticket would be several, nor for two rounds of items.
+  const int64_t tickets = (int64_t)n_rows / L.per_item * n_kv_heads, kv_bytes = (int64_t)n_rows * p->H * 4;
+  a.heads_at = n_kv_heads;
+  if (n_rows / n_seq >= L.per_item && tickets >= 2 * device_sm_count()) {
+    a.tickets = (int32_t)tickets;
+    // K and V beyond what L2 keeps, in sequences so short that reading them takes the time: about 48 MB of heads at a
+    // time (30 prompts of 400 to 1,200 tokens, 32 heads of 128 242 -> 218 us, 16 of 256 306 -> 208; 7 of 1,700 tokens
+    // 167 -> 170, which the rule leaves alone).
+    if (kv_bytes > kKvInL2 && (int64_t)n_rows / n_seq * L.per_item < kShortRows)
+      a.heads_at = (int)std::max<int64_t>(n_kv_heads / ((2 * kv_bytes + kKvInL2 - 1) / kKvInL2), 1);
+  }
   return launch_prompt(p, a, L, tm_q, tm_k, tm_v, reinterpret_cast<cudaStream_t>(stream));
 }
 

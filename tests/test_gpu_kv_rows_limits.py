@@ -71,6 +71,72 @@ def test_as_many_trees_as_there_may_be(L, n_kv, G, D):  # noqa: F811
         L.lora_pool_destroy(pool)
 
 
+SHARED_OUT = [   # n_kv, G, D, lengths, rows before and behind: enough full items that the CTAs take them in turn
+    (20, 4, 128, [700, 1, 0, 300, 77, 64], 0, 0),
+    (8, 8, 64, [1300, 33, 32, 31], 3, 700),
+    (4, 16, 64, [17, 40, 16, 33] * 50, 1, 2),          # listed by a kernel of their own
+    (12, 2, 256, [500, 640, 3, 900], 5, 1),
+    (3, 16, 256, [1000], 0, 0),
+    (256, 1, 64, [400, 330, 0, 513, 256, 110], 0, 1),  # K and V beyond L2: 85 heads at a time, and the one left
+    (64, 1, 256, [900, 128, 700], 0, 0),
+    (40, 2, 128, [128, 127, 300, 600, 5], 0, 2000),    # fewer items than tickets
+]
+
+
+@pytest.mark.parametrize("n_kv,G,D,lengths,before,behind", SHARED_OUT)
+def test_items_taken_in_turn(L, n_kv, G, D, lengths, before, behind):  # noqa: F811
+    import torch
+    c = Prompt(L, n_kv, G, D, lengths, seed=46, before=before, behind=behind)
+    try:
+        out, lse = c.run()
+        L.lora_status(c.pool)
+        _check(c.reference(), out, lse, D)
+        for _ in range(3):
+            again = c.run()
+            assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    finally:
+        c.close()
+
+
+def test_items_taken_in_turn_on_two_streams_and_in_a_graph(L):  # noqa: F811
+    import torch
+    c = Prompt(L, 20, 4, 64, [700, 1, 0, 300, 77, 64], seed=47)
+    d = Prompt(L, 8, 8, 128, [90, 1200, 8], seed=48)
+    try:
+        want_c, want_d = c.run(), d.run()
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        results = []
+        for _ in range(6):
+            with torch.cuda.stream(s1):
+                results.append((c.run(stream=s1), want_c))
+            with torch.cuda.stream(s2):
+                results.append((d.run(stream=s2), want_d))
+        torch.cuda.synchronize()
+        for got, want in results:
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        q, k, v = (bits_to_torch(x) for x in (c.q, c.k, c.v))
+        starts = torch.tensor(c.starts, dtype=torch.int32, device="cuda")
+        out, lse = _outputs(c.rows, c.heads * c.D, c.heads)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            L.lora_attention_prompt(c.pool, 6, starts, c.rows, q, k, v, out, c.heads, c.n_kv, c.ws, c.ws_bytes, lse_dev=lse)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want_c[0]) and torch.equal(lse, want_c[1])
+        for now in ([0, 100, 200, 300, 400, 500, 600], [1142] * 7, [0] + [1142] * 6):
+            starts.copy_(torch.tensor(now, dtype=torch.int32))
+            out.fill_(-3)
+            lse.fill_(-7)
+            g.replay()
+            torch.cuda.synchronize()
+            _check(O.attention_prompt(c.q, c.k, c.v, now, c.heads, c.n_kv), out, lse, c.D)
+        L.lora_status(c.pool)
+    finally:
+        c.close()
+        d.close()
+
+
 def test_one_tensor_as_q_k_and_v(L):  # noqa: F811
     c = Prompt(L, 2, 1, 128, [300, 40], seed=34)
     try:
