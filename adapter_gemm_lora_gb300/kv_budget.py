@@ -124,10 +124,9 @@ class BudgetedCache:
         if any(self.lengths):
             raise ValueError("prefill: the cache is not empty")
         counts = self._checked(lengths, self.cap, "prefill")
-        self._append(counts)
-        self.prompt, self.drafted = counts, None
-        self._rows_ws_bytes = self.lib.lora_attention_prompt_size(self.pool, len(self.ids), self.rows, self.n_heads,
-                                                                  self.n_kv_heads)
+        ws_bytes = self.lib.lora_attention_prompt_size(self.pool, len(self.ids), sum(counts), self.n_heads, self.n_kv_heads)
+        self._append(counts)                                   # not before the call is known to be small enough
+        self.prompt, self.drafted, self._rows_ws_bytes = counts, None, ws_bytes
         self._rows_ws = torch.empty(max(self._rows_ws_bytes, 256), dtype=torch.uint8, device=self.table.device)
 
     def attend_prompt(self, layer: int, q, k, v, out) -> None:

@@ -101,6 +101,26 @@ def test_refusals(L, on_cpu):  # noqa: F811
         L.lora_pool_destroy(pool)
 
 
+class RealSizes(AppendLib):
+    def lora_attention_prompt_size(self, *args):
+        return self.lib.lora_attention_prompt_size(*args)
+
+
+def test_more_prompt_tokens_than_a_call_takes_change_nothing(L, on_cpu):  # noqa: F811
+    from adapter_gemm_lora_gb300.kv_budget import BudgetedCache
+    pool = L.lora_pool_create(None, 300000, 64, 1, 1)
+    cache = BudgetedCache(RealSizes(L), pool, [1, 2], 1, 1, 1, 40000, 2, 100)
+    try:
+        with pytest.raises(L.LoraError) as e:
+            cache.prefill([40000, 25537])
+        assert e.value.code == L.LORA_EINVAL
+        assert L.lora_pool_stats(pool)["free"] == 300000 and cache.lengths == [0, 0] and cache.prompt is None
+        cache.prefill([40000, 25536])
+        assert cache.lengths == [40000, 25536] and L.lora_pool_stats(pool)["free"] == 300000 - 2 * 65536
+    finally:
+        L.lora_pool_destroy(pool)
+
+
 def test_random_tree():
     from adapter_gemm_lora_gb300.kv_budget import random_tree
     mask, parent = random_tree(np.random.default_rng(3), 64)
