@@ -4,6 +4,39 @@
 // Per query head h (KV head h / G, G = n_heads / n_kv_heads, width D) and row i, over the tokens j it sees:
 //     s_j = q_{i,h} . k_j / sqrt(D),  lse = log sum_j exp(s_j),  out_{i,h} = sum_j exp(s_j - lse) v_j
 // Softmax in base 2: scores carry log2(e) / sqrt(D).
+//
+// One kernel for both.  A CTA per SM takes items one after another: 128 query rows (tokens or nodes times the group's
+// heads) in each of two tiles (one at D = 256), over blocks of 128 tokens of one KV head.  Per tile and block
+//     S = Q K^T (tcgen05, Q and K in shared memory, S in TMEM), P = 2^(S - m - 24) as bf16 in the same columns,
+//     O += P V (P from TMEM, V in shared memory, O in TMEM for the whole item), l += sum P in fp32,
+// so scores and weights never leave the SM.  Warps have roles that hand over by mbarriers: one finds the items, one
+// thread issues the MMAs, one warp (tree: four, that gather) keeps a ring of K and V slots filled, a thread per row does
+// the softmax and the outputs, with registers taken from the others.  The two tiles alternate: one's products run
+// under the other's softmax.
+//
+// Masks.  A prompt's blocks below the diagonal and a tree's before the first node are seen whole.  In the others the
+// softmax threads put -infinity into TMEM first, and infinities and NaN of V, whose products with weights of 0 would be
+// NaN, are cleared in shared memory by a warp of its own; the outputs get back those that their row sees.
+//
+// Weights enter the V product as bf16, off by half a step, 2^-8, at most: a second term would be half as many MMAs
+// again where MMAs bound the time.  The weights' sum takes them unrounded in fp32.  Against 64 bits outputs are off by 0.0019 to 0.0024 of their size, their own rounding
+// included (plain fp32 form, rounded once: 0.0015 to 0.0017).
+//
+// What bounds it, on one GB300 (MMA 1,952 TFLOP/s, copies 6,763 GB/s as measured):
+//   prompts of 16,384 tokens, 32 heads of 128       1,447 us  1,520 TFLOP/s, 0.78 of the burst, 0.88 of the sustained rate
+//   7 prompts of 386 to 5,000, 8 KV heads x 4 of 128  291 us  1,395 TFLOP/s: a block takes 3,000 cycles, its MMAs 2,048; a
+//                                                             tile's scores wait for its own weights' product
+//   2 of 3,926 and 4,097, 8 KV heads x 2 of 256       195 us  1,350 TFLOP/s: likewise, one tile with two score buffers
+//   16 of 305 to 1,024, 32 heads of 128               102 us  3.7 TB/s of the inputs and outputs: items of 1 to 8 blocks,
+//                                                             of which an item's start and end take 5,000 cycles
+//   33 of 40 to 515, 32 KV heads x 2 of 64             64 us  2.7 TB/s: likewise
+//   trees of 32 nodes, 64 requests of up to 2,047 tokens, 32 heads of 128   192 us  6.0 TB/s, 0.88 of the copy rate
+//   one of 64 nodes, 131,072 tokens, 32 heads of 128                        323 us  6.7 TB/s, 0.98
+//   48 nodes, 7 requests of 500 to 33,333 tokens, 8 KV heads x 4 of 128     132 us  4.8 TB/s, 0.71; tensor pipe 0.60 busy
+// Pages are gathered by TMA, 256 bytes of each, four a copy (131,072 tokens with 16-byte cp.async instead: 503 us against
+// 346 at that step; 4 warps, since a copy takes 50 cycles to issue).
+// The CTA's warps share the instruction cache and an item of a short prompt runs through most of the code, so code size
+// is time: 80 KB -> 54 KB took 10 to 17 % off short sequences.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -194,7 +227,9 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const RowsArgs 
 
 // ---- the kernel ----------------------------------------------------------------------------------
 // An item is two tiles of query rows that work side by side (one tile at D = 256): rows of one KV head, which share
-// its K and V blocks, or with kPair (at most 64 nodes in a tile) the same rows of two neighbouring KV heads.
+// its K and V blocks, or with kPair the same rows of two neighbouring KV heads.  A pair is taken where one tile holds a
+// whole tree of 64 nodes (G <= 2), so that the second would be empty: 64 requests of 128 to 2,048 tokens, 32 heads of 128
+// 208 -> 192 us (one request of 705 tokens, 4 heads of 64 10.8 -> 11.4).
 template <int D_, bool kTree_, bool kPair_ = false>
 struct Geo {
   static constexpr int D = D_;
@@ -220,7 +255,8 @@ struct Geo {
   static constexpr int kScanWarp = kSoftWarps + (kTree ? 2 : 3);
   static constexpr int kScanWarps = kTree ? 2 : 1;
   static constexpr int kThreads = 32 * (kSoftWarps + (kTree ? 8 : 4));       // whole warpgroups: they trade registers
-  // Registers a thread: a softmax thread holds a row of scores.  Launch 128 or 168 (D = 256: 168 or 255).
+  // Registers a thread: a softmax thread holds a row of scores (without the trade 16 prompts 151 -> 177 us).  Launch 128
+  // or 168 (D = 256: 168 or 232).
   static constexpr int kSoftRegs = NT == 1 ? 232 : kTree ? 192 : 208;
   static constexpr int kOtherRegs = NT == 1 ? (kTree ? 136 : 232) : kTree ? 64 : 88;
   static constexpr uint32_t kData = NT * kQTile + NS * kSlot;
@@ -417,7 +453,9 @@ template <typename G>
 constexpr uint32_t smem_bytes() { return G::kData + sizeof(Tail<G>); }
 
 // The items of a CTA, one after another, found by one warp.  Up to kFew sequences it looks at the caller's starts and
-// lengths itself; beyond, a kernel before this one has listed the items (prompt) or added up the units (tree).
+// lengths itself; beyond, a kernel before this one has listed the items (prompt) or added up the units (tree).  With that
+// kernel always: 4 prompts of 4 to 9 tokens 6.4 -> 11.3 us, one tree behind 705 tokens 11.4 -> 14.8, 127 prompts of 40 tokens
+// 34.5 -> 39.0, 33 of 40 to 515 64.0 -> 67.5; every CTA reads the starts, so the limit is four of them a lane.
 template <typename G>
 struct Walk {
   int32_t* bounds_s;             // few: Tail's
@@ -1488,11 +1526,27 @@ TreeLayout tree_layout(int D, int32_t n_req, int32_t group) {
   return L;
 }
 
+// The softmax warps take registers that the others give back: a kernel that was compiled to fewer than both hold would
+// wait for them for ever.
+template <typename G>
+int check_registers(const char* what) {
+  static const int regs = [] {
+    cudaFuncAttributes attr{};
+    return cudaFuncGetAttributes(&attr, rows_kernel<G>) == cudaSuccess ? attr.numRegs : 0;
+  }();
+  constexpr int kWarps = G::kThreads / 32, kNeed = G::kSoftWarps * G::kSoftRegs + (kWarps - G::kSoftWarps) * G::kOtherRegs;
+  if (regs * kWarps < kNeed)
+    return lora_fail(LORA_ECUDA, std::string(what) + ": the kernel has " + std::to_string(regs) + " registers a thread, its warps trade " +
+                                     std::to_string((kNeed + kWarps - 1) / kWarps));
+  return LORA_OK;
+}
+
 template <typename G>
 int launch_rows(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                 int ctas, const char* what, cudaStream_t st) {
   static DeviceFlags flags;
-  const int rc = ensure_smem_attr(flags, &rows_kernel<G>, (int)smem_bytes<G>(), what);
+  int rc = ensure_smem_attr(flags, &rows_kernel<G>, (int)smem_bytes<G>(), what);
+  if (rc == LORA_OK) rc = check_registers<G>(what);
   if (rc != LORA_OK) return rc;
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
   const cudaError_t e = launch_pdl(!p->prof_on, rows_kernel<G>, dim3(ctas), dim3(G::kThreads), smem_bytes<G>(), st, q, k, v, a);

@@ -307,7 +307,7 @@ int lora_kv_keep(lora_pool* pool, int64_t request_id, int32_t layers, int32_t n_
  *   row_req, row_pos  out: device int32 [row_cap].
  * A negative count (taken as 0), an old length outside [0, max_len] (clamped), a token at or past max_len
  * (its row gets row_req = -1 and its page goes nowhere) and rows past row_cap (dropped) set the device error
- * word; new_len counts what the table holds.  At most 65535 requests; max_len at most 2^30.
+ * word; new_len counts what the table holds.  At most 65535 requests and 2^20 layers; max_len at most 2^30.
  */
 int lora_kv_append(lora_pool* pool, int32_t n_req, const int32_t* count, const int32_t* old_len, const int32_t* pages,
                    int32_t row_cap, int32_t* table_dev, int32_t max_len, int32_t layers, int32_t* new_len,
@@ -334,7 +334,7 @@ int lora_kv_append(lora_pool* pool, int32_t n_req, const int32_t* count, const i
  *              ordered (two captured graphs that share it must not run at once).
  * A row depends on its own sequence's rows up to itself alone, whatever stands in other rows.  Scores and sums
  * are fp32; a weight enters the V product as bf16.  An infinite V gives that infinity where it is seen (NaN
- * where both signs meet, or where its weight is below 2^-100 of the row's largest).  If no score of a row is
+ * where both signs meet, and it may where its weight is below 2^-100 of the row's largest).  If no score of a row is
  * above -infinity, out is 0 and lse -infinity.  Starts that descend or leave [0, n_rows] set the device error
  * word and each is taken as the largest up to it, clamped.  At most 65535 sequences.
  */
