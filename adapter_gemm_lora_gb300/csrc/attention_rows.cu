@@ -1695,11 +1695,11 @@ extern "C" int lora_attention_tree(lora_pool* p, int32_t n_req, const int32_t* t
     return lora_fail(LORA_EINVAL, fn + ": table and mask must be 8-byte aligned");
   if (((reinterpret_cast<uintptr_t>(seq_len_dev) | reinterpret_cast<uintptr_t>(node_start) | reinterpret_cast<uintptr_t>(lse)) & 3) != 0)
     return lora_fail(LORA_EINVAL, fn + ": lengths, starts and lse must be 4-byte aligned");
-  if (p->planning) return lora_fail(LORA_EINVAL, fn + ": planning pool has no device state");
   const int D = p->H / n_kv_heads, group = n_heads / n_kv_heads;
   const TreeLayout L = tree_layout(D, n_req, group);
   rc = check_workspace(fn, workspace, workspace_bytes, some ? (int64_t)L.total : 0);
   if (rc != LORA_OK) return rc;
+  if (p->planning) return lora_fail(LORA_EINVAL, fn + ": planning pool has no device state");
   if (!some) return LORA_OK;
   CUtensorMap tm_q, tm_pages;
   rc = encode_pages(&tm_pages, p->pool_dev, p->H, p->num_pages);
