@@ -74,6 +74,8 @@ struct RowsArgs {
   int64_t v_stride;
   int32_t* n_items;                                 // workspace: work items per KV head, and they: (sequence, tile pair)
   int2* items;
+  int32_t* seq_items;                               // workspace: items that begin with a sequence
+  int32_t pack;                                     // short sequences share items
   int32_t heads_at;                                 // KV heads whose items run at the same time
   int32_t tickets;                                  // 0: a fixed share of the items a CTA; else CTAs of the grid, taken by those that run
   // tree
@@ -113,35 +115,55 @@ __device__ __forceinline__ T block_exclusive(T v, T* part, T& total) {
   return before + incl - v;
 }
 
+// Exclusive maximum likewise (INT32_MIN before the first).
+__device__ __forceinline__ int32_t block_exclusive_max(int32_t v, int32_t* part, int32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = blockDim.x >> 5;
+  int32_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl = max(incl, x);
+  }
+  int32_t before = __shfl_up_sync(0xffffffffu, incl, 1);
+  if (lane == 0) before = INT32_MIN;
+  __syncthreads();
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  total = INT32_MIN;
+  for (int w = 0; w < n; ++w) {
+    if (w < warp) before = max(before, part[w]);
+    total = max(total, part[w]);
+  }
+  return before;
+}
+
 // Row starts as the running maximum of the caller's, clamped into [0, n_rows]: sequences never overlap.
 constexpr int kPlanThreads = 1024;
 __device__ void plan_bounds(const RowsArgs& a) {
   __shared__ int32_t part[kPlanThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int32_t before = 0;
+  int32_t before = INT32_MIN, total;
   for (int i0 = 0; i0 <= a.n_req; i0 += kPlanThreads) {
     const int i = i0 + threadIdx.x;
     const int32_t x = i <= a.n_req ? a.start[i] : INT32_MIN;
-    int32_t m = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, m, o);
-      if (lane >= o) m = max(m, y);
-    }
-    if (lane == 31) part[warp] = m;
-    __syncthreads();
-    m = max(m, before);
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-      if (w < warp) m = max(m, part[w]);
-      before = max(before, part[w]);
-    }
-    const int32_t b = min(max(m, 0), a.n_rows);
+    const int32_t m = max(max(x, before), block_exclusive_max(x, part, total));
+    before = max(before, total);
     if (i <= a.n_req) {
+      const int32_t b = min(max(m, 0), a.n_rows);
       if (b != x) flag_error(a.err, LORA_DEV_BAD_SEGMENT);
       a.bounds[i] = b;
     }
-    __syncthreads();
   }
+  __syncthreads();
+}
+
+// Items that begin with the sequence of rows [first, end), of per rows each.  Packed, sequences that lie in one window
+// of as many rows share an item, which the first of them begins; before: the start of the last sequence with rows ahead
+// of this one, if any.  An item's sequences are neighbours in q, k and v, so it is loaded like one sequence's, and each
+// row is shown the tokens of its own.
+__device__ __forceinline__ int prompt_items(bool pack, int per, int before, int first, int end) {
+  const int window = pack ? first / per * per : 0;
+  if (end <= first || (pack && end <= window + per && before >= window)) return 0;
+  return (end - first + per - 1) / per;
 }
 
 // The prompts' work items, the longest first: item (s, L) is the L-th tile pair of sequence s, and it reads
@@ -153,8 +175,14 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const RowsArg
   for (int i = tid; i < levels; i += kPlanThreads) cursor[i] = 0;
   pdl_wait_then_release();
   plan_bounds(a);
-  for (int s = tid; s < a.n_req; s += kPlanThreads) {
-    const int n = (a.bounds[s + 1] - a.bounds[s] + per_item - 1) / per_item;
+  int32_t before = INT32_MIN, last;
+  for (int s0 = 0; s0 < a.n_req; s0 += kPlanThreads) {
+    const int s = s0 + tid, first = a.bounds[min(s, a.n_req)], end = a.bounds[min(s + 1, a.n_req)];
+    const int32_t ahead = max(before, block_exclusive_max(end > first ? first : INT32_MIN, part, last));
+    before = max(before, last);
+    if (s >= a.n_req) continue;
+    const int n = prompt_items(a.pack, per_item, ahead, first, end);
+    a.seq_items[s] = n;
     if (n > 0) atomicAdd(&cursor[n - 1], 1);
   }
   __syncthreads();
@@ -179,7 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const RowsArg
   __syncthreads();
   const int warp = tid >> 5, lane = tid & 31;
   for (int s = warp; s < a.n_req; s += kPlanThreads / 32) {
-    const int n = (a.bounds[s + 1] - a.bounds[s] + per_item - 1) / per_item;
+    const int n = a.seq_items[s];
     for (int L = lane; L < n; L += 32) a.items[atomicAdd(&cursor[L], 1)] = make_int2(s, L);
   }
 }
@@ -230,11 +258,12 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const RowsArgs 
 // its K and V blocks, or with kPair the same rows of two neighbouring KV heads.  A pair is taken where one tile holds a
 // whole tree of 64 nodes (G <= 2), so that the second would be empty: 64 requests of 128 to 2,048 tokens, 32 heads of 128
 // 208 -> 192 us (one request of 705 tokens, 4 heads of 64 10.8 -> 11.4).
-template <int D_, bool kTree_, bool kPair_ = false>
+template <int D_, bool kTree_, bool kPair_ = false, bool kPack_ = false>
 struct Geo {
   static constexpr int D = D_;
   static constexpr bool kTree = kTree_;
   static constexpr bool kPair = kPair_;
+  static constexpr bool kPack = kPack_;                    // prompt: short sequences share items
   static constexpr int NT = D == 256 ? 1 : 2;              // tiles of an item
   static constexpr int RT = kPair ? 1 : NT;                // of the rows of one head
   static constexpr int HT = kPair ? NT : 1;                // heads
@@ -420,6 +449,12 @@ __device__ __forceinline__ void clean16(uint32_t addr) {
   sts128(addr, x);
 }
 
+// Of 32 tokens those from the first to the last, a bit each; either may lie outside.
+__device__ __forceinline__ uint32_t prompt_sees(int first, int last) {
+  const uint32_t v = last < 0 ? 0u : last >= 31 ? 0xffffffffu : (2u << last) - 1u;
+  return first <= 0 ? v : first >= 32 ? 0u : v & (0xffffffffu << first);
+}
+
 // What a CTA works on at a time: the rows of a tile pair of one sequence and KV head, over some blocks of its tokens.
 struct Item {
   int head;                      // KV head
@@ -428,7 +463,7 @@ struct Item {
   int b0, b1;                    // blocks of tokens
   int guard;                     // first block in which some row does not see every token
   // tree
-  int len, base;                 // cached tokens, the first node's position
+  int len, base;                 // cached tokens (prompt: sequences), the first node's position
   int slot;                      // partial, or -1: the item has all blocks
   int nb0, nb1;                  // blocks of the tiles, 0: no rows
 };
@@ -490,6 +525,7 @@ struct Walk {
         }
       }
       __syncwarp();
+      int ahead = INT32_MIN;                               // prompt: the start of the last sequence with rows so far
 #pragma unroll 1
       for (int r0 = 0; r0 < a.n_req; r0 += 32) {
         const int r = min(r0 + lane, a.n_req - 1);
@@ -510,7 +546,19 @@ struct Walk {
           if (live) units_s[r] = total + incl - n;
           total += __shfl_sync(0xffffffffu, incl, 31);
         } else {
-          if (live) n = (row1 - row0 + G::RT * a.npt - 1) / (G::RT * a.npt);
+          int before = INT32_MIN;
+          if (G::kPack) {
+            int m = row1 > row0 ? row0 : INT32_MIN;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int y = __shfl_up_sync(0xffffffffu, m, o);
+              if (lane >= o) m = max(m, y);
+            }
+            before = __shfl_up_sync(0xffffffffu, m, 1);
+            before = lane == 0 ? ahead : max(ahead, before);
+            ahead = max(ahead, __shfl_sync(0xffffffffu, m, 31));
+          }
+          if (live) n = prompt_items(G::kPack, G::RT * a.npt, before, row0, row1);
           if (live) units_s[r] = n;
           total += __reduce_add_sync(0xffffffffu, n);
           most = max(most, (int)__reduce_max_sync(0xffffffffu, n));
@@ -646,14 +694,28 @@ struct Walk {
       it.req = e.x;
       tile = e.y;
     }
-    it.pos0 = tile * G::RT * a.npt;
+    const int per = G::RT * a.npt, window_end = first / per * per + per;
+    it.len = 1;
+    if (G::kPack && end <= window_end) {                     // with the sequences behind it that end in its window
+      const int32_t* bounds = a.few ? bounds_s : a.bounds;
+      int lo = it.req + 1, hi = a.n_req;                   // 32 places a turn, bounds[lo] <= window_end
+#pragma unroll 1
+      while (lo < hi) {
+        const int stride = (hi - lo) / 32 + 1, at = lo + lane * stride;
+        const unsigned in = __ballot_sync(0xffffffffu, at <= hi && bounds[min(at, hi)] <= window_end);
+        lo += (31 - __clz(in)) * stride;
+        hi = min(hi, lo + stride - 1);
+      }
+      end = bounds[lo];
+      it.len = lo - it.req;
+    }
+    it.pos0 = tile * per;
     it.row0 = first + it.pos0;
     it.count = end - first - it.pos0;
     it.b0 = 0;
-    it.b1 = (it.pos0 + min(it.count, G::RT * a.npt) + kBlock - 1) / kBlock;
+    it.b1 = (it.pos0 + min(it.count, per) + kBlock - 1) / kBlock;
     it.guard = it.pos0 / kBlock;
     it.slot = -1;
-    it.len = end - first;
     it.base = 0;
     return true;
   }
@@ -813,6 +875,19 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       const int pos = pos0 + min(tok, left - 1);
       uint64_t mask = 0;
       if (G::kTree) mask = a.mask[row0 + min(tok, left - 1)];
+      int from = 0;                                        // prompt: the first token of the row's sequence
+      if (G::kPack && it.len > 1) {
+        const int32_t* bounds = a.few ? tail.bounds : a.bounds;
+        int lo = it.req, hi = it.req + it.len;
+#pragma unroll 1
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (bounds[mid] <= row0 - pos0 + pos) lo = mid;
+          else hi = mid;
+        }
+        from = bounds[lo] - (row0 - pos0);
+        __syncwarp();
+      }
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < nb; ++i) {
         const int x = NB == 1 ? t : (i & 1);
@@ -826,7 +901,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         // Blocks of which a row does not see every token: what it does not see becomes -infinity, in place, so that the
         // code of the other blocks serves them too.
         const int j0 = (it.b0 + i) * kBlock;
-        bool some = !G::kTree && it.b0 + i >= pos0 / kBlock;
+        bool some = !G::kTree && (it.b0 + i >= pos0 / kBlock || (G::kPack && it.len > 1));
         if (G::kTree) {
           bool all = j0 + kBlock <= it.base;
 #pragma unroll
@@ -842,8 +917,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               v = words[((blocks_done + i) % G::kWordsRing) * 4 + c];
               if (d + 32 > 0) v &= d >= 64 ? 0u : d >= 0 ? (uint32_t)(mask >> d) : ((uint32_t)mask << -d) | ((1u << -d) - 1u);
             } else {
-              const int n = pos - j0 - 32 * c;             // the last token of these that the row sees
-              v = n < 0 ? 0u : n >= 31 ? 0xffffffffu : (2u << n) - 1u;
+              v = prompt_sees(from - j0 - 32 * c, pos - j0 - 32 * c);
             }
             if (!__any_sync(0xffffffffu, v != 0xffffffffu)) continue;
             tmem_ld_32x32b_x32(scores + 32 * c, u);
@@ -983,8 +1057,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const int d = j0 - it.base;
             if (d + 32 > 0) v &= d >= 64 ? 0u : d >= 0 ? (uint32_t)(mask >> d) : ((uint32_t)mask << -d) | ((1u << -d) - 1u);
           } else {
-            const int n = pos - j0;
-            v &= n < 0 ? 0u : n >= 31 ? 0xffffffffu : (2u << n) - 1u;
+            v &= prompt_sees(from - j0, pos - j0);
           }
           return v;
         };
@@ -999,15 +1072,15 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll 1
             for (uint32_t v = seen(at); v; v &= v - 1) {
               const int j = first * kBlock + 32 * at + __ffs(v) - 1;
-              const uint16_t* from;
+              const uint16_t* at_v;
               if (G::kTree) {
                 const int2 pg = a.table[((int64_t)it.req * a.max_len + j) * a.layers + a.layer];
                 if (pg.x < 0 || pg.x >= a.num_pages || pg.y < 0 || pg.y >= a.num_pages) continue;
-                from = a.pool + (int64_t)pg.y * a.H + kv * D + d;
+                at_v = a.pool + (int64_t)pg.y * a.H + kv * D + d;
               } else {
-                from = a.v + (row0 - pos0 + j) * a.v_stride + kv * D + d;
+                at_v = a.v + (row0 - pos0 + j) * a.v_stride + kv * D + d;
               }
-              const uint32_t x = *from;
+              const uint32_t x = *at_v;
               if ((x & 0x7F80u) == 0x7F80u) c += __uint_as_float(x << 16);
             }
           }
@@ -1492,7 +1565,7 @@ int tiles_of(int D) { return D == 256 ? 1 : 2; }
 
 // Workspaces; every array starts on a 256-byte boundary.
 struct PromptLayout {
-  size_t bounds, n_items, items, total;
+  size_t bounds, n_items, items, seq_items, total;
   int32_t per_item, levels;
 };
 PromptLayout prompt_layout(int D, int32_t n_seq, int32_t n_rows, int32_t group) {
@@ -1503,6 +1576,7 @@ PromptLayout prompt_layout(int D, int32_t n_seq, int32_t n_rows, int32_t group) 
   L.bounds = off;   off = align256(off + ((size_t)n_seq + 1) * 4);
   L.n_items = off;  off = align256(off + 4);
   L.items = off;    off = align256(off + ((size_t)n_rows / L.per_item + n_seq) * sizeof(int2));
+  L.seq_items = off; off = align256(off + (size_t)n_seq * 4);
   L.total = off;
   return L;
 }
@@ -1553,6 +1627,13 @@ int launch_rows(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, con
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, what);
 }
 
+template <int D>
+int launch_prompt_rows(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                       int ctas, const char* what, cudaStream_t st) {
+  return a.pack ? launch_rows<Geo<D, false, false, true>>(p, a, q, k, v, ctas, what, st)
+                : launch_rows<Geo<D, false>>(p, a, q, k, v, ctas, what, st);
+}
+
 int launch_prompt(const lora_pool* p, const RowsArgs& a, const PromptLayout& L, const CUtensorMap& q, const CUtensorMap& k,
                   const CUtensorMap& v, cudaStream_t st) {
   const char* what = "lora_attention_prompt launch";
@@ -1565,9 +1646,9 @@ int launch_prompt(const lora_pool* p, const RowsArgs& a, const PromptLayout& L, 
   const int64_t most = ((int64_t)a.n_rows / L.per_item + a.n_req) * a.n_kv;
   const int ctas = a.tickets ? a.tickets : (int)std::min<int64_t>(device_sm_count(), most);
   switch (p->H / a.n_kv) {
-    case 64: return launch_rows<Geo<64, false>>(p, a, q, k, v, ctas, what, st);
-    case 128: return launch_rows<Geo<128, false>>(p, a, q, k, v, ctas, what, st);
-    default: return launch_rows<Geo<256, false>>(p, a, q, k, v, ctas, what, st);
+    case 64: return launch_prompt_rows<64>(p, a, q, k, v, ctas, what, st);
+    case 128: return launch_prompt_rows<128>(p, a, q, k, v, ctas, what, st);
+    default: return launch_prompt_rows<256>(p, a, q, k, v, ctas, what, st);
   }
 }
 
@@ -1647,12 +1728,17 @@ extern "C" int lora_attention_prompt(lora_pool* p, int32_t n_seq, const int32_t*
   a.v_stride = v_stride;
   a.n_items = reinterpret_cast<int32_t*>(ws + L.n_items);
   a.items = reinterpret_cast<int2*>(ws + L.items);
+  a.seq_items = reinterpret_cast<int32_t*>(ws + L.seq_items);
+  // Sequences of two thirds of an item or less share items, unless each has an SM to itself: 127 prompts of 5 tokens, 8 KV
+  // heads x 4 of 128 25.9 -> 11.5 us, 86 of 16, 16 heads of 256 45.1 -> 17.7; of 40 tokens of an item's 64 34.7 -> 34.9.
+  // The code for it would cost longer ones 4 % (33 of 40 to 515 tokens 64.0 -> 66.7).
+  a.pack = (int64_t)n_seq * n_kv_heads > device_sm_count() && n_rows / n_seq * 3 <= 2 * L.per_item;
   // A ticket per full item, the CTAs of the grid: those that run take the others' in turn, so that each has its share
   // by time.  Against a fixed share 0 to 10 % less (24,000 tokens of 32 heads of 128 in 4 prompts 324 -> 314 us).  Not
   // where the sequences are shorter than an item, of which a ticket would be several, nor for two rounds of items.
   const int64_t tickets = (int64_t)n_rows / L.per_item * n_kv_heads, kv_bytes = (int64_t)n_rows * p->H * 4;
   a.heads_at = n_kv_heads;
-  if (n_rows / n_seq >= L.per_item && tickets >= 2 * device_sm_count()) {
+  if ((a.pack || n_rows / n_seq >= L.per_item) && tickets >= 2 * device_sm_count()) {
     a.tickets = (int32_t)tickets;
     // K and V beyond what L2 keeps, in sequences so short that reading them takes the time: about 48 MB of heads at a
     // time (30 prompts of 400 to 1,200 tokens, 32 heads of 128 242 -> 218 us, 16 of 256 306 -> 208; 7 of 1,700 tokens

@@ -98,6 +98,37 @@ def test_items_taken_in_turn(L, n_kv, G, D, lengths, before, behind):  # noqa: F
         c.close()
 
 
+SHORT = [   # n_kv, G, D, lengths, rows before and behind: short sequences, which share items
+    (40, 1, 128, [5, 0, 1, 90, 0, 0, 140, 3, 3, 250, 7, 1], 0, 3),
+    (30, 4, 64, [31, 33, 64, 1, 0, 2, 60, 64, 5, 5], 7, 0),
+    (25, 2, 256, [1, 63, 64, 65, 30, 34, 0, 128, 1], 63, 40),
+    (33, 3, 128, [42, 84, 41, 1, 85, 20, 20], 1, 1),
+    (20, 16, 64, [1, 2, 3, 4, 5, 6, 7, 8, 9, 0, 16, 17, 15], 5, 0),
+    (20, 5, 256, [25, 1, 24, 26, 0, 13, 12], 2, 9),
+    (3, 2, 128, [1, 0, 2, 127, 3, 0, 0, 9] * 20, 120, 0),
+    (2, 1, 64, [200, 56, 0, 256, 1, 255, 90, 90, 76] * 9, 0, 1),
+]
+
+
+@pytest.mark.parametrize("n_kv,G,D,lengths,before,behind", SHORT)
+def test_short_prompts_that_share_items(L, n_kv, G, D, lengths, before, behind):  # noqa: F811
+    """Against the oracle; then NaN in q, k and v of every other sequence leave the rest as it was."""
+    import torch
+    c = Prompt(L, n_kv, G, D, lengths, seed=49, before=before, behind=behind)
+    try:
+        out, lse = c.run()
+        L.lora_status(c.pool)
+        _check(c.reference(), out, lse, D)
+        for a, b in list(zip(c.starts[:-1], c.starts[1:]))[::2]:
+            for x in (c.q, c.k, c.v):
+                x[a:b] = 0x7FC0
+        got, lse2 = c.run()
+        for a, b in list(zip(c.starts[:-1], c.starts[1:]))[1::2]:
+            assert torch.equal(got[a:b], out[a:b]) and torch.equal(lse2[a:b], lse[a:b])
+    finally:
+        c.close()
+
+
 def test_items_taken_in_turn_on_two_streams_and_in_a_graph(L):  # noqa: F811
     import torch
     c = Prompt(L, 20, 4, 64, [700, 1, 0, 300, 77, 64], seed=47)
