@@ -1438,9 +1438,11 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 }
 
 // ---- joining a segment's partials ------------------------------------------------------------------
-// Segments that lie in several parts: block (p, y) takes the one that begins in part p and goes on behind it, a
+// Segments that lie in several parts: blocks (p, y) take the one that begins in part p and goes on behind it, a
 // warp per row.  m = max m_i, l = sum l_i 2^(m_i - m), out = sum o_i 2^(m_i - m) / l, in the parts' order.
-constexpr int kJoinWarps = 8;
+// The latency of its loads bounds it: 16 blocks a part and four parts in flight took 131,072 tokens from 323 to 319 us, 8 blocks
+// 321, 24 blocks 320 (and a small call from 10.5 to 11.6).
+constexpr int kJoinWarps = 8, kJoinBlocks = 16, kJoinBatch = 4;     // warps of a block, blocks of a part, parts that a warp has in flight
 template <typename G>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ RowsArgs a) {
   constexpr int D = G::D, E = D / 32;
@@ -1455,9 +1457,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
     const int t = G::kPair ? h : node / a.npt;
     const int64_t at = t * (a.slot_rows / G::NT) + (G::kPair ? node : node - t * a.npt) * a.group + g;
     const auto slot = [&](int i) { return (2 * (int64_t)i + (i == p ? 1 : 0)) * a.slot_rows + at; };
-    float m = -INFINITY;
+    float2 ml = make_float2(-INFINITY, 0.f);               // of 32 parts, a lane each
+    if (p + lane <= rec.w) ml = a.ws_ml[slot(p + lane)];
+    float m = ml.x;
 #pragma unroll 1
-    for (int i = p + lane; i <= rec.w; i += 32) m = fmaxf(m, a.ws_ml[slot(i)].x);
+    for (int i = p + 32 + lane; i <= rec.w; i += 32) m = fmaxf(m, a.ws_ml[slot(i)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float ms = m == -INFINITY ? 0.f : m;
@@ -1466,21 +1470,31 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 1
     for (int i0 = p; i0 <= rec.w; i0 += 32) {
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (i0 + lane <= rec.w) ml = a.ws_ml[slot(i0 + lane)];
+      if (i0 > p) {
+        ml = make_float2(-INFINITY, 0.f);
+        if (i0 + lane <= rec.w) ml = a.ws_ml[slot(i0 + lane)];
+      }
       const float c_own = ex2(ml.x - ms);
       const int n = min(32, rec.w - i0 + 1);
-      for (int b = 0; b < n; ++b) {
-        const float c = __shfl_sync(0xffffffffu, c_own, b);
-        l = fmaf(__shfl_sync(0xffffffffu, ml.y, b), c, l);
-        if (c == 0.f) continue;
-        const float* src = a.ws_acc + slot(i0 + b) * D + lane * E;
+#pragma unroll 1
+      for (int b0 = 0; b0 < n; b0 += kJoinBatch) {
+        float c[kJoinBatch];
+        float2 v[kJoinBatch][E / 2];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(src + e);
-          acc[e] = fmaf(v.x, c, acc[e]);
-          acc[e + 1] = fmaf(v.y, c, acc[e + 1]);
+        for (int b = 0; b < kJoinBatch; ++b) {
+          c[b] = __shfl_sync(0xffffffffu, c_own, b0 + b);  // 0 behind the last part
+          l = fmaf(__shfl_sync(0xffffffffu, ml.y, b0 + b), c[b], l);
+          const float2* src = reinterpret_cast<const float2*>(a.ws_acc + slot(i0 + b0 + b) * D + lane * E);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) v[b][e] = c[b] == 0.f ? make_float2(0.f, 0.f) : src[e];
         }
+#pragma unroll
+        for (int b = 0; b < kJoinBatch; ++b)
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            acc[2 * e] = fmaf(v[b][e].x, c[b], acc[2 * e]);
+            acc[2 * e + 1] = fmaf(v[b][e].y, c[b], acc[2 * e + 1]);
+          }
       }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1661,9 +1675,9 @@ int launch_tree(const lora_pool* p, const RowsArgs& a, const CUtensorMap& q, con
     if (e != cudaSuccess) return lora_cuda_fail(e, what);
   }
   const int rc = launch_rows<G>(p, a, q, pages, pages, a.parts, what, st);
-  if (rc != LORA_OK) return rc;
+  if (rc != LORA_OK || a.max_len <= kBlock) return rc;     // a single block is never cut
   ProfScope prof(p, LORA_KIND_ATTENTION, st);
-  const cudaError_t e = launch_pdl(!p->prof_on, tree_join_kernel<G>, dim3(a.parts, 8), dim3(32 * kJoinWarps), 0, st, a);
+  const cudaError_t e = launch_pdl(!p->prof_on, tree_join_kernel<G>, dim3(a.parts, kJoinBlocks), dim3(32 * kJoinWarps), 0, st, a);
   return e == cudaSuccess ? LORA_OK : lora_cuda_fail(e, what);
 }
 
