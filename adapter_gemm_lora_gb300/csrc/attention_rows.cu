@@ -31,7 +31,7 @@
 //                                                             of which an item's start and end take 5,000 cycles
 //   33 of 40 to 515, 32 KV heads x 2 of 64             64 us  2.7 TB/s: likewise
 //   trees of 32 nodes, 64 requests of up to 2,047 tokens, 32 heads of 128   192 us  6.0 TB/s, 0.88 of the copy rate
-//   one of 64 nodes, 131,072 tokens, 32 heads of 128                        323 us  6.7 TB/s, 0.98
+//   one of 64 nodes, 131,072 tokens, 32 heads of 128                        319 us  6.7 TB/s, 1.00
 //   48 nodes, 7 requests of 500 to 33,333 tokens, 8 KV heads x 4 of 128     132 us  4.8 TB/s, 0.71; tensor pipe 0.60 busy
 // Pages are gathered by TMA, 256 bytes of each, four a copy (131,072 tokens with 16-byte cp.async instead: 503 us against
 // 346 at that step; 4 warps, since a copy takes 50 cycles to issue).
