@@ -127,11 +127,12 @@ kv_write_packed_kernel(uint16_t* pool, int64_t num_pages, int32_t H, int32_t n_r
 // the counts itself (a thread adds up n_req / 256 requests, one scan over the threads), so the call is one
 // launch; a row's request is then found by bisection over the threads and a walk over that thread's
 // requests.  Pages are moved a layer's K and V (8 bytes) a thread, or two layers' (16) where the layers are even and
-// the arrays aligned.  64 prompts of 500 to 2,048 tokens, 40 layers, into a new table: 71 MB in 16.4 us, 4.3 TB/s (0.64 of
-// the copy rate; entries are moved in 1.7 rounds of CTAs that each begin with the counts).
+// the arrays aligned.  64 prompts of 500 to 2,048 tokens, 40 layers, into a new table: 71 MB in 13.8 us, 5.1 TB/s (0.76 of
+// the copy rate; entries are moved in 1.8 rounds of CTAs that each begin with the counts).  Four entries in flight and four
+// CTAs an SM; eight entries and two CTAs 16.4 us, and with the registers of four 14.3.
 constexpr int kAppendThreads = 256;
-constexpr int kAppendBatch = 8;                            // entries a thread has in flight
-constexpr int kAppendEntries = 2 * kAppendBatch * kAppendThreads;   // entries that a CTA writes, about
+constexpr int kAppendBatch = 4;                            // entries a thread has in flight
+constexpr int kAppendEntries = 4 * kAppendBatch * kAppendThreads;   // entries that a CTA writes, about
 constexpr int kAppendMaxRows = 1024;                       // rows a CTA takes, at most
 
 struct AppendArgs {
@@ -156,7 +157,7 @@ __device__ __forceinline__ int32_t append_old(const AppendArgs& a, int r) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendArgs a) {
   __shared__ int64_t before[kAppendThreads];               // rows of the requests of the threads before
   __shared__ int64_t warp_sum[kAppendThreads / 32];
   __shared__ int32_t req_s[kAppendMaxRows], pos_s[kAppendMaxRows];
@@ -982,7 +983,7 @@ extern "C" int lora_kv_append(lora_pool* p, int32_t n_req, const int32_t* count,
   a.n_req = n_req;
   a.count = count;
   a.old_len = old_len;
-  // Two layers at a time (64 prompts of 500 to 2,048 tokens, 40 layers: 16.4 us, one at a time 19.2).
+  // Two layers at a time (64 prompts of 500 to 2,048 tokens, 40 layers 13.8 us; 39 layers, one at a time, 16.5).
   const bool wide = layers % 2 == 0 && ((reinterpret_cast<uintptr_t>(table_dev) | reinterpret_cast<uintptr_t>(pages)) & 15) == 0;
   if (wide) layers /= 2;
   a.pages = pages;
