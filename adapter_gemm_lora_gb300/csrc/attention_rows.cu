@@ -338,7 +338,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 // mbar_wait in fewer instructions, for the kernel has some thirty waits and its warps share the instruction cache: it
 // counts polls instead of cycles, 3 KB less code and 1 to 2 % of the time of short prompts.  A poll of a phase that does
 // not end takes 22 to 8,000 cycles, so the limit lies between 50 ms and 20 s; what is waited for takes microseconds,
-// and some 20 ms at most where a tile's outputs get infinities back.
+// and some 3 ms at most where a tile's outputs get infinities back.
 constexpr uint32_t kWaitPolls = 1u << 22;
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
@@ -1065,8 +1065,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) any |= seen(c);
 #pragma unroll 1
-        for (int d = 0; d < D && live && any && l != 0.f; ++d) {
-          float c = 0.f;
+        for (int d = 0; d < D && live && any && l != 0.f; d += 8) {
+          float c[8] = {};
 #pragma unroll 1
           for (int at = 0; at < 8; ++at) {
 #pragma unroll 1
@@ -1080,16 +1080,25 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               } else {
                 at_v = a.v + (row0 - pos0 + j) * a.v_stride + kv * D + d;
               }
-              const uint32_t x = *at_v;
-              if ((x & 0x7F80u) == 0x7F80u) c += __uint_as_float(x << 16);
+              const uint4 x = *reinterpret_cast<const uint4*>(at_v);
+              const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t bad = non_finite2(u[e]);
+                if (bad & 0x8000u) c[2 * e] += __uint_as_float(u[e] << 16);
+                if (bad & 0x80000000u) c[2 * e + 1] += __uint_as_float(u[e] & 0xffff0000u);
+              }
             }
           }
-          if (c == 0.f) continue;
-          if (part) {
-            a.ws_acc[prow * D + d] += c;
-          } else {
-            uint16_t* y = a.out + orow * a.out_stride + (int64_t)head * D + d;
-            *y = f32_to_bf16_rn(__uint_as_float((uint32_t)*y << 16) + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (c[e] == 0.f) continue;
+            if (part) {
+              a.ws_acc[prow * D + d + e] += c[e];
+            } else {
+              uint16_t* y = a.out + orow * a.out_stride + (int64_t)head * D + d + e;
+              *y = f32_to_bf16_rn(__uint_as_float((uint32_t)*y << 16) + c[e]);
+            }
           }
         }
       }
