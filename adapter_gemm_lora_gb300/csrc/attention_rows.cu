@@ -1449,6 +1449,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 // ---- joining a segment's partials ------------------------------------------------------------------
 // Segments that lie in several parts: blocks (p, y) take the one that begins in part p and goes on behind it, a
 // warp per row.  m = max m_i, l = sum l_i 2^(m_i - m), out = sum o_i 2^(m_i - m) / l, in the parts' order.
+// A part far below the others has the factor 0 and its sums are multiplied by it all the same: an infinity or NaN of V there
+// gives NaN, as it does within a part, wherever the request is cut.
 // The latency of its loads bounds it: 16 blocks a part and four parts in flight took 131,072 tokens from 323 to 319 us, 8 blocks
 // 321, 24 blocks 320 (and a small call from 10.5 to 11.6).
 constexpr int kJoinWarps = 8, kJoinBlocks = 16, kJoinBatch = 4;     // warps of a block, blocks of a part, parts that a warp has in flight
@@ -1495,7 +1497,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
           l = fmaf(__shfl_sync(0xffffffffu, ml.y, b0 + b), c[b], l);
           const float2* src = reinterpret_cast<const float2*>(a.ws_acc + slot(i0 + b0 + b) * D + lane * E);
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) v[b][e] = c[b] == 0.f ? make_float2(0.f, 0.f) : src[e];
+          for (int e = 0; e < E / 2; ++e) v[b][e] = b0 + b < n ? src[e] : make_float2(0.f, 0.f);
         }
 #pragma unroll
         for (int b = 0; b < kJoinBatch; ++b)

@@ -1,0 +1,42 @@
+"""Values at the ends of the range in prompt and tree attention."""
+import numpy as np
+import pytest
+
+import workloads
+from test_gpu_kv_rows import L, Tree  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("n_kv,G,D", [(2, 1, 64), (1, 2, 128), (1, 3, 128), (1, 2, 256), (1, 16, 64)])
+@pytest.mark.parametrize("low", ["first", "last"])
+def test_tree_infinities_in_a_part_far_below(L, n_kv, G, D, low):  # noqa: F811
+    """One request over many SMs, half of its scores 300 above the others: an infinity of V whose weight is far below
+    2^-100 of the row's largest is that infinity or NaN, a NaN is NaN, whichever part they lie in."""
+    import torch
+    n, m = 4000, 9
+    c = Tree(L, n_kv, G, D, [n], [m], seed=21, kinds=("any",))
+    try:
+        tab, base = c.tables()[0], n - m
+        q, k = np.zeros((m, c.heads * D), np.float32), np.zeros((n, n_kv * D), np.float32)
+        q[:, ::D] = np.sqrt(D)
+        k[(np.arange(n) >= 2000) == (low == "first"), ::D] = 300.0
+        c.q, c.bits[tab[:, 0]] = workloads.to_bf16_bits(q), workloads.to_bf16_bits(k)
+        c.masks = [(1 << m) - 2 if i % 2 else (1 << m) - 1 for i in range(m)]              # odd rows do not see node 0
+        want, z = c.run()
+        tokens = (130, 700, 1900) if low == "first" else (2100, 2700, base)
+        for d, j, value in zip((3, 5, 9), tokens, (0x7F80, 0x7FC0, 0xFF80)):
+            c.bits[tab[j, 1], d] = value
+        got, z2 = c.run()
+        L.lora_status(c.pool)
+        assert torch.equal(z, z2) and want.isfinite().all()
+        hit = torch.zeros((m, n_kv, G, D), dtype=torch.bool, device="cuda")
+        hit[:, 0, :, [3, 5, 9]] = True
+        if low == "last":
+            hit[1::2, 0, :, 9] = False                                                     # the infinity is node 0's
+        hit = hit.view(m, -1)
+        assert not got[hit].isfinite().any()
+        assert got.view(m, n_kv, G, D)[:, 0, :, 5].isnan().all()
+        assert torch.equal(got[~hit], want[~hit])
+    finally:
+        c.close()
