@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 import workloads
-from test_gpu_kv_rows import L, Tree  # noqa: F401
+from test_gpu_kv_rows import L, Prompt, Tree, _bf16  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -38,5 +38,43 @@ def test_tree_infinities_in_a_part_far_below(L, n_kv, G, D, low):  # noqa: F811
         assert not got[hit].isfinite().any()
         assert got.view(m, n_kv, G, D)[:, 0, :, 5].isnan().all()
         assert torch.equal(got[~hit], want[~hit])
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("n_kv,G,D", [(1, 1, 64), (1, 1, 128), (2, 3, 128), (1, 2, 256), (40, 4, 64)])
+def test_prompt_rows_without_weight_behind_infinities(L, n_kv, G, D):  # noqa: F811
+    """Every score -infinity: out 0 and lse -infinity, whatever V holds in blocks that every row of a tile sees."""
+    c = Prompt(L, n_kv, G, D, [700, 3], seed=22)
+    try:
+        c.q[:], c.k[:] = _bf16(1.0), 0
+        c.q[:, ::D], c.k[:, ::D] = _bf16(3e38), _bf16(-3e38)
+        c.v[:100] = 0x7F80
+        c.v[3:90:5] = 0x7FC0
+        c.v[300:310] = 0xFF80
+        out, lse = c.run()
+        L.lora_status(c.pool)
+        assert (out == 0).all() and (lse == float("-inf")).all()
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("n_kv,G,D", [(16, 1, 64), (8, 2, 128), (6, 3, 128), (5, 2, 256), (2, 16, 64)])
+def test_tree_rows_without_weight_behind_infinities(L, n_kv, G, D):  # noqa: F811
+    """Likewise, requests of several blocks that lie in one part or in two."""
+    lengths = [400 + 13 * i for i in range(40)]
+    c = Tree(L, n_kv, G, D, lengths, [9] * 40, seed=23)
+    try:
+        c.q[:] = _bf16(1.0)
+        c.q[:, ::D] = _bf16(3e38)
+        for tab in c.tables():
+            k = np.zeros((len(tab), n_kv * D), np.uint16)
+            k[:, ::D] = _bf16(-3e38)
+            c.bits[tab[:, 0]] = k
+            c.bits[tab[:100, 1]] = 0x7F80
+            c.bits[tab[140:150, 1]] = 0x7FC0
+        out, lse = c.run()
+        L.lora_status(c.pool)
+        assert (out == 0).all() and (lse == float("-inf")).all()
     finally:
         c.close()
