@@ -1050,9 +1050,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       if (live && part) a.ws_ml[prow] = make_float2(m, l);
       if (live && !part && a.lse)
         a.lse[orow * a.n_heads + head] = l == 0.f ? -INFINITY : (m + kShift + log2f(l)) * 0.6931471805599453f;
-      if (n_item >= *first_bad) {
+      if (n_item >= *first_bad && it.guard < it.b1) {
         // Infinities and NaN of V in the blocks that not every row sees whole were left out of the products: the rows
-        // that see them get them here.
+        // that see them get them here.  Products with such blocks came after the scan of this item; an item without one
+        // (of a tree cut before its nodes) has no words of its own, and nothing orders the scan's before it.
         __syncwarp();
         const int first = max(it.b0, it.guard);
         const volatile uint32_t* bad_words = &tail.bad[n_item % 8][0][0][0];

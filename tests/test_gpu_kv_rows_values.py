@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 import workloads
+from helpers import bits_to_torch
 from test_gpu_kv_rows import L, Prompt, Tree, _bf16  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -76,5 +77,35 @@ def test_tree_rows_without_weight_behind_infinities(L, n_kv, G, D):  # noqa: F81
         out, lse = c.run()
         L.lora_status(c.pool)
         assert (out == 0).all() and (lse == float("-inf")).all()
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("n_kv,G,D,n", [(26, 1, 64, 120), (12, 1, 128, 300), (10, 3, 64, 200), (9, 2, 256, 180)])
+def test_tree_many_items_of_a_cta_with_infinities_in_most(L, n_kv, G, D, n):  # noqa: F811
+    """Ten items and more per SM, the last of them often a request's first blocks without its nodes, infinities and NaN
+    in the nodes of most requests, mask bits above the nodes' number: every row has those that it sees and no others."""
+    import torch
+    rng = np.random.default_rng(27)
+    lengths, nodes = [int(x) for x in rng.integers(130, 330, n)], [int(x) for x in rng.integers(1, 20, n)]
+    c = Tree(L, n_kv, G, D, lengths, nodes, seed=28, kinds=("any", "tree"))
+    try:
+        want, z = c.run()
+        alive = ~torch.isneginf(z).view(c.rows, n_kv, G, 1)
+        expect = want.float().view(c.rows, n_kv, G, D).clone()
+        tabs = c.tables()
+        for r in rng.permutation(n)[:n * 4 // 5]:
+            i, d, kv = int(rng.integers(0, nodes[r])), int(rng.integers(0, D)), int(rng.integers(0, n_kv))
+            value = rng.choice(np.array([0x7F80, 0xFF80, 0x7FC0], np.uint16), 1)
+            c.bits[tabs[r][lengths[r] - nodes[r] + i, 1], kv * D + d] = value[0]
+            for row in range(c.starts[r], c.starts[r + 1]):
+                if (c.masks[row] >> i) & 1:
+                    expect[row, kv, :, d] += bits_to_torch(value).float()
+        got, z2 = c.run()
+        L.lora_status(c.pool)
+        assert torch.equal(z, z2)
+        expect = torch.where(alive, expect, torch.zeros_like(expect)).view(c.rows, -1)
+        assert torch.equal(got.isnan(), expect.isnan())
+        assert torch.equal(got.float().nan_to_num(0), expect.nan_to_num(0))
     finally:
         c.close()
