@@ -18,9 +18,12 @@
 // softmax threads put -infinity into TMEM first, and infinities and NaN of V, whose products with weights of 0 would be
 // NaN, are cleared in shared memory by a warp of its own; the outputs get back those that their row sees.
 //
-// Weights enter the V product as bf16, off by half a step, 2^-8, at most: a second term would be half as many MMAs
-// again where MMAs bound the time.  The weights' sum takes them unrounded in fp32.  Against 64 bits outputs are off by 0.0019 to 0.0024 of their size, their own rounding
-// included (plain fp32 form, rounded once: 0.0015 to 0.0017).
+// Weights enter the V product as one bf16 term, off by half a step, 2^-8, at most; the weights' sum takes them unrounded
+// in fp32.  Against 64 bits outputs are off by 0.0019 to 0.0024 of their size, their own rounding included (plain fp32
+// form, rounded once: 0.0015 to 0.0017).  A second term, 2^-15 in all, is half as many MMAs again and three more
+// operations a pair of weights in the softmax, which lies on a tile's chain whatever bounds the call: prompts 103 -> 167
+// us (16 of 305 to 1,024 tokens), 1,440 -> 2,124 (16,384 tokens), 65 -> 104 (33 of 40 to 515), 195 -> 262 (D = 256), and trees that
+// read pages at HBM's rate 193 -> 223 (64 requests of up to 2,047 tokens) and 319 -> 362 (131,072), of shared heads 135 -> 178.
 //
 // What bounds it, on one GB300 (MMA 1,952 TFLOP/s, copies 6,763 GB/s as measured):
 //   prompts of 16,384 tokens, 32 heads of 128       1,447 us  1,520 TFLOP/s, 0.78 of the burst, 0.88 of the sustained rate

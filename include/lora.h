@@ -354,7 +354,9 @@ int lora_attention_prompt(lora_pool* pool, int32_t n_seq, const int32_t* seq_sta
  *     out_{i,h} = sum_j exp(s_ij - lse_{i,h}) V_j over the tokens that it sees, heads and s as for
  *     lora_attention_split (one KV head per n_heads / n_kv_heads query heads, D = 64, 128 or 256)
  * so a tree's mask holds the node itself and its ancestors, a chain's (the next tokens of one guess) bits
- * 0 .. i, and one node of mask 1 is plain decode attention.
+ * 0 .. i, and one node of mask 1 has the formula of decode attention, though not lora_attention_split's bits: here a
+ * weight enters the V product as one bf16 term (off by up to 2^-8 of itself), there with all its fp32 bits, so logits
+ * that nearly tie may fall the other way.
  *   table_dev, seq_len_dev, max_len, layers, layer   as for lora_attention_split;
  *   node_start device int32 [n_req + 1], ascending within [0, n_rows]; a request may have no node;
  *   n_rows     rows of q, out and mask, >= 0;   mask: device uint64 [n_rows] (8-byte aligned);
