@@ -2,8 +2,10 @@
 import numpy as np
 import pytest
 
+import oracle as O
 import workloads
-from helpers import bits_to_torch
+from helpers import bits_to_torch, torch_to_bits
+from kv_bounds import row_tolerances
 from test_gpu_kv_rows import L, Prompt, Tree, _bf16  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -107,5 +109,49 @@ def test_tree_many_items_of_a_cta_with_infinities_in_most(L, n_kv, G, D, n):  # 
         expect = torch.where(alive, expect, torch.zeros_like(expect)).view(c.rows, -1)
         assert torch.equal(got.isnan(), expect.isnan())
         assert torch.equal(got.float().nan_to_num(0), expect.nan_to_num(0))
+    finally:
+        c.close()
+
+
+def _far(rng, shape, D, power):
+    """Rows whose first feature of each head alone is not zero: 2^power times a bf16 value of 1 to 2, of either sign."""
+    x = np.zeros(shape, np.float32)
+    x[:, ::D] = 2.0 ** power * (1 + rng.integers(0, 128, x[:, ::D].shape) / 128.0) * rng.choice([-1.0, 1.0], x[:, ::D].shape)
+    return workloads.to_bf16_bits(x)
+
+
+def _check_far(ref, out, lse, D):
+    """Scores are one product each, exact in fp32, and far apart or equal: as row_tolerances, without their errors."""
+    tol, tol_z = row_tolerances({**ref, "mag": np.zeros_like(ref["mag"])}, D)
+    assert (np.abs(O.bf16_to_f64(torch_to_bits(out)) - ref["out"]) <= tol).all()
+    assert (np.abs(lse.cpu().numpy() - ref["lse"]) <= tol_z).all()
+
+
+@pytest.mark.parametrize("n_kv,G,D", [(2, 1, 64), (1, 2, 128), (1, 3, 128), (1, 2, 256), (50, 1, 64)])
+@pytest.mark.parametrize("power", [13, 16, 18, 30, 62])
+def test_prompt_scores_past_the_range_of_the_exponent(L, n_kv, G, D, power):  # noqa: F811
+    """Scores whose steps in fp32 are larger than any exponent, V near the end of its range."""
+    c = Prompt(L, n_kv, G, D, [300, 45], seed=25)
+    try:
+        c.q, c.k = (_far(c.rng, x.shape, D, power) for x in (c.q, c.k))
+        c.v = workloads.to_bf16_bits((3.0e38 * (0.5 + 0.5 * c.rng.random(c.v.shape))).astype(np.float32))
+        out, lse = c.run()
+        L.lora_status(c.pool)
+        _check_far(c.reference(), out, lse, D)
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("n_kv,G,D", [(2, 1, 64), (1, 2, 128), (1, 3, 128), (1, 2, 256)])
+@pytest.mark.parametrize("power", [13, 16, 18, 30, 62])
+def test_tree_scores_past_the_range_of_the_exponent(L, n_kv, G, D, power):  # noqa: F811
+    c = Tree(L, n_kv, G, D, [2000, 90, 300], [30, 5, 64], seed=26, kinds=("any", "tree"))
+    try:
+        tab = np.concatenate(c.tables())
+        c.q, c.bits[tab[:, 0]] = _far(c.rng, c.q.shape, D, power), _far(c.rng, (len(tab), n_kv * D), D, power)
+        c.bits[tab[:, 1]] = workloads.to_bf16_bits((3.0e38 * (0.5 + 0.5 * c.rng.random((len(tab), n_kv * D)))).astype(np.float32))
+        out, lse = c.run()
+        L.lora_status(c.pool)
+        _check_far(c.reference(), out, lse, D)
     finally:
         c.close()
