@@ -974,11 +974,13 @@ extern "C" int lora_kv_append(lora_pool* p, int32_t n_req, const int32_t* count,
         reinterpret_cast<uintptr_t>(row_start) | reinterpret_cast<uintptr_t>(row_req) |
         reinterpret_cast<uintptr_t>(row_pos)) & 3) != 0)
     return lora_fail(LORA_EINVAL, "lora_kv_append: counts, lengths and rows must be 4-byte aligned");
-  if (n_req > 0 && (new_len == old_len || new_len == count || row_start == count || row_start == old_len ||
-                    row_start == new_len))
-    return lora_fail(LORA_EINVAL, "lora_kv_append: outputs must not be the inputs");
-  if (row_cap > 0 && (pages == table_dev || row_req == row_pos))
-    return lora_fail(LORA_EINVAL, "lora_kv_append: outputs must not be the inputs");
+  const struct {
+    const void* at;
+    double bytes;                                          // may pass 64 bits
+    bool out;
+  } arrays[] = {{count, 4. * n_req, false}, {old_len, 4. * n_req, false}, {pages, 8. * row_cap * layers, false},
+                {table_dev, 8. * n_req * max_len * layers, true}, {new_len, 4. * n_req, true}, {row_start, 4. * (n_req + 1.), true},
+                {row_req, 4. * row_cap, true}, {row_pos, 4. * row_cap, true}};
   AppendArgs a{};
   a.n_req = n_req;
   a.count = count;
@@ -1000,6 +1002,12 @@ extern "C" int lora_kv_append(lora_pool* p, int32_t n_req, const int32_t* count,
   const int64_t rest = old_len ? 0 : ((int64_t)n_req * max_len + a.rows_per_cta - 1) / a.rows_per_cta;
   a.row_ctas = (int32_t)std::max(((int64_t)row_cap + a.rows_per_cta - 1) / a.rows_per_cta, (int64_t)1);
   if (a.row_ctas + rest > INT32_MAX) return lora_fail(LORA_EINVAL, "lora_kv_append: the table is too large for one call");
+  for (const auto& x : arrays)                             // CTAs read counts, lengths and pages while others write
+    for (const auto& y : arrays)
+      if (x.out && &x != &y && x.at && y.at && x.bytes > 0 && y.bytes > 0 &&
+          (x.at <= y.at ? (double)(static_cast<const char*>(y.at) - static_cast<const char*>(x.at)) < x.bytes
+                        : (double)(static_cast<const char*>(x.at) - static_cast<const char*>(y.at)) < y.bytes))
+        return lora_fail(LORA_EINVAL, "lora_kv_append: outputs must not overlap the inputs or one another");
   if (p->planning) return lora_fail(LORA_EINVAL, "lora_kv_append: planning pool has no device state");
   a.err = p->d_err;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

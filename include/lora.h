@@ -303,8 +303,8 @@ int lora_kv_keep(lora_pool* pool, int64_t request_id, int32_t layers, int32_t n_
  *   row_cap    rows that pages, row_req and row_pos hold, >= 0.  Rows at and past row_start[n_req] get
  *              row_req = -1 (lora_kv_write skips them) and row_pos = 0;
  *   table_dev  out: device int32 [n_req][max_len][layers][2] (8-byte aligned);
- *   new_len    out: device int32 [n_req], not old_len;   row_start out: device int32 [n_req + 1];
- *   row_req, row_pos  out: device int32 [row_cap].
+ *   new_len    out: device int32 [n_req];   row_start out: device int32 [n_req + 1];
+ *   row_req, row_pos  out: device int32 [row_cap].  No output may overlap an input or another output.
  * A negative count (taken as 0), an old length outside [0, max_len] (clamped), a token at or past max_len
  * (its row gets row_req = -1 and its page goes nowhere) and rows past row_cap (dropped) set the device error
  * word; new_len counts what the table holds.  At most 65535 requests and 2^20 layers; max_len at most 2^30.

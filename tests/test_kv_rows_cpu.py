@@ -108,6 +108,22 @@ def test_kv_append_refuses(L, pool, over, message):
     _refused(L, lambda **o: L.lora_kv_append(**{**base, **o}), message, **over)
 
 
+@pytest.mark.parametrize("out", ["table_dev", "new_len_dev", "row_start_dev", "row_req_dev", "row_pos_dev"])
+def test_kv_append_refuses_outputs_over_any_other_array(L, pool, out):
+    """By a single element at either end; arrays that touch are taken (and the planning pool refused)."""
+    at = dict(count_dev=A, old_len_dev=B, pages_dev=C, table_dev=D, new_len_dev=E, row_start_dev=F, row_req_dev=G, row_pos_dev=K)
+    size = dict(count_dev=12, old_len_dev=12, pages_dev=160, table_dev=384, new_len_dev=12, row_start_dev=16, row_req_dev=40,
+                row_pos_dev=40)
+    unit = 8 if out == "table_dev" else 4
+    call = lambda **o: L.lora_kv_append(**{**at, **dict(pool=pool, n_req=3, row_cap=10, max_len=8, layers=2, stream=0), **o})  # noqa: E731
+    for other in at:
+        if other != out:
+            for over in (unit - size[out], 0, (size[other] - 1) // unit * unit):       # first element, start, last element
+                _refused(L, call, "inputs", **{out: at[other] + over})
+            for beside in (-size[out], -(-size[other] // unit) * unit):
+                _refused(L, call, "planning pool", **{out: at[other] + beside})
+
+
 def test_oracle_tree_of_a_chain_is_the_end_of_a_prompt():
     """The last m tokens of a prompt as a chain of drafted nodes: the same rows."""
     rng = np.random.default_rng(0)
