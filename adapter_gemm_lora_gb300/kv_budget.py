@@ -31,7 +31,8 @@ class BudgetedCache:
 
     A request holds at most ``budget + slack`` tokens; ``make_room`` cuts the batch back to ``budget``
     when one of them is full.  The requests must hold no KV pages yet.  All device state is allocated
-    here; ``attend`` only enqueues work.
+    here; ``attend`` only enqueues work.  Each kind of attention belongs to the growth, prompts or drafts that came last
+    (``grow`` / ``attend``, ``prefill`` / ``attend_prompt``, ``draft`` / ``attend_drafts``) and is refused after anything else.
     """
 
     def __init__(self, lib, pool, request_ids, layers: int, n_heads: int, n_kv_heads: int, budget: int, recent: int,
@@ -61,11 +62,15 @@ class BudgetedCache:
         self.lengths = [0] * n
         self.evicted = 0
         self.prompt = self.drafted = None                      # tokens of the last prefill / draft, per request
+        self.grown = False                                     # row_pos names the last growth's tokens
 
     def make_room(self, tokens: int = 1) -> None:
         """Evict down to the budget if a request has no room for `tokens` more (reads the kept positions back)."""
+        if self.drafted is not None:
+            raise ValueError("make_room: the last drafts are neither kept nor dropped (accept)")
         if not self.lengths or max(self.lengths) + tokens <= self.cap:
             return
+        self.prompt, self.grown = None, False                  # tokens move: their rows are no longer where they were
         n = len(self.ids)
         table, weight, seq_len = self._next
         self.lib.lora_kv_evict(self.pool, n, self.table, self.seq_len, self.cap, self.layers, self.weight, self.budget,
@@ -94,6 +99,7 @@ class BudgetedCache:
         self.row_pos.copy_(pos)
         self.seq_len += 1
         self.lengths = [x + 1 for x in self.lengths]
+        self.prompt, self.grown = None, True
 
     def _append(self, counts) -> None:
         """Pages, table entries, lengths and slot maps of counts[i] new tokens per request."""
@@ -126,7 +132,7 @@ class BudgetedCache:
         counts = self._checked(lengths, self.cap, "prefill")
         ws_bytes = self.lib.lora_attention_prompt_size(self.pool, len(self.ids), sum(counts), self.n_heads, self.n_kv_heads)
         self._append(counts)                                   # not before the call is known to be small enough
-        self.prompt, self.drafted, self._rows_ws_bytes = counts, None, ws_bytes
+        self.prompt, self.drafted, self.grown, self._rows_ws_bytes = counts, None, False, ws_bytes
         self._rows_ws = torch.empty(max(self._rows_ws_bytes, 256), dtype=torch.uint8, device=self.table.device)
 
     def attend_prompt(self, layer: int, q, k, v, out) -> None:
@@ -149,7 +155,7 @@ class BudgetedCache:
         counts = self._checked(counts, min(self.cap - self.budget, self.lib.LORA_MAX_TREE), "draft")
         self.make_room(max(counts, default=0))
         self._append(counts)
-        self.prompt, self.drafted = None, counts
+        self.prompt, self.drafted, self.grown = None, counts, False
         self._rows_ws_bytes = self.lib.lora_attention_tree_size(self.pool, len(self.ids), self.cap, self.n_heads,
                                                                 self.n_kv_heads)
         self._rows_ws = torch.empty(max(self._rows_ws_bytes, 256), dtype=torch.uint8, device=self.table.device)
@@ -191,6 +197,8 @@ class BudgetedCache:
 
     def attend(self, layer: int, q, k, v, out) -> None:
         """Write the new tokens' K and V rows at `layer`, then attend over the cache, the new token included."""
+        if not self.grown:
+            raise ValueError("attend: no new tokens (grow)")
         n = len(self.ids)
         self.lib.lora_kv_write(self.pool, n, self.row_req, self.row_pos, k, v, n, self.table, self.cap, self.layers, layer)
         self.lib.lora_attention_split(self.pool, n, self.table, self.seq_len, self.cap, self.layers, layer, q, out,
@@ -202,7 +210,7 @@ class BudgetedCache:
             if self.lib.lora_kv_length(self.pool, request) >= 0:
                 self.lib.lora_kv_free(self.pool, request)
         self.lengths = [0] * len(self.ids)
-        self.prompt = self.drafted = None
+        self.prompt, self.drafted, self.grown = None, None, False
         self.seq_len.zero_()
         self.weight.zero_()
         self.table.fill_(-1)

@@ -101,6 +101,75 @@ def test_refusals(L, on_cpu):  # noqa: F811
         L.lora_pool_destroy(pool)
 
 
+class WriteLib(AppendLib):
+    """AppendLib that notes the cache rows a call writes, and attends to nothing."""
+
+    def __init__(self, lib):
+        super().__init__(lib)
+        self.rows = None
+
+    def lora_kv_write(self, pool, rows, req, pos, k, v, n, table, max_len, layers, layer):
+        self.rows = list(zip(req.tolist(), pos.tolist()))
+
+    def lora_attention_split(self, *args, **kw):
+        pass
+
+    lora_attention_prompt = lora_attention_tree = lora_attention_split
+
+
+def test_attention_out_of_turn_is_refused(L, on_cpu):  # noqa: F811
+    """A cached token's K and V rows are written with its own attention alone: whatever came between the growth, the
+    prompts or the drafts and their attention would have it write over other tokens."""
+    from adapter_gemm_lora_gb300.kv_budget import BudgetedCache
+    pool = L.lora_pool_create(None, 400, 64, 1, 1)
+    lib = WriteLib(L)
+    cache = BudgetedCache(lib, pool, [1, 2], 2, 1, 1, 6, 2, 5)
+    calls = {"attend": lambda: cache.attend(0, None, None, None, None),
+             "attend_prompt": lambda: cache.attend_prompt(0, None, None, None, None),
+             "attend_drafts": lambda: cache.attend_drafts(0, None, None, None, None, None)}
+
+    def only(name, rows):
+        for other, call in calls.items():
+            lib.rows = None
+            if other == name:
+                call()
+                assert lib.rows == rows
+            else:
+                with pytest.raises(ValueError, match=f"{other}: no "):
+                    call()
+                assert lib.rows is None
+
+    try:
+        only(None, None)
+        cache.prefill([3, 11])
+        only("attend_prompt", [(0, i) for i in range(3)] + [(1, i) for i in range(11)])
+        cache.make_room()                                     # evicts: the prompts' rows lie elsewhere now
+        assert cache.lengths == [3, 6]
+        only(None, None)
+        cache.grow()
+        only("attend", [(0, 3), (1, 6)])
+        cache.draft([2, 1])
+        only("attend_drafts", [(0, 4), (0, 5), (1, 7)])
+        with pytest.raises(ValueError, match="make_room: the last drafts"):
+            cache.make_room(40)
+        cache.accept([[1], []])
+        only(None, None)
+        cache.grow()
+        only("attend", [(0, 5), (1, 7)])
+        for _ in range(4):
+            cache.grow()
+        cache.make_room(5)
+        assert cache.lengths == [6, 6]
+        only(None, None)
+        cache.free()
+        only(None, None)
+        cache.prefill([1, 0])
+        cache.grow()
+        only("attend", [(0, 1), (1, 0)])
+    finally:
+        L.lora_pool_destroy(pool)
+
+
 class RealSizes(AppendLib):
     def lora_attention_prompt_size(self, *args):
         return self.lib.lora_attention_prompt_size(*args)
