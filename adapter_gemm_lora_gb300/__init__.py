@@ -52,6 +52,7 @@ EXPORTED = ["lora_pool_create", "lora_pool_reserve", "lora_pool_release", "lora_
             "lora_adapter_load_packed", "lora_adapter_wait", "lora_kv_grow", "lora_kv_free", "lora_kv_length",
             "lora_kv_table", "lora_kv_batch_table", "lora_attention_decode", "lora_kv_write",
             "lora_attention_split_size", "lora_attention_split", "lora_kv_evict", "lora_kv_keep",
+            "lora_kv_keep_last",
             "lora_kv_append", "lora_attention_prompt_size", "lora_attention_prompt", "lora_attention_tree_size",
             "lora_attention_tree"]
 KINDS = ("segments", "delta", "gemm", "scatter", "shrink", "attention", "kv")
@@ -135,6 +136,7 @@ def _load():
                                        I64, VP]),
         "lora_kv_evict": (I32, [VP, I32, VP, VP, I32, I32, VP, I32, I32, VP, VP, VP, VP, I32, VP]),
         "lora_kv_keep": (I32, [VP, I64, I32, I32, VP, I64]),
+        "lora_kv_keep_last": (I32, [VP, I64, I32, I32, VP]),
         "lora_kv_append": (I32, [VP, I32, VP, VP, VP, I32, VP, I32, I32, VP, VP, VP, VP, VP]),
         "lora_attention_prompt_size": (I64, [VP, I32, I32, I32, I32]),
         "lora_attention_prompt": (I32, [VP, I32, VP, I32, VP, I64, VP, I64, VP, I64, VP, I64, I32, I32, VP, VP, I64, VP]),
@@ -389,6 +391,14 @@ def lora_kv_keep(pool, request_id: int, keep_host) -> None:
     if keep.ndim != 2:
         raise ValueError("keep_host must be [layers, n_keep]")
     _check(_load().lora_kv_keep(pool, request_id, keep.shape[0], keep.shape[1], _ptr(keep), keep.shape[1]))
+
+
+def lora_kv_keep_last(pool, request_id: int, n_last: int, keep_host) -> None:
+    """Of the request's last n_last tokens those at keep_host (ascending, 0: the first of them) stay, at every layer."""
+    keep = np.ascontiguousarray(keep_host, dtype=np.int32)
+    if keep.ndim != 1:
+        raise ValueError("lora_kv_keep_last: keep_host must be [n_keep]")
+    _check(_load().lora_kv_keep_last(pool, request_id, n_last, len(keep), _ptr(keep)))
 
 
 def lora_kv_append(pool, n_req: int, count_dev, old_len_dev, pages_dev, row_cap: int, table_dev, max_len: int, layers: int,

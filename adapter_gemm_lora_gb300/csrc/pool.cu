@@ -412,6 +412,41 @@ int lora_kv_keep(lora_pool* p, int64_t request, int32_t layers, int32_t n_keep, 
   return LORA_OK;
 }
 
+int lora_kv_keep_last(lora_pool* p, int64_t request, int32_t n_last, int32_t n_keep, const int32_t* keep) {
+  if (!p || n_last < 0 || n_keep < 0 || (n_keep > 0 && !keep)) return lora_fail(LORA_EINVAL, "lora_kv_keep_last: bad arguments");
+  auto it = p->kv.find(request);
+  if (it == p->kv.end()) return lora_fail(LORA_EINVAL, "lora_kv_keep_last: request " + std::to_string(request) + " holds no pages");
+  std::vector<int32_t>& pages = it->second.pages;
+  const int64_t token = 2 * (int64_t)it->second.layers, n = (int64_t)pages.size() / token;
+  if (n_last > n)
+    return lora_fail(LORA_EINVAL, "lora_kv_keep_last: request " + std::to_string(request) + " has " + std::to_string(n) + " tokens");
+  for (int32_t i = 0; i < n_keep; ++i)
+    if (keep[i] < 0 || keep[i] >= n_last || (i > 0 && keep[i] <= keep[i - 1]))
+      return lora_fail(LORA_EINVAL, "lora_kv_keep_last: positions must ascend within " + std::to_string(n_last) + " tokens");
+  try {
+    p->free_list.reserve(p->free_list.size() + (size_t)((n_last - n_keep) * token));
+  } catch (const std::bad_alloc&) {
+    return lora_fail(LORA_EINVAL, "lora_kv_keep_last: out of host memory");
+  }
+  // A token never moves up, so the last ones are compacted in place; the others are freed in page order.
+  int32_t* const last = pages.data() + (n - n_last) * token;
+  int32_t kept = 0;
+  for (int32_t j = 0; j < n_last; ++j) {
+    int32_t* const from = last + j * token;
+    if (kept < n_keep && keep[kept] == j) {
+      std::copy(from, from + token, last + kept++ * token);
+      continue;
+    }
+    for (int64_t k = 0; k < token; ++k) {
+      p->page_state[from[k]] = 0;
+      p->free_list.push_back(from[k]);
+    }
+  }
+  p->reserved_pages -= (n_last - n_keep) * token;
+  pages.resize((size_t)((n - n_last + n_keep) * token));
+  return LORA_OK;
+}
+
 int64_t lora_kv_length(const lora_pool* p, int64_t request) {
   if (!p) return -1;
   auto it = p->kv.find(request);

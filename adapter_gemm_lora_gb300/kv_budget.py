@@ -186,8 +186,7 @@ class BudgetedCache:
             base = self.lengths[i] - m
             place += [(i, base + j, base + k[j] if j < len(k) else -1) for j in range(m)]
             if m > len(k):
-                positions = list(range(base)) + [base + j for j in k]
-                self.lib.lora_kv_keep(self.pool, self.ids[i], np.tile(np.array(positions, np.int32), (self.layers, 1)))
+                self.lib.lora_kv_keep_last(self.pool, self.ids[i], m, k)
             self.lengths[i] = base + len(k)
         if place:
             r, to, frm = torch.tensor(place, dtype=torch.int64).t().to(self.table.device)

@@ -286,6 +286,15 @@ int lora_kv_keep(lora_pool* pool, int64_t request_id, int32_t layers, int32_t n_
                  int64_t keep_stride);
 
 /*
+ * Of the last n_last cached tokens of a request those at keep_host[i], i < n_keep, stay, in that order behind the
+ * tokens before them, the same ones at every layer: what accepting some of a request's drafted tokens leaves.
+ * Positions count from the first of the n_last tokens and ascend strictly (LORA_EINVAL otherwise, or where the
+ * request holds fewer tokens; nothing changed then).  As lora_kv_keep of all positions of the request, but its
+ * time goes by n_last, not by the tokens cached.
+ */
+int lora_kv_keep_last(lora_pool* pool, int64_t request_id, int32_t n_last, int32_t n_keep, const int32_t* keep_host);
+
+/*
  * Page table, lengths and slot maps of a batch's new tokens, built on the device from the requests' token
  * counts: request r gets count[r] tokens behind the old_len[r] that it has cached, and the batch's rows are
  * the new tokens of all requests one behind another, request by request:

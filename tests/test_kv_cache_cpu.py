@@ -196,6 +196,52 @@ def test_kv_keep_matches_the_oracle_over_random_sequences(L):
         L.lora_pool_destroy(pool)
 
 
+# ---- bookkeeping of drafted tokens -----------------------------------------------------------------
+def test_kv_keep_last_is_kv_keep_of_all_positions(L):
+    """Tables and the free list's order are the oracle's after kv_keep of the tokens before and the kept ones."""
+    rng = np.random.default_rng(18)
+    order = rng.permutation(600)
+    pool, model = L.lora_pool_create(None, 600, 64, 1, 1, order), O.PoolModel(600, 1, 1, order)
+    layers = 3
+    try:
+        for step in range(150):
+            r, grow = int(rng.integers(0, 4)), int(rng.integers(0, 9))
+            st, ids = model.kv_grow(r, grow, layers)
+            if st == O.OK:
+                assert L.lora_kv_grow(pool, r, grow, layers) == ids
+            n = len(model.kv.get(r, [])) // (2 * layers)
+            if r in model.kv:
+                m = int(rng.choice([0, n, rng.integers(0, n + 1)]))
+                keep = sorted(rng.choice(m, size=int(rng.integers(0, m + 1)), replace=False).tolist())
+                assert model.kv_keep(r, [list(range(n - m)) + [n - m + j for j in keep]] * layers) == O.OK
+                L.lora_kv_keep_last(pool, r, m, keep)
+            for q in model.kv:
+                assert L.lora_kv_length(pool, q) == len(model.kv[q]) // (2 * layers)
+                for l in range(layers):
+                    assert L.lora_kv_table(pool, q, l).tolist() == model.kv_table(q, l).tolist()
+            s, ms = L.lora_pool_stats(pool), model.stats()
+            assert (s["free"], s["reserved"]) == (ms["free"], ms["reserved"])
+        n_free = L.lora_pool_stats(pool)["free"]
+        assert L.lora_pool_reserve(pool, n_free).tolist() == model.free[::-1]
+    finally:
+        L.lora_pool_destroy(pool)
+
+
+@pytest.mark.parametrize("n_last,keep,message", [
+    (2, [2], "ascend"), (2, [-1], "ascend"), (3, [1, 1], "ascend"), (3, [2, 1], "ascend"), (0, [0], "ascend"),
+    (4, [0], "has 3 tokens"), (-1, [], "bad arguments"),
+])
+def test_kv_keep_last_refuses_and_changes_nothing(L, pool, n_last, keep, message):
+    L.lora_kv_grow(pool, 1, 3, 2)
+    before = [L.lora_kv_table(pool, 1, l).tolist() for l in range(2)], L.lora_pool_stats(pool)
+    _refused(L, lambda: L.lora_kv_keep_last(pool, 1, n_last, keep), message)
+    _refused(L, lambda: L.lora_kv_keep_last(pool, 2, 0, []), "holds no pages")
+    _refused(L, lambda: L.lora_kv_keep_last(None, 1, 0, []), "bad arguments")
+    with pytest.raises(ValueError):
+        L.lora_kv_keep_last(pool, 1, 1, [[0]])
+    assert ([L.lora_kv_table(pool, 1, l).tolist() for l in range(2)], L.lora_pool_stats(pool)) == before
+
+
 # ---- the oracle against closed forms ------------------------------------------------------------
 def test_oracle_weights_of_two_tokens():
     """One query head, D = 64, K differing in one coordinate: scores 0 and 8 a / 8 = a, so the

@@ -170,6 +170,39 @@ def test_attention_out_of_turn_is_refused(L, on_cpu):  # noqa: F811
         L.lora_pool_destroy(pool)
 
 
+class CountingLib(AppendLib):
+    """AppendLib that counts the positions handed to the pool's bookkeeping."""
+    handed = 0
+
+    def lora_kv_keep(self, pool, request, keep):
+        self.handed += np.asarray(keep).size
+        self.lib.lora_kv_keep(pool, request, keep)
+
+    def lora_kv_keep_last(self, pool, request, n_last, keep):
+        self.handed += n_last
+        self.lib.lora_kv_keep_last(pool, request, n_last, keep)
+
+
+def test_accepting_drafts_takes_time_by_the_drafts(L, on_cpu):  # noqa: F811
+    """However long the cache, accept hands on no more than the drafted tokens."""
+    from adapter_gemm_lora_gb300.kv_budget import BudgetedCache
+    pool = L.lora_pool_create(None, 40000, 64, 1, 1)
+    lib = CountingLib(L)
+    cache = BudgetedCache(lib, pool, [1, 2, 3], 5, 1, 1, 1200, 2, 20)
+    try:
+        cache.prefill([1000, 1, 700])
+        cache.draft([7, 20, 0])
+        cache.accept([[0, 3], [19], []])
+        assert lib.handed <= 27 and cache.lengths == [1002, 2, 700]
+        _host_is_device(L, pool, cache)
+        cache.draft([1, 2, 3])
+        cache.accept([[0], [0, 1], [0, 1, 2]])                    # nothing is dropped
+        assert lib.handed <= 27
+        _host_is_device(L, pool, cache)
+    finally:
+        L.lora_pool_destroy(pool)
+
+
 class RealSizes(AppendLib):
     def lora_attention_prompt_size(self, *args):
         return self.lib.lora_attention_prompt_size(*args)
