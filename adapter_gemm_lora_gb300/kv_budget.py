@@ -7,7 +7,10 @@ batch under a token budget: each step writes the new token's K and V rows into t
 over the cache, which adds up the attention weight that every cached token receives; when a request's
 cache is full, the lightest older tokens are evicted at every layer and their pages go back to the pool.
 Prompts enter an empty cache whole (``prefill``), and drafted tokens are attended as a tree and then kept or
-dropped (``draft``, ``accept``): their table entries and slot maps are made on the GPU.
+dropped (``draft``, ``accept``): their table entries and slot maps are made on the GPU.  Only decode steps (``grow``,
+``attend``) add weight.  Prompts and drafts look at tokens without a trace, so in a loop of drafts alone all weights are
+equal, and an eviction keeps the oldest ``budget - recent`` tokens and the newest ``recent``, whatever was looked at; among
+decode steps, tokens that none of them saw (those of accepted drafts) are the first to leave.
 
     python -m adapter_gemm_lora_gb300.kv_budget [--H 4096] [--heads 32] [--requests 64] [--steps 256]
                                                 [--layers 2] [--budget 128] [--recent 32] [--slack 32]
@@ -16,7 +19,7 @@ dropped (``draft``, ``accept``): their table entries and slot maps are made on t
 runs such a loop over random weights and prints one JSON line: time per step, evictions, and the KV
 pages held against what the same requests would hold without a budget.  With --prompt P every request
 starts with a prompt of P/2 to P tokens; with --draft M a step checks a tree of M drafted tokens per
-request and keeps one path of it.
+request and keeps one path of it (no step adds weight then).
 """
 from __future__ import annotations
 
@@ -137,7 +140,7 @@ class BudgetedCache:
 
     def attend_prompt(self, layer: int, q, k, v, out) -> None:
         """Write the prompts' K and V rows at `layer`; causal attention of every prompt over itself.  (Prompt tokens
-        receive no weight from it: eviction goes by what new tokens look at.)"""
+        receive no weight from it: eviction goes by what decode steps look at.)"""
         if self.prompt is None:
             raise ValueError("attend_prompt: no prefill")
         n = len(self.ids)
@@ -148,7 +151,8 @@ class BudgetedCache:
 
     def draft(self, counts) -> None:
         """Room for a tree of counts[i] drafted tokens per request behind what is cached; evicts first if they do not
-        fit (so at most `slack` of them).  ``attend_drafts`` takes their rows, ``accept`` says which stay."""
+        fit (so at most `slack` of them), by the weights that decode steps have left: without any, the tokens between
+        the oldest ``budget - recent`` and the newest ``recent``.  ``attend_drafts`` takes their rows, ``accept`` says which stay."""
         import torch
         if self.drafted is not None:
             raise ValueError("draft: the last drafts are neither kept nor dropped (accept)")
@@ -162,7 +166,7 @@ class BudgetedCache:
 
     def attend_drafts(self, layer: int, q, k, v, mask, out) -> None:
         """Write the drafted tokens' K and V rows at `layer`, then attend: each sees the cache and the drafted tokens
-        of its request that its mask (int64 per row, bit j: node j) names."""
+        of its request that its mask (int64 per row, bit j: node j) names.  Cached tokens receive no weight from it."""
         if self.drafted is None:
             raise ValueError("attend_drafts: no drafts")
         n = len(self.ids)

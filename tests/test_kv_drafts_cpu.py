@@ -170,6 +170,38 @@ def test_attention_out_of_turn_is_refused(L, on_cpu):  # noqa: F811
         L.lora_pool_destroy(pool)
 
 
+def test_what_a_loop_of_drafts_alone_keeps(L, on_cpu):  # noqa: F811
+    """No decode step, no weight: the oldest tokens and the most recent ones stay.  Decode steps' weights count, and
+    accepted tokens that none of them saw leave first."""
+    pool, cache = _cache(L)                                       # budget 6, recent 2, room for 11
+    try:
+        cache.prefill([9, 3, 0])
+        pages = [cache.table[i, :n].clone() for i, n in enumerate([9, 3, 0])]
+        for step in range(12):
+            counts = [3, 2, 1]
+            if any(n + c > cache.cap for n, c in zip(cache.lengths, [max(counts)] * 3)):
+                pages = [p if len(p) <= 6 else torch.cat([p[:4], p[-2:]]) for p in pages]
+            cache.draft(counts)
+            new = [cache.table[i, cache.lengths[i] - c:cache.lengths[i]].clone() for i, c in enumerate(counts)]
+            assert (cache.weight == 0).all()
+            cache.accept([[0, 2], [1], [0]])
+            pages = [torch.cat([p, x[k]]) for p, x, k in zip(pages, new, ([0, 2], [1], [0]))]
+            for i, p in enumerate(pages):
+                assert torch.equal(cache.table[i, :cache.lengths[i]], p)
+        assert cache.evicted > 0
+        _host_is_device(L, pool, cache)
+        cache.free()
+        cache.prefill([5, 5, 5])
+        cache.weight[:, :, :5] = torch.tensor([1.0, 5, 2, 4, 3])      # what decode steps have left
+        cache.draft([5, 5, 5])
+        cache.accept([[0, 1, 2, 3, 4]] * 3)
+        was = cache.table[0, :10].clone()
+        cache.draft([2, 2, 2])
+        assert torch.equal(cache.table[0, :6], was[[1, 2, 3, 4, 8, 9]])
+    finally:
+        L.lora_pool_destroy(pool)
+
+
 class CountingLib(AppendLib):
     """AppendLib that counts the positions handed to the pool's bookkeeping."""
     handed = 0
