@@ -355,6 +355,18 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
+// A wait that lasts as long as an item does: of a tree, whose items have up to 2^23 blocks, for as long as the CTA's
+// products go on (an item of 12 million tokens takes some 150 ms).  Its code costs trees of shared heads 1.5 %: 131.8 -> 133.8 us.
+template <bool kTree>
+__device__ __forceinline__ bool wait_item(uint32_t bar, uint32_t parity, const volatile uint32_t* blocks) {
+  if (!kTree) return wait_for(bar, parity);
+  uint32_t seen;
+  do {
+    seen = *blocks;
+    if (wait_for(bar, parity)) return true;
+  } while (seen != *blocks);
+  return false;
+}
 // Takes a CTA of the grid that has not been launched out of it, in place of the hardware: 16 bytes into shared memory
 // say whether there was one, and which.  Not to be asked again after a no.
 __device__ __forceinline__ void try_cancel(uint32_t dst, uint32_t bar) {
@@ -487,6 +499,7 @@ struct Tail {
   uint32_t bad[8][G::kScanWarps][2][4];  // which tokens' of its guarded blocks, an item's in turn: 64 nodes, 128 tokens,
                                          // or 256 from a multiple of 256 on lie in two blocks
   uint32_t tmem;
+  uint32_t blocks;                       // tree: blocks whose products are issued
   uint32_t guard_slot[G::NS];            // where guarded V slots lie, in turn
   Item items[G::kItems];
   int32_t bounds[kFew + 1];              // few sequences: their row starts, and
@@ -792,6 +805,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   volatile uint32_t* words = &tail.words[0][0];
   volatile int* first_bad = &tail.first_bad;
   volatile uint32_t* guard_slot = tail.guard_slot;
+  volatile uint32_t* blocks = &tail.blocks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
 #pragma unroll 1
@@ -818,6 +832,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *first_bad = INT32_MAX;
+    *blocks = 0;
   }
   pdl_wait_then_release();                                 // TMEM is taken after it: an earlier kernel may still need its own
   if (warp == G::kMmaWarp) {
@@ -830,22 +845,25 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   const uint32_t tmem = tail.tmem;
   Item it = {};
   bool ok = true;
-  // The n-th item, as the planning warp found it; false behind the last one.
-  const auto read_item = [&](int n, Item& x) {
+  // The n-th item, as the planning warp found it; false behind the last one.  early: by a warp that may have nothing to
+  // do in the items before it.
+  constexpr std::true_type kEarly{};
+  constexpr std::false_type kInTurn{};
+  const auto read_item = [&](int n, Item& x, auto early) {
     const int at = n % G::kItems;
-    if (!__all_sync(0xffffffffu, wait_for(bar_item + 8 * at, (uint32_t)(n / G::kItems) & 1u))) return false;
+    if (!__all_sync(0xffffffffu, wait_item<G::kTree && early.value>(bar_item + 8 * at, (uint32_t)(n / G::kItems) & 1u, blocks))) return false;
     x = tail.items[at];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_taken + 8 * at);
     return true;
   };
-  const auto take = [&](int n) {
-    ok = read_item(n, it);
+  const auto take = [&](int n, auto early) {
+    ok = read_item(n, it, early);
     return ok && it.req >= 0;
   };
   // Q of the item `it`, the n-th, by one thread.
   const auto load_q = [&](int n) {
-    if (!wait_for(bar_qempty, (n & 1) ^ 1)) return false;
+    if (!wait_item<G::kTree>(bar_qempty, (n & 1) ^ 1, blocks)) return false;
     const bool two = it.nb1 > 0;
     const uint32_t bytes = (uint32_t)(a.npt * a.group * 128 * (D / 64));
     mbar_arrive_expect_tx(bar_qfull, two ? 2 * bytes : bytes);
@@ -870,12 +888,12 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     uint32_t use[2] = {0, 0}, items_t = 0, products = 0, blocks_done = 0;
     Item nxt;
-    take(0);
+    take(0, kInTurn);
     for (int n_item = 0; ok && it.req >= 0; ++n_item, it = nxt) {
       const int nb = t == 0 ? it.nb0 : it.nb1, nb_all = it.b1 - it.b0;
       if (nb == 0) {
         blocks_done += nb_all;
-        ok = read_item(n_item + 1, nxt);
+        ok = read_item(n_item + 1, nxt, kEarly);
         continue;
       }
       const int left = Walk<G>::count(a, it, t), row0 = it.row0 + Walk<G>::offset(a, t);
@@ -1037,7 +1055,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         dst[e] = tok_r < left ? a.out + (int64_t)(row0 + tok_r) * a.out_stride + (int64_t)(kv * a.group + r - tok_r * a.group) * D + 8 * (lane & 3)
                               : nullptr;
       }
-      if (!read_item(n_item + 1, nxt) || !__all_sync(0xffffffffu, wait_for(bar_sums + 8 * t, items_t & 1))) {
+      if (!read_item(n_item + 1, nxt, kInTurn) || !__all_sync(0xffffffffu, wait_for(bar_sums + 8 * t, items_t & 1))) {
         ok = false;
         break;
       }
@@ -1264,6 +1282,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
           }
           if (i + NB + 1 == n) mma_commit(bar_qempty);
+          if (G::kTree) ++*blocks;
         }
       }
     }
@@ -1305,7 +1324,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     Ring<NS> ring{0, 1};                                   // phase: of the slot's release
     uint32_t guarded = 0;
     int issued = 0;
-    for (int n_item = 0; ok && take(n_item); ++n_item) {
+    for (int n_item = 0; ok && take(n_item, kInTurn); ++n_item) {
       if (elect_one()) {
         const auto load = [&](bool is_v, int i) {
           const CUtensorMap* map = is_v ? &tm_v : &tm_k;
@@ -1350,7 +1369,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // products with the weights 0 would be NaN; the tile's outputs get those that a row does see ----
     const int w = warp - G::kScanWarp;
     uint32_t guarded = 0;
-    for (int n_item = 0; ok && take(n_item); ++n_item) {
+    for (int n_item = 0; ok && take(n_item, kEarly); ++n_item) {
       const int n = it.b1 - it.b0, tiles = G::kPair && it.nb1 > 0 ? 2 : 1;
       const int slots = (n - max(it.guard - it.b0, 0)) * PD * tiles;
       uint32_t* bad_words = &tail.bad[n_item % 8][w][0][0];
@@ -1359,7 +1378,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       __syncwarp();
 #pragma unroll 1
       for (int k = 0; k < slots && ok; ++k) {
-          ok = __all_sync(0xffffffffu, wait_for(bar_landed + 8 * (guarded % NS), (guarded / NS) & 1));
+          ok = __all_sync(0xffffffffu, wait_item<G::kTree>(bar_landed + 8 * (guarded % NS), (guarded / NS) & 1, blocks));
           if (!ok) break;
           const uint32_t s = guard_slot[guarded % NS];
           const uint32_t off = w * (G::kSlot / G::kScanWarps), at = s_ring + s * G::kSlot + off + lane * 16;
@@ -1394,7 +1413,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     Ring<NS> ring{0, 1};                                   // phase: of the slot's release
     uint32_t guarded = 0;
     int blocks_done = 0, issued = 0;
-    for (int n_item = 0; ok && take(n_item); ++n_item) {
+    for (int n_item = 0; ok && take(n_item, kInTurn); ++n_item) {
       const int n = it.b1 - it.b0;
       const auto entry = [&](int i) {                      // this lane's token of block i
         const int j = (it.b0 + i) * kBlock + 32 * w + lane;

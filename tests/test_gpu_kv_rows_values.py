@@ -155,3 +155,37 @@ def test_tree_scores_past_the_range_of_the_exponent(L, n_kv, G, D, power):  # no
         _check_far(c.reference(), out, lse, D)
     finally:
         c.close()
+
+
+def test_tree_items_that_take_long(L):  # noqa: F811
+    """24 million cached tokens that share 512 pages: an SM's share is one item of 94,000 blocks, which takes longer than
+    any wait for a single block may.  Sums of n terms are off by n steps of fp32, 2^-23, at most: 8 products a block."""
+    import torch
+    heads, D, n, m = 152, 64, 24_000_000, 64
+    H, blocks = heads * D, n / 128
+    g = torch.Generator(device="cuda").manual_seed(29)
+    pool_t = torch.randn((512, H), generator=g, device="cuda").to(torch.bfloat16)
+    pool_t[256:] += 1
+    pool = L.lora_pool_create(pool_t, 512, H, 1, 1)
+    try:
+        ids = torch.randint(0, 256, (n,), generator=g, device="cuda", dtype=torch.int32)
+        table = torch.stack([ids, ids + 256], 1).contiguous().view(1, n, 1, 2)
+        i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        q = (0.5 * torch.randn((m, H), generator=g, device="cuda")).to(torch.bfloat16)
+        mask = torch.full((m,), -1, dtype=torch.int64, device="cuda")
+        out, lse = torch.empty_like(q), torch.empty((m, heads), dtype=torch.float32, device="cuda")
+        nb = L.lora_attention_tree_size(pool, 1, n, heads, heads)
+        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        L.lora_attention_tree(pool, 1, table, i32(n), n, 1, 0, i32(0, m), m, mask, q, out, heads, heads, ws, nb, lse_dev=lse)
+        L.lora_status(pool)
+        k, v = (x.double().view(256, heads, D) for x in (pool_t[:256], pool_t[256:]))
+        s = torch.einsum("ihd,jhd->ihj", q.double().view(m, heads, D), k) / D ** 0.5
+        times = torch.bincount(ids, minlength=256).double()
+        want_lse = torch.logsumexp(s + times.log(), 2)
+        p = torch.exp(s + times.log() - want_lse[..., None])
+        want, size = torch.einsum("ihj,jhd->ihd", p, v), torch.einsum("ihj,jhd->ihd", p, v.abs())
+        tol = (9 * blocks * 2.0 ** -23 + 2.0 ** -7) * size + 2.0 ** -8 * want.abs()
+        assert ((out.double().view(m, heads, D) - want).abs() <= tol).all()
+        assert ((lse.double() - want_lse).abs() <= 2 * blocks * 2.0 ** -23 + 1e-4).all()
+    finally:
+        L.lora_pool_destroy(pool)
