@@ -26,16 +26,16 @@
 // read pages at HBM's rate 193 -> 223 (64 requests of up to 2,047 tokens) and 319 -> 362 (131,072), of shared heads 135 -> 178.
 //
 // What bounds it, on one GB300 (MMA 1,952 TFLOP/s, copies 6,763 GB/s as measured):
-//   prompts of 16,384 tokens, 32 heads of 128       1,447 us  1,520 TFLOP/s, 0.78 of the burst, 0.88 of the sustained rate
-//   7 prompts of 386 to 5,000, 8 KV heads x 4 of 128  291 us  1,395 TFLOP/s: a block takes 3,000 cycles, its MMAs 2,048; a
+//   prompts of 16,384 tokens, 32 heads of 128       1,470 us  1,495 TFLOP/s, 0.77 of the burst, 0.87 of the sustained rate
+//   7 prompts of 386 to 5,000, 8 KV heads x 4 of 128  299 us  1,357 TFLOP/s: a block takes 3,000 cycles, its MMAs 2,048; a
 //                                                             tile's scores wait for its own weights' product
-//   2 of 3,926 and 4,097, 8 KV heads x 2 of 256       195 us  1,350 TFLOP/s: likewise, one tile with two score buffers
-//   16 of 305 to 1,024, 32 heads of 128               102 us  3.7 TB/s of the inputs and outputs: items of 1 to 8 blocks,
+//   2 of 3,926 and 4,097, 8 KV heads x 2 of 256       198 us  1,332 TFLOP/s: likewise, one tile with two score buffers
+//   16 of 305 to 1,024, 32 heads of 128               105 us  3.5 TB/s of the inputs and outputs: items of 1 to 8 blocks,
 //                                                             of which an item's start and end take 5,000 cycles
-//   33 of 40 to 515, 32 KV heads x 2 of 64             64 us  2.7 TB/s: likewise
-//   trees of 32 nodes, 64 requests of up to 2,047 tokens, 32 heads of 128   192 us  6.0 TB/s, 0.88 of the copy rate
-//   one of 64 nodes, 131,072 tokens, 32 heads of 128                        319 us  6.7 TB/s, 1.00
-//   48 nodes, 7 requests of 500 to 33,333 tokens, 8 KV heads x 4 of 128     132 us  4.8 TB/s, 0.71; tensor pipe 0.60 busy
+//   33 of 40 to 515, 32 KV heads x 2 of 64             67 us  2.5 TB/s: likewise
+//   trees of 32 nodes, 64 requests of up to 2,047 tokens, 32 heads of 128   191 us  6.0 TB/s, 0.88 of the copy rate
+//   one of 64 nodes, 131,072 tokens, 32 heads of 128                        315 us  6.8 TB/s, 1.00
+//   48 nodes, 7 requests of 500 to 33,333 tokens, 8 KV heads x 4 of 128     136 us  4.7 TB/s, 0.69; tensor pipe 0.57 busy
 // Pages are gathered by TMA, 256 bytes of each, four a copy (131,072 tokens with 16-byte cp.async instead: 503 us against
 // 346 at that step; 4 warps, since a copy takes 50 cycles to issue).
 // The CTA's warps share the instruction cache and an item of a short prompt runs through most of the code, so code size
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const RowsArgs 
 // An item is two tiles of query rows that work side by side (one tile at D = 256): rows of one KV head, which share
 // its K and V blocks, or with kPair the same rows of two neighbouring KV heads.  A pair is taken where one tile holds a
 // whole tree of 64 nodes (G <= 2), so that the second would be empty: 64 requests of 128 to 2,048 tokens, 32 heads of 128
-// 208 -> 192 us (one request of 705 tokens, 4 heads of 64 10.8 -> 11.4).
+// 215 -> 193 us (one request of 705 tokens, 4 heads of 64 10.5 -> 11.4).
 template <int D_, bool kTree_, bool kPair_ = false, bool kPack_ = false>
 struct Geo {
   static constexpr int D = D_;
@@ -511,8 +511,8 @@ constexpr uint32_t smem_bytes() { return G::kData + sizeof(Tail<G>); }
 
 // The items of a CTA, one after another, found by one warp.  Up to kFew sequences it looks at the caller's starts and
 // lengths itself; beyond, a kernel before this one has listed the items (prompt) or added up the units (tree).  With that
-// kernel always: 4 prompts of 4 to 9 tokens 6.4 -> 11.3 us, one tree behind 705 tokens 11.4 -> 14.8, 127 prompts of 40 tokens
-// 34.5 -> 39.0, 33 of 40 to 515 64.0 -> 67.5; every CTA reads the starts, so the limit is four of them a lane.
+// kernel always: 4 prompts of 4 to 9 tokens 6.5 -> 13.0 us, one tree behind 705 tokens 11.5 -> 15.4, 127 prompts of 40 tokens
+// 36.1 -> 41.7, 33 of 40 to 515 66.9 -> 71.4; every CTA reads the starts, so the limit is four of them a lane.
 template <typename G>
 struct Walk {
   int32_t* bounds_s;             // few: Tail's

@@ -127,9 +127,10 @@ kv_write_packed_kernel(uint16_t* pool, int64_t num_pages, int32_t H, int32_t n_r
 // the counts itself (a thread adds up n_req / 256 requests, one scan over the threads), so the call is one
 // launch; a row's request is then found by bisection over the threads and a walk over that thread's
 // requests.  Pages are moved a layer's K and V (8 bytes) a thread, or two layers' (16) where the layers are even and
-// the arrays aligned.  64 prompts of 500 to 2,048 tokens, 40 layers, into a new table: 71 MB in 13.8 us, 5.1 TB/s (0.76 of
-// the copy rate; entries are moved in 1.8 rounds of CTAs that each begin with the counts).  Four entries in flight and four
-// CTAs an SM; eight entries and two CTAs 16.4 us, and with the registers of four 14.3.
+// the arrays aligned.  64 prompts of 500 to 2,048 tokens, 40 layers, into a new table: 71 MB in 13.9 us.
+// DRAM moves 28 MB of it (the pages read) and L2 keeps the rest; DRAM is 24 % busy, L2 29 %, so neither rate bounds it but
+// the chain of a CTA: the counts first, then its entries, in 1.8 rounds.  Four entries in flight and four CTAs an SM;
+// eight entries and two CTAs 16.4 us, and with the registers of four 14.3.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendBatch = 4;                            // entries a thread has in flight
 constexpr int kAppendEntries = 4 * kAppendBatch * kAppendThreads;   // entries that a CTA writes, about
@@ -985,7 +986,7 @@ extern "C" int lora_kv_append(lora_pool* p, int32_t n_req, const int32_t* count,
   a.n_req = n_req;
   a.count = count;
   a.old_len = old_len;
-  // Two layers at a time (64 prompts of 500 to 2,048 tokens, 40 layers 13.8 us; 39 layers, one at a time, 16.5).
+  // Two layers at a time (64 prompts of 500 to 2,048 tokens, 40 layers 13.9 us; 39 layers, one at a time, 16.5).
   const bool wide = layers % 2 == 0 && ((reinterpret_cast<uintptr_t>(table_dev) | reinterpret_cast<uintptr_t>(pages)) & 15) == 0;
   if (wide) layers /= 2;
   a.pages = pages;
